@@ -4,11 +4,14 @@ Lion, with W data-parallel workers simulated as W buffer sets in one GPU.
 The compute path is liblioncub.so (hand-written CUDA for sm_103a behind the C
 ABI of include/lioncub.h); :mod:`.lioncub` is its ctypes binding and
 :class:`LionCubOptimizer` a small convenience wrapper that takes torch CUDA
-tensors and passes their pointers through.
+tensors and passes their pointers through.  :mod:`.embed` binds the input-layer
+operators of include/lioncub_embed.h, whose gradients fill the embedding rows
+of the vector that a step reads.
 """
 from __future__ import annotations
 
 from . import lioncub
+from .embed import Drop, TokenEmbedding, dropout, dropout_backward  # noqa: F401
 from .lioncub import (  # noqa: F401
     FLAG_AVERAGE, FLAG_TIE_ALTERNATE, GRAD_BF16, GRAD_F32, MODE_L1_INTSUM, MODE_SIGN_MAJORITY,
     TENSOR_SYNC_M, LionCubError,

@@ -28,6 +28,7 @@
 // order-free) and the maximum with an integer atomicMax on the non-negative
 // float's bits.
 #include "device_common.cuh"
+#include "splitmix64.cuh"
 
 namespace lc {
 namespace {
@@ -296,14 +297,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_diagnose_persistent(const StepA
 // worker * 2^40 + e from the caller's seed, times 2^-24.  The codes are
 // summed over the workers in order and the sign of the sum (ties by the
 // handle's tie rule) is compared with the full-precision sign.
-
-__device__ __forceinline__ uint64_t splitmix64(uint64_t seed, uint64_t k)
-{
-    uint64_t z = seed + (k + 1ull) * 0x9e3779b97f4a7c15ull;
-    z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
-    z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
-    return z ^ (z >> 31);
-}
 
 // max |c| of each (worker, tensor): one block per (tile, worker), an integer
 // atomicMax on the bits of the non-negative float (exact, order-free)

@@ -1,0 +1,487 @@
+// embed.cu -- the C ABI of the input-layer operators (include/lioncub_embed.h):
+// argument checks, the handle's workspace, launches and errors.
+#include <nvtx3/nvToolsExt.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+
+#include "embed.h"
+#include "guard.h"
+#include "splitmix64.cuh"
+
+// Layouts the language bindings rely on.
+static_assert(sizeof(lioncub_rows) == 24, "lioncub_rows must stay 24 bytes");
+static_assert(sizeof(lioncub_token_batch) == 48, "lioncub_token_batch must stay 48 bytes");
+static_assert(sizeof(lioncub_drop) == 24, "lioncub_drop must stay 24 bytes");
+static_assert(lc::kStatusIndex == LIONCUB_EMBED_STATUS_INDEX, "status bits are part of the ABI");
+
+namespace {
+constexpr int kMaxAllocs = 4;
+}
+
+struct lioncub_embed_s {
+    int device = 0;
+    int64_t vocab = 0, dim = 0, positions = 0, max_tokens = 0;
+    float scale = 1.0f;
+
+    // device workspace, each buffer that kernels write between guard bands
+    void* allocs[kMaxAllocs] = {};
+    int nallocs = 0;
+    lc::GuardList guards{};
+    int* status = nullptr;
+    int32_t* order = nullptr;   // max_tokens places, grouped by key
+    int2* segment = nullptr;    // max(vocab, positions) ranges of order
+
+    // fault injection (environment, read at create; 0 = off)
+    int64_t fail_alloc_at = 0, alloc_count = 0;
+    int64_t fail_launch_at = 0, launch_count = 0;
+
+    char err[256] = "";
+};
+
+namespace {
+
+// Message of this thread's last failed call without a handle.
+thread_local char g_err[256] = "";
+
+int fail(lioncub_embed_t h, int code, const char* fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(h ? h->err : g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+int cuda_fail(lioncub_embed_t h, cudaError_t e, const char* what)
+{
+    return fail(h, LIONCUB_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+struct NvtxRange {
+    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
+    NvtxRange(const NvtxRange&) = delete;
+    NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+int64_t env_index(const char* name)
+{
+    const char* v = std::getenv(name);
+    if (!v || !*v)
+        return 0;
+    char* end = nullptr;
+    const long long x = std::strtoll(v, &end, 10);
+    return (*end == '\0' && x > 0) ? static_cast<int64_t>(x) : 0;
+}
+
+// `count` elements of T between two guard bands, for the handle's lifetime.
+template <typename T>
+cudaError_t guarded_alloc(lioncub_embed_t h, T** p, int64_t count)
+{
+    const size_t inner = static_cast<size_t>(count > 0 ? count : 1) * sizeof(T);
+    *p = nullptr;
+    if (h->nallocs >= kMaxAllocs || h->guards.n + 2 > lc::kMaxGuardBands)
+        return cudaErrorInvalidValue;
+    if (++h->alloc_count == h->fail_alloc_at)
+        return cudaErrorMemoryAllocation;
+    char* base = nullptr;
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&base), 2 * lc::kGuardBytes + inner);
+    if (e != cudaSuccess)
+        return e;
+    h->allocs[h->nallocs++] = base;
+    char* back = base + lc::kGuardBytes + inner;
+    e = cudaMemset(base, static_cast<int>(lc::kGuardByte), lc::kGuardBytes);
+    if (e == cudaSuccess)
+        e = cudaMemset(back, static_cast<int>(lc::kGuardByte), lc::kGuardBytes);
+    if (e != cudaSuccess)
+        return e;
+    h->guards.band[h->guards.n++] = reinterpret_cast<const uint32_t*>(base);
+    h->guards.band[h->guards.n++] = reinterpret_cast<const uint32_t*>(back);
+    *p = reinterpret_cast<T*>(base + lc::kGuardBytes);
+    return cudaSuccess;
+}
+
+void release(lioncub_embed_t h)
+{
+    for (int k = 0; k < h->nallocs; ++k)
+        cudaFree(h->allocs[k]);
+    delete h;
+}
+
+template <typename Launch>
+cudaError_t launch(lioncub_embed_t h, const char* name, Launch&& go)
+{
+    NvtxRange range(name);
+    if (++h->launch_count == h->fail_launch_at)
+        return cudaErrorLaunchOutOfResources;
+    return go();
+}
+
+// --- arguments ---------------------------------------------------------------------
+
+size_t element_size(int type) { return type == LIONCUB_ROWS_BF16 ? 2 : 4; }
+
+int check_rows(lioncub_embed_t h, const char* name, const lioncub_rows* m, int64_t rows, int64_t cols)
+{
+    if (!m || (!m->data && rows > 0 && cols > 0))
+        return fail(h, LIONCUB_ERR_ARG, "%s is NULL", name);
+    if (m->type != LIONCUB_ROWS_BF16 && m->type != LIONCUB_ROWS_F32)
+        return fail(h, LIONCUB_ERR_ARG, "%s: unknown type %d", name, m->type);
+    if (m->stride < cols || m->stride > (int64_t(1) << 40))
+        return fail(h, LIONCUB_ERR_ARG, "%s: stride %lld for %lld columns", name, (long long)m->stride, (long long)cols);
+    if (reinterpret_cast<uintptr_t>(m->data) % element_size(m->type))
+        return fail(h, LIONCUB_ERR_ALIGN, "%s is not aligned to its elements", name);
+    return LIONCUB_OK;
+}
+
+// Whether two matrices may have bytes in common: their spans do, and they are
+// not disjoint columns of rows that lie the same distance apart.
+bool overlap(const lioncub_rows& a, int64_t arows, const lioncub_rows& b, int64_t brows, int64_t cols)
+{
+    if (arows == 0 || brows == 0 || cols == 0)
+        return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.data), b0 = reinterpret_cast<uintptr_t>(b.data);
+    const uintptr_t a1 = a0 + ((arows - 1) * a.stride + cols) * element_size(a.type);
+    const uintptr_t b1 = b0 + ((brows - 1) * b.stride + cols) * element_size(b.type);
+    if (a0 >= b1 || b0 >= a1)
+        return false;
+    const uintptr_t step = a.stride * element_size(a.type);
+    if (step != b.stride * element_size(b.type))
+        return true;
+    const uintptr_t ahead = b0 >= a0 ? (b0 - a0) % step : step - 1 - (a0 - b0 - 1) % step;  // (b0 - a0) mod step
+    return ahead < cols * element_size(a.type) || ahead + cols * element_size(b.type) > step;
+}
+
+bool same_matrix(const lioncub_rows& a, const lioncub_rows& b)
+{
+    return a.data == b.data && a.stride == b.stride && a.type == b.type;
+}
+
+// Rows that start on 16-byte boundaries.
+bool aligned_rows(const lioncub_rows* m)
+{
+    return !m || (reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && m->stride * element_size(m->type) % 16 == 0);
+}
+
+lc::Rows rows_of(const lioncub_rows* m) { return m ? lc::Rows{m->data, m->stride} : lc::Rows{nullptr, 0}; }
+
+// NULL, p == 0 and a p that rounds to 0 mean no dropout.
+int check_drop(lioncub_embed_t h, const lioncub_drop* d, lc::DropArgs* out, bool* on)
+{
+    *out = lc::DropArgs{0, 0, 1.0f};
+    *on = false;
+    if (!d)
+        return LIONCUB_OK;
+    if (!(d->p >= 0.0f && d->p <= 1.0f))
+        return fail(h, LIONCUB_ERR_ARG, "p must be in [0, 1]");
+    const uint32_t T = static_cast<uint32_t>(std::floor(static_cast<double>(d->p) * 65536.0 + 0.5));
+    if (T == 0)
+        return LIONCUB_OK;
+    out->key = lc::splitmix64(d->seed, d->stream);
+    out->limit = static_cast<uint32_t>((static_cast<uint64_t>(T) << 16) - 1);
+    out->rescale = T == 65536 ? 0.0f : static_cast<float>(65536.0 / (65536.0 - T));
+    *on = true;
+    return LIONCUB_OK;
+}
+
+int check_places(lioncub_embed_t h, const lioncub_token_batch* b, bool positions_used, lc::Places* out)
+{
+    if (!b || b->n < 0 || b->n > h->max_tokens)
+        return fail(h, LIONCUB_ERR_ARG, "a batch of 0..%lld places is needed", (long long)h->max_tokens);
+    if (b->n > 0 && !b->tokens)
+        return fail(h, LIONCUB_ERR_ARG, "tokens is NULL");
+    if (b->index_type != LIONCUB_INDEX_I64 && b->index_type != LIONCUB_INDEX_I32)
+        return fail(h, LIONCUB_ERR_ARG, "unknown index type %d", b->index_type);
+    const uintptr_t size = b->index_type == LIONCUB_INDEX_I64 ? 8 : 4;
+    if (reinterpret_cast<uintptr_t>(b->tokens) % size || reinterpret_cast<uintptr_t>(b->positions) % size)
+        return fail(h, LIONCUB_ERR_ALIGN, "tokens or positions are not aligned to their elements");
+    if (positions_used && h->positions == 0)
+        return fail(h, LIONCUB_ERR_ARG, "the layer has no position rows");
+    if (positions_used && !b->positions) {
+        const int64_t span = b->seq_len < b->n ? b->seq_len : b->n;
+        if (b->seq_len < 1 || b->first_position < 0 || b->first_position > h->positions - span)
+            return fail(h, LIONCUB_ERR_ARG, "positions %lld..%lld are outside the table's %lld", (long long)b->first_position,
+                        (long long)(b->first_position + span - 1), (long long)h->positions);
+    }
+    out->tokens = b->tokens;
+    out->positions = b->positions;
+    out->seq_len = b->seq_len < 1 ? 1 : b->seq_len;
+    out->first = b->first_position;
+    out->n = static_cast<int32_t>(b->n);
+    out->wide = b->index_type == LIONCUB_INDEX_I64;
+    out->vocab = static_cast<int32_t>(h->vocab);
+    out->npos = static_cast<int32_t>(h->positions);
+    return LIONCUB_OK;
+}
+
+int check_device(lioncub_embed_t h)
+{
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return cuda_fail(h, e, "cudaGetDevice");
+    if (dev != h->device)
+        return fail(h, LIONCUB_ERR_STATE, "device %d is current, the handle belongs to %d", dev, h->device);
+    return LIONCUB_OK;
+}
+
+// The gradient of one table: the sort by key and the row sums.
+int table_gradient(lioncub_embed_t h, const lc::Places& at, lc::KeyKind kind, int64_t rows, const lioncub_rows* dout,
+                   const lioncub_rows* base, const lioncub_rows* grad, const lc::DropArgs& drop, bool drop_on,
+                   float factor, cudaStream_t s)
+{
+    lc::SortArgs so{};
+    so.at = at;
+    so.keys = static_cast<int32_t>(rows);
+    so.capacity = static_cast<int32_t>(h->max_tokens);
+    so.order = h->order;
+    so.segment = h->segment;
+    so.status = h->status;
+    cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, kind, s); });
+    if (e != cudaSuccess)
+        return cuda_fail(h, e, "sort launch");
+    lc::RowSumArgs su{};
+    su.dout = rows_of(dout);
+    su.base = rows_of(base);
+    su.grad = rows_of(grad);
+    su.order = h->order;
+    su.segment = h->segment;
+    su.drop = drop;
+    su.factor = factor;
+    su.rows = static_cast<int32_t>(rows);
+    su.dim = static_cast<int32_t>(h->dim);
+    su.n = at.n;
+    su.status = h->status;
+    const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(base) && aligned_rows(grad);
+    e = launch(h, "embed_row_sums", [&] { return lc::launch_row_sums(su, dout->type, grad->type, vec, drop_on, s); });
+    return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "row sum launch");
+}
+
+// grad with its optional base: types, strides and overlaps.
+int check_gradient(lioncub_embed_t h, const char* name, const lioncub_rows* base, const lioncub_rows* grad, int64_t rows,
+                   const lioncub_rows* dout, int64_t n)
+{
+    int rc = check_rows(h, name, grad, rows, h->dim);
+    if (rc == LIONCUB_OK && base)
+        rc = check_rows(h, "base", base, rows, h->dim);
+    if (rc != LIONCUB_OK)
+        return rc;
+    if (base && base->type != grad->type)
+        return fail(h, LIONCUB_ERR_ARG, "%s and its base must have one type", name);
+    if (base && !same_matrix(*base, *grad) && overlap(*base, rows, *grad, rows, h->dim))
+        return fail(h, LIONCUB_ERR_ARG, "%s overlaps its base without being it", name);
+    if (overlap(*dout, n, *grad, rows, h->dim))
+        return fail(h, LIONCUB_ERR_ARG, "%s overlaps dout", name);
+    return LIONCUB_OK;
+}
+
+int run_dropout(const char* in_name, const char* out_name, int64_t rows, int64_t cols, const lioncub_rows* x,
+                const lioncub_rows* residual, const lioncub_rows* out, const lioncub_drop* drop, cudaStream_t s)
+{
+    NvtxRange range("lioncub_dropout");
+    g_err[0] = '\0';
+    if (rows < 0 || cols < 0 || rows > INT_MAX || cols > (int64_t(1) << 40) || (rows > 0 && cols > (int64_t(1) << 41) / rows))
+        return fail(nullptr, LIONCUB_ERR_ARG, "bad sizes: %lld x %lld", (long long)rows, (long long)cols);
+    int rc = check_rows(nullptr, in_name, x, rows, cols);
+    if (rc == LIONCUB_OK)
+        rc = check_rows(nullptr, out_name, out, rows, cols);
+    if (rc == LIONCUB_OK && residual)
+        rc = check_rows(nullptr, "residual", residual, rows, cols);
+    if (rc != LIONCUB_OK)
+        return rc;
+    if (residual && residual->type != out->type)
+        return fail(nullptr, LIONCUB_ERR_ARG, "residual and %s must have one type", out_name);
+    for (const lioncub_rows* m : {x, residual})
+        if (m && !same_matrix(*m, *out) && overlap(*m, rows, *out, rows, cols))
+            return fail(nullptr, LIONCUB_ERR_ARG, "%s overlaps an input without being it", out_name);
+    lc::DropoutArgs a{};
+    bool on = false;
+    rc = check_drop(nullptr, drop, &a.drop, &on);
+    if (rc != LIONCUB_OK)
+        return rc;
+    a.x = rows_of(x);
+    a.residual = rows_of(residual);
+    a.out = rows_of(out);
+    a.rows = rows;
+    a.cols = cols;
+    const bool starts = reinterpret_cast<uintptr_t>(x->data) % 16 == 0 && reinterpret_cast<uintptr_t>(out->data) % 16 == 0 &&
+                        (!residual || reinterpret_cast<uintptr_t>(residual->data) % 16 == 0);
+    const bool dense = x->stride == cols && out->stride == cols && (!residual || residual->stride == cols);
+    const bool vec = starts && (dense || (aligned_rows(x) && aligned_rows(out) && aligned_rows(residual)));
+    if (!(vec && dense) && cols > int64_t(65535) * 256)
+        return fail(nullptr, LIONCUB_ERR_ARG, "rows that are apart or unaligned may have 65535 * 256 columns at most");
+    const cudaError_t e = lc::launch_dropout(a, x->type, out->type, vec, on, s);
+    return e == cudaSuccess ? LIONCUB_OK : cuda_fail(nullptr, e, "dropout launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* lioncub_embed_last_error(lioncub_embed_t h)
+{
+    return h ? h->err : g_err;
+}
+
+int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64_t positions, int64_t max_tokens,
+                         float scale)
+{
+    g_err[0] = '\0';
+    if (!out)
+        return fail(nullptr, LIONCUB_ERR_ARG, "out is NULL");
+    *out = nullptr;
+    if (vocab < 1 || vocab > LIONCUB_EMBED_MAX_VOCAB || positions < 0 || positions > LIONCUB_EMBED_MAX_VOCAB)
+        return fail(nullptr, LIONCUB_ERR_ARG, "tables of 1..%d token rows and 0..%d position rows are supported (got %lld, %lld)",
+                    LIONCUB_EMBED_MAX_VOCAB, LIONCUB_EMBED_MAX_VOCAB, (long long)vocab, (long long)positions);
+    if (dim < 1 || dim > LIONCUB_EMBED_MAX_DIM)
+        return fail(nullptr, LIONCUB_ERR_ARG, "dim must be 1..%d (got %lld)", LIONCUB_EMBED_MAX_DIM, (long long)dim);
+    if (max_tokens < 0 || max_tokens > LIONCUB_EMBED_MAX_TOKENS)
+        return fail(nullptr, LIONCUB_ERR_ARG, "max_tokens must be 0..%d (got %lld)", LIONCUB_EMBED_MAX_TOKENS,
+                    (long long)max_tokens);
+    if (!std::isfinite(scale))
+        return fail(nullptr, LIONCUB_ERR_ARG, "scale must be finite");
+    lioncub_embed_t h = new (std::nothrow) lioncub_embed_s();
+    if (!h)
+        return fail(nullptr, LIONCUB_ERR_OOM, "no host memory for the handle");
+    h->vocab = vocab;
+    h->dim = dim;
+    h->positions = positions;
+    h->max_tokens = max_tokens;
+    h->scale = scale;
+    h->fail_alloc_at = env_index("LIONCUB_FAIL_ALLOC");
+    h->fail_launch_at = env_index("LIONCUB_FAIL_LAUNCH");
+    cudaError_t e = cudaGetDevice(&h->device);
+    if (e == cudaSuccess)
+        e = guarded_alloc(h, &h->status, 1);
+    if (e == cudaSuccess)
+        e = cudaMemset(h->status, 0, sizeof(int));
+    if (e == cudaSuccess)
+        e = guarded_alloc(h, &h->order, max_tokens);
+    if (e == cudaSuccess)
+        e = guarded_alloc(h, &h->segment, vocab > positions ? vocab : positions);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+        release(h);
+        cudaGetLastError();  // a failed allocation leaves a non-sticky error behind
+        return e == cudaErrorMemoryAllocation ? fail(nullptr, LIONCUB_ERR_OOM, "no device memory for the workspace")
+                                              : cuda_fail(nullptr, e, "create");
+    }
+    *out = h;
+    return LIONCUB_OK;
+}
+
+int lioncub_embed_forward(lioncub_embed_t h, const lioncub_token_batch* batch, const lioncub_rows* table,
+                          const lioncub_rows* pos_table, const lioncub_rows* out, const lioncub_drop* drop,
+                          lioncub_stream_t stream)
+{
+    if (!h)
+        return LIONCUB_ERR_ARG;
+    NvtxRange range("lioncub_embed_forward");
+    lc::LookupArgs a{};
+    int rc = check_places(h, batch, pos_table != nullptr, &a.at);
+    if (rc == LIONCUB_OK)
+        rc = check_rows(h, "table", table, h->vocab, h->dim);
+    if (rc == LIONCUB_OK && pos_table)
+        rc = check_rows(h, "pos_table", pos_table, h->positions, h->dim);
+    if (rc == LIONCUB_OK)
+        rc = check_rows(h, "out", out, batch->n, h->dim);
+    if (rc != LIONCUB_OK)
+        return rc;
+    if (pos_table && pos_table->type != table->type)
+        return fail(h, LIONCUB_ERR_ARG, "table and pos_table must have one type");
+    if (overlap(*out, batch->n, *table, h->vocab, h->dim) ||
+        (pos_table && overlap(*out, batch->n, *pos_table, h->positions, h->dim)))
+        return fail(h, LIONCUB_ERR_ARG, "out overlaps a table");
+    bool on = false;
+    rc = check_drop(h, drop, &a.drop, &on);
+    if (rc == LIONCUB_OK)
+        rc = check_device(h);
+    if (rc != LIONCUB_OK)
+        return rc;
+    a.table = rows_of(table);
+    a.pos_table = rows_of(pos_table);
+    a.out = rows_of(out);
+    a.scale = h->scale;
+    a.dim = static_cast<int32_t>(h->dim);
+    a.status = h->status;
+    const bool vec = h->dim % 8 == 0 && aligned_rows(table) && aligned_rows(pos_table) && aligned_rows(out);
+    const cudaError_t e =
+        launch(h, "embed_lookup", [&] { return lc::launch_lookup(a, table->type, out->type, vec, on, stream); });
+    return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "lookup launch");
+}
+
+int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, const lioncub_rows* dout,
+                           const lioncub_rows* base, const lioncub_rows* grad, const lioncub_rows* pos_base,
+                           const lioncub_rows* pos_grad, const lioncub_drop* drop, lioncub_stream_t stream)
+{
+    if (!h)
+        return LIONCUB_ERR_ARG;
+    NvtxRange range("lioncub_embed_backward");
+    lc::Places at{};
+    int rc = check_places(h, batch, pos_grad != nullptr, &at);
+    if (rc == LIONCUB_OK)
+        rc = check_rows(h, "dout", dout, batch->n, h->dim);
+    if (rc == LIONCUB_OK)
+        rc = check_gradient(h, "grad", base, grad, h->vocab, dout, batch->n);
+    if (rc == LIONCUB_OK && pos_base && !pos_grad)
+        rc = fail(h, LIONCUB_ERR_ARG, "pos_base without pos_grad");
+    if (rc == LIONCUB_OK && pos_grad)
+        rc = check_gradient(h, "pos_grad", pos_base, pos_grad, h->positions, dout, batch->n);
+    if (rc != LIONCUB_OK)
+        return rc;
+    if (pos_grad && pos_grad->type != grad->type)
+        return fail(h, LIONCUB_ERR_ARG, "grad and pos_grad must have one type");
+    if (pos_grad && overlap(*grad, h->vocab, *pos_grad, h->positions, h->dim))
+        return fail(h, LIONCUB_ERR_ARG, "grad and pos_grad overlap");
+    lc::DropArgs d;
+    bool on = false;
+    rc = check_drop(h, drop, &d, &on);
+    if (rc == LIONCUB_OK)
+        rc = check_device(h);
+    if (rc == LIONCUB_OK)
+        rc = table_gradient(h, at, lc::kKeyToken, h->vocab, dout, base, grad, d, on, h->scale * d.rescale, stream);
+    if (rc == LIONCUB_OK && pos_grad)
+        rc = table_gradient(h, at, lc::kKeyPosition, h->positions, dout, pos_base, pos_grad, d, on, d.rescale, stream);
+    return rc;
+}
+
+int lioncub_embed_status(lioncub_embed_t h, int32_t* dst_dev, lioncub_stream_t stream)
+{
+    if (!h)
+        return LIONCUB_ERR_ARG;
+    if (!dst_dev)
+        return fail(h, LIONCUB_ERR_ARG, "dst_dev is NULL");
+    int rc = check_device(h);
+    if (rc != LIONCUB_OK)
+        return rc;
+    cudaError_t e = lc::launch_guard_check(h->guards, h->status, stream);
+    if (e == cudaSuccess)
+        e = cudaMemcpyAsync(dst_dev, h->status, sizeof(int32_t), cudaMemcpyDeviceToDevice, stream);
+    return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "status");
+}
+
+void lioncub_embed_destroy(lioncub_embed_t h)
+{
+    if (h)
+        release(h);
+}
+
+int lioncub_dropout_forward(int64_t rows, int64_t cols, const lioncub_rows* x, const lioncub_rows* residual,
+                            const lioncub_rows* out, const lioncub_drop* drop, lioncub_stream_t stream)
+{
+    return run_dropout("x", "out", rows, cols, x, residual, out, drop, stream);
+}
+
+int lioncub_dropout_backward(int64_t rows, int64_t cols, const lioncub_rows* dout, const lioncub_rows* dx,
+                             const lioncub_drop* drop, lioncub_stream_t stream)
+{
+    return run_dropout("dout", "dx", rows, cols, dout, nullptr, dx, drop, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,321 @@
+"""ctypes binding of the input-layer operators (the C ABI in
+include/lioncub_embed.h) and their torch-tensor wrappers.
+
+:class:`TokenEmbedding` is the embedding lookup with scaling (and position
+rows, and dropout) with its gradient by sorted tokens; :func:`dropout` and
+:func:`dropout_backward` draw their mask from a counter-based generator
+(:class:`Drop`) and never store it.  As in :mod:`.lioncub`, the functions
+named ``lioncub_*`` keep the C names and raise :class:`LionCubError` with the
+library's message; the wrappers check tensors, pass their pointers through and
+allocate results with torch.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+from . import lioncub
+from .lioncub import ERR_STATE, OK, LionCubError
+
+ROWS_BF16, ROWS_F32 = 0, 1
+INDEX_I64, INDEX_I32 = 0, 1
+MAX_VOCAB, MAX_DIM, MAX_TOKENS = 1 << 20, 1 << 16, 1 << 30
+STATUS_INDEX = 8
+
+# Every symbol include/lioncub_embed.h declares, for load checks.
+EXPORTED = (
+    "lioncub_embed_create", "lioncub_embed_forward", "lioncub_embed_backward", "lioncub_embed_status",
+    "lioncub_embed_last_error", "lioncub_embed_destroy", "lioncub_dropout_forward", "lioncub_dropout_backward",
+)
+
+
+class Rows(ctypes.Structure):
+    """lioncub_rows: a matrix whose row i starts stride * i elements after data."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class TokenBatch(ctypes.Structure):
+    """lioncub_token_batch: the places of a batch."""
+    _fields_ = [("tokens", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("seq_len", ctypes.c_int64), ("first_position", ctypes.c_int64), ("index_type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class DropSpec(ctypes.Structure):
+    """lioncub_drop."""
+    _fields_ = [("seed", ctypes.c_uint64), ("stream", ctypes.c_uint64), ("p", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
+class Drop(NamedTuple):
+    """Dropout with probability p (to the nearest 1/65536), drawn from stream
+    number `stream` of `seed`; give each (step, worker, layer) its own."""
+    p: float
+    seed: int
+    stream: int = 0
+
+
+_lib = None
+
+
+def load() -> ctypes.CDLL:
+    """The library with this header's functions declared (raises if it is missing)."""
+    global _lib
+    if _lib is None:
+        L = lioncub.load()
+        vp, i64 = ctypes.c_void_p, ctypes.c_int64
+        rows, batch, drop = ctypes.POINTER(Rows), ctypes.POINTER(TokenBatch), ctypes.POINTER(DropSpec)
+        L.lioncub_embed_create.argtypes = [ctypes.POINTER(vp), i64, i64, i64, i64, ctypes.c_float]
+        L.lioncub_embed_forward.argtypes = [vp, batch, rows, rows, rows, drop, vp]
+        L.lioncub_embed_backward.argtypes = [vp, batch, rows, rows, rows, rows, rows, drop, vp]
+        L.lioncub_embed_status.argtypes = [vp, vp, vp]
+        L.lioncub_embed_last_error.argtypes = [vp]
+        L.lioncub_embed_destroy.argtypes = [vp]
+        L.lioncub_embed_destroy.restype = None
+        L.lioncub_dropout_forward.argtypes = [i64, i64, rows, rows, rows, drop, vp]
+        L.lioncub_dropout_backward.argtypes = [i64, i64, rows, rows, drop, vp]
+        for name in EXPORTED:
+            if name != "lioncub_embed_destroy":
+                getattr(L, name).restype = ctypes.c_int
+        L.lioncub_embed_last_error.restype = ctypes.c_char_p
+        _lib = L
+    return _lib
+
+
+def _check(rc: int, h) -> None:
+    if rc != OK:
+        L = load()
+        msg = L.lioncub_embed_last_error(h).decode() or L.lioncub_strerror(rc).decode()
+        raise LionCubError(rc, msg)
+
+
+def lioncub_embed_create(vocab: int, dim: int, positions: int, max_tokens: int, scale: float) -> int:
+    h = ctypes.c_void_p()
+    _check(load().lioncub_embed_create(ctypes.byref(h), vocab, dim, positions, max_tokens, scale), None)
+    return h.value
+
+
+def lioncub_embed_forward(h: int, batch: TokenBatch, table: Rows, pos_table, out: Rows, drop, stream: int = 0) -> None:
+    rc = load().lioncub_embed_forward(h, batch, table, pos_table, out, drop, stream or None)
+    if rc:
+        _check(rc, h)
+
+
+def lioncub_embed_backward(h: int, batch: TokenBatch, dout: Rows, base, grad: Rows, pos_base, pos_grad, drop,
+                           stream: int = 0) -> None:
+    rc = load().lioncub_embed_backward(h, batch, dout, base, grad, pos_base, pos_grad, drop, stream or None)
+    if rc:
+        _check(rc, h)
+
+
+def lioncub_embed_status(h: int, dst_ptr: int, stream: int = 0) -> None:
+    _check(load().lioncub_embed_status(h, dst_ptr, stream or None), h)
+
+
+def lioncub_embed_destroy(h: int) -> None:
+    if h:
+        load().lioncub_embed_destroy(h)
+
+
+def lioncub_dropout_forward(rows: int, cols: int, x: Rows, residual, out: Rows, drop, stream: int = 0) -> None:
+    rc = load().lioncub_dropout_forward(rows, cols, x, residual, out, drop, stream or None)
+    if rc:
+        _check(rc, None)
+
+
+def lioncub_dropout_backward(rows: int, cols: int, dout: Rows, dx: Rows, drop, stream: int = 0) -> None:
+    rc = load().lioncub_dropout_backward(rows, cols, dout, dx, drop, stream or None)
+    if rc:
+        _check(rc, None)
+
+
+# ---- torch tensors -------------------------------------------------------------
+
+_types = None
+
+
+def _torch_types():
+    global _types
+    if _types is None:
+        import torch
+        _types = ({torch.bfloat16: ROWS_BF16, torch.float32: ROWS_F32},
+                  {torch.int64: INDEX_I64, torch.int32: INDEX_I32})
+    return _types
+
+
+def _rows(t, name, nrows, cols, device) -> Rows:
+    """A tensor (..., cols) of nrows rows as a Rows; a view, never a copy."""
+    kind = _torch_types()[0].get(t.dtype)
+    if kind is None or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a bfloat16 or float32 tensor on {device}")
+    shape = t.shape
+    if not shape or shape[-1] != cols or t.numel() != nrows * cols:
+        raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(shape)})")
+    if t.is_contiguous():
+        return Rows(t.data_ptr(), cols, kind, 0)
+    try:
+        t = t.view(-1, cols)  # rows a fixed distance apart
+    except RuntimeError:
+        raise ValueError(f"{name}: its rows do not lie a fixed distance apart") from None
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the columns of a row must be contiguous")
+    return Rows(t.data_ptr(), t.stride(0) if nrows > 1 else cols, kind, 0)
+
+
+def _drop_spec(drop):
+    if drop is None:
+        return None
+    p, seed, stream = drop
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be in [0, 1] (got {p})")
+    return DropSpec(seed & 0xffffffffffffffff, stream & 0xffffffffffffffff, p, 0)
+
+
+def _stream_of(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A result allocated for the stream that writes it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class TokenEmbedding:
+    """The embedding lookup drop(scale * table[token] + pos_table[position])
+    of `vocab` token rows and `positions` position rows (0: none) of `dim`
+    columns, and its gradient, for batches of at most max_tokens places.
+
+    Tensors are CUDA tensors on the device that was current at construction:
+    tokens int64 or int32, tables, activations and gradients bfloat16 or
+    float32 with contiguous columns.  A negative token is an empty place.  The
+    tables may be views of the flat parameter vector and the gradients views
+    of a worker's flat gradient vector.  `stream` defaults to torch's current
+    stream; calls to :meth:`backward` of one layer must be ordered.
+    """
+
+    def __init__(self, vocab, dim, max_tokens, *, positions=0, scale=1.0):
+        import torch
+        self.vocab, self.dim, self.max_tokens = int(vocab), int(dim), int(max_tokens)
+        self.positions, self.scale = int(positions), float(scale)
+        self.h = None
+        self.h = lioncub_embed_create(self.vocab, self.dim, self.positions, self.max_tokens, self.scale)
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _batch(self, tokens, positions, seq_len, first_position):
+        kind = _torch_types()[1].get(tokens.dtype)
+        if kind is None or tokens.device != self.device or not tokens.is_contiguous():
+            raise ValueError(f"tokens must be a contiguous int64 or int32 tensor on {self.device}")
+        at = None
+        if positions is not None:
+            if (positions.dtype != tokens.dtype or positions.device != self.device or not positions.is_contiguous()
+                    or positions.numel() != tokens.numel()):
+                raise ValueError("positions must be a contiguous tensor of tokens' type, size and device")
+            at = positions.data_ptr()
+        if seq_len is None:
+            seq_len = tokens.shape[-1] if tokens.dim() else 1
+        return TokenBatch(tokens.data_ptr(), at, tokens.numel(), max(1, seq_len), first_position, kind, 0)
+
+    def _handle(self):
+        if not self.h:
+            raise LionCubError(ERR_STATE, "the layer is closed")
+        return self.h
+
+    def forward(self, tokens, table, pos_table=None, *, positions=None, seq_len=None, first_position=0, drop=None,
+                out=None, out_dtype=None, stream=None):
+        """Rows for `tokens` (any shape): a tensor tokens.shape + (dim,), or `out`.
+
+        table: (vocab, dim); pos_table: (positions, dim) of table's type, read
+        at `positions` (tokens' shape and type) or, without them, at
+        first_position + the place's index in its sequence of seq_len (the
+        last dimension of tokens).  out_dtype: bfloat16 (default) or float32.
+        """
+        h = self._handle()
+        batch = self._batch(tokens, positions, seq_len, first_position)
+        D = self.dim
+        # the tensors stay referenced until the launch, so that no result is allocated in an argument's memory
+        rows = _rows(table, "table", self.vocab, D, self.device)
+        pos = None if pos_table is None else _rows(pos_table, "pos_table", self.positions, D, self.device)
+        if out is None:
+            import torch
+            out = _empty((*tokens.shape, D), out_dtype or torch.bfloat16, self.device, stream)
+        lioncub_embed_forward(h, batch, rows, pos, _rows(out, "out", batch.n, D, self.device), _drop_spec(drop),
+                              _stream_of(stream))
+        return out
+
+    def backward(self, tokens, dout, grad, *, pos_grad=None, base=None, pos_base=None, positions=None, seq_len=None,
+                 first_position=0, drop=None, stream=None):
+        """Writes grad (vocab, dim) and, when given, pos_grad (positions, dim)
+        from dout (tokens.shape + (dim,)), with the forward call's places and
+        drop.  base / pos_base are added; passing grad itself as base adds in
+        place and touches only the rows of the batch's tokens."""
+        h = self._handle()
+        batch = self._batch(tokens, positions, seq_len, first_position)
+        D, dev = self.dim, self.device
+        g = _rows(grad, "grad", self.vocab, D, dev)
+        b = None if base is None else _rows(base, "base", self.vocab, D, dev)
+        pg = None if pos_grad is None else _rows(pos_grad, "pos_grad", self.positions, D, dev)
+        pb = None if pos_base is None else _rows(pos_base, "pos_base", self.positions, D, dev)
+        lioncub_embed_backward(h, batch, _rows(dout, "dout", batch.n, D, dev), b, g, pb, pg, _drop_spec(drop),
+                               _stream_of(stream))
+        return grad
+
+    def status(self) -> int:
+        """The status word (LIONCUB_STATUS_* and STATUS_INDEX bits; 0: all is well).  Synchronizes."""
+        import torch
+        word = torch.zeros(1, dtype=torch.int32, device=self.device)
+        lioncub_embed_status(self._handle(), word.data_ptr(), _stream_of(None))
+        return int(word.item())
+
+    def close(self):
+        if self.h:
+            lioncub_embed_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _matrix_shape(x, name):
+    import torch
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if x.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = x.shape[-1]
+    return (x.numel() // cols if cols else 0), cols
+
+
+def dropout(x, drop: Drop, *, residual=None, out=None, stream=None):
+    """drop(x), plus `residual` (of the result's type) when given.  out: where
+    to write (x itself, or the residual itself, is allowed); default a new
+    tensor of residual's type, or x's."""
+    rows, cols = _matrix_shape(x, "x")
+    dev = x.device
+    if out is None:
+        out = _empty(x.shape, (x if residual is None else residual).dtype, dev, stream)
+    r = None if residual is None else _rows(residual, "residual", rows, cols, dev)
+    lioncub_dropout_forward(rows, cols, _rows(x, "x", rows, cols, dev), r, _rows(out, "out", rows, cols, dev),
+                            _drop_spec(drop), _stream_of(stream))
+    return out
+
+
+def dropout_backward(dout, drop: Drop, *, out=None, stream=None):
+    """The gradient of :func:`dropout` with respect to x, from the gradient of
+    its result, with the same drop; out may be dout itself."""
+    rows, cols = _matrix_shape(dout, "dout")
+    if out is None:
+        out = _empty(dout.shape, dout.dtype, dout.device, stream)
+    lioncub_dropout_backward(rows, cols, _rows(dout, "dout", rows, cols, dout.device),
+                             _rows(out, "out", rows, cols, dout.device), _drop_spec(drop), _stream_of(stream))
+    return out
