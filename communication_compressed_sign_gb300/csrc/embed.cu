@@ -21,6 +21,7 @@ static_assert(lc::kStatusIndex == LIONCUB_EMBED_STATUS_INDEX, "status bits are p
 
 namespace {
 constexpr int kMaxAllocs = 4;
+constexpr int kWords = 2;  // single words of the workspace: the status word, the sort's total
 }
 
 struct lioncub_embed_s {
@@ -32,9 +33,11 @@ struct lioncub_embed_s {
     void* allocs[kMaxAllocs] = {};
     int nallocs = 0;
     lc::GuardList guards{};
-    int* status = nullptr;
-    int32_t* order = nullptr;   // max_tokens places, grouped by key
+    int* status = nullptr;      // kWords words, the first the status word
+    int32_t* order = nullptr;   // max_tokens places, grouped by key, and their keys
     int2* segment = nullptr;    // max(vocab, positions) ranges of order
+    float* partial = nullptr;   // partial_rows x partial_stride sums of the pieces of long segments
+    int64_t partial_rows = 0, partial_stride = 0;
 
     // fault injection (environment, read at create; 0 = off)
     int64_t fail_alloc_at = 0, alloc_count = 0;
@@ -240,7 +243,9 @@ int table_gradient(lioncub_embed_t h, const lc::Places& at, lc::KeyKind kind, in
     so.keys = static_cast<int32_t>(rows);
     so.capacity = static_cast<int32_t>(h->max_tokens);
     so.order = h->order;
+    so.sorted_key = h->order + h->max_tokens;
     so.segment = h->segment;
+    so.total = h->status + 1;
     so.status = h->status;
     cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, kind, s); });
     if (e != cudaSuccess)
@@ -249,8 +254,13 @@ int table_gradient(lioncub_embed_t h, const lc::Places& at, lc::KeyKind kind, in
     su.dout = rows_of(dout);
     su.base = rows_of(base);
     su.grad = rows_of(grad);
-    su.order = h->order;
-    su.segment = h->segment;
+    su.order = so.order;
+    su.sorted_key = so.sorted_key;
+    su.segment = so.segment;
+    su.total = so.total;
+    su.partial = h->partial;
+    su.partial_stride = h->partial_stride;
+    su.partial_rows = h->partial_rows;
     su.drop = drop;
     su.factor = factor;
     su.rows = static_cast<int32_t>(rows);
@@ -353,17 +363,21 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     h->positions = positions;
     h->max_tokens = max_tokens;
     h->scale = scale;
+    h->partial_rows = max_tokens > lc::kGradPiece ? 2 * lc::grad_stretches(max_tokens) : 0;
+    h->partial_stride = (dim + 3) / 4 * 4;
     h->fail_alloc_at = env_index("LIONCUB_FAIL_ALLOC");
     h->fail_launch_at = env_index("LIONCUB_FAIL_LAUNCH");
     cudaError_t e = cudaGetDevice(&h->device);
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->status, 1);
+        e = guarded_alloc(h, &h->status, kWords);
     if (e == cudaSuccess)
-        e = cudaMemset(h->status, 0, sizeof(int));
+        e = cudaMemset(h->status, 0, kWords * sizeof(int));
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->order, max_tokens);
+        e = guarded_alloc(h, &h->order, 2 * max_tokens);
     if (e == cudaSuccess)
         e = guarded_alloc(h, &h->segment, vocab > positions ? vocab : positions);
+    if (e == cudaSuccess)
+        e = guarded_alloc(h, &h->partial, h->partial_rows * h->partial_stride);
     if (e == cudaSuccess)
         e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {

@@ -53,14 +53,21 @@ struct LookupArgs {
 // Which number a place is sorted by.
 enum KeyKind { kKeyToken = 0, kKeyPosition = 1 };
 
+// Segments longer than this are summed in pieces, cut at its multiples.
+constexpr int kGradPiece = 64;
+inline int64_t grad_stretches(int64_t n) { return (n + kGradPiece - 1) / kGradPiece; }
+
 // The sort of a batch's places by key: order holds the places grouped by key,
-// ascending within a key; segment[key] is the key's range in order.
+// ascending within a key, sorted_key their keys; segment[key] is the key's
+// range in order, total the number of places that have a key.
 struct SortArgs {
     Places at;
     int32_t keys;      // key values: [0, keys)
     int32_t capacity;  // entries of order (checked builds)
     int32_t* order;
+    int32_t* sorted_key;
     int2* segment;
+    int32_t* total;
     int* status;
 };
 
@@ -68,7 +75,12 @@ struct SortArgs {
 struct RowSumArgs {
     Rows dout, base, grad;  // base.data null: zeros
     const int32_t* order;
+    const int32_t* sorted_key;
     const int2* segment;
+    const int32_t* total;
+    float* partial;          // two fp32 rows a stretch of kGradPiece places
+    int64_t partial_stride;  // dim rounded up to 16 bytes
+    int64_t partial_rows;
     DropArgs drop;
     float factor;
     int32_t rows;    // rows of grad

@@ -11,26 +11,54 @@ namespace lc {
 
 // --- V consecutive elements of a row <-> floats ---------------------------------
 
+// The elements as they lie in memory, so that groups waiting in registers take
+// no more room than they did there.
+template <typename T, int V>
+struct Group {
+    static_assert(V == 1, "one element or a 16-byte aligned group of 8");
+    T raw;
+    __device__ __forceinline__ void load(const void* base, int64_t e) { raw = static_cast<const T*>(base)[e]; }
+    __device__ __forceinline__ void unpack(float (&x)[1]) const { x[0] = static_cast<float>(raw); }
+};
+
+template <>
+struct Group<__nv_bfloat16, 8> {
+    uint4 raw;
+    __device__ __forceinline__ void load(const void* base, int64_t e)
+    {
+        raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + e);
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const
+    {
+        x[0] = bf16_bits_lo(raw.x); x[1] = bf16_bits_hi(raw.x);
+        x[2] = bf16_bits_lo(raw.y); x[3] = bf16_bits_hi(raw.y);
+        x[4] = bf16_bits_lo(raw.z); x[5] = bf16_bits_hi(raw.z);
+        x[6] = bf16_bits_lo(raw.w); x[7] = bf16_bits_hi(raw.w);
+    }
+};
+
+template <>
+struct Group<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* base, int64_t e)
+    {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + e);
+        a = p[0];
+        b = p[1];
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+
 template <typename T, int V>
 __device__ __forceinline__ void load_row(const void* base, int64_t e, float (&x)[V])
 {
-    static_assert(V == 1 || V == 8, "one element or a 16-byte aligned group of 8");
-    if constexpr (V == 8 && sizeof(T) == 2) {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + e);
-        x[0] = bf16_bits_lo(v.x); x[1] = bf16_bits_hi(v.x);
-        x[2] = bf16_bits_lo(v.y); x[3] = bf16_bits_hi(v.y);
-        x[4] = bf16_bits_lo(v.z); x[5] = bf16_bits_hi(v.z);
-        x[6] = bf16_bits_lo(v.w); x[7] = bf16_bits_hi(v.w);
-    } else if constexpr (V == 8) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + e);
-        const float4 a = p[0], b = p[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else if constexpr (sizeof(T) == 2) {
-        x[0] = bf16_bits_lo(static_cast<const uint16_t*>(base)[e]);
-    } else {
-        x[0] = static_cast<const float*>(base)[e];
-    }
+    Group<T, V> g;
+    g.load(base, e);
+    g.unpack(x);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)

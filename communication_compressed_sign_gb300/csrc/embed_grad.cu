@@ -1,11 +1,11 @@
 // embed_grad.cu -- gradient of the embedding lookup:
 //   grad[v,:] = base[v,:] + f * sum over places i with key_i == v of keep * dout[i,:].
 //
-// Two launches: a sort of the places by key, then one thread per (row, column
-// group) that adds the rows of dout of its key's places in ascending order and
-// writes the row once -- rows without a place as zeros (or base), so the dense
-// gradient needs no clearing pass and no atomics, and the order of every sum
-// depends on the batch alone.
+// A sort of the places by key, then one thread per (row, column group) that adds
+// the rows of dout of its key's places in ascending order and writes the row
+// once -- rows without a place as zeros (or base), so the dense gradient needs
+// no clearing pass and no atomics, and the order of every sum depends on the
+// batch alone.
 #include "embed_device.cuh"
 
 namespace lc {
@@ -92,6 +92,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortArgs a, int log
         if (index_ok(a.status, key < a.keys && start + total <= a.capacity))
             a.segment[key] = make_int2(start, start + total);
     }
+    if (mine == (1 << log_blocks) - 1 && tid == kSortThreads - 1)
+        *a.total = start + total;
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
         const int c = cnt[w][tid];
@@ -113,44 +115,64 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const SortArgs a, int log
             if ((same >> lane) == 1u)  // the last lane with this key
                 cnt[warp][k] = at + 1;
             __syncwarp(takers);
-            if (index_ok(a.status, at >= 0 && at < a.capacity))
+            if (index_ok(a.status, at >= 0 && at < a.capacity)) {
                 a.order[at] = static_cast<int32_t>(i);
+                a.sorted_key[at] = key;
+            }
         }
         __syncwarp();
     }
 }
 
 // --- row sums ----------------------------------------------------------------------
-
+//
+// Rows of up to kLong places are added by the threads of their row.  Longer
+// segments would leave a few threads adding thousands of rows (token
+// frequencies follow a power law), so they are cut at the multiples of kLong
+// of `order`: each piece is summed by a row of threads of its own into an fp32
+// partial, and a second launch adds a segment's partials in order.  A stretch
+// of kLong entries holds at most two pieces of long segments: the end of one
+// that began before it (slot 0) and the begin of one that goes on (slot 1).
 constexpr int kSumThreads = 256;
+constexpr int kLong = kGradPiece;
+constexpr int kInFlight = 4;  // rows of dout a thread loads before it adds them
 
-template <typename DT, typename GT, int V, bool DROP>
-__global__ void __launch_bounds__(kSumThreads) k_row_sums(const RowSumArgs a)
+// Adds the rows of dout of the places order[lo..hi) to sum, in order.
+template <typename DT, int V, bool DROP>
+__device__ __forceinline__ void add_places(const RowSumArgs& a, int lo, int hi, int32_t j, float (&sum)[V])
 {
-    const int64_t v = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const int32_t g = blockIdx.y * blockDim.x + threadIdx.x;
-    if (v >= a.rows || g >= a.groups)
-        return;
-    const int32_t j = g * V;
-    const int2 seg = a.segment[v];
-    if (seg.x == seg.y && a.base.data == a.grad.data)
-        return;
-    float sum[V];
+    for (int p = lo; p < hi; p += kInFlight) {
+        Group<DT, V> x[kInFlight];
+        int64_t i[kInFlight];
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-        sum[k] = 0.0f;
-    for (int p = seg.x; p < seg.y; ++p) {
-        const int64_t i = a.order[p];
-        if (!index_ok(a.status, i >= 0 && i < a.n))
-            continue;
-        float x[V];
-        load_row<DT, V>(a.dout.data, i * a.dout.stride + j, x);
-        const uint32_t keep = DROP ? keep_bits<V>(a.drop, static_cast<uint64_t>(i) * a.dim + j) : 0xffu;
+        for (int u = 0; u < kInFlight; ++u) {
+            i[u] = p + u < hi ? a.order[p + u] : -1;
+            if (!index_ok(a.status, i[u] < a.n && (i[u] >= 0 || p + u >= hi)))
+                i[u] = -1;
+        }
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            if (keep >> k & 1u)
-                sum[k] = __fadd_rn(sum[k], x[k]);
+        for (int u = 0; u < kInFlight; ++u)
+            if (i[u] >= 0)
+                x[u].load(a.dout.data, i[u] * a.dout.stride + j);
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            if (i[u] < 0)
+                continue;
+            const uint32_t keep = DROP ? keep_bits<V>(a.drop, static_cast<uint64_t>(i[u]) * a.dim + j) : 0xffu;
+            float y[V];
+            x[u].unpack(y);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (keep >> k & 1u)
+                    sum[k] = __fadd_rn(sum[k], y[k]);
+        }
     }
+}
+
+// grad[v, j..j+V) = base + factor * sum.
+template <typename GT, int V>
+__device__ __forceinline__ void finish_row(const RowSumArgs& a, int64_t v, int32_t j, float (&sum)[V])
+{
 #pragma unroll
     for (int k = 0; k < V; ++k)
         sum[k] = __fmul_rn(a.factor, sum[k]);
@@ -164,15 +186,143 @@ __global__ void __launch_bounds__(kSumThreads) k_row_sums(const RowSumArgs a)
     store_row<GT, V>(a.grad.data, v * a.grad.stride + j, sum);
 }
 
+// The pieces of long segments in entries [c * kLong, (c + 1) * kLong) of
+// order: [lo[s], hi[s]) for slot s, empty when there is none.  key[s]: whose.
+__device__ __forceinline__ void pieces_of(const RowSumArgs& a, int64_t c, int total, int (&lo)[2], int (&hi)[2], int (&key)[2])
+{
+    const int begin = static_cast<int>(c * kLong), end = static_cast<int>(min((c + 1) * kLong, static_cast<int64_t>(total)));
+    lo[0] = hi[0] = lo[1] = hi[1] = 0;
+    key[0] = key[1] = -1;
+    if (begin >= end)
+        return;
+    const int first = a.sorted_key[begin], last = a.sorted_key[end - 1];
+    const int2 f = a.segment[first], l = a.segment[last];
+    if (f.x < begin && f.y - f.x > kLong) {
+        lo[0] = begin;
+        hi[0] = min(f.y, end);
+        key[0] = first;
+    }
+    if (l.x >= begin && l.y - l.x > kLong) {
+        lo[1] = l.x;
+        hi[1] = end;
+        key[1] = last;
+    }
+}
+
+// Blocks [0, piece_blocks) of a column slab sum pieces, the others rows.
+template <typename DT, typename GT, int V, bool DROP>
+__global__ void __launch_bounds__(kSumThreads) k_row_sums(const RowSumArgs a, unsigned piece_blocks)
+{
+    const int32_t g = blockIdx.y * blockDim.x + threadIdx.x;
+    if (g >= a.groups)
+        return;
+    const int32_t j = g * V;
+    if (blockIdx.x < piece_blocks) {
+        const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+        int lo[2], hi[2], key[2];
+        pieces_of(a, c, *a.total, lo, hi, key);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (lo[s] == hi[s])
+                continue;
+            float sum[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                sum[k] = 0.0f;
+            add_places<DT, V, DROP>(a, lo[s], hi[s], j, sum);
+            if (index_ok(a.status, 2 * c + s < a.partial_rows))
+                store_row<float, V>(a.partial, (2 * c + s) * a.partial_stride + j, sum);
+        }
+        return;
+    }
+    const int64_t v = static_cast<int64_t>(blockIdx.x - piece_blocks) * blockDim.y + threadIdx.y;
+    if (v >= a.rows)
+        return;
+    const int2 seg = a.segment[v];
+    if (seg.y - seg.x > kLong || (seg.x == seg.y && a.base.data == a.grad.data))
+        return;
+    float sum[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        sum[k] = 0.0f;
+    add_places<DT, V, DROP>(a, seg.x, seg.y, j, sum);
+    finish_row<GT, V>(a, v, j, sum);
+}
+
+// Adds the partials of the long segment that begins in stretch c, if one does:
+// a block's 8 warps each add a contiguous share of its pieces in order, warp 0
+// the shares in order.
+constexpr int kJoinWarps = 8;
+template <typename GT, int V>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_join_pieces(const RowSumArgs a)
+{
+    __shared__ float share[kJoinWarps][32][V + 1];
+    const int64_t c = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int total = *a.total;
+    int lo[2], hi[2], key[2];
+    pieces_of(a, c, total, lo, hi, key);
+    // a segment that begins exactly at a stretch, or inside it
+    if (key[1] < 0)
+        return;
+    const int2 seg = a.segment[key[1]];
+    const int64_t pieces = (seg.y - 1) / kLong - c + 1;
+    const int64_t each = (pieces + kJoinWarps - 1) / kJoinWarps;
+    const int64_t from = min(warp * each, pieces), to = min(from + each, pieces);
+    const int32_t g = blockIdx.y * 32 + lane;
+    float sum[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        sum[k] = 0.0f;
+    if (g < a.groups) {
+        for (int64_t q = from; q < to; q += kInFlight) {
+            float x[kInFlight][V];
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u) {
+                // slot 1 of the stretch it begins in, slot 0 of the later ones
+                const int64_t row = 2 * (c + q + u) + (q + u == 0 ? 1 : 0);
+                if (q + u < to && index_ok(a.status, row < a.partial_rows))
+                    load_row<float, V>(a.partial, row * a.partial_stride + g * V, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u)
+                if (q + u < to)
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        sum[k] = __fadd_rn(sum[k], x[u][k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        share[warp][lane][k] = sum[k];
+    __syncthreads();
+    if (warp != 0 || g >= a.groups)
+        return;
+    for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            sum[k] = __fadd_rn(sum[k], share[w][lane][k]);
+    finish_row<GT, V>(a, key[1], g * V, sum);
+}
+
 template <typename DT, typename GT, int V>
 cudaError_t launch_v(const RowSumArgs& a, bool drop, cudaStream_t s)
 {
-    const RowGrid g = row_grid(a.rows, a.groups, kSumThreads);
+    RowGrid g = row_grid(a.rows, a.groups, kSumThreads);
+    const int64_t stretches = a.n > kLong ? grad_stretches(a.n) : 0;  // no segment is long otherwise
+    const unsigned piece_blocks = static_cast<unsigned>((stretches + g.block.y - 1) / g.block.y);
+    g.grid.x += piece_blocks;
     if (drop)
-        k_row_sums<DT, GT, V, true><<<g.grid, g.block, 0, s>>>(a);
+        k_row_sums<DT, GT, V, true><<<g.grid, g.block, 0, s>>>(a, piece_blocks);
     else
-        k_row_sums<DT, GT, V, false><<<g.grid, g.block, 0, s>>>(a);
-    return cudaGetLastError();
+        k_row_sums<DT, GT, V, false><<<g.grid, g.block, 0, s>>>(a, piece_blocks);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && stretches > 0) {
+        const dim3 grid(static_cast<unsigned>(stretches), static_cast<unsigned>((a.groups + 31) / 32));
+        k_join_pieces<GT, V><<<grid, kJoinWarps * 32, 0, s>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 template <typename DT, typename GT>
