@@ -20,10 +20,11 @@ __device__ __forceinline__ void drop_group(const DropoutArgs& a, int64_t e, int6
     float x[V];
     load_row<XT, V>(a.x.data, ex, x);
     if constexpr (DROP) {
-        const uint32_t keep = keep_bits<V>(a.drop, static_cast<uint64_t>(e));
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            x[k] = (keep >> k & 1u) ? __fmul_rn(a.drop.rescale, x[k]) : 0.0f;
+        auto scale = [&](int k, bool keep) { x[k] = keep ? __fmul_rn(a.drop.rescale, x[k]) : 0.0f; };
+        if constexpr (V == 8)
+            for_kept8(a.drop, a.drop.first + (static_cast<uint64_t>(e) >> 2) * kSplitMix64Step, scale);
+        else
+            scale(0, stays1(a.drop, e));
     }
     if (a.residual.data) {
         float y[V];

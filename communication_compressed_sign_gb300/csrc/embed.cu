@@ -20,7 +20,7 @@ static_assert(sizeof(lioncub_drop) == 24, "lioncub_drop must stay 24 bytes");
 static_assert(lc::kStatusIndex == LIONCUB_EMBED_STATUS_INDEX, "status bits are part of the ABI");
 
 namespace {
-constexpr int kMaxAllocs = 4;
+constexpr int kMaxAllocs = lc::kMaxGuardBands / 2;
 constexpr int kWords = 2;  // single words of the workspace: the status word, the sort's total
 }
 
@@ -33,11 +33,14 @@ struct lioncub_embed_s {
     void* allocs[kMaxAllocs] = {};
     int nallocs = 0;
     lc::GuardList guards{};
-    int* status = nullptr;      // kWords words, the first the status word
-    int32_t* order = nullptr;   // max_tokens places, grouped by key, and their keys
-    int2* segment = nullptr;    // max(vocab, positions) ranges of order
-    float* partial = nullptr;   // partial_rows x partial_stride sums of the pieces of long segments
-    int64_t partial_rows = 0, partial_stride = 0;
+    int* status = nullptr;          // kWords words, the first the status word
+    int32_t* order = nullptr;       // max_tokens places, grouped by key, and their keys
+    int2* segment = nullptr;        // max(vocab, positions) ranges of order
+    int2* pairs = nullptr;          // max_tokens (key, place) of the tiled sort
+    int32_t* tile_count = nullptr;  // its counts, and its buckets' starts
+    int32_t* arrived = nullptr;     // arrival counters of the row sums
+    float* partial = nullptr;       // partial_rows x partial_stride sums of pieces
+    int64_t tile_counts = 0, buckets = 0, arrived_count = 0, partial_rows = 0, partial_stride = 0;
 
     // fault injection (environment, read at create; 0 = off)
     int64_t fail_alloc_at = 0, alloc_count = 0;
@@ -88,7 +91,7 @@ cudaError_t guarded_alloc(lioncub_embed_t h, T** p, int64_t count)
 {
     const size_t inner = static_cast<size_t>(count > 0 ? count : 1) * sizeof(T);
     *p = nullptr;
-    if (h->nallocs >= kMaxAllocs || h->guards.n + 2 > lc::kMaxGuardBands)
+    if (h->nallocs >= kMaxAllocs)
         return cudaErrorInvalidValue;
     if (++h->alloc_count == h->fail_alloc_at)
         return cudaErrorMemoryAllocation;
@@ -174,9 +177,9 @@ bool aligned_rows(const lioncub_rows* m)
 lc::Rows rows_of(const lioncub_rows* m) { return m ? lc::Rows{m->data, m->stride} : lc::Rows{nullptr, 0}; }
 
 // NULL, p == 0 and a p that rounds to 0 mean no dropout.
-int check_drop(lioncub_embed_t h, const lioncub_drop* d, lc::DropArgs* out, bool* on)
+int check_drop(lioncub_embed_t h, const lioncub_drop* d, int64_t cols, lc::DropArgs* out, bool* on)
 {
-    *out = lc::DropArgs{0, 0, 1.0f};
+    *out = lc::DropArgs{0, 0, 0, 1.0f};
     *on = false;
     if (!d)
         return LIONCUB_OK;
@@ -185,7 +188,8 @@ int check_drop(lioncub_embed_t h, const lioncub_drop* d, lc::DropArgs* out, bool
     const uint32_t T = static_cast<uint32_t>(std::floor(static_cast<double>(d->p) * 65536.0 + 0.5));
     if (T == 0)
         return LIONCUB_OK;
-    out->key = lc::splitmix64(d->seed, d->stream);
+    out->first = lc::splitmix64(d->seed, d->stream) + lc::kSplitMix64Step;
+    out->row_step = static_cast<uint64_t>(cols / 4) * lc::kSplitMix64Step;
     out->limit = static_cast<uint32_t>((static_cast<uint64_t>(T) << 16) - 1);
     out->rescale = T == 65536 ? 0.0f : static_cast<float>(65536.0 / (65536.0 - T));
     *on = true;
@@ -233,42 +237,60 @@ int check_device(lioncub_embed_t h)
     return LIONCUB_OK;
 }
 
-// The gradient of one table: the sort by key and the row sums.
+// The gradient of one table: the sort by key and the row sums.  Positions that
+// run with the place are summed without a sort while a position has few places
+// (kRunning): each is one warp's work, and a longer one would be a long serial
+// sum on few warps.
+constexpr int64_t kRunning = 128;
+
 int table_gradient(lioncub_embed_t h, const lc::Places& at, lc::KeyKind kind, int64_t rows, const lioncub_rows* dout,
                    const lioncub_rows* base, const lioncub_rows* grad, const lc::DropArgs& drop, bool drop_on,
                    float factor, cudaStream_t s)
 {
-    lc::SortArgs so{};
-    so.at = at;
-    so.keys = static_cast<int32_t>(rows);
-    so.capacity = static_cast<int32_t>(h->max_tokens);
-    so.order = h->order;
-    so.sorted_key = h->order + h->max_tokens;
-    so.segment = h->segment;
-    so.total = h->status + 1;
-    so.status = h->status;
-    cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, kind, s); });
-    if (e != cudaSuccess)
-        return cuda_fail(h, e, "sort launch");
     lc::RowSumArgs su{};
     su.dout = rows_of(dout);
     su.base = rows_of(base);
     su.grad = rows_of(grad);
-    su.order = so.order;
-    su.sorted_key = so.sorted_key;
-    su.segment = so.segment;
-    su.total = so.total;
+    su.order = h->order;
+    su.sorted_key = h->order + h->max_tokens;
+    su.segment = h->segment;
+    su.total = h->status + 1;
     su.partial = h->partial;
     su.partial_stride = h->partial_stride;
     su.partial_rows = h->partial_rows;
+    su.arrived = h->arrived;
+    su.arrived_count = h->arrived_count;
     su.drop = drop;
     su.factor = factor;
     su.rows = static_cast<int32_t>(rows);
     su.dim = static_cast<int32_t>(h->dim);
     su.n = at.n;
     su.status = h->status;
+    const bool running = kind == lc::kKeyPosition && !at.positions && (at.n + at.seq_len - 1) / at.seq_len <= kRunning;
+    cudaError_t e;
+    if (!running) {
+        lc::SortArgs so{};
+        so.at = at;
+        so.keys = static_cast<int32_t>(rows);
+        so.capacity = static_cast<int32_t>(h->max_tokens);
+        so.order = h->order;
+        so.sorted_key = h->order + h->max_tokens;
+        so.segment = h->segment;
+        so.total = h->status + 1;
+        so.pairs = h->pairs;
+        so.tile_count = h->tile_count;
+        so.bucket_start = h->tile_count + h->tile_counts;
+        so.arrived = h->arrived;
+        so.arrived_count = lc::grad_stretches(at.n) * lc::grad_slabs(h->dim);
+        so.status = h->status;
+        e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, kind, s); });
+        if (e != cudaSuccess)
+            return cuda_fail(h, e, "sort launch");
+    }
     const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(base) && aligned_rows(grad);
-    e = launch(h, "embed_row_sums", [&] { return lc::launch_row_sums(su, dout->type, grad->type, vec, drop_on, s); });
+    e = launch(h, "embed_row_sums", [&] {
+        return lc::launch_row_sums(su, running ? &at : nullptr, dout->type, grad->type, vec, drop_on, s);
+    });
     return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "row sum launch");
 }
 
@@ -311,7 +333,7 @@ int run_dropout(const char* in_name, const char* out_name, int64_t rows, int64_t
             return fail(nullptr, LIONCUB_ERR_ARG, "%s overlaps an input without being it", out_name);
     lc::DropoutArgs a{};
     bool on = false;
-    rc = check_drop(nullptr, drop, &a.drop, &on);
+    rc = check_drop(nullptr, drop, cols, &a.drop, &on);
     if (rc != LIONCUB_OK)
         return rc;
     a.x = rows_of(x);
@@ -363,8 +385,13 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     h->positions = positions;
     h->max_tokens = max_tokens;
     h->scale = scale;
-    h->partial_rows = max_tokens > lc::kGradPiece ? 2 * lc::grad_stretches(max_tokens) : 0;
-    h->partial_stride = (dim + 3) / 4 * 4;
+    const int64_t keys = vocab > positions ? vocab : positions;
+    h->buckets = int64_t(1) << lc::sort_log_buckets(keys);
+    const bool tiled = max_tokens > lc::kDirectPlaces;
+    h->tile_counts = tiled ? lc::sort_max_tiles(max_tokens) * h->buckets : 0;
+    h->partial_rows = 2 * lc::grad_stretches(max_tokens);
+    h->partial_stride = lc::grad_slabs(dim) * int64_t(256);
+    h->arrived_count = lc::grad_stretches(max_tokens) * lc::grad_slabs(dim);
     h->fail_alloc_at = env_index("LIONCUB_FAIL_ALLOC");
     h->fail_launch_at = env_index("LIONCUB_FAIL_LAUNCH");
     cudaError_t e = cudaGetDevice(&h->device);
@@ -375,7 +402,13 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     if (e == cudaSuccess)
         e = guarded_alloc(h, &h->order, 2 * max_tokens);
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->segment, vocab > positions ? vocab : positions);
+        e = guarded_alloc(h, &h->segment, keys);
+    if (e == cudaSuccess)
+        e = guarded_alloc(h, &h->pairs, tiled ? max_tokens : 0);
+    if (e == cudaSuccess)
+        e = guarded_alloc(h, &h->tile_count, h->tile_counts + h->buckets + 1);
+    if (e == cudaSuccess)
+        e = guarded_alloc(h, &h->arrived, h->arrived_count);
     if (e == cudaSuccess)
         e = guarded_alloc(h, &h->partial, h->partial_rows * h->partial_stride);
     if (e == cudaSuccess)
@@ -413,7 +446,7 @@ int lioncub_embed_forward(lioncub_embed_t h, const lioncub_token_batch* batch, c
         (pos_table && overlap(*out, batch->n, *pos_table, h->positions, h->dim)))
         return fail(h, LIONCUB_ERR_ARG, "out overlaps a table");
     bool on = false;
-    rc = check_drop(h, drop, &a.drop, &on);
+    rc = check_drop(h, drop, h->dim, &a.drop, &on);
     if (rc == LIONCUB_OK)
         rc = check_device(h);
     if (rc != LIONCUB_OK)
@@ -455,13 +488,14 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
         return fail(h, LIONCUB_ERR_ARG, "grad and pos_grad overlap");
     lc::DropArgs d;
     bool on = false;
-    rc = check_drop(h, drop, &d, &on);
+    rc = check_drop(h, drop, h->dim, &d, &on);
     if (rc == LIONCUB_OK)
         rc = check_device(h);
-    if (rc == LIONCUB_OK)
-        rc = table_gradient(h, at, lc::kKeyToken, h->vocab, dout, base, grad, d, on, h->scale * d.rescale, stream);
+    // positions first: they read dout in order, and what fits L2 stays there for the tokens
     if (rc == LIONCUB_OK && pos_grad)
         rc = table_gradient(h, at, lc::kKeyPosition, h->positions, dout, pos_base, pos_grad, d, on, d.rescale, stream);
+    if (rc == LIONCUB_OK)
+        rc = table_gradient(h, at, lc::kKeyToken, h->vocab, dout, base, grad, d, on, h->scale * d.rescale, stream);
     return rc;
 }
 

@@ -17,7 +17,8 @@ constexpr int kStatusIndex = 8;
 // in [1, 65536], so T == 65536 keeps nothing without a case of its own (T == 0
 // is a launch without dropout).
 struct DropArgs {
-    uint64_t key;
+    uint64_t first;     // the generator's state for output 0
+    uint64_t row_step;  // from a row's states to the next row's (a width that is a multiple of 4)
     uint32_t limit;
     float rescale;
 };
@@ -46,16 +47,37 @@ struct LookupArgs {
     DropArgs drop;
     float scale;
     int32_t dim;
-    int32_t groups;  // column groups of the kernel's vector width in a row
+    int32_t slabs;  // set by launch_lookup
+    int64_t span;   // places of a sequence; likewise
     int* status;
 };
 
 // Which number a place is sorted by.
 enum KeyKind { kKeyToken = 0, kKeyPosition = 1 };
 
-// Segments longer than this are summed in pieces, cut at its multiples.
-constexpr int kGradPiece = 64;
+// Places a warp of the row sums takes; segments longer than this are summed in
+// pieces.
+constexpr int kGradPiece = 16;
 inline int64_t grad_stretches(int64_t n) { return (n + kGradPiece - 1) / kGradPiece; }
+inline int32_t grad_slabs(int64_t dim) { return static_cast<int32_t>((dim + 255) / 256); }
+
+// A batch of up to this many places is sorted in one launch.
+constexpr int64_t kDirectPlaces = 8192;
+// Buckets of the sort (a power of two, at most 1024 keys each), and places a
+// tile of its tiled form takes (at most 256 tiles).
+inline int sort_log_buckets(int64_t keys)
+{
+    int b = 8;
+    while ((int64_t(1024) << b) < keys)
+        ++b;
+    return b;
+}
+inline int64_t sort_tile(int64_t n)
+{
+    const int64_t t = (n + 255) / 256;
+    return t <= 1024 ? 1024 : (t + 255) / 256 * 256;
+}
+inline int64_t sort_max_tiles(int64_t n) { return n > 256 * 1024 ? 256 : (n + 1023) / 1024; }
 
 // The sort of a batch's places by key: order holds the places grouped by key,
 // ascending within a key, sorted_key their keys; segment[key] is the key's
@@ -68,6 +90,13 @@ struct SortArgs {
     int32_t* sorted_key;
     int2* segment;
     int32_t* total;
+    int2* pairs;            // tiled: (key, place) by bucket
+    int32_t* tile_count;    // tiled: keys of each (tile, bucket)
+    int32_t* bucket_start;  // tiled: buckets + 1 offsets into pairs
+    int32_t* arrived;       // the row sums' counters, zeroed here
+    int64_t arrived_count;
+    int64_t tile;           // set by launch_sort
+    int log_buckets;
     int* status;
 };
 
@@ -78,15 +107,17 @@ struct RowSumArgs {
     const int32_t* sorted_key;
     const int2* segment;
     const int32_t* total;
-    float* partial;          // two fp32 rows a stretch of kGradPiece places
-    int64_t partial_stride;  // dim rounded up to 16 bytes
+    float* partial;          // two fp32 rows for each stretch of kGradPiece places
+    int64_t partial_stride;  // 256 * slabs
     int64_t partial_rows;
+    int32_t* arrived;        // pieces done, for each (stretch a long segment begins in, slab)
+    int64_t arrived_count;
     DropArgs drop;
     float factor;
-    int32_t rows;    // rows of grad
+    int32_t rows;   // rows of grad
     int32_t dim;
-    int32_t groups;
-    int32_t n;       // rows of dout
+    int32_t slabs;  // set by launch_row_sums
+    int32_t n;      // rows of dout
     int* status;
 };
 
@@ -100,8 +131,11 @@ struct DropoutArgs {
 // vec: the matrices allow 16-byte moves of 8 columns (launch_dropout: their
 // starts and strides do); drop: dropout is on.
 cudaError_t launch_lookup(const LookupArgs& a, int table_type, int out_type, bool vec, bool drop, cudaStream_t s);
-cudaError_t launch_sort(const SortArgs& a, KeyKind kind, cudaStream_t s);
-cudaError_t launch_row_sums(const RowSumArgs& a, int dout_type, int grad_type, bool vec, bool drop, cudaStream_t s);
+cudaError_t launch_sort(SortArgs a, KeyKind kind, cudaStream_t s);
+// running: the places of a batch whose positions run with the place (the rows
+// of grad are positions, and no sort is read), or null.
+cudaError_t launch_row_sums(RowSumArgs a, const Places* running, int dout_type, int grad_type, bool vec, bool drop,
+                            cudaStream_t s);
 cudaError_t launch_dropout(const DropoutArgs& a, int x_type, int out_type, bool vec, bool drop, cudaStream_t s);
 
 // Column groups of a row -> thread blocks: TX threads along a row, TY rows a

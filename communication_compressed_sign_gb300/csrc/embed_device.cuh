@@ -28,6 +28,10 @@ struct Group<__nv_bfloat16, 8> {
     {
         raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + e);
     }
+    __device__ __forceinline__ void store(void* base, int64_t e) const
+    {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e) = raw;
+    }
     __device__ __forceinline__ void unpack(float (&x)[8]) const
     {
         x[0] = bf16_bits_lo(raw.x); x[1] = bf16_bits_hi(raw.x);
@@ -45,6 +49,12 @@ struct Group<float, 8> {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + e);
         a = p[0];
         b = p[1];
+    }
+    __device__ __forceinline__ void store(void* base, int64_t e) const
+    {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + e);
+        p[0] = a;
+        p[1] = b;
     }
     __device__ __forceinline__ void unpack(float (&x)[8]) const
     {
@@ -85,30 +95,191 @@ __device__ __forceinline__ void store_row(void* base, int64_t e, const float (&x
 }
 
 // --- the dropout mask -------------------------------------------------------------
+//
+// One output of the generator serves 4 elements, 16 bits each: a draw per
+// element would make bf16 streams bound by integer instructions instead of
+// memory.  Output k comes from the state key + (k + 1) * gamma, so states are
+// stepped by additions and the product with gamma is paid once a row or thread.
 
-// Bit j set: element e + j stays (e a multiple of 8 when V == 8).  One output
-// of the generator serves 4 elements, 16 bits each: two 64-bit products for 4
-// elements, where a draw per element would make bf16 streams bound by integer
-// instructions instead of memory.
-template <int V>
-__device__ __forceinline__ uint32_t keep_bits(const DropArgs& d, uint64_t e)
+// Whether the two 16-bit fields of a word stay.  The upper one decides the
+// comparison of the whole word by itself, the lower one is moved up.  (The
+// two-halves maximum instruction that also gives both comparisons measured 12 %
+// slower on a bf16 dropout.)
+__device__ __forceinline__ bool lower_stays(const DropArgs& d, uint32_t w) { return w << 16 > d.limit; }
+__device__ __forceinline__ bool upper_stays(const DropArgs& d, uint32_t w) { return w > d.limit; }
+
+// f(k, whether element k stays) for 8 elements whose first output has the
+// state z (the element number is a multiple of 4).
+template <typename F>
+__device__ __forceinline__ void for_kept8(const DropArgs& d, uint64_t z, F&& f)
 {
-    if constexpr (V == 8) {
-        uint32_t keep = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint64_t u = splitmix64(d.key, (e >> 2) + h);
-            const uint32_t lo = static_cast<uint32_t>(u), hi = static_cast<uint32_t>(u >> 32);
-            keep |= (lo << 16 > d.limit ? 1u : 0u) << (4 * h);
-            keep |= (lo > d.limit ? 2u : 0u) << (4 * h);
-            keep |= (hi << 16 > d.limit ? 4u : 0u) << (4 * h);
-            keep |= (hi > d.limit ? 8u : 0u) << (4 * h);
-        }
-        return keep;
+    for (int h = 0; h < 2; ++h) {
+        const uint64_t u = splitmix64_mix(z + h * kSplitMix64Step);
+        const uint32_t lo = static_cast<uint32_t>(u), hi = static_cast<uint32_t>(u >> 32);
+        f(4 * h, lower_stays(d, lo));
+        f(4 * h + 1, upper_stays(d, lo));
+        f(4 * h + 2, lower_stays(d, hi));
+        f(4 * h + 3, upper_stays(d, hi));
+    }
+}
+
+__device__ __forceinline__ bool stays1(const DropArgs& d, uint64_t e)
+{
+    const uint64_t u = splitmix64_mix(d.first + (e >> 2) * kSplitMix64Step);
+    return lower_stays(d, static_cast<uint32_t>(u >> (16 * (e & 3))));
+}
+
+// --- a warp on a slab of 256 columns -------------------------------------------------
+//
+// Each lane holds 8 of the slab's columns: 8 in a row where the matrices allow
+// 16-byte moves (VEC), else every 32nd from its own, so that a warp's scalar
+// moves are contiguous.
+
+template <bool VEC>
+struct Slab;
+
+template <>
+struct Slab<true> {
+    int col;
+    bool on;
+    __device__ __forceinline__ Slab(int slab, int lane, int dim) : col(slab * 256 + lane * 8), on(col < dim) {}
+};
+
+template <>
+struct Slab<false> {
+    int col;
+    int count;  // columns of this lane: col, col + 32, ...
+    __device__ __forceinline__ Slab(int slab, int lane, int dim) : col(slab * 256 + lane)
+    {
+        const int left = dim - col;
+        count = left <= 0 ? 0 : (left > 224 ? 8 : (left + 31) / 32);
+    }
+};
+
+// The mask of a lane's 8 columns of a slab, row by row.
+template <bool VEC>
+struct SlabMask;
+
+// dim is a multiple of 4 here, so a row's first output is a whole step from
+// the next row's: state = first + row * d.row_step + column / 4 * gamma.
+template <>
+struct SlabMask<true> {
+    const DropArgs& d;
+    uint64_t z;
+    __device__ __forceinline__ SlabMask(const DropArgs& args, int slab, int lane, int, void*)
+        : d(args), z(args.first + static_cast<uint64_t>(slab * 64 + lane * 2) * kSplitMix64Step)
+    {
+    }
+    template <typename F>
+    __device__ __forceinline__ void row(int64_t i, F&& f)
+    {
+        for_kept8(d, z + static_cast<uint32_t>(i) * d.row_step, f);
+    }
+};
+
+// A row may begin inside an output's four elements.  The warp draws the 65
+// outputs that a slab's 256 elements can touch once, into shared memory; there
+// the elements' fields lie one after the other, 16 bits each.  Two buffers
+// take turns, so one barrier a row is enough.
+template <>
+struct SlabMask<false> {
+    struct Buffer {
+        uint64_t outputs[2][66];
+    };
+    const DropArgs& d;
+    Buffer* buffer;
+    int64_t dim;
+    int first_col, lane, turn;
+    __device__ __forceinline__ SlabMask(const DropArgs& args, int slab, int l, int width, void* shared)
+        : d(args), buffer(static_cast<Buffer*>(shared)), dim(width), first_col(slab * 256), lane(l), turn(0)
+    {
+    }
+    template <typename F>
+    __device__ __forceinline__ void row(int64_t i, F&& f)
+    {
+        const uint64_t e = static_cast<uint64_t>(i * dim + first_col);
+        const int off = static_cast<int>(e & 3);
+        const uint64_t z = d.first + ((e >> 2) + lane) * kSplitMix64Step;
+        uint64_t* out = buffer->outputs[turn];
+        out[lane] = splitmix64_mix(z);
+        out[lane + 32] = splitmix64_mix(z + 32 * kSplitMix64Step);
+        if (off != 0 && lane == 0)
+            out[64] = splitmix64_mix(z + 64 * kSplitMix64Step);
+        __syncwarp();
+        const uint16_t* field = reinterpret_cast<const uint16_t*>(out) + off + lane;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            f(k, lower_stays(d, field[32 * k]));
+        turn ^= 1;
+    }
+};
+// Shared memory of a block's warps' masks.
+template <bool VEC>
+constexpr size_t mask_bytes(int warps)
+{
+    return VEC ? 0 : warps * sizeof(SlabMask<false>::Buffer);
+}
+
+// A lane's elements of the row that starts at element e.
+template <typename T, bool VEC>
+struct SlabGroup;
+
+template <typename T>
+struct SlabGroup<T, true> {
+    Group<T, 8> g;
+    __device__ __forceinline__ void load(const Slab<true>& c, const void* base, int64_t e)
+    {
+        if (c.on)
+            g.load(base, e + c.col);
+        else
+            g = Group<T, 8>{};
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const { g.unpack(x); }
+    __device__ __forceinline__ void store(const Slab<true>& c, void* base, int64_t e) const
+    {
+        if (c.on)
+            g.store(base, e + c.col);
+    }
+};
+
+template <typename T>
+struct SlabGroup<T, false> {
+    T x[8];
+    __device__ __forceinline__ void load(const Slab<false>& c, const void* base, int64_t e)
+    {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = k < c.count ? static_cast<const T*>(base)[e + c.col + 32 * k] : T(0.0f);
+    }
+    __device__ __forceinline__ void unpack(float (&y)[8]) const
+    {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            y[k] = static_cast<float>(x[k]);
+    }
+    __device__ __forceinline__ void store(const Slab<false>& c, void* base, int64_t e) const
+    {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < c.count)
+                static_cast<T*>(base)[e + c.col + 32 * k] = x[k];
+    }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_slab(const Slab<VEC>& c, void* base, int64_t e, const float (&x)[8])
+{
+    if constexpr (VEC) {
+        if (c.on)
+            store_row<T, 8>(base, e + c.col, x);
     } else {
-        const uint64_t u = splitmix64(d.key, e >> 2);
-        const uint32_t f = static_cast<uint32_t>(u >> (16 * (e & 3)));
-        return f << 16 > d.limit ? 1u : 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < c.count) {
+                const float y[1] = {x[k]};
+                store_row<T, 1>(base, e + c.col + 32 * k, y);
+            }
     }
 }
 

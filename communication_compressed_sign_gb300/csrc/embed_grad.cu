@@ -1,359 +1,354 @@
-// embed_grad.cu -- gradient of the embedding lookup:
-//   grad[v,:] = base[v,:] + f * sum over places i with key_i == v of keep * dout[i,:].
+// embed_grad.cu -- gradient of the embedding lookup from the sorted places:
+//   grad[v,:] = base[v,:] + factor * sum over places i with key_i == v of keep * dout[i,:].
 //
-// A sort of the places by key, then one thread per (row, column group) that adds
-// the rows of dout of its key's places in ascending order and writes the row
-// once -- rows without a place as zeros (or base), so the dense gradient needs
-// no clearing pass and no atomics, and the order of every sum depends on the
-// batch alone.
+// Every row of the dense gradient is written once -- rows without a place as
+// zeros (or base) -- so there is no clearing pass, and no float atomics: the
+// order of every sum depends on the batch alone.
+//
+// The unit of work is one warp on a slab of 256 columns.
+//   walk   a stretch of kGradPiece entries of `order`: the warp adds the rows of
+//          dout of the segments that begin there, several rows in flight
+//          whatever the segments' lengths, and writes a row of grad at each
+//          segment's end.  A segment of up to kGradPiece places belongs to the
+//          stretch it begins in.  A longer one is cut at the stretches' bounds:
+//          each warp leaves an fp32 partial, and the last to arrive (an integer
+//          counter) adds the partials in order.  So units are alike in size
+//          however skewed the tokens are.
+//   fill   rows without a place.
+// Bound by memory: dout is read once and grad written once.
 #include "embed_device.cuh"
 
 namespace lc {
 namespace {
 
-// --- sort ------------------------------------------------------------------------
-//
-// Counting sort without communication between blocks: block r owns the keys
-// with key % R == r (interleaved, so that frequent low ids spread over the
-// blocks) and reads all keys itself: it counts those of lower blocks, which
-// gives the base of its part of `order`, and its own per key and warp.  After
-// a scan it reads the keys again and places its own.  Each warp takes a
-// contiguous slice of the places in order, so places stay ascending within a
-// key.
-constexpr int kSortThreads = 512;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortKeys = kSortThreads;  // keys a block can own: one per thread in the scan
+constexpr int kSumThreads = 256;
+constexpr int kWarpsPerBlock = kSumThreads / 32;
+constexpr int kFillRows = 8;  // rows of grad a fill warp looks at
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kInFlight = 4;   // rows of dout a warp loads before it adds them
 
-template <int KIND>
-__device__ __forceinline__ int32_t sort_key(const SortArgs& a, int64_t i, int* status)
+// The warp's share of the block's shared memory for its mask.
+template <bool VEC, bool DROP>
+__device__ __forceinline__ void* warp_buffer(int warp)
 {
-    const int32_t t = token_at(a.at, i, status);
-    if (KIND == kKeyToken || t < 0)
-        return t;
-    return position_at(a.at, i, status);
+    if constexpr (!VEC && DROP) {
+        __shared__ SlabMask<false>::Buffer buffers[kWarpsPerBlock];
+        return &buffers[warp];
+    }
+    return nullptr;
 }
 
-template <int KIND>
-__global__ void __launch_bounds__(kSortThreads) k_sort(const SortArgs a, int log_blocks)
+// Adds rows of dout to a running sum and writes it where the key changes.
+template <typename DT, typename GT, bool VEC, bool DROP>
+struct Walker {
+    const RowSumArgs& a;
+    const Slab<VEC> cols;
+    SlabMask<VEC> mask;
+    float sum[8];
+
+    __device__ __forceinline__ Walker(const RowSumArgs& args, int slab, int lane, void* shared)
+        : a(args), cols(slab, lane, args.dim), mask(args.drop, slab, lane, args.dim, shared)
+    {
+        clear();
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sum[k] = 0.0f;
+    }
+    __device__ __forceinline__ void add(const SlabGroup<DT, VEC>& x, int32_t i)
+    {
+        float y[8];
+        x.unpack(y);
+        if constexpr (DROP) {
+            mask.row(i, [&](int k, bool keep) {
+                if (keep)
+                    sum[k] = __fadd_rn(sum[k], y[k]);
+            });
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sum[k] = __fadd_rn(sum[k], y[k]);
+        }
+    }
+    // grad[v] = base[v] + factor * sum
+    __device__ __forceinline__ void finish(int64_t v)
+    {
+        if (!index_ok(a.status, v >= 0 && v < a.rows))
+            return;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sum[k] = __fmul_rn(a.factor, sum[k]);
+        if (a.base.data) {
+            SlabGroup<GT, VEC> b;
+            b.load(cols, a.base.data, v * a.base.stride);
+            float y[8];
+            b.unpack(y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sum[k] = __fadd_rn(y[k], sum[k]);
+        }
+        store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, sum);
+    }
+    // One piece of a long segment: stores its partial and, if it is the last of
+    // the segment's pieces to arrive, gathers the segment's sum.
+    __device__ __forceinline__ bool gather(int2 seg, int stretch, int slab, int lane)
+    {
+        const int first = seg.x / kGradPiece, pieces = (seg.y - 1) / kGradPiece - first + 1;
+        // slot 1 of the stretch the segment begins in, slot 0 of the later ones
+        const int64_t row = 2 * static_cast<int64_t>(stretch) + (stretch == first ? 1 : 0);
+        const int64_t counter = static_cast<int64_t>(first) * a.slabs + slab;
+        if (!index_ok(a.status, row < a.partial_rows && counter < a.arrived_count))
+            return false;
+        const int64_t column = slab * 256 + lane * 8;  // partial rows are whole slabs
+        store_row<float, 8>(a.partial, row * a.partial_stride + column, sum);
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0)
+            before = atomicAdd(&a.arrived[counter], 1);
+        if (__shfl_sync(kAll, before, 0) != pieces - 1)
+            return false;
+        __threadfence();
+        const float* p = a.partial + (2 * static_cast<int64_t>(first) + 1) * a.partial_stride + column;
+        clear();
+        add_partial(p);
+        p += a.partial_stride;
+#pragma unroll 4
+        for (int q = 1; q < pieces; ++q) {
+            add_partial(p);
+            p += 2 * a.partial_stride;
+        }
+        return true;
+    }
+    // Columns are where add() has them: only lanes move as a whole, so a
+    // partial row may hold them in any order as long as it is always the same.
+    __device__ __forceinline__ void add_partial(const float* p)
+    {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p)), y = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+        sum[0] = __fadd_rn(sum[0], x.x); sum[1] = __fadd_rn(sum[1], x.y);
+        sum[2] = __fadd_rn(sum[2], x.z); sum[3] = __fadd_rn(sum[3], x.w);
+        sum[4] = __fadd_rn(sum[4], y.x); sum[5] = __fadd_rn(sum[5], y.y);
+        sum[6] = __fadd_rn(sum[6], y.z); sum[7] = __fadd_rn(sum[7], y.w);
+    }
+};
+
+// Rows [row0, row0 + kFillRows) that have no place: zeros, or base.
+template <typename GT, bool VEC, typename Empty>
+__device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int lane, Empty&& empty)
 {
-    __shared__ int cnt[kSortWarps][kSortKeys];
-    __shared__ int part[kSortWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int mask = (1 << log_blocks) - 1;
-    const int mine = blockIdx.x;
-    const int owned = mine < a.keys ? ((a.keys - 1 - mine) >> log_blocks) + 1 : 0;
-    for (int k = tid; k < kSortWarps * kSortKeys; k += kSortThreads)
-        (&cnt[0][0])[k] = 0;
-    __syncthreads();
-
-    const int64_t slice = (a.at.n + kSortThreads - 1) / kSortThreads * 32;
-    const int64_t lo = warp * slice, hi = min(lo + slice, static_cast<int64_t>(a.at.n));
-    int below = 0;
-    int* status = mine == 0 ? a.status : nullptr;
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-        const int32_t key = sort_key<KIND>(a, i, status);
-        if (key < 0)
-            continue;
-        const int b = key & mask;
-        below += b < mine ? 1 : 0;
-        if (b == mine)
-            atomicAdd(&cnt[warp][key >> log_blocks], 1);
-    }
-    below = __reduce_add_sync(0xffffffffu, below);
-    if (lane == 0)
-        part[warp] = below;
-    __syncthreads();
-    int base = 0;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w)
-        base += part[w];
-    __syncthreads();
-
-    // thread k: key k's total, then its start, then a start for each warp
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w)
-        total += cnt[w][tid];
-    int run = total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, run, o);
-        run += lane >= o ? up : 0;
-    }
-    if (lane == 31)
-        part[warp] = run;
-    __syncthreads();
-    int start = base + run - total;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w)
-        start += w < warp ? part[w] : 0;
-    if (tid < owned) {
-        const int32_t key = (tid << log_blocks) | mine;
-        if (index_ok(a.status, key < a.keys && start + total <= a.capacity))
-            a.segment[key] = make_int2(start, start + total);
-    }
-    if (mine == (1 << log_blocks) - 1 && tid == kSortThreads - 1)
-        *a.total = start + total;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) {
-        const int c = cnt[w][tid];
-        cnt[w][tid] = start;
-        start += c;
-    }
-    __syncthreads();
-
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int32_t key = i < hi ? sort_key<KIND>(a, i, nullptr) : -1;
-        const bool take = key >= 0 && (key & mask) == mine;
-        const unsigned takers = __ballot_sync(0xffffffffu, take);
-        if (take) {
-            const int k = key >> log_blocks;
-            const unsigned same = __match_any_sync(takers, k);
-            const int at = cnt[warp][k] + __popc(same & ((1u << lane) - 1));
-            __syncwarp(takers);
-            if ((same >> lane) == 1u)  // the last lane with this key
-                cnt[warp][k] = at + 1;
-            __syncwarp(takers);
-            if (index_ok(a.status, at >= 0 && at < a.capacity)) {
-                a.order[at] = static_cast<int32_t>(i);
-                a.sorted_key[at] = key;
+    const int64_t row = row0 + lane;
+    unsigned todo = __ballot_sync(kAll, lane < kFillRows && row < a.rows && empty(row));
+    while (todo) {
+        const int64_t v = row0 + __ffs(todo) - 1;
+        todo &= todo - 1;
+        for (int slab = 0; slab < a.slabs; ++slab) {
+            const Slab<VEC> cols(slab, lane, a.dim);
+            if (a.base.data) {
+                SlabGroup<GT, VEC> b;
+                b.load(cols, a.base.data, v * a.base.stride);
+                b.store(cols, a.grad.data, v * a.grad.stride);
+            } else {
+                const float zero[8] = {};
+                store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, zero);
             }
         }
-        __syncwarp();
     }
 }
 
-// --- row sums ----------------------------------------------------------------------
-//
-// Rows of up to kLong places are added by the threads of their row.  Longer
-// segments would leave a few threads adding thousands of rows (token
-// frequencies follow a power law), so they are cut at the multiples of kLong
-// of `order`: each piece is summed by a row of threads of its own into an fp32
-// partial, and a second launch adds a segment's partials in order.  A stretch
-// of kLong entries holds at most two pieces of long segments: the end of one
-// that began before it (slot 0) and the begin of one that goes on (slot 1).
-constexpr int kSumThreads = 256;
-constexpr int kLong = kGradPiece;
-constexpr int kInFlight = 4;  // rows of dout a thread loads before it adds them
-
-// Adds the rows of dout of the places order[lo..hi) to sum, in order.
-template <typename DT, int V, bool DROP>
-__device__ __forceinline__ void add_places(const RowSumArgs& a, int lo, int hi, int32_t j, float (&sum)[V])
+// The position of the n-th (from 0) set bit of a word that has more than n.
+__device__ __forceinline__ int nth_bit(unsigned word, int n)
 {
-    for (int p = lo; p < hi; p += kInFlight) {
-        Group<DT, V> x[kInFlight];
-        int64_t i[kInFlight];
+    int at = 0;
 #pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            i[u] = p + u < hi ? a.order[p + u] : -1;
-            if (!index_ok(a.status, i[u] < a.n && (i[u] >= 0 || p + u >= hi)))
-                i[u] = -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kInFlight; ++u)
-            if (i[u] >= 0)
-                x[u].load(a.dout.data, i[u] * a.dout.stride + j);
-#pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            if (i[u] < 0)
-                continue;
-            const uint32_t keep = DROP ? keep_bits<V>(a.drop, static_cast<uint64_t>(i[u]) * a.dim + j) : 0xffu;
-            float y[V];
-            x[u].unpack(y);
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (keep >> k & 1u)
-                    sum[k] = __fadd_rn(sum[k], y[k]);
+    for (int half = 16; half > 0; half >>= 1) {
+        const int low = __popc(word & ((1u << half) - 1));
+        if (n >= low) {
+            n -= low;
+            word >>= half;
+            at += half;
         }
     }
+    return at;
 }
 
-// grad[v, j..j+V) = base + factor * sum.
-template <typename GT, int V>
-__device__ __forceinline__ void finish_row(const RowSumArgs& a, int64_t v, int32_t j, float (&sum)[V])
-{
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-        sum[k] = __fmul_rn(a.factor, sum[k]);
-    if (a.base.data) {
-        float b[V];
-        load_row<GT, V>(a.base.data, v * a.base.stride + j, b);
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            sum[k] = __fadd_rn(b[k], sum[k]);
+// Blocks that walk and blocks that fill, spread evenly over the grid: fills are
+// bound by memory, walks with dropout by instructions, so they run side by side.
+struct Mix {
+    uint64_t share;  // fill blocks / all blocks, in 2^-32
+    __host__ __device__ __forceinline__ unsigned fills_before(unsigned block) const
+    {
+        return static_cast<unsigned>((block * share) >> 32);
     }
-    store_row<GT, V>(a.grad.data, v * a.grad.stride + j, sum);
-}
+};
 
-// The pieces of long segments in entries [c * kLong, (c + 1) * kLong) of
-// order: [lo[s], hi[s]) for slot s, empty when there is none.  key[s]: whose.
-__device__ __forceinline__ void pieces_of(const RowSumArgs& a, int64_t c, int total, int (&lo)[2], int (&hi)[2], int (&key)[2])
+// Walk blocks: stretches of the sorted places; fill blocks: rows without a
+// place (none in place).
+template <typename DT, typename GT, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_row_sums(const RowSumArgs a, const Mix mix)
 {
-    const int begin = static_cast<int>(c * kLong), end = static_cast<int>(min((c + 1) * kLong, static_cast<int64_t>(total)));
-    lo[0] = hi[0] = lo[1] = hi[1] = 0;
-    key[0] = key[1] = -1;
-    if (begin >= end)
-        return;
-    const int first = a.sorted_key[begin], last = a.sorted_key[end - 1];
-    const int2 f = a.segment[first], l = a.segment[last];
-    if (f.x < begin && f.y - f.x > kLong) {
-        lo[0] = begin;
-        hi[0] = min(f.y, end);
-        key[0] = first;
-    }
-    if (l.x >= begin && l.y - l.x > kLong) {
-        lo[1] = l.x;
-        hi[1] = end;
-        key[1] = last;
-    }
-}
-
-// Blocks [0, piece_blocks) of a column slab sum pieces, the others rows.
-template <typename DT, typename GT, int V, bool DROP>
-__global__ void __launch_bounds__(kSumThreads) k_row_sums(const RowSumArgs a, unsigned piece_blocks)
-{
-    const int32_t g = blockIdx.y * blockDim.x + threadIdx.x;
-    if (g >= a.groups)
-        return;
-    const int32_t j = g * V;
-    if (blockIdx.x < piece_blocks) {
-        const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-        int lo[2], hi[2], key[2];
-        pieces_of(a, c, *a.total, lo, hi, key);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (lo[s] == hi[s])
-                continue;
-            float sum[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                sum[k] = 0.0f;
-            add_places<DT, V, DROP>(a, lo[s], hi[s], j, sum);
-            if (index_ok(a.status, 2 * c + s < a.partial_rows))
-                store_row<float, V>(a.partial, (2 * c + s) * a.partial_stride + j, sum);
-        }
-        return;
-    }
-    const int64_t v = static_cast<int64_t>(blockIdx.x - piece_blocks) * blockDim.y + threadIdx.y;
-    if (v >= a.rows)
-        return;
-    const int2 seg = a.segment[v];
-    if (seg.y - seg.x > kLong || (seg.x == seg.y && a.base.data == a.grad.data))
-        return;
-    float sum[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-        sum[k] = 0.0f;
-    add_places<DT, V, DROP>(a, seg.x, seg.y, j, sum);
-    finish_row<GT, V>(a, v, j, sum);
-}
-
-// Adds the partials of the long segment that begins in stretch c, if one does:
-// a block's 8 warps each add a contiguous share of its pieces in order, warp 0
-// the shares in order.
-constexpr int kJoinWarps = 8;
-template <typename GT, int V>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_join_pieces(const RowSumArgs a)
-{
-    __shared__ float share[kJoinWarps][32][V + 1];
-    const int64_t c = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int total = *a.total;
-    int lo[2], hi[2], key[2];
-    pieces_of(a, c, total, lo, hi, key);
-    // a segment that begins exactly at a stretch, or inside it
-    if (key[1] < 0)
+    const unsigned fills = mix.fills_before(blockIdx.x);
+    if (mix.fills_before(blockIdx.x + 1) != fills) {
+        const int64_t row0 = (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows;
+        fill_rows<GT, VEC>(a, row0, lane, [&](int64_t v) {
+            const int2 seg = a.segment[v];
+            return seg.x == seg.y;
+        });
         return;
-    const int2 seg = a.segment[key[1]];
-    const int64_t pieces = (seg.y - 1) / kLong - c + 1;
-    const int64_t each = (pieces + kJoinWarps - 1) / kJoinWarps;
-    const int64_t from = min(warp * each, pieces), to = min(from + each, pieces);
-    const int32_t g = blockIdx.y * 32 + lane;
-    float sum[V];
+    }
+    const int64_t unit = static_cast<int64_t>(blockIdx.x - fills) * kWarpsPerBlock + warp;
+    const int stretch = static_cast<int>(unit / a.slabs);  // places and so stretches fit 31 bits
+    const int slab = static_cast<int>(unit - static_cast<int64_t>(stretch) * a.slabs);
+    const int total = *a.total;
+    if (static_cast<int64_t>(stretch) * kGradPiece >= total)
+        return;
+    const int begin = stretch * kGradPiece, end = min(begin + kGradPiece, total);
+    const int32_t key0 = a.sorted_key[begin], key1 = a.sorted_key[end - 1];
+    if (!index_ok(a.status, key0 >= 0 && key0 < a.rows && key1 >= 0 && key1 < a.rows))
+        return;
+    const int2 seg0 = a.segment[key0], seg1 = a.segment[key1];
+    const bool tail = seg0.x < begin && seg0.y - seg0.x > kGradPiece;   // a long segment goes on here
+    const bool head = seg1.x >= begin && seg1.y - seg1.x > kGradPiece;  // a long segment begins here
+    // short segments: one that began before belongs there, one that begins here is taken to its end
+    const int from = seg0.x < begin ? seg0.y : begin, to = head ? seg1.x : (seg1.x < begin ? begin : seg1.y);
+
+    Walker<DT, GT, VEC, DROP> w(a, slab, lane, warp_buffer<VEC, DROP>(warp));
+#pragma unroll 1
+    for (int part = 0; part < 3; ++part) {  // the long segment's end, short segments, a long segment's begin
+        if (part == 0 ? !tail : part == 2 && !head)
+            continue;
+        const int lo = part == 0 ? begin : part == 1 ? from : seg1.x;
+        const int hi = part == 0 ? min(seg0.y, end) : part == 1 ? to : end;
+        if (lo >= hi)
+            continue;
+        w.clear();
+        int32_t current = -1;
+#pragma unroll 1
+        for (int p0 = lo; p0 < hi; p0 += 32) {
+            const int mine = p0 + lane;
+            const int32_t my_place = mine < hi ? a.order[mine] : 0;
+            const int32_t my_key = mine < hi ? a.sorted_key[mine] : 0;
+            if (!__all_sync(kAll, index_ok(a.status, my_place >= 0 && my_place < a.n)))
+                return;
+            const int here = min(32, hi - p0);
+            const int32_t above = __shfl_up_sync(kAll, my_key, 1);
+            const int32_t key_before = lane == 0 ? current : above;
+            const unsigned begins = __ballot_sync(kAll, my_key != key_before);
+#pragma unroll 1
+            for (int q = 0; q < here; q += kInFlight) {
+                SlabGroup<DT, VEC> x[kInFlight];
+                int32_t place[kInFlight];
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-        sum[k] = 0.0f;
-    if (g < a.groups) {
-        for (int64_t q = from; q < to; q += kInFlight) {
-            float x[kInFlight][V];
+                for (int u = 0; u < kInFlight; ++u) {  // past the end the last row again: no branch between the loads
+                    place[u] = __shfl_sync(kAll, my_place, min(q + u, here - 1));
+                    x[u].load(w.cols, a.dout.data, static_cast<uint32_t>(place[u]) * a.dout.stride);
+                }
+#pragma unroll
+                for (int u = 0; u < kInFlight; ++u) {
+                    if (q + u >= here)
+                        break;
+                    if (begins >> (q + u) & 1u) {
+                        if (current >= 0) {
+                            w.finish(current);
+                            w.clear();
+                        }
+                        current = __shfl_sync(kAll, my_key, q + u);
+                    }
+                    w.add(x[u], place[u]);
+                }
+            }
+        }
+        if (part == 1 || w.gather(part == 0 ? seg0 : seg1, stretch, slab, lane))
+            w.finish(current);
+    }
+}
+
+// Positions that run with the place, first + i % seq_len: row q's places are
+// q - first, q - first + seq_len, ... and need no sort.  Walk blocks: rows that
+// have places; fill blocks: rows that have none.
+template <typename DT, typename GT, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_running_row_sums(const RowSumArgs a, const Places at, const Mix mix)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int span = static_cast<int>(min(at.seq_len, static_cast<int64_t>(at.n)));
+    const unsigned fills = mix.fills_before(blockIdx.x);
+    if (mix.fills_before(blockIdx.x + 1) != fills) {
+        const int64_t row0 = (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows;
+        fill_rows<GT, VEC>(a, row0, lane, [&](int64_t v) { return v < at.first || v >= at.first + span; });
+        return;
+    }
+    const int64_t unit = static_cast<int64_t>(blockIdx.x - fills) * kWarpsPerBlock + warp;
+    const int64_t place0 = unit / a.slabs;
+    const int slab = static_cast<int>(unit - place0 * a.slabs);
+    if (place0 >= span)
+        return;
+    Walker<DT, GT, VEC, DROP> w(a, slab, lane, warp_buffer<VEC, DROP>(warp));
+    for (int64_t p0 = place0; p0 < at.n; p0 += 32 * at.seq_len) {
+        const int64_t mine = p0 + lane * at.seq_len;
+        const unsigned there = __ballot_sync(kAll, mine < at.n && token_at(at, mine, nullptr) >= 0);
+        const int here = __popc(there);
+        const int32_t my_place = static_cast<int32_t>(p0 + nth_bit(there, lane) * at.seq_len);  // lane l: the l-th there
+#pragma unroll 1
+        for (int q = 0; q < here; q += kInFlight) {
+            SlabGroup<DT, VEC> x[kInFlight];
+            int32_t place[kInFlight];
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {
-                // slot 1 of the stretch it begins in, slot 0 of the later ones
-                const int64_t row = 2 * (c + q + u) + (q + u == 0 ? 1 : 0);
-                if (q + u < to && index_ok(a.status, row < a.partial_rows))
-                    load_row<float, V>(a.partial, row * a.partial_stride + g * V, x[u]);
+                place[u] = __shfl_sync(kAll, my_place, min(q + u, here - 1));
+                x[u].load(w.cols, a.dout.data, static_cast<uint32_t>(place[u]) * a.dout.stride);
             }
 #pragma unroll
-            for (int u = 0; u < kInFlight; ++u)
-                if (q + u < to)
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        sum[k] = __fadd_rn(sum[k], x[u][k]);
+            for (int u = 0; u < kInFlight; ++u) {
+                if (q + u >= here)
+                    break;
+                w.add(x[u], place[u]);
+            }
         }
     }
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-        share[warp][lane][k] = sum[k];
-    __syncthreads();
-    if (warp != 0 || g >= a.groups)
-        return;
-    for (int w = 1; w < kJoinWarps; ++w)
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            sum[k] = __fadd_rn(sum[k], share[w][lane][k]);
-    finish_row<GT, V>(a, key[1], g * V, sum);
+    w.finish(at.first + place0);
 }
 
-template <typename DT, typename GT, int V>
-cudaError_t launch_v(const RowSumArgs& a, bool drop, cudaStream_t s)
+unsigned blocks_for(int64_t warps) { return static_cast<unsigned>((warps + kWarpsPerBlock - 1) / kWarpsPerBlock); }
+
+template <typename DT, typename GT, bool VEC, bool DROP>
+cudaError_t launch_k(const RowSumArgs& a, const Places* running, cudaStream_t s)
 {
-    RowGrid g = row_grid(a.rows, a.groups, kSumThreads);
-    const int64_t stretches = a.n > kLong ? grad_stretches(a.n) : 0;  // no segment is long otherwise
-    const unsigned piece_blocks = static_cast<unsigned>((stretches + g.block.y - 1) / g.block.y);
-    g.grid.x += piece_blocks;
-    if (drop)
-        k_row_sums<DT, GT, V, true><<<g.grid, g.block, 0, s>>>(a, piece_blocks);
+    const int64_t units =
+        (running ? (running->seq_len < running->n ? running->seq_len : running->n) : grad_stretches(a.n)) * a.slabs;
+    const bool in_place = a.base.data == a.grad.data;
+    const unsigned fill = in_place ? 0 : blocks_for((a.rows + kFillRows - 1) / kFillRows);
+    const unsigned blocks = blocks_for(units) + fill;
+    if (blocks == 0)
+        return cudaSuccess;
+    const Mix mix = {((static_cast<uint64_t>(fill) << 32) + blocks - 1) / blocks};
+    if (running)
+        k_running_row_sums<DT, GT, VEC, DROP><<<blocks, kSumThreads, 0, s>>>(a, *running, mix);
     else
-        k_row_sums<DT, GT, V, false><<<g.grid, g.block, 0, s>>>(a, piece_blocks);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && stretches > 0) {
-        const dim3 grid(static_cast<unsigned>(stretches), static_cast<unsigned>((a.groups + 31) / 32));
-        k_join_pieces<GT, V><<<grid, kJoinWarps * 32, 0, s>>>(a);
-        e = cudaGetLastError();
-    }
-    return e;
+        k_row_sums<DT, GT, VEC, DROP><<<blocks, kSumThreads, 0, s>>>(a, mix);
+    return cudaGetLastError();
 }
 
 template <typename DT, typename GT>
-cudaError_t launch_t(RowSumArgs a, bool vec, bool drop, cudaStream_t s)
+cudaError_t launch_t(const RowSumArgs& a, const Places* running, bool vec, bool drop, cudaStream_t s)
 {
-    a.groups = vec ? a.dim / 8 : a.dim;
-    return vec ? launch_v<DT, GT, 8>(a, drop, s) : launch_v<DT, GT, 1>(a, drop, s);
+    if (vec)
+        return drop ? launch_k<DT, GT, true, true>(a, running, s) : launch_k<DT, GT, true, false>(a, running, s);
+    return drop ? launch_k<DT, GT, false, true>(a, running, s) : launch_k<DT, GT, false, false>(a, running, s);
 }
 
 }  // namespace
 
-cudaError_t launch_sort(const SortArgs& a, KeyKind kind, cudaStream_t s)
+cudaError_t launch_row_sums(RowSumArgs a, const Places* running, int dout_type, int grad_type, bool vec, bool drop,
+                            cudaStream_t s)
 {
-    int log_blocks = 8;
-    while ((static_cast<int64_t>(kSortKeys) << log_blocks) < a.keys)
-        ++log_blocks;
-    const int blocks = 1 << log_blocks;
-    if (kind == kKeyToken)
-        k_sort<kKeyToken><<<blocks, kSortThreads, 0, s>>>(a, log_blocks);
-    else
-        k_sort<kKeyPosition><<<blocks, kSortThreads, 0, s>>>(a, log_blocks);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_row_sums(const RowSumArgs& a, int dout_type, int grad_type, bool vec, bool drop, cudaStream_t s)
-{
+    a.slabs = grad_slabs(a.dim);
     if (dout_type == LIONCUB_ROWS_BF16)
-        return grad_type == LIONCUB_ROWS_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, vec, drop, s)
-                                              : launch_t<__nv_bfloat16, float>(a, vec, drop, s);
-    return grad_type == LIONCUB_ROWS_BF16 ? launch_t<float, __nv_bfloat16>(a, vec, drop, s)
-                                          : launch_t<float, float>(a, vec, drop, s);
+        return grad_type == LIONCUB_ROWS_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, running, vec, drop, s)
+                                              : launch_t<__nv_bfloat16, float>(a, running, vec, drop, s);
+    return grad_type == LIONCUB_ROWS_BF16 ? launch_t<float, __nv_bfloat16>(a, running, vec, drop, s)
+                                          : launch_t<float, float>(a, running, vec, drop, s);
 }
 
 }  // namespace lc

@@ -6,65 +6,124 @@
 // thread takes one group of 8 columns (one column where the width or the
 // alignment does not allow 16-byte moves) of one place; see row_grid for how
 // threads map to rows.
+#include <type_traits>
+
 #include "embed_device.cuh"
 
 namespace lc {
 namespace {
 
-constexpr int kLookupThreads = 256;
+constexpr int kThreads1 = 256;
+constexpr int kWarps = kThreads1 / 32;
+constexpr unsigned kAll = 0xffffffffu;
 
-template <typename TT, typename OT, int V, bool DROP>
-__global__ void __launch_bounds__(kLookupThreads) k_lookup(const LookupArgs a)
+// One warp: PLACES places on a slab of columns.  With running positions they
+// are the same place of that many sequences, so its position row is read once;
+// otherwise neighbours.
+template <typename TT, typename OT, bool VEC, bool DROP, int PLACES, bool RUNNING>
+__global__ void __launch_bounds__(kThreads1) k_lookup(const LookupArgs a)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const int32_t g = blockIdx.y * blockDim.x + threadIdx.x;
-    if (i >= a.at.n || g >= a.groups)
+    __shared__ typename std::conditional<!VEC && DROP, SlabMask<false>::Buffer, char>::type buffers[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int64_t group = unit / a.slabs;
+    const int slab = static_cast<int>(unit - group * a.slabs);
+    const int span = static_cast<int>(a.span);
+    int64_t place0 = group * PLACES, step = 1;
+    if constexpr (RUNNING) {
+        const int64_t sequences = group / span;  // of PLACES sequences each
+        step = span;
+        place0 = sequences * PLACES * step + (group - sequences * span);
+    }
+    if (place0 >= a.at.n)
         return;
-    const int32_t j = g * V;
-    const int32_t t = token_at(a.at, i, a.status);
-    float y[V];
+
+    // lane u: the token and position of place u
+    int my_token = -1, my_position = -1;
+    if (lane < PLACES && place0 + lane * step < a.at.n) {
+        my_token = token_at(a.at, place0 + lane * step, a.status);
+        if (a.pos_table.data)
+            my_position = RUNNING ? static_cast<int>(a.at.first + place0 % span) : position_at(a.at, place0 + lane * step, a.status);
+    }
+    const Slab<VEC> cols(slab, lane, a.dim);
+    SlabMask<VEC> mask(a.drop, slab, lane, a.dim, &buffers[warp]);
+    SlabGroup<TT, VEC> x[PLACES], p[RUNNING ? 1 : PLACES];
+    int token[PLACES], position[PLACES];
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-        y[k] = 0.0f;
-    if (t >= 0) {
-        load_row<TT, V>(a.table.data, t * a.table.stride + j, y);
+    for (int u = 0; u < PLACES; ++u) {
+        token[u] = __shfl_sync(kAll, my_token, u);
+        x[u].load(cols, a.table.data, max(token[u], 0) * a.table.stride);
+    }
+    if (a.pos_table.data) {
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            y[k] = __fmul_rn(a.scale, y[k]);
-        const int32_t q = a.pos_table.data ? position_at(a.at, i, a.status) : -1;
-        if (q >= 0) {
-            float p[V];
-            load_row<TT, V>(a.pos_table.data, q * a.pos_table.stride + j, p);
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                y[k] = __fadd_rn(y[k], p[k]);
-        }
-        if constexpr (DROP) {
-            const uint32_t keep = keep_bits<V>(a.drop, static_cast<uint64_t>(i) * a.dim + j);
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                y[k] = (keep >> k & 1u) ? __fmul_rn(a.drop.rescale, y[k]) : 0.0f;
+        for (int u = 0; u < PLACES; ++u) {
+            position[u] = __shfl_sync(kAll, my_position, u);
+            if (u == 0 || !RUNNING)
+                p[u].load(cols, a.pos_table.data, max(position[u], 0) * a.pos_table.stride);
         }
     }
-    store_row<OT, V>(a.out.data, i * a.out.stride + j, y);
+#pragma unroll
+    for (int u = 0; u < PLACES; ++u) {
+        const int64_t i = place0 + u * step;
+        if (i >= a.at.n)
+            break;
+        float y[8];
+        x[u].unpack(y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            y[k] = __fmul_rn(a.scale, y[k]);
+        if (a.pos_table.data && position[u] >= 0) {
+            float q[8];
+            p[RUNNING ? 0 : u].unpack(q);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                y[k] = __fadd_rn(y[k], q[k]);
+        }
+        if constexpr (DROP)
+            mask.row(i, [&](int k, bool keep) { y[k] = keep ? __fmul_rn(a.drop.rescale, y[k]) : 0.0f; });
+        if (token[u] < 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                y[k] = 0.0f;
+        }
+        store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, y);
+    }
 }
 
-template <typename TT, typename OT, int V>
-cudaError_t launch_v(const LookupArgs& a, bool drop, cudaStream_t s)
+// Four places a warp keep enough bytes in flight and share a position row;
+// fewer warps than the SMs hold run one place each, for the latency.
+constexpr int kPlaces = 4;
+constexpr int64_t kFewWarps = 152 * kWarps;
+
+template <typename TT, typename OT, bool VEC, bool DROP>
+cudaError_t launch_k(const LookupArgs& a, cudaStream_t s)
 {
-    const RowGrid g = row_grid(a.at.n, a.groups, kLookupThreads);
-    if (drop)
-        k_lookup<TT, OT, V, true><<<g.grid, g.block, 0, s>>>(a);
+    const bool few = a.at.n * static_cast<int64_t>(a.slabs) <= kFewWarps;
+    const bool running = a.pos_table.data && !a.at.positions && !few;
+    const int64_t places = few ? 1 : kPlaces;
+    int64_t groups = (a.at.n + places - 1) / places;
+    if (running) {
+        const int64_t sequences = (a.at.n + a.span - 1) / a.span;
+        groups = (sequences + places - 1) / places * a.span;
+    }
+    const unsigned blocks = static_cast<unsigned>((groups * a.slabs + kWarps - 1) / kWarps);
+    if (few)
+        k_lookup<TT, OT, VEC, DROP, 1, false><<<blocks, kThreads1, 0, s>>>(a);
+    else if (running)
+        k_lookup<TT, OT, VEC, DROP, kPlaces, true><<<blocks, kThreads1, 0, s>>>(a);
     else
-        k_lookup<TT, OT, V, false><<<g.grid, g.block, 0, s>>>(a);
+        k_lookup<TT, OT, VEC, DROP, kPlaces, false><<<blocks, kThreads1, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename TT, typename OT>
 cudaError_t launch_t(LookupArgs a, bool vec, bool drop, cudaStream_t s)
 {
-    a.groups = vec ? a.dim / 8 : a.dim;
-    return vec ? launch_v<TT, OT, 8>(a, drop, s) : launch_v<TT, OT, 1>(a, drop, s);
+    a.slabs = (a.dim + 255) / 256;
+    a.span = a.at.seq_len < a.at.n ? a.at.seq_len : a.at.n;
+    if (vec)
+        return drop ? launch_k<TT, OT, true, true>(a, s) : launch_k<TT, OT, true, false>(a, s);
+    return drop ? launch_k<TT, OT, false, true>(a, s) : launch_k<TT, OT, false, false>(a, s);
 }
 
 }  // namespace

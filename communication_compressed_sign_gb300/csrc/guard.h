@@ -15,7 +15,7 @@ constexpr int kStatusGuard = 4;
 // scratch buffer the kernels write (wire, M1 partials, M1, 1/M1).
 constexpr int kGuardBytes = 256;
 constexpr uint32_t kGuardByte = 0xA5u;
-constexpr int kMaxGuardBands = 8;
+constexpr int kMaxGuardBands = 16;
 
 struct GuardList {
     const uint32_t* band[kMaxGuardBands];  // each kGuardBytes long, 4-byte aligned
