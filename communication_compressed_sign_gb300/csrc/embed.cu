@@ -21,7 +21,7 @@ static_assert(lc::kStatusIndex == LIONCUB_EMBED_STATUS_INDEX, "status bits are p
 
 namespace {
 constexpr int kMaxAllocs = lc::kMaxGuardBands / 2;
-constexpr int kWords = 2;  // single words of the workspace: the status word, the sort's total
+constexpr int kWords = 3;  // single words of the workspace: the status word, the sorts' totals
 }
 
 struct lioncub_embed_s {
@@ -33,14 +33,12 @@ struct lioncub_embed_s {
     void* allocs[kMaxAllocs] = {};
     int nallocs = 0;
     lc::GuardList guards{};
-    int* status = nullptr;          // kWords words, the first the status word
-    int32_t* order = nullptr;       // max_tokens places, grouped by key, and their keys
-    int2* segment = nullptr;        // max(vocab, positions) ranges of order
-    int2* pairs = nullptr;          // max_tokens (key, place) of the tiled sort
-    int32_t* tile_count = nullptr;  // its counts, and its buckets' starts
-    int32_t* arrived = nullptr;     // arrival counters of the row sums
-    float* partial = nullptr;       // partial_rows x partial_stride sums of pieces
-    int64_t tile_counts = 0, buckets = 0, arrived_count = 0, partial_rows = 0, partial_stride = 0;
+    int* status = nullptr;       // kWords words, the first the status word
+    int32_t* order = nullptr;    // for each table: max_tokens places, grouped by key, and their keys
+    int2* segment = nullptr;     // vocab + positions ranges of order
+    int32_t* arrived = nullptr;  // arrival counters of the row sums, for each table
+    float* partial = nullptr;    // partial_rows x partial_stride sums of pieces
+    int64_t arrived_count = 0, partial_rows = 0, partial_stride = 0;
 
     // fault injection (environment, read at create; 0 = off)
     int64_t fail_alloc_at = 0, alloc_count = 0;
@@ -217,7 +215,7 @@ int check_places(lioncub_embed_t h, const lioncub_token_batch* b, bool positions
     }
     out->tokens = b->tokens;
     out->positions = b->positions;
-    out->seq_len = b->seq_len < 1 ? 1 : b->seq_len;
+    out->seq_len = b->seq_len < 1 ? 1 : b->seq_len < INT_MAX ? b->seq_len : INT_MAX;
     out->first = b->first_position;
     out->n = static_cast<int32_t>(b->n);
     out->wide = b->index_type == LIONCUB_INDEX_I64;
@@ -237,59 +235,59 @@ int check_device(lioncub_embed_t h)
     return LIONCUB_OK;
 }
 
-// The gradient of one table: the sort by key and the row sums.  Positions that
-// run with the place are summed without a sort while a position has few places
-// (kRunning): each is one warp's work, and a longer one would be a long serial
-// sum on few warps.
-constexpr int64_t kRunning = 128;
+// One table's part of a backward call.
+struct TableGradient {
+    lc::KeyKind kind;
+    int64_t rows;
+    const lioncub_rows *base, *grad;
+    float factor;
+    bool sorted;  // its rows are summed in the order of a sort, else by running positions
+};
 
-int table_gradient(lioncub_embed_t h, const lc::Places& at, lc::KeyKind kind, int64_t rows, const lioncub_rows* dout,
-                   const lioncub_rows* base, const lioncub_rows* grad, const lc::DropArgs& drop, bool drop_on,
-                   float factor, cudaStream_t s)
+// Positions that run with the place are summed without a sort while a position
+// has few places: each is one warp's work, and a longer one would be a long
+// serial sum on few warps.
+constexpr int64_t kRunning = 128;
+lc::SortTask sort_task(lioncub_embed_t h, const lc::Places& at, const TableGradient& g)
 {
-    lc::RowSumArgs su{};
-    su.dout = rows_of(dout);
-    su.base = rows_of(base);
-    su.grad = rows_of(grad);
-    su.order = h->order;
-    su.sorted_key = h->order + h->max_tokens;
-    su.segment = h->segment;
-    su.total = h->status + 1;
-    su.partial = h->partial;
-    su.partial_stride = h->partial_stride;
-    su.partial_rows = h->partial_rows;
-    su.arrived = h->arrived;
-    su.arrived_count = h->arrived_count;
-    su.drop = drop;
-    su.factor = factor;
-    su.rows = static_cast<int32_t>(rows);
-    su.dim = static_cast<int32_t>(h->dim);
-    su.n = at.n;
-    su.status = h->status;
-    const bool running = kind == lc::kKeyPosition && !at.positions && (at.n + at.seq_len - 1) / at.seq_len <= kRunning;
-    cudaError_t e;
-    if (!running) {
-        lc::SortArgs so{};
-        so.at = at;
-        so.keys = static_cast<int32_t>(rows);
-        so.capacity = static_cast<int32_t>(h->max_tokens);
-        so.order = h->order;
-        so.sorted_key = h->order + h->max_tokens;
-        so.segment = h->segment;
-        so.total = h->status + 1;
-        so.pairs = h->pairs;
-        so.tile_count = h->tile_count;
-        so.bucket_start = h->tile_count + h->tile_counts;
-        so.arrived = h->arrived;
-        so.arrived_count = lc::grad_stretches(at.n) * lc::grad_slabs(h->dim);
-        so.status = h->status;
-        e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, kind, s); });
-        if (e != cudaSuccess)
-            return cuda_fail(h, e, "sort launch");
-    }
-    const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(base) && aligned_rows(grad);
-    e = launch(h, "embed_row_sums", [&] {
-        return lc::launch_row_sums(su, running ? &at : nullptr, dout->type, grad->type, vec, drop_on, s);
+    lc::SortTask t{};
+    const int which = g.kind;
+    t.at = at;
+    t.kind = which;
+    t.keys = static_cast<int32_t>(g.rows);
+    t.capacity = static_cast<int32_t>(h->max_tokens);
+    t.order = h->order + 2 * which * h->max_tokens;
+    t.sorted_key = t.order + h->max_tokens;
+    t.segment = h->segment + which * h->vocab;
+    t.total = h->status + 1 + which;
+    return t;
+}
+
+int sum_rows(lioncub_embed_t h, const lc::Places& at, const TableGradient& g, const lioncub_rows* dout,
+             const lc::DropArgs& drop, bool drop_on, cudaStream_t s)
+{
+    const lc::SortTask t = sort_task(h, at, g);
+    lc::RowSumArgs a{};
+    a.dout = rows_of(dout);
+    a.base = rows_of(g.base);
+    a.grad = rows_of(g.grad);
+    a.order = t.order;
+    a.sorted_key = t.sorted_key;
+    a.segment = t.segment;
+    a.total = t.total;
+    a.partial = h->partial;
+    a.partial_stride = h->partial_stride;
+    a.partial_rows = h->partial_rows;
+    a.arrived = h->arrived + g.kind * h->arrived_count;
+    a.drop = drop;
+    a.factor = g.factor;
+    a.rows = static_cast<int32_t>(g.rows);
+    a.dim = static_cast<int32_t>(h->dim);
+    a.n = at.n;
+    a.status = h->status;
+    const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(g.base) && aligned_rows(g.grad);
+    const cudaError_t e = launch(h, "embed_row_sums", [&] {
+        return lc::launch_row_sums(a, g.sorted ? nullptr : &at, dout->type, g.grad->type, vec, drop_on, s);
     });
     return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "row sum launch");
 }
@@ -385,13 +383,11 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     h->positions = positions;
     h->max_tokens = max_tokens;
     h->scale = scale;
-    const int64_t keys = vocab > positions ? vocab : positions;
-    h->buckets = int64_t(1) << lc::sort_log_buckets(keys);
-    const bool tiled = max_tokens > lc::kDirectPlaces;
-    h->tile_counts = tiled ? lc::sort_max_tiles(max_tokens) * h->buckets : 0;
-    h->partial_rows = 2 * lc::grad_stretches(max_tokens);
+    const int64_t tables = positions > 0 ? 2 : 1;
+    const int64_t stretches = lc::grad_max_stretches(max_tokens, lc::grad_slabs(dim));
+    h->partial_rows = 2 * stretches;
     h->partial_stride = lc::grad_slabs(dim) * int64_t(256);
-    h->arrived_count = lc::grad_stretches(max_tokens) * lc::grad_slabs(dim);
+    h->arrived_count = h->partial_rows * lc::grad_slabs(dim);
     h->fail_alloc_at = env_index("LIONCUB_FAIL_ALLOC");
     h->fail_launch_at = env_index("LIONCUB_FAIL_LAUNCH");
     cudaError_t e = cudaGetDevice(&h->device);
@@ -400,15 +396,11 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     if (e == cudaSuccess)
         e = cudaMemset(h->status, 0, kWords * sizeof(int));
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->order, 2 * max_tokens);
+        e = guarded_alloc(h, &h->order, tables * 2 * max_tokens);
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->segment, keys);
+        e = guarded_alloc(h, &h->segment, vocab + positions);
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->pairs, tiled ? max_tokens : 0);
-    if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->tile_count, h->tile_counts + h->buckets + 1);
-    if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->arrived, h->arrived_count);
+        e = guarded_alloc(h, &h->arrived, 2 * h->arrived_count);
     if (e == cudaSuccess)
         e = guarded_alloc(h, &h->partial, h->partial_rows * h->partial_stride);
     if (e == cudaSuccess)
@@ -491,11 +483,32 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
     rc = check_drop(h, drop, h->dim, &d, &on);
     if (rc == LIONCUB_OK)
         rc = check_device(h);
-    // positions first: they read dout in order, and what fits L2 stays there for the tokens
-    if (rc == LIONCUB_OK && pos_grad)
-        rc = table_gradient(h, at, lc::kKeyPosition, h->positions, dout, pos_base, pos_grad, d, on, d.rescale, stream);
+    if (rc != LIONCUB_OK)
+        return rc;
+
+    // 1 sort; 2 position rows: they read dout in order, and what
+    // fits L2 stays there for 3 token rows
+    TableGradient tables[2] = {{lc::kKeyToken, h->vocab, base, grad, h->scale * d.rescale, true},
+                               {lc::kKeyPosition, h->positions, pos_base, pos_grad, d.rescale, true}};
+    lc::SortArgs so{};
+    for (int k = 0; k < (pos_grad ? 2 : 1); ++k) {
+        TableGradient& g = tables[k];
+        g.sorted = k == 0 || at.positions || (at.n + at.seq_len - 1) / at.seq_len > kRunning;
+        if (g.sorted)
+            so.task[so.tasks++] = sort_task(h, at, g);
+    }
+    const int64_t slabs = lc::grad_slabs(h->dim);
+    so.arrived[0] = h->arrived;
+    so.arrived[1] = h->arrived + h->arrived_count;
+    so.arrived_count = 2 * lc::grad_stretches(at.n, lc::grad_piece(at.n, slabs)) * slabs;
+    so.status = h->status;
+    const cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, stream); });
+    if (e != cudaSuccess)
+        return cuda_fail(h, e, "sort launch");
+    if (pos_grad)
+        rc = sum_rows(h, at, tables[1], dout, d, on, stream);
     if (rc == LIONCUB_OK)
-        rc = table_gradient(h, at, lc::kKeyToken, h->vocab, dout, base, grad, d, on, h->scale * d.rescale, stream);
+        rc = sum_rows(h, at, tables[0], dout, d, on, stream);
     return rc;
 }
 

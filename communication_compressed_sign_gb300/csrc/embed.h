@@ -56,47 +56,46 @@ struct LookupArgs {
 enum KeyKind { kKeyToken = 0, kKeyPosition = 1 };
 
 // Places a warp of the row sums takes; segments longer than this are summed in
-// pieces.
-constexpr int kGradPiece = 16;
-inline int64_t grad_stretches(int64_t n) { return (n + kGradPiece - 1) / kGradPiece; }
+// pieces.  At most 16, so that a stretch and a short segment's overhang fit 32
+// lanes; less while that leaves SMs without work.
+constexpr int kMaxPiece = 16, kMinPiece = 4;
+inline int grad_piece(int64_t n, int64_t slabs)
+{
+    int piece = kMinPiece;
+    while (piece < kMaxPiece && n * slabs > piece * int64_t(152 * 32))
+        piece *= 2;
+    return piece;
+}
+inline int64_t grad_stretches(int64_t n, int piece) { return (n + piece - 1) / piece; }
+// The most that a batch of up to n places has.
+inline int64_t grad_max_stretches(int64_t n, int64_t slabs)
+{
+    const int64_t few = 152 * 32 / slabs + 1, many = grad_stretches(n, kMaxPiece);
+    const int64_t most = few > many ? few : many;
+    return most < grad_stretches(n, kMinPiece) ? most : grad_stretches(n, kMinPiece);
+}
 inline int32_t grad_slabs(int64_t dim) { return static_cast<int32_t>((dim + 255) / 256); }
-
-// A batch of up to this many places is sorted in one launch.
-constexpr int64_t kDirectPlaces = 8192;
-// Buckets of the sort (a power of two, at most 1024 keys each), and places a
-// tile of its tiled form takes (at most 256 tiles).
-inline int sort_log_buckets(int64_t keys)
-{
-    int b = 8;
-    while ((int64_t(1024) << b) < keys)
-        ++b;
-    return b;
-}
-inline int64_t sort_tile(int64_t n)
-{
-    const int64_t t = (n + 255) / 256;
-    return t <= 1024 ? 1024 : (t + 255) / 256 * 256;
-}
-inline int64_t sort_max_tiles(int64_t n) { return n > 256 * 1024 ? 256 : (n + 1023) / 1024; }
 
 // The sort of a batch's places by key: order holds the places grouped by key,
 // ascending within a key, sorted_key their keys; segment[key] is the key's
 // range in order, total the number of places that have a key.
-struct SortArgs {
+struct SortTask {
     Places at;
+    int32_t kind;      // KeyKind
     int32_t keys;      // key values: [0, keys)
     int32_t capacity;  // entries of order (checked builds)
+    int32_t log_blocks;  // set by launch_sort
     int32_t* order;
     int32_t* sorted_key;
     int2* segment;
     int32_t* total;
-    int2* pairs;            // tiled: (key, place) by bucket
-    int32_t* tile_count;    // tiled: keys of each (tile, bucket)
-    int32_t* bucket_start;  // tiled: buckets + 1 offsets into pairs
-    int32_t* arrived;       // the row sums' counters, zeroed here
+};
+
+struct SortArgs {
+    SortTask task[2];
+    int32_t tasks;
+    int32_t* arrived[2];  // the row sums' counters, zeroed here
     int64_t arrived_count;
-    int64_t tile;           // set by launch_sort
-    int log_buckets;
     int* status;
 };
 
@@ -107,16 +106,15 @@ struct RowSumArgs {
     const int32_t* sorted_key;
     const int2* segment;
     const int32_t* total;
-    float* partial;          // two fp32 rows for each stretch of kGradPiece places
+    float* partial;          // two fp32 rows for each stretch
     int64_t partial_stride;  // 256 * slabs
     int64_t partial_rows;
-    int32_t* arrived;        // pieces done, for each (stretch a long segment begins in, slab)
-    int64_t arrived_count;
+    int32_t* arrived;        // arrivals, for each (row of partial, slab)
     DropArgs drop;
     float factor;
-    int32_t rows;   // rows of grad
+    int32_t rows;  // rows of grad
     int32_t dim;
-    int32_t slabs;  // set by launch_row_sums
+    int32_t slabs, piece;  // set by launch_row_sums
     int32_t n;      // rows of dout
     int* status;
 };
@@ -131,9 +129,11 @@ struct DropoutArgs {
 // vec: the matrices allow 16-byte moves of 8 columns (launch_dropout: their
 // starts and strides do); drop: dropout is on.
 cudaError_t launch_lookup(const LookupArgs& a, int table_type, int out_type, bool vec, bool drop, cudaStream_t s);
-cudaError_t launch_sort(SortArgs a, KeyKind kind, cudaStream_t s);
+cudaError_t launch_sort(SortArgs a, cudaStream_t s);
 // running: the places of a batch whose positions run with the place (the rows
-// of grad are positions, and no sort is read), or null.
+// of grad are positions, and no sort is read), or null.  Launched to overlap the
+// end of the launch before it, whose results it waits for (running: before it
+// ends, as it needs none of them).
 cudaError_t launch_row_sums(RowSumArgs a, const Places* running, int dout_type, int grad_type, bool vec, bool drop,
                             cudaStream_t s);
 cudaError_t launch_dropout(const DropoutArgs& a, int x_type, int out_type, bool vec, bool drop, cudaStream_t s);

@@ -6,13 +6,13 @@
 // order of every sum depends on the batch alone.
 //
 // The unit of work is one warp on a slab of 256 columns.
-//   walk   a stretch of kGradPiece entries of `order`: the warp adds the rows of
+//   walk   a stretch of `piece` entries of `order`: the warp adds the rows of
 //          dout of the segments that begin there, several rows in flight
 //          whatever the segments' lengths, and writes a row of grad at each
-//          segment's end.  A segment of up to kGradPiece places belongs to the
+//          segment's end.  A segment of up to `piece` places belongs to the
 //          stretch it begins in.  A longer one is cut at the stretches' bounds:
-//          each warp leaves an fp32 partial, and the last to arrive (an integer
-//          counter) adds the partials in order.  So units are alike in size
+//          each warp leaves an fp32 partial, and the last of a group of partials to
+//          arrive (an integer counter) adds them in order.  So units are alike in size
 //          however skewed the tokens are.
 //   fill   rows without a place.
 // Bound by memory: dout is read once and grad written once.
@@ -91,39 +91,42 @@ struct Walker {
         }
         store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, sum);
     }
-    // One piece of a long segment: stores its partial and, if it is the last of
-    // the segment's pieces to arrive, gathers the segment's sum.
+    // Adds up the pieces of a long segment: a tree of groups of 8, in which the
+    // last of a group to arrive adds the group's partials in order and goes on
+    // as one piece of the next level.  True where the whole sum has come together.
     __device__ __forceinline__ bool gather(int2 seg, int stretch, int slab, int lane)
     {
-        const int first = seg.x / kGradPiece, pieces = (seg.y - 1) / kGradPiece - first + 1;
-        // slot 1 of the stretch the segment begins in, slot 0 of the later ones
-        const int64_t row = 2 * static_cast<int64_t>(stretch) + (stretch == first ? 1 : 0);
-        const int64_t counter = static_cast<int64_t>(first) * a.slabs + slab;
-        if (!index_ok(a.status, row < a.partial_rows && counter < a.arrived_count))
-            return false;
+        const int first = seg.x / a.piece;
+        int node = stretch - first, nodes = (seg.y - 1) / a.piece - first + 1;
         const int64_t column = slab * 256 + lane * 8;  // partial rows are whole slabs
-        store_row<float, 8>(a.partial, row * a.partial_stride + column, sum);
-        __threadfence();
-        __syncwarp();
-        int before = 0;
-        if (lane == 0)
-            before = atomicAdd(&a.arrived[counter], 1);
-        if (__shfl_sync(kAll, before, 0) != pieces - 1)
+        // piece r's partial and counter: slot 1 of the stretch the segment begins in, slot 0 of the later ones
+        auto slot = [&](int r) { return 2 * static_cast<int64_t>(first + r) + (r == 0 ? 1 : 0); };
+        auto partial = [&](int r) { return a.partial + slot(r) * a.partial_stride + column; };
+        if (!index_ok(a.status, 2 * static_cast<int64_t>(stretch) + 1 < a.partial_rows))
             return false;
-        __threadfence();
-        const float* p = a.partial + (2 * static_cast<int64_t>(first) + 1) * a.partial_stride + column;
-        clear();
-        add_partial(p);
-        p += a.partial_stride;
+#pragma unroll 1
+        for (int level = 0; nodes > 1; ++level) {
+            const int group = node >> 3, members = min(8, nodes - group * 8), scale = 3 * level;
+            store_row<float, 8>(partial(node << scale), 0, sum);
+            __threadfence();
+            __syncwarp();
+            int before = 0;
+            if (lane == 0)  // four bits a level
+                before = atomicAdd(&a.arrived[slot(group << scale << 3) * a.slabs + slab], 1 << (4 * level));
+            before = __shfl_sync(kAll, before, 0);
+            if ((before >> (4 * level) & 15) != members - 1)
+                return false;
+            __threadfence();
+            clear();
 #pragma unroll 4
-        for (int q = 1; q < pieces; ++q) {
-            add_partial(p);
-            p += 2 * a.partial_stride;
+            for (int m = 0; m < members; ++m)
+                add_partial(partial((group * 8 + m) << scale));
+            node = group;
+            nodes = (nodes + 7) / 8;
         }
         return true;
     }
-    // Columns are where add() has them: only lanes move as a whole, so a
-    // partial row may hold them in any order as long as it is always the same.
+    // A lane's 8 sums lie together in a partial row, whichever columns they are.
     __device__ __forceinline__ void add_partial(const float* p)
     {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(p)), y = __ldcg(reinterpret_cast<const float4*>(p) + 1);
@@ -156,6 +159,11 @@ __device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int
         }
     }
 }
+
+// Programmatic launches: a kernel may start before the launch before it in the
+// stream has ended, and waits here until all of that is done and visible.
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 // The position of the n-th (from 0) set bit of a word that has more than n.
 __device__ __forceinline__ int nth_bit(unsigned word, int n)
@@ -190,6 +198,7 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_row_sums(const Row
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned fills = mix.fills_before(blockIdx.x);
+    wait_for_launch_before();
     if (mix.fills_before(blockIdx.x + 1) != fills) {
         const int64_t row0 = (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows;
         fill_rows<GT, VEC>(a, row0, lane, [&](int64_t v) {
@@ -199,20 +208,24 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_row_sums(const Row
         return;
     }
     const int64_t unit = static_cast<int64_t>(blockIdx.x - fills) * kWarpsPerBlock + warp;
-    const int stretch = static_cast<int>(unit / a.slabs);  // places and so stretches fit 31 bits
+    const int stretch = static_cast<int>(quotient(unit, a.slabs));  // places and so stretches fit 31 bits
     const int slab = static_cast<int>(unit - static_cast<int64_t>(stretch) * a.slabs);
     const int total = *a.total;
-    if (static_cast<int64_t>(stretch) * kGradPiece >= total)
+    if (static_cast<int64_t>(stretch) * a.piece >= total)
         return;
-    const int begin = stretch * kGradPiece, end = min(begin + kGradPiece, total);
-    const int32_t key0 = a.sorted_key[begin], key1 = a.sorted_key[end - 1];
-    if (!index_ok(a.status, key0 >= 0 && key0 < a.rows && key1 >= 0 && key1 < a.rows))
+    const int begin = stretch * a.piece, end = min(begin + a.piece, total);
+    // the stretch, and what a short segment can reach beyond it
+    const int mine = begin + lane;
+    const int32_t my_place = mine < total ? a.order[mine] : 0, my_key = mine < total ? a.sorted_key[mine] : 0;
+    if (!__all_sync(kAll, index_ok(a.status, my_place >= 0 && my_place < a.n && my_key >= 0 && my_key < a.rows)))
         return;
-    const int2 seg0 = a.segment[key0], seg1 = a.segment[key1];
-    const bool tail = seg0.x < begin && seg0.y - seg0.x > kGradPiece;   // a long segment goes on here
-    const bool head = seg1.x >= begin && seg1.y - seg1.x > kGradPiece;  // a long segment begins here
+    const int2 seg0 = a.segment[__shfl_sync(kAll, my_key, 0)], seg1 = a.segment[__shfl_sync(kAll, my_key, end - 1 - begin)];
+    const bool tail = seg0.x < begin && seg0.y - seg0.x > a.piece;   // a long segment goes on here
+    const bool head = seg1.x >= begin && seg1.y - seg1.x > a.piece;  // a long segment begins here
     // short segments: one that began before belongs there, one that begins here is taken to its end
     const int from = seg0.x < begin ? seg0.y : begin, to = head ? seg1.x : (seg1.x < begin ? begin : seg1.y);
+    const int32_t above = __shfl_up_sync(kAll, my_key, 1);
+    const unsigned begins = __ballot_sync(kAll, lane == 0 || my_key != above);
 
     Walker<DT, GT, VEC, DROP> w(a, slab, lane, warp_buffer<VEC, DROP>(warp));
 #pragma unroll 1
@@ -224,40 +237,27 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_row_sums(const Row
         if (lo >= hi)
             continue;
         w.clear();
-        int32_t current = -1;
+        const int here = hi - begin;
+        int32_t current = __shfl_sync(kAll, my_key, lo - begin);
 #pragma unroll 1
-        for (int p0 = lo; p0 < hi; p0 += 32) {
-            const int mine = p0 + lane;
-            const int32_t my_place = mine < hi ? a.order[mine] : 0;
-            const int32_t my_key = mine < hi ? a.sorted_key[mine] : 0;
-            if (!__all_sync(kAll, index_ok(a.status, my_place >= 0 && my_place < a.n)))
-                return;
-            const int here = min(32, hi - p0);
-            const int32_t above = __shfl_up_sync(kAll, my_key, 1);
-            const int32_t key_before = lane == 0 ? current : above;
-            const unsigned begins = __ballot_sync(kAll, my_key != key_before);
-#pragma unroll 1
-            for (int q = 0; q < here; q += kInFlight) {
-                SlabGroup<DT, VEC> x[kInFlight];
-                int32_t place[kInFlight];
+        for (int q = lo - begin; q < here; q += kInFlight) {
+            SlabGroup<DT, VEC> x[kInFlight];
+            int32_t place[kInFlight];
 #pragma unroll
-                for (int u = 0; u < kInFlight; ++u) {  // past the end the last row again: no branch between the loads
-                    place[u] = __shfl_sync(kAll, my_place, min(q + u, here - 1));
-                    x[u].load(w.cols, a.dout.data, static_cast<uint32_t>(place[u]) * a.dout.stride);
-                }
+            for (int u = 0; u < kInFlight; ++u) {  // past the end the last row again: no branch between the loads
+                place[u] = __shfl_sync(kAll, my_place, min(q + u, here - 1));
+                x[u].load(w.cols, a.dout.data, static_cast<uint32_t>(place[u]) * a.dout.stride);
+            }
 #pragma unroll
-                for (int u = 0; u < kInFlight; ++u) {
-                    if (q + u >= here)
-                        break;
-                    if (begins >> (q + u) & 1u) {
-                        if (current >= 0) {
-                            w.finish(current);
-                            w.clear();
-                        }
-                        current = __shfl_sync(kAll, my_key, q + u);
-                    }
-                    w.add(x[u], place[u]);
+            for (int u = 0; u < kInFlight; ++u) {
+                if (q + u >= here)
+                    break;
+                if ((begins >> (q + u) & 1u) && q + u > lo - begin) {
+                    w.finish(current);
+                    w.clear();
+                    current = __shfl_sync(kAll, my_key, q + u);
                 }
+                w.add(x[u], place[u]);
             }
         }
         if (part == 1 || w.gather(part == 0 ? seg0 : seg1, stretch, slab, lane))
@@ -269,18 +269,9 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_row_sums(const Row
 // q - first, q - first + seq_len, ... and need no sort.  Walk blocks: rows that
 // have places; fill blocks: rows that have none.
 template <typename DT, typename GT, bool VEC, bool DROP>
-__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_running_row_sums(const RowSumArgs a, const Places at, const Mix mix)
+__device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& at, int64_t unit, int span, int warp, int lane)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int span = static_cast<int>(min(at.seq_len, static_cast<int64_t>(at.n)));
-    const unsigned fills = mix.fills_before(blockIdx.x);
-    if (mix.fills_before(blockIdx.x + 1) != fills) {
-        const int64_t row0 = (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows;
-        fill_rows<GT, VEC>(a, row0, lane, [&](int64_t v) { return v < at.first || v >= at.first + span; });
-        return;
-    }
-    const int64_t unit = static_cast<int64_t>(blockIdx.x - fills) * kWarpsPerBlock + warp;
-    const int64_t place0 = unit / a.slabs;
+    const int64_t place0 = quotient(unit, a.slabs);
     const int slab = static_cast<int>(unit - place0 * a.slabs);
     if (place0 >= span)
         return;
@@ -310,24 +301,47 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_running_row_sums(c
     w.finish(at.first + place0);
 }
 
+template <typename DT, typename GT, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_running_row_sums(const RowSumArgs a, const Places at, const Mix mix)
+{
+    let_next_launch_start();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int span = static_cast<int>(min(at.seq_len, static_cast<int64_t>(at.n)));
+    const unsigned fills = mix.fills_before(blockIdx.x);
+    if (mix.fills_before(blockIdx.x + 1) != fills) {
+        const int64_t row0 = (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows;
+        fill_rows<GT, VEC>(a, row0, lane, [&](int64_t v) { return v < at.first || v >= at.first + span; });
+    } else {
+        running_row<DT, GT, VEC, DROP>(a, at, static_cast<int64_t>(blockIdx.x - fills) * kWarpsPerBlock + warp, span, warp, lane);
+    }
+    wait_for_launch_before();  // the launch after this one relies on both
+}
+
 unsigned blocks_for(int64_t warps) { return static_cast<unsigned>((warps + kWarpsPerBlock - 1) / kWarpsPerBlock); }
 
 template <typename DT, typename GT, bool VEC, bool DROP>
 cudaError_t launch_k(const RowSumArgs& a, const Places* running, cudaStream_t s)
 {
     const int64_t units =
-        (running ? (running->seq_len < running->n ? running->seq_len : running->n) : grad_stretches(a.n)) * a.slabs;
+        (running ? (running->seq_len < running->n ? running->seq_len : running->n) : grad_stretches(a.n, a.piece)) * a.slabs;
     const bool in_place = a.base.data == a.grad.data;
     const unsigned fill = in_place ? 0 : blocks_for((a.rows + kFillRows - 1) / kFillRows);
     const unsigned blocks = blocks_for(units) + fill;
     if (blocks == 0)
         return cudaSuccess;
     const Mix mix = {((static_cast<uint64_t>(fill) << 32) + blocks - 1) / blocks};
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(blocks);
+    c.blockDim = dim3(kSumThreads);
+    c.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = attr;
+    c.numAttrs = 1;
     if (running)
-        k_running_row_sums<DT, GT, VEC, DROP><<<blocks, kSumThreads, 0, s>>>(a, *running, mix);
-    else
-        k_row_sums<DT, GT, VEC, DROP><<<blocks, kSumThreads, 0, s>>>(a, mix);
-    return cudaGetLastError();
+        return cudaLaunchKernelEx(&c, k_running_row_sums<DT, GT, VEC, DROP>, a, *running, mix);
+    return cudaLaunchKernelEx(&c, k_row_sums<DT, GT, VEC, DROP>, a, mix);
 }
 
 template <typename DT, typename GT>
@@ -344,6 +358,7 @@ cudaError_t launch_row_sums(RowSumArgs a, const Places* running, int dout_type, 
                             cudaStream_t s)
 {
     a.slabs = grad_slabs(a.dim);
+    a.piece = grad_piece(a.n, a.slabs);
     if (dout_type == LIONCUB_ROWS_BF16)
         return grad_type == LIONCUB_ROWS_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, running, vec, drop, s)
                                               : launch_t<__nv_bfloat16, float>(a, running, vec, drop, s);

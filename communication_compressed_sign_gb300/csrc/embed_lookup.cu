@@ -26,14 +26,15 @@ __global__ void __launch_bounds__(kThreads1) k_lookup(const LookupArgs a)
     __shared__ typename std::conditional<!VEC && DROP, SlabMask<false>::Buffer, char>::type buffers[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    const int64_t group = unit / a.slabs;
+    const int64_t group = quotient(unit, a.slabs);
     const int slab = static_cast<int>(unit - group * a.slabs);
     const int span = static_cast<int>(a.span);
-    int64_t place0 = group * PLACES, step = 1;
+    int64_t place0 = group * PLACES, step = 1, in_sequence = 0;
     if constexpr (RUNNING) {
-        const int64_t sequences = group / span;  // of PLACES sequences each
+        const int64_t sequences = quotient(group, span);  // PLACES sequences each
         step = span;
-        place0 = sequences * PLACES * step + (group - sequences * span);
+        in_sequence = group - sequences * span;
+        place0 = sequences * PLACES * step + in_sequence;
     }
     if (place0 >= a.at.n)
         return;
@@ -43,7 +44,7 @@ __global__ void __launch_bounds__(kThreads1) k_lookup(const LookupArgs a)
     if (lane < PLACES && place0 + lane * step < a.at.n) {
         my_token = token_at(a.at, place0 + lane * step, a.status);
         if (a.pos_table.data)
-            my_position = RUNNING ? static_cast<int>(a.at.first + place0 % span) : position_at(a.at, place0 + lane * step, a.status);
+            my_position = RUNNING ? static_cast<int>(a.at.first + in_sequence) : position_at(a.at, place0 + lane * step, a.status);
     }
     const Slab<VEC> cols(slab, lane, a.dim);
     SlabMask<VEC> mask(a.drop, slab, lane, a.dim, &buffers[warp]);

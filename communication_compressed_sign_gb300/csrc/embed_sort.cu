@@ -1,328 +1,253 @@
-// embed_sort.cu -- stable sort of a batch's places by key (token or position).
+// embed_sort.cu -- the stable sort of a batch's places by key (token or
+// position), the first launch of an embedding gradient.
 //
-// Keys are spread over R buckets by their low bits (interleaved, so that the
-// frequent low ids of a vocabulary do not meet in one), and a block sorts one
-// bucket by counting.  No block waits for another.  Two ways into the buckets:
-//
-//   direct   every bucket's block reads all keys: it takes its own and counts
-//            those of lower buckets, which gives its base.  One launch, R * n
-//            key reads from L2.
-//   tiled    count (tile x bucket), scatter into buckets, then a block per
-//            bucket: three launches, 4 n key reads.
-//
-// Direct up to kDirectPlaces places.  A sort is bound by latency (dependent
-// loads, launches), not by the few bytes it moves.
-//
-// Stability: a warp takes a contiguous slice of its block's places in order,
-// counts per (warp, key), and after the scan places its keys 32 at a time,
-// ranked among equal keys of the 32 by a warp match.
+// By counting, without communication between blocks.  Block b of C owns
+// the keys with key % C == b (interleaved, so that the frequent low ids of a
+// vocabulary spread over the blocks) and reads all keys itself: it counts those
+// of lower blocks, which gives the base of its part of `order`, and its own for
+// each warp and key.  Each warp takes a contiguous slice of the places, so a
+// scan over warps keeps places ascending within a key.  What a warp finds of
+// its block's keys it keeps in a list in shared memory, and only that list is
+// placed, ranked among equal keys by ballots (a ballot a key bit; the match
+// instruction took about 150 cycles).  A sort moves few bytes; it is bound by
+// each block's reads of all keys from L2 (8 bytes a place at 64 bytes a cycle)
+// and by latency.  A radix sort of two passes in one thread-block cluster read
+// each key once, but its barriers and passes took 2 to 5 times as long.
+#include <type_traits>
+
 #include "embed_device.cuh"
 
 namespace lc {
 namespace {
 
-constexpr int kThreads1 = 256;
-constexpr int kWarps = kThreads1 / 32;
-constexpr int kMaxOwn = 1024;     // keys of one bucket
-constexpr int kMaxBuckets = 1024;
-constexpr int kBatch = 4;         // groups of 32 keys a warp loads at once
+constexpr int kBlock = 1024;
+constexpr int kWarps = kBlock / 32;
+constexpr int kMaxOwned = kBlock;  // keys of a block: one a thread in the scan
+constexpr int kBatch = 8;          // groups of 32 keys a warp loads at once
+constexpr int kList = 256;         // a warp's list; a slice with more is read again
 constexpr unsigned kAll = 0xffffffffu;
 
-// Where a sort's keys come from: the places themselves, or a bucket's pairs.
-enum Source { kTokens = kKeyToken, kPositions = kKeyPosition, kPairs = 2 };
-
-template <int SRC>
-__device__ __forceinline__ int32_t key_of(const SortArgs& a, int64_t i, int* status)
+// The key of a place from its token (and position, where that is the key), or
+// -1.  IT: the type of ids and positions.
+template <int KIND, typename IT>
+__device__ __forceinline__ int32_t key_of(const Places& at, IT token, IT position, int* status)
 {
-    const int32_t t = token_at(a.at, i, status);
-    if (SRC == kTokens || t < 0)
-        return t;
-    return position_at(a.at, i, status);
+    using U = typename std::make_unsigned<IT>::type;
+    const bool there = static_cast<U>(token) < static_cast<U>(at.vocab);
+    const IT key = KIND == kKeyToken ? token : position;
+    const bool good = static_cast<U>(key) < static_cast<U>(KIND == kKeyToken ? at.vocab : at.npos);
+    if ((!there && token >= 0) || (there && !good))
+        flag(status, kStatusIndex);
+    return there && good ? static_cast<int32_t>(key) : -1;
 }
 
-__device__ __forceinline__ int warp_inclusive(int x, int lane)
+// Keys of places i0 + 32 u + lane below hi: the loads before any use, so that
+// they are in flight together.
+template <int KIND, typename IT, bool WHOLE>
+__device__ __forceinline__ void read_keys(const Places& at, int64_t i0, int64_t hi, int lane, int* status, int32_t (&key)[kBatch])
 {
+    IT token[kBatch], position[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = i0 + u * 32 + lane;
+        token[u] = -1;
+        position[u] = 0;
+        if (WHOLE || i < hi) {
+            token[u] = static_cast<const IT*>(at.tokens)[i];
+            if (KIND == kKeyPosition)
+                position[u] = at.positions ? static_cast<const IT*>(at.positions)[i]
+                                           : static_cast<IT>(at.first + static_cast<uint32_t>(i) % static_cast<uint32_t>(at.seq_len));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+        key[u] = key_of<KIND, IT>(at, token[u], position[u], status);
+}
+
+// Places one key of each lane that has one: the lane's rank among equal keys
+// of the warp, after those its warp placed before.
+__device__ __forceinline__ void place_keys(const SortTask& t, int* next, bool has, int owned_key, int key_bits, int32_t key,
+                                           int32_t place, int lane, int* status)
+{
+    unsigned same = __ballot_sync(kAll, has);
+    for (int b = 0; b < key_bits; ++b) {
+        const bool bit = owned_key >> b & 1;
+        const unsigned ones = __ballot_sync(kAll, bit);
+        same &= bit ? ones : ~ones;
+    }
+    int at = 0;
+    if (has)
+        at = next[owned_key] + __popc(same & ((1u << lane) - 1));
+    __syncwarp();
+    if (has) {
+        if ((same >> lane) == 1u)  // the last lane with this key
+            next[owned_key] = at + 1;
+        if (index_ok(status, at >= 0 && at < t.capacity)) {
+            t.order[at] = place;
+            t.sorted_key[at] = key;
+        }
+    }
+    __syncwarp();
+}
+
+template <int KIND, typename IT>
+__device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_status)
+{
+    __shared__ int part[kWarps + 1];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int shift = t.log_blocks, mask = (1 << shift) - 1;
+    const int owned = mine < t.keys ? ((t.keys - 1 - mine) >> shift) + 1 : 0;
+    const int width = (t.keys + mask) >> shift;  // of the rows of count
+    int* count = memory;                         // kWarps x width: keys of each (warp, key), then where the next goes
+    uint32_t* list = reinterpret_cast<uint32_t*>(memory + kWarps * width) + warp * kList;  // place in slice | owned key << 16
+    int* status = mine == 0 ? all_status : nullptr;
+    for (int k = tid; k < kWarps * width; k += kBlock)
+        count[k] = 0;
+    __syncthreads();
+    count += warp * width;
+
+    const int64_t n = t.at.n;
+    const int64_t slice = (n + kBlock - 1) / kBlock * 32;
+    const int64_t lo = warp * slice, hi = min(lo + slice, n);
+    int found = 0, below = 0;
+    auto count_keys = [&](int64_t i0, const int32_t (&key)[kBatch]) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int b = key[u] & mask;
+            below += key[u] >= 0 && b < mine ? 1 : 0;
+            const bool take = key[u] >= 0 && b == mine;
+            const unsigned takers = __ballot_sync(kAll, take);
+            if (takers == 0)
+                continue;
+            if (take) {
+                const int k = key[u] >> shift, at = found + __popc(takers & ((1u << lane) - 1));
+                atomicAdd(&count[k], 1);
+                if (at < kList)
+                    list[at] = static_cast<uint32_t>(i0 - lo + u * 32 + lane) | static_cast<uint32_t>(k) << 16;
+            }
+            found += __popc(takers);
+        }
+    };
+    int64_t i0 = lo;
+    for (; i0 + kBatch * 32 <= hi; i0 += kBatch * 32) {
+        int32_t key[kBatch];
+        read_keys<KIND, IT, true>(t.at, i0, hi, lane, status, key);
+        count_keys(i0, key);
+    }
+    if (i0 < hi) {
+        int32_t key[kBatch];
+        read_keys<KIND, IT, false>(t.at, i0, hi, lane, status, key);
+        count_keys(i0, key);
+    }
+    below = __reduce_add_sync(kAll, below);
+    if (lane == 0)
+        part[warp] = below;
+    __syncthreads();
+    const int base = __reduce_add_sync(kAll, part[lane]);
+    __syncthreads();
+
+    // thread k: the block's key k, over the warps
+    int total = 0;
+    if (tid < owned) {
+#pragma unroll 8
+        for (int w = 0; w < kWarps; ++w)
+            total += memory[w * width + tid];
+    }
+    int inc = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(kAll, x, o);
-        x += lane >= o ? up : 0;
+        const int up = __shfl_up_sync(kAll, inc, o);
+        inc += lane >= o ? up : 0;
     }
-    return x;
-}
-
-// Exclusive prefix of x over the block's threads; the block's total in `sum`.
-__device__ __forceinline__ int block_exclusive(int x, int* part, int& sum)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int inc = warp_inclusive(x, lane);
-    __syncthreads();  // part may still be read from an earlier use
     if (lane == 31)
         part[warp] = inc;
     __syncthreads();
-    int before = 0;
-    sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        before += w < warp ? part[w] : 0;
-        sum += part[w];
-    }
-    return before + inc - x;
-}
-
-// The rank of this lane among lower lanes with the same digit, and whether it
-// is the last of them; lanes outside `takers` take no part.
-__device__ __forceinline__ int rank_of(unsigned takers, int digit, int lane, bool& last)
-{
-    const unsigned same = __match_any_sync(takers, digit);
-    last = (same >> lane) == 1u;
-    return __popc(same & ((1u << lane) - 1));
-}
-
-// Zeroes the arrival counters of the row sums, spread over the grid.
-__device__ __forceinline__ void clear_arrived(const SortArgs& a)
-{
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; k < a.arrived_count;
-         k += static_cast<int64_t>(gridDim.x) * blockDim.x)
-        a.arrived[k] = 0;
-}
-
-// --- tiled, first: keys of each (tile, bucket) ----------------------------------------
-
-template <int SRC>
-__global__ void __launch_bounds__(kThreads1) k_sort_count(const SortArgs a)
-{
-    __shared__ int hist[kMaxBuckets];
-    const int buckets = 1 << a.log_buckets;
-    for (int k = threadIdx.x; k < buckets; k += kThreads1)
-        hist[k] = 0;
-    clear_arrived(a);
-    __syncthreads();
-    const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.tile, hi = min(lo + a.tile, static_cast<int64_t>(a.at.n));
-    for (int64_t i0 = lo + threadIdx.x; i0 < hi; i0 += kBatch * kThreads1) {
-        int32_t key[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-            key[u] = i0 + u * kThreads1 < hi ? key_of<SRC>(a, i0 + u * kThreads1, a.status) : -1;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-            if (key[u] >= 0)
-                atomicAdd(&hist[key[u] & (buckets - 1)], 1);
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < buckets; k += kThreads1)
-        a.tile_count[static_cast<int64_t>(blockIdx.x) * buckets + k] = hist[k];
-}
-
-// --- tiled, second: (key, place) pairs into buckets -------------------------------------
-
-template <int SRC>
-__global__ void __launch_bounds__(kThreads1) k_sort_scatter(const SortArgs a)
-{
-    __shared__ int cnt[kWarps][kMaxBuckets];
-    __shared__ int part[kWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int buckets = 1 << a.log_buckets, tiles = gridDim.x, mine = blockIdx.x;
-    for (int k = tid; k < buckets; k += kThreads1)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            cnt[w][k] = 0;
-    __syncthreads();
-
-    const int64_t begin = static_cast<int64_t>(mine) * a.tile, end = min(begin + a.tile, static_cast<int64_t>(a.at.n));
-    const int64_t slice = a.tile / kWarps;  // a multiple of 32
-    const int64_t lo = begin + warp * slice, hi = min(lo + slice, end);
-    for (int64_t i0 = lo + lane; i0 < hi; i0 += 32) {
-        const int32_t key = key_of<SRC>(a, i0, nullptr);
-        if (key >= 0)
-            atomicAdd(&cnt[warp][key & (buckets - 1)], 1);
-    }
-    __syncthreads();
-
-    // thread t: bases of buckets t, t + 256, ...: everything in lower buckets,
-    // then the same bucket's keys in lower tiles, then in lower warps
-    int carried = 0;
-    for (int k0 = 0; k0 < buckets; k0 += kThreads1) {
-        const int k = k0 + tid;
-        int total = 0, lower = 0;
+    const int start = base + __reduce_add_sync(kAll, lane < warp ? part[lane] : 0) + inc - total;
+    if (tid < owned) {
+        const int32_t key = (tid << shift) | mine;
+        if (index_ok(all_status, key < t.keys && start >= 0 && start + total <= t.capacity))
+            t.segment[key] = make_int2(start, start + total);
+        int at = start;
 #pragma unroll 8
-        for (int t = 0; t < tiles; ++t) {
-            const int c = a.tile_count[static_cast<int64_t>(t) * buckets + k];
-            total += c;
-            lower += t < mine ? c : 0;
-        }
-        int sum;
-        const int start = carried + block_exclusive(total, part, sum);
-        carried += sum;
-        if (mine == 0)
-            a.bucket_start[k] = start;
-        int at = start + lower;
-#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const int c = cnt[w][k];
-            cnt[w][k] = at;
+            const int c = memory[w * width + tid];
+            memory[w * width + tid] = at;
             at += c;
         }
     }
-    if (mine == 0 && tid == 0) {
-        a.bucket_start[buckets] = carried;
-        *a.total = carried;
-    }
+    if (mine == mask && tid == kBlock - 1)
+        *t.total = start + total;
     __syncthreads();
 
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int32_t key = i < hi ? key_of<SRC>(a, i, nullptr) : -1;
-        const unsigned takers = __ballot_sync(kAll, key >= 0);
-        if (key >= 0) {
-            const int b = key & (buckets - 1);
-            bool last;
-            const int at = cnt[warp][b] + rank_of(takers, b, lane, last);
-            __syncwarp(takers);
-            if (last)
-                cnt[warp][b] = at + 1;
-            if (index_ok(a.status, at >= 0 && at < a.capacity))
-                a.pairs[at] = make_int2(key, static_cast<int32_t>(i));
+    const int key_bits = 32 - __clz(width - 1);
+    if (found <= kList && slice <= 65536) {
+        for (int q = 0; q < found; q += 32) {
+            const bool has = q + lane < found;
+            const uint32_t item = has ? list[q + lane] : 0;
+            const int k = static_cast<int>(item >> 16);
+            place_keys(t, count, has, k, key_bits, (k << shift) | mine, static_cast<int32_t>(lo + (item & 0xffff)), lane, all_status);
         }
-        __syncwarp();
+    } else {
+        for (int64_t i1 = lo; i1 < hi; i1 += kBatch * 32) {
+            int32_t key[kBatch];
+            read_keys<KIND, IT, false>(t.at, i1, hi, lane, nullptr, key);
+            for (int u = 0; u < kBatch; ++u) {
+                const bool has = key[u] >= 0 && (key[u] & mask) == mine;
+                if (__ballot_sync(kAll, has))
+                    place_keys(t, count, has, has ? key[u] >> shift : 0, key_bits, key[u],
+                               static_cast<int32_t>(i1 + u * 32 + lane), lane, all_status);
+            }
+        }
     }
 }
 
-// --- a bucket's keys, sorted -------------------------------------------------------------
-
-template <int SRC>
-__global__ void __launch_bounds__(kThreads1) k_sort_bucket(const SortArgs a)
+__global__ void __launch_bounds__(kBlock) k_sort(const __grid_constant__ SortArgs a)
 {
-    __shared__ int cnt[kWarps][kMaxOwn];
-    __shared__ int part[kWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int shift = a.log_buckets, mask = (1 << shift) - 1;
-    const int mine = blockIdx.x;
-    const int own = mine < a.keys ? ((a.keys - 1 - mine) >> shift) + 1 : 0;  // keys of this bucket
-    for (int k = tid; k < own; k += kThreads1)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            cnt[w][k] = 0;
-    if (SRC != kPairs)
-        clear_arrived(a);
-    __syncthreads();
-
-    int64_t begin = 0, end = a.at.n;
-    if (SRC == kPairs) {
-        begin = a.bucket_start[mine];
-        end = a.bucket_start[mine + 1];
-    }
-    const int64_t slice = (end - begin + kThreads1 - 1) / kThreads1 * 32;
-    const int64_t lo = begin + warp * slice, hi = min(lo + slice, end);
-    int* status = SRC != kPairs && mine == 0 ? a.status : nullptr;
-    int below = 0;
-    for (int64_t i0 = lo + lane; i0 < hi; i0 += kBatch * 32) {
-        int32_t key[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            key[u] = -1;
-            if (i0 + u * 32 < hi)
-                key[u] = SRC == kPairs ? a.pairs[i0 + u * 32].x : key_of<SRC>(a, i0 + u * 32, status);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (key[u] < 0)
-                continue;
-            if (SRC == kPairs || (key[u] & mask) == mine)
-                atomicAdd(&cnt[warp][key[u] >> shift], 1);
+    extern __shared__ int memory[];
+    asm volatile("griddepcontrol.launch_dependents;");
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; k < a.arrived_count;
+         k += static_cast<int64_t>(gridDim.x) * kBlock)
+        a.arrived[0][k] = a.arrived[1][k] = 0;
+    int block = blockIdx.x;
+    for (int k = 0; k < a.tasks; ++k) {
+        const int sorters = 1 << a.task[k].log_blocks;
+        if (block < sorters) {
+            const SortTask& t = a.task[k];
+            if (t.kind == kKeyToken)
+                t.at.wide ? sort_task<kKeyToken, int64_t>(t, block, memory, a.status)
+                          : sort_task<kKeyToken, int32_t>(t, block, memory, a.status);
             else
-                below += (key[u] & mask) < mine ? 1 : 0;
+                t.at.wide ? sort_task<kKeyPosition, int64_t>(t, block, memory, a.status)
+                          : sort_task<kKeyPosition, int32_t>(t, block, memory, a.status);
+            return;
         }
+        block -= sorters;
     }
-    int base = static_cast<int>(begin);
-    if (SRC != kPairs)
-        block_exclusive(below, part, base);
-    __syncthreads();
-
-    for (int k0 = 0; k0 < own; k0 += kThreads1) {
-        const int k = k0 + tid;
-        int count[kWarps], total = 0, sum;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            count[w] = k < own ? cnt[w][k] : 0;
-            total += count[w];
-        }
-        int at = base + block_exclusive(total, part, sum);
-        base += sum;
-        if (k < own) {
-            const int32_t key = (k << shift) | mine;
-            if (index_ok(a.status, key < a.keys && at >= 0 && at + total <= a.capacity))
-                a.segment[key] = make_int2(at, at + total);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                cnt[w][k] = at;
-                at += count[w];
-            }
-        }
-    }
-    if (SRC != kPairs && mine == mask && tid == 0)
-        *a.total = base;
-    __syncthreads();
-
-    for (int64_t i0 = lo; i0 < hi; i0 += kBatch * 32) {
-        int32_t key[kBatch], place[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int64_t i = i0 + u * 32 + lane;
-            key[u] = -1;
-            place[u] = static_cast<int32_t>(i);
-            if (i < hi) {
-                if (SRC == kPairs) {
-                    const int2 p = a.pairs[i];
-                    key[u] = p.x;
-                    place[u] = p.y;
-                } else {
-                    key[u] = key_of<SRC>(a, i, nullptr);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const bool take = key[u] >= 0 && (key[u] & mask) == mine;
-            const unsigned takers = __ballot_sync(kAll, take);
-            if (take) {
-                const int k = key[u] >> shift;
-                bool last;
-                const int at = cnt[warp][k] + rank_of(takers, k, lane, last);
-                __syncwarp(takers);
-                if (last)
-                    cnt[warp][k] = at + 1;
-                if (index_ok(a.status, at >= 0 && at < a.capacity)) {
-                    a.order[at] = place[u];
-                    a.sorted_key[at] = key[u];
-                }
-            }
-            __syncwarp();
-        }
-    }
-}
-
-template <int SRC>
-cudaError_t launch_from(const SortArgs& a, cudaStream_t s)
-{
-    const int buckets = 1 << a.log_buckets;
-    if (a.at.n <= kDirectPlaces) {
-        k_sort_bucket<SRC><<<buckets, kThreads1, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-    const unsigned tiles = static_cast<unsigned>((a.at.n + a.tile - 1) / a.tile);
-    k_sort_count<SRC><<<tiles, kThreads1, 0, s>>>(a);
-    k_sort_scatter<SRC><<<tiles, kThreads1, 0, s>>>(a);
-    k_sort_bucket<kPairs><<<buckets, kThreads1, 0, s>>>(a);
-    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_sort(SortArgs a, KeyKind kind, cudaStream_t s)
+cudaError_t launch_sort(SortArgs a, cudaStream_t s)
 {
-    a.log_buckets = sort_log_buckets(a.keys);
-    a.tile = sort_tile(a.at.n);
-    return kind == kKeyToken ? launch_from<kTokens>(a, s) : launch_from<kPositions>(a, s);
+    int width = 1, sorters = 0;
+    for (int k = 0; k < a.tasks; ++k) {
+        SortTask& t = a.task[k];
+        t.log_blocks = t.keys >= 128 ? 7 : 0;
+        while ((static_cast<int64_t>(kMaxOwned) << t.log_blocks) < t.keys)
+            ++t.log_blocks;
+        const int w = (t.keys + (1 << t.log_blocks) - 1) >> t.log_blocks;
+        width = width < w ? w : width;
+        sorters += 1 << t.log_blocks;
+    }
+    const size_t shared = sizeof(int) * kWarps * (width + kList);
+    static_assert(sizeof(int) * kWarps * (kMaxOwned + kList) <= 220 * 1024, "a block fits an SM");
+    if (shared > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+        if (e != cudaSuccess)
+            return e;
+    }
+    k_sort<<<sorters, kBlock, shared, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace lc

@@ -495,7 +495,7 @@ def test_refusals(ops):
         ops.dropout(torch.zeros(4, 6, 8, device="cuda")[:, 1:], drop)
 
 
-@pytest.mark.parametrize("k", [1, 2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("k", [1, 2, 3, 4, 5])
 def test_failed_allocation(ops, k, monkeypatch):
     monkeypatch.setenv("LIONCUB_FAIL_ALLOC", str(k))
     with pytest.raises(ops.LionCubError, match="memory"):
