@@ -241,7 +241,6 @@ struct TableGradient {
     int64_t rows;
     const lioncub_rows *base, *grad;
     float factor;
-    bool sorted;  // its rows are summed in the order of a sort, else by running positions
 };
 
 // Positions that run with the place are summed without a sort while a position
@@ -263,8 +262,8 @@ lc::SortTask sort_task(lioncub_embed_t h, const lc::Places& at, const TableGradi
     return t;
 }
 
-int sum_rows(lioncub_embed_t h, const lc::Places& at, const TableGradient& g, const lioncub_rows* dout,
-             const lc::DropArgs& drop, bool drop_on, cudaStream_t s)
+lc::RowSumArgs row_sum_args(lioncub_embed_t h, const lc::Places& at, const TableGradient& g, const lioncub_rows* dout,
+                            const lc::DropArgs& drop)
 {
     const lc::SortTask t = sort_task(h, at, g);
     lc::RowSumArgs a{};
@@ -285,11 +284,7 @@ int sum_rows(lioncub_embed_t h, const lc::Places& at, const TableGradient& g, co
     a.dim = static_cast<int32_t>(h->dim);
     a.n = at.n;
     a.status = h->status;
-    const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(g.base) && aligned_rows(g.grad);
-    const cudaError_t e = launch(h, "embed_row_sums", [&] {
-        return lc::launch_row_sums(a, g.sorted ? nullptr : &at, dout->type, g.grad->type, vec, drop_on, s);
-    });
-    return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "row sum launch");
+    return a;
 }
 
 // grad with its optional base: types, strides and overlaps.
@@ -486,30 +481,36 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
     if (rc != LIONCUB_OK)
         return rc;
 
-    // 1 sort; 2 position rows: they read dout in order, and what
-    // fits L2 stays there for 3 token rows
-    TableGradient tables[2] = {{lc::kKeyToken, h->vocab, base, grad, h->scale * d.rescale, true},
-                               {lc::kKeyPosition, h->positions, pos_base, pos_grad, d.rescale, true}};
+    TableGradient token = {lc::kKeyToken, h->vocab, base, grad, h->scale * d.rescale};
+    TableGradient position = {lc::kKeyPosition, h->positions, pos_base, pos_grad, d.rescale};
+    const bool running = pos_grad && !at.positions && (at.n + at.seq_len - 1) / at.seq_len <= kRunning;
+    const bool sorted_positions = pos_grad && !running;
+
     lc::SortArgs so{};
-    for (int k = 0; k < (pos_grad ? 2 : 1); ++k) {
-        TableGradient& g = tables[k];
-        g.sorted = k == 0 || at.positions || (at.n + at.seq_len - 1) / at.seq_len > kRunning;
-        if (g.sorted)
-            so.task[so.tasks++] = sort_task(h, at, g);
-    }
+    so.task[so.tasks++] = sort_task(h, at, token);
+    if (sorted_positions)
+        so.task[so.tasks++] = sort_task(h, at, position);
     const int64_t slabs = lc::grad_slabs(h->dim);
     so.arrived[0] = h->arrived;
     so.arrived[1] = h->arrived + h->arrived_count;
     so.arrived_count = 2 * lc::grad_stretches(at.n, lc::grad_piece(at.n, slabs)) * slabs;
     so.status = h->status;
-    const cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, stream); });
+    cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, stream); });
     if (e != cudaSuccess)
         return cuda_fail(h, e, "sort launch");
-    if (pos_grad)
-        rc = sum_rows(h, at, tables[1], dout, d, on, stream);
-    if (rc == LIONCUB_OK)
-        rc = sum_rows(h, at, tables[0], dout, d, on, stream);
-    return rc;
+
+    const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(base) && aligned_rows(grad) &&
+                     aligned_rows(pos_base) && aligned_rows(pos_grad);
+    const lc::RowSumArgs t = row_sum_args(h, at, token, dout, d), p = row_sum_args(h, at, position, dout, d);
+    if (sorted_positions) {
+        e = launch(h, "embed_position_sums",
+                   [&] { return lc::launch_row_sums(p, nullptr, at, dout->type, grad->type, vec, on, stream); });
+        if (e != cudaSuccess)
+            return cuda_fail(h, e, "row sum launch");
+    }
+    e = launch(h, "embed_row_sums",
+               [&] { return lc::launch_row_sums(t, running ? &p : nullptr, at, dout->type, grad->type, vec, on, stream); });
+    return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "row sum launch");
 }
 
 int lioncub_embed_status(lioncub_embed_t h, int32_t* dst_dev, lioncub_stream_t stream)

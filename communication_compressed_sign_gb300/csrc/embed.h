@@ -130,12 +130,11 @@ struct DropoutArgs {
 // starts and strides do); drop: dropout is on.
 cudaError_t launch_lookup(const LookupArgs& a, int table_type, int out_type, bool vec, bool drop, cudaStream_t s);
 cudaError_t launch_sort(SortArgs a, cudaStream_t s);
-// running: the places of a batch whose positions run with the place (the rows
-// of grad are positions, and no sort is read), or null.  Launched to overlap the
-// end of the launch before it, whose results it waits for (running: before it
-// ends, as it needs none of them).
-cudaError_t launch_row_sums(RowSumArgs a, const Places* running, int dout_type, int grad_type, bool vec, bool drop,
-                            cudaStream_t s);
+// Row sums of a table whose places are sorted, and of running's rows, the
+// positions of a batch that run with its places `at` (null: none).  Starts
+// before the launch before it has ended, and waits for it.
+cudaError_t launch_row_sums(RowSumArgs a, const RowSumArgs* running, const Places& at, int dout_type, int grad_type, bool vec,
+                            bool drop, cudaStream_t s);
 cudaError_t launch_dropout(const DropoutArgs& a, int x_type, int out_type, bool vec, bool drop, cudaStream_t s);
 
 // Column groups of a row -> thread blocks: TX threads along a row, TY rows a

@@ -130,6 +130,24 @@ __device__ __forceinline__ bool stays1(const DropArgs& d, uint64_t e)
     return lower_stays(d, static_cast<uint32_t>(u >> (16 * (e & 3))));
 }
 
+// --- sums of bf16 elements ------------------------------------------------------------
+//
+// fp32 additions that take one operand in bf16 (exact: the operand is widened,
+// the sum rounded once), so that elements need no unpacking; with a mask, one
+// comparison and one predicated addition an element.  10 % fewer instructions
+// than unpacking in a pass that integer instructions bound.
+
+__device__ __forceinline__ void add_bf16(float& sum, uint32_t x)
+{
+    asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(sum) : "h"(static_cast<unsigned short>(x)));
+}
+// the same where word > limit
+__device__ __forceinline__ void add_bf16_where(float& sum, uint32_t x, uint32_t word, uint32_t limit)
+{
+    asm("{\n\t.reg .pred p;\n\tsetp.gt.u32 p, %2, %3;\n\t@p add.rn.f32.bf16 %0, %1, %0;\n\t}"
+        : "+f"(sum) : "h"(static_cast<unsigned short>(x)), "r"(word), "r"(limit));
+}
+
 // --- a warp on a slab of 256 columns -------------------------------------------------
 //
 // Each lane holds 8 of the slab's columns: 8 in a row where the matrices allow
@@ -176,6 +194,21 @@ struct SlabMask<true> {
     {
         for_kept8(d, z + static_cast<uint32_t>(i) * d.row_step, f);
     }
+    // sum += the kept elements of a group of 8 bf16
+    __device__ __forceinline__ void add(int32_t i, const uint4& raw, float (&sum)[8])
+    {
+        const uint64_t at = z + static_cast<uint32_t>(i) * d.row_step;
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint64_t u = splitmix64_mix(at + h * kSplitMix64Step);
+            const uint32_t lo = static_cast<uint32_t>(u), hi = static_cast<uint32_t>(u >> 32);
+            add_bf16_where(sum[4 * h], w[2 * h] & 0xffff, lo << 16, d.limit);
+            add_bf16_where(sum[4 * h + 1], w[2 * h] >> 16, lo, d.limit);
+            add_bf16_where(sum[4 * h + 2], w[2 * h + 1] & 0xffff, hi << 16, d.limit);
+            add_bf16_where(sum[4 * h + 3], w[2 * h + 1] >> 16, hi, d.limit);
+        }
+    }
 };
 
 // A row may begin inside an output's four elements.  The warp draws the 65
@@ -214,12 +247,6 @@ struct SlabMask<false> {
         turn ^= 1;
     }
 };
-// Shared memory of a block's warps' masks.
-template <bool VEC>
-constexpr size_t mask_bytes(int warps)
-{
-    return VEC ? 0 : warps * sizeof(SlabMask<false>::Buffer);
-}
 
 // A lane's elements of the row that starts at element e.
 template <typename T, bool VEC>

@@ -23,7 +23,8 @@ namespace {
 
 constexpr int kSumThreads = 256;
 constexpr int kWarpsPerBlock = kSumThreads / 32;
-constexpr int kFillRows = 8;  // rows of grad a fill warp looks at
+constexpr int kFillRows = 8;           // rows of grad a fill warp looks at
+constexpr unsigned kLead = 152 * 4;    // blocks the SMs hold
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kInFlight = 4;   // rows of dout a warp loads before it adds them
 
@@ -59,17 +60,28 @@ struct Walker {
     }
     __device__ __forceinline__ void add(const SlabGroup<DT, VEC>& x, int32_t i)
     {
-        float y[8];
-        x.unpack(y);
-        if constexpr (DROP) {
-            mask.row(i, [&](int k, bool keep) {
-                if (keep)
-                    sum[k] = __fadd_rn(sum[k], y[k]);
-            });
-        } else {
+        if constexpr (VEC && sizeof(DT) == 2) {
+            if constexpr (DROP) {
+                mask.add(i, x.g.raw, sum);
+            } else {
+                const uint32_t w[4] = {x.g.raw.x, x.g.raw.y, x.g.raw.z, x.g.raw.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                sum[k] = __fadd_rn(sum[k], y[k]);
+                for (int k = 0; k < 8; ++k)
+                    add_bf16(sum[k], k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xffff);
+            }
+        } else {
+            float y[8];
+            x.unpack(y);
+            if constexpr (DROP) {
+                mask.row(i, [&](int k, bool keep) {
+                    if (keep)
+                        sum[k] = __fadd_rn(sum[k], y[k]);
+                });
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    sum[k] = __fadd_rn(sum[k], y[k]);
+            }
         }
     }
     // grad[v] = base[v] + factor * sum
@@ -137,33 +149,41 @@ struct Walker {
     }
 };
 
-// Rows [row0, row0 + kFillRows) that have no place: zeros, or base.
-template <typename GT, bool VEC, typename Empty>
-__device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int lane, Empty&& empty)
+// Row v on one slab: zeros, or base.
+template <typename GT, bool VEC>
+__device__ __forceinline__ void fill_slab(const RowSumArgs& a, const Slab<VEC>& cols, int64_t v)
 {
-    const int64_t row = row0 + lane;
-    unsigned todo = __ballot_sync(kAll, lane < kFillRows && row < a.rows && empty(row));
+    if (a.base.data) {
+        SlabGroup<GT, VEC> b;
+        b.load(cols, a.base.data, v * a.base.stride);
+        b.store(cols, a.grad.data, v * a.grad.stride);
+    } else {
+        const float zero[8] = {};
+        store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, zero);
+    }
+}
+
+// Those of rows [row0, row0 + kFillRows) that have no place.
+template <typename GT, bool VEC>
+__device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int lane)
+{
+    bool empty = false;
+    if (lane < kFillRows && row0 + lane < a.rows) {
+        const int2 seg = a.segment[row0 + lane];
+        empty = seg.x == seg.y;
+    }
+    unsigned todo = __ballot_sync(kAll, empty);
     while (todo) {
         const int64_t v = row0 + __ffs(todo) - 1;
         todo &= todo - 1;
-        for (int slab = 0; slab < a.slabs; ++slab) {
-            const Slab<VEC> cols(slab, lane, a.dim);
-            if (a.base.data) {
-                SlabGroup<GT, VEC> b;
-                b.load(cols, a.base.data, v * a.base.stride);
-                b.store(cols, a.grad.data, v * a.grad.stride);
-            } else {
-                const float zero[8] = {};
-                store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, zero);
-            }
-        }
+        for (int slab = 0; slab < a.slabs; ++slab)
+            fill_slab<GT, VEC>(a, Slab<VEC>(slab, lane, a.dim), v);
     }
 }
 
 // Programmatic launches: a kernel may start before the launch before it in the
 // stream has ended, and waits here until all of that is done and visible.
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 // The position of the n-th (from 0) set bit of a word that has more than n.
 __device__ __forceinline__ int nth_bit(unsigned word, int n)
@@ -181,33 +201,28 @@ __device__ __forceinline__ int nth_bit(unsigned word, int n)
     return at;
 }
 
-// Blocks that walk and blocks that fill, spread evenly over the grid: fills are
-// bound by memory, walks with dropout by instructions, so they run side by side.
-struct Mix {
-    uint64_t share;  // fill blocks / all blocks, in 2^-32
+// What the blocks of a launch do.  Running positions need no sort, so their
+// blocks lead (while the sort may still run); the rest of them and the fills
+// are spread evenly among the walks: walks with dropout are bound by integer
+// instructions and fills by memory, so they run side by side.
+struct Roles {
+    unsigned lead;      // running blocks at the front
+    uint64_t running;   // share of running blocks among the others, in 2^-32
+    uint64_t fill;      // share of fill blocks among walks and fills, likewise
+    __host__ __device__ __forceinline__ unsigned running_before(unsigned block) const
+    {
+        return block <= lead ? block : lead + static_cast<unsigned>(((block - lead) * running) >> 32);
+    }
     __host__ __device__ __forceinline__ unsigned fills_before(unsigned block) const
     {
-        return static_cast<unsigned>((block * share) >> 32);
+        return static_cast<unsigned>((block * fill) >> 32);
     }
 };
 
-// Walk blocks: stretches of the sorted places; fill blocks: rows without a
-// place (none in place).
+// One stretch of the sorted places on one slab.
 template <typename DT, typename GT, bool VEC, bool DROP>
-__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_row_sums(const RowSumArgs a, const Mix mix)
+__device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int warp, int lane)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned fills = mix.fills_before(blockIdx.x);
-    wait_for_launch_before();
-    if (mix.fills_before(blockIdx.x + 1) != fills) {
-        const int64_t row0 = (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows;
-        fill_rows<GT, VEC>(a, row0, lane, [&](int64_t v) {
-            const int2 seg = a.segment[v];
-            return seg.x == seg.y;
-        });
-        return;
-    }
-    const int64_t unit = static_cast<int64_t>(blockIdx.x - fills) * kWarpsPerBlock + warp;
     const int stretch = static_cast<int>(quotient(unit, a.slabs));  // places and so stretches fit 31 bits
     const int slab = static_cast<int>(unit - static_cast<int64_t>(stretch) * a.slabs);
     const int total = *a.total;
@@ -266,15 +281,20 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_row_sums(const Row
 }
 
 // Positions that run with the place, first + i % seq_len: row q's places are
-// q - first, q - first + seq_len, ... and need no sort.  Walk blocks: rows that
-// have places; fill blocks: rows that have none.
+// q - first, q - first + seq_len, ... and need no sort.  One row on one slab.
 template <typename DT, typename GT, bool VEC, bool DROP>
-__device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& at, int64_t unit, int span, int warp, int lane)
+__device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& at, int64_t unit, int warp, int lane)
 {
-    const int64_t place0 = quotient(unit, a.slabs);
-    const int slab = static_cast<int>(unit - place0 * a.slabs);
-    if (place0 >= span)
+    const int64_t row = quotient(unit, a.slabs);
+    const int slab = static_cast<int>(unit - row * a.slabs);
+    if (row >= a.rows)
         return;
+    const int64_t place0 = row - at.first;
+    if (place0 < 0 || place0 >= at.seq_len || place0 >= at.n) {
+        if (a.base.data != a.grad.data)
+            fill_slab<GT, VEC>(a, Slab<VEC>(slab, lane, a.dim), row);
+        return;
+    }
     Walker<DT, GT, VEC, DROP> w(a, slab, lane, warp_buffer<VEC, DROP>(warp));
     for (int64_t p0 = place0; p0 < at.n; p0 += 32 * at.seq_len) {
         const int64_t mine = p0 + lane * at.seq_len;
@@ -298,38 +318,53 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
             }
         }
     }
-    w.finish(at.first + place0);
+    w.finish(row);
 }
 
-template <typename DT, typename GT, bool VEC, bool DROP>
-__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3) k_running_row_sums(const RowSumArgs a, const Places at, const Mix mix)
+// a: the table whose places are sorted; p (RUNNING): running positions, whose
+// places are `at`.
+template <typename DT, typename GT, bool VEC, bool DROP, bool RUNNING>
+__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3)
+    k_row_sums(const __grid_constant__ RowSumArgs a, const __grid_constant__ RowSumArgs p, const Places at, const Roles roles)
 {
-    let_next_launch_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int span = static_cast<int>(min(at.seq_len, static_cast<int64_t>(at.n)));
-    const unsigned fills = mix.fills_before(blockIdx.x);
-    if (mix.fills_before(blockIdx.x + 1) != fills) {
-        const int64_t row0 = (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows;
-        fill_rows<GT, VEC>(a, row0, lane, [&](int64_t v) { return v < at.first || v >= at.first + span; });
-    } else {
-        running_row<DT, GT, VEC, DROP>(a, at, static_cast<int64_t>(blockIdx.x - fills) * kWarpsPerBlock + warp, span, warp, lane);
+    unsigned block = blockIdx.x;
+    if constexpr (RUNNING) {
+        const unsigned before = roles.running_before(block);
+        if (roles.running_before(block + 1) != before) {
+            running_row<DT, GT, VEC, DROP>(p, at, static_cast<int64_t>(before) * kWarpsPerBlock + warp, warp, lane);
+            wait_for_launch_before();  // the launch after this one relies on it
+            return;
+        }
+        block -= before;
     }
-    wait_for_launch_before();  // the launch after this one relies on both
+    wait_for_launch_before();
+    const unsigned fills = roles.fills_before(block);
+    if (roles.fills_before(block + 1) != fills)
+        fill_rows<GT, VEC>(a, (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows, lane);
+    else
+        walk<DT, GT, VEC, DROP>(a, static_cast<int64_t>(block - fills) * kWarpsPerBlock + warp, warp, lane);
 }
 
 unsigned blocks_for(int64_t warps) { return static_cast<unsigned>((warps + kWarpsPerBlock - 1) / kWarpsPerBlock); }
 
-template <typename DT, typename GT, bool VEC, bool DROP>
-cudaError_t launch_k(const RowSumArgs& a, const Places* running, cudaStream_t s)
+// The share of `part` among `all`, in 2^-32, rounded up: exactly part of them.
+uint64_t share_of(unsigned part, unsigned all) { return all ? ((static_cast<uint64_t>(part) << 32) + all - 1) / all : 0; }
+
+template <typename DT, typename GT, bool VEC, bool DROP, bool RUNNING>
+cudaError_t launch_r(const RowSumArgs& a, const RowSumArgs& p, const Places& at, cudaStream_t s)
 {
-    const int64_t units =
-        (running ? (running->seq_len < running->n ? running->seq_len : running->n) : grad_stretches(a.n, a.piece)) * a.slabs;
     const bool in_place = a.base.data == a.grad.data;
-    const unsigned fill = in_place ? 0 : blocks_for((a.rows + kFillRows - 1) / kFillRows);
-    const unsigned blocks = blocks_for(units) + fill;
+    const unsigned walks = blocks_for(grad_stretches(a.n, a.piece) * a.slabs);
+    const unsigned fills = in_place ? 0 : blocks_for((a.rows + kFillRows - 1) / kFillRows);
+    const unsigned running = RUNNING ? blocks_for(static_cast<int64_t>(p.rows) * p.slabs) : 0;
+    const unsigned blocks = walks + fills + running;
     if (blocks == 0)
         return cudaSuccess;
-    const Mix mix = {((static_cast<uint64_t>(fill) << 32) + blocks - 1) / blocks};
+    Roles roles;
+    roles.lead = running < kLead ? running : kLead;
+    roles.running = share_of(running - roles.lead, blocks - roles.lead);
+    roles.fill = share_of(fills, walks + fills);
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(blocks);
     c.blockDim = dim3(kSumThreads);
@@ -339,31 +374,38 @@ cudaError_t launch_k(const RowSumArgs& a, const Places* running, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     c.attrs = attr;
     c.numAttrs = 1;
-    if (running)
-        return cudaLaunchKernelEx(&c, k_running_row_sums<DT, GT, VEC, DROP>, a, *running, mix);
-    return cudaLaunchKernelEx(&c, k_row_sums<DT, GT, VEC, DROP>, a, mix);
+    return cudaLaunchKernelEx(&c, k_row_sums<DT, GT, VEC, DROP, RUNNING>, a, p, at, roles);
+}
+
+template <typename DT, typename GT, bool VEC, bool DROP>
+cudaError_t launch_k(const RowSumArgs& a, const RowSumArgs* p, const Places& at, cudaStream_t s)
+{
+    return p ? launch_r<DT, GT, VEC, DROP, true>(a, *p, at, s) : launch_r<DT, GT, VEC, DROP, false>(a, a, at, s);
 }
 
 template <typename DT, typename GT>
-cudaError_t launch_t(const RowSumArgs& a, const Places* running, bool vec, bool drop, cudaStream_t s)
+cudaError_t launch_t(const RowSumArgs& a, const RowSumArgs* p, const Places& at, bool vec, bool drop, cudaStream_t s)
 {
     if (vec)
-        return drop ? launch_k<DT, GT, true, true>(a, running, s) : launch_k<DT, GT, true, false>(a, running, s);
-    return drop ? launch_k<DT, GT, false, true>(a, running, s) : launch_k<DT, GT, false, false>(a, running, s);
+        return drop ? launch_k<DT, GT, true, true>(a, p, at, s) : launch_k<DT, GT, true, false>(a, p, at, s);
+    return drop ? launch_k<DT, GT, false, true>(a, p, at, s) : launch_k<DT, GT, false, false>(a, p, at, s);
 }
 
 }  // namespace
 
-cudaError_t launch_row_sums(RowSumArgs a, const Places* running, int dout_type, int grad_type, bool vec, bool drop,
-                            cudaStream_t s)
+cudaError_t launch_row_sums(RowSumArgs a, const RowSumArgs* running, const Places& at, int dout_type, int grad_type, bool vec,
+                            bool drop, cudaStream_t s)
 {
     a.slabs = grad_slabs(a.dim);
     a.piece = grad_piece(a.n, a.slabs);
+    RowSumArgs p = running ? *running : a;
+    p.slabs = a.slabs;
+    const RowSumArgs* q = running ? &p : nullptr;
     if (dout_type == LIONCUB_ROWS_BF16)
-        return grad_type == LIONCUB_ROWS_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, running, vec, drop, s)
-                                              : launch_t<__nv_bfloat16, float>(a, running, vec, drop, s);
-    return grad_type == LIONCUB_ROWS_BF16 ? launch_t<float, __nv_bfloat16>(a, running, vec, drop, s)
-                                          : launch_t<float, float>(a, running, vec, drop, s);
+        return grad_type == LIONCUB_ROWS_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, q, at, vec, drop, s)
+                                              : launch_t<__nv_bfloat16, float>(a, q, at, vec, drop, s);
+    return grad_type == LIONCUB_ROWS_BF16 ? launch_t<float, __nv_bfloat16>(a, q, at, vec, drop, s)
+                                          : launch_t<float, float>(a, q, at, vec, drop, s);
 }
 
 }  // namespace lc
