@@ -116,6 +116,7 @@ struct RowSumArgs {
     int32_t dim;
     int32_t slabs, piece;  // set by launch_row_sums
     int32_t n;      // rows of dout
+    int32_t scan;   // the rows are tokens': a row's places can be looked for among the batch's tokens
     int* status;
 };
 

@@ -25,6 +25,9 @@ constexpr int kSumThreads = 256;
 constexpr int kWarpsPerBlock = kSumThreads / 32;
 constexpr int kFillRows = 8;           // rows of grad a fill warp looks at
 constexpr unsigned kLead = 152 * 4;    // blocks the SMs hold
+constexpr unsigned kLeadScans = 152 * 2;  // scanning fills that run beside the sort
+constexpr int kScanRows = 64;          // rows of grad a scanning fill block takes
+constexpr int64_t kScan = 2048;        // batches up to this many places fill by scanning
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kInFlight = 4;   // rows of dout a warp loads before it adds them
 
@@ -163,6 +166,37 @@ __device__ __forceinline__ void fill_slab(const RowSumArgs& a, const Slab<VEC>& 
     }
 }
 
+// Those of rows [row0, row0 + kScanRows) that no token of the batch has, found
+// without the sort: the block looks through all tokens.
+template <typename GT, bool VEC>
+__device__ __forceinline__ void scan_and_fill(const RowSumArgs& a, const Places& at, int64_t row0, int warp, int lane)
+{
+    __shared__ unsigned has[kScanRows / 32];
+    if (threadIdx.x < kScanRows / 32)
+        has[threadIdx.x] = 0;
+    __syncthreads();
+    constexpr int kTokens = 8;  // loads in flight
+    for (int i0 = threadIdx.x; i0 < at.n; i0 += kTokens * kSumThreads) {
+        int64_t t[kTokens];
+#pragma unroll
+        for (int u = 0; u < kTokens; ++u)
+            t[u] = i0 + u * kSumThreads < at.n ? index_at(at.tokens, i0 + u * kSumThreads, at.wide) : -1;
+#pragma unroll
+        for (int u = 0; u < kTokens; ++u) {
+            const uint64_t r = static_cast<uint64_t>(t[u] - row0);
+            if (t[u] >= 0 && r < kScanRows)
+                atomicOr(&has[r >> 5], 1u << (r & 31));
+        }
+    }
+    __syncthreads();
+    for (int r = warp; r < kScanRows; r += kWarpsPerBlock) {
+        if ((has[r >> 5] >> (r & 31) & 1u) || row0 + r >= a.rows)
+            continue;
+        for (int slab = 0; slab < a.slabs; ++slab)
+            fill_slab<GT, VEC>(a, Slab<VEC>(slab, lane, a.dim), row0 + r);
+    }
+}
+
 // Those of rows [row0, row0 + kFillRows) that have no place.
 template <typename GT, bool VEC>
 __device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int lane)
@@ -201,14 +235,16 @@ __device__ __forceinline__ int nth_bit(unsigned word, int n)
     return at;
 }
 
-// What the blocks of a launch do.  Running positions need no sort, so their
-// blocks lead (while the sort may still run); the rest of them and the fills
-// are spread evenly among the walks: walks with dropout are bound by integer
-// instructions and fills by memory, so they run side by side.
+// What the blocks of a launch do.  Blocks that need no sort lead, while it may
+// still run: fills that scan the tokens (small batches), else running positions.
+// The rest are spread evenly: walks are bound by latency or, with dropout, by
+// integer instructions, and fills by memory, so they run side by side.
 struct Roles {
-    unsigned lead;      // running blocks at the front
-    uint64_t running;   // share of running blocks among the others, in 2^-32
-    uint64_t fill;      // share of fill blocks among walks and fills, likewise
+    int scan;          // fills look through the tokens (kScanRows rows a block), else through the segments
+    unsigned scans;    // such blocks at the front
+    unsigned lead;     // running blocks at the front
+    uint64_t running;  // share of running blocks among the others, in 2^-32
+    uint64_t fill;     // share of fill blocks among walks and fills, likewise
     __host__ __device__ __forceinline__ unsigned running_before(unsigned block) const
     {
         return block <= lead ? block : lead + static_cast<unsigned>(((block - lead) * running) >> 32);
@@ -329,20 +365,29 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned block = blockIdx.x;
+    if (block < roles.scans) {
+        scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(block) * kScanRows, warp, lane);
+        wait_for_launch_before();  // the launch after this one relies on it
+        return;
+    }
+    block -= roles.scans;
     if constexpr (RUNNING) {
         const unsigned before = roles.running_before(block);
         if (roles.running_before(block + 1) != before) {
             running_row<DT, GT, VEC, DROP>(p, at, static_cast<int64_t>(before) * kWarpsPerBlock + warp, warp, lane);
-            wait_for_launch_before();  // the launch after this one relies on it
+            wait_for_launch_before();
             return;
         }
         block -= before;
     }
-    wait_for_launch_before();
     const unsigned fills = roles.fills_before(block);
-    if (roles.fills_before(block + 1) != fills)
+    const bool fill = roles.fills_before(block + 1) != fills;
+    if (fill && roles.scan)
+        scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(roles.scans + fills) * kScanRows, warp, lane);
+    wait_for_launch_before();
+    if (fill && !roles.scan)
         fill_rows<GT, VEC>(a, (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows, lane);
-    else
+    else if (!fill)
         walk<DT, GT, VEC, DROP>(a, static_cast<int64_t>(block - fills) * kWarpsPerBlock + warp, warp, lane);
 }
 
@@ -356,17 +401,23 @@ cudaError_t launch_r(const RowSumArgs& a, const RowSumArgs& p, const Places& at,
 {
     const bool in_place = a.base.data == a.grad.data;
     const unsigned walks = blocks_for(grad_stretches(a.n, a.piece) * a.slabs);
-    const unsigned fills = in_place ? 0 : blocks_for((a.rows + kFillRows - 1) / kFillRows);
+    const bool scan = !in_place && a.scan && a.n <= kScan;
+    const unsigned all_fills = in_place ? 0
+                               : scan   ? static_cast<unsigned>((a.rows + kScanRows - 1) / kScanRows)
+                                        : blocks_for((a.rows + kFillRows - 1) / kFillRows);
+    const unsigned scans = scan ? (all_fills < kLeadScans ? all_fills : kLeadScans) : 0, fills = all_fills - scans;
     const unsigned running = RUNNING ? blocks_for(static_cast<int64_t>(p.rows) * p.slabs) : 0;
     const unsigned blocks = walks + fills + running;
-    if (blocks == 0)
+    if (scans + blocks == 0)
         return cudaSuccess;
     Roles roles;
-    roles.lead = running < kLead ? running : kLead;
+    roles.scan = scan;
+    roles.scans = scans;
+    roles.lead = scan ? 0 : running < kLead ? running : kLead;
     roles.running = share_of(running - roles.lead, blocks - roles.lead);
     roles.fill = share_of(fills, walks + fills);
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(blocks);
+    c.gridDim = dim3(scans + blocks);
     c.blockDim = dim3(kSumThreads);
     c.stream = s;
     cudaLaunchAttribute attr[1];

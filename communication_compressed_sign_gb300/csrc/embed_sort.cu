@@ -20,9 +20,12 @@
 namespace lc {
 namespace {
 
-constexpr int kBlock = 1024;
-constexpr int kWarps = kBlock / 32;
-constexpr int kMaxOwned = kBlock;  // keys of a block: one a thread in the scan
+// Threads of a block: 1024, or 512 for small batches, where half an SM's
+// registers are left to the row sums' launch, whose first blocks do not wait
+// for the sort.
+constexpr int kBlock = 1024, kSmallBlock = 512;
+constexpr int64_t kSmallBatch = 8192;
+constexpr int kMaxOwned = 1024;    // keys of a block
 constexpr int kBatch = 8;          // groups of 32 keys a warp loads at once
 constexpr int kList = 256;         // a warp's list; a slice with more is read again
 constexpr unsigned kAll = 0xffffffffu;
@@ -90,10 +93,11 @@ __device__ __forceinline__ void place_keys(const SortTask& t, int* next, bool ha
     __syncwarp();
 }
 
-template <int KIND, typename IT>
+template <int KIND, typename IT, int BLOCK>
 __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_status)
 {
-    __shared__ int part[kWarps + 1];
+    constexpr int kWarps = BLOCK / 32;
+    __shared__ int part[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int shift = t.log_blocks, mask = (1 << shift) - 1;
     const int owned = mine < t.keys ? ((t.keys - 1 - mine) >> shift) + 1 : 0;
@@ -101,13 +105,13 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     int* count = memory;                         // kWarps x width: keys of each (warp, key), then where the next goes
     uint32_t* list = reinterpret_cast<uint32_t*>(memory + kWarps * width) + warp * kList;  // place in slice | owned key << 16
     int* status = mine == 0 ? all_status : nullptr;
-    for (int k = tid; k < kWarps * width; k += kBlock)
+    for (int k = tid; k < kWarps * width; k += BLOCK)
         count[k] = 0;
     __syncthreads();
     count += warp * width;
 
     const int64_t n = t.at.n;
-    const int64_t slice = (n + kBlock - 1) / kBlock * 32;
+    const int64_t slice = (n + BLOCK - 1) / BLOCK * 32;
     const int64_t lo = warp * slice, hi = min(lo + slice, n);
     int found = 0, below = 0;
     auto count_keys = [&](int64_t i0, const int32_t (&key)[kBatch]) {
@@ -143,40 +147,45 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     if (lane == 0)
         part[warp] = below;
     __syncthreads();
-    const int base = __reduce_add_sync(kAll, part[lane]);
-    __syncthreads();
+    int base = __reduce_add_sync(kAll, lane < kWarps ? part[lane] : 0);
 
-    // thread k: the block's key k, over the warps
-    int total = 0;
-    if (tid < owned) {
+    // thread: one of the block's keys, over the warps
+    for (int k0 = 0; k0 < owned; k0 += BLOCK) {
+        const int k = k0 + tid;
+        int total = 0;
+        if (k < owned) {
 #pragma unroll 8
-        for (int w = 0; w < kWarps; ++w)
-            total += memory[w * width + tid];
-    }
-    int inc = total;
+            for (int w = 0; w < kWarps; ++w)
+                total += memory[w * width + k];
+        }
+        int inc = total;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(kAll, inc, o);
-        inc += lane >= o ? up : 0;
-    }
-    if (lane == 31)
-        part[warp] = inc;
-    __syncthreads();
-    const int start = base + __reduce_add_sync(kAll, lane < warp ? part[lane] : 0) + inc - total;
-    if (tid < owned) {
-        const int32_t key = (tid << shift) | mine;
-        if (index_ok(all_status, key < t.keys && start >= 0 && start + total <= t.capacity))
-            t.segment[key] = make_int2(start, start + total);
-        int at = start;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(kAll, inc, o);
+            inc += lane >= o ? up : 0;
+        }
+        __syncthreads();  // part is read above and in the round before
+        if (lane == 31)
+            part[warp] = inc;
+        __syncthreads();
+        const int others = lane < kWarps ? part[lane] : 0;
+        const int start = base + __reduce_add_sync(kAll, lane < warp ? others : 0) + inc - total;
+        base += __reduce_add_sync(kAll, others);
+        if (k < owned) {
+            const int32_t key = (k << shift) | mine;
+            if (index_ok(all_status, key < t.keys && start >= 0 && start + total <= t.capacity))
+                t.segment[key] = make_int2(start, start + total);
+            int at = start;
 #pragma unroll 8
-        for (int w = 0; w < kWarps; ++w) {
-            const int c = memory[w * width + tid];
-            memory[w * width + tid] = at;
-            at += c;
+            for (int w = 0; w < kWarps; ++w) {
+                const int c = memory[w * width + k];
+                memory[w * width + k] = at;
+                at += c;
+            }
         }
     }
-    if (mine == mask && tid == kBlock - 1)
-        *t.total = start + total;
+    if (mine == mask && tid == 0)
+        *t.total = base;
     __syncthreads();
 
     const int key_bits = 32 - __clz(width - 1);
@@ -201,12 +210,13 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     }
 }
 
-__global__ void __launch_bounds__(kBlock) k_sort(const __grid_constant__ SortArgs a)
+template <int BLOCK>
+__global__ void __launch_bounds__(BLOCK) k_sort(const __grid_constant__ SortArgs a)
 {
     extern __shared__ int memory[];
     asm volatile("griddepcontrol.launch_dependents;");
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; k < a.arrived_count;
-         k += static_cast<int64_t>(gridDim.x) * kBlock)
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * BLOCK + threadIdx.x; k < a.arrived_count;
+         k += static_cast<int64_t>(gridDim.x) * BLOCK)
         a.arrived[0][k] = a.arrived[1][k] = 0;
     int block = blockIdx.x;
     for (int k = 0; k < a.tasks; ++k) {
@@ -214,15 +224,29 @@ __global__ void __launch_bounds__(kBlock) k_sort(const __grid_constant__ SortArg
         if (block < sorters) {
             const SortTask& t = a.task[k];
             if (t.kind == kKeyToken)
-                t.at.wide ? sort_task<kKeyToken, int64_t>(t, block, memory, a.status)
-                          : sort_task<kKeyToken, int32_t>(t, block, memory, a.status);
+                t.at.wide ? sort_task<kKeyToken, int64_t, BLOCK>(t, block, memory, a.status)
+                          : sort_task<kKeyToken, int32_t, BLOCK>(t, block, memory, a.status);
             else
-                t.at.wide ? sort_task<kKeyPosition, int64_t>(t, block, memory, a.status)
-                          : sort_task<kKeyPosition, int32_t>(t, block, memory, a.status);
+                t.at.wide ? sort_task<kKeyPosition, int64_t, BLOCK>(t, block, memory, a.status)
+                          : sort_task<kKeyPosition, int32_t, BLOCK>(t, block, memory, a.status);
             return;
         }
         block -= sorters;
     }
+}
+
+template <int BLOCK>
+cudaError_t launch_block(const SortArgs& a, int blocks, int width, cudaStream_t s)
+{
+    const size_t shared = sizeof(int) * (BLOCK / 32) * (width + kList);
+    static_assert(sizeof(int) * (BLOCK / 32) * (kMaxOwned + kList) <= 220 * 1024, "a block fits an SM");
+    if (shared > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k_sort<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+        if (e != cudaSuccess)
+            return e;
+    }
+    k_sort<BLOCK><<<blocks, BLOCK, shared, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -239,15 +263,8 @@ cudaError_t launch_sort(SortArgs a, cudaStream_t s)
         width = width < w ? w : width;
         sorters += 1 << t.log_blocks;
     }
-    const size_t shared = sizeof(int) * kWarps * (width + kList);
-    static_assert(sizeof(int) * kWarps * (kMaxOwned + kList) <= 220 * 1024, "a block fits an SM");
-    if (shared > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
-        if (e != cudaSuccess)
-            return e;
-    }
-    k_sort<<<sorters, kBlock, shared, s>>>(a);
-    return cudaGetLastError();
+    return a.task[0].at.n <= kSmallBatch ? launch_block<kSmallBlock>(a, sorters, width, s)
+                                         : launch_block<kBlock>(a, sorters, width, s);
 }
 
 }  // namespace lc

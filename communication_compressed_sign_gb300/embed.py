@@ -12,6 +12,7 @@ allocate results with torch.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple
 
 from . import lioncub
@@ -48,6 +49,13 @@ class DropSpec(ctypes.Structure):
                 ("reserved", ctypes.c_uint32)]
 
 
+# The same three as bytes: a packed struct costs a third of a ctypes one, and a
+# small call is bound by what the host does.
+_pack_rows = struct.Struct("@Pqii").pack
+_pack_batch = struct.Struct("@PPqqqii").pack
+_pack_drop = struct.Struct("@QQfI").pack
+
+
 class Drop(NamedTuple):
     """Dropout with probability p (to the nearest 1/65536), drawn from stream
     number `stream` of `seed`; give each (step, worker, layer) its own."""
@@ -65,7 +73,7 @@ def load() -> ctypes.CDLL:
     if _lib is None:
         L = lioncub.load()
         vp, i64 = ctypes.c_void_p, ctypes.c_int64
-        rows, batch, drop = ctypes.POINTER(Rows), ctypes.POINTER(TokenBatch), ctypes.POINTER(DropSpec)
+        rows = batch = drop = vp  # a struct's address: byref() of one, or its bytes
         L.lioncub_embed_create.argtypes = [ctypes.POINTER(vp), i64, i64, i64, i64, ctypes.c_float]
         L.lioncub_embed_forward.argtypes = [vp, batch, rows, rows, rows, drop, vp]
         L.lioncub_embed_backward.argtypes = [vp, batch, rows, rows, rows, rows, rows, drop, vp]
@@ -96,15 +104,15 @@ def lioncub_embed_create(vocab: int, dim: int, positions: int, max_tokens: int, 
     return h.value
 
 
-def lioncub_embed_forward(h: int, batch: TokenBatch, table: Rows, pos_table, out: Rows, drop, stream: int = 0) -> None:
-    rc = load().lioncub_embed_forward(h, batch, table, pos_table, out, drop, stream or None)
+def lioncub_embed_forward(h: int, batch, table, pos_table, out, drop, stream: int = 0) -> None:
+    """batch, table, ...: structs as bytes or ctypes.byref(), None for NULL (likewise below)."""
+    rc = (_lib or load()).lioncub_embed_forward(h, batch, table, pos_table, out, drop, stream or None)
     if rc:
         _check(rc, h)
 
 
-def lioncub_embed_backward(h: int, batch: TokenBatch, dout: Rows, base, grad: Rows, pos_base, pos_grad, drop,
-                           stream: int = 0) -> None:
-    rc = load().lioncub_embed_backward(h, batch, dout, base, grad, pos_base, pos_grad, drop, stream or None)
+def lioncub_embed_backward(h: int, batch, dout, base, grad, pos_base, pos_grad, drop, stream: int = 0) -> None:
+    rc = (_lib or load()).lioncub_embed_backward(h, batch, dout, base, grad, pos_base, pos_grad, drop, stream or None)
     if rc:
         _check(rc, h)
 
@@ -118,49 +126,54 @@ def lioncub_embed_destroy(h: int) -> None:
         load().lioncub_embed_destroy(h)
 
 
-def lioncub_dropout_forward(rows: int, cols: int, x: Rows, residual, out: Rows, drop, stream: int = 0) -> None:
-    rc = load().lioncub_dropout_forward(rows, cols, x, residual, out, drop, stream or None)
+def lioncub_dropout_forward(rows: int, cols: int, x, residual, out, drop, stream: int = 0) -> None:
+    rc = (_lib or load()).lioncub_dropout_forward(rows, cols, x, residual, out, drop, stream or None)
     if rc:
         _check(rc, None)
 
 
-def lioncub_dropout_backward(rows: int, cols: int, dout: Rows, dx: Rows, drop, stream: int = 0) -> None:
-    rc = load().lioncub_dropout_backward(rows, cols, dout, dx, drop, stream or None)
+def lioncub_dropout_backward(rows: int, cols: int, dout, dx, drop, stream: int = 0) -> None:
+    rc = (_lib or load()).lioncub_dropout_backward(rows, cols, dout, dx, drop, stream or None)
     if rc:
         _check(rc, None)
 
 
 # ---- torch tensors -------------------------------------------------------------
 
-_types = None
+# What the wrappers use of torch, looked up at their first call.
+_torch = None
+_row_types = _index_types = _raw_stream = _device = None
 
 
-def _torch_types():
-    global _types
-    if _types is None:
-        import torch
-        _types = ({torch.bfloat16: ROWS_BF16, torch.float32: ROWS_F32},
-                  {torch.int64: INDEX_I64, torch.int32: INDEX_I32})
-    return _types
+def _use_torch():
+    global _torch, _row_types, _index_types, _raw_stream, _device
+    import torch
+    _row_types = {torch.bfloat16: ROWS_BF16, torch.float32: ROWS_F32}
+    _index_types = {torch.int64: INDEX_I64, torch.int32: INDEX_I32}
+    # the current stream's handle, without the Stream object that torch.cuda.current_stream() makes
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _device = torch.cuda.current_device
+    _torch = torch
 
 
-def _rows(t, name, nrows, cols, device) -> Rows:
-    """A tensor (..., cols) of nrows rows as a Rows; a view, never a copy."""
-    kind = _torch_types()[0].get(t.dtype)
-    if kind is None or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a bfloat16 or float32 tensor on {device}")
-    shape = t.shape
-    if not shape or shape[-1] != cols or t.numel() != nrows * cols:
-        raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(shape)})")
+def _rows(t, name, nrows, cols, device):
+    """A tensor (..., cols) of nrows rows on CUDA device number `device` as a
+    packed Rows; a view, never a copy."""
+    kind = _row_types.get(t.dtype)
+    if kind is None or t.get_device() != device:
+        raise ValueError(f"{name} must be a bfloat16 or float32 tensor on cuda:{device}")
+    if not t.dim() or t.size(-1) != cols or t.numel() != nrows * cols:
+        raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(t.shape)})")
     if t.is_contiguous():
-        return Rows(t.data_ptr(), cols, kind, 0)
+        return _pack_rows(t.data_ptr(), cols, kind, 0)
     try:
         t = t.view(-1, cols)  # rows a fixed distance apart
     except RuntimeError:
         raise ValueError(f"{name}: its rows do not lie a fixed distance apart") from None
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: the columns of a row must be contiguous")
-    return Rows(t.data_ptr(), t.stride(0) if nrows > 1 else cols, kind, 0)
+    return _pack_rows(t.data_ptr(), t.stride(0) if nrows > 1 else cols, kind, 0)
 
 
 def _drop_spec(drop):
@@ -169,23 +182,15 @@ def _drop_spec(drop):
     p, seed, stream = drop
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be in [0, 1] (got {p})")
-    return DropSpec(seed & 0xffffffffffffffff, stream & 0xffffffffffffffff, p, 0)
-
-
-def _stream_of(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    return _pack_drop(seed & 0xffffffffffffffff, stream & 0xffffffffffffffff, p, 0)
 
 
 def _empty(shape, dtype, device, stream):
     """A result allocated for the stream that writes it."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 class TokenEmbedding:
@@ -202,31 +207,30 @@ class TokenEmbedding:
     """
 
     def __init__(self, vocab, dim, max_tokens, *, positions=0, scale=1.0):
-        import torch
+        if _torch is None:
+            _use_torch()
         self.vocab, self.dim, self.max_tokens = int(vocab), int(dim), int(max_tokens)
         self.positions, self.scale = int(positions), float(scale)
         self.h = None
         self.h = lioncub_embed_create(self.vocab, self.dim, self.positions, self.max_tokens, self.scale)
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device = _torch.device("cuda", _device())
+        self._index = self.device.index
 
     def _batch(self, tokens, positions, seq_len, first_position):
-        kind = _torch_types()[1].get(tokens.dtype)
-        if kind is None or tokens.device != self.device or not tokens.is_contiguous():
+        if not self.h:
+            raise LionCubError(ERR_STATE, "the layer is closed")
+        kind = _index_types.get(tokens.dtype)
+        if kind is None or tokens.get_device() != self._index or not tokens.is_contiguous():
             raise ValueError(f"tokens must be a contiguous int64 or int32 tensor on {self.device}")
-        at = None
+        n, at = tokens.numel(), 0
         if positions is not None:
-            if (positions.dtype != tokens.dtype or positions.device != self.device or not positions.is_contiguous()
-                    or positions.numel() != tokens.numel()):
+            if (positions.dtype != tokens.dtype or positions.get_device() != self._index
+                    or not positions.is_contiguous() or positions.numel() != n):
                 raise ValueError("positions must be a contiguous tensor of tokens' type, size and device")
             at = positions.data_ptr()
         if seq_len is None:
-            seq_len = tokens.shape[-1] if tokens.dim() else 1
-        return TokenBatch(tokens.data_ptr(), at, tokens.numel(), max(1, seq_len), first_position, kind, 0)
-
-    def _handle(self):
-        if not self.h:
-            raise LionCubError(ERR_STATE, "the layer is closed")
-        return self.h
+            seq_len = tokens.size(-1) if tokens.dim() else 1
+        return n, _pack_batch(tokens.data_ptr(), at, n, max(1, seq_len), first_position, kind, 0)
 
     def forward(self, tokens, table, pos_table=None, *, positions=None, seq_len=None, first_position=0, drop=None,
                 out=None, out_dtype=None, stream=None):
@@ -237,17 +241,15 @@ class TokenEmbedding:
         first_position + the place's index in its sequence of seq_len (the
         last dimension of tokens).  out_dtype: bfloat16 (default) or float32.
         """
-        h = self._handle()
-        batch = self._batch(tokens, positions, seq_len, first_position)
-        D = self.dim
+        n, batch = self._batch(tokens, positions, seq_len, first_position)
+        D, dev = self.dim, self._index
         # the tensors stay referenced until the launch, so that no result is allocated in an argument's memory
-        rows = _rows(table, "table", self.vocab, D, self.device)
-        pos = None if pos_table is None else _rows(pos_table, "pos_table", self.positions, D, self.device)
+        rows = _rows(table, "table", self.vocab, D, dev)
+        pos = None if pos_table is None else _rows(pos_table, "pos_table", self.positions, D, dev)
         if out is None:
-            import torch
-            out = _empty((*tokens.shape, D), out_dtype or torch.bfloat16, self.device, stream)
-        lioncub_embed_forward(h, batch, rows, pos, _rows(out, "out", batch.n, D, self.device), _drop_spec(drop),
-                              _stream_of(stream))
+            out = _empty((*tokens.shape, D), out_dtype or _torch.bfloat16, self.device, stream)
+        lioncub_embed_forward(self.h, batch, rows, pos, _rows(out, "out", n, D, dev), _drop_spec(drop),
+                              _raw_stream(dev) if stream is None else stream.cuda_stream)
         return out
 
     def backward(self, tokens, dout, grad, *, pos_grad=None, base=None, pos_base=None, positions=None, seq_len=None,
@@ -256,22 +258,22 @@ class TokenEmbedding:
         from dout (tokens.shape + (dim,)), with the forward call's places and
         drop.  base / pos_base are added; passing grad itself as base adds in
         place and touches only the rows of the batch's tokens."""
-        h = self._handle()
-        batch = self._batch(tokens, positions, seq_len, first_position)
-        D, dev = self.dim, self.device
+        n, batch = self._batch(tokens, positions, seq_len, first_position)
+        D, dev = self.dim, self._index
         g = _rows(grad, "grad", self.vocab, D, dev)
         b = None if base is None else _rows(base, "base", self.vocab, D, dev)
         pg = None if pos_grad is None else _rows(pos_grad, "pos_grad", self.positions, D, dev)
         pb = None if pos_base is None else _rows(pos_base, "pos_base", self.positions, D, dev)
-        lioncub_embed_backward(h, batch, _rows(dout, "dout", batch.n, D, dev), b, g, pb, pg, _drop_spec(drop),
-                               _stream_of(stream))
+        lioncub_embed_backward(self.h, batch, _rows(dout, "dout", n, D, dev), b, g, pb, pg, _drop_spec(drop),
+                               _raw_stream(dev) if stream is None else stream.cuda_stream)
         return grad
 
     def status(self) -> int:
         """The status word (LIONCUB_STATUS_* and STATUS_INDEX bits; 0: all is well).  Synchronizes."""
-        import torch
-        word = torch.zeros(1, dtype=torch.int32, device=self.device)
-        lioncub_embed_status(self._handle(), word.data_ptr(), _stream_of(None))
+        if not self.h:
+            raise LionCubError(ERR_STATE, "the layer is closed")
+        word = _torch.zeros(1, dtype=_torch.int32, device=self.device)
+        lioncub_embed_status(self.h, word.data_ptr(), _raw_stream(self._index))
         return int(word.item())
 
     def close(self):
@@ -286,36 +288,38 @@ class TokenEmbedding:
             pass
 
 
-def _matrix_shape(x, name):
-    import torch
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+def _matrix(x, name):
+    """(rows, cols, device number) of a tensor on the current CUDA device."""
+    if _torch is None:
+        _use_torch()
+    dev = x.get_device()
+    if dev < 0 or dev != _device():
         raise ValueError(f"{name} must be on the current CUDA device")
-    if x.dim() == 0:
+    if not x.dim():
         raise ValueError(f"{name} must have at least one dimension")
-    cols = x.shape[-1]
-    return (x.numel() // cols if cols else 0), cols
+    cols = x.size(-1)
+    return x.numel() // cols if cols else 0, cols, dev
 
 
 def dropout(x, drop: Drop, *, residual=None, out=None, stream=None):
     """drop(x), plus `residual` (of the result's type) when given.  out: where
     to write (x itself, or the residual itself, is allowed); default a new
     tensor of residual's type, or x's."""
-    rows, cols = _matrix_shape(x, "x")
-    dev = x.device
+    rows, cols, dev = _matrix(x, "x")
     if out is None:
-        out = _empty(x.shape, (x if residual is None else residual).dtype, dev, stream)
+        out = _empty(x.shape, (x if residual is None else residual).dtype, x.device, stream)
     r = None if residual is None else _rows(residual, "residual", rows, cols, dev)
     lioncub_dropout_forward(rows, cols, _rows(x, "x", rows, cols, dev), r, _rows(out, "out", rows, cols, dev),
-                            _drop_spec(drop), _stream_of(stream))
+                            _drop_spec(drop), _raw_stream(dev) if stream is None else stream.cuda_stream)
     return out
 
 
 def dropout_backward(dout, drop: Drop, *, out=None, stream=None):
     """The gradient of :func:`dropout` with respect to x, from the gradient of
     its result, with the same drop; out may be dout itself."""
-    rows, cols = _matrix_shape(dout, "dout")
+    rows, cols, dev = _matrix(dout, "dout")
     if out is None:
         out = _empty(dout.shape, dout.dtype, dout.device, stream)
-    lioncub_dropout_backward(rows, cols, _rows(dout, "dout", rows, cols, dout.device),
-                             _rows(out, "out", rows, cols, dout.device), _drop_spec(drop), _stream_of(stream))
+    lioncub_dropout_backward(rows, cols, _rows(dout, "dout", rows, cols, dev), _rows(out, "out", rows, cols, dev),
+                             _drop_spec(drop), _raw_stream(dev) if stream is None else stream.cuda_stream)
     return out

@@ -32,6 +32,9 @@ def test_symbols_and_struct_sizes(em):
     lib = ctypes.CDLL(em.lioncub.LIB_PATH)
     assert all(hasattr(lib, name) for name in declared)
     assert [ctypes.sizeof(t) for t in (em.Rows, em.TokenBatch, em.DropSpec)] == [24, 48, 24]
+    assert em._pack_rows(1 << 40, 5, 1, 0) == bytes(em.Rows(1 << 40, 5, 1, 0))
+    assert em._pack_batch(1 << 40, 0, 7, 3, 2, 1, 0) == bytes(em.TokenBatch(1 << 40, None, 7, 3, 2, 1, 0))
+    assert em._pack_drop(2**64 - 1, 9, 0.25, 0) == bytes(em.DropSpec(2**64 - 1, 9, 0.25, 0))
 
 
 def test_create_refusals(em):
@@ -59,8 +62,8 @@ def test_dropout_refusals(em):
     drop = em.DropSpec(1, 2, 0.5, 0)
 
     def call(rows, cols, x=(4096, None, 1), out=(1 << 20, None, 1), res=None, d=drop):
-        r = lambda t: em.Rows(t[0], cols if t[1] is None else t[1], t[2], 0)  # noqa: E731
-        return L.lioncub_dropout_forward(rows, cols, r(x), r(res) if res else None, r(out), d, None)
+        r = lambda t: ctypes.byref(em.Rows(t[0], cols if t[1] is None else t[1], t[2], 0))  # noqa: E731
+        return L.lioncub_dropout_forward(rows, cols, r(x), r(res) if res else None, r(out), ctypes.byref(d), None)
 
     assert call(-1, 8) == arg and call(8, -1) == arg and call(1 << 32, 8) == arg and call(1, 1 << 42) == arg
     assert call(8, 8, x=(None, None, 1)) == arg
