@@ -4,60 +4,111 @@
 // from the same counters.
 //
 // Memory-bound: each element is read and written once and no mask exists in
-// memory.  One thread takes a group of 8 elements (one where rows are apart and
-// not 16-byte aligned).
+// memory.  Dense, aligned matrices are one flat vector, 8 elements a thread;
+// others are taken by rows, a warp on a slab of columns.
+#include <climits>
+
 #include "embed_device.cuh"
 
 namespace lc {
 namespace {
 
-constexpr int kDropoutThreads = 256;
+constexpr int kBlock = 256;
+constexpr int kWarps = kBlock / 32;
 
-// Elements [e, e + V) of a matrix whose rows start at these element offsets.
-template <typename XT, typename OT, int V, bool DROP>
-__device__ __forceinline__ void drop_group(const DropoutArgs& a, int64_t e, int64_t ex, int64_t er, int64_t eo)
+// x = keep ? r x : 0 (+ residual)
+__device__ __forceinline__ float dropped(const DropArgs& d, float x, bool keep)
 {
-    float x[V];
-    load_row<XT, V>(a.x.data, ex, x);
-    if constexpr (DROP) {
-        auto scale = [&](int k, bool keep) { x[k] = keep ? __fmul_rn(a.drop.rescale, x[k]) : 0.0f; };
-        if constexpr (V == 8)
-            for_kept8(a.drop, a.drop.first + (static_cast<uint64_t>(e) >> 2) * kSplitMix64Step, scale);
-        else
-            scale(0, stays1(a.drop, e));
-    }
-    if (a.residual.data) {
-        float y[V];
-        load_row<OT, V>(a.residual.data, er, y);
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            x[k] = __fadd_rn(x[k], y[k]);
-    }
-    store_row<OT, V>(a.out.data, eo, x);
+    return keep ? __fmul_rn(d.rescale, x) : 0.0f;
 }
 
-// Dense matrices: one flat vector, whatever the width, the last group ragged.
+// The last elements of a flat vector, one by one.
 template <typename XT, typename OT, bool DROP>
-__global__ void __launch_bounds__(kDropoutThreads) k_dropout_flat(const DropoutArgs a)
+__device__ __forceinline__ void drop_one(const DropoutArgs& a, int64_t e)
+{
+    float x = static_cast<float>(static_cast<const XT*>(a.x.data)[e]);
+    if constexpr (DROP) {
+        const uint64_t u = splitmix64_mix(a.drop.first + (static_cast<uint64_t>(e) >> 2) * kSplitMix64Step);
+        x = dropped(a.drop, x, lower_stays(a.drop, static_cast<uint32_t>(u >> (16 * (e & 3)))));
+    }
+    if (a.residual.data)
+        x = __fadd_rn(x, static_cast<float>(static_cast<const OT*>(a.residual.data)[e]));
+    static_cast<OT*>(a.out.data)[e] = static_cast<OT>(x);
+}
+
+template <typename XT, typename OT, bool DROP>
+__global__ void __launch_bounds__(kBlock) k_dropout_flat(const DropoutArgs a)
 {
     const int64_t n = a.rows * a.cols;
-    const int64_t e = (static_cast<int64_t>(blockIdx.x) * kDropoutThreads + threadIdx.x) * 8;
-    if (e + 8 <= n)
-        drop_group<XT, OT, 8, DROP>(a, e, e, e, e);
-    else
+    const int64_t e = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * 8;
+    if (e + 8 > n) {
         for (int64_t k = e; k < n; ++k)
-            drop_group<XT, OT, 1, DROP>(a, k, k, k, k);
+            drop_one<XT, OT, DROP>(a, k);
+        return;
+    }
+    Group8<XT> in;
+    Group8<OT> res, out;
+    in.load(a.x.data, e);
+    if (a.residual.data)
+        res.load(a.residual.data, e);
+    float x[8];
+    in.unpack(x);
+    if constexpr (DROP)
+        for_kept8(a.drop, a.drop.first + (static_cast<uint64_t>(e) >> 2) * kSplitMix64Step,
+                  [&](int k, bool keep) { x[k] = dropped(a.drop, x[k], keep); });
+    if (a.residual.data) {
+        float y[8];
+        res.unpack(y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = __fadd_rn(x[k], y[k]);
+    }
+    out.pack(x);
+    out.store(a.out.data, e);
 }
 
-// Rows apart from one another (or not 16-byte aligned).
-template <typename XT, typename OT, int V, bool DROP>
-__global__ void __launch_bounds__(kDropoutThreads) k_dropout_rows(const DropoutArgs a)
+constexpr int kRows = 4;  // rows a warp loads before it works on them
+
+template <typename XT, typename OT, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kBlock) k_dropout_rows(const DropoutArgs a, const int slabs)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const int64_t j = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V;
-    if (i < a.rows && j < a.cols)
-        drop_group<XT, OT, V, DROP>(a, i * a.cols + j, i * a.x.stride + j, i * a.residual.stride + j,
-                                    i * a.out.stride + j);
+    constexpr int N = kLaneCols<VEC>;
+    __shared__ typename SlabMask<VEC>::Shared shared[DROP ? kWarps : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int64_t row0 = quotient(unit, slabs) * kRows;
+    const int slab = static_cast<int>(unit - row0 / kRows * slabs);
+    if (row0 >= a.rows)
+        return;
+    const Slab<VEC> cols(slab, lane, static_cast<int>(a.cols));
+    SlabMask<VEC> mask(a.drop, slab, lane, static_cast<int>(a.cols), &shared[DROP ? warp : 0]);
+    SlabGroup<XT, VEC> in[kRows];
+    SlabGroup<OT, VEC> res[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const int64_t i = min(row0 + u, a.rows - 1);
+        in[u].load(cols, a.x.data, i * a.x.stride);
+        if (a.residual.data)
+            res[u].load(cols, a.residual.data, i * a.residual.stride);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const int64_t i = row0 + u;
+        if (i >= a.rows)
+            break;
+        float x[N];
+        in[u].unpack(x);
+        if constexpr (DROP)
+            mask.row(static_cast<uint32_t>(i), [&](int k, bool keep) { x[k] = dropped(a.drop, x[k], keep); });
+        if (a.residual.data) {
+            float y[N];
+            res[u].unpack(y);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                x[k] = __fadd_rn(x[k], y[k]);
+        }
+        store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, x);
+    }
 }
 
 template <typename XT, typename OT, bool DROP>
@@ -65,15 +116,19 @@ cudaError_t launch_t(const DropoutArgs& a, bool vec, cudaStream_t s)
 {
     const bool dense = a.x.stride == a.cols && a.out.stride == a.cols && (!a.residual.data || a.residual.stride == a.cols);
     if (vec && dense) {
-        const int64_t blocks = (a.rows * a.cols + kDropoutThreads * 8 - 1) / (kDropoutThreads * 8);
-        k_dropout_flat<XT, OT, DROP><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, s>>>(a);
-    } else if (vec && a.cols % 8 == 0) {
-        const RowGrid g = row_grid(a.rows, a.cols / 8, kDropoutThreads);
-        k_dropout_rows<XT, OT, 8, DROP><<<g.grid, g.block, 0, s>>>(a);
-    } else {
-        const RowGrid g = row_grid(a.rows, a.cols, kDropoutThreads);
-        k_dropout_rows<XT, OT, 1, DROP><<<g.grid, g.block, 0, s>>>(a);
+        const int64_t blocks = (a.rows * a.cols + kBlock * 8 - 1) / (kBlock * 8);
+        k_dropout_flat<XT, OT, DROP><<<static_cast<unsigned>(blocks), kBlock, 0, s>>>(a);
+        return cudaGetLastError();
     }
+    const bool wide = vec && a.cols % 8 == 0;
+    const int slabs = slabs_of(a.cols, wide);
+    const int64_t blocks = ((a.rows + kRows - 1) / kRows * slabs + kWarps - 1) / kWarps;
+    if (blocks > INT_MAX)
+        return cudaErrorInvalidConfiguration;
+    if (wide)
+        k_dropout_rows<XT, OT, true, DROP><<<static_cast<unsigned>(blocks), kBlock, 0, s>>>(a, slabs);
+    else
+        k_dropout_rows<XT, OT, false, DROP><<<static_cast<unsigned>(blocks), kBlock, 0, s>>>(a, slabs);
     return cudaGetLastError();
 }
 

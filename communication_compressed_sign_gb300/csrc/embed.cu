@@ -37,7 +37,7 @@ struct lioncub_embed_s {
     int32_t* order = nullptr;    // for each table: max_tokens places, grouped by key, and their keys
     int2* segment = nullptr;     // vocab + positions ranges of order
     int32_t* arrived = nullptr;  // arrival counters of the row sums, for each table
-    float* partial = nullptr;    // partial_rows x partial_stride sums of pieces
+    float* partial = nullptr;    // partial_rows x partial_stride sums of pieces, for each table
     int64_t arrived_count = 0, partial_rows = 0, partial_stride = 0;
 
     // fault injection (environment, read at create; 0 = off)
@@ -274,7 +274,7 @@ lc::RowSumArgs row_sum_args(lioncub_embed_t h, const lc::Places& at, const Table
     a.sorted_key = t.sorted_key;
     a.segment = t.segment;
     a.total = t.total;
-    a.partial = h->partial;
+    a.partial = h->partial + g.kind * h->partial_rows * h->partial_stride;
     a.partial_stride = h->partial_stride;
     a.partial_rows = h->partial_rows;
     a.arrived = h->arrived + g.kind * h->arrived_count;
@@ -380,10 +380,11 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     h->max_tokens = max_tokens;
     h->scale = scale;
     const int64_t tables = positions > 0 ? 2 : 1;
-    const int64_t stretches = lc::grad_max_stretches(max_tokens, lc::grad_slabs(dim));
+    const int64_t slabs = lc::slabs_of(dim, false);  // the most: rows that allow 16-byte moves have fewer
+    const int64_t stretches = lc::grad_max_stretches(max_tokens, lc::slabs_of(dim, true));
     h->partial_rows = 2 * stretches;
-    h->partial_stride = lc::grad_slabs(dim) * int64_t(256);
-    h->arrived_count = h->partial_rows * lc::grad_slabs(dim);
+    h->partial_stride = slabs * 256;
+    h->arrived_count = h->partial_rows * slabs;
     h->fail_alloc_at = env_index("LIONCUB_FAIL_ALLOC");
     h->fail_launch_at = env_index("LIONCUB_FAIL_LAUNCH");
     cudaError_t e = cudaGetDevice(&h->device);
@@ -396,9 +397,9 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     if (e == cudaSuccess)
         e = guarded_alloc(h, &h->segment, vocab + positions);
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->arrived, 2 * h->arrived_count);
+        e = guarded_alloc(h, &h->arrived, tables * h->arrived_count);
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->partial, h->partial_rows * h->partial_stride);
+        e = guarded_alloc(h, &h->partial, tables * h->partial_rows * h->partial_stride);
     if (e == cudaSuccess)
         e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
@@ -491,26 +492,22 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
     so.task[so.tasks++] = sort_task(h, at, token);
     if (sorted_positions)
         so.task[so.tasks++] = sort_task(h, at, position);
-    const int64_t slabs = lc::grad_slabs(h->dim);
+    const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(base) && aligned_rows(grad) &&
+                     aligned_rows(pos_base) && aligned_rows(pos_grad);
+    const int64_t slabs = lc::slabs_of(h->dim, vec);
     so.arrived[0] = h->arrived;
-    so.arrived[1] = h->arrived + h->arrived_count;
+    so.arrived[1] = sorted_positions ? h->arrived + h->arrived_count : h->arrived;
     so.arrived_count = 2 * lc::grad_stretches(at.n, lc::grad_piece(at.n, slabs)) * slabs;
     so.status = h->status;
     cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, stream); });
     if (e != cudaSuccess)
         return cuda_fail(h, e, "sort launch");
 
-    const bool vec = h->dim % 8 == 0 && aligned_rows(dout) && aligned_rows(base) && aligned_rows(grad) &&
-                     aligned_rows(pos_base) && aligned_rows(pos_grad);
     const lc::RowSumArgs t = row_sum_args(h, at, token, dout, d), p = row_sum_args(h, at, position, dout, d);
-    if (sorted_positions) {
-        e = launch(h, "embed_position_sums",
-                   [&] { return lc::launch_row_sums(p, nullptr, at, dout->type, grad->type, vec, on, stream); });
-        if (e != cudaSuccess)
-            return cuda_fail(h, e, "row sum launch");
-    }
-    e = launch(h, "embed_row_sums",
-               [&] { return lc::launch_row_sums(t, running ? &p : nullptr, at, dout->type, grad->type, vec, on, stream); });
+    const lc::PositionKind kind = !pos_grad ? lc::kNoPositions : running ? lc::kRunningPositions : lc::kSortedPositions;
+    e = launch(h, "embed_row_sums", [&] {
+        return lc::launch_row_sums(t, pos_grad ? &p : nullptr, kind, at, dout->type, grad->type, vec, on, stream);
+    });
     return e == cudaSuccess ? LIONCUB_OK : cuda_fail(h, e, "row sum launch");
 }
 

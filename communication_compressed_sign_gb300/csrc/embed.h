@@ -41,6 +41,10 @@ struct Places {
     int32_t npos;  // rows of the position table
 };
 
+// Slabs of columns that warps take a row by: 256 wide where matrices allow
+// 16-byte moves, else 224.
+inline int32_t slabs_of(int64_t cols, bool vec) { return static_cast<int32_t>(vec ? (cols + 255) / 256 : (cols + 223) / 224); }
+
 struct LookupArgs {
     Places at;
     Rows table, pos_table, out;  // pos_table.data may be null
@@ -74,7 +78,6 @@ inline int64_t grad_max_stretches(int64_t n, int64_t slabs)
     const int64_t most = few > many ? few : many;
     return most < grad_stretches(n, kMinPiece) ? most : grad_stretches(n, kMinPiece);
 }
-inline int32_t grad_slabs(int64_t dim) { return static_cast<int32_t>((dim + 255) / 256); }
 
 // The sort of a batch's places by key: order holds the places grouped by key,
 // ascending within a key, sorted_key their keys; segment[key] is the key's
@@ -107,7 +110,7 @@ struct RowSumArgs {
     const int2* segment;
     const int32_t* total;
     float* partial;          // two fp32 rows for each stretch
-    int64_t partial_stride;  // 256 * slabs
+    int64_t partial_stride;  // 256 for each slab
     int64_t partial_rows;
     int32_t* arrived;        // arrivals, for each (row of partial, slab)
     DropArgs drop;
@@ -131,28 +134,12 @@ struct DropoutArgs {
 // starts and strides do); drop: dropout is on.
 cudaError_t launch_lookup(const LookupArgs& a, int table_type, int out_type, bool vec, bool drop, cudaStream_t s);
 cudaError_t launch_sort(SortArgs a, cudaStream_t s);
-// Row sums of a table whose places are sorted, and of running's rows, the
-// positions of a batch that run with its places `at` (null: none).  Starts
+// Row sums of a table whose places are sorted and, in the same launch, of
+// `positions` (null: none): sorted too, or running with its places `at`.  Starts
 // before the launch before it has ended, and waits for it.
-cudaError_t launch_row_sums(RowSumArgs a, const RowSumArgs* running, const Places& at, int dout_type, int grad_type, bool vec,
-                            bool drop, cudaStream_t s);
+enum PositionKind { kNoPositions = 0, kRunningPositions = 1, kSortedPositions = 2 };
+cudaError_t launch_row_sums(RowSumArgs a, const RowSumArgs* positions, PositionKind kind, const Places& at, int dout_type,
+                            int grad_type, bool vec, bool drop, cudaStream_t s);
 cudaError_t launch_dropout(const DropoutArgs& a, int x_type, int out_type, bool vec, bool drop, cudaStream_t s);
-
-// Column groups of a row -> thread blocks: TX threads along a row, TY rows a
-// block, so that a thread's row and columns need no division and nearly every
-// thread of a block has work whatever the width.
-struct RowGrid {
-    dim3 block, grid;
-};
-inline RowGrid row_grid(int64_t rows, int64_t groups, int threads)
-{
-    const int64_t slabs = (groups + threads - 1) / threads;
-    const int64_t tx = (groups + slabs - 1) / slabs;
-    const int64_t ty = threads / tx;
-    RowGrid g;
-    g.block = dim3(static_cast<unsigned>(tx), static_cast<unsigned>(ty));
-    g.grid = dim3(static_cast<unsigned>((rows + ty - 1) / ty), static_cast<unsigned>(slabs));
-    return g;
-}
 
 }  // namespace lc

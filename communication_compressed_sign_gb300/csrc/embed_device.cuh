@@ -1,6 +1,6 @@
 // embed_device.cuh -- element moves, the dropout mask and place lookups shared
 // by the input-layer kernels.  As in device_common.cuh, every float operation
-// is an explicit round-to-nearest intrinsic.
+// rounds once to nearest and no product is fused with a sum.
 #pragma once
 
 #include "device_common.cuh"
@@ -9,20 +9,17 @@
 
 namespace lc {
 
-// --- V consecutive elements of a row <-> floats ---------------------------------
+constexpr unsigned kAll = 0xffffffffu;
+
+// --- 8 consecutive, 16-byte aligned elements ------------------------------------------
 
 // The elements as they lie in memory, so that groups waiting in registers take
 // no more room than they did there.
-template <typename T, int V>
-struct Group {
-    static_assert(V == 1, "one element or a 16-byte aligned group of 8");
-    T raw;
-    __device__ __forceinline__ void load(const void* base, int64_t e) { raw = static_cast<const T*>(base)[e]; }
-    __device__ __forceinline__ void unpack(float (&x)[1]) const { x[0] = static_cast<float>(raw); }
-};
+template <typename T>
+struct Group8;
 
 template <>
-struct Group<__nv_bfloat16, 8> {
+struct Group8<__nv_bfloat16> {
     uint4 raw;
     __device__ __forceinline__ void load(const void* base, int64_t e)
     {
@@ -39,10 +36,19 @@ struct Group<__nv_bfloat16, 8> {
         x[4] = bf16_bits_lo(raw.z); x[5] = bf16_bits_hi(raw.z);
         x[6] = bf16_bits_lo(raw.w); x[7] = bf16_bits_hi(raw.w);
     }
+    static __device__ __forceinline__ uint32_t pair(float lo, float hi)
+    {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    __device__ __forceinline__ void pack(const float (&x)[8])
+    {
+        raw = make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(x[4], x[5]), pair(x[6], x[7]));
+    }
 };
 
 template <>
-struct Group<float, 8> {
+struct Group8<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const void* base, int64_t e)
     {
@@ -61,37 +67,115 @@ struct Group<float, 8> {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
+    __device__ __forceinline__ void pack(const float (&x)[8])
+    {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const void* base, int64_t e, float (&x)[V])
-{
-    Group<T, V> g;
-    g.load(base, e);
-    g.unpack(x);
-}
+// --- a warp on a slab of a row --------------------------------------------------------
+//
+// Where the matrices allow 16-byte moves (VEC) a slab is 256 columns, 8 in a
+// row for each lane.  Else it is 224, every 32nd from a lane's own, so that a
+// warp's scalar moves are contiguous; 224 rather than 256 because its elements
+// then touch 57 outputs of the generator at most, two for each lane.
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
+template <bool VEC>
+constexpr int kLaneCols = VEC ? 8 : 7;
 
-template <typename T, int V>
-__device__ __forceinline__ void store_row(void* base, int64_t e, const float (&x)[V])
-{
-    if constexpr (V == 8 && sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e) =
-            make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
-    } else if constexpr (V == 8) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + e);
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else if constexpr (sizeof(T) == 2) {
-        static_cast<__nv_bfloat16*>(base)[e] = __float2bfloat16_rn(x[0]);
-    } else {
-        static_cast<float*>(base)[e] = x[0];
+template <bool VEC>
+struct Slab;
+
+template <>
+struct Slab<true> {
+    int col;
+    bool on;
+    __device__ __forceinline__ Slab(int slab, int lane, int dim) : col(slab * 256 + lane * 8), on(col < dim) {}
+};
+
+template <>
+struct Slab<false> {
+    int col;
+    int count;  // columns of this lane: col, col + 32, ...
+    __device__ __forceinline__ Slab(int slab, int lane, int dim) : col(slab * 224 + lane)
+    {
+        const int left = dim - col;
+        count = left <= 0 ? 0 : (left > 192 ? 7 : (left + 31) / 32);
     }
+};
+
+// A lane's elements of the row that starts at element e.
+template <typename T, bool VEC>
+struct SlabGroup;
+
+template <typename T>
+struct SlabGroup<T, true> {
+    Group8<T> g;
+    __device__ __forceinline__ void load(const Slab<true>& c, const void* base, int64_t e)
+    {
+        if (c.on)
+            g.load(base, e + c.col);
+        else
+            g = Group8<T>{};
+    }
+    __device__ __forceinline__ void store(const Slab<true>& c, void* base, int64_t e) const
+    {
+        if (c.on)
+            g.store(base, e + c.col);
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const { g.unpack(x); }
+    __device__ __forceinline__ void pack(const float (&x)[8]) { g.pack(x); }
+};
+
+template <typename T>
+struct SlabGroup<T, false> {
+    T x[7];
+    __device__ __forceinline__ void load(const Slab<false>& c, const void* base, int64_t e)
+    {
+        const T* p = static_cast<const T*>(base) + e + c.col;
+        if (c.count == 7) {
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                x[k] = p[32 * k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                x[k] = k < c.count ? p[32 * k] : T(0.0f);
+        }
+    }
+    __device__ __forceinline__ void store(const Slab<false>& c, void* base, int64_t e) const
+    {
+        T* p = static_cast<T*>(base) + e + c.col;
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+            if (k < c.count)
+                p[32 * k] = x[k];
+    }
+    __device__ __forceinline__ void unpack(float (&y)[7]) const
+    {
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+            y[k] = static_cast<float>(x[k]);
+    }
+    __device__ __forceinline__ void pack(const float (&y)[7])
+    {
+#pragma unroll
+        for (int k = 0; k < 7; ++k) {
+            if constexpr (sizeof(T) == 2)
+                x[k] = __float2bfloat16_rn(y[k]);
+            else
+                x[k] = y[k];
+        }
+    }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_slab(const Slab<VEC>& c, void* base, int64_t e, const float (&x)[kLaneCols<VEC>])
+{
+    SlabGroup<T, VEC> g;
+    g.pack(x);
+    g.store(c, base, e);
 }
 
 // --- the dropout mask -------------------------------------------------------------
@@ -124,19 +208,10 @@ __device__ __forceinline__ void for_kept8(const DropArgs& d, uint64_t z, F&& f)
     }
 }
 
-__device__ __forceinline__ bool stays1(const DropArgs& d, uint64_t e)
-{
-    const uint64_t u = splitmix64_mix(d.first + (e >> 2) * kSplitMix64Step);
-    return lower_stays(d, static_cast<uint32_t>(u >> (16 * (e & 3))));
-}
-
-// --- sums of bf16 elements ------------------------------------------------------------
-//
 // fp32 additions that take one operand in bf16 (exact: the operand is widened,
 // the sum rounded once), so that elements need no unpacking; with a mask, one
 // comparison and one predicated addition an element.  10 % fewer instructions
 // than unpacking in a pass that integer instructions bound.
-
 __device__ __forceinline__ void add_bf16(float& sum, uint32_t x)
 {
     asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(sum) : "h"(static_cast<unsigned short>(x)));
@@ -148,34 +223,7 @@ __device__ __forceinline__ void add_bf16_where(float& sum, uint32_t x, uint32_t 
         : "+f"(sum) : "h"(static_cast<unsigned short>(x)), "r"(word), "r"(limit));
 }
 
-// --- a warp on a slab of 256 columns -------------------------------------------------
-//
-// Each lane holds 8 of the slab's columns: 8 in a row where the matrices allow
-// 16-byte moves (VEC), else every 32nd from its own, so that a warp's scalar
-// moves are contiguous.
-
-template <bool VEC>
-struct Slab;
-
-template <>
-struct Slab<true> {
-    int col;
-    bool on;
-    __device__ __forceinline__ Slab(int slab, int lane, int dim) : col(slab * 256 + lane * 8), on(col < dim) {}
-};
-
-template <>
-struct Slab<false> {
-    int col;
-    int count;  // columns of this lane: col, col + 32, ...
-    __device__ __forceinline__ Slab(int slab, int lane, int dim) : col(slab * 256 + lane)
-    {
-        const int left = dim - col;
-        count = left <= 0 ? 0 : (left > 224 ? 8 : (left + 31) / 32);
-    }
-};
-
-// The mask of a lane's 8 columns of a slab, row by row.
+// The mask of a lane's columns of a slab, row by row.
 template <bool VEC>
 struct SlabMask;
 
@@ -183,22 +231,23 @@ struct SlabMask;
 // the next row's: state = first + row * d.row_step + column / 4 * gamma.
 template <>
 struct SlabMask<true> {
+    struct Shared {};
     const DropArgs& d;
     uint64_t z;
-    __device__ __forceinline__ SlabMask(const DropArgs& args, int slab, int lane, int, void*)
+    __device__ __forceinline__ SlabMask(const DropArgs& args, int slab, int lane, int, Shared*)
         : d(args), z(args.first + static_cast<uint64_t>(slab * 64 + lane * 2) * kSplitMix64Step)
     {
     }
     template <typename F>
-    __device__ __forceinline__ void row(int64_t i, F&& f)
+    __device__ __forceinline__ void row(uint32_t i, F&& f)
     {
-        for_kept8(d, z + static_cast<uint32_t>(i) * d.row_step, f);
+        for_kept8(d, z + i * d.row_step, f);
     }
-    // sum += the kept elements of a group of 8 bf16
-    __device__ __forceinline__ void add(int32_t i, const uint4& raw, float (&sum)[8])
+    // sum += the kept elements
+    __device__ __forceinline__ void add(uint32_t i, const SlabGroup<__nv_bfloat16, true>& x, float (&sum)[8])
     {
-        const uint64_t at = z + static_cast<uint32_t>(i) * d.row_step;
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        const uint64_t at = z + i * d.row_step;
+        const uint32_t w[4] = {x.g.raw.x, x.g.raw.y, x.g.raw.z, x.g.raw.w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint64_t u = splitmix64_mix(at + h * kSplitMix64Step);
@@ -211,104 +260,53 @@ struct SlabMask<true> {
     }
 };
 
-// A row may begin inside an output's four elements.  The warp draws the 65
-// outputs that a slab's 256 elements can touch once, into shared memory; there
-// the elements' fields lie one after the other, 16 bits each.  Two buffers
-// take turns, so one barrier a row is enough.
+// A row may begin inside an output's four elements.  The warp draws the outputs
+// that a slab's 224 elements can touch once, into shared memory; there the
+// elements' fields lie one after the other, 16 bits each.  Two buffers take
+// turns, so one barrier a row is enough.
 template <>
 struct SlabMask<false> {
-    struct Buffer {
-        uint64_t outputs[2][66];
+    struct Shared {
+        uint64_t outputs[2][64];
     };
     const DropArgs& d;
-    Buffer* buffer;
-    int64_t dim;
-    int first_col, lane, turn;
-    __device__ __forceinline__ SlabMask(const DropArgs& args, int slab, int l, int width, void* shared)
-        : d(args), buffer(static_cast<Buffer*>(shared)), dim(width), first_col(slab * 256), lane(l), turn(0)
+    Shared* shared;
+    uint32_t dim, first_col, lane;
+    int turn;
+    __device__ __forceinline__ SlabMask(const DropArgs& args, int slab, int l, int width, Shared* buffers)
+        : d(args), shared(buffers), dim(width), first_col(slab * 224), lane(l), turn(0)
     {
     }
-    template <typename F>
-    __device__ __forceinline__ void row(int64_t i, F&& f)
+    // the lane's fields: of its column k at [32 k]
+    __device__ __forceinline__ const uint16_t* draw(uint32_t i)
     {
-        const uint64_t e = static_cast<uint64_t>(i * dim + first_col);
-        const int off = static_cast<int>(e & 3);
+        const uint64_t e = static_cast<uint64_t>(i) * dim + first_col;
         const uint64_t z = d.first + ((e >> 2) + lane) * kSplitMix64Step;
-        uint64_t* out = buffer->outputs[turn];
+        uint64_t* out = shared->outputs[turn];
+        turn ^= 1;
         out[lane] = splitmix64_mix(z);
         out[lane + 32] = splitmix64_mix(z + 32 * kSplitMix64Step);
-        if (off != 0 && lane == 0)
-            out[64] = splitmix64_mix(z + 64 * kSplitMix64Step);
         __syncwarp();
-        const uint16_t* field = reinterpret_cast<const uint16_t*>(out) + off + lane;
+        return reinterpret_cast<const uint16_t*>(out) + (static_cast<uint32_t>(e) & 3) + lane;
+    }
+    template <typename F>
+    __device__ __forceinline__ void row(uint32_t i, F&& f)
+    {
+        const uint16_t* field = draw(i);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            f(k, lower_stays(d, field[32 * k]));
-        turn ^= 1;
+        for (int k = 0; k < 7; ++k)
+            f(k, field[32 * k] > d.limit >> 16);
+    }
+    __device__ __forceinline__ void add(uint32_t i, const SlabGroup<__nv_bfloat16, false>& x, float (&sum)[7])
+    {
+        const uint16_t* field = draw(i);
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+            add_bf16_where(sum[k], __bfloat16_as_ushort(x.x[k]), field[32 * k], d.limit >> 16);
     }
 };
 
-// A lane's elements of the row that starts at element e.
-template <typename T, bool VEC>
-struct SlabGroup;
-
-template <typename T>
-struct SlabGroup<T, true> {
-    Group<T, 8> g;
-    __device__ __forceinline__ void load(const Slab<true>& c, const void* base, int64_t e)
-    {
-        if (c.on)
-            g.load(base, e + c.col);
-        else
-            g = Group<T, 8>{};
-    }
-    __device__ __forceinline__ void unpack(float (&x)[8]) const { g.unpack(x); }
-    __device__ __forceinline__ void store(const Slab<true>& c, void* base, int64_t e) const
-    {
-        if (c.on)
-            g.store(base, e + c.col);
-    }
-};
-
-template <typename T>
-struct SlabGroup<T, false> {
-    T x[8];
-    __device__ __forceinline__ void load(const Slab<false>& c, const void* base, int64_t e)
-    {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            x[k] = k < c.count ? static_cast<const T*>(base)[e + c.col + 32 * k] : T(0.0f);
-    }
-    __device__ __forceinline__ void unpack(float (&y)[8]) const
-    {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            y[k] = static_cast<float>(x[k]);
-    }
-    __device__ __forceinline__ void store(const Slab<false>& c, void* base, int64_t e) const
-    {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < c.count)
-                static_cast<T*>(base)[e + c.col + 32 * k] = x[k];
-    }
-};
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_slab(const Slab<VEC>& c, void* base, int64_t e, const float (&x)[8])
-{
-    if constexpr (VEC) {
-        if (c.on)
-            store_row<T, 8>(base, e + c.col, x);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < c.count) {
-                const float y[1] = {x[k]};
-                store_row<T, 1>(base, e + c.col + 32 * k, y);
-            }
-    }
-}
+// --- places --------------------------------------------------------------------------
 
 // a / b for a >= 0: 64-bit division takes about five times the instructions of a
 // 32-bit one, which is nearly always enough.
@@ -316,8 +314,6 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int b)
 {
     return a <= 0xffffffffll ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
-
-// --- places --------------------------------------------------------------------------
 
 __device__ __forceinline__ int64_t index_at(const void* p, int64_t i, int wide)
 {

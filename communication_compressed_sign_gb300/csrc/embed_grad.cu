@@ -21,36 +21,25 @@
 namespace lc {
 namespace {
 
-constexpr int kSumThreads = 256;
-constexpr int kWarpsPerBlock = kSumThreads / 32;
-constexpr int kFillRows = 8;           // rows of grad a fill warp looks at
-constexpr unsigned kLead = 152 * 4;    // blocks the SMs hold
+constexpr int kBlock = 256;
+constexpr int kWarps = kBlock / 32;
+constexpr int kInFlight = 4;              // rows of dout a warp loads before it adds them
+constexpr int kFillRows = 8;              // rows of grad a fill warp looks at
+constexpr int kScanRows = 64;             // rows of grad a scanning fill block takes
+constexpr int64_t kScan = 2048;           // batches up to this many places fill by scanning
+constexpr unsigned kLead = 152 * 4;       // blocks the SMs hold
 constexpr unsigned kLeadScans = 152 * 2;  // scanning fills that run beside the sort
-constexpr int kScanRows = 64;          // rows of grad a scanning fill block takes
-constexpr int64_t kScan = 2048;        // batches up to this many places fill by scanning
-constexpr unsigned kAll = 0xffffffffu;
-constexpr int kInFlight = 4;   // rows of dout a warp loads before it adds them
-
-// The warp's share of the block's shared memory for its mask.
-template <bool VEC, bool DROP>
-__device__ __forceinline__ void* warp_buffer(int warp)
-{
-    if constexpr (!VEC && DROP) {
-        __shared__ SlabMask<false>::Buffer buffers[kWarpsPerBlock];
-        return &buffers[warp];
-    }
-    return nullptr;
-}
 
 // Adds rows of dout to a running sum and writes it where the key changes.
 template <typename DT, typename GT, bool VEC, bool DROP>
 struct Walker {
+    static constexpr int N = kLaneCols<VEC>;
     const RowSumArgs& a;
     const Slab<VEC> cols;
     SlabMask<VEC> mask;
-    float sum[8];
+    float sum[N];
 
-    __device__ __forceinline__ Walker(const RowSumArgs& args, int slab, int lane, void* shared)
+    __device__ __forceinline__ Walker(const RowSumArgs& args, int slab, int lane, typename SlabMask<VEC>::Shared* shared)
         : a(args), cols(slab, lane, args.dim), mask(args.drop, slab, lane, args.dim, shared)
     {
         clear();
@@ -58,22 +47,24 @@ struct Walker {
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < N; ++k)
             sum[k] = 0.0f;
     }
-    __device__ __forceinline__ void add(const SlabGroup<DT, VEC>& x, int32_t i)
+    __device__ __forceinline__ void add(const SlabGroup<DT, VEC>& x, uint32_t i)
     {
-        if constexpr (VEC && sizeof(DT) == 2) {
-            if constexpr (DROP) {
-                mask.add(i, x.g.raw, sum);
-            } else {
-                const uint32_t w[4] = {x.g.raw.x, x.g.raw.y, x.g.raw.z, x.g.raw.w};
+        if constexpr (DROP && sizeof(DT) == 2) {
+            mask.add(i, x, sum);
+        } else if constexpr (VEC && sizeof(DT) == 2) {
+            const uint32_t w[4] = {x.g.raw.x, x.g.raw.y, x.g.raw.z, x.g.raw.w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    add_bf16(sum[k], k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xffff);
-            }
+            for (int k = 0; k < 8; ++k)
+                add_bf16(sum[k], k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xffff);
+        } else if constexpr (sizeof(DT) == 2) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                add_bf16(sum[k], __bfloat16_as_ushort(x.x[k]));
         } else {
-            float y[8];
+            float y[N];
             x.unpack(y);
             if constexpr (DROP) {
                 mask.row(i, [&](int k, bool keep) {
@@ -82,7 +73,7 @@ struct Walker {
                 });
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < N; ++k)
                     sum[k] = __fadd_rn(sum[k], y[k]);
             }
         }
@@ -93,15 +84,15 @@ struct Walker {
         if (!index_ok(a.status, v >= 0 && v < a.rows))
             return;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < N; ++k)
             sum[k] = __fmul_rn(a.factor, sum[k]);
         if (a.base.data) {
             SlabGroup<GT, VEC> b;
             b.load(cols, a.base.data, v * a.base.stride);
-            float y[8];
+            float y[N];
             b.unpack(y);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < N; ++k)
                 sum[k] = __fadd_rn(y[k], sum[k]);
         }
         store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, sum);
@@ -122,7 +113,7 @@ struct Walker {
 #pragma unroll 1
         for (int level = 0; nodes > 1; ++level) {
             const int group = node >> 3, members = min(8, nodes - group * 8), scale = 3 * level;
-            store_row<float, 8>(partial(node << scale), 0, sum);
+            store_partial(partial(node << scale));
             __threadfence();
             __syncwarp();
             int before = 0;
@@ -141,14 +132,19 @@ struct Walker {
         }
         return true;
     }
-    // A lane's 8 sums lie together in a partial row, whichever columns they are.
+    // A lane's sums lie together in a partial row, whichever columns they are.
+    __device__ __forceinline__ void store_partial(float* p) const
+    {
+        reinterpret_cast<float4*>(p)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(sum[4], sum[5], sum[6], N == 8 ? sum[N - 1] : 0.0f);
+    }
     __device__ __forceinline__ void add_partial(const float* p)
     {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(p)), y = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-        sum[0] = __fadd_rn(sum[0], x.x); sum[1] = __fadd_rn(sum[1], x.y);
-        sum[2] = __fadd_rn(sum[2], x.z); sum[3] = __fadd_rn(sum[3], x.w);
-        sum[4] = __fadd_rn(sum[4], y.x); sum[5] = __fadd_rn(sum[5], y.y);
-        sum[6] = __fadd_rn(sum[6], y.z); sum[7] = __fadd_rn(sum[7], y.w);
+        const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            sum[k] = __fadd_rn(sum[k], z[k]);
     }
 };
 
@@ -161,7 +157,7 @@ __device__ __forceinline__ void fill_slab(const RowSumArgs& a, const Slab<VEC>& 
         b.load(cols, a.base.data, v * a.base.stride);
         b.store(cols, a.grad.data, v * a.grad.stride);
     } else {
-        const float zero[8] = {};
+        const float zero[kLaneCols<VEC>] = {};
         store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, zero);
     }
 }
@@ -176,11 +172,11 @@ __device__ __forceinline__ void scan_and_fill(const RowSumArgs& a, const Places&
         has[threadIdx.x] = 0;
     __syncthreads();
     constexpr int kTokens = 8;  // loads in flight
-    for (int i0 = threadIdx.x; i0 < at.n; i0 += kTokens * kSumThreads) {
+    for (int i0 = threadIdx.x; i0 < at.n; i0 += kTokens * kBlock) {
         int64_t t[kTokens];
 #pragma unroll
         for (int u = 0; u < kTokens; ++u)
-            t[u] = i0 + u * kSumThreads < at.n ? index_at(at.tokens, i0 + u * kSumThreads, at.wide) : -1;
+            t[u] = i0 + u * kBlock < at.n ? index_at(at.tokens, i0 + u * kBlock, at.wide) : -1;
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
             const uint64_t r = static_cast<uint64_t>(t[u] - row0);
@@ -189,7 +185,7 @@ __device__ __forceinline__ void scan_and_fill(const RowSumArgs& a, const Places&
         }
     }
     __syncthreads();
-    for (int r = warp; r < kScanRows; r += kWarpsPerBlock) {
+    for (int r = warp; r < kScanRows; r += kWarps) {
         if ((has[r >> 5] >> (r & 31) & 1u) || row0 + r >= a.rows)
             continue;
         for (int slab = 0; slab < a.slabs; ++slab)
@@ -240,14 +236,15 @@ __device__ __forceinline__ int nth_bit(unsigned word, int n)
 // The rest are spread evenly: walks are bound by latency or, with dropout, by
 // integer instructions, and fills by memory, so they run side by side.
 struct Roles {
-    int scan;          // fills look through the tokens (kScanRows rows a block), else through the segments
-    unsigned scans;    // such blocks at the front
-    unsigned lead;     // running blocks at the front
-    uint64_t running;  // share of running blocks among the others, in 2^-32
-    uint64_t fill;     // share of fill blocks among walks and fills, likewise
-    __host__ __device__ __forceinline__ unsigned running_before(unsigned block) const
+    int scan;            // fills look through the tokens (kScanRows rows a block), else through the segments
+    unsigned scans;      // such blocks at the front
+    unsigned lead;       // position blocks at the front
+    uint64_t positions;  // share of position blocks among the others, in 2^-32
+    uint64_t fill;       // share of fill blocks among walks and fills, likewise
+    unsigned position_walks;  // sorted positions: walks before fills
+    __host__ __device__ __forceinline__ unsigned positions_before(unsigned block) const
     {
-        return block <= lead ? block : lead + static_cast<unsigned>(((block - lead) * running) >> 32);
+        return block <= lead ? block : lead + static_cast<unsigned>(((block - lead) * positions) >> 32);
     }
     __host__ __device__ __forceinline__ unsigned fills_before(unsigned block) const
     {
@@ -257,7 +254,7 @@ struct Roles {
 
 // One stretch of the sorted places on one slab.
 template <typename DT, typename GT, bool VEC, bool DROP>
-__device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int warp, int lane)
+__device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int lane, typename SlabMask<VEC>::Shared* shared)
 {
     const int stretch = static_cast<int>(quotient(unit, a.slabs));  // places and so stretches fit 31 bits
     const int slab = static_cast<int>(unit - static_cast<int64_t>(stretch) * a.slabs);
@@ -278,7 +275,7 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int warp
     const int32_t above = __shfl_up_sync(kAll, my_key, 1);
     const unsigned begins = __ballot_sync(kAll, lane == 0 || my_key != above);
 
-    Walker<DT, GT, VEC, DROP> w(a, slab, lane, warp_buffer<VEC, DROP>(warp));
+    Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared);
 #pragma unroll 1
     for (int part = 0; part < 3; ++part) {  // the long segment's end, short segments, a long segment's begin
         if (part == 0 ? !tail : part == 2 && !head)
@@ -319,7 +316,8 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int warp
 // Positions that run with the place, first + i % seq_len: row q's places are
 // q - first, q - first + seq_len, ... and need no sort.  One row on one slab.
 template <typename DT, typename GT, bool VEC, bool DROP>
-__device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& at, int64_t unit, int warp, int lane)
+__device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& at, int64_t unit, int lane,
+                                            typename SlabMask<VEC>::Shared* shared)
 {
     const int64_t row = quotient(unit, a.slabs);
     const int slab = static_cast<int>(unit - row * a.slabs);
@@ -331,7 +329,7 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
             fill_slab<GT, VEC>(a, Slab<VEC>(slab, lane, a.dim), row);
         return;
     }
-    Walker<DT, GT, VEC, DROP> w(a, slab, lane, warp_buffer<VEC, DROP>(warp));
+    Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared);
     for (int64_t p0 = place0; p0 < at.n; p0 += 32 * at.seq_len) {
         const int64_t mine = p0 + lane * at.seq_len;
         const unsigned there = __ballot_sync(kAll, mine < at.n && token_at(at, mine, nullptr) >= 0);
@@ -357,13 +355,14 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
     w.finish(row);
 }
 
-// a: the table whose places are sorted; p (RUNNING): running positions, whose
-// places are `at`.
-template <typename DT, typename GT, bool VEC, bool DROP, bool RUNNING>
-__global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3)
+// a: the table whose places are sorted; p: the positions' table.
+template <typename DT, typename GT, bool VEC, bool DROP, int POSITIONS>
+__global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
     k_row_sums(const __grid_constant__ RowSumArgs a, const __grid_constant__ RowSumArgs p, const Places at, const Roles roles)
 {
+    __shared__ typename SlabMask<VEC>::Shared buffers[DROP ? kWarps : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    typename SlabMask<VEC>::Shared* shared = &buffers[DROP ? warp : 0];
     unsigned block = blockIdx.x;
     if (block < roles.scans) {
         scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(block) * kScanRows, warp, lane);
@@ -371,11 +370,19 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3)
         return;
     }
     block -= roles.scans;
-    if constexpr (RUNNING) {
-        const unsigned before = roles.running_before(block);
-        if (roles.running_before(block + 1) != before) {
-            running_row<DT, GT, VEC, DROP>(p, at, static_cast<int64_t>(before) * kWarpsPerBlock + warp, warp, lane);
+    if constexpr (POSITIONS != kNoPositions) {
+        const unsigned before = roles.positions_before(block);
+        if (roles.positions_before(block + 1) != before) {
+            const int64_t unit = static_cast<int64_t>(before) * kWarps + warp;
+            if constexpr (POSITIONS == kRunningPositions)
+                running_row<DT, GT, VEC, DROP>(p, at, unit, lane, shared);
             wait_for_launch_before();
+            if constexpr (POSITIONS == kSortedPositions) {
+                if (before < roles.position_walks)
+                    walk<DT, GT, VEC, DROP>(p, unit, lane, shared);
+                else
+                    fill_rows<GT, VEC>(p, (unit - static_cast<int64_t>(roles.position_walks) * kWarps) * kFillRows, lane);
+            }
             return;
         }
         block -= before;
@@ -386,77 +393,90 @@ __global__ void __launch_bounds__(kSumThreads, VEC ? 4 : 3)
         scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(roles.scans + fills) * kScanRows, warp, lane);
     wait_for_launch_before();
     if (fill && !roles.scan)
-        fill_rows<GT, VEC>(a, (static_cast<int64_t>(fills) * kWarpsPerBlock + warp) * kFillRows, lane);
+        fill_rows<GT, VEC>(a, (static_cast<int64_t>(fills) * kWarps + warp) * kFillRows, lane);
     else if (!fill)
-        walk<DT, GT, VEC, DROP>(a, static_cast<int64_t>(block - fills) * kWarpsPerBlock + warp, warp, lane);
+        walk<DT, GT, VEC, DROP>(a, static_cast<int64_t>(block - fills) * kWarps + warp, lane, shared);
 }
 
-unsigned blocks_for(int64_t warps) { return static_cast<unsigned>((warps + kWarpsPerBlock - 1) / kWarpsPerBlock); }
+unsigned blocks_for(int64_t warps) { return static_cast<unsigned>((warps + kWarps - 1) / kWarps); }
 
 // The share of `part` among `all`, in 2^-32, rounded up: exactly part of them.
 uint64_t share_of(unsigned part, unsigned all) { return all ? ((static_cast<uint64_t>(part) << 32) + all - 1) / all : 0; }
 
-template <typename DT, typename GT, bool VEC, bool DROP, bool RUNNING>
-cudaError_t launch_r(const RowSumArgs& a, const RowSumArgs& p, const Places& at, cudaStream_t s)
+unsigned walk_blocks(const RowSumArgs& a) { return blocks_for(grad_stretches(a.n, a.piece) * a.slabs); }
+unsigned fill_blocks(const RowSumArgs& a)
 {
-    const bool in_place = a.base.data == a.grad.data;
-    const unsigned walks = blocks_for(grad_stretches(a.n, a.piece) * a.slabs);
-    const bool scan = !in_place && a.scan && a.n <= kScan;
-    const unsigned all_fills = in_place ? 0
-                               : scan   ? static_cast<unsigned>((a.rows + kScanRows - 1) / kScanRows)
-                                        : blocks_for((a.rows + kFillRows - 1) / kFillRows);
-    const unsigned scans = scan ? (all_fills < kLeadScans ? all_fills : kLeadScans) : 0, fills = all_fills - scans;
-    const unsigned running = RUNNING ? blocks_for(static_cast<int64_t>(p.rows) * p.slabs) : 0;
-    const unsigned blocks = walks + fills + running;
-    if (scans + blocks == 0)
+    return a.base.data == a.grad.data ? 0 : blocks_for((a.rows + kFillRows - 1) / kFillRows);  // none in place
+}
+
+template <typename DT, typename GT, bool VEC, bool DROP, int POSITIONS>
+cudaError_t launch_p(const RowSumArgs& a, const RowSumArgs& p, const Places& at, cudaStream_t s)
+{
+    Roles roles = {};
+    const unsigned walks = walk_blocks(a);
+    unsigned fills = fill_blocks(a), positions = 0;
+    if (fills > 0 && a.scan && a.n <= kScan) {
+        const unsigned scans = static_cast<unsigned>((a.rows + kScanRows - 1) / kScanRows);
+        roles.scan = 1;
+        roles.scans = scans < kLeadScans ? scans : kLeadScans;
+        fills = scans - roles.scans;
+    }
+    if (POSITIONS == kRunningPositions) {
+        positions = blocks_for(static_cast<int64_t>(p.rows) * p.slabs);
+        roles.lead = roles.scan ? 0 : positions < kLead ? positions : kLead;
+    } else if (POSITIONS == kSortedPositions) {
+        roles.position_walks = walk_blocks(p);
+        positions = roles.position_walks + fill_blocks(p);
+    }
+    const unsigned blocks = walks + fills + positions;
+    if (roles.scans + blocks == 0)
         return cudaSuccess;
-    Roles roles;
-    roles.scan = scan;
-    roles.scans = scans;
-    roles.lead = scan ? 0 : running < kLead ? running : kLead;
-    roles.running = share_of(running - roles.lead, blocks - roles.lead);
+    roles.positions = share_of(positions - roles.lead, blocks - roles.lead);
     roles.fill = share_of(fills, walks + fills);
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(scans + blocks);
-    c.blockDim = dim3(kSumThreads);
+    c.gridDim = dim3(roles.scans + blocks);
+    c.blockDim = dim3(kBlock);
     c.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     c.attrs = attr;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, k_row_sums<DT, GT, VEC, DROP, RUNNING>, a, p, at, roles);
+    return cudaLaunchKernelEx(&c, k_row_sums<DT, GT, VEC, DROP, POSITIONS>, a, p, at, roles);
 }
 
 template <typename DT, typename GT, bool VEC, bool DROP>
-cudaError_t launch_k(const RowSumArgs& a, const RowSumArgs* p, const Places& at, cudaStream_t s)
+cudaError_t launch_k(RowSumArgs a, RowSumArgs p, PositionKind kind, const Places& at, cudaStream_t s)
 {
-    return p ? launch_r<DT, GT, VEC, DROP, true>(a, *p, at, s) : launch_r<DT, GT, VEC, DROP, false>(a, a, at, s);
+    a.slabs = p.slabs = slabs_of(a.dim, VEC);
+    a.piece = p.piece = grad_piece(a.n, a.slabs);
+    if (kind == kRunningPositions)
+        return launch_p<DT, GT, VEC, DROP, kRunningPositions>(a, p, at, s);
+    if (kind == kSortedPositions)
+        return launch_p<DT, GT, VEC, DROP, kSortedPositions>(a, p, at, s);
+    return launch_p<DT, GT, VEC, DROP, kNoPositions>(a, p, at, s);
 }
 
 template <typename DT, typename GT>
-cudaError_t launch_t(const RowSumArgs& a, const RowSumArgs* p, const Places& at, bool vec, bool drop, cudaStream_t s)
+cudaError_t launch_t(const RowSumArgs& a, const RowSumArgs& p, PositionKind kind, const Places& at, bool vec, bool drop,
+                     cudaStream_t s)
 {
     if (vec)
-        return drop ? launch_k<DT, GT, true, true>(a, p, at, s) : launch_k<DT, GT, true, false>(a, p, at, s);
-    return drop ? launch_k<DT, GT, false, true>(a, p, at, s) : launch_k<DT, GT, false, false>(a, p, at, s);
+        return drop ? launch_k<DT, GT, true, true>(a, p, kind, at, s) : launch_k<DT, GT, true, false>(a, p, kind, at, s);
+    return drop ? launch_k<DT, GT, false, true>(a, p, kind, at, s) : launch_k<DT, GT, false, false>(a, p, kind, at, s);
 }
 
 }  // namespace
 
-cudaError_t launch_row_sums(RowSumArgs a, const RowSumArgs* running, const Places& at, int dout_type, int grad_type, bool vec,
-                            bool drop, cudaStream_t s)
+cudaError_t launch_row_sums(RowSumArgs a, const RowSumArgs* positions, PositionKind kind, const Places& at, int dout_type,
+                            int grad_type, bool vec, bool drop, cudaStream_t s)
 {
-    a.slabs = grad_slabs(a.dim);
-    a.piece = grad_piece(a.n, a.slabs);
-    RowSumArgs p = running ? *running : a;
-    p.slabs = a.slabs;
-    const RowSumArgs* q = running ? &p : nullptr;
+    const RowSumArgs& p = positions ? *positions : a;
     if (dout_type == LIONCUB_ROWS_BF16)
-        return grad_type == LIONCUB_ROWS_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, q, at, vec, drop, s)
-                                              : launch_t<__nv_bfloat16, float>(a, q, at, vec, drop, s);
-    return grad_type == LIONCUB_ROWS_BF16 ? launch_t<float, __nv_bfloat16>(a, q, at, vec, drop, s)
-                                          : launch_t<float, float>(a, q, at, vec, drop, s);
+        return grad_type == LIONCUB_ROWS_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, p, kind, at, vec, drop, s)
+                                              : launch_t<__nv_bfloat16, float>(a, p, kind, at, vec, drop, s);
+    return grad_type == LIONCUB_ROWS_BF16 ? launch_t<float, __nv_bfloat16>(a, p, kind, at, vec, drop, s)
+                                          : launch_t<float, float>(a, p, kind, at, vec, drop, s);
 }
 
 }  // namespace lc

@@ -1,29 +1,51 @@
 // embed_lookup.cu -- embedding lookup with scaling, position rows and dropout:
 //   out[i,j] = keep(i*D+j) ? RN(r * RN(RN(scale * table[t_i,j]) + pos_table[q_i,j])) : 0.
 //
-// Memory-bound: a table row is read and an output row written once per place
-// (repeated tokens hit L2), the mask costs integer instructions only.  One
-// thread takes one group of 8 columns (one column where the width or the
-// alignment does not allow 16-byte moves) of one place; see row_grid for how
-// threads map to rows.
-#include <type_traits>
-
+// A table row is read and an output row written once for each place (repeated
+// tokens hit L2).  One warp takes several places on a slab of columns, so that
+// their rows are in flight together and the index arithmetic is shared.  Wide
+// rows with dropout are bound by instructions about as much as by memory, so
+// sums and rescalings are done two at a time (fp32 pairs).
 #include "embed_device.cuh"
 
 namespace lc {
 namespace {
 
-constexpr int kThreads1 = 256;
-constexpr int kWarps = kThreads1 / 32;
-constexpr unsigned kAll = 0xffffffffu;
+constexpr int kBlock = 256;
+constexpr int kWarps = kBlock / 32;
+
+// y += q and y *= r, in pairs.  Pairs are used for a sum whose result is
+// rescaled, never for a product that is then summed: the assembler fuses a
+// paired product and sum, whatever their rounding modifiers.
+template <int N>
+__device__ __forceinline__ void add_pairs(float (&y)[N], const float (&q)[N])
+{
+#pragma unroll
+    for (int k = 0; k + 1 < N; k += 2)
+        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+            : "+f"(y[k]), "+f"(y[k + 1]) : "f"(q[k]), "f"(q[k + 1]));
+    if constexpr (N % 2)
+        y[N - 1] = __fadd_rn(y[N - 1], q[N - 1]);
+}
+template <int N>
+__device__ __forceinline__ void scale_pairs(float (&y)[N], float r)
+{
+#pragma unroll
+    for (int k = 0; k + 1 < N; k += 2)
+        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+            : "+f"(y[k]), "+f"(y[k + 1]) : "f"(r));
+    if constexpr (N % 2)
+        y[N - 1] = __fmul_rn(y[N - 1], r);
+}
 
 // One warp: PLACES places on a slab of columns.  With running positions they
 // are the same place of that many sequences, so its position row is read once;
 // otherwise neighbours.
 template <typename TT, typename OT, bool VEC, bool DROP, int PLACES, bool RUNNING>
-__global__ void __launch_bounds__(kThreads1) k_lookup(const LookupArgs a)
+__global__ void __launch_bounds__(kBlock) k_lookup(const LookupArgs a)
 {
-    __shared__ typename std::conditional<!VEC && DROP, SlabMask<false>::Buffer, char>::type buffers[kWarps];
+    constexpr int N = kLaneCols<VEC>;
+    __shared__ typename SlabMask<VEC>::Shared shared[DROP ? kWarps : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     const int64_t group = quotient(unit, a.slabs);
@@ -47,45 +69,50 @@ __global__ void __launch_bounds__(kThreads1) k_lookup(const LookupArgs a)
             my_position = RUNNING ? static_cast<int>(a.at.first + in_sequence) : position_at(a.at, place0 + lane * step, a.status);
     }
     const Slab<VEC> cols(slab, lane, a.dim);
-    SlabMask<VEC> mask(a.drop, slab, lane, a.dim, &buffers[warp]);
+    SlabMask<VEC> mask(a.drop, slab, lane, a.dim, &shared[DROP ? warp : 0]);
     SlabGroup<TT, VEC> x[PLACES], p[RUNNING ? 1 : PLACES];
     int token[PLACES], position[PLACES];
 #pragma unroll
     for (int u = 0; u < PLACES; ++u) {
         token[u] = __shfl_sync(kAll, my_token, u);
-        x[u].load(cols, a.table.data, max(token[u], 0) * a.table.stride);
+        x[u].load(cols, a.table.data, static_cast<uint32_t>(max(token[u], 0)) * a.table.stride);
     }
     if (a.pos_table.data) {
 #pragma unroll
         for (int u = 0; u < PLACES; ++u) {
             position[u] = __shfl_sync(kAll, my_position, u);
             if (u == 0 || !RUNNING)
-                p[u].load(cols, a.pos_table.data, max(position[u], 0) * a.pos_table.stride);
+                p[u].load(cols, a.pos_table.data, static_cast<uint32_t>(max(position[u], 0)) * a.pos_table.stride);
         }
     }
 #pragma unroll
     for (int u = 0; u < PLACES; ++u) {
-        const int64_t i = place0 + u * step;
-        if (i >= a.at.n)
+        const int64_t place = place0 + u * step;
+        if (place >= a.at.n)
             break;
-        float y[8];
-        x[u].unpack(y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            y[k] = __fmul_rn(a.scale, y[k]);
-        if (a.pos_table.data && position[u] >= 0) {
-            float q[8];
-            p[RUNNING ? 0 : u].unpack(q);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                y[k] = __fadd_rn(y[k], q[k]);
-        }
-        if constexpr (DROP)
-            mask.row(i, [&](int k, bool keep) { y[k] = keep ? __fmul_rn(a.drop.rescale, y[k]) : 0.0f; });
+        const uint32_t i = static_cast<uint32_t>(place);
+        float y[N];
         if (token[u] < 0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < N; ++k)
                 y[k] = 0.0f;
+            store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, y);
+            continue;
+        }
+        x[u].unpack(y);
+        if (a.scale != 1.0f) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                y[k] = __fmul_rn(a.scale, y[k]);
+        }
+        if (a.pos_table.data && position[u] >= 0) {
+            float q[N];
+            p[RUNNING ? 0 : u].unpack(q);
+            add_pairs(y, q);
+        }
+        if constexpr (DROP) {
+            scale_pairs(y, a.drop.rescale);
+            mask.row(i, [&](int k, bool keep) { y[k] = keep ? y[k] : 0.0f; });
         }
         store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, y);
     }
@@ -97,8 +124,10 @@ constexpr int kPlaces = 4;
 constexpr int64_t kFewWarps = 152 * kWarps;
 
 template <typename TT, typename OT, bool VEC, bool DROP>
-cudaError_t launch_k(const LookupArgs& a, cudaStream_t s)
+cudaError_t launch_k(LookupArgs a, cudaStream_t s)
 {
+    a.slabs = slabs_of(a.dim, VEC);
+    a.span = a.at.seq_len < a.at.n ? a.at.seq_len : a.at.n;
     const bool few = a.at.n * static_cast<int64_t>(a.slabs) <= kFewWarps;
     const bool running = a.pos_table.data && !a.at.positions && !few;
     const int64_t places = few ? 1 : kPlaces;
@@ -109,19 +138,17 @@ cudaError_t launch_k(const LookupArgs& a, cudaStream_t s)
     }
     const unsigned blocks = static_cast<unsigned>((groups * a.slabs + kWarps - 1) / kWarps);
     if (few)
-        k_lookup<TT, OT, VEC, DROP, 1, false><<<blocks, kThreads1, 0, s>>>(a);
+        k_lookup<TT, OT, VEC, DROP, 1, false><<<blocks, kBlock, 0, s>>>(a);
     else if (running)
-        k_lookup<TT, OT, VEC, DROP, kPlaces, true><<<blocks, kThreads1, 0, s>>>(a);
+        k_lookup<TT, OT, VEC, DROP, kPlaces, true><<<blocks, kBlock, 0, s>>>(a);
     else
-        k_lookup<TT, OT, VEC, DROP, kPlaces, false><<<blocks, kThreads1, 0, s>>>(a);
+        k_lookup<TT, OT, VEC, DROP, kPlaces, false><<<blocks, kBlock, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename TT, typename OT>
-cudaError_t launch_t(LookupArgs a, bool vec, bool drop, cudaStream_t s)
+cudaError_t launch_t(const LookupArgs& a, bool vec, bool drop, cudaStream_t s)
 {
-    a.slabs = (a.dim + 255) / 256;
-    a.span = a.at.seq_len < a.at.n ? a.at.seq_len : a.at.n;
     if (vec)
         return drop ? launch_k<TT, OT, true, true>(a, s) : launch_k<TT, OT, true, false>(a, s);
     return drop ? launch_k<TT, OT, false, true>(a, s) : launch_k<TT, OT, false, false>(a, s);

@@ -28,7 +28,6 @@ constexpr int64_t kSmallBatch = 8192;
 constexpr int kMaxOwned = 1024;    // keys of a block
 constexpr int kBatch = 8;          // groups of 32 keys a warp loads at once
 constexpr int kList = 256;         // a warp's list; a slice with more is read again
-constexpr unsigned kAll = 0xffffffffu;
 
 // The key of a place from its token (and position, where that is the key), or
 // -1.  IT: the type of ids and positions.
@@ -256,7 +255,9 @@ cudaError_t launch_sort(SortArgs a, cudaStream_t s)
     int width = 1, sorters = 0;
     for (int k = 0; k < a.tasks; ++k) {
         SortTask& t = a.task[k];
-        t.log_blocks = t.keys >= 128 ? 7 : 0;
+        // one wave of blocks, each with a key at least
+        while (t.log_blocks < (a.tasks > 1 ? 6 : 7) && t.keys >> (t.log_blocks + 1) > 0)
+            ++t.log_blocks;
         while ((static_cast<int64_t>(kMaxOwned) << t.log_blocks) < t.keys)
             ++t.log_blocks;
         const int w = (t.keys + (1 << t.log_blocks) - 1) >> t.log_blocks;
