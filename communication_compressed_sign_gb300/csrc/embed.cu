@@ -34,9 +34,9 @@ struct lioncub_embed_s {
     int nallocs = 0;
     lc::GuardList guards{};
     int* status = nullptr;       // kWords words, the first the status word
-    int32_t* order = nullptr;    // for each table: max_tokens places, grouped by key, and their keys
+    int4* order = nullptr;       // for each table: max_tokens entries of the sort
     int2* segment = nullptr;     // vocab + positions ranges of order
-    int32_t* arrived = nullptr;  // arrival counters of the row sums, for each table
+    uint64_t* arrived = nullptr; // arrival counters of the row sums, for each table
     float* partial = nullptr;    // partial_rows x partial_stride sums of pieces, for each table
     int64_t arrived_count = 0, partial_rows = 0, partial_stride = 0;
 
@@ -255,8 +255,7 @@ lc::SortTask sort_task(lioncub_embed_t h, const lc::Places& at, const TableGradi
     t.kind = which;
     t.keys = static_cast<int32_t>(g.rows);
     t.capacity = static_cast<int32_t>(h->max_tokens);
-    t.order = h->order + 2 * which * h->max_tokens;
-    t.sorted_key = t.order + h->max_tokens;
+    t.order = h->order + which * h->max_tokens;
     t.segment = h->segment + which * h->vocab;
     t.total = h->status + 1 + which;
     return t;
@@ -271,7 +270,6 @@ lc::RowSumArgs row_sum_args(lioncub_embed_t h, const lc::Places& at, const Table
     a.base = rows_of(g.base);
     a.grad = rows_of(g.grad);
     a.order = t.order;
-    a.sorted_key = t.sorted_key;
     a.segment = t.segment;
     a.total = t.total;
     a.partial = h->partial + g.kind * h->partial_rows * h->partial_stride;
@@ -393,7 +391,7 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     if (e == cudaSuccess)
         e = cudaMemset(h->status, 0, kWords * sizeof(int));
     if (e == cudaSuccess)
-        e = guarded_alloc(h, &h->order, tables * 2 * max_tokens);
+        e = guarded_alloc(h, &h->order, tables * max_tokens);
     if (e == cudaSuccess)
         e = guarded_alloc(h, &h->segment, vocab + positions);
     if (e == cudaSuccess)

@@ -51,8 +51,8 @@ struct LookupArgs {
     DropArgs drop;
     float scale;
     int32_t dim;
-    int32_t slabs;  // set by launch_lookup
-    int64_t span;   // places of a sequence; likewise
+    int32_t slabs, span;  // set by launch_lookup; span: places of a sequence
+    uint32_t rounds;      // likewise
     int* status;
 };
 
@@ -79,17 +79,17 @@ inline int64_t grad_max_stretches(int64_t n, int64_t slabs)
     return most < grad_stretches(n, kMinPiece) ? most : grad_stretches(n, kMinPiece);
 }
 
-// The sort of a batch's places by key: order holds the places grouped by key,
-// ascending within a key, sorted_key their keys; segment[key] is the key's
-// range in order, total the number of places that have a key.
+// The sort of a batch's places by key.  order has an entry for each place that
+// has a key, grouped by key and ascending within one: (place, key, begin and end
+// of the key's entries), so that what a walk needs comes with one load.
+// segment[key] holds begin and end too, for every key; total counts the entries.
 struct SortTask {
     Places at;
     int32_t kind;      // KeyKind
     int32_t keys;      // key values: [0, keys)
     int32_t capacity;  // entries of order (checked builds)
     int32_t log_blocks;  // set by launch_sort
-    int32_t* order;
-    int32_t* sorted_key;
+    int4* order;
     int2* segment;
     int32_t* total;
 };
@@ -97,7 +97,7 @@ struct SortTask {
 struct SortArgs {
     SortTask task[2];
     int32_t tasks;
-    int32_t* arrived[2];  // the row sums' counters, zeroed here
+    uint64_t* arrived[2];  // the row sums' counters, zeroed here
     int64_t arrived_count;
     int* status;
 };
@@ -105,14 +105,13 @@ struct SortArgs {
 // Row sums of dout over the segments.
 struct RowSumArgs {
     Rows dout, base, grad;  // base.data null: zeros
-    const int32_t* order;
-    const int32_t* sorted_key;
+    const int4* order;
     const int2* segment;
     const int32_t* total;
     float* partial;          // two fp32 rows for each stretch
     int64_t partial_stride;  // 256 for each slab
     int64_t partial_rows;
-    int32_t* arrived;        // arrivals, for each (row of partial, slab)
+    uint64_t* arrived;       // arrivals, for each (row of partial, slab)
     DropArgs drop;
     float factor;
     int32_t rows;  // rows of grad

@@ -83,6 +83,8 @@ struct Group8<float> {
 
 template <bool VEC>
 constexpr int kLaneCols = VEC ? 8 : 7;
+template <bool VEC>
+constexpr int kSlabCols = 32 * kLaneCols<VEC>;
 
 template <bool VEC>
 struct Slab;

@@ -16,6 +16,8 @@
 //          however skewed the tokens are.
 //   fill   rows without a place.
 // Bound by memory: dout is read once and grad written once.
+#include <type_traits>
+
 #include "embed_device.cuh"
 
 namespace lc {
@@ -23,12 +25,15 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
+constexpr int kJoinLog = 4, kJoin = 1 << kJoinLog;  // pieces of a group, and counter bits for a level of groups:
+constexpr int kJoinBits = kJoinLog + 1;             // 64 / kJoinBits levels are more than 2^30 places can need
 constexpr int kInFlight = 4;              // rows of dout a warp loads before it adds them
 constexpr int kFillRows = 8;              // rows of grad a fill warp looks at
-constexpr int kScanRows = 64;             // rows of grad a scanning fill block takes
-constexpr int64_t kScan = 2048;           // batches up to this many places fill by scanning
 constexpr unsigned kLead = 152 * 4;       // blocks the SMs hold
-constexpr unsigned kLeadScans = 152 * 2;  // scanning fills that run beside the sort
+constexpr unsigned kWalkLead = 152 * XWL;   // walks that start first: they take longest
+constexpr unsigned kScans = 152 * 2;      // scanning fill blocks, which leave room for walks
+constexpr int kMaxScanRows = 4096;        // rows such a block takes at most
+constexpr int64_t kScan = 0;          // batches up to this many places fill by scanning
 
 // Adds rows of dout to a running sum and writes it where the key changes.
 template <typename DT, typename GT, bool VEC, bool DROP>
@@ -97,13 +102,14 @@ struct Walker {
         }
         store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, sum);
     }
-    // Adds up the pieces of a long segment: a tree of groups of 8, in which the
-    // last of a group to arrive adds the group's partials in order and goes on
-    // as one piece of the next level.  True where the whole sum has come together.
-    __device__ __forceinline__ bool gather(int2 seg, int stretch, int slab, int lane)
+    // Adds up the pieces of a long segment: a tree of groups of kJoin, in which
+    // the last of a group to arrive adds the group's partials in order and goes
+    // on as one piece of the next level.  True where the whole sum has come
+    // together.
+    __device__ __forceinline__ bool gather(int begin, int end, int stretch, int slab, int lane)
     {
-        const int first = seg.x / a.piece;
-        int node = stretch - first, nodes = (seg.y - 1) / a.piece - first + 1;
+        const int first = begin / a.piece;
+        int node = stretch - first, nodes = (end - 1) / a.piece - first + 1;
         const int64_t column = slab * 256 + lane * 8;  // partial rows are whole slabs
         // piece r's partial and counter: slot 1 of the stretch the segment begins in, slot 0 of the later ones
         auto slot = [&](int r) { return 2 * static_cast<int64_t>(first + r) + (r == 0 ? 1 : 0); };
@@ -112,25 +118,32 @@ struct Walker {
             return false;
 #pragma unroll 1
         for (int level = 0; nodes > 1; ++level) {
-            const int group = node >> 3, members = min(8, nodes - group * 8), scale = 3 * level;
+            const int group = node / kJoin, members = min(kJoin, nodes - group * kJoin), scale = kJoinLog * level;
             store_partial(partial(node << scale));
-            __threadfence();
             __syncwarp();
-            int before = 0;
-            if (lane == 0)  // four bits a level
-                before = atomicAdd(&a.arrived[slot(group << scale << 3) * a.slabs + slab], 1 << (4 * level));
+            uint64_t before = 0;
+            if (lane == 0)
+                before = arrive(&a.arrived[slot(group << scale << kJoinLog) * a.slabs + slab], 1ull << (kJoinBits * level));
             before = __shfl_sync(kAll, before, 0);
-            if ((before >> (4 * level) & 15) != members - 1)
+            if ((before >> (kJoinBits * level) & ((1u << kJoinBits) - 1)) != members - 1)
                 return false;
-            __threadfence();
             clear();
 #pragma unroll 4
             for (int m = 0; m < members; ++m)
-                add_partial(partial((group * 8 + m) << scale));
+                add_partial(partial((group * kJoin + m) << scale));
             node = group;
-            nodes = (nodes + 7) / 8;
+            nodes = (nodes + kJoin - 1) / kJoin;
         }
         return true;
+    }
+    // Counts an arrival: what the warp wrote before is visible to whom the
+    // counter tells of it (release, cumulative over the warp's barrier), and
+    // what it tells of is visible here (acquire).
+    static __device__ __forceinline__ uint64_t arrive(uint64_t* counter, uint64_t one)
+    {
+        uint64_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(before) : "l"(counter), "l"(one) : "memory");
+        return before;
     }
     // A lane's sums lie together in a partial row, whichever columns they are.
     __device__ __forceinline__ void store_partial(float* p) const
@@ -148,28 +161,36 @@ struct Walker {
     }
 };
 
-// Row v on one slab: zeros, or base.
+// Row v, columns [begin, end): zeros, or base.  (16 bytes or one element a lane
+// and step: a tight loop, since a fill should be bound by its stores.)
 template <typename GT, bool VEC>
-__device__ __forceinline__ void fill_slab(const RowSumArgs& a, const Slab<VEC>& cols, int64_t v)
+__device__ __forceinline__ void fill_row(const RowSumArgs& a, int64_t v, int begin, int end, int lane)
 {
+    constexpr int kPer = VEC ? 16 / sizeof(GT) : 1;
+    using Unit = typename std::conditional<VEC, uint4, GT>::type;
+    Unit* dst = reinterpret_cast<Unit*>(static_cast<GT*>(a.grad.data) + v * a.grad.stride);
+    const int last = end / kPer;
     if (a.base.data) {
-        SlabGroup<GT, VEC> b;
-        b.load(cols, a.base.data, v * a.base.stride);
-        b.store(cols, a.grad.data, v * a.grad.stride);
+        const Unit* src = reinterpret_cast<const Unit*>(static_cast<const GT*>(a.base.data) + v * a.base.stride);
+#pragma unroll 4
+        for (int k = begin / kPer + lane; k < last; k += 32)
+            dst[k] = src[k];
     } else {
-        const float zero[kLaneCols<VEC>] = {};
-        store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, zero);
+        const Unit zero{};
+#pragma unroll 4
+        for (int k = begin / kPer + lane; k < last; k += 32)
+            dst[k] = zero;
     }
 }
 
-// Those of rows [row0, row0 + kScanRows) that no token of the batch has, found
+// Those of rows [row0, row0 + count) that no token of the batch has, found
 // without the sort: the block looks through all tokens.
 template <typename GT, bool VEC>
-__device__ __forceinline__ void scan_and_fill(const RowSumArgs& a, const Places& at, int64_t row0, int warp, int lane)
+__device__ __forceinline__ void scan_and_fill(const RowSumArgs& a, const Places& at, int64_t row0, int count, int warp, int lane)
 {
-    __shared__ unsigned has[kScanRows / 32];
-    if (threadIdx.x < kScanRows / 32)
-        has[threadIdx.x] = 0;
+    __shared__ unsigned has[kMaxScanRows / 32];
+    for (int k = threadIdx.x; k < kMaxScanRows / 32; k += kBlock)
+        has[k] = 0;
     __syncthreads();
     constexpr int kTokens = 8;  // loads in flight
     for (int i0 = threadIdx.x; i0 < at.n; i0 += kTokens * kBlock) {
@@ -180,16 +201,15 @@ __device__ __forceinline__ void scan_and_fill(const RowSumArgs& a, const Places&
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
             const uint64_t r = static_cast<uint64_t>(t[u] - row0);
-            if (t[u] >= 0 && r < kScanRows)
+            if (t[u] >= 0 && r < count)
                 atomicOr(&has[r >> 5], 1u << (r & 31));
         }
     }
     __syncthreads();
-    for (int r = warp; r < kScanRows; r += kWarps) {
+    for (int r = warp; r < count; r += kWarps) {
         if ((has[r >> 5] >> (r & 31) & 1u) || row0 + r >= a.rows)
             continue;
-        for (int slab = 0; slab < a.slabs; ++slab)
-            fill_slab<GT, VEC>(a, Slab<VEC>(slab, lane, a.dim), row0 + r);
+        fill_row<GT, VEC>(a, row0 + r, 0, a.dim, lane);
     }
 }
 
@@ -206,8 +226,7 @@ __device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int
     while (todo) {
         const int64_t v = row0 + __ffs(todo) - 1;
         todo &= todo - 1;
-        for (int slab = 0; slab < a.slabs; ++slab)
-            fill_slab<GT, VEC>(a, Slab<VEC>(slab, lane, a.dim), v);
+        fill_row<GT, VEC>(a, v, 0, a.dim, lane);
     }
 }
 
@@ -232,15 +251,17 @@ __device__ __forceinline__ int nth_bit(unsigned word, int n)
 }
 
 // What the blocks of a launch do.  Blocks that need no sort lead, while it may
-// still run: fills that scan the tokens (small batches), else running positions.
-// The rest are spread evenly: walks are bound by latency or, with dropout, by
-// integer instructions, and fills by memory, so they run side by side.
+// still run: fills that scan the tokens (all of them, in small batches), else
+// running positions.  The rest are spread evenly: walks are bound by latency
+// or, with dropout, by integer instructions, and fills by memory, so they run
+// side by side.
 struct Roles {
-    int scan;            // fills look through the tokens (kScanRows rows a block), else through the segments
-    unsigned scans;      // such blocks at the front
+    unsigned scans;      // scanning fill blocks, the first
+    int scan_rows;       // rows of each
     unsigned lead;       // position blocks at the front
     uint64_t positions;  // share of position blocks among the others, in 2^-32
     uint64_t fill;       // share of fill blocks among walks and fills, likewise
+    unsigned walk_lead;       // walk blocks in front of the mix of walks and fills
     unsigned position_walks;  // sorted positions: walks before fills
     __host__ __device__ __forceinline__ unsigned positions_before(unsigned block) const
     {
@@ -248,7 +269,7 @@ struct Roles {
     }
     __host__ __device__ __forceinline__ unsigned fills_before(unsigned block) const
     {
-        return static_cast<unsigned>((block * fill) >> 32);
+        return block <= walk_lead ? 0 : static_cast<unsigned>(((block - walk_lead) * fill) >> 32);
     }
 };
 
@@ -258,42 +279,48 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int lane
 {
     const int stretch = static_cast<int>(quotient(unit, a.slabs));  // places and so stretches fit 31 bits
     const int slab = static_cast<int>(unit - static_cast<int64_t>(stretch) * a.slabs);
-    const int total = *a.total;
-    if (static_cast<int64_t>(stretch) * a.piece >= total)
+    const int64_t begin64 = static_cast<int64_t>(stretch) * a.piece;
+    if (begin64 >= a.n)
         return;
-    const int begin = stretch * a.piece, end = min(begin + a.piece, total);
-    // the stretch, and what a short segment can reach beyond it
+    const int begin = static_cast<int>(begin64);
+    // the stretch's entries and what a short segment can reach beyond it, not waiting for how many are set
     const int mine = begin + lane;
-    const int32_t my_place = mine < total ? a.order[mine] : 0, my_key = mine < total ? a.sorted_key[mine] : 0;
-    if (!__all_sync(kAll, index_ok(a.status, my_place >= 0 && my_place < a.n && my_key >= 0 && my_key < a.rows)))
+    const int4 entry = mine < a.n ? a.order[mine] : make_int4(0, 0, 0, 0);
+    const int total = *a.total;
+    if (begin >= total)
         return;
-    const int2 seg0 = a.segment[__shfl_sync(kAll, my_key, 0)], seg1 = a.segment[__shfl_sync(kAll, my_key, end - 1 - begin)];
-    const bool tail = seg0.x < begin && seg0.y - seg0.x > a.piece;   // a long segment goes on here
-    const bool head = seg1.x >= begin && seg1.y - seg1.x > a.piece;  // a long segment begins here
+    const int end = min(begin + a.piece, total);
+    if (!__all_sync(kAll, index_ok(a.status, mine >= total || (entry.x >= 0 && entry.x < a.n && entry.y >= 0 && entry.y < a.rows))))
+        return;
+    const int last = end - 1 - begin;
+    const int begin0 = __shfl_sync(kAll, entry.z, 0), end0 = __shfl_sync(kAll, entry.w, 0);
+    const int begin1 = __shfl_sync(kAll, entry.z, last), end1 = __shfl_sync(kAll, entry.w, last);
+    const bool tail = begin0 < begin && end0 - begin0 > a.piece;   // a long segment goes on here
+    const bool head = begin1 >= begin && end1 - begin1 > a.piece;  // a long segment begins here
     // short segments: one that began before belongs there, one that begins here is taken to its end
-    const int from = seg0.x < begin ? seg0.y : begin, to = head ? seg1.x : (seg1.x < begin ? begin : seg1.y);
-    const int32_t above = __shfl_up_sync(kAll, my_key, 1);
-    const unsigned begins = __ballot_sync(kAll, lane == 0 || my_key != above);
+    const int from = begin0 < begin ? end0 : begin, to = head ? begin1 : (begin1 < begin ? begin : end1);
+    const int32_t above = __shfl_up_sync(kAll, entry.y, 1);
+    const unsigned begins = __ballot_sync(kAll, lane == 0 || entry.y != above);
 
     Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared);
 #pragma unroll 1
     for (int part = 0; part < 3; ++part) {  // the long segment's end, short segments, a long segment's begin
         if (part == 0 ? !tail : part == 2 && !head)
             continue;
-        const int lo = part == 0 ? begin : part == 1 ? from : seg1.x;
-        const int hi = part == 0 ? min(seg0.y, end) : part == 1 ? to : end;
+        const int lo = part == 0 ? begin : part == 1 ? from : begin1;
+        const int hi = part == 0 ? min(end0, end) : part == 1 ? to : end;
         if (lo >= hi)
             continue;
         w.clear();
         const int here = hi - begin;
-        int32_t current = __shfl_sync(kAll, my_key, lo - begin);
+        int32_t current = __shfl_sync(kAll, entry.y, lo - begin);
 #pragma unroll 1
         for (int q = lo - begin; q < here; q += kInFlight) {
             SlabGroup<DT, VEC> x[kInFlight];
             int32_t place[kInFlight];
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {  // past the end the last row again: no branch between the loads
-                place[u] = __shfl_sync(kAll, my_place, min(q + u, here - 1));
+                place[u] = __shfl_sync(kAll, entry.x, min(q + u, here - 1));
                 x[u].load(w.cols, a.dout.data, static_cast<uint32_t>(place[u]) * a.dout.stride);
             }
 #pragma unroll
@@ -303,12 +330,12 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int lane
                 if ((begins >> (q + u) & 1u) && q + u > lo - begin) {
                     w.finish(current);
                     w.clear();
-                    current = __shfl_sync(kAll, my_key, q + u);
+                    current = __shfl_sync(kAll, entry.y, q + u);
                 }
                 w.add(x[u], place[u]);
             }
         }
-        if (part == 1 || w.gather(part == 0 ? seg0 : seg1, stretch, slab, lane))
+        if (part == 1 || w.gather(part == 0 ? begin0 : begin1, part == 0 ? end0 : end1, stretch, slab, lane))
             w.finish(current);
     }
 }
@@ -326,7 +353,7 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
     const int64_t place0 = row - at.first;
     if (place0 < 0 || place0 >= at.seq_len || place0 >= at.n) {
         if (a.base.data != a.grad.data)
-            fill_slab<GT, VEC>(a, Slab<VEC>(slab, lane, a.dim), row);
+            fill_row<GT, VEC>(a, row, slab * kSlabCols<VEC>, min((slab + 1) * kSlabCols<VEC>, a.dim), lane);
         return;
     }
     Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared);
@@ -365,7 +392,7 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
     typename SlabMask<VEC>::Shared* shared = &buffers[DROP ? warp : 0];
     unsigned block = blockIdx.x;
     if (block < roles.scans) {
-        scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(block) * kScanRows, warp, lane);
+        scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(block) * roles.scan_rows, roles.scan_rows, warp, lane);
         wait_for_launch_before();  // the launch after this one relies on it
         return;
     }
@@ -388,13 +415,10 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
         block -= before;
     }
     const unsigned fills = roles.fills_before(block);
-    const bool fill = roles.fills_before(block + 1) != fills;
-    if (fill && roles.scan)
-        scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(roles.scans + fills) * kScanRows, warp, lane);
     wait_for_launch_before();
-    if (fill && !roles.scan)
+    if (roles.fills_before(block + 1) != fills)
         fill_rows<GT, VEC>(a, (static_cast<int64_t>(fills) * kWarps + warp) * kFillRows, lane);
-    else if (!fill)
+    else
         walk<DT, GT, VEC, DROP>(a, static_cast<int64_t>(block - fills) * kWarps + warp, lane, shared);
 }
 
@@ -416,14 +440,13 @@ cudaError_t launch_p(const RowSumArgs& a, const RowSumArgs& p, const Places& at,
     const unsigned walks = walk_blocks(a);
     unsigned fills = fill_blocks(a), positions = 0;
     if (fills > 0 && a.scan && a.n <= kScan) {
-        const unsigned scans = static_cast<unsigned>((a.rows + kScanRows - 1) / kScanRows);
-        roles.scan = 1;
-        roles.scans = scans < kLeadScans ? scans : kLeadScans;
-        fills = scans - roles.scans;
+        roles.scan_rows = static_cast<int>((a.rows + kScans * 32 - 1) / (kScans * 32) * 32);
+        roles.scans = static_cast<unsigned>((a.rows + roles.scan_rows - 1) / roles.scan_rows);
+        fills = 0;
     }
     if (POSITIONS == kRunningPositions) {
         positions = blocks_for(static_cast<int64_t>(p.rows) * p.slabs);
-        roles.lead = roles.scan ? 0 : positions < kLead ? positions : kLead;
+        roles.lead = roles.scans ? 0 : positions < kLead ? positions : kLead;
     } else if (POSITIONS == kSortedPositions) {
         roles.position_walks = walk_blocks(p);
         positions = roles.position_walks + fill_blocks(p);
@@ -432,7 +455,8 @@ cudaError_t launch_p(const RowSumArgs& a, const RowSumArgs& p, const Places& at,
     if (roles.scans + blocks == 0)
         return cudaSuccess;
     roles.positions = share_of(positions - roles.lead, blocks - roles.lead);
-    roles.fill = share_of(fills, walks + fills);
+    roles.walk_lead = walks < kWalkLead ? walks : kWalkLead;
+    roles.fill = share_of(fills, walks - roles.walk_lead + fills);
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(roles.scans + blocks);
     c.blockDim = dim3(kBlock);

@@ -38,112 +38,136 @@ __device__ __forceinline__ void scale_pairs(float (&y)[N], float r)
         y[N - 1] = __fmul_rn(y[N - 1], r);
 }
 
-// One warp: PLACES places on a slab of columns.  With running positions they
+// Which position row a place adds.
+enum Positions { kNone, kRunning, kGiven };
+
+// One warp: a.rounds times PLACES places on a slab of columns, PLACES in flight
+// and the tokens of the next round on their way.  With running positions they
 // are the same place of that many sequences, so its position row is read once;
 // otherwise neighbours.
-template <typename TT, typename OT, bool VEC, bool DROP, int PLACES, bool RUNNING>
+template <typename TT, typename OT, bool VEC, bool DROP, int PLACES, int POSITIONS>
 __global__ void __launch_bounds__(kBlock) k_lookup(const LookupArgs a)
 {
     constexpr int N = kLaneCols<VEC>;
+    constexpr int kRows = POSITIONS == kGiven ? PLACES : 1;  // position rows in flight
     __shared__ typename SlabMask<VEC>::Shared shared[DROP ? kWarps : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    const int64_t group = quotient(unit, a.slabs);
-    const int slab = static_cast<int>(unit - group * a.slabs);
-    const int span = static_cast<int>(a.span);
-    int64_t place0 = group * PLACES, step = 1, in_sequence = 0;
-    if constexpr (RUNNING) {
-        const int64_t sequences = quotient(group, span);  // PLACES sequences each
-        step = span;
-        in_sequence = group - sequences * span;
-        place0 = sequences * PLACES * step + in_sequence;
+    const uint32_t group = static_cast<uint32_t>(quotient(unit, a.slabs));
+    const int slab = static_cast<int>(unit - static_cast<int64_t>(group) * a.slabs);
+    const uint32_t places = PLACES * a.rounds, n = a.at.n;
+    uint32_t step = 1, first = group * places, in_sequence = 0;
+    if constexpr (POSITIONS == kRunning) {
+        const uint32_t sequences = group / static_cast<uint32_t>(a.span);
+        step = a.span;
+        in_sequence = group - sequences * step;
+        first = sequences * places * step + in_sequence;
     }
-    if (place0 >= a.at.n)
+    if (first >= n)
         return;
-
-    // lane u: the token and position of place u
-    int my_token = -1, my_position = -1;
-    if (lane < PLACES && place0 + lane * step < a.at.n) {
-        my_token = token_at(a.at, place0 + lane * step, a.status);
-        if (a.pos_table.data)
-            my_position = RUNNING ? static_cast<int>(a.at.first + in_sequence) : position_at(a.at, place0 + lane * step, a.status);
-    }
     const Slab<VEC> cols(slab, lane, a.dim);
     SlabMask<VEC> mask(a.drop, slab, lane, a.dim, &shared[DROP ? warp : 0]);
-    SlabGroup<TT, VEC> x[PLACES], p[RUNNING ? 1 : PLACES];
-    int token[PLACES], position[PLACES];
-#pragma unroll
-    for (int u = 0; u < PLACES; ++u) {
-        token[u] = __shfl_sync(kAll, my_token, u);
-        x[u].load(cols, a.table.data, static_cast<uint32_t>(max(token[u], 0)) * a.table.stride);
-    }
-    if (a.pos_table.data) {
+    SlabGroup<TT, VEC> x[PLACES], p[kRows];
+    // lane u: the token (and position) of place u of the round
+    int next_token = -1, next_position = -1;
+    auto fetch = [&](uint32_t round) {
+        const uint64_t place = first + static_cast<uint64_t>(round * PLACES + lane) * step;
+        next_token = next_position = -1;
+        if (lane < PLACES && place < n) {
+            next_token = token_at(a.at, place, a.status);
+            if (POSITIONS == kGiven)
+                next_position = position_at(a.at, place, a.status);
+        }
+    };
+    fetch(0);
+    if (POSITIONS == kRunning)
+        p[0].load(cols, a.pos_table.data, (a.at.first + in_sequence) * a.pos_table.stride);
+    for (uint32_t round = 0; round < a.rounds; ++round) {
+        int token[PLACES], position[PLACES];
 #pragma unroll
         for (int u = 0; u < PLACES; ++u) {
-            position[u] = __shfl_sync(kAll, my_position, u);
-            if (u == 0 || !RUNNING)
-                p[u].load(cols, a.pos_table.data, static_cast<uint32_t>(max(position[u], 0)) * a.pos_table.stride);
+            token[u] = __shfl_sync(kAll, next_token, u);
+            x[u].load(cols, a.table.data, static_cast<uint32_t>(max(token[u], 0)) * a.table.stride);
         }
-    }
+        if (POSITIONS == kGiven) {
 #pragma unroll
-    for (int u = 0; u < PLACES; ++u) {
-        const int64_t place = place0 + u * step;
-        if (place >= a.at.n)
-            break;
-        const uint32_t i = static_cast<uint32_t>(place);
-        float y[N];
-        if (token[u] < 0) {
+            for (int u = 0; u < PLACES; ++u) {
+                position[u] = __shfl_sync(kAll, next_position, u);
+                p[kRows > u ? u : 0].load(cols, a.pos_table.data, static_cast<uint32_t>(max(position[u], 0)) * a.pos_table.stride);
+            }
+        }
+        if (round + 1 < a.rounds)
+            fetch(round + 1);
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                y[k] = 0.0f;
+        for (int u = 0; u < PLACES; ++u) {
+            const uint64_t place = first + static_cast<uint64_t>(round * PLACES + u) * step;
+            if (place >= n)
+                return;
+            const uint32_t i = static_cast<uint32_t>(place);
+            float y[N];
+            if (token[u] < 0) {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    y[k] = 0.0f;
+                store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, y);
+                continue;
+            }
+            x[u].unpack(y);
+            if (a.scale != 1.0f) {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    y[k] = __fmul_rn(a.scale, y[k]);
+            }
+            if (POSITIONS == kRunning || (POSITIONS == kGiven && position[u] >= 0)) {
+                float q[N];
+                p[kRows > u ? u : 0].unpack(q);
+                add_pairs(y, q);
+            }
+            if constexpr (DROP) {
+                scale_pairs(y, a.drop.rescale);
+                mask.row(i, [&](int k, bool keep) { y[k] = keep ? y[k] : 0.0f; });
+            }
             store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, y);
-            continue;
         }
-        x[u].unpack(y);
-        if (a.scale != 1.0f) {
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                y[k] = __fmul_rn(a.scale, y[k]);
-        }
-        if (a.pos_table.data && position[u] >= 0) {
-            float q[N];
-            p[RUNNING ? 0 : u].unpack(q);
-            add_pairs(y, q);
-        }
-        if constexpr (DROP) {
-            scale_pairs(y, a.drop.rescale);
-            mask.row(i, [&](int k, bool keep) { y[k] = keep ? y[k] : 0.0f; });
-        }
-        store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, y);
     }
 }
 
-// Four places a warp keep enough bytes in flight and share a position row;
-// fewer warps than the SMs hold run one place each, for the latency.
-constexpr int kPlaces = 4;
+// Places in flight keep the memory busy (4; 2 where each has a position row of
+// its own, for the registers); rounds of them hide the tokens' loads and share
+// the index arithmetic and a position row, while there are warps for the SMs
+// nearly once over: 64 x 1024 places of 2048 columns 101 -> 88 us with 8 rounds,
+// 8 x 1024 of 768 7.5 -> 7.2 us with 2; 4907 of 771 lost by them (6.1 -> 7.0 us).
+// Fewer warps than the SMs hold run one place each, for the latency.
 constexpr int64_t kFewWarps = 152 * kWarps;
+constexpr int64_t kManyWarps = 152 * 36;
+constexpr uint32_t kMaxRounds = 8;
+
+template <typename TT, typename OT, bool VEC, bool DROP, int PLACES, int POSITIONS>
+cudaError_t launch_p(LookupArgs a, cudaStream_t s)
+{
+    const int64_t warps = a.at.n * static_cast<int64_t>(a.slabs), sequences = (a.at.n + a.span - 1) / a.span;
+    a.rounds = 1;
+    while (PLACES > 1 && a.rounds < kMaxRounds && warps > kManyWarps * PLACES * a.rounds &&
+           (POSITIONS != kRunning || sequences > PLACES * a.rounds))
+        a.rounds *= 2;
+    const int64_t places = PLACES * a.rounds;
+    const int64_t groups = POSITIONS == kRunning ? (sequences + places - 1) / places * a.span : (a.at.n + places - 1) / places;
+    k_lookup<TT, OT, VEC, DROP, PLACES, POSITIONS>
+        <<<static_cast<unsigned>((groups * a.slabs + kWarps - 1) / kWarps), kBlock, 0, s>>>(a);
+    return cudaGetLastError();
+}
 
 template <typename TT, typename OT, bool VEC, bool DROP>
 cudaError_t launch_k(LookupArgs a, cudaStream_t s)
 {
     a.slabs = slabs_of(a.dim, VEC);
-    a.span = a.at.seq_len < a.at.n ? a.at.seq_len : a.at.n;
-    const bool few = a.at.n * static_cast<int64_t>(a.slabs) <= kFewWarps;
-    const bool running = a.pos_table.data && !a.at.positions && !few;
-    const int64_t places = few ? 1 : kPlaces;
-    int64_t groups = (a.at.n + places - 1) / places;
-    if (running) {
-        const int64_t sequences = (a.at.n + a.span - 1) / a.span;
-        groups = (sequences + places - 1) / places * a.span;
-    }
-    const unsigned blocks = static_cast<unsigned>((groups * a.slabs + kWarps - 1) / kWarps);
-    if (few)
-        k_lookup<TT, OT, VEC, DROP, 1, false><<<blocks, kBlock, 0, s>>>(a);
-    else if (running)
-        k_lookup<TT, OT, VEC, DROP, kPlaces, true><<<blocks, kBlock, 0, s>>>(a);
-    else
-        k_lookup<TT, OT, VEC, DROP, kPlaces, false><<<blocks, kBlock, 0, s>>>(a);
-    return cudaGetLastError();
+    a.span = static_cast<int32_t>(a.at.seq_len < a.at.n ? a.at.seq_len : a.at.n);
+    if (!a.pos_table.data)
+        return a.at.n * static_cast<int64_t>(a.slabs) <= kFewWarps ? launch_p<TT, OT, VEC, DROP, 1, kNone>(a, s)
+                                                                    : launch_p<TT, OT, VEC, DROP, 4, kNone>(a, s);
+    if (a.at.n * static_cast<int64_t>(a.slabs) <= kFewWarps)
+        return launch_p<TT, OT, VEC, DROP, 1, kGiven>(a, s);
+    return a.at.positions ? launch_p<TT, OT, VEC, DROP, 2, kGiven>(a, s) : launch_p<TT, OT, VEC, DROP, 4, kRunning>(a, s);
 }
 
 template <typename TT, typename OT>

@@ -43,33 +43,37 @@ __device__ __forceinline__ int32_t key_of(const Places& at, IT token, IT positio
     return there && good ? static_cast<int32_t>(key) : -1;
 }
 
-// Keys of places i0 + 32 u + lane below hi: the loads before any use, so that
-// they are in flight together.
-template <int KIND, typename IT, bool WHOLE>
-__device__ __forceinline__ void read_keys(const Places& at, int64_t i0, int64_t hi, int lane, int* status, int32_t (&key)[kBatch])
-{
-    IT token[kBatch], position[kBatch];
+// Tokens (and positions) of places i0 + 32 u + lane below hi: the loads before
+// any use, so that they are in flight together.
+template <int KIND, typename IT>
+struct RawKeys {
+    IT token[kBatch], position[KIND == kKeyPosition ? kBatch : 1];
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const Places& at, int64_t i0, int64_t hi, int lane)
+    {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = i0 + u * 32 + lane;
-        token[u] = -1;
-        position[u] = 0;
-        if (WHOLE || i < hi) {
-            token[u] = static_cast<const IT*>(at.tokens)[i];
-            if (KIND == kKeyPosition)
-                position[u] = at.positions ? static_cast<const IT*>(at.positions)[i]
-                                           : static_cast<IT>(at.first + static_cast<uint32_t>(i) % static_cast<uint32_t>(at.seq_len));
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * 32 + lane;
+            token[u] = -1;
+            if (WHOLE || i < hi) {
+                token[u] = static_cast<const IT*>(at.tokens)[i];
+                if (KIND == kKeyPosition)
+                    position[KIND == kKeyPosition ? u : 0] =
+                        at.positions ? static_cast<const IT*>(at.positions)[i]
+                                     : static_cast<IT>(at.first + static_cast<uint32_t>(i) % static_cast<uint32_t>(at.seq_len));
+            }
         }
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-        key[u] = key_of<KIND, IT>(at, token[u], position[u], status);
-}
+    __device__ __forceinline__ int32_t key(const Places& at, int u, int* status) const
+    {
+        return key_of<KIND, IT>(at, token[u], position[KIND == kKeyPosition ? u : 0], status);
+    }
+};
 
 // Places one key of each lane that has one: the lane's rank among equal keys
 // of the warp, after those its warp placed before.
-__device__ __forceinline__ void place_keys(const SortTask& t, int* next, bool has, int owned_key, int key_bits, int32_t key,
-                                           int32_t place, int lane, int* status)
+__device__ __forceinline__ void place_keys(const SortTask& t, int* next, const int2* range, bool has, int owned_key, int key_bits,
+                                           int32_t key, int32_t place, int lane, int* status)
 {
     unsigned same = __ballot_sync(kAll, has);
     for (int b = 0; b < key_bits; ++b) {
@@ -84,12 +88,16 @@ __device__ __forceinline__ void place_keys(const SortTask& t, int* next, bool ha
     if (has) {
         if ((same >> lane) == 1u)  // the last lane with this key
             next[owned_key] = at + 1;
-        if (index_ok(status, at >= 0 && at < t.capacity)) {
-            t.order[at] = place;
-            t.sorted_key[at] = key;
-        }
+        if (index_ok(status, at >= 0 && at < t.capacity))
+            t.order[at] = make_int4(place, key, range[owned_key].x, range[owned_key].y);
     }
     __syncwarp();
+}
+
+// Keys a block owns at most, rounded to 16 bytes of counts.
+__host__ __device__ constexpr int owned_width(int keys, int shift)
+{
+    return (((keys + (1 << shift) - 1) >> shift) + 3) / 4 * 4;
 }
 
 template <int KIND, typename IT, int BLOCK>
@@ -100,30 +108,36 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int shift = t.log_blocks, mask = (1 << shift) - 1;
     const int owned = mine < t.keys ? ((t.keys - 1 - mine) >> shift) + 1 : 0;
-    const int width = (t.keys + mask) >> shift;  // of the rows of count
+    const int width = owned_width(t.keys, shift);  // of the rows of count
     int* count = memory;                         // kWarps x width: keys of each (warp, key), then where the next goes
     uint32_t* list = reinterpret_cast<uint32_t*>(memory + kWarps * width) + warp * kList;  // place in slice | owned key << 16
+    int2* range = reinterpret_cast<int2*>(memory + kWarps * (width + kList));  // the block's segments
     int* status = mine == 0 ? all_status : nullptr;
-    for (int k = tid; k < kWarps * width; k += BLOCK)
-        count[k] = 0;
-    __syncthreads();
+    for (int k = tid; k < kWarps * width / 4; k += BLOCK)
+        reinterpret_cast<int4*>(count)[k] = make_int4(0, 0, 0, 0);
     count += warp * width;
+    // what came before in the stream is done and visible; then the row sums may start beside this
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
 
     const int64_t n = t.at.n;
     const int64_t slice = (n + BLOCK - 1) / BLOCK * 32;
     const int64_t lo = warp * slice, hi = min(lo + slice, n);
     int found = 0, below = 0;
-    auto count_keys = [&](int64_t i0, const int32_t (&key)[kBatch]) {
+    __syncthreads();  // count is zero
+    RawKeys<KIND, IT> raw;
+    auto count_keys = [&](int64_t i0) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int b = key[u] & mask;
-            below += key[u] >= 0 && b < mine ? 1 : 0;
-            const bool take = key[u] >= 0 && b == mine;
+            const int32_t key = raw.key(t.at, u, status);
+            const int b = key & mask;
+            below += key >= 0 && b < mine ? 1 : 0;
+            const bool take = key >= 0 && b == mine;
             const unsigned takers = __ballot_sync(kAll, take);
             if (takers == 0)
                 continue;
             if (take) {
-                const int k = key[u] >> shift, at = found + __popc(takers & ((1u << lane) - 1));
+                const int k = key >> shift, at = found + __popc(takers & ((1u << lane) - 1));
                 atomicAdd(&count[k], 1);
                 if (at < kList)
                     list[at] = static_cast<uint32_t>(i0 - lo + u * 32 + lane) | static_cast<uint32_t>(k) << 16;
@@ -133,14 +147,12 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     };
     int64_t i0 = lo;
     for (; i0 + kBatch * 32 <= hi; i0 += kBatch * 32) {
-        int32_t key[kBatch];
-        read_keys<KIND, IT, true>(t.at, i0, hi, lane, status, key);
-        count_keys(i0, key);
+        raw.template load<true>(t.at, i0, hi, lane);
+        count_keys(i0);
     }
     if (i0 < hi) {
-        int32_t key[kBatch];
-        read_keys<KIND, IT, false>(t.at, i0, hi, lane, status, key);
-        count_keys(i0, key);
+        raw.template load<false>(t.at, i0, hi, lane);
+        count_keys(i0);
     }
     below = __reduce_add_sync(kAll, below);
     if (lane == 0)
@@ -174,12 +186,18 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
             const int32_t key = (k << shift) | mine;
             if (index_ok(all_status, key < t.keys && start >= 0 && start + total <= t.capacity))
                 t.segment[key] = make_int2(start, start + total);
+            range[k] = make_int2(start, start + total);
             int at = start;
-#pragma unroll 8
-            for (int w = 0; w < kWarps; ++w) {
-                const int c = memory[w * width + k];
-                memory[w * width + k] = at;
-                at += c;
+            for (int w0 = 0; w0 < kWarps; w0 += 8) {  // 8 loads at a time: a store between two keeps them apart
+                int each[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w)
+                    each[w] = memory[(w0 + w) * width + k];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    memory[(w0 + w) * width + k] = at;
+                    at += each[w];
+                }
             }
         }
     }
@@ -193,17 +211,17 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
             const bool has = q + lane < found;
             const uint32_t item = has ? list[q + lane] : 0;
             const int k = static_cast<int>(item >> 16);
-            place_keys(t, count, has, k, key_bits, (k << shift) | mine, static_cast<int32_t>(lo + (item & 0xffff)), lane, all_status);
+            place_keys(t, count, range, has, k, key_bits, (k << shift) | mine, static_cast<int32_t>(lo + (item & 0xffff)), lane, all_status);
         }
     } else {
         for (int64_t i1 = lo; i1 < hi; i1 += kBatch * 32) {
-            int32_t key[kBatch];
-            read_keys<KIND, IT, false>(t.at, i1, hi, lane, nullptr, key);
+            raw.template load<false>(t.at, i1, hi, lane);
             for (int u = 0; u < kBatch; ++u) {
-                const bool has = key[u] >= 0 && (key[u] & mask) == mine;
+                const int32_t key = raw.key(t.at, u, nullptr);
+                const bool has = key >= 0 && (key & mask) == mine;
                 if (__ballot_sync(kAll, has))
-                    place_keys(t, count, has, has ? key[u] >> shift : 0, key_bits, key[u],
-                               static_cast<int32_t>(i1 + u * 32 + lane), lane, all_status);
+                    place_keys(t, count, range, has, has ? key >> shift : 0, key_bits, key, static_cast<int32_t>(i1 + u * 32 + lane),
+                               lane, all_status);
             }
         }
     }
@@ -212,11 +230,7 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
 template <int BLOCK>
 __global__ void __launch_bounds__(BLOCK) k_sort(const __grid_constant__ SortArgs a)
 {
-    extern __shared__ int memory[];
-    asm volatile("griddepcontrol.launch_dependents;");
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * BLOCK + threadIdx.x; k < a.arrived_count;
-         k += static_cast<int64_t>(gridDim.x) * BLOCK)
-        a.arrived[0][k] = a.arrived[1][k] = 0;
+    extern __shared__ __align__(16) int memory[];
     int block = blockIdx.x;
     for (int k = 0; k < a.tasks; ++k) {
         const int sorters = 1 << a.task[k].log_blocks;
@@ -228,24 +242,36 @@ __global__ void __launch_bounds__(BLOCK) k_sort(const __grid_constant__ SortArgs
             else
                 t.at.wide ? sort_task<kKeyPosition, int64_t, BLOCK>(t, block, memory, a.status)
                           : sort_task<kKeyPosition, int32_t, BLOCK>(t, block, memory, a.status);
-            return;
+            break;
         }
         block -= sorters;
     }
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * BLOCK + threadIdx.x; k < a.arrived_count;
+         k += static_cast<int64_t>(gridDim.x) * BLOCK)
+        a.arrived[0][k] = a.arrived[1][k] = 0;
 }
 
 template <int BLOCK>
 cudaError_t launch_block(const SortArgs& a, int blocks, int width, cudaStream_t s)
 {
-    const size_t shared = sizeof(int) * (BLOCK / 32) * (width + kList);
-    static_assert(sizeof(int) * (BLOCK / 32) * (kMaxOwned + kList) <= 220 * 1024, "a block fits an SM");
+    const size_t shared = sizeof(int) * (BLOCK / 32) * (width + kList) + sizeof(int2) * width;
+    static_assert(sizeof(int) * (BLOCK / 32) * (kMaxOwned + kList) + sizeof(int2) * kMaxOwned <= 220 * 1024, "a block fits an SM");
     if (shared > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k_sort<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
         if (e != cudaSuccess)
             return e;
     }
-    k_sort<BLOCK><<<blocks, BLOCK, shared, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(static_cast<unsigned>(blocks));
+    c.blockDim = dim3(BLOCK);
+    c.dynamicSmemBytes = shared;
+    c.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, k_sort<BLOCK>, a);
 }
 
 }  // namespace
@@ -260,7 +286,7 @@ cudaError_t launch_sort(SortArgs a, cudaStream_t s)
             ++t.log_blocks;
         while ((static_cast<int64_t>(kMaxOwned) << t.log_blocks) < t.keys)
             ++t.log_blocks;
-        const int w = (t.keys + (1 << t.log_blocks) - 1) >> t.log_blocks;
+        const int w = owned_width(t.keys, t.log_blocks);
         width = width < w ? w : width;
         sorters += 1 << t.log_blocks;
     }
