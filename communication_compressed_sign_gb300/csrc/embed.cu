@@ -380,7 +380,7 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     const int64_t tables = positions > 0 ? 2 : 1;
     const int64_t slabs = lc::slabs_of(dim, false);  // the most: rows that allow 16-byte moves have fewer
     const int64_t stretches = lc::grad_max_stretches(max_tokens, lc::slabs_of(dim, true));
-    h->partial_rows = 2 * stretches;
+    h->partial_rows = lc::grad_partial_rows(stretches);
     h->partial_stride = slabs * 256;
     h->arrived_count = h->partial_rows * slabs;
     h->fail_alloc_at = env_index("LIONCUB_FAIL_ALLOC");
@@ -495,7 +495,7 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
     const int64_t slabs = lc::slabs_of(h->dim, vec);
     so.arrived[0] = h->arrived;
     so.arrived[1] = sorted_positions ? h->arrived + h->arrived_count : h->arrived;
-    so.arrived_count = 2 * lc::grad_stretches(at.n, lc::grad_piece(at.n, slabs)) * slabs;
+    so.arrived_count = lc::grad_partial_rows(lc::grad_stretches(at.n, lc::grad_piece(at.n, slabs))) * slabs;
     so.status = h->status;
     cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, stream); });
     if (e != cudaSuccess)

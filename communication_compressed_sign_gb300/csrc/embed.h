@@ -71,6 +71,8 @@ inline int grad_piece(int64_t n, int64_t slabs)
     return piece;
 }
 inline int64_t grad_stretches(int64_t n, int piece) { return (n + piece - 1) / piece; }
+// Blocks of 8 stretches, each of which may leave two partials.
+inline int64_t grad_partial_rows(int64_t stretches) { return (stretches + 7) / 8 * 2; }
 // The most that a batch of up to n places has.
 inline int64_t grad_max_stretches(int64_t n, int64_t slabs)
 {
@@ -108,7 +110,7 @@ struct RowSumArgs {
     const int4* order;
     const int2* segment;
     const int32_t* total;
-    float* partial;          // two fp32 rows for each stretch
+    float* partial;          // two fp32 rows for each block of stretches
     int64_t partial_stride;  // 256 for each slab
     int64_t partial_rows;
     uint64_t* arrived;       // arrivals, for each (row of partial, slab)

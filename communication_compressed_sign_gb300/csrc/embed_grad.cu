@@ -5,15 +5,16 @@
 // zeros (or base) -- so there is no clearing pass, and no float atomics: the
 // order of every sum depends on the batch alone.
 //
-// The unit of work is one warp on a slab of 256 columns.
+// The unit of work is one warp on a slab of columns.
 //   walk   a stretch of `piece` entries of `order`: the warp adds the rows of
 //          dout of the segments that begin there, several rows in flight
 //          whatever the segments' lengths, and writes a row of grad at each
 //          segment's end.  A segment of up to `piece` places belongs to the
-//          stretch it begins in.  A longer one is cut at the stretches' bounds:
-//          each warp leaves an fp32 partial, and the last of a group of partials to
-//          arrive (an integer counter) adds them in order.  So units are alike in size
-//          however skewed the tokens are.
+//          stretch it begins in.  A longer one is cut at the stretches' bounds: a
+//          block's warps take consecutive stretches and add their pieces in
+//          shared memory, blocks leave an fp32 partial, and the last of a group of
+//          blocks to arrive (an integer counter) adds the partials in order.  So
+//          units are alike in size however skewed the tokens are.
 //   fill   rows without a place.
 // Bound by memory: dout is read once and grad written once.
 #include <type_traits>
@@ -30,7 +31,7 @@ constexpr int kJoinBits = kJoinLog + 1;             // 64 / kJoinBits levels are
 constexpr int kInFlight = 4;              // rows of dout a warp loads before it adds them
 constexpr int kFillRows = 8;              // rows of grad a fill warp looks at
 constexpr unsigned kLead = 152 * 4;       // blocks the SMs hold
-constexpr unsigned kWalkLead = 152 * XWL;   // walks that start first: they take longest
+constexpr unsigned kWalkLead = 152 * 4;   // walks that start first: they take longest
 constexpr unsigned kScans = 152 * 2;      // scanning fill blocks, which leave room for walks
 constexpr int kMaxScanRows = 4096;        // rows such a block takes at most
 constexpr int64_t kScan = 0;          // batches up to this many places fill by scanning
@@ -102,19 +103,19 @@ struct Walker {
         }
         store_slab<GT, VEC>(cols, a.grad.data, v * a.grad.stride, sum);
     }
-    // Adds up the pieces of a long segment: a tree of groups of kJoin, in which
-    // the last of a group to arrive adds the group's partials in order and goes
-    // on as one piece of the next level.  True where the whole sum has come
-    // together.
-    __device__ __forceinline__ bool gather(int begin, int end, int stretch, int slab, int lane)
+    // Adds up the blocks' sums of a long segment [begin, end): a tree of groups of
+    // kJoin, in which the last of a group to arrive adds the group's partials in
+    // order and goes on as one block of the next level.  True where the whole
+    // sum has come together.
+    __device__ __forceinline__ bool gather(int begin, int end, int block, int slab, int lane)
     {
-        const int first = begin / a.piece;
-        int node = stretch - first, nodes = (end - 1) / a.piece - first + 1;
+        const int first = begin / a.piece / kWarps;
+        int node = block - first, nodes = (end - 1) / a.piece / kWarps - first + 1;
         const int64_t column = slab * 256 + lane * 8;  // partial rows are whole slabs
-        // piece r's partial and counter: slot 1 of the stretch the segment begins in, slot 0 of the later ones
+        // the r-th block's partial and counter: slot 1 of the block the segment begins in, slot 0 of the later ones
         auto slot = [&](int r) { return 2 * static_cast<int64_t>(first + r) + (r == 0 ? 1 : 0); };
         auto partial = [&](int r) { return a.partial + slot(r) * a.partial_stride + column; };
-        if (!index_ok(a.status, 2 * static_cast<int64_t>(stretch) + 1 < a.partial_rows))
+        if (!index_ok(a.status, 2 * static_cast<int64_t>(block) + 1 < a.partial_rows))
             return false;
 #pragma unroll 1
         for (int level = 0; nodes > 1; ++level) {
@@ -145,6 +146,11 @@ struct Walker {
         asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(before) : "l"(counter), "l"(one) : "memory");
         return before;
     }
+    __device__ __forceinline__ void put(float4 (&to)[2][32], int lane) const
+    {
+        to[0][lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        to[1][lane] = make_float4(sum[4], sum[5], sum[6], N == 8 ? sum[N - 1] : 0.0f);
+    }
     // A lane's sums lie together in a partial row, whichever columns they are.
     __device__ __forceinline__ void store_partial(float* p) const
     {
@@ -153,7 +159,10 @@ struct Walker {
     }
     __device__ __forceinline__ void add_partial(const float* p)
     {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p)), y = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+        add_group(__ldcg(reinterpret_cast<const float4*>(p)), __ldcg(reinterpret_cast<const float4*>(p) + 1));
+    }
+    __device__ __forceinline__ void add_group(const float4& x, const float4& y)
+    {
         const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int k = 0; k < N; ++k)
@@ -273,39 +282,44 @@ struct Roles {
     }
 };
 
-// One stretch of the sorted places on one slab.
+// What a block of walks shares: the masks' draws, and its warps' sums of long
+// segments, of the one that goes on from before a warp's stretch and of the one
+// that begins in it.
+template <bool VEC, bool DROP>
+struct WalkShared {
+    typename SlabMask<VEC>::Shared mask[DROP ? kWarps : 1];
+    float4 sums[kWarps][2][2][32];
+    __device__ __forceinline__ typename SlabMask<VEC>::Shared* of(int warp) { return &mask[DROP ? warp : 0]; }
+};
+
+// A block of stretches of the sorted places, one a warp, on one slab.
 template <typename DT, typename GT, bool VEC, bool DROP>
-__device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int lane, typename SlabMask<VEC>::Shared* shared)
+__device__ __forceinline__ void walk(const RowSumArgs& a, unsigned index, int warp, int lane, WalkShared<VEC, DROP>& shared)
 {
-    const int stretch = static_cast<int>(quotient(unit, a.slabs));  // places and so stretches fit 31 bits
-    const int slab = static_cast<int>(unit - static_cast<int64_t>(stretch) * a.slabs);
-    const int64_t begin64 = static_cast<int64_t>(stretch) * a.piece;
-    if (begin64 >= a.n)
-        return;
-    const int begin = static_cast<int>(begin64);
+    const int block = static_cast<int>(index / static_cast<unsigned>(a.slabs));  // places and so stretches fit 31 bits
+    const int slab = static_cast<int>(index - static_cast<unsigned>(block) * a.slabs);
+    const int64_t begin64 = (static_cast<int64_t>(block) * kWarps + warp) * a.piece;
+    const int begin = static_cast<int>(min(begin64, static_cast<int64_t>(a.n)));
     // the stretch's entries and what a short segment can reach beyond it, not waiting for how many are set
-    const int mine = begin + lane;
+    const int mine = min(begin + lane, a.n);  // below 2^31
     const int4 entry = mine < a.n ? a.order[mine] : make_int4(0, 0, 0, 0);
-    const int total = *a.total;
-    if (begin >= total)
-        return;
-    const int end = min(begin + a.piece, total);
-    if (!__all_sync(kAll, index_ok(a.status, mine >= total || (entry.x >= 0 && entry.x < a.n && entry.y >= 0 && entry.y < a.rows))))
-        return;
-    const int last = end - 1 - begin;
+    const int total = *a.total, end = min(begin + a.piece, total);
+    bool work = begin < total;
+    work = __all_sync(kAll, index_ok(a.status, mine >= total || (entry.x >= 0 && entry.x < a.n && entry.y >= 0 && entry.y < a.rows))) && work;
+    const int last = max(end - 1 - begin, 0);
     const int begin0 = __shfl_sync(kAll, entry.z, 0), end0 = __shfl_sync(kAll, entry.w, 0);
     const int begin1 = __shfl_sync(kAll, entry.z, last), end1 = __shfl_sync(kAll, entry.w, last);
-    const bool tail = begin0 < begin && end0 - begin0 > a.piece;   // a long segment goes on here
-    const bool head = begin1 >= begin && end1 - begin1 > a.piece;  // a long segment begins here
+    const bool tail = work && begin0 < begin && end0 - begin0 > a.piece;   // a long segment goes on here
+    const bool head = work && begin1 >= begin && end1 - begin1 > a.piece;  // a long segment begins here
     // short segments: one that began before belongs there, one that begins here is taken to its end
     const int from = begin0 < begin ? end0 : begin, to = head ? begin1 : (begin1 < begin ? begin : end1);
     const int32_t above = __shfl_up_sync(kAll, entry.y, 1);
     const unsigned begins = __ballot_sync(kAll, lane == 0 || entry.y != above);
 
-    Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared);
+    Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared.of(warp));
 #pragma unroll 1
     for (int part = 0; part < 3; ++part) {  // the long segment's end, short segments, a long segment's begin
-        if (part == 0 ? !tail : part == 2 && !head)
+        if (part == 0 ? !tail : part == 1 ? !work : !head)
             continue;
         const int lo = part == 0 ? begin : part == 1 ? from : begin1;
         const int hi = part == 0 ? min(end0, end) : part == 1 ? to : end;
@@ -335,8 +349,28 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, int64_t unit, int lane
                 w.add(x[u], place[u]);
             }
         }
-        if (part == 1 || w.gather(part == 0 ? begin0 : begin1, part == 0 ? end0 : end1, stretch, slab, lane))
+        if (part == 1)
             w.finish(current);
+        else
+            w.put(shared.sums[warp][part == 0 ? 0 : 1], lane);
+    }
+    if (!__syncthreads_or(tail || head))
+        return;
+
+    // a long segment's pieces in this block, added in order by the warp of the
+    // first of them: the one it begins in, or the block's first
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+        if (part == 0 ? !tail || warp > 0 : !head)
+            continue;
+        const int seg_begin = part == 0 ? begin0 : begin1, seg_end = part == 0 ? end0 : end1;
+        const int until = min(kWarps - 1, (seg_end - 1) / a.piece - block * kWarps);
+        w.clear();
+        w.add_group(shared.sums[warp][part][0][lane], shared.sums[warp][part][1][lane]);
+        for (int other = warp + 1; other <= until; ++other)
+            w.add_group(shared.sums[other][0][0][lane], shared.sums[other][0][1][lane]);
+        if (w.gather(seg_begin, seg_end, block, slab, lane))
+            w.finish(__shfl_sync(kAll, entry.y, part == 0 ? 0 : last));
     }
 }
 
@@ -387,9 +421,8 @@ template <typename DT, typename GT, bool VEC, bool DROP, int POSITIONS>
 __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
     k_row_sums(const __grid_constant__ RowSumArgs a, const __grid_constant__ RowSumArgs p, const Places at, const Roles roles)
 {
-    __shared__ typename SlabMask<VEC>::Shared buffers[DROP ? kWarps : 1];
+    __shared__ WalkShared<VEC, DROP> shared;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    typename SlabMask<VEC>::Shared* shared = &buffers[DROP ? warp : 0];
     unsigned block = blockIdx.x;
     if (block < roles.scans) {
         scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(block) * roles.scan_rows, roles.scan_rows, warp, lane);
@@ -402,11 +435,11 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
         if (roles.positions_before(block + 1) != before) {
             const int64_t unit = static_cast<int64_t>(before) * kWarps + warp;
             if constexpr (POSITIONS == kRunningPositions)
-                running_row<DT, GT, VEC, DROP>(p, at, unit, lane, shared);
+                running_row<DT, GT, VEC, DROP>(p, at, unit, lane, shared.of(warp));
             wait_for_launch_before();
             if constexpr (POSITIONS == kSortedPositions) {
                 if (before < roles.position_walks)
-                    walk<DT, GT, VEC, DROP>(p, unit, lane, shared);
+                    walk<DT, GT, VEC, DROP>(p, before, warp, lane, shared);
                 else
                     fill_rows<GT, VEC>(p, (unit - static_cast<int64_t>(roles.position_walks) * kWarps) * kFillRows, lane);
             }
@@ -419,7 +452,7 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
     if (roles.fills_before(block + 1) != fills)
         fill_rows<GT, VEC>(a, (static_cast<int64_t>(fills) * kWarps + warp) * kFillRows, lane);
     else
-        walk<DT, GT, VEC, DROP>(a, static_cast<int64_t>(block - fills) * kWarps + warp, lane, shared);
+        walk<DT, GT, VEC, DROP>(a, block - fills, warp, lane, shared);
 }
 
 unsigned blocks_for(int64_t warps) { return static_cast<unsigned>((warps + kWarps - 1) / kWarps); }
@@ -427,7 +460,7 @@ unsigned blocks_for(int64_t warps) { return static_cast<unsigned>((warps + kWarp
 // The share of `part` among `all`, in 2^-32, rounded up: exactly part of them.
 uint64_t share_of(unsigned part, unsigned all) { return all ? ((static_cast<uint64_t>(part) << 32) + all - 1) / all : 0; }
 
-unsigned walk_blocks(const RowSumArgs& a) { return blocks_for(grad_stretches(a.n, a.piece) * a.slabs); }
+unsigned walk_blocks(const RowSumArgs& a) { return blocks_for(grad_stretches(a.n, a.piece)) * a.slabs; }
 unsigned fill_blocks(const RowSumArgs& a)
 {
     return a.base.data == a.grad.data ? 0 : blocks_for((a.rows + kFillRows - 1) / kFillRows);  // none in place
