@@ -281,7 +281,6 @@ lc::RowSumArgs row_sum_args(lioncub_embed_t h, const lc::Places& at, const Table
     a.rows = static_cast<int32_t>(g.rows);
     a.dim = static_cast<int32_t>(h->dim);
     a.n = at.n;
-    a.scan = g.kind == lc::kKeyToken;
     a.status = h->status;
     return a;
 }

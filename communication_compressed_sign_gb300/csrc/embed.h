@@ -61,25 +61,29 @@ enum KeyKind { kKeyToken = 0, kKeyPosition = 1 };
 
 // Places a warp of the row sums takes; segments longer than this are summed in
 // pieces.  At most 16, so that a stretch and a short segment's overhang fit 32
-// lanes; less while that leaves SMs without work.
-constexpr int kMaxPiece = 16, kMinPiece = 4;
+// lanes.  Less in a batch whose walks then still fit three of the four blocks
+// that an SM holds, the fourth left to fills: a walk is bound by latency, so its
+// places cost time while SMs are idle (16384 places of 768 columns, added in
+// place: 16 a warp 25.8 us, 11 to 14 21 to 24; with the fills of a whole table
+// 11 took 53 us and 14 or 16 48.6).
+constexpr int kMaxPiece = 16, kMinPiece = 4, kWalkSlots = 152 * 3;
+inline int64_t grad_stretches(int64_t n, int piece) { return (n + piece - 1) / piece; }
 inline int grad_piece(int64_t n, int64_t slabs)
 {
-    int piece = kMinPiece;
-    while (piece < kMaxPiece && n * slabs > piece * int64_t(152 * 32))
-        piece *= 2;
-    return piece;
+    for (int piece = kMinPiece; piece < kMaxPiece; ++piece)
+        if ((grad_stretches(n, piece) + 7) / 8 * slabs <= kWalkSlots)
+            return piece;
+    return kMaxPiece;
 }
-inline int64_t grad_stretches(int64_t n, int piece) { return (n + piece - 1) / piece; }
-// Blocks of 8 stretches, each of which may leave two partials.
-inline int64_t grad_partial_rows(int64_t stretches) { return (stretches + 7) / 8 * 2; }
 // The most that a batch of up to n places has.
 inline int64_t grad_max_stretches(int64_t n, int64_t slabs)
 {
-    const int64_t few = 152 * 32 / slabs + 1, many = grad_stretches(n, kMaxPiece);
+    const int64_t few = kWalkSlots * 8 / slabs, many = grad_stretches(n, kMaxPiece);
     const int64_t most = few > many ? few : many;
     return most < grad_stretches(n, kMinPiece) ? most : grad_stretches(n, kMinPiece);
 }
+// Blocks of 8 stretches, each of which may leave two partials.
+inline int64_t grad_partial_rows(int64_t stretches) { return (stretches + 7) / 8 * 2; }
 
 // The sort of a batch's places by key.  order has an entry for each place that
 // has a key, grouped by key and ascending within one: (place, key, begin and end
@@ -120,7 +124,6 @@ struct RowSumArgs {
     int32_t dim;
     int32_t slabs, piece;  // set by launch_row_sums
     int32_t n;      // rows of dout
-    int32_t scan;   // the rows are tokens': a row's places can be looked for among the batch's tokens
     int* status;
 };
 

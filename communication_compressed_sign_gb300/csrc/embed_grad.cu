@@ -26,15 +26,11 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
-constexpr int kJoinLog = 4, kJoin = 1 << kJoinLog;  // pieces of a group, and counter bits for a level of groups:
-constexpr int kJoinBits = kJoinLog + 1;             // 64 / kJoinBits levels are more than 2^30 places can need
-constexpr int kInFlight = 4;              // rows of dout a warp loads before it adds them
-constexpr int kFillRows = 8;              // rows of grad a fill warp looks at
-constexpr unsigned kLead = 152 * 4;       // blocks the SMs hold
-constexpr unsigned kWalkLead = 152 * 4;   // walks that start first: they take longest
-constexpr unsigned kScans = 152 * 2;      // scanning fill blocks, which leave room for walks
-constexpr int kMaxScanRows = 4096;        // rows such a block takes at most
-constexpr int64_t kScan = 0;          // batches up to this many places fill by scanning
+constexpr int kInFlight = 4;           // rows of dout a warp loads before it adds them
+constexpr int kFillRows = 8;           // rows of grad a fill warp looks at
+constexpr unsigned kLead = 152 * 4;    // blocks the SMs hold: how many of a kind go ahead of the mix
+constexpr int kJoinLog = 4, kJoin = 1 << kJoinLog;  // partials of a group of the gathering tree
+constexpr int kJoinBits = kJoinLog + 1;             // counter bits of a level: 12 levels, 2^30 places need 6
 
 // Adds rows of dout to a running sum and writes it where the key changes.
 template <typename DT, typename GT, bool VEC, bool DROP>
@@ -192,36 +188,6 @@ __device__ __forceinline__ void fill_row(const RowSumArgs& a, int64_t v, int beg
     }
 }
 
-// Those of rows [row0, row0 + count) that no token of the batch has, found
-// without the sort: the block looks through all tokens.
-template <typename GT, bool VEC>
-__device__ __forceinline__ void scan_and_fill(const RowSumArgs& a, const Places& at, int64_t row0, int count, int warp, int lane)
-{
-    __shared__ unsigned has[kMaxScanRows / 32];
-    for (int k = threadIdx.x; k < kMaxScanRows / 32; k += kBlock)
-        has[k] = 0;
-    __syncthreads();
-    constexpr int kTokens = 8;  // loads in flight
-    for (int i0 = threadIdx.x; i0 < at.n; i0 += kTokens * kBlock) {
-        int64_t t[kTokens];
-#pragma unroll
-        for (int u = 0; u < kTokens; ++u)
-            t[u] = i0 + u * kBlock < at.n ? index_at(at.tokens, i0 + u * kBlock, at.wide) : -1;
-#pragma unroll
-        for (int u = 0; u < kTokens; ++u) {
-            const uint64_t r = static_cast<uint64_t>(t[u] - row0);
-            if (t[u] >= 0 && r < count)
-                atomicOr(&has[r >> 5], 1u << (r & 31));
-        }
-    }
-    __syncthreads();
-    for (int r = warp; r < count; r += kWarps) {
-        if ((has[r >> 5] >> (r & 31) & 1u) || row0 + r >= a.rows)
-            continue;
-        fill_row<GT, VEC>(a, row0 + r, 0, a.dim, lane);
-    }
-}
-
 // Those of rows [row0, row0 + kFillRows) that have no place.
 template <typename GT, bool VEC>
 __device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int lane)
@@ -259,14 +225,11 @@ __device__ __forceinline__ int nth_bit(unsigned word, int n)
     return at;
 }
 
-// What the blocks of a launch do.  Blocks that need no sort lead, while it may
-// still run: fills that scan the tokens (all of them, in small batches), else
-// running positions.  The rest are spread evenly: walks are bound by latency
-// or, with dropout, by integer instructions, and fills by memory, so they run
-// side by side.
+// What the blocks of a launch do.  Running positions need no sort, so they lead
+// while it may still run; walks start next, since they take longest; the rest
+// are spread evenly: walks are bound by latency or, with dropout, by integer
+// instructions, and fills by memory, so they run side by side.
 struct Roles {
-    unsigned scans;      // scanning fill blocks, the first
-    int scan_rows;       // rows of each
     unsigned lead;       // position blocks at the front
     uint64_t positions;  // share of position blocks among the others, in 2^-32
     uint64_t fill;       // share of fill blocks among walks and fills, likewise
@@ -424,19 +387,13 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
     __shared__ WalkShared<VEC, DROP> shared;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned block = blockIdx.x;
-    if (block < roles.scans) {
-        scan_and_fill<GT, VEC>(a, at, static_cast<int64_t>(block) * roles.scan_rows, roles.scan_rows, warp, lane);
-        wait_for_launch_before();  // the launch after this one relies on it
-        return;
-    }
-    block -= roles.scans;
     if constexpr (POSITIONS != kNoPositions) {
         const unsigned before = roles.positions_before(block);
         if (roles.positions_before(block + 1) != before) {
             const int64_t unit = static_cast<int64_t>(before) * kWarps + warp;
             if constexpr (POSITIONS == kRunningPositions)
                 running_row<DT, GT, VEC, DROP>(p, at, unit, lane, shared.of(warp));
-            wait_for_launch_before();
+            wait_for_launch_before();  // at the end too: the launch after this one relies on it
             if constexpr (POSITIONS == kSortedPositions) {
                 if (before < roles.position_walks)
                     walk<DT, GT, VEC, DROP>(p, before, warp, lane, shared);
@@ -471,27 +428,23 @@ cudaError_t launch_p(const RowSumArgs& a, const RowSumArgs& p, const Places& at,
 {
     Roles roles = {};
     const unsigned walks = walk_blocks(a);
-    unsigned fills = fill_blocks(a), positions = 0;
-    if (fills > 0 && a.scan && a.n <= kScan) {
-        roles.scan_rows = static_cast<int>((a.rows + kScans * 32 - 1) / (kScans * 32) * 32);
-        roles.scans = static_cast<unsigned>((a.rows + roles.scan_rows - 1) / roles.scan_rows);
-        fills = 0;
-    }
+    const unsigned fills = fill_blocks(a);
+    unsigned positions = 0;
     if (POSITIONS == kRunningPositions) {
         positions = blocks_for(static_cast<int64_t>(p.rows) * p.slabs);
-        roles.lead = roles.scans ? 0 : positions < kLead ? positions : kLead;
+        roles.lead = positions < kLead ? positions : kLead;
     } else if (POSITIONS == kSortedPositions) {
         roles.position_walks = walk_blocks(p);
         positions = roles.position_walks + fill_blocks(p);
     }
     const unsigned blocks = walks + fills + positions;
-    if (roles.scans + blocks == 0)
+    if (blocks == 0)
         return cudaSuccess;
     roles.positions = share_of(positions - roles.lead, blocks - roles.lead);
-    roles.walk_lead = walks < kWalkLead ? walks : kWalkLead;
+    roles.walk_lead = walks < kLead ? walks : kLead;
     roles.fill = share_of(fills, walks - roles.walk_lead + fills);
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(roles.scans + blocks);
+    c.gridDim = dim3(blocks);
     c.blockDim = dim3(kBlock);
     c.stream = s;
     cudaLaunchAttribute attr[1];
