@@ -374,6 +374,43 @@ def test_gradient_against_differences(ops):
     assert loss == (g.double() * e.double()).sum().item() + (pg.double() * pe.double()).sum().item()
 
 
+def test_offsets_beyond_32_bits(ops):
+    """Rows of a 40000 x 65536 matrix (2.6e9 elements): a lookup into it and the gradient from it, on columns of
+    the last slab; every sum is a small integer, so exact."""
+    n, D, V = 40000, 65536, 5
+    rng = np.random.default_rng(2)
+    tok = torch.from_numpy(rng.integers(0, V, n)).cuda()
+    layer = ops.TokenEmbedding(V, D, n)
+    table = torch.arange(V * D, device="cuda").remainder_(127).view(V, D).to(torch.bfloat16)
+    x = layer.forward(tok, table)
+    for lo in (0, 20000, n - 64):
+        assert torch.equal(x[lo:lo + 64], table[tok[lo:lo + 64]])
+    x.zero_()
+    x[:, -300:] = 1.0
+    x[n - 1, -1] = 3.0
+    grad = torch.empty(V, D, device="cuda")
+    layer.backward(tok, x, grad)
+    count = torch.bincount(tok, minlength=V).float()
+    want = count[:, None].repeat(1, 300)
+    want[tok[n - 1], -1] += 2.0
+    assert torch.equal(grad[:, -300:], want) and (grad[:, :-300] == 0).all()
+    assert layer.status() == 0
+
+
+def test_everything_dropped(ops):
+    """p == 1: zeros, whatever the values, and gradients that only copy their base."""
+    V, D, P, n = 40, 24, 8, 32
+    layer = ops.TokenEmbedding(V, D, n, positions=P)
+    drop = ops.Drop(1.0, 3, 4)
+    tok = torch.arange(n, device="cuda").view(4, 8) % 5
+    table = torch.full((V, D), float("inf"), device="cuda")
+    assert (layer.forward(tok, table, table[:P], drop=drop) == 0).all()
+    base, pos_base = _rand((V, D), "f32", 1).cuda(), _rand((P, D), "f32", 2).cuda()
+    grad, pos_grad = torch.empty_like(base), torch.empty_like(pos_base)
+    layer.backward(tok, table[:n].view(4, 8, D), grad, base=base, pos_grad=pos_grad, pos_base=pos_base, drop=drop)
+    assert torch.equal(grad, base) and torch.equal(pos_grad, pos_base)
+
+
 # ---- streams, graphs, layouts ------------------------------------------------------
 
 def test_other_streams_and_graphs(ops):
@@ -513,3 +550,21 @@ def test_failed_launch(ops, monkeypatch):
     with pytest.raises(ops.LionCubError, match="launch"):
         layer.forward(tok, table)
     assert torch.equal(layer.forward(tok, table, out_dtype=torch.float32), table[tok])
+
+
+@pytest.mark.parametrize("k", [1, 2])
+def test_failed_launch_of_a_gradient(ops, k, monkeypatch):
+    """Whichever launch of a backward call fails, the next call is whole."""
+    monkeypatch.setenv("LIONCUB_FAIL_LAUNCH", str(k))
+    V, D, n = 300, 40, 3000
+    layer = ops.TokenEmbedding(V, D, n)
+    monkeypatch.delenv("LIONCUB_FAIL_LAUNCH")
+    tok = torch.from_numpy(np.random.default_rng(k).integers(0, 9, n)).cuda()
+    dout = _rand((n, D), "f32", k).cuda()
+    grad, again = torch.empty(V, D, device="cuda"), torch.empty(V, D, device="cuda")
+    with pytest.raises(ops.LionCubError, match="launch"):
+        layer.backward(tok, dout, grad)
+    layer.backward(tok, dout, grad)
+    fresh = ops.TokenEmbedding(V, D, n)
+    fresh.backward(tok, dout, again)
+    assert torch.equal(grad, again)

@@ -18,7 +18,7 @@ def test_gradients_under_bounds_checks():
     __graft_entry__.build()
     lib = build.build(bounds_check=True)
     r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_gpu_embed.py", "-m", "gpu", "-x", "-q",
-                        "-p", "no:cacheprovider", "-k", "repeated or many_sequences or large_vocabulary or empty_batch or beyond_the_tables"],
+                        "-p", "no:cacheprovider", "-k", "repeated or many_sequences or large_vocabulary or empty_batch or beyond_the_tables or packed or flat_vector"],
                        cwd=ROOT, env={**os.environ, "LIONCUB_LIBRARY": lib}, capture_output=True, text=True, timeout=1200)
     tail = (r.stdout + r.stderr)[-3000:]
     assert r.returncode == 0, tail
