@@ -16,7 +16,12 @@
 //          blocks to arrive (an integer counter) adds the partials in order.  So
 //          units are alike in size however skewed the tokens are.
 //   fill   rows without a place.
-// Bound by memory: dout is read once and grad written once.
+// Large gradients without dropout are bound by memory (dout is read and grad
+// written once), small ones by the walks' latency, and those with dropout by the
+// integer instructions of the mask: about 86 a row and slab, of which drawing
+// takes 40.  Running positions read dout, and draw the mask, a second time.
+// Measured (bf16, 50257 rows): 16 x 1024 places of 1024 columns 32 us (137 MB),
+// 64 x 1024 of 2048 with positions and dropout 165 us (750 MB).
 #include <type_traits>
 
 #include "embed_device.cuh"

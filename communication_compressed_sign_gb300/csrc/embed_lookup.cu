@@ -5,7 +5,9 @@
 // tokens hit L2).  One warp takes several places on a slab of columns, so that
 // their rows are in flight together and the index arithmetic is shared.  Wide
 // rows with dropout are bound by instructions about as much as by memory, so
-// sums and rescalings are done two at a time (fp32 pairs).
+// sums and rescalings are done two at a time (fp32 pairs).  Measured (fp32 rows
+// of 2048 columns to bf16, 64 x 1024 places, 413 MB at least): 88 us with
+// dropout, 78 without; 8 x 1024 of 768 (27 MB): 7.3 and 5.7 us.
 #include "embed_device.cuh"
 
 namespace lc {
