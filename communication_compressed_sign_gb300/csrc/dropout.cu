@@ -42,6 +42,7 @@ __device__ __forceinline__ void drop_one(const DropoutArgs& a, int64_t e)
 template <typename XT, typename OT, bool DROP>
 __global__ void __launch_bounds__(kBlock) k_dropout_flat(const DropoutArgs a)
 {
+    wait_for_launch_before();
     const int64_t n = a.rows * a.cols;
     const int64_t e = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * 8;
     if (e + 8 > n) {
@@ -81,6 +82,7 @@ __global__ void __launch_bounds__(kBlock) k_dropout_rows(const DropoutArgs a, co
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     const int64_t row0 = quotient(unit, slabs) * kRows;
     const int slab = static_cast<int>(unit - row0 / kRows * slabs);
+    wait_for_launch_before();
     if (row0 >= a.rows)
         return;
     const Slab<VEC> cols(slab, lane, static_cast<int>(a.cols));
@@ -120,19 +122,15 @@ cudaError_t launch_t(const DropoutArgs& a, bool vec, cudaStream_t s)
     const bool dense = a.x.stride == a.cols && a.out.stride == a.cols && (!a.residual.data || a.residual.stride == a.cols);
     if (vec && dense) {
         const int64_t blocks = (a.rows * a.cols + kBlock * 8 - 1) / (kBlock * 8);
-        k_dropout_flat<XT, OT, DROP><<<static_cast<unsigned>(blocks), kBlock, 0, s>>>(a);
-        return cudaGetLastError();
+        return launch_programmatic(k_dropout_flat<XT, OT, DROP>, static_cast<unsigned>(blocks), kBlock, 0, s, a);
     }
     const bool wide = vec && a.cols % 8 == 0;
     const int slabs = slabs_of(a.cols, wide);
     const int64_t blocks = ((a.rows + kRows - 1) / kRows * slabs + kWarps - 1) / kWarps;
     if (blocks > INT_MAX)
         return cudaErrorInvalidConfiguration;
-    if (wide)
-        k_dropout_rows<XT, OT, true, DROP><<<static_cast<unsigned>(blocks), kBlock, 0, s>>>(a, slabs);
-    else
-        k_dropout_rows<XT, OT, false, DROP><<<static_cast<unsigned>(blocks), kBlock, 0, s>>>(a, slabs);
-    return cudaGetLastError();
+    return wide ? launch_programmatic(k_dropout_rows<XT, OT, true, DROP>, static_cast<unsigned>(blocks), kBlock, 0, s, a, slabs)
+                : launch_programmatic(k_dropout_rows<XT, OT, false, DROP>, static_cast<unsigned>(blocks), kBlock, 0, s, a, slabs);
 }
 
 template <typename XT, typename OT>

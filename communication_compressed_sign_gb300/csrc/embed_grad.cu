@@ -210,10 +210,6 @@ __device__ __forceinline__ void fill_rows(const RowSumArgs& a, int64_t row0, int
     }
 }
 
-// Programmatic launches: a kernel may start before the launch before it in the
-// stream has ended, and waits here until all of that is done and visible.
-__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The position of the n-th (from 0) set bit of a word that has more than n.
 __device__ __forceinline__ int nth_bit(unsigned word, int n)
 {
@@ -448,16 +444,7 @@ cudaError_t launch_p(const RowSumArgs& a, const RowSumArgs& p, const Places& at,
     roles.positions = share_of(positions - roles.lead, blocks - roles.lead);
     roles.walk_lead = walks < kLead ? walks : kLead;
     roles.fill = share_of(fills, walks - roles.walk_lead + fills);
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(blocks);
-    c.blockDim = dim3(kBlock);
-    c.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = attr;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, k_row_sums<DT, GT, VEC, DROP, POSITIONS>, a, p, at, roles);
+    return launch_programmatic(k_row_sums<DT, GT, VEC, DROP, POSITIONS>, blocks, kBlock, 0, s, a, p, at, roles);
 }
 
 template <typename DT, typename GT, bool VEC, bool DROP>

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kBlock) k_lookup(const LookupArgs a)
         in_sequence = group - sequences * step;
         first = sequences * places * step + in_sequence;
     }
+    wait_for_launch_before();
     if (first >= n)
         return;
     const Slab<VEC> cols(slab, lane, a.dim);
@@ -154,9 +155,8 @@ cudaError_t launch_p(LookupArgs a, cudaStream_t s)
         a.rounds *= 2;
     const int64_t places = PLACES * a.rounds;
     const int64_t groups = POSITIONS == kRunning ? (sequences + places - 1) / places * a.span : (a.at.n + places - 1) / places;
-    k_lookup<TT, OT, VEC, DROP, PLACES, POSITIONS>
-        <<<static_cast<unsigned>((groups * a.slabs + kWarps - 1) / kWarps), kBlock, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_programmatic(k_lookup<TT, OT, VEC, DROP, PLACES, POSITIONS>,
+                               static_cast<unsigned>((groups * a.slabs + kWarps - 1) / kWarps), kBlock, 0, s, a);
 }
 
 template <typename TT, typename OT, bool VEC, bool DROP>

@@ -117,9 +117,9 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     for (int k = tid; k < kWarps * width / 4; k += BLOCK)
         reinterpret_cast<int4*>(count)[k] = make_int4(0, 0, 0, 0);
     count += warp * width;
-    // what came before in the stream is done and visible; then the row sums may start beside this
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+    // what came before in the stream is done; then the row sums may start beside this, and rely on that
+    wait_for_launch_before();
+    let_next_launch_start();
 
     const int64_t n = t.at.n;
     const int64_t slice = (n + BLOCK - 1) / BLOCK * 32;
@@ -262,17 +262,7 @@ cudaError_t launch_block(const SortArgs& a, int blocks, int width, cudaStream_t 
         if (e != cudaSuccess)
             return e;
     }
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(static_cast<unsigned>(blocks));
-    c.blockDim = dim3(BLOCK);
-    c.dynamicSmemBytes = shared;
-    c.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = attr;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, k_sort<BLOCK>, a);
+    return launch_programmatic(k_sort<BLOCK>, static_cast<unsigned>(blocks), BLOCK, shared, s, a);
 }
 
 }  // namespace
