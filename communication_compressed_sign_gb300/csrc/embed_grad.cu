@@ -349,16 +349,14 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
     if (row >= a.rows)
         return;
     const int64_t place0 = row - at.first;
-    if (place0 < 0 || place0 >= at.seq_len || place0 >= at.n) {
-        if (a.base.data != a.grad.data)
-            fill_row<GT, VEC>(a, row, slab * kSlabCols<VEC>, min((slab + 1) * kSlabCols<VEC>, a.dim), lane);
-        return;
-    }
+    const bool in_batch = place0 >= 0 && place0 < at.seq_len && place0 < at.n;
+    bool any = false;
     Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared);
-    for (int64_t p0 = place0; p0 < at.n; p0 += 32 * at.seq_len) {
+    for (int64_t p0 = place0; in_batch && p0 < at.n; p0 += 32 * at.seq_len) {
         const int64_t mine = p0 + lane * at.seq_len;
         const unsigned there = __ballot_sync(kAll, mine < at.n && token_at(at, mine, nullptr) >= 0);
         const int here = __popc(there);
+        any |= here > 0;
         const int32_t my_place = static_cast<int32_t>(p0 + nth_bit(there, lane) * at.seq_len);  // lane l: the l-th there
 #pragma unroll 1
         for (int q = 0; q < here; q += kInFlight) {
@@ -377,7 +375,10 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
             }
         }
     }
-    w.finish(row);
+    if (any)
+        w.finish(row);
+    else if (a.base.data != a.grad.data)
+        fill_row<GT, VEC>(a, row, slab * kSlabCols<VEC>, min((slab + 1) * kSlabCols<VEC>, a.dim), lane);
 }
 
 // a: the table whose places are sorted; p: the positions' table.

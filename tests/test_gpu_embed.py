@@ -374,6 +374,29 @@ def test_gradient_against_differences(ops):
     assert loss == (g.double() * e.double()).sum().item() + (pg.double() * pe.double()).sum().item()
 
 
+@pytest.mark.parametrize("B,S,packed", [(3, 16, False), (200, 16, False), (3, 16, True)])
+def test_rows_without_a_place_keep_their_bits(ops, B, S, packed):
+    """A base row without a place, -0 and NaN included, is left (in place) or copied bit for bit: rows outside the
+    batch, and positions whose places are all empty."""
+    V, D, P = 50, 24, 20
+    tok = torch.full((B, S), -1, dtype=torch.int64, device="cuda")
+    tok[:, ::2] = 7
+    pos = torch.arange(S, device="cuda").repeat(B, 1) if packed else None
+    dout = torch.ones(B, S, D, device="cuda")
+    layer = ops.TokenEmbedding(V, D, B * S, positions=P)
+    odd = torch.tensor([-0.0, float("nan"), 0.0, float("inf")], device="cuda").repeat(6)
+    base, pos_base = odd.repeat(V, 1), odd.repeat(P, 1)
+    for in_place in (True, False):
+        g, pg = (base.clone(), pos_base.clone()) if in_place else (torch.ones_like(base), torch.ones_like(pos_base))
+        layer.backward(tok, dout, g, pos_grad=pg, base=g if in_place else base, pos_base=pg if in_place else pos_base,
+                       positions=pos)
+        rows = torch.arange(V) != 7
+        spots = (torch.arange(P) >= S) | (torch.arange(P) % 2 == 1)
+        assert torch.equal(g[rows.cuda()].view(torch.int32), base[rows.cuda()].view(torch.int32))
+        assert torch.equal(pg[spots.cuda()].view(torch.int32), pos_base[spots.cuda()].view(torch.int32))
+        assert (g[7, 2] == B * S // 2) and (pg[0, 2] == B)
+
+
 def test_offsets_beyond_32_bits(ops):
     """Rows of a 40000 x 65536 matrix (2.6e9 elements): a lookup into it and the gradient from it, on columns of
     the last slab; every sum is a small integer, so exact."""
@@ -506,12 +529,6 @@ def test_refusals(ops):
     with pytest.raises(err, match="pos_base"):
         layer.backward(tok, dout, grad, pos_base=wpe)
     both = torch.zeros(V + 8, D, device="cuda")
-    with pytest.raises(err, match="base"):
-        layer.backward(tok, dout, both[:V], base=both[8:])
-    with pytest.raises(err, match="overlap"):
-        layer.backward(tok, dout, both[:V], pos_grad=both[V - 4:V + 4])
-    with pytest.raises(err, match="overlaps"):
-        layer.backward(tok, both[:16].view(2, 8, D), both[:V])
     flat = ops.TokenEmbedding(V, D, 32)
     with pytest.raises(err, match="position"):
         flat.forward(tok, table, torch.zeros(0, D, device="cuda"))
