@@ -7,7 +7,7 @@
 // memory.  Dense, aligned matrices are one flat vector, 8 elements a thread;
 // others are taken by rows, a warp on a slab of columns.  Measured: 65536 x 2048
 // bf16 81 us (6.6 TB/s, 98 % of a measured copy), 8192 x 768 bf16 onto an fp32
-// residual 10.9 us (5.8 TB/s); rows of 771 bf16, 776 apart, 16384 of them 19.6 us
+// residual 10.4 us (6.0 TB/s); rows of 771 bf16, 776 apart, 16384 of them 19.6 us
 // (2.6 TB/s: scalar moves).
 #include <climits>
 

@@ -471,6 +471,9 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
         return fail(h, LIONCUB_ERR_ARG, "grad and pos_grad must have one type");
     if (pos_grad && overlap(*grad, h->vocab, *pos_grad, h->positions, h->dim))
         return fail(h, LIONCUB_ERR_ARG, "grad and pos_grad overlap");
+    if ((pos_grad && base && overlap(*base, h->vocab, *pos_grad, h->positions, h->dim)) ||
+        (pos_base && overlap(*pos_base, h->positions, *grad, h->vocab, h->dim)))
+        return fail(h, LIONCUB_ERR_ARG, "a gradient overlaps the other's base");
     lc::DropArgs d;
     bool on = false;
     rc = check_drop(h, drop, h->dim, &d, &on);

@@ -529,6 +529,16 @@ def test_refusals(ops):
     with pytest.raises(err, match="pos_base"):
         layer.backward(tok, dout, grad, pos_base=wpe)
     both = torch.zeros(V + 8, D, device="cuda")
+    with pytest.raises(err, match="base"):
+        layer.backward(tok, dout, both[:V], base=both[8:])
+    with pytest.raises(err, match="overlap"):
+        layer.backward(tok, dout, both[:V], pos_grad=both[V - 4:V + 4])
+    with pytest.raises(err, match="overlaps"):
+        layer.backward(tok, both[:16].view(2, 8, D), both[:V])
+    with pytest.raises(err, match="base"):
+        layer.backward(tok, dout, grad, base=both[:V], pos_grad=both[:P])
+    with pytest.raises(err, match="base"):
+        layer.backward(tok, dout, both[:V], pos_grad=wpe.clone(), pos_base=both[:P])
     flat = ops.TokenEmbedding(V, D, 32)
     with pytest.raises(err, match="position"):
         flat.forward(tok, table, torch.zeros(0, D, device="cuda"))
