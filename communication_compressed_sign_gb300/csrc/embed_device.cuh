@@ -24,19 +24,29 @@ __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddep
 __device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename Kernel, typename... Args>
-cudaError_t launch_programmatic(Kernel kernel, unsigned blocks, int threads, size_t shared, cudaStream_t s, const Args&... args)
+cudaError_t launch_programmatic_clusters(Kernel kernel, unsigned blocks, int threads, unsigned cluster, size_t shared, cudaStream_t s,
+                                         const Args&... args)
 {
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(blocks);
     c.blockDim = dim3(static_cast<unsigned>(threads));
     c.dynamicSmemBytes = shared;
     c.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     c.attrs = attr;
-    c.numAttrs = 1;
+    c.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_programmatic(Kernel kernel, unsigned blocks, int threads, size_t shared, cudaStream_t s, const Args&... args)
+{
+    return launch_programmatic_clusters(kernel, blocks, threads, 1, shared, s, args...);
 }
 
 // --- 8 consecutive, 16-byte aligned elements ------------------------------------------

@@ -321,6 +321,49 @@ def test_gradient_of_repeated_tokens(ops, n, spread):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), "the same call twice differs"
 
 
+@pytest.mark.parametrize("n,V,share", [(16384, 50257, 0.0), (16385, 50257, 0.0), (40000, 50257, 0.1), (40000, 8, 0.0),
+                                       (100000, 4000, 0.1), (131072, 50257, 0.04), (131072, 50257, 0.3), (131071, 700, 0.3),
+                                       (131073, 50257, 0.1), (300000, 130000, 0.05), (2200000, 5, 0.5)])
+@pytest.mark.parametrize("packed,index", [(False, torch.int64), (True, torch.int32)])
+def test_sums_of_large_repeated_batches(ops, n, V, share, packed, index):
+    """A share of the places holds one token and a few are empty; dout is small integers, so every sum is exact."""
+    g = np.random.default_rng(n + V)
+    tok = g.integers(0, V, n)
+    tok[g.random(n) < share] = min(V - 1, 777)
+    tok[g.random(n) < 0.01] = -1
+    P = 37
+    pos = g.integers(0, P, n) * (g.random(n) < 0.9)
+    dout = g.integers(-2, 3, (n, 4)).astype(np.float32)
+    layer = ops.TokenEmbedding(V, 4, n, positions=P)
+    tables = [torch.full((rows, 4), float("nan"), device="cuda") for rows in (V, P)]
+    layer.backward(torch.from_numpy(tok).to(index).cuda(), torch.from_numpy(dout).cuda(), tables[0],
+                   pos_grad=tables[1] if packed else None,
+                   positions=torch.from_numpy(pos).to(index).cuda() if packed else None)
+    there = tok >= 0
+    for got, key, rows in ((tables[0], tok, V), (tables[1], pos, P))[:2 if packed else 1]:
+        want = np.stack([np.bincount(key[there], dout[there, c], rows) for c in range(4)], 1)
+        assert np.array_equal(got.cpu().numpy(), want)
+    assert layer.status() == 0
+    layer.close()
+
+
+@pytest.mark.parametrize("n", [3000, 12000, 40000, 140000])
+def test_short_sums_run_in_the_places_order(ops, n):
+    """Up to four places of a token are added one after the other in fp32."""
+    V = 50257
+    g = np.random.default_rng(n)
+    tok = (g.random(n) ** 2 * V).astype(np.int64)
+    dout = g.standard_normal((n, 5)).astype(np.float32)
+    layer = ops.TokenEmbedding(V, 5, n)
+    got = torch.empty(V, 5, device="cuda")
+    layer.backward(torch.from_numpy(tok).cuda(), torch.from_numpy(dout).cuda(), got)
+    want = np.zeros((V, 5), np.float32)
+    np.add.at(want, tok, dout)
+    few = np.bincount(tok, minlength=V) <= 4
+    assert np.array_equal(got.cpu().numpy()[few], want[few])
+    layer.close()
+
+
 @pytest.mark.parametrize("S,P", [(1, 1), (1, 3), (2, 2), (100, 100), (7000, 7000)])
 def test_position_gradient_of_many_sequences(ops, S, P):
     B = 7000 // S
