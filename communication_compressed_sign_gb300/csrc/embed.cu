@@ -244,11 +244,12 @@ struct TableGradient {
 };
 
 // Positions that run with the place are summed without a sort while a position
-// has few places: each is one warp's work, and a longer one would be a long
-// serial sum on few warps.  (Whole gradients of 768 columns: 128 sequences of
-// 1024 127.8 us without a sort and 173 with, 160 of 64 45.7 and 39.5, 256 of 256
-// 135 and 98.5, 1024 of 64 247 and 98.)
-constexpr int64_t kRunning = 128;
+// has few places, since a block at most adds those of a slab.  (Whole gradients of
+// 768 columns, microseconds without and with a sort: 128 sequences of 16 19.0 and
+// 22.2, of 1024 121 and 149; 1024 of 16 43.1 and 42.8, of 64 80.7 and 87.8, of 256
+// 258 and 337; 2048 of 16 80 and 57, of 32 137 and 87.)
+constexpr int64_t kRunning = 1024;
+
 lc::SortTask sort_task(lioncub_embed_t h, const lc::Places& at, const TableGradient& g)
 {
     lc::SortTask t{};

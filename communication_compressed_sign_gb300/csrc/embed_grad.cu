@@ -21,7 +21,8 @@
 // integer instructions of the mask: about 86 a row and slab, of which drawing
 // takes 40.  Running positions read dout, and draw the mask, a second time.
 // Measured (bf16, 50257 rows): 16 x 1024 places of 1024 columns 32 us (137 MB),
-// 64 x 1024 of 2048 with positions and dropout 165 us (750 MB).
+// 64 x 1024 of 2048 with positions and dropout 163 us (750 MB).
+#include <algorithm>
 #include <type_traits>
 
 #include "embed_device.cuh"
@@ -34,6 +35,13 @@ constexpr int kWarps = kBlock / 32;
 constexpr int kInFlight = 4;           // rows of dout a warp loads before it adds them
 constexpr int kFillRows = 8;           // rows of grad a fill warp looks at
 constexpr unsigned kLead = 152 * 4;    // blocks the SMs hold: how many of a kind go ahead of the mix
+// A running position of more sequences than kWay is shared by up to eight warps
+// of a block, while all of them fit the SMs at once: its places are added one
+// after the other by a warp.  (Whole gradients of 768 columns, microseconds: 128
+// sequences of 64 by one warp 38.4, shared above 8, 16, 32 and 64 sequences 26.1,
+// 26.1, 24.7 and 25.2; 64 of 16 23.1, then 19.6, 18.0, 18.0 and 23.6.  128 of 1024,
+// which fill the SMs, 121, and 124 if shared all the same.)
+constexpr int64_t kWay = 32;
 constexpr int kJoinLog = 4, kJoin = 1 << kJoinLog;  // partials of a group of the gathering tree
 constexpr int kJoinBits = kJoinLog + 1;             // counter bits of a level: 12 levels, 2^30 places need 6
 
@@ -236,6 +244,8 @@ struct Roles {
     uint64_t fill;       // share of fill blocks among walks and fills, likewise
     unsigned walk_lead;       // walk blocks in front of the mix of walks and fills
     unsigned position_walks;  // sorted positions: walks before fills
+    int log_ways;             // running positions: warps of a row and slab
+    int64_t way;              // and the places of a warp's sequences
     __host__ __device__ __forceinline__ unsigned positions_before(unsigned block) const
     {
         return block <= lead ? block : lead + static_cast<unsigned>(((block - lead) * positions) >> 32);
@@ -253,6 +263,7 @@ template <bool VEC, bool DROP>
 struct WalkShared {
     typename SlabMask<VEC>::Shared mask[DROP ? kWarps : 1];
     float4 sums[kWarps][2][2][32];
+    bool any[kWarps];  // running positions: whether a warp's part has a place
     __device__ __forceinline__ typename SlabMask<VEC>::Shared* of(int warp) { return &mask[DROP ? warp : 0]; }
 };
 
@@ -339,22 +350,23 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, unsigned index, int wa
 }
 
 // Positions that run with the place, first + i % seq_len: row q's places are
-// q - first, q - first + seq_len, ... and need no sort.  One row on one slab.
+// q - first, q - first + seq_len, ... and need no sort.  One row on one slab,
+// `ways` warps of a block a part of the sequences each.
 template <typename DT, typename GT, bool VEC, bool DROP>
-__device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& at, int64_t unit, int lane,
-                                            typename SlabMask<VEC>::Shared* shared)
+__device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& at, const Roles& roles, int64_t unit, int warp, int lane,
+                                            WalkShared<VEC, DROP>& shared)
 {
+    const int part = warp & ((1 << roles.log_ways) - 1);
+    unit >>= roles.log_ways;
     const int64_t row = quotient(unit, a.slabs);
     const int slab = static_cast<int>(unit - row * a.slabs);
-    if (row >= a.rows)
-        return;
-    const int64_t place0 = row - at.first;
-    const bool in_batch = place0 >= 0 && place0 < at.seq_len && place0 < at.n;
+    const int64_t place0 = row - at.first, from = place0 + part * roles.way, until = min(from + roles.way, static_cast<int64_t>(at.n));
+    const bool in_batch = row < a.rows && place0 >= 0 && place0 < at.seq_len;
     bool any = false;
-    Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared);
-    for (int64_t p0 = place0; in_batch && p0 < at.n; p0 += 32 * at.seq_len) {
+    Walker<DT, GT, VEC, DROP> w(a, slab, lane, shared.of(warp));
+    for (int64_t p0 = from; in_batch && p0 < until; p0 += 32 * at.seq_len) {
         const int64_t mine = p0 + lane * at.seq_len;
-        const unsigned there = __ballot_sync(kAll, mine < at.n && token_at(at, mine, nullptr) >= 0);
+        const unsigned there = __ballot_sync(kAll, mine < until && token_at(at, mine, nullptr) >= 0);
         const int here = __popc(there);
         any |= here > 0;
         const int32_t my_place = static_cast<int32_t>(p0 + nth_bit(there, lane) * at.seq_len);  // lane l: the l-th there
@@ -375,6 +387,22 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
             }
         }
     }
+    if (roles.log_ways > 0) {  // the parts together, in order
+        if (part > 0)
+            w.put(shared.sums[warp][0], lane);
+        if (lane == 0)
+            shared.any[warp] = any;
+        __syncthreads();
+        if (part > 0)
+            return;
+#pragma unroll 1
+        for (int other = warp + 1; other < warp + (1 << roles.log_ways); ++other) {
+            any |= shared.any[other];
+            w.add_group(shared.sums[other][0][0][lane], shared.sums[other][0][1][lane]);
+        }
+    }
+    if (row >= a.rows)
+        return;
     if (any)
         w.finish(row);
     else if (a.base.data != a.grad.data)
@@ -394,7 +422,7 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
         if (roles.positions_before(block + 1) != before) {
             const int64_t unit = static_cast<int64_t>(before) * kWarps + warp;
             if constexpr (POSITIONS == kRunningPositions)
-                running_row<DT, GT, VEC, DROP>(p, at, unit, lane, shared.of(warp));
+                running_row<DT, GT, VEC, DROP>(p, at, roles, unit, warp, lane, shared);
             wait_for_launch_before();  // at the end too: the launch after this one relies on it
             if constexpr (POSITIONS == kSortedPositions) {
                 if (before < roles.position_walks)
@@ -433,7 +461,11 @@ cudaError_t launch_p(const RowSumArgs& a, const RowSumArgs& p, const Places& at,
     const unsigned fills = fill_blocks(a);
     unsigned positions = 0;
     if (POSITIONS == kRunningPositions) {
-        positions = blocks_for(static_cast<int64_t>(p.rows) * p.slabs);
+        const int64_t sequences = (at.n + at.seq_len - 1) / at.seq_len, used = std::min<int64_t>(at.seq_len, at.n) * p.slabs;
+        while (roles.log_ways < 3 && sequences >> roles.log_ways > kWay && used << (roles.log_ways + 1) <= kLead * kWarps)
+            ++roles.log_ways;
+        roles.way = ((sequences - 1) >> roles.log_ways) * at.seq_len + at.seq_len;
+        positions = blocks_for((static_cast<int64_t>(p.rows) * p.slabs) << roles.log_ways);
         roles.lead = positions < kLead ? positions : kLead;
     } else if (POSITIONS == kSortedPositions) {
         roles.position_walks = walk_blocks(p);

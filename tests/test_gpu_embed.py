@@ -371,6 +371,35 @@ def test_position_gradient_of_many_sequences(ops, S, P):
     _gradient(ops, tok, None, 300, 40, P, "bf16", "f32")
 
 
+@pytest.mark.parametrize("Q,S", [(32, 5), (33, 5), (64, 1), (65, 7), (129, 16), (257, 3), (1000, 9), (1024, 2), (1025, 2),
+                                 (40, 3000)])
+@pytest.mark.parametrize("D,dtype", [(4, torch.float32), (264, torch.bfloat16), (771, torch.bfloat16), (24, torch.float32)])
+@pytest.mark.parametrize("mode", ["fresh", "in place"])
+def test_running_positions_of_repeated_sequences(ops, Q, S, D, dtype, mode):
+    """Positions shared by several warps: the last sequence is cut short, a few places, two whole positions and the
+    whole first quarter of another are empty; dout is small integers, so every fp32 sum is exact."""
+    g = np.random.default_rng(Q * S + D)
+    n, P, first, V = Q * S - S // 2, S + 11, 3, 13
+    tok = g.integers(0, V, n)
+    tok[g.random(n) < 0.1] = -1
+    spot = np.arange(n) % S
+    if S > 4:
+        tok[(spot == 1) | (spot == 4) | ((spot == 2) & (np.arange(n) < n // 4))] = -1
+    dout = g.integers(-2, 3, (n, D)).astype(np.float32)
+    base = g.integers(-3, 4, (P, D)).astype(np.float32)
+    layer = ops.TokenEmbedding(V, D, n, positions=P)
+    grad = torch.empty(V, D, device="cuda")
+    pos_grad = torch.from_numpy(base).cuda() if mode == "in place" else torch.full((P, D), float("nan"), device="cuda")
+    layer.backward(torch.from_numpy(tok).cuda(), torch.from_numpy(dout).to(dtype).cuda(), grad, pos_grad=pos_grad,
+                   seq_len=S, first_position=first, pos_base=pos_grad if mode == "in place" else None)
+    want = base.astype(np.float64) if mode == "in place" else np.zeros((P, D))
+    there = tok >= 0
+    np.add.at(want, first + spot[there], dout[there])
+    assert np.array_equal(pos_grad.cpu().numpy(), want)
+    assert layer.status() == 0
+    layer.close()
+
+
 def test_gradient_of_a_large_vocabulary(ops):
     V = 1 << 20
     tok = torch.tensor([[0, V - 1, V - 1, 1, 524288, 255, 256, 0, 131072, 77777]], device="cuda")
