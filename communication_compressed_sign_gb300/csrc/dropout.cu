@@ -7,8 +7,8 @@
 // memory.  Dense, aligned matrices are one flat vector, 8 elements a thread;
 // others are taken by rows, a warp on a slab of columns.  Measured: 65536 x 2048
 // bf16 81 us (6.6 TB/s, 98 % of a measured copy), 8192 x 768 bf16 onto an fp32
-// residual 10.4 us (6.0 TB/s); rows of 771 bf16, 776 apart, 16384 of them 19.6 us
-// (2.6 TB/s: scalar moves).
+// residual 10.4 us (6.0 TB/s); rows of 771 bf16, 776 apart, 16384 of them 15.6 us
+// (3.2 TB/s: scalar moves).
 #include <climits>
 
 #include "embed_device.cuh"
@@ -96,6 +96,8 @@ __global__ void __launch_bounds__(kBlock) k_dropout_rows(const DropoutArgs a, co
         if (a.residual.data)
             res[u].load(cols, a.residual.data, i * a.residual.stride);
     }
+    if (DROP)
+        mask.template draw<kRows>(static_cast<int>(min(a.rows - row0, static_cast<int64_t>(kRows))), [&](int u) { return row0 + u; });
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
         const int64_t i = row0 + u;
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kBlock) k_dropout_rows(const DropoutArgs a, co
         float x[N];
         in[u].unpack(x);
         if constexpr (DROP)
-            mask.row(static_cast<uint32_t>(i), [&](int k, bool keep) { x[k] = dropped(a.drop, x[k], keep); });
+            mask.row(u, static_cast<uint32_t>(i), [&](int k, bool keep) { x[k] = dropped(a.drop, x[k], keep); });
         if (a.residual.data) {
             float y[N];
             res[u].unpack(y);

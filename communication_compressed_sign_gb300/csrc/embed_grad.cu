@@ -65,10 +65,10 @@ struct Walker {
         for (int k = 0; k < N; ++k)
             sum[k] = 0.0f;
     }
-    __device__ __forceinline__ void add(const SlabGroup<DT, VEC>& x, uint32_t i)
+    __device__ __forceinline__ void add(const SlabGroup<DT, VEC>& x, int u, uint32_t i)
     {
         if constexpr (DROP && sizeof(DT) == 2) {
-            mask.add(i, x, sum);
+            mask.add(u, i, x, sum);
         } else if constexpr (VEC && sizeof(DT) == 2) {
             const uint32_t w[4] = {x.g.raw.x, x.g.raw.y, x.g.raw.z, x.g.raw.w};
 #pragma unroll
@@ -82,7 +82,7 @@ struct Walker {
             float y[N];
             x.unpack(y);
             if constexpr (DROP) {
-                mask.row(i, [&](int k, bool keep) {
+                mask.row(u, i, [&](int k, bool keep) {
                     if (keep)
                         sum[k] = __fadd_rn(sum[k], y[k]);
                 });
@@ -312,6 +312,8 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, unsigned index, int wa
                 place[u] = __shfl_sync(kAll, entry.x, min(q + u, here - 1));
                 x[u].load(w.cols, a.dout.data, static_cast<uint32_t>(place[u]) * a.dout.stride);
             }
+            if (DROP)
+                w.mask.template draw<kInFlight>(here - q, [&](int u) { return place[u]; });
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {
                 if (q + u >= here)
@@ -321,7 +323,7 @@ __device__ __forceinline__ void walk(const RowSumArgs& a, unsigned index, int wa
                     w.clear();
                     current = __shfl_sync(kAll, entry.y, q + u);
                 }
-                w.add(x[u], place[u]);
+                w.add(x[u], u, place[u]);
             }
         }
         if (part == 1)
@@ -379,11 +381,13 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
                 place[u] = __shfl_sync(kAll, my_place, min(q + u, here - 1));
                 x[u].load(w.cols, a.dout.data, static_cast<uint32_t>(place[u]) * a.dout.stride);
             }
+            if (DROP)
+                w.mask.template draw<kInFlight>(here - q, [&](int u) { return place[u]; });
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {
                 if (q + u >= here)
                     break;
-                w.add(x[u], place[u]);
+                w.add(x[u], u, place[u]);
             }
         }
     }

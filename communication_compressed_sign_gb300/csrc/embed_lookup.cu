@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kBlock) k_lookup(const LookupArgs a)
         }
         if (round + 1 < a.rounds)
             fetch(round + 1);
+        if (DROP)
+            mask.template draw<PLACES>(PLACES, [&](int u) { return first + (round * PLACES + u) * step; });
 #pragma unroll
         for (int u = 0; u < PLACES; ++u) {
             const uint64_t place = first + static_cast<uint64_t>(round * PLACES + u) * step;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kBlock) k_lookup(const LookupArgs a)
             }
             if constexpr (DROP) {
                 scale_pairs(y, a.drop.rescale);
-                mask.row(i, [&](int k, bool keep) { y[k] = keep ? y[k] : 0.0f; });
+                mask.row(u, i, [&](int k, bool keep) { y[k] = keep ? y[k] : 0.0f; });
             }
             store_slab<OT, VEC>(cols, a.out.data, i * a.out.stride, y);
         }
