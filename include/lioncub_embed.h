@@ -131,7 +131,9 @@ LIONCUB_API int lioncub_embed_forward(lioncub_embed_t h, const lioncub_token_bat
  * base (NULL: zeros) and grad have one type; base->data == grad->data (then
  * with the same stride) adds in place and touches only the rows of the
  * batch's tokens.  pos_grad (NULL: not wanted) and pos_base likewise, of
- * grad's type.  drop: as in the forward call.  Errors as the forward call.
+ * grad's type.  The two gradients may overlap neither each other, nor dout,
+ * nor a base except as above.  drop: as in the forward call.  Errors as the
+ * forward call.
  */
 LIONCUB_API int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, const lioncub_rows* dout,
                                        const lioncub_rows* base, const lioncub_rows* grad,
