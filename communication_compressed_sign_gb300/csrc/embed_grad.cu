@@ -134,6 +134,7 @@ struct Walker {
             uint64_t before = 0;
             if (lane == 0)
                 before = arrive(&a.arrived[slot(group << scale << kJoinLog) * a.slabs + slab], 1ull << (kJoinBits * level));
+            __syncwarp();  // what lane 0's arrival acquired is the other lanes' too
             before = __shfl_sync(kAll, before, 0);
             if ((before >> (kJoinBits * level) & ((1u << kJoinBits) - 1)) != members - 1)
                 return false;
@@ -146,9 +147,10 @@ struct Walker {
         }
         return true;
     }
-    // Counts an arrival: what the warp wrote before is visible to whom the
-    // counter tells of it (release, cumulative over the warp's barrier), and
-    // what it tells of is visible here (acquire).
+    // Counts an arrival, by one lane between two barriers of its warp: what the
+    // warp wrote before the first is visible to whom the counter tells of it
+    // (release), and what it tells of is visible to the warp after the second
+    // (acquire).  A shuffle would hand on the count, not the order of memory.
     static __device__ __forceinline__ uint64_t arrive(uint64_t* counter, uint64_t one)
     {
         uint64_t before;
