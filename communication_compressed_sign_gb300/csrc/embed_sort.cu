@@ -136,7 +136,7 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     for (int k = tid; k < kWarps * width / 4; k += BLOCK)
         reinterpret_cast<int4*>(count)[k] = make_int4(0, 0, 0, 0);
     count += warp * width;
-    // what came before in the stream is done; then the row sums may start beside this, and rely on that
+    // what came before in the stream is done; then the row sums may start beside this
     wait_for_launch_before();
     let_next_launch_start();
 

@@ -43,3 +43,39 @@ def test_joined_sums_on_every_lane(ops, n, D, dtype):
         assert torch.equal(grad.double(), _sums(tok, dout, V)), seed
     assert layer.status() == 0
     layer.close()
+
+
+@pytest.mark.parametrize("B,S,D", [(1, 1024, 768), (5, 300, 771), (64, 64, 256)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_running_positions_of_inputs_just_written(ops, B, S, D, captured):
+    """Each pass writes its tokens and dout on the stream right before the gradient reads them."""
+    V, P, n = 500, S, B * S
+    layer = ops.TokenEmbedding(V, D, n, positions=P)
+    tokens = [torch.randint(-1, V, (B, S), device="cuda") for _ in range(2)]
+    douts = [_integers((n, D), torch.bfloat16, seed) for seed in range(2)]
+    place = torch.arange(n, device="cuda") % S
+    want = [(_sums(t.view(-1), x, V), _sums(torch.where(t.view(-1) < 0, -1, place), x, P)) for t, x in zip(tokens, douts)]
+    tok, dout = torch.empty_like(tokens[0]), torch.empty_like(douts[0])
+    grad, pos_grad = torch.empty(V, D, device="cuda"), torch.empty(P, D, device="cuda")
+
+    def one(k):
+        grad.fill_(float("nan"))
+        pos_grad.fill_(float("nan"))
+        tok.copy_(tokens[k])
+        dout.copy_(douts[k])
+        layer.backward(tok, dout.view(B, S, D), grad, pos_grad=pos_grad)
+
+    passes = [lambda: one(0), lambda: one(1)]
+    if captured:
+        one(0)
+        graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+        for k, graph in enumerate(graphs):
+            with torch.cuda.graph(graph):
+                one(k)
+        passes = [graph.replay for graph in graphs]
+    for k in range(20):
+        passes[k % 2]()
+        got = grad.clone(), pos_grad.clone()
+        assert all(torch.equal(a.double(), b) for a, b in zip(got, want[k % 2])), k
+    assert layer.status() == 0
+    layer.close()
