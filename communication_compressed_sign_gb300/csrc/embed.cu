@@ -224,6 +224,27 @@ int check_places(lioncub_embed_t h, const lioncub_token_batch* b, bool positions
     return LIONCUB_OK;
 }
 
+// A result must not share bytes with the ids that the call reads: they would change
+// under it.
+int check_apart(lioncub_embed_t h, const char* name, const lioncub_rows& m, int64_t rows, const lioncub_token_batch& b,
+                bool positions_used)
+{
+    if (rows == 0 || b.n == 0)
+        return LIONCUB_OK;
+    const uintptr_t m0 = reinterpret_cast<uintptr_t>(m.data), step = m.stride * element_size(m.type);
+    const uintptr_t width = h->dim * element_size(m.type), m1 = m0 + (rows - 1) * step + width;
+    const uintptr_t bytes = b.n * (b.index_type == LIONCUB_INDEX_I64 ? 8 : 4);
+    for (const void* ids : {b.tokens, positions_used ? b.positions : nullptr}) {
+        const uintptr_t i0 = reinterpret_cast<uintptr_t>(ids);
+        if (!ids || i0 >= m1 || i0 + bytes <= m0)
+            continue;
+        // begins before a row's end, or reaches the next row
+        if (i0 < m0 || (i0 - m0) % step < width || (i0 - m0) % step + bytes > step)
+            return fail(h, LIONCUB_ERR_ARG, "%s overlaps the tokens or positions", name);
+    }
+    return LIONCUB_OK;
+}
+
 int check_device(lioncub_embed_t h)
 {
     int dev = -1;
@@ -431,8 +452,10 @@ int lioncub_embed_forward(lioncub_embed_t h, const lioncub_token_batch* batch, c
     if (overlap(*out, batch->n, *table, h->vocab, h->dim) ||
         (pos_table && overlap(*out, batch->n, *pos_table, h->positions, h->dim)))
         return fail(h, LIONCUB_ERR_ARG, "out overlaps a table");
+    rc = check_apart(h, "out", *out, batch->n, *batch, pos_table != nullptr);
     bool on = false;
-    rc = check_drop(h, drop, h->dim, &a.drop, &on);
+    if (rc == LIONCUB_OK)
+        rc = check_drop(h, drop, h->dim, &a.drop, &on);
     if (rc == LIONCUB_OK)
         rc = check_device(h);
     if (rc != LIONCUB_OK)
@@ -475,9 +498,13 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
     if ((pos_grad && base && overlap(*base, h->vocab, *pos_grad, h->positions, h->dim)) ||
         (pos_base && overlap(*pos_base, h->positions, *grad, h->vocab, h->dim)))
         return fail(h, LIONCUB_ERR_ARG, "a gradient overlaps the other's base");
+    rc = check_apart(h, "grad", *grad, h->vocab, *batch, pos_grad != nullptr);
+    if (rc == LIONCUB_OK && pos_grad)
+        rc = check_apart(h, "pos_grad", *pos_grad, h->positions, *batch, true);
     lc::DropArgs d;
     bool on = false;
-    rc = check_drop(h, drop, h->dim, &d, &on);
+    if (rc == LIONCUB_OK)
+        rc = check_drop(h, drop, h->dim, &d, &on);
     if (rc == LIONCUB_OK)
         rc = check_device(h);
     if (rc != LIONCUB_OK)

@@ -117,7 +117,8 @@ LIONCUB_API int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_
  * out (n x dim) from table (vocab x dim) and, unless it is NULL, pos_table
  * (positions x dim, of table's type).  drop may be NULL.  One launch; a single
  * token of a sequence that is being generated is a batch with n == 1 and its
- * place in first_position.  out must not overlap the tables.  Errors:
+ * place in first_position.  out must not overlap the tables, the tokens or
+ * the positions it reads.  Errors:
  * ERR_ARG, ERR_ALIGN (a pointer that is not aligned to its element), ERR_STATE
  * (another device is current), ERR_CUDA.
  */
@@ -132,7 +133,7 @@ LIONCUB_API int lioncub_embed_forward(lioncub_embed_t h, const lioncub_token_bat
  * with the same stride) adds in place and touches only the rows of the
  * batch's tokens.  pos_grad (NULL: not wanted) and pos_base likewise, of
  * grad's type.  The two gradients may overlap neither each other, nor dout,
- * nor a base except as above.  drop: as in the forward call.  Errors as the
+ * the tokens or the positions, nor a base except as above.  drop: as in the forward call.  Errors as the
  * forward call.
  */
 LIONCUB_API int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, const lioncub_rows* dout,

@@ -1,0 +1,55 @@
+"""What calls of the input-layer operators refuse, report and share: overlaps
+with the places, empty places' positions, host threads, tensors that require a
+gradient, sequence lengths."""
+import pytest
+
+from tests.test_gpu_embed import _rand, ops  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def test_results_over_the_places_are_refused(ops):
+    """A result that shares bytes with the tokens or positions would change what the call still reads."""
+    V, D, P = 100, 16, 8
+    layer = ops.TokenEmbedding(V, D, 16, positions=P)
+    table, wpe = _rand((V, D), "f32", 1).cuda(), _rand((P, D), "f32", 2).cuda()
+    dout = torch.ones(2, 8, D, device="cuda")
+    free = torch.zeros(2, 8, dtype=torch.int64, device="cuda")
+    for at in (0, 40, 127):  # the first, an inner and the last 8 bytes of the 16 x 16 fp32 result
+        buffer = torch.zeros(1024, dtype=torch.int64, device="cuda")
+        over = buffer[at:at + 16].view(2, 8)
+        out = buffer.view(torch.float32)[:256].view(2, 8, D)
+        with pytest.raises(ops.LionCubError, match="out overlaps"):
+            layer.forward(over, table, out=out)
+        with pytest.raises(ops.LionCubError, match="out overlaps"):
+            layer.forward(free, table, wpe, positions=over, out=out)
+        grad = buffer.view(torch.float32)[:V * D].view(V, D)
+        with pytest.raises(ops.LionCubError, match="grad overlaps"):
+            layer.backward(over, dout, grad)
+        spare = torch.empty(V, D, device="cuda")
+        pos_grad = buffer.view(torch.float32)[:P * D].view(P, D)
+        where = buffer[at % 64:at % 64 + 16].view(2, 8)
+        with pytest.raises(ops.LionCubError, match="pos_grad overlaps"):
+            layer.backward(where, dout, spare, pos_grad=pos_grad)
+        with pytest.raises(ops.LionCubError, match="pos_grad overlaps"):
+            layer.backward(free, dout, spare, pos_grad=pos_grad, positions=where)
+        assert (buffer == 0).all()
+    layer.close()
+
+
+def test_places_beside_the_results_rows(ops):
+    """Tokens that lie right before or behind a result, or in the gap between two of its rows, share nothing with it."""
+    V, D = 50, 16
+    layer = ops.TokenEmbedding(V, D, 8)
+    table = _rand((V, D), "f32", 1).cuda()
+    want = torch.randint(0, V, (8,), dtype=torch.int32, device="cuda")
+    for at in (0, 8 + 16, 8 + 24 + 16, 8 + 7 * 24 + 16):
+        buffer = torch.zeros(8 + 8 * 24, dtype=torch.int32, device="cuda")
+        tok = buffer[at:at + 8]
+        tok.copy_(want)
+        out = buffer[8:].view(torch.float32).view(8, 24)[:, :D]
+        layer.forward(tok, table, out=out)
+        assert torch.equal(tok, want) and torch.equal(out, table[want.long()])
+    layer.close()
