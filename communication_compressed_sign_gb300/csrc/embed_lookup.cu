@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kBlock) k_lookup(const LookupArgs a)
         next_token = next_position = -1;
         if (lane < PLACES && place < n) {
             next_token = token_at(a.at, place, a.status);
-            if (POSITIONS == kGiven)
-                next_position = position_at(a.at, place, a.status);
+            if (POSITIONS == kGiven)  // an empty place's is loaded beside its token, but never an error
+                next_position = position_at(a.at, place, next_token >= 0 ? a.status : nullptr);
         }
     };
     fetch(0);

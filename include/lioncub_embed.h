@@ -25,7 +25,8 @@
  * like an empty place and sets LIONCUB_EMBED_STATUS_INDEX in the handle's
  * status word.  q_i is positions[i], or first_position + i % seq_len when
  * positions is NULL; an explicit position outside [0, positions) adds no
- * position row, has no position gradient, and sets the same status bit.
+ * position row, has no position gradient, and sets the same status bit.  The
+ * position of an empty place may be anything.
  *
  * Random numbers: SplitMix64 (Steele, Lea and Flood 2014) as a function of
  * (start, k): output number k (from 0) of the generator that starts at

@@ -1,9 +1,12 @@
 """What calls of the input-layer operators refuse, report and share: overlaps
 with the places, empty places' positions, host threads, tensors that require a
 gradient, sequence lengths."""
+
+import numpy as np
 import pytest
 
-from tests.test_gpu_embed import _rand, ops  # noqa: F401  (the fixture)
+from tests import embed_reference as ref
+from tests.test_gpu_embed import _check, _np, _rand, ops  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -52,4 +55,30 @@ def test_places_beside_the_results_rows(ops):
         out = buffer[8:].view(torch.float32).view(8, 24)[:, :D]
         layer.forward(tok, table, out=out)
         assert torch.equal(tok, want) and torch.equal(out, table[want.long()])
+    layer.close()
+
+
+@pytest.mark.parametrize("index", [torch.int64, torch.int32])
+@pytest.mark.parametrize("n", [6, 3000])  # one place a warp, and several
+def test_positions_of_empty_places_may_be_anything(ops, index, n):
+    """Both arrays padded alike, with -1 or with numbers beyond the table."""
+    V, P, D = 50, 10, 256
+    rng = np.random.default_rng(n)
+    tok, pos = rng.integers(0, V, n), rng.integers(0, P, n)
+    tok[1::3] = -1
+    pos[1::3] = np.where(np.arange(len(pos[1::3])) % 2, -1, P + 5)
+    t, q = (torch.from_numpy(v).to(index).cuda() for v in (tok, pos))
+    table, wpe, dout = _rand((V, D), "f32", 1), _rand((P, D), "f32", 2), _rand((n, D), "f32", 3)
+    layer = ops.TokenEmbedding(V, D, n, positions=P)
+    out = layer.forward(t, table.cuda(), wpe.cuda(), positions=q, out_dtype=torch.float32)
+    assert layer.status() == 0
+    want = torch.where(t[:, None] < 0, torch.zeros(1, device="cuda"),
+                       table.cuda()[t.long().clamp(min=0)] + wpe.cuda()[q.long().clamp(0, P - 1)])
+    assert torch.equal(out, want)
+    grad, pos_grad = torch.empty(V, D, device="cuda"), torch.empty(P, D, device="cuda")
+    layer.backward(t, dout.cuda(), grad, pos_grad=pos_grad, positions=q)
+    assert layer.status() == 0
+    token, position = ref.gradients(tok, V, P, _np(dout), 1.0, None, positions=pos)
+    for got, (exact, mag, count) in ((grad, token), (pos_grad, position)):
+        _check(got, exact, mag, count + 3, "f32")
     layer.close()
