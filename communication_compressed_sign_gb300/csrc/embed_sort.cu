@@ -374,10 +374,12 @@ cudaError_t launch_block(const SortArgs& a, int blocks, int width, cudaStream_t 
     constexpr int kWarps = BLOCK / 32;
     constexpr size_t kLists = sizeof(int) * kWarps * kList + (CLUSTERED ? sizeof(uint32_t) * kWarps * kShared : 0);
     const size_t shared = sizeof(int) * kWarps * width + kLists + sizeof(int2) * width;
-    static_assert(sizeof(int) * kWarps * kMaxOwned + kLists + sizeof(int2) * kMaxOwned <= 220 * 1024, "a block fits an SM");
+    constexpr size_t kMost = sizeof(int) * kWarps * kMaxOwned + kLists + sizeof(int2) * kMaxOwned;
+    static_assert(kMost <= 220 * 1024, "a block fits an SM");
     if (shared > 48 * 1024) {
+        // the kernel's limit, the same for every call: calls of other threads launch by it too
         const cudaError_t e =
-            cudaFuncSetAttribute(k_sort<BLOCK, CLUSTERED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+            cudaFuncSetAttribute(k_sort<BLOCK, CLUSTERED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
         if (e != cudaSuccess)
             return e;
     }

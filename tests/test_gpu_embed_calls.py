@@ -1,6 +1,7 @@
 """What calls of the input-layer operators refuse, report and share: overlaps
 with the places, empty places' positions, host threads, tensors that require a
 gradient, sequence lengths."""
+import threading
 
 import numpy as np
 import pytest
@@ -82,3 +83,47 @@ def test_positions_of_empty_places_may_be_anything(ops, index, n):
     for got, (exact, mag, count) in ((grad, token), (pos_grad, position)):
         _check(got, exact, mag, count + 3, "f32")
     layer.close()
+
+
+def _side_by_side(*work):
+    """Runs the functions in threads of their own; what they raised."""
+    raised = []
+
+    def go(f):
+        try:
+            f()
+        except Exception as e:  # noqa: BLE001
+            raised.append(e)
+
+    threads = [threading.Thread(target=go, args=(f,)) for f in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return raised
+
+
+def test_layers_of_different_sizes_in_two_threads(ops):
+    """Gradients of two layers whose sorts take different amounts of shared memory, from a host thread each."""
+    D, n, calls = 8, 64, 4000
+
+    def layer_of(V, seed):
+        layer, stream = ops.TokenEmbedding(V, D, n), torch.cuda.Stream()
+        tok = torch.randint(0, V, (n,), generator=torch.Generator().manual_seed(seed)).cuda()
+        dout, grad = torch.ones(n, D, device="cuda"), torch.zeros(V, D, device="cuda")
+        want = torch.zeros_like(grad).index_add_(0, tok, dout)
+        torch.cuda.synchronize()
+
+        def work():
+            for _ in range(calls):
+                layer.backward(tok, dout, grad, stream=stream)
+
+        return work, layer, grad, want
+
+    parts = [layer_of(1 << 20, 1), layer_of(600000, 2)]
+    raised = _side_by_side(*(p[0] for p in parts))
+    torch.cuda.synchronize()
+    assert not raised, raised[0]
+    for _, layer, grad, want in parts:
+        assert torch.equal(grad, want) and layer.status() == 0
+        layer.close()
