@@ -2,11 +2,14 @@
 // argument checks, the handle's workspace, launches and errors.
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
+#include <mutex>
 #include <new>
 
 #include "embed.h"
@@ -42,22 +45,35 @@ struct lioncub_embed_s {
 
     // fault injection (environment, read at create; 0 = off)
     int64_t fail_alloc_at = 0, alloc_count = 0;
-    int64_t fail_launch_at = 0, launch_count = 0;
+    int64_t fail_launch_at = 0;
+    std::atomic<int64_t> launch_count{0};
 
+    uint64_t number = 0;  // of the handles, from 1
+    std::mutex err_lock;  // lookups may fail in several threads
     char err[256] = "";
 };
 
 namespace {
 
-// Message of this thread's last failed call without a handle.
+std::atomic<uint64_t> g_handles{0};
+
+// Messages of this thread's last failed call without a handle, and of that on a
+// handle, whose number (not its address, which another may get) goes with it.
 thread_local char g_err[256] = "";
+thread_local char t_err[256] = "";
+thread_local uint64_t t_err_of = 0;
 
 int fail(lioncub_embed_t h, int code, const char* fmt, ...)
 {
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(h ? h->err : g_err, sizeof g_err, fmt, ap);
+    vsnprintf(h ? t_err : g_err, sizeof g_err, fmt, ap);
     va_end(ap);
+    if (h) {
+        t_err_of = h->number;
+        std::lock_guard<std::mutex> hold(h->err_lock);
+        std::memcpy(h->err, t_err, sizeof t_err);
+    }
     return code;
 }
 
@@ -372,7 +388,14 @@ extern "C" {
 
 const char* lioncub_embed_last_error(lioncub_embed_t h)
 {
-    return h ? h->err : g_err;
+    if (!h)
+        return g_err;
+    if (t_err_of != h->number) {
+        std::lock_guard<std::mutex> hold(h->err_lock);
+        std::memcpy(t_err, h->err, sizeof t_err);
+        t_err_of = 0;  // read anew next time
+    }
+    return t_err;
 }
 
 int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64_t positions, int64_t max_tokens,
@@ -395,6 +418,7 @@ int lioncub_embed_create(lioncub_embed_t* out, int64_t vocab, int64_t dim, int64
     lioncub_embed_t h = new (std::nothrow) lioncub_embed_s();
     if (!h)
         return fail(nullptr, LIONCUB_ERR_OOM, "no host memory for the handle");
+    h->number = ++g_handles;
     h->vocab = vocab;
     h->dim = dim;
     h->positions = positions;

@@ -46,7 +46,8 @@
  * synchronized outside create, and a call can be captured into a CUDA graph
  * (the seed and stream are then frozen in it).  A handle's workspace is used
  * by backward calls only; they must be ordered one after another (one stream,
- * or events between them).  Forward calls and dropout share nothing.
+ * or events between them), on the host too.  Forward calls and dropout share
+ * nothing and may be made by several host threads at once.
  * Return codes are those of lioncub.h.
  */
 #ifndef LIONCUB_EMBED_H
@@ -146,8 +147,10 @@ LIONCUB_API int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_ba
  * dst_dev (one int32 in device memory) on `stream`. */
 LIONCUB_API int lioncub_embed_status(lioncub_embed_t h, int32_t* dst_dev, lioncub_stream_t stream);
 
-/* Message of the handle's last error; h == NULL: of this thread's last failed
- * create or dropout call. */
+/* Message of this thread's last failed call on a handle where that was h, else of
+ * h's last failed call in any thread ("" if none); valid until this thread's next
+ * failed call or message.  h == NULL: of this thread's last failed create or
+ * dropout call. */
 LIONCUB_API const char* lioncub_embed_last_error(lioncub_embed_t h);
 
 /* Frees the handle and its workspace (NULL is a no-op); synchronizes. */

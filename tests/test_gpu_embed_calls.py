@@ -127,3 +127,53 @@ def test_layers_of_different_sizes_in_two_threads(ops):
     for _, layer, grad, want in parts:
         assert torch.equal(grad, want) and layer.status() == 0
         layer.close()
+
+
+def test_lookups_of_one_layer_in_several_threads(ops, monkeypatch):
+    """Lookups share nothing: every launch is counted once (one of them is made to fail), results are each call's own."""
+    V, D, threads, calls = 300, 64, 4, 2000
+    monkeypatch.setenv("LIONCUB_FAIL_LAUNCH", str(threads * calls))
+    layer = ops.TokenEmbedding(V, D, 64)
+    monkeypatch.delenv("LIONCUB_FAIL_LAUNCH")
+    table = _rand((V, D), "f32", 1).cuda()
+    tokens = [torch.randint(0, V, (64,), device="cuda") for _ in range(threads)]
+    outs = [torch.empty(64, D, device="cuda") for _ in range(threads)]
+    torch.cuda.synchronize()
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        for _ in range(calls):
+            layer.forward(tokens[k], table, out=outs[k], stream=stream)
+
+    raised = _side_by_side(*(lambda k=k: work(k) for k in range(threads)))
+    torch.cuda.synchronize()
+    assert len(raised) == 1 and "launch" in str(raised[0]), raised
+    for t, out in zip(tokens, outs):
+        assert torch.equal(out, table[t])
+    layer.close()
+
+
+def test_messages_are_each_threads_own(ops):
+    """What failed last in this thread, whatever failed on the handle elsewhere since; else what failed last."""
+    from communication_compressed_sign_gb300 import embed
+    L = embed.load()
+    layer = ops.TokenEmbedding(10, 8, 4)
+    other = ops.TokenEmbedding(10, 8, 4)
+    batch = embed.TokenBatch(None, None, 5, 1, 0, 0, 0)  # more places than the layer's
+    unknown = embed.TokenBatch(None, None, 0, 1, 0, 7, 0)
+
+    def fail(b):
+        import ctypes
+        assert L.lioncub_embed_forward(layer.h, ctypes.byref(b), None, None, None, None, None) != 0
+
+    message = lambda: L.lioncub_embed_last_error(layer.h).decode()  # noqa: E731
+    assert message() == ""
+    assert not _side_by_side(lambda: fail(batch))
+    assert "places" in message()  # a thread without a failure of its own reads the handle's
+    fail(batch)
+    seen = []
+    assert not _side_by_side(lambda: (fail(unknown), seen.append(message())))
+    assert "index type 7" in seen[0] and "places" in message()
+    assert L.lioncub_embed_last_error(other.h) == b""
+    layer.close()
+    other.close()
