@@ -7,7 +7,10 @@ rows, and dropout) with its gradient by sorted tokens; :func:`dropout` and
 (:class:`Drop`) and never store it.  As in :mod:`.lioncub`, the functions
 named ``lioncub_*`` keep the C names and raise :class:`LionCubError` with the
 library's message; the wrappers check tensors, pass their pointers through and
-allocate results with torch.
+allocate results with torch.  Results are not part of torch's autograd graph:
+gradients come from the backward functions, called by hand (or from a
+torch.autograd.Function of the caller's), and tensors that require a gradient
+are refused while torch records one.
 """
 from __future__ import annotations
 
@@ -163,6 +166,9 @@ def _rows(t, name, nrows, cols, device):
     kind = _row_types.get(t.dtype)
     if kind is None or t.get_device() != device:
         raise ValueError(f"{name} must be a bfloat16 or float32 tensor on cuda:{device}")
+    if t.requires_grad and _torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, but results are not part of torch's graph: "
+                         "call under torch.no_grad() or pass a detached tensor")
     if not t.dim() or t.size(-1) != cols or t.numel() != nrows * cols:
         raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(t.shape)})")
     if t.is_contiguous():

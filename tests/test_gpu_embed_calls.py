@@ -177,3 +177,26 @@ def test_messages_are_each_threads_own(ops):
     assert L.lioncub_embed_last_error(other.h) == b""
     layer.close()
     other.close()
+
+
+def test_tensors_that_require_a_gradient(ops):
+    """Results are not part of torch's graph, so while it records, such tensors are refused rather than losing their
+    gradient; without recording they are taken."""
+    V, D, P = 20, 16, 4
+    layer = ops.TokenEmbedding(V, D, 4, positions=P)
+    tok = torch.arange(4, device="cuda").view(1, 4)
+    free, leaf = torch.ones(V, D, device="cuda"), torch.ones(V, D, device="cuda", requires_grad=True)
+    wpe = torch.ones(P, D, device="cuda", requires_grad=True)
+    x = torch.ones(1, 4, D, device="cuda", requires_grad=True)
+    drop = ops.Drop(0.5, 1)
+    calls = [lambda: layer.forward(tok, leaf), lambda: layer.forward(tok, free, wpe), lambda: ops.dropout(x, drop),
+             lambda: ops.dropout(x.detach(), drop, residual=x), lambda: ops.dropout_backward(x, drop),
+             lambda: layer.backward(tok, x, free.clone()), lambda: layer.backward(tok, x.detach(), free.clone(), base=leaf)]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+    with torch.no_grad():
+        for call in calls:
+            call()
+    assert torch.equal(layer.forward(tok, leaf.detach(), out_dtype=torch.float32)[0], free[:4])
+    layer.close()
