@@ -224,8 +224,10 @@ int check_places(lioncub_embed_t h, const lioncub_token_batch* b, bool positions
     if (positions_used && h->positions == 0)
         return fail(h, LIONCUB_ERR_ARG, "the layer has no position rows");
     if (positions_used && !b->positions) {
+        if (b->seq_len < 1)
+            return fail(h, LIONCUB_ERR_ARG, "seq_len must be 1 or more for running positions (got %lld)", (long long)b->seq_len);
         const int64_t span = b->seq_len < b->n ? b->seq_len : b->n;
-        if (b->seq_len < 1 || b->first_position < 0 || b->first_position > h->positions - span)
+        if (b->first_position < 0 || b->first_position > h->positions - span)
             return fail(h, LIONCUB_ERR_ARG, "positions %lld..%lld are outside the table's %lld", (long long)b->first_position,
                         (long long)(b->first_position + span - 1), (long long)h->positions);
     }

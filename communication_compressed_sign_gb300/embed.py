@@ -235,8 +235,8 @@ class TokenEmbedding:
                 raise ValueError("positions must be a contiguous tensor of tokens' type, size and device")
             at = positions.data_ptr()
         if seq_len is None:
-            seq_len = tokens.size(-1) if tokens.dim() else 1
-        return n, _pack_batch(tokens.data_ptr(), at, n, max(1, seq_len), first_position, kind, 0)
+            seq_len = max(1, tokens.size(-1)) if tokens.dim() else 1
+        return n, _pack_batch(tokens.data_ptr(), at, n, seq_len, first_position, kind, 0)
 
     def forward(self, tokens, table, pos_table=None, *, positions=None, seq_len=None, first_position=0, drop=None,
                 out=None, out_dtype=None, stream=None):

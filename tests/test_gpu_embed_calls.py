@@ -200,3 +200,17 @@ def test_tensors_that_require_a_gradient(ops):
             call()
     assert torch.equal(layer.forward(tok, leaf.detach(), out_dtype=torch.float32)[0], free[:4])
     layer.close()
+
+
+def test_sequence_lengths_below_one(ops):
+    V, D, P = 20, 16, 4
+    layer = ops.TokenEmbedding(V, D, 4, positions=P)
+    tok = torch.arange(4, device="cuda")
+    table, wpe = torch.ones(V, D, device="cuda"), torch.ones(P, D, device="cuda")
+    for seq_len in (0, -3):
+        with pytest.raises(ops.LionCubError, match="positions"):
+            layer.forward(tok, table, wpe, seq_len=seq_len)
+        with pytest.raises(ops.LionCubError, match="positions"):
+            layer.backward(tok, table[:4], table.clone(), pos_grad=wpe.clone(), seq_len=seq_len)
+    assert layer.forward(torch.empty(3, 0, dtype=torch.int64, device="cuda"), table, wpe).shape == (3, 0, D)
+    layer.close()
