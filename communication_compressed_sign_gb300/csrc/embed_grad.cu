@@ -124,7 +124,9 @@ struct Walker {
         // the r-th block's partial and counter: slot 1 of the block the segment begins in, slot 0 of the later ones
         auto slot = [&](int r) { return 2 * static_cast<int64_t>(first + r) + (r == 0 ? 1 : 0); };
         auto partial = [&](int r) { return a.partial + slot(r) * a.partial_stride + column; };
-        if (!index_ok(a.status, 2 * static_cast<int64_t>(block) + 1 < a.partial_rows))
+        // every slot used lies between this segment's first and last
+        if (!index_ok(a.status, first >= 0 && node >= 0 && node < nodes && slot(nodes - 1) < a.partial_rows && slab < a.slabs &&
+                                    column + 8 <= a.partial_stride))
             return false;
 #pragma unroll 1
         for (int level = 0; nodes > 1; ++level) {
@@ -186,6 +188,8 @@ struct Walker {
 template <typename GT, bool VEC>
 __device__ __forceinline__ void fill_row(const RowSumArgs& a, int64_t v, int begin, int end, int lane)
 {
+    if (!index_ok(a.status, v >= 0 && v < a.rows && begin >= 0 && end <= a.dim))
+        return;
     constexpr int kPer = VEC ? 16 / sizeof(GT) : 1;
     using Unit = typename std::conditional<VEC, uint4, GT>::type;
     Unit* dst = reinterpret_cast<Unit*>(static_cast<GT*>(a.grad.data) + v * a.grad.stride);
@@ -373,6 +377,10 @@ __device__ __forceinline__ void running_row(const RowSumArgs& a, const Places& a
         const int here = __popc(there);
         any |= here > 0;
         const int32_t my_place = static_cast<int32_t>(p0 + nth_bit(there, lane) * at.seq_len);  // lane l: the l-th there
+        if constexpr (kBoundsCheck) {
+            if (!__all_sync(kAll, index_ok(a.status, lane >= here || (my_place >= 0 && my_place < a.n))))
+                continue;
+        }
 #pragma unroll 1
         for (int q = 0; q < here; q += kInFlight) {
             SlabGroup<DT, VEC> x[kInFlight];

@@ -83,19 +83,23 @@ __global__ void __launch_bounds__(kBlock) k_lookup(const LookupArgs a)
         }
     };
     fetch(0);
-    if (POSITIONS == kRunning)
+    if (POSITIONS == kRunning && index_ok(a.status, a.at.first + in_sequence < a.at.npos))
         p[0].load(cols, a.pos_table.data, (a.at.first + in_sequence) * a.pos_table.stride);
     for (uint32_t round = 0; round < a.rounds; ++round) {
         int token[PLACES], position[PLACES];
 #pragma unroll
         for (int u = 0; u < PLACES; ++u) {
             token[u] = __shfl_sync(kAll, next_token, u);
+            if (!index_ok(a.status, token[u] < a.at.vocab))
+                return;
             x[u].load(cols, a.table.data, static_cast<uint32_t>(max(token[u], 0)) * a.table.stride);
         }
         if (POSITIONS == kGiven) {
 #pragma unroll
             for (int u = 0; u < PLACES; ++u) {
                 position[u] = __shfl_sync(kAll, next_position, u);
+                if (!index_ok(a.status, position[u] < a.at.npos))
+                    return;
                 p[kRows > u ? u : 0].load(cols, a.pos_table.data, static_cast<uint32_t>(max(position[u], 0)) * a.pos_table.stride);
             }
         }

@@ -88,7 +88,7 @@ struct RawKeys {
 
 // Places one key of each lane that has one: the lane's rank among equal keys
 // of the warp, after those its warp placed before.
-__device__ __forceinline__ void place_keys(const SortTask& t, int* next, const int2* range, bool has, int owned_key, int key_bits,
+__device__ __forceinline__ void place_keys(const SortTask& t, int* next, const int2* range, int owned, bool has, int owned_key, int key_bits,
                                            int32_t key, int32_t place, int lane, int* status)
 {
     unsigned same = __ballot_sync(kAll, has);
@@ -97,6 +97,7 @@ __device__ __forceinline__ void place_keys(const SortTask& t, int* next, const i
         const unsigned ones = __ballot_sync(kAll, bit);
         same &= bit ? ones : ~ones;
     }
+    has = index_ok(status, !has || owned_key < owned) && has;
     int at = 0;
     if (has)
         at = next[owned_key] + __popc(same & ((1u << lane) - 1));
@@ -154,8 +155,10 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
             return;
         if (take) {
             const int k = key >> shift, at = found + __popc(takers & ((1u << lane) - 1));
-            atomicAdd(&count[k], 1);
-            if (at < kList)
+            const bool good = index_ok(all_status, k < owned && place_in_slice >= 0 && place_in_slice < slice);
+            if (good)
+                atomicAdd(&count[k], 1);
+            if (good && at < kList)
                 list[at] = static_cast<uint32_t>(place_in_slice) | static_cast<uint32_t>(k) << 16;
         }
         found += __popc(takers);
@@ -219,7 +222,9 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
                 int32_t key = -1;
                 int place_in_slice = 0;
                 if (q + lane < items) {
-                    const uint32_t item = their_lists[l * kShared + q + lane - start], k = item >> 16;
+                    const int in_list = q + lane - start;
+                    const uint32_t item = index_ok(all_status, in_list >= 0 && in_list < kShared) ? their_lists[l * kShared + in_list] : 0,
+                                   k = item >> 16;
                     key = static_cast<int32_t>(k / kCluster) << shift | (first + static_cast<int>(k % kCluster));
                     place_in_slice = l * static_cast<int>(fine) + static_cast<int>(item & 0xffff);
                 }
@@ -304,7 +309,7 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
             const bool has = q + lane < items;
             const uint32_t item = has ? list[q + lane] : 0;
             const int k = static_cast<int>(item >> 16);
-            place_keys(t, count, range, has, k, key_bits, (k << shift) | mine, static_cast<int32_t>(first_place + (item & 0xffff)),
+            place_keys(t, count, range, owned, has, k, key_bits, (k << shift) | mine, static_cast<int32_t>(first_place + (item & 0xffff)),
                        lane, all_status);
         }
     };
@@ -329,7 +334,7 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
                 const int32_t key = raw.key(t.at, u, nullptr);
                 const bool has = key >= 0 && (key & mask) == mine;
                 const unsigned takers = __ballot_sync(kAll, has);
-                if (has)
+                if (has && index_ok(all_status, items + __popc(takers) <= kList))
                     list[items + __popc(takers & ((1u << lane) - 1))] =
                         static_cast<uint32_t>(i1 - first_place + u * 32 + lane) | static_cast<uint32_t>(key >> shift) << 16;
                 items += __popc(takers);
