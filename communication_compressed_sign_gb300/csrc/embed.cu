@@ -23,7 +23,7 @@ static_assert(sizeof(lioncub_drop) == 24, "lioncub_drop must stay 24 bytes");
 static_assert(lc::kStatusIndex == LIONCUB_EMBED_STATUS_INDEX, "status bits are part of the ABI");
 
 namespace {
-constexpr int kWords = 3;    // single words of the workspace: the status word, the sorts' totals
+constexpr int kWords = 4;    // single words of the workspace: the status word, the sorts' totals, `begun`
 constexpr int kBuffers = 5;
 static_assert(kBuffers + 1 <= lc::kMaxGuardBands, "a band before, between and after the buffers");
 }  // namespace
@@ -47,6 +47,8 @@ struct lioncub_embed_s {
     int64_t fail_alloc_at = 0, alloc_count = 0;
     int64_t fail_launch_at = 0;
     std::atomic<int64_t> launch_count{0};
+
+    uint32_t calls = 0;  // gradients, numbered 1, 2, ... (see lc::SortArgs::call)
 
     uint64_t number = 0;  // of the handles, from 1
     std::mutex err_lock;  // lookups may fail in several threads
@@ -274,6 +276,8 @@ int check_device(lioncub_embed_t h)
     return LIONCUB_OK;
 }
 
+uint32_t* begun_word(lioncub_embed_t h) { return reinterpret_cast<uint32_t*>(h->status + kWords - 1); }
+
 // One table's part of a backward call.
 struct TableGradient {
     lc::KeyKind kind;
@@ -323,6 +327,8 @@ lc::RowSumArgs row_sum_args(lioncub_embed_t h, const lc::Places& at, const Table
     a.rows = static_cast<int32_t>(g.rows);
     a.dim = static_cast<int32_t>(h->dim);
     a.n = at.n;
+    a.begun = begun_word(h);
+    a.call = h->calls;
     a.status = h->status;
     return a;
 }
@@ -552,6 +558,9 @@ int lioncub_embed_backward(lioncub_embed_t h, const lioncub_token_batch* batch, 
     so.arrived[1] = sorted_positions ? h->arrived + h->arrived_count : h->arrived;
     so.arrived_count = lc::grad_partial_rows(lc::grad_stretches(at.n, lc::grad_piece(at.n, slabs))) * slabs;
     so.status = h->status;
+    so.begun = begun_word(h);
+    h->calls = h->calls == UINT32_MAX ? 1 : h->calls + 1;
+    so.call = h->calls;  // its own: a call whose row sums failed leaves its number in the word
     cudaError_t e = launch(h, "embed_sort", [&] { return lc::launch_sort(so, stream); });
     if (e != cudaSuccess)
         return cuda_fail(h, e, "sort launch");

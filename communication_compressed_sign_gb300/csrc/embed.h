@@ -105,6 +105,8 @@ struct SortArgs {
     int32_t tasks;
     uint64_t* arrived[2];  // the row sums' counters, zeroed here
     int64_t arrived_count;
+    uint32_t* begun;  // set to `call` once the launches before the sort are done
+    uint32_t call;    // a number of this call's own, not 0
     int* status;
 };
 
@@ -124,6 +126,8 @@ struct RowSumArgs {
     int32_t dim;
     int32_t slabs, piece;  // set by launch_row_sums
     int32_t n;      // rows of dout
+    uint32_t* begun;  // as in SortArgs
+    uint32_t call;
     int* status;
 };
 
@@ -140,7 +144,9 @@ cudaError_t launch_lookup(const LookupArgs& a, int table_type, int out_type, boo
 cudaError_t launch_sort(SortArgs a, cudaStream_t s);
 // Row sums of a table whose places are sorted and, in the same launch, of
 // `positions` (null: none): sorted too, or running with its places `at`.  Starts
-// before the launch before it has ended, and waits for it.
+// before the launch before it, the sort of the same `call`, has ended, and waits
+// for it; running positions, which do not use it, wait only until `begun` tells
+// that what came before the sort is done, and leave `begun` at 0.
 enum PositionKind { kNoPositions = 0, kRunningPositions = 1, kSortedPositions = 2 };
 cudaError_t launch_row_sums(RowSumArgs a, const RowSumArgs* positions, PositionKind kind, const Places& at, int dout_type,
                             int grad_type, bool vec, bool drop, cudaStream_t s);

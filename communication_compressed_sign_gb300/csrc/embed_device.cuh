@@ -17,11 +17,33 @@ constexpr unsigned kAll = 0xffffffffu;
 // has ended (the gap between two launches is a good part of a small one's
 // time: a decoding step's lookup 1.9 -> 1.6 us).  They touch no memory that
 // others use until wait_for_launch_before() returns: all of that launch, and of
-// what it waited for, is then done and visible.  let_next_launch_start() lets
+// what it waited for, is then done and visible.  (A gradient's running positions
+// need nothing of the launch before theirs, only what was there before that: see
+// wait_until_begun.)  let_next_launch_start() lets
 // the blocks of the next launch start beside this one's, which only the sort
 // wants (the lookup and dropout gained nothing or lost).
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A launch may hand on before it ends that those before it are done.  One of its
+// threads, which has waited and so sees what they wrote, stores the call's number
+// in a word (release); a warp of the next launch that reads that number there
+// (acquire) comes after the thread, and so after all that the thread had waited
+// for.  That the next launch was let start says nothing of memory.  A warp that
+// does not find the number waits like any other, so none ever waits for the word.
+__device__ __forceinline__ void tell_begun(uint32_t* begun, uint32_t call)
+{
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(begun), "r"(call) : "memory");
+}
+__device__ __forceinline__ void wait_until_begun(const uint32_t* begun, uint32_t call, int lane)
+{
+    uint32_t found = 0;
+    if (lane == 0)
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(found) : "l"(begun) : "memory");
+    __syncwarp();  // what lane 0 acquired is the other lanes' too
+    if (__shfl_sync(kAll, found, 0) != call)
+        wait_for_launch_before();
+}
 
 template <typename Kernel, typename... Args>
 cudaError_t launch_programmatic_clusters(Kernel kernel, unsigned blocks, int threads, unsigned cluster, size_t shared, cudaStream_t s,

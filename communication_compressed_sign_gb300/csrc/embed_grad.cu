@@ -21,7 +21,7 @@
 // integer instructions of the mask: about 86 a row and slab, of which drawing
 // takes 40.  Running positions read dout, and draw the mask, a second time.
 // Measured (bf16, 50257 rows): 16 x 1024 places of 1024 columns 32 us (137 MB),
-// 64 x 1024 of 2048 with positions and dropout 169 us (750 MB).
+// 64 x 1024 of 2048 with positions and dropout 164 us (750 MB).
 #include <algorithm>
 #include <type_traits>
 
@@ -240,8 +240,9 @@ __device__ __forceinline__ int nth_bit(unsigned word, int n)
     return at;
 }
 
-// What the blocks of a launch do.  Running positions lead; walks start next, since
-// they take longest; the rest are spread evenly: walks are bound by latency or, with dropout, by integer
+// What the blocks of a launch do.  Running positions need no sort, so they lead
+// while it may still run; walks start next, since they take longest; the rest
+// are spread evenly: walks are bound by latency or, with dropout, by integer
 // instructions, and fills by memory, so they run side by side.
 struct Roles {
     unsigned lead;       // position blocks at the front
@@ -430,17 +431,21 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
     __shared__ WalkShared<VEC, DROP> shared;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned block = blockIdx.x;
-    // Running positions need nothing of the sort, but what the launches before it
-    // left (dout, the tokens) is sure to be visible here only after this.  (Started
-    // without it a gradient of one sequence of 1024 x 768 measured 17.3 us instead of
-    // 17.7, of 64 x 1024 x 2048 164 instead of 169.)
-    wait_for_launch_before();
     if constexpr (POSITIONS != kNoPositions) {
         const unsigned before = roles.positions_before(block);
         if (roles.positions_before(block + 1) != before) {
             const int64_t unit = static_cast<int64_t>(before) * kWarps + warp;
-            if constexpr (POSITIONS == kRunningPositions)
+            // Running positions need nothing of the sort, only what the launches before
+            // it left (dout, the tokens), and so run while it does.  (All after the sort:
+            // 64 x 1024 places of 2048 columns 169 us instead of 164, 1024 sequences of
+            // 256 of 768 299 instead of 258.)
+            if constexpr (POSITIONS == kRunningPositions) {
+                wait_until_begun(p.begun, p.call, lane);
                 running_row<DT, GT, VEC, DROP>(p, at, roles, unit, warp, lane, shared);
+            }
+            wait_for_launch_before();  // the launch after this one relies on the sort's end too
+            if (POSITIONS == kRunningPositions && blockIdx.x == 0 && threadIdx.x == 0)
+                tell_begun(p.begun, 0);  // blocks that start from here on find the sort done
             if constexpr (POSITIONS == kSortedPositions) {
                 if (before < roles.position_walks)
                     walk<DT, GT, VEC, DROP>(p, before, warp, lane, shared);
@@ -452,6 +457,7 @@ __global__ void __launch_bounds__(kBlock, VEC ? 4 : 3)
         block -= before;
     }
     const unsigned fills = roles.fills_before(block);
+    wait_for_launch_before();
     if (roles.fills_before(block + 1) != fills)
         fill_rows<GT, VEC>(a, (static_cast<int64_t>(fills) * kWarps + warp) * kFillRows, lane);
     else

@@ -118,7 +118,7 @@ __host__ __device__ constexpr int owned_width(int keys, int shift)
 }
 
 template <int KIND, typename IT, int BLOCK, bool CLUSTERED>
-__device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_status)
+__device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_status, uint32_t* begun, uint32_t call)
 {
     namespace cg = cooperative_groups;
     constexpr int kWarps = BLOCK / 32;
@@ -137,8 +137,11 @@ __device__ void sort_task(const SortTask& t, int mine, int* memory, int* all_sta
     for (int k = tid; k < kWarps * width / 4; k += BLOCK)
         reinterpret_cast<int4*>(count)[k] = make_int4(0, 0, 0, 0);
     count += warp * width;
-    // what came before in the stream is done; then the row sums may start beside this
+    // what came before in the stream is done; then the row sums may start beside this,
+    // and running positions may read it as soon as the one thread has told so
     wait_for_launch_before();
+    if (begun && tid == 0)
+        tell_begun(begun, call);
     let_next_launch_start();
 
     const int64_t n = t.at.n;
@@ -354,16 +357,17 @@ __global__ void __launch_bounds__(BLOCK) k_sort(const __grid_constant__ SortArgs
 {
     extern __shared__ __align__(16) int memory[];
     int block = blockIdx.x;
+    uint32_t* const begun = block == 0 ? a.begun : nullptr;  // one block tells
     for (int k = 0; k < a.tasks; ++k) {
         const int sorters = 1 << a.task[k].log_blocks;
         if (block < sorters) {
             const SortTask& t = a.task[k];
             if (t.kind == kKeyToken)
-                t.at.wide ? sort_task<kKeyToken, int64_t, BLOCK, CLUSTERED>(t, block, memory, a.status)
-                          : sort_task<kKeyToken, int32_t, BLOCK, CLUSTERED>(t, block, memory, a.status);
+                t.at.wide ? sort_task<kKeyToken, int64_t, BLOCK, CLUSTERED>(t, block, memory, a.status, begun, a.call)
+                          : sort_task<kKeyToken, int32_t, BLOCK, CLUSTERED>(t, block, memory, a.status, begun, a.call);
             else
-                t.at.wide ? sort_task<kKeyPosition, int64_t, BLOCK, CLUSTERED>(t, block, memory, a.status)
-                          : sort_task<kKeyPosition, int32_t, BLOCK, CLUSTERED>(t, block, memory, a.status);
+                t.at.wide ? sort_task<kKeyPosition, int64_t, BLOCK, CLUSTERED>(t, block, memory, a.status, begun, a.call)
+                          : sort_task<kKeyPosition, int32_t, BLOCK, CLUSTERED>(t, block, memory, a.status, begun, a.call);
             break;
         }
         block -= sorters;

@@ -79,3 +79,43 @@ def test_running_positions_of_inputs_just_written(ops, B, S, D, captured):
         assert all(torch.equal(a.double(), b) for a, b in zip(got, want[k % 2])), k
     assert layer.status() == 0
     layer.close()
+
+
+def test_running_positions_after_a_call_without_its_row_sums(ops, monkeypatch):
+    """A gradient whose second launch fails leaves its sort behind; the next ones, direct and replayed in turn, read
+    inputs written right before them all the same."""
+    B, S, D, V = 64, 64, 256, 500
+    n, P = B * S, S
+    monkeypatch.setenv("LIONCUB_FAIL_LAUNCH", "4")
+    layer = ops.TokenEmbedding(V, D, n, positions=P)
+    monkeypatch.delenv("LIONCUB_FAIL_LAUNCH")
+    tokens = [torch.randint(-1, V, (B, S), device="cuda") for _ in range(2)]
+    douts = [_integers((n, D), torch.float32, seed) for seed in range(2)]
+    place = torch.arange(n, device="cuda") % S
+    want = [(_sums(t.view(-1), x, V), _sums(torch.where(t.view(-1) < 0, -1, place), x, P)) for t, x in zip(tokens, douts)]
+    tok, dout = torch.empty_like(tokens[0]), torch.empty_like(douts[0])
+    grad, pos_grad = torch.empty(V, D, device="cuda"), torch.empty(P, D, device="cuda")
+
+    def one(k, with_positions=True):
+        pos_grad.fill_(float("nan"))
+        tok.copy_(tokens[k])
+        dout.copy_(douts[k])
+        layer.backward(tok, dout.view(B, S, D), grad, pos_grad=pos_grad if with_positions else None)
+
+    one(0)
+    with pytest.raises(ops.LionCubError, match="launch"):
+        one(1)
+    one(0)
+    assert torch.equal(grad.double(), want[0][0]) and torch.equal(pos_grad.double(), want[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one(1)
+    for k in range(30):
+        go = [lambda: one(0), graph.replay, lambda: one(0, with_positions=False)][k % 3]
+        go()
+        got = grad.clone(), pos_grad.clone()
+        assert torch.equal(got[0].double(), want[k % 3 == 1][0]), k
+        if k % 3 < 2:
+            assert torch.equal(got[1].double(), want[k % 3][1]), k
+    assert layer.status() == 0
+    layer.close()
