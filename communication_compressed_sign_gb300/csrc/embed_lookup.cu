@@ -6,8 +6,8 @@
 // their rows are in flight together and the index arithmetic is shared.  Wide
 // rows with dropout are bound by instructions about as much as by memory, so
 // sums and rescalings are done two at a time (fp32 pairs).  Measured (fp32 rows
-// of 2048 columns to bf16, 64 x 1024 places, 413 MB at least): 88 us with
-// dropout, 78 without; 8 x 1024 of 768 (27 MB): 7.3 and 5.7 us.
+// of 2048 columns to bf16, 64 x 1024 places, 413 MB at least): 87 us with
+// dropout, 77 without; 8 x 1024 of 768 (27 MB): 7.2 and 5.0 us.
 #include "embed_device.cuh"
 
 namespace lc {

@@ -403,7 +403,10 @@ cudaError_t launch_sort(SortArgs a, cudaStream_t s)
     bool clustered = static_cast<int64_t>(a.task[0].at.n) * a.tasks > kClusterAbove && a.task[0].at.n <= kClusterUpTo;
     for (int k = 0; k < a.tasks; ++k) {
         SortTask& t = a.task[k];
-        // one wave of blocks, each with a key at least
+        // One wave of blocks, each with a key at least.  So a table of few rows is
+        // sorted by few blocks, whose lists overflow and are read again (whole
+        // gradients of 65536 places of 768 columns, microseconds: of 1 row 80.7, 2 rows
+        // 75.0, 8 65.0, 37 60.8, 100 44.9, 1000 44.8).
         while (t.log_blocks < (a.tasks > 1 ? 6 : 7) && t.keys >> (t.log_blocks + 1) > 0)
             ++t.log_blocks;
         while ((static_cast<int64_t>(kMaxOwned) << t.log_blocks) < t.keys)

@@ -209,7 +209,9 @@ class TokenEmbedding:
     float32 with contiguous columns.  A negative token is an empty place.  The
     tables may be views of the flat parameter vector and the gradients views
     of a worker's flat gradient vector.  `stream` defaults to torch's current
-    stream; calls to :meth:`backward` of one layer must be ordered.
+    stream; calls to :meth:`backward` of one layer must be ordered.  The layer
+    keeps the gradient's workspace, whose size goes by max_tokens, from
+    construction on.
     """
 
     def __init__(self, vocab, dim, max_tokens, *, positions=0, scale=1.0):
@@ -275,7 +277,8 @@ class TokenEmbedding:
         return grad
 
     def status(self) -> int:
-        """The status word (LIONCUB_STATUS_* and STATUS_INDEX bits; 0: all is well).  Synchronizes."""
+        """The status word (LIONCUB_STATUS_* and STATUS_INDEX bits; 0: all is well) after the calls
+        before it on torch's current stream.  Synchronizes."""
         if not self.h:
             raise LionCubError(ERR_STATE, "the layer is closed")
         word = _torch.zeros(1, dtype=_torch.int32, device=self.device)

@@ -39,8 +39,11 @@
  * lookup followed by dropout with the same seed and stream.  Give each (step,
  * worker, layer) a stream of its own.
  *
- * The sums of the gradient are fp32 in an order that depends only on the
- * batch, never on the schedule, so results repeat bit for bit.
+ * The sums of the gradient are fp32 in an order that depends on the batch, the
+ * width, whether every matrix allows 16-byte moves (see lioncub_rows) and, for
+ * positions, whether they are given or run; never on the schedule.  So a call
+ * repeats bit for bit, but long sums may differ in their last bits from those of
+ * the same values laid out otherwise.
  *
  * Calls only enqueue kernels on `stream`: nothing is allocated or
  * synchronized outside create, and a call can be captured into a CUDA graph
@@ -106,9 +109,11 @@ typedef struct {
 /*
  * A layer of `vocab` token rows and `positions` position rows (0: none) of
  * `dim` columns, for batches of at most max_tokens places; `scale` multiplies
- * the token rows.  Allocates the workspace of the gradient on the current
- * device, which must be current in every later call on the handle, and
- * synchronizes the legacy default stream once.  LIONCUB_FAIL_ALLOC and
+ * the token rows.  Allocates the workspace of the gradient, which lookups do not
+ * use (16 bytes a place and table, 8 a row of either table, about 4 * dim bytes
+ * for every 16 to 64 places and table; 23 MB for 65536 places of 2048 columns
+ * with positions), on the current device, which must be current in every later
+ * call on the handle, and synchronizes the legacy default stream once.  LIONCUB_FAIL_ALLOC and
  * LIONCUB_FAIL_LAUNCH (lioncub.h) apply to the handle's own allocations and
  * kernel launches.  Errors: ERR_ARG, ERR_OOM, ERR_CUDA (*out is NULL then).
  */
