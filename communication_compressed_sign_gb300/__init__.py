@@ -6,11 +6,15 @@ ABI of include/lioncub.h); :mod:`.lioncub` is its ctypes binding and
 :class:`LionCubOptimizer` a small convenience wrapper that takes torch CUDA
 tensors and passes their pointers through.  :mod:`.embed` binds the input-layer
 operators of include/lioncub_embed.h, whose gradients fill the embedding rows
-of the vector that a step reads.
+of the vector that a step reads, and :mod:`.block` the block operators of
+include/lioncub_block.h: norm, 8-bit checkpoints, activation, rotary positions.
 """
 from __future__ import annotations
 
 from . import lioncub
+from .block import (  # noqa: F401
+    Packed, RmsNorm, Rotary, RotaryScaling, activation, activation_backward, pack8, unpack8,
+)
 from .embed import Drop, TokenEmbedding, dropout, dropout_backward  # noqa: F401
 from .lioncub import (  # noqa: F401
     FLAG_AVERAGE, FLAG_TIE_ALTERNATE, GRAD_BF16, GRAD_F32, MODE_L1_INTSUM, MODE_SIGN_MAJORITY,

@@ -1,8 +1,8 @@
 """Build the lioncub CUDA library (liblioncub.so) in-tree for sm_103a.
 
 Each .cu file under csrc/ is compiled in parallel with nvcc and the objects
-are linked into one shared library with the C ABIs of include/lioncub.h and
-include/lioncub_embed.h.  No PyTorch headers or types are involved: the
+are linked into one shared library with the C ABIs of include/lioncub.h,
+include/lioncub_embed.h and include/lioncub_block.h.  No PyTorch headers or types are involved: the
 library is plain CUDA C++ with the CUDA runtime linked statically.
 
     python -m communication_compressed_sign_gb300.build [--verbose]
@@ -45,7 +45,7 @@ def sources() -> list[str]:
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
              if f.endswith((".cu", ".cuh", ".h"))]
-    files += [os.path.join(INCLUDE, f) for f in ("lioncub.h", "lioncub_embed.h")]
+    files += [os.path.join(INCLUDE, f) for f in ("lioncub.h", "lioncub_embed.h", "lioncub_block.h")]
     files.append(os.path.abspath(__file__))
     return files
 

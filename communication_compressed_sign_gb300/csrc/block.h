@@ -1,0 +1,103 @@
+// block.h -- shared declarations of the block operators (norm, 8-bit
+// checkpoints, activation, rotary positions); the public C ABI is
+// include/lioncub_block.h.
+#pragma once
+
+#include "embed.h"
+#include "lioncub_block.h"
+
+namespace lc {
+
+// A matrix with the type of its elements (LIONCUB_ROWS_*); data may be null.
+struct TypedRows {
+    void* data;
+    int64_t stride;
+    int32_t type;
+};
+
+// A matrix in 8 bits; codes may be null.  Groups are 1 << log_group columns, or
+// the whole row (kRowGroup).
+constexpr int kRowGroup = 62;
+struct PackedRows {
+    uint8_t* codes;
+    float* scales;
+    int64_t stride, scale_stride;
+    int32_t log_group;
+    int32_t e4m3;  // else whole numbers
+};
+
+struct NormArgs {
+    TypedRows x, residual, weight, summed, out;
+    PackedRows saved, packed;  // the sum's and the result's codes
+    float* rstd;
+    int64_t n;
+    int32_t dim;
+    int32_t warps;  // of a row; set by launch_norm
+    float eps;
+    int* status;
+};
+
+struct NormGradArgs {
+    TypedRows dout, saved, residual_grad, dx, weight, again;
+    PackedRows packed;
+    const float* rstd;
+    float* partial;  // a row of dim for each block, null: no weight gradient
+    int64_t partial_rows;
+    int64_t n;
+    int32_t dim;
+    int32_t warps, teams;  // warps of a row, rows at once in a block; set by launch_norm_grad
+    int* status;
+};
+
+struct WeightGradArgs {
+    const float* partial;
+    int64_t rows;  // of partial
+    TypedRows base, grad;
+    int32_t dim;
+    int* status;
+};
+
+struct ActivationArgs {
+    TypedRows x, up, out;           // forward; backward: x and up null where packed
+    TypedRows dout, dx, dup, again;  // backward
+    PackedRows saved, saved_up;     // forward: written; backward: read
+    int64_t rows, cols;
+};
+
+struct HeadsArgs {
+    const void* in;
+    void* out;
+    int64_t in_batch, in_place, in_head, out_batch, out_place, out_head;
+};
+
+struct RotaryArgs {
+    HeadsArgs side[2];
+    int32_t heads[2];
+    const uint64_t* turns;  // of each pair: turns a position, in units of 2^-64
+    const void* positions;
+    int64_t first;
+    int64_t places;  // of all sequences
+    int32_t seq;
+    int32_t wide;  // positions are int64, else int32
+    int32_t head_dim, pairs;
+    int32_t copy;  // columns behind the rotated ones are copied
+    int32_t groups;  // threads that share a place's heads; set by launch_rotary
+    float cos_factor, sin_factor;
+};
+
+// Blocks that leave a row of partial sums each: one for each multiprocessor.
+// vec: the matrices allow 16-byte moves.
+cudaError_t launch_norm(NormArgs a, bool vec, cudaStream_t s);
+cudaError_t launch_norm_grad(NormGradArgs a, int blocks, bool vec, cudaStream_t s);
+int norm_grad_blocks(int64_t n, int dim, int multiprocessors);
+cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t s);
+// Codes with one scale a row (forward norms without the norm).
+cudaError_t launch_pack_rows(const TypedRows& x, const PackedRows& out, int64_t rows, int dim, bool vec, cudaStream_t s);
+// kind: LIONCUB_ACTIVATION_*, or kIdentity (out may then be null: x is only packed).
+constexpr int kIdentity = -1;
+cudaError_t launch_activation(const ActivationArgs& a, int kind, bool vec, cudaStream_t s);
+cudaError_t launch_activation_grad(const ActivationArgs& a, int kind, bool vec, cudaStream_t s);
+cudaError_t launch_unpack(const PackedRows& x, const TypedRows& out, int64_t rows, int64_t cols, bool vec, cudaStream_t s);
+cudaError_t launch_rotary(RotaryArgs a, int type, bool interleaved, bool vec, cudaStream_t s);
+
+}  // namespace lc

@@ -1,7 +1,5 @@
 // embed.cu -- the C ABI of the input-layer operators (include/lioncub_embed.h):
 // argument checks, the handle's workspace, launches and errors.
-#include <nvtx3/nvToolsExt.h>
-
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -14,6 +12,7 @@
 
 #include "embed.h"
 #include "guard.h"
+#include "operands.h"
 #include "splitmix64.cuh"
 
 // Layouts the language bindings rely on.
@@ -57,6 +56,14 @@ struct lioncub_embed_s {
 
 namespace {
 
+using lc::aligned_rows;
+using lc::element_size;
+using lc::env_index;
+using lc::NvtxRange;
+using lc::overlap;
+using lc::rows_of;
+using lc::same_matrix;
+
 std::atomic<uint64_t> g_handles{0};
 
 // Messages of this thread's last failed call without a handle, and of that on a
@@ -82,23 +89,6 @@ int fail(lioncub_embed_t h, int code, const char* fmt, ...)
 int cuda_fail(lioncub_embed_t h, cudaError_t e, const char* what)
 {
     return fail(h, LIONCUB_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-int64_t env_index(const char* name)
-{
-    const char* v = std::getenv(name);
-    if (!v || !*v)
-        return 0;
-    char* end = nullptr;
-    const long long x = std::strtoll(v, &end, 10);
-    return (*end == '\0' && x > 0) ? static_cast<int64_t>(x) : 0;
 }
 
 // The workspace: buffers of these sizes, each on a 256-byte boundary with guard
@@ -146,8 +136,6 @@ cudaError_t launch(lioncub_embed_t h, const char* name, Launch&& go)
 
 // --- arguments ---------------------------------------------------------------------
 
-size_t element_size(int type) { return type == LIONCUB_ROWS_BF16 ? 2 : 4; }
-
 int check_rows(lioncub_embed_t h, const char* name, const lioncub_rows* m, int64_t rows, int64_t cols)
 {
     if (!m || (!m->data && rows > 0 && cols > 0))
@@ -160,37 +148,6 @@ int check_rows(lioncub_embed_t h, const char* name, const lioncub_rows* m, int64
         return fail(h, LIONCUB_ERR_ALIGN, "%s is not aligned to its elements", name);
     return LIONCUB_OK;
 }
-
-// Whether two matrices may have bytes in common: their spans do, and they are
-// not disjoint columns of rows that lie the same distance apart.
-bool overlap(const lioncub_rows& a, int64_t arows, const lioncub_rows& b, int64_t brows, int64_t cols)
-{
-    if (arows == 0 || brows == 0 || cols == 0)
-        return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.data), b0 = reinterpret_cast<uintptr_t>(b.data);
-    const uintptr_t a1 = a0 + ((arows - 1) * a.stride + cols) * element_size(a.type);
-    const uintptr_t b1 = b0 + ((brows - 1) * b.stride + cols) * element_size(b.type);
-    if (a0 >= b1 || b0 >= a1)
-        return false;
-    const uintptr_t step = a.stride * element_size(a.type);
-    if (step != b.stride * element_size(b.type))
-        return true;
-    const uintptr_t ahead = b0 >= a0 ? (b0 - a0) % step : step - 1 - (a0 - b0 - 1) % step;  // (b0 - a0) mod step
-    return ahead < cols * element_size(a.type) || ahead + cols * element_size(b.type) > step;
-}
-
-bool same_matrix(const lioncub_rows& a, const lioncub_rows& b)
-{
-    return a.data == b.data && a.stride == b.stride && a.type == b.type;
-}
-
-// Rows that start on 16-byte boundaries.
-bool aligned_rows(const lioncub_rows* m)
-{
-    return !m || (reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && m->stride * element_size(m->type) % 16 == 0);
-}
-
-lc::Rows rows_of(const lioncub_rows* m) { return m ? lc::Rows{m->data, m->stride} : lc::Rows{nullptr, 0}; }
 
 // NULL, p == 0 and a p that rounds to 0 mean no dropout.
 int check_drop(lioncub_embed_t h, const lioncub_drop* d, int64_t cols, lc::DropArgs* out, bool* on)

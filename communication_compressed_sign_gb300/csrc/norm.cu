@@ -1,0 +1,245 @@
+// norm.cu -- the root-mean-square norm of rows, with the residual added before
+// and 8-bit codes of the sum and of the result after:
+//   h = x + residual,  out = h * rstd * weight,  rstd = 1 / sqrt(mean(h^2) + eps).
+//
+// Memory-bound.  A row stays in the registers of one or more warps from its only
+// reading to its writing; one sum over the row stands between.
+#include <climits>
+
+#include "block_device.cuh"
+
+namespace lc {
+namespace {
+
+constexpr int kMaxWarps = 16;  // of a row
+constexpr int kRowsOfWarps = 8;  // rows of a block, where a row is one warp's
+
+// The sum over a row of what each of its warps has, and likewise the largest.
+__device__ __forceinline__ float row_sum(float v, float* shared, int warps, int warp, int lane)
+{
+    v = warp_sum(v);
+    if (warps > 1) {
+        if (lane == 0)
+            shared[warp] = v;
+        __syncthreads();
+        v = 0.0f;
+        for (int k = 0; k < warps; ++k)
+            v = __fadd_rn(v, shared[k]);
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* shared, int warps, int warp, int lane)
+{
+    v = __reduce_max_sync(kAll, v);
+    if (warps > 1) {
+        if (lane == 0)
+            shared[warp] = v;
+        __syncthreads();
+        for (int k = 0; k < warps; ++k)
+            v = max(v, shared[k]);
+    }
+    return v;
+}
+
+// The codes of a row whose chunks are in x.
+template <int C, bool VEC>
+__device__ __forceinline__ void pack_row(const PackedRows& p, const Columns<VEC> (&cols)[C], int64_t row, const float (&x)[C][8],
+                                         uint32_t* shared, int warps, int warp, int lane)
+{
+    if (p.log_group != kRowGroup) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            pack_chunk<VEC>(p, cols[c], row, x[c], lane);
+        return;
+    }
+    uint32_t largest = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            largest = max(largest, magnitude(x[c][k]));
+    const GroupScale s(row_max(largest, shared, warps, warp, lane), p.e4m3);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        pack_chunk_of_row<VEC>(p, cols[c], row, x[c], s);
+    if (warp == 0 && lane == 0)
+        p.scales[row * p.scale_stride] = s.scale;
+}
+
+// A row is that of `warps` warps, C chunks each: warp w has chunks w, w + warps, ...
+template <typename XT, typename RT, int C, bool VEC>
+__global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__ NormArgs a)
+{
+    __shared__ float sums[kMaxWarps];
+    __shared__ uint32_t maxima[2][kMaxWarps];
+    const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5;
+    const int warps = a.warps, warp = warps == 1 ? 0 : in_block;
+    const int64_t row = warps == 1 ? static_cast<int64_t>(blockIdx.x) * kRowsOfWarps + in_block : blockIdx.x;
+    wait_for_launch_before();
+    if (row >= a.n)  // only where a row is one warp's, which meets no barrier
+        return;
+    Columns<VEC> cols[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        cols[c] = Columns<VEC>((warp + c * warps) * kChunk, lane, a.dim);
+
+    float h[C][8];
+    {
+        Chunk<XT, VEC> x[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            x[c].load(cols[c], a.x.data, row * a.x.stride, a.x.type);
+        if (a.residual.data) {
+            Chunk<RT, VEC> r[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                r[c].load(cols[c], a.residual.data, row * a.residual.stride, a.residual.type);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float y[8];
+                x[c].unpack(h[c]);
+                r[c].unpack(y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    h[c][k] = __fadd_rn(h[c][k], y[k]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                x[c].unpack(h[c]);
+        }
+    }
+    if (a.summed.data)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            store_typed<VEC>(cols[c], a.summed.data, row * a.summed.stride, a.summed.type, h[c]);
+
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sum = fmaf(h[c][k], h[c][k], sum);
+    sum = row_sum(sum, sums, warps, warp, lane);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.dim)), a.eps)));
+    if (a.rstd && warp == 0 && lane == 0)
+        a.rstd[row] = rstd;
+    if (a.saved.codes)
+        pack_row<C, VEC>(a.saved, cols, row, h, maxima[0], warps, warp, lane);
+
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            h[c][k] = __fmul_rn(h[c][k], rstd);
+        if (a.weight.data) {
+            float w[8];
+            load_typed<VEC>(cols[c], a.weight.data, 0, a.weight.type, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                h[c][k] = __fmul_rn(h[c][k], w[k]);
+        }
+    }
+    if (a.packed.codes) {
+        pack_row<C, VEC>(a.packed, cols, row, h, maxima[1], warps, warp, lane);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            store_typed<VEC>(cols[c], a.out.data, row * a.out.stride, a.out.type, h[c]);
+    }
+}
+
+// The codes of rows that have one scale each.
+template <typename XT, int C, bool VEC>
+__global__ void __launch_bounds__(kMaxWarps * 32) k_pack_rows(const TypedRows x, const PackedRows out, const int64_t rows, const int dim,
+                                                              const int warps)
+{
+    __shared__ uint32_t maxima[kMaxWarps];
+    const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, warp = warps == 1 ? 0 : in_block;
+    const int64_t row = warps == 1 ? static_cast<int64_t>(blockIdx.x) * kRowsOfWarps + in_block : blockIdx.x;
+    wait_for_launch_before();
+    if (row >= rows)
+        return;
+    Columns<VEC> cols[C];
+    Chunk<XT, VEC> v[C];
+    float h[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        cols[c] = Columns<VEC>((warp + c * warps) * kChunk, lane, dim);
+        v[c].load(cols[c], x.data, row * x.stride, x.type);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        v[c].unpack(h[c]);
+    pack_row<C, VEC>(out, cols, row, h, maxima, warps, warp, lane);
+}
+
+// How a row of `dim` columns is spread: C chunks for each of `warps` warps.
+struct Spread {
+    int c, warps;
+    explicit Spread(int dim)
+    {
+        const int chunks = (dim + kChunk - 1) / kChunk;
+        c = chunks <= 4 ? chunks : 2;
+        if (chunks > 2 * kMaxWarps)
+            c = 4;
+        warps = (chunks + c - 1) / c;
+    }
+};
+
+// f(integral constant C) for the spread's C
+template <typename F>
+cudaError_t with_chunks(int c, F&& f)
+{
+    switch (c) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    default: return f(std::integral_constant<int, 4>());
+    }
+}
+
+unsigned row_blocks(int64_t rows, int warps) { return static_cast<unsigned>(warps == 1 ? (rows + kRowsOfWarps - 1) / kRowsOfWarps : rows); }
+int row_threads(int warps) { return 32 * (warps == 1 ? kRowsOfWarps : warps); }
+
+template <typename XT, typename RT, bool VEC>
+cudaError_t launch_t(const NormArgs& a, int c, cudaStream_t s)
+{
+    return with_chunks(c, [&](auto n) {
+        return launch_programmatic(k_norm<XT, RT, decltype(n)::value, VEC>, row_blocks(a.n, a.warps), row_threads(a.warps), 0, s, a);
+    });
+}
+
+}  // namespace
+
+cudaError_t launch_norm(NormArgs a, bool vec, cudaStream_t s)
+{
+    if (a.n == 0)
+        return cudaSuccess;
+    const Spread spread(a.dim);
+    a.warps = spread.warps;
+    if (!vec)
+        return launch_t<float, float, false>(a, spread.c, s);
+    const bool xb = a.x.type == LIONCUB_ROWS_BF16, rb = a.residual.type == LIONCUB_ROWS_BF16;
+    if (xb)
+        return rb ? launch_t<__nv_bfloat16, __nv_bfloat16, true>(a, spread.c, s) : launch_t<__nv_bfloat16, float, true>(a, spread.c, s);
+    return rb ? launch_t<float, __nv_bfloat16, true>(a, spread.c, s) : launch_t<float, float, true>(a, spread.c, s);
+}
+
+cudaError_t launch_pack_rows(const TypedRows& x, const PackedRows& out, int64_t rows, int dim, bool vec, cudaStream_t s)
+{
+    const Spread spread(dim);
+    return with_chunks(spread.c, [&](auto n) {
+        constexpr int C = decltype(n)::value;
+        const unsigned blocks = row_blocks(rows, spread.warps);
+        const int threads = row_threads(spread.warps);
+        if (!vec)
+            return launch_programmatic(k_pack_rows<float, C, false>, blocks, threads, 0, s, x, out, rows, dim, spread.warps);
+        return x.type == LIONCUB_ROWS_BF16
+                   ? launch_programmatic(k_pack_rows<__nv_bfloat16, C, true>, blocks, threads, 0, s, x, out, rows, dim, spread.warps)
+                   : launch_programmatic(k_pack_rows<float, C, true>, blocks, threads, 0, s, x, out, rows, dim, spread.warps);
+    });
+}
+
+}  // namespace lc
