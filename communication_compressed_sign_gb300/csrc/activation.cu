@@ -15,142 +15,203 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
+constexpr int kUnits = 2;  // chunks of a warp, whose loads are in flight together
 
-// f(x) and, where it is wanted, f'(x).  |x| > 30 is beyond where s changes: the
-// bound keeps powers of x finite.
-template <int KIND, bool SLOPE>
-__device__ __forceinline__ void value_and_slope(float x, float& f, float& slope)
+__device__ __forceinline__ float exp2_approx(float x)  // off by at most 2 units in the last place
 {
-    constexpr float kTwice = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float y = KIND == LIONCUB_ACTIVATION_GELU ? fminf(fmaxf(x, -30.0f), 30.0f) : x;
-    const float square = __fmul_rn(y, y);
-    const float z = KIND == LIONCUB_ACTIVATION_GELU ? __fmul_rn(kTwice, __fmul_rn(y, fmaf(0.044715f, square, 1.0f))) : x;
-    const float s = __fdividef(1.0f, __fadd_rn(1.0f, expf(-z)));
-    f = __fmul_rn(x, s);
-    if (SLOPE) {
-        const float dz = KIND == LIONCUB_ACTIVATION_GELU ? fmaf(kTwice * 3 * 0.044715f, square, kTwice) : 1.0f;
-        slope = fmaf(__fmul_rn(f, __fsub_rn(1.0f, s)), dz, s);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x)  // off by at most one unit; 0 for x above 2^126
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// f(x) and, where it is wanted, f'(x), of a pair.  s = 1 / (1 + 2^w) with w = -z log2(e).
+template <int KIND, bool SLOPE>
+__device__ __forceinline__ void value_and_slope(float2 x, float2& f, float2& slope)
+{
+    constexpr double kLog2e = 1.4426950408889634, kTwice = 1.5957691216057308, kCube = 0.044715;  // kTwice: 2 sqrt(2 / pi)
+    float2 w, square;
+    if constexpr (KIND == LIONCUB_ACTIVATION_GELU) {
+        square = mul2(x, x);
+        w = mul2(x, fma2(square, both(static_cast<float>(-kTwice * kCube * kLog2e)), both(static_cast<float>(-kTwice * kLog2e))));
+    } else {
+        w = mul2(x, both(static_cast<float>(-kLog2e)));
+    }
+    const float2 below = add2(make_float2(exp2_approx(w.x), exp2_approx(w.y)), both(1.0f));
+    const float2 s = make_float2(reciprocal_approx(below.x), reciprocal_approx(below.y));
+    f = mul2(x, s);
+    if constexpr (SLOPE) {
+        const float2 t = mul2(f, fma2(s, both(-1.0f), both(1.0f)));
+        if constexpr (KIND == LIONCUB_ACTIVATION_GELU) {
+            // s is 0 or 1 long before the square could overflow, and t is then 0
+            square = make_float2(fminf(square.x, 1e30f), fminf(square.y, 1e30f));
+            slope = fma2(t, fma2(square, both(static_cast<float>(3 * kTwice * kCube)), both(static_cast<float>(kTwice))), s);
+        } else {
+            slope = add2(t, s);
+        }
     }
 }
 
-// A row and the chunk of it that a warp has.
+// The chunks of a warp: kUnits neighbours in a row, of which it has `spans` times as many.
 template <bool VEC>
-struct Unit {
-    int64_t row;
-    Columns<VEC> cols;
-    bool on;
-    __device__ __forceinline__ Unit(int64_t rows, int64_t width, int64_t chunks) : row(0)
+struct Units {
+    int64_t row, first, width;
+    Columns<VEC> cols[kUnits];
+    __device__ __forceinline__ Units(int64_t rows, int64_t w, int64_t spans) : width(w)
     {
         const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-        row = rows == 1 ? 0 : quotient(unit, static_cast<int>(chunks));
-        const int64_t chunk = unit - row * chunks;
-        on = row < rows && chunk < chunks;
-        cols = Columns<VEC>(chunk * kChunk, threadIdx.x & 31, width);
+        row = rows == 1 ? 0 : quotient(unit, static_cast<int>(spans));
+        first = (unit - row * spans) * (kUnits * kChunk);
+        if (row >= rows)  // behind the last
+            first = width;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+            cols[u] = Columns<VEC>(first + u * kChunk, threadIdx.x & 31, width);
     }
+    __device__ __forceinline__ bool none() const { return first >= width; }
+    __device__ __forceinline__ bool on(int u) const { return first + u * kChunk < width; }
 };
 
 template <typename T, int KIND, bool VEC>
-__global__ void __launch_bounds__(kBlock) k_activation(const __grid_constant__ ActivationArgs a, const int64_t chunks)
+__global__ void __launch_bounds__(kBlock) k_activation(const __grid_constant__ ActivationArgs a, const int64_t spans)
 {
-    const Unit<VEC> u(a.rows, a.cols, chunks);
+    const Units<VEC> u(a.rows, a.cols, spans);
     const int lane = threadIdx.x & 31;
     wait_for_launch_before();
-    if (!u.on)
+    if (u.none())
         return;
-    Chunk<T, VEC> vx, vup;
-    vx.load(u.cols, a.x.data, u.row * a.x.stride, a.x.type);
-    if (KIND != kIdentity && a.up.data)
-        vup.load(u.cols, a.up.data, u.row * a.up.stride, a.up.type);
-    float x[8];
-    vx.unpack(x);
-    if (a.saved.codes)
-        pack_chunk<VEC>(a.saved, u.cols, u.row, x, lane);
-    if constexpr (KIND != kIdentity) {
-        float unused;
+    Chunk<T, VEC> vx[kUnits], vup[kUnits];
+    const bool gated = KIND != kIdentity && a.up.data;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            value_and_slope<KIND, false>(x[k], x[k], unused);
-        if (a.up.data) {
-            float y[8];
-            vup.unpack(y);
-            if (a.saved_up.codes)
-                pack_chunk<VEC>(a.saved_up, u.cols, u.row, y, lane);
+    for (int i = 0; i < kUnits; ++i) {
+        vx[i].load(u.cols[i], a.x.data, u.row * a.x.stride, a.x.type);
+        if (gated)
+            vup[i].load(u.cols[i], a.up.data, u.row * a.up.stride, a.up.type);
+    }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                x[k] = __fmul_rn(x[k], y[k]);
+    for (int i = 0; i < kUnits; ++i) {
+        if (!u.on(i))
+            continue;
+        float x[8];
+        vx[i].unpack(x);
+        if (a.saved.codes)
+            pack_chunk<VEC>(a.saved, u.cols[i], u.row, x, vx[i].largest(), lane);
+        if constexpr (KIND != kIdentity) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float2 f, unused;
+                value_and_slope<KIND, false>(pair_of(x, k), f, unused);
+                set_pair(x, k, f);
+            }
+            if (gated) {
+                float y[8];
+                vup[i].unpack(y);
+                if (a.saved_up.codes)
+                    pack_chunk<VEC>(a.saved_up, u.cols[i], u.row, y, vup[i].largest(), lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    set_pair(x, k, mul2(pair_of(x, k), pair_of(y, k)));
+            }
+            store_typed<VEC>(u.cols[i], a.out.data, u.row * a.out.stride, a.out.type, x);
         }
-        store_typed<VEC>(u.cols, a.out.data, u.row * a.out.stride, a.out.type, x);
     }
 }
 
 template <typename T, int KIND, bool PACKED, bool VEC>
-__global__ void __launch_bounds__(kBlock) k_activation_grad(const __grid_constant__ ActivationArgs a, const int64_t chunks)
+__global__ void __launch_bounds__(kBlock) k_activation_grad(const __grid_constant__ ActivationArgs a, const int64_t spans)
 {
-    const Unit<VEC> u(a.rows, a.cols, chunks);
+    const Units<VEC> u(a.rows, a.cols, spans);
+    const int lane = threadIdx.x & 31;
     wait_for_launch_before();
-    if (!u.on)
+    if (u.none())
         return;
     const bool gated = PACKED ? a.saved_up.codes != nullptr : a.up.data != nullptr;
-    Chunk<T, VEC> vd;
-    vd.load(u.cols, a.dout.data, u.row * a.dout.stride, a.dout.type);
-    float x[8], up[8], d[8];
-    if constexpr (PACKED) {
-        CodeChunk<VEC> vx, vup;
-        vx.load(a.saved, u.cols, u.row);
-        if (gated)
-            vup.load(a.saved_up, u.cols, u.row);
-        vx.unpack(a.saved, x);
-        if (gated)
-            vup.unpack(a.saved_up, up);
-    } else {
-        Chunk<T, VEC> vx, vup;
-        vx.load(u.cols, a.x.data, u.row * a.x.stride, a.x.type);
-        if (gated)
-            vup.load(u.cols, a.up.data, u.row * a.up.stride, a.up.type);
-        vx.unpack(x);
-        if (gated)
-            vup.unpack(up);
-    }
-    vd.unpack(d);
-    float y[8], dup[8];
+    using Saved = std::conditional_t<PACKED, CodeChunk<VEC>, Chunk<T, VEC>>;
+    Chunk<T, VEC> vd[kUnits];
+    Saved vx[kUnits], vup[kUnits];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float f, slope;
-        value_and_slope<KIND, true>(x[k], f, slope);
-        dup[k] = __fmul_rn(d[k], f);
-        y[k] = gated ? __fmul_rn(f, up[k]) : f;
-        x[k] = __fmul_rn(gated ? __fmul_rn(d[k], up[k]) : d[k], slope);
+    for (int i = 0; i < kUnits; ++i) {
+        vd[i].load(u.cols[i], a.dout.data, u.row * a.dout.stride, a.dout.type);
+        if constexpr (PACKED) {
+            vx[i].load(a.saved, u.cols[i], u.row, lane);
+            if (gated)
+                vup[i].load(a.saved_up, u.cols[i], u.row, lane);
+        } else {
+            vx[i].load(u.cols[i], a.x.data, u.row * a.x.stride, a.x.type);
+            if (gated)
+                vup[i].load(u.cols[i], a.up.data, u.row * a.up.stride, a.up.type);
+        }
     }
-    store_typed<VEC>(u.cols, a.dx.data, u.row * a.dx.stride, a.dx.type, x);
-    if (gated && a.dup.data)
-        store_typed<VEC>(u.cols, a.dup.data, u.row * a.dup.stride, a.dup.type, dup);
-    if (a.again.data)
-        store_typed<VEC>(u.cols, a.again.data, u.row * a.again.stride, a.again.type, y);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        if (!u.on(i))
+            continue;
+        float x[8], up[8], d[8];
+        vd[i].unpack(d);
+        if constexpr (PACKED) {
+            vx[i].unpack(a.saved, x);
+            if (gated)
+                vup[i].unpack(a.saved_up, up);
+        } else {
+            vx[i].unpack(x);
+            if (gated)
+                vup[i].unpack(up);
+        }
+        float y[8], dup[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float2 f, slope;
+            value_and_slope<KIND, true>(pair_of(x, k), f, slope);
+            float2 g = pair_of(d, k);
+            set_pair(dup, k, mul2(g, f));
+            if (gated) {
+                g = mul2(g, pair_of(up, k));
+                f = mul2(f, pair_of(up, k));
+            }
+            set_pair(y, k, f);
+            set_pair(x, k, mul2(g, slope));
+        }
+        store_typed<VEC>(u.cols[i], a.dx.data, u.row * a.dx.stride, a.dx.type, x);
+        if (gated && a.dup.data)
+            store_typed<VEC>(u.cols[i], a.dup.data, u.row * a.dup.stride, a.dup.type, dup);
+        if (a.again.data)
+            store_typed<VEC>(u.cols[i], a.again.data, u.row * a.again.stride, a.again.type, y);
+    }
 }
 
 template <bool VEC>
 __global__ void __launch_bounds__(kBlock) k_unpack(const PackedRows x, const TypedRows out, const int64_t rows, const int64_t cols,
-                                                   const int64_t chunks)
+                                                   const int64_t spans)
 {
-    const Unit<VEC> u(rows, cols, chunks);
+    const Units<VEC> u(rows, cols, spans);
     wait_for_launch_before();
-    if (!u.on)
+    if (u.none())
         return;
-    CodeChunk<VEC> v;
-    v.load(x, u.cols, u.row);
-    float y[8];
-    v.unpack(x, y);
-    store_typed<VEC>(u.cols, out.data, u.row * out.stride, out.type, y);
+    CodeChunk<VEC> v[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+        v[i].load(x, u.cols[i], u.row, threadIdx.x & 31);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        float y[8];
+        v[i].unpack(x, y);
+        store_typed<VEC>(u.cols[i], out.data, u.row * out.stride, out.type, y);
+    }
 }
 
 struct Grid {
-    int64_t chunks, blocks;
+    int64_t spans, blocks;
     Grid(int64_t rows, int64_t cols)
     {
-        chunks = (cols + kChunk - 1) / kChunk;
-        blocks = (rows * chunks + kWarps - 1) / kWarps;
+        spans = (cols + kUnits * kChunk - 1) / (kUnits * kChunk);
+        blocks = (rows * spans + kWarps - 1) / kWarps;
     }
-    bool fits(int64_t rows) const { return blocks <= INT_MAX && (rows == 1 || chunks <= INT_MAX); }
+    bool fits(int64_t rows) const { return blocks <= INT_MAX && (rows == 1 || spans <= INT_MAX); }
 };
 
 template <typename T, bool VEC>
@@ -161,9 +222,9 @@ cudaError_t forward_t(const ActivationArgs& a, int kind, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     const unsigned blocks = static_cast<unsigned>(g.blocks);
     switch (kind) {
-    case LIONCUB_ACTIVATION_SILU: return launch_programmatic(k_activation<T, LIONCUB_ACTIVATION_SILU, VEC>, blocks, kBlock, 0, s, a, g.chunks);
-    case LIONCUB_ACTIVATION_GELU: return launch_programmatic(k_activation<T, LIONCUB_ACTIVATION_GELU, VEC>, blocks, kBlock, 0, s, a, g.chunks);
-    default: return launch_programmatic(k_activation<T, kIdentity, VEC>, blocks, kBlock, 0, s, a, g.chunks);
+    case LIONCUB_ACTIVATION_SILU: return launch_programmatic(k_activation<T, LIONCUB_ACTIVATION_SILU, VEC>, blocks, kBlock, 0, s, a, g.spans);
+    case LIONCUB_ACTIVATION_GELU: return launch_programmatic(k_activation<T, LIONCUB_ACTIVATION_GELU, VEC>, blocks, kBlock, 0, s, a, g.spans);
+    default: return launch_programmatic(k_activation<T, kIdentity, VEC>, blocks, kBlock, 0, s, a, g.spans);
     }
 }
 
@@ -175,8 +236,8 @@ cudaError_t backward_t(const ActivationArgs& a, int kind, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     const unsigned blocks = static_cast<unsigned>(g.blocks);
     return kind == LIONCUB_ACTIVATION_SILU
-               ? launch_programmatic(k_activation_grad<T, LIONCUB_ACTIVATION_SILU, PACKED, VEC>, blocks, kBlock, 0, s, a, g.chunks)
-               : launch_programmatic(k_activation_grad<T, LIONCUB_ACTIVATION_GELU, PACKED, VEC>, blocks, kBlock, 0, s, a, g.chunks);
+               ? launch_programmatic(k_activation_grad<T, LIONCUB_ACTIVATION_SILU, PACKED, VEC>, blocks, kBlock, 0, s, a, g.spans)
+               : launch_programmatic(k_activation_grad<T, LIONCUB_ACTIVATION_GELU, PACKED, VEC>, blocks, kBlock, 0, s, a, g.spans);
 }
 
 template <bool PACKED>
@@ -213,8 +274,8 @@ cudaError_t launch_unpack(const PackedRows& x, const TypedRows& out, int64_t row
     if (!g.fits(rows))
         return cudaErrorInvalidConfiguration;
     const unsigned blocks = static_cast<unsigned>(g.blocks);
-    return vec ? launch_programmatic(k_unpack<true>, blocks, kBlock, 0, s, x, out, rows, cols, g.chunks)
-               : launch_programmatic(k_unpack<false>, blocks, kBlock, 0, s, x, out, rows, cols, g.chunks);
+    return vec ? launch_programmatic(k_unpack<true>, blocks, kBlock, 0, s, x, out, rows, cols, g.spans)
+               : launch_programmatic(k_unpack<false>, blocks, kBlock, 0, s, x, out, rows, cols, g.spans);
 }
 
 }  // namespace lc

@@ -34,6 +34,7 @@ struct lioncub_rms_norm_s {
     // fault injection (environment, read at create; 0 = off)
     int64_t fail_launch_at = 0;
     std::atomic<int64_t> launch_count{0};
+    uint32_t first_wait_polls = 0;
 };
 
 struct lioncub_rotary_s {
@@ -201,7 +202,7 @@ lc::TypedRows typed(const lioncub_rows* m)
     return m ? lc::TypedRows{m->data, m->stride, m->type} : lc::TypedRows{nullptr, 0, LIONCUB_ROWS_BF16};
 }
 
-lc::PackedRows packed(const lioncub_packed* m)
+lc::PackedRows packed(const lioncub_packed* m, int64_t cols)
 {
     if (!m)
         return lc::PackedRows{};
@@ -209,7 +210,7 @@ lc::PackedRows packed(const lioncub_packed* m)
     for (int k = 5; k <= 8; ++k)
         if (m->group == 1 << k)
             log_group = k;
-    return lc::PackedRows{static_cast<uint8_t*>(m->codes), m->scales, m->stride, m->scale_stride, log_group, m->format == LIONCUB_CODES_E4M3};
+    return lc::PackedRows{static_cast<uint8_t*>(m->codes), m->scales, m->stride, m->scale_stride, cols, log_group, m->format == LIONCUB_CODES_E4M3};
 }
 
 // Matrices whose rows follow one another are one long row to the kernels that
@@ -402,6 +403,7 @@ int lioncub_rms_norm_create(lioncub_rms_norm_t* out, int64_t dim, float eps)
     h->dim = dim;
     h->eps = eps;
     h->fail_launch_at = lc::env_index("LIONCUB_FAIL_LAUNCH");
+    h->first_wait_polls = static_cast<uint32_t>(std::min<int64_t>(lc::env_index("LIONCUB_WAIT_POLLS"), 1 << 20));
     cudaError_t e = cudaGetDevice(&h->device);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&h->multiprocessors, cudaDevAttrMultiProcessorCount, h->device);
@@ -487,8 +489,8 @@ int lioncub_rms_norm_forward(lioncub_rms_norm_t h, int64_t n, const lioncub_rows
     a.weight = typed(weight);
     a.summed = typed(summed);
     a.out = typed(out);
-    a.saved = packed(saved);
-    a.packed = packed(packed_out);
+    a.saved = packed(saved, h->dim);
+    a.packed = packed(packed_out, h->dim);
     a.rstd = rstd;
     a.n = n;
     a.dim = static_cast<int32_t>(h->dim);
@@ -526,7 +528,9 @@ int lioncub_rms_norm_backward(lioncub_rms_norm_t h, int64_t n, const lioncub_row
     o.input("residual_grad", residual_grad, n, h->dim);
     o.result("dx", dx, n, h->dim);
     o.result("again", again, n, h->dim);
-    const bool vec = o.vec && h->dim % 8 == 0;  // the weight's gradient is moved element by element
+    // Rows are copied by 16 bytes, codes among them.  The weight's gradient is moved element by element.
+    const bool vec = o.vec && h->dim % (packed_saved ? 16 : 8) == 0 &&
+                     (!packed_saved || (reinterpret_cast<uintptr_t>(packed_saved->codes) | (n > 1 ? packed_saved->stride : 0)) % 16 == 0);
     o.input("weight_base", weight_base, 1, h->dim);
     o.result("weight_grad", weight_grad, 1, h->dim);
     int rc = o.finish();
@@ -541,12 +545,13 @@ int lioncub_rms_norm_backward(lioncub_rms_norm_t h, int64_t n, const lioncub_row
     a.dx = typed(dx);
     a.weight = typed(weight);
     a.again = typed(again);
-    a.packed = packed(packed_saved);
+    a.packed = packed(packed_saved, h->dim);
     a.rstd = rstd;
     a.partial = weight_grad ? h->partial : nullptr;
     a.partial_rows = h->multiprocessors;
     a.n = n;
     a.dim = static_cast<int32_t>(h->dim);
+    a.first_wait_polls = h->first_wait_polls;
     a.status = h->status;
     const int blocks = lc::norm_grad_blocks(n, a.dim, h->multiprocessors);
     cudaError_t e = launch(h, "rms_norm_grad", [&] { return lc::launch_norm_grad(a, blocks, vec, stream); });
@@ -583,12 +588,12 @@ int lioncub_pack8(int64_t rows, int64_t cols, const lioncub_rows* x, const lionc
     if (rows == 0 || cols == 0)
         return LIONCUB_OK;
     if (out->group == 0)
-        return finish_launch(lc::launch_pack_rows(typed(x), packed(out), rows, static_cast<int>(cols), o.vec && cols % 8 == 0, stream),
+        return finish_launch(lc::launch_pack_rows(typed(x), packed(out, cols), rows, static_cast<int>(cols), o.vec && cols % 8 == 0, stream),
                              "pack launch");
     lc::ActivationArgs a{};
     const bool vec = as_one_row(o, rows, cols);
     a.x = typed(x);
-    a.saved = packed(out);
+    a.saved = packed(out, cols);
     a.rows = rows;
     a.cols = cols;
     return finish_launch(lc::launch_activation(a, lc::kIdentity, vec, stream), "pack launch");
@@ -607,7 +612,7 @@ int lioncub_unpack8(int64_t rows, int64_t cols, const lioncub_packed* x, const l
     if (rc != LIONCUB_OK)
         return rc;
     const bool vec = as_one_row(o, rows, cols);
-    return finish_launch(lc::launch_unpack(packed(x), typed(out), rows, cols, vec, stream), "unpack launch");
+    return finish_launch(lc::launch_unpack(packed(x, cols), typed(out), rows, cols, vec, stream), "unpack launch");
 }
 
 // ---- the activation --------------------------------------------------------------------------
@@ -644,8 +649,8 @@ int lioncub_activation_forward(int64_t rows, int64_t cols, int kind, const lionc
     a.x = typed(x);
     a.up = typed(up);
     a.out = typed(out);
-    a.saved = packed(saved);
-    a.saved_up = packed(saved_up);
+    a.saved = packed(saved, cols);
+    a.saved_up = packed(saved_up, cols);
     a.rows = rows;
     a.cols = cols;
     return finish_launch(lc::launch_activation(a, kind, vec, stream), "activation launch");
@@ -686,8 +691,8 @@ int lioncub_activation_backward(int64_t rows, int64_t cols, int kind, const lion
     a.dout = typed(dout);
     a.x = typed(x);
     a.up = typed(up);
-    a.saved = packed(packed_x);
-    a.saved_up = packed(packed_up);
+    a.saved = packed(packed_x, cols);
+    a.saved_up = packed(packed_up, cols);
     a.dx = typed(dx);
     a.dup = typed(dup);
     a.again = typed(again);
@@ -803,7 +808,7 @@ int lioncub_rotary_apply(lioncub_rotary_t h, const lioncub_sequences* places, co
     const lioncub_heads* in[2] = {q, k};
     const lioncub_heads* to[2] = {q_out, k_out};
     static const char* const names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
-    bool vec = h->head_dim % 8 == 0 && (h->interleaved ? h->rotary_dim % 8 : h->rotary_dim % 16) == 0;
+    bool vec = h->head_dim % 8 == 0 && h->rotary_dim % 16 == 0;
     bool copy = false;
     for (int i = 0; i < 2 && in[i]; ++i) {
         int rc = check_heads(names[i][0], in[i], p, h->head_dim, false, &vec);

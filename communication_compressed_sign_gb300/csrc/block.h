@@ -22,6 +22,7 @@ struct PackedRows {
     uint8_t* codes;
     float* scales;
     int64_t stride, scale_stride;
+    int64_t cols;
     int32_t log_group;
     int32_t e4m3;  // else whole numbers
 };
@@ -32,8 +33,9 @@ struct NormArgs {
     float* rstd;
     int64_t n;
     int32_t dim;
-    int32_t warps;  // of a row; set by launch_norm
+    int32_t warps;  // of a row; set by launch_norm, per_column too
     float eps;
+    float per_column;  // 1 / dim
     int* status;
 };
 
@@ -45,7 +47,11 @@ struct NormGradArgs {
     int64_t partial_rows;
     int64_t n;
     int32_t dim;
-    int32_t warps, teams;  // warps of a row, rows at once in a block; set by launch_norm_grad
+    // set by launch_norm_grad: warps of a row, rows at once in a block, rows in flight for each
+    // of those, bytes of such a row and where its parts begin, 1 / dim
+    int32_t warps, teams, slots, slot_bytes, at_saved, at_residual;
+    float per_column;
+    uint32_t first_wait_polls;  // fault injection: >0 caps the first wait for copies at this many polls
     int* status;
 };
 
@@ -81,7 +87,6 @@ struct RotaryArgs {
     int32_t wide;  // positions are int64, else int32
     int32_t head_dim, pairs;
     int32_t copy;  // columns behind the rotated ones are copied
-    int32_t groups;  // threads that share a place's heads; set by launch_rotary
     float cos_factor, sin_factor;
 };
 
@@ -98,6 +103,6 @@ constexpr int kIdentity = -1;
 cudaError_t launch_activation(const ActivationArgs& a, int kind, bool vec, cudaStream_t s);
 cudaError_t launch_activation_grad(const ActivationArgs& a, int kind, bool vec, cudaStream_t s);
 cudaError_t launch_unpack(const PackedRows& x, const TypedRows& out, int64_t rows, int64_t cols, bool vec, cudaStream_t s);
-cudaError_t launch_rotary(RotaryArgs a, int type, bool interleaved, bool vec, cudaStream_t s);
+cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, bool vec, cudaStream_t s);
 
 }  // namespace lc

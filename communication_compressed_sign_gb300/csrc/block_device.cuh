@@ -6,6 +6,8 @@
 
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "block.h"
 #include "embed_device.cuh"
 
@@ -19,17 +21,91 @@ template <bool VEC>
 struct Columns {
     int64_t at;
     int count;
+    bool whole;  // all of the chunk's columns are there
     Columns() = default;
     __device__ __forceinline__ Columns(int64_t first, int lane, int64_t cols)
     {
         at = first + (VEC ? lane * 8 : lane);
         const int64_t left = cols - at;
+        whole = cols - first >= kChunk;
         if (VEC)
             count = left > 0 ? 8 : 0;
         else
             count = left <= 0 ? 0 : left > 224 ? 8 : static_cast<int>((left + 31) >> 5);
     }
 };
+
+// --- fp32 pairs ---------------------------------------------------------------------------
+//
+// These kernels move so few bytes an element that instructions bound them before
+// memory does, so arithmetic is done two elements an instruction.  The assembler
+// fuses a paired product with a paired sum that takes it, whatever their rounding
+// modifiers say: what must be rounded between is written as an fma, or its product
+// goes elsewhere.
+#define LC_PAIR_OP2(name, op)                                                                                            \
+    __device__ __forceinline__ float2 name(float2 x, float2 y)                                                           \
+    {                                                                                                                    \
+        float2 d;                                                                                                        \
+        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t" op " a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}" \
+            : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));                                            \
+        return d;                                                                                                        \
+    }
+LC_PAIR_OP2(add2, "add.rn.f32x2")
+LC_PAIR_OP2(mul2, "mul.rn.f32x2")
+#undef LC_PAIR_OP2
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair_of(const float (&x)[8], int k) { return make_float2(x[2 * k], x[2 * k + 1]); }
+__device__ __forceinline__ void set_pair(float (&x)[8], int k, float2 v)
+{
+    x[2 * k] = v.x;
+    x[2 * k + 1] = v.y;
+}
+
+// --- sums and maxima over a row -------------------------------------------------------------
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int by = 16; by; by >>= 1)
+        v = __fadd_rn(v, __shfl_xor_sync(kAll, v, by));
+    return v;
+}
+
+// The largest magnitude of 8 elements, as the bits of a float: infinities come after all
+// finite ones and NaN after those, so a maximum of these numbers keeps them.
+__device__ __forceinline__ uint32_t largest_of(const float (&x)[8])
+{
+    float a, b, c;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(b), "f"(c), "f"(c));
+    return __float_as_uint(a);
+}
+
+// The largest over each group of 2^log_lanes lanes, at least 4.  (Masked warp
+// reductions run once for each group: 32 columns a group took 31 M warp
+// instructions on 8192 x 4096 elements, these 15 M.)
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int log_lanes)
+{
+    v = max(v, __shfl_xor_sync(kAll, v, 1));
+    v = max(v, __shfl_xor_sync(kAll, v, 2));
+    if (log_lanes >= 3)
+        v = max(v, __shfl_xor_sync(kAll, v, 4));
+    if (log_lanes >= 4)
+        v = max(v, __shfl_xor_sync(kAll, v, 8));
+    if (log_lanes >= 5)
+        v = max(v, __shfl_xor_sync(kAll, v, 16));
+    return v;
+}
 
 // --- a lane's 8 elements ----------------------------------------------------------------
 
@@ -48,25 +124,46 @@ struct Chunk<T, true> {
             g = Group8<T>{};
     }
     __device__ __forceinline__ void unpack(float (&x)[8]) const { g.unpack(x); }
+    // the bits of the largest magnitude (see largest_of)
+    __device__ __forceinline__ uint32_t largest() const
+    {
+        if constexpr (sizeof(T) == 2) {
+            uint32_t a, b;
+            asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(g.raw.x), "r"(g.raw.y));
+            asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(g.raw.z), "r"(g.raw.w));
+            asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+            return max(a << 16 & 0x7fffffffu, a & 0x7fff0000u);
+        } else {
+            float x[8];
+            g.unpack(x);
+            return largest_of(x);
+        }
+    }
 };
 
 // Scalar moves are of a type that the launch gives: their widening is no burden.
 template <typename T>
 struct Chunk<T, false> {
     float x[8];
+    template <typename E>
+    __device__ __forceinline__ void load_of(const Columns<false>& c, const E* p)
+    {
+        if (c.whole) {  // without a comparison for each
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = static_cast<float>(p[32 * k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = k < c.count ? static_cast<float>(p[32 * k]) : 0.0f;
+        }
+    }
     __device__ __forceinline__ void load(const Columns<false>& c, const void* base, int64_t e, int type)
     {
-        if (type == LIONCUB_ROWS_BF16) {
-            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + e + c.at;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                x[k] = k < c.count ? __bfloat162float(p[32 * k]) : 0.0f;
-        } else {
-            const float* p = static_cast<const float*>(base) + e + c.at;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                x[k] = k < c.count ? p[32 * k] : 0.0f;
-        }
+        if (type == LIONCUB_ROWS_BF16)
+            load_of(c, static_cast<const __nv_bfloat16*>(base) + e + c.at);
+        else
+            load_of(c, static_cast<const float*>(base) + e + c.at);
     }
     __device__ __forceinline__ void unpack(float (&y)[8]) const
     {
@@ -74,6 +171,7 @@ struct Chunk<T, false> {
         for (int k = 0; k < 8; ++k)
             y[k] = x[k];
     }
+    __device__ __forceinline__ uint32_t largest() const { return 0; }  // not used
 };
 
 // Loads and stores of a type that the launch gives.
@@ -106,34 +204,26 @@ __device__ __forceinline__ void store_typed(const Columns<VEC>& c, void* base, i
             g.pack(x);
             g.store(base, e + c.at);
         }
-    } else if (type == LIONCUB_ROWS_BF16) {
-        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + e + c.at;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < c.count)
-                p[32 * k] = __float2bfloat16_rn(x[k]);
     } else {
-        float* p = static_cast<float*>(base) + e + c.at;
+        const auto store = [&](auto* p) {
+            using E = std::remove_pointer_t<decltype(p)>;
+            if (c.whole) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < c.count)
-                p[32 * k] = x[k];
+                for (int k = 0; k < 8; ++k)
+                    p[32 * k] = static_cast<E>(x[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < c.count)
+                        p[32 * k] = static_cast<E>(x[k]);
+            }
+        };
+        if (type == LIONCUB_ROWS_BF16)
+            store(static_cast<__nv_bfloat16*>(base) + e + c.at);
+        else
+            store(static_cast<float*>(base) + e + c.at);
     }
 }
-
-// --- sums and maxima over a row -------------------------------------------------------------
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int by = 16; by; by >>= 1)
-        v = __fadd_rn(v, __shfl_xor_sync(kAll, v, by));
-    return v;
-}
-
-// Magnitudes are compared as the numbers that their bits are: infinities come
-// after all finite ones and NaN after those, so a maximum keeps them.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // --- codes of 8 bits --------------------------------------------------------------------------
 
@@ -143,93 +233,134 @@ struct GroupScale {
     bool bad;
     __device__ __forceinline__ GroupScale(uint32_t largest, bool e4m3)
     {
+        constexpr uint32_t kSmallest = 0x0d800000u, kInfinity = 0x7f800000u;  // 2^-100
         const float a = __uint_as_float(largest);
-        bad = largest >= 0x7f800000u;
-        const bool none = bad || a < 0x1p-100f;
-        inv = none ? 0.0f : __fdiv_rn(e4m3 ? 448.0f : 127.0f, a);
-        scale = bad ? __uint_as_float(0x7fffffffu) : none ? 0.0f : __fmul_rn(a, e4m3 ? 1.0f / 448.0f : 1.0f / 127.0f);
+        const bool some = largest - kSmallest < kInfinity - kSmallest;
+        bad = largest >= kInfinity;
+        inv = some ? __fdiv_rn(e4m3 ? 448.0f : 127.0f, a) : 0.0f;
+        scale = some ? __fmul_rn(a, e4m3 ? 1.0f / 448.0f : 1.0f / 127.0f) : __uint_as_float(bad ? 0x7fffffffu : 0u);
     }
 };
 
-// Four codes, the first in the lowest byte.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const GroupScale& s, bool e4m3)
+// Eight codes, the first in the lowest byte.  The paths are kept apart by asm
+// that may not be moved: computing both and choosing costs more than the branch.
+__device__ __forceinline__ uint32_t e4m3_pairs(float2 a, float2 b)
 {
-    a = __fmul_rn(a, s.inv);
-    b = __fmul_rn(b, s.inv);
-    c = __fmul_rn(c, s.inv);
-    d = __fmul_rn(d, s.inv);
     uint32_t w;
+    asm volatile("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+                 "mov.b32 %0, {lo, hi};\n\t}" : "=r"(w) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return w;
+}
+// 1.5 * 2^23 more is rounded to a whole number, whose two's complement is then the lowest bits
+__device__ __forceinline__ uint32_t int8_pairs(float2 a, float2 b, float2 inv)
+{
+    const float2 magic = both(12582912.0f);
+    a = fma2(a, inv, magic);
+    b = fma2(b, inv, magic);
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const GroupScale& s, bool e4m3)
+{
+    uint2 w;
+    const float2 inv = both(s.inv);
     if (e4m3) {
-        w = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
-            static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
-    } else {  // adding 1.5 * 2^23 rounds to a whole number, whose two's complement is then the lowest bits
-        const float magic = 12582912.0f;
-        const uint32_t ab = __byte_perm(__float_as_uint(__fadd_rn(a, magic)), __float_as_uint(__fadd_rn(b, magic)), 0x0040);
-        const uint32_t cd = __byte_perm(__float_as_uint(__fadd_rn(c, magic)), __float_as_uint(__fadd_rn(d, magic)), 0x0040);
-        w = __byte_perm(ab, cd, 0x5410);
+        w.x = e4m3_pairs(mul2(pair_of(x, 0), inv), mul2(pair_of(x, 1), inv));
+        w.y = e4m3_pairs(mul2(pair_of(x, 2), inv), mul2(pair_of(x, 3), inv));
+    } else {
+        w.x = int8_pairs(pair_of(x, 0), pair_of(x, 1), inv);
+        w.y = int8_pairs(pair_of(x, 2), pair_of(x, 3), inv);
     }
-    return s.bad ? 0 : w;
+    if (s.bad)
+        w = make_uint2(0, 0);
+    return w;
 }
 
-// What four codes are, without their scale.
-__device__ __forceinline__ void numbers4(uint32_t w, bool e4m3, float& a, float& b, float& c, float& d)
+// One code.
+__device__ __forceinline__ uint8_t code1(float x, float inv, bool bad, bool e4m3)
+{
+    uint32_t w;
+    if (e4m3)
+        w = __nv_cvt_float_to_fp8(__fmul_rn(x, inv), __NV_SATFINITE, __NV_E4M3);
+    else
+        w = __float_as_uint(fmaf(x, inv, 12582912.0f));
+    return static_cast<uint8_t>(bad ? 0 : w);
+}
+
+// What eight codes stand for.
+__device__ __forceinline__ void restore4(uint32_t w, bool e4m3, float scale, float2& a, float2& b)
 {
     if (e4m3) {
-        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffff), __NV_E4M3);
-        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-        const float2 p = __half22float2(__half2(lo)), q = __half22float2(__half2(hi));
-        a = p.x; b = p.y; c = q.x; d = q.y;
+        a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffff), __NV_E4M3)));
+        b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)));
     } else {  // the byte + 128 as the lowest bits of 2^23 + it
         w ^= 0x80808080u;
-        const float off = 8388736.0f;
-        a = __fsub_rn(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)), off);
-        b = __fsub_rn(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)), off);
-        c = __fsub_rn(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)), off);
-        d = __fsub_rn(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)), off);
+        const float2 off = both(-8388736.0f);
+        a = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)), __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441))), off);
+        b = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)), __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443))), off);
     }
+    a = mul2(a, both(scale));
+    b = mul2(b, both(scale));
+}
+__device__ __forceinline__ void restore8(uint2 w, bool e4m3, float scale, float (&x)[8])
+{
+    float2 a, b;
+    restore4(w.x, e4m3, scale, a, b);
+    set_pair(x, 0, a);
+    set_pair(x, 1, b);
+    restore4(w.y, e4m3, scale, a, b);
+    set_pair(x, 2, a);
+    set_pair(x, 3, b);
+}
+
+// What one code stands for.
+__device__ __forceinline__ float restore1(uint32_t code, bool e4m3, float scale)
+{
+    const float v = e4m3 ? __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)))
+                         : __fsub_rn(__uint_as_float((code ^ 0x80u) | 0x4b000000u), 8388736.0f);
+    return __fmul_rn(v, scale);
 }
 
 // Codes and scales of a chunk of a row whose groups lie inside chunks; x holds
-// zeros where there are no columns.
+// zeros where there are no columns.  largest: of x (VEC).
 template <bool VEC>
-__device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VEC>& c, int64_t row, const float (&x)[8], int lane)
+__device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VEC>& c, int64_t row, const float (&x)[8], uint32_t largest,
+                                           int lane)
 {
     float* scales = p.scales + row * p.scale_stride;
     uint8_t* codes = p.codes + row * p.stride + c.at;
     const bool e4m3 = p.e4m3;
-    uint32_t m[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        m[k] = magnitude(x[k]);
     if constexpr (VEC) {
-        uint32_t largest = max(max(max(m[0], m[1]), max(m[2], m[3])), max(max(m[4], m[5]), max(m[6], m[7])));
-        const int lanes = 1 << (p.log_group - 3);  // of a group
-        for (int by = lanes >> 1; by; by >>= 1)
-            largest = max(largest, __shfl_xor_sync(kAll, largest, by));
-        const GroupScale s(largest, e4m3);
+        const int log_lanes = p.log_group - 3;  // of a group
+        const GroupScale s(lanes_max(largest, log_lanes), e4m3);
+        const uint2 w = codes8(x, s, e4m3);
         if (c.count) {
-            *reinterpret_cast<uint2*>(codes) = make_uint2(codes4(x[0], x[1], x[2], x[3], s, e4m3), codes4(x[4], x[5], x[6], x[7], s, e4m3));
-            if ((lane & (lanes - 1)) == 0)
+            *reinterpret_cast<uint2*>(codes) = w;
+            if ((lane & ((1 << log_lanes) - 1)) == 0)
                 scales[c.at >> p.log_group] = s.scale;
         }
-    } else {  // a group is 32 lanes wide and 1 to 8 values deep
-        const int deep = 1 << (p.log_group - 5);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            m[k] = __reduce_max_sync(kAll, m[k]);
+    } else {
+        // A group is 32 lanes wide and 1 to 8 values deep.  Lane k works out the scale of
+        // the group of value k, and the warp takes it from there.
+        const int deep = 1 << (p.log_group - 5), mine = lane & 7;
+        uint32_t m = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            uint32_t largest = 0;
+            const uint32_t all = __reduce_max_sync(kAll, __float_as_uint(x[k]) & 0x7fffffffu);
+            m = mine == k ? all : m;
+        }
+        for (int by = 1; by < deep; by <<= 1)
+            m = max(m, __shfl_xor_sync(kAll, m, by));
+        const GroupScale s(m, e4m3);
+        const uint32_t bad = __ballot_sync(kAll, s.bad);
+        const int64_t at = c.at - lane + 32 * mine;  // the first column of value `mine`
+        if (lane < 8 && (mine & (deep - 1)) == 0 && at < p.cols)
+            scales[at >> p.log_group] = s.scale;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if ((j ^ k) < deep)  // deep is a power of two: the same group
-                    largest = max(largest, m[j]);
-            const GroupScale s(largest, e4m3);
-            if (k < c.count) {
-                codes[32 * k] = static_cast<uint8_t>(codes4(x[k], 0.0f, 0.0f, 0.0f, s, e4m3));
-                if (lane == 0 && (k & (deep - 1)) == 0)
-                    scales[(c.at + 32 * k) >> p.log_group] = s.scale;
-            }
+        for (int k = 0; k < 8; ++k) {
+            const float inv = __shfl_sync(kAll, s.inv, k);
+            if (k < c.count)
+                codes[32 * k] = code1(x[k], inv, bad >> k & 1, e4m3);
         }
     }
 }
@@ -243,16 +374,16 @@ __device__ __forceinline__ void pack_chunk_of_row(const PackedRows& p, const Col
     const bool e4m3 = p.e4m3;
     if constexpr (VEC) {
         if (c.count)
-            *reinterpret_cast<uint2*>(codes) = make_uint2(codes4(x[0], x[1], x[2], x[3], s, e4m3), codes4(x[4], x[5], x[6], x[7], s, e4m3));
+            *reinterpret_cast<uint2*>(codes) = codes8(x, s, e4m3);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < c.count)
-                codes[32 * k] = static_cast<uint8_t>(codes4(x[k], 0.0f, 0.0f, 0.0f, s, e4m3));
+                codes[32 * k] = code1(x[k], s.inv, s.bad, e4m3);
     }
 }
 
-// A lane's 8 codes of a chunk and their scales, as they lie in memory.
+// A lane's 8 codes of a chunk and their scales.
 template <bool VEC>
 struct CodeChunk;
 
@@ -260,7 +391,7 @@ template <>
 struct CodeChunk<true> {
     uint2 w;
     float scale;
-    __device__ __forceinline__ void load(const PackedRows& p, const Columns<true>& c, int64_t row)
+    __device__ __forceinline__ void load(const PackedRows& p, const Columns<true>& c, int64_t row, int)
     {
         w = make_uint2(0, 0);
         scale = 0.0f;
@@ -269,38 +400,28 @@ struct CodeChunk<true> {
             scale = p.scales[row * p.scale_stride + (c.at >> p.log_group)];
         }
     }
-    __device__ __forceinline__ void unpack(const PackedRows& p, float (&x)[8]) const
-    {
-        numbers4(w.x, p.e4m3, x[0], x[1], x[2], x[3]);
-        numbers4(w.y, p.e4m3, x[4], x[5], x[6], x[7]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            x[k] = __fmul_rn(x[k], scale);
-    }
+    __device__ __forceinline__ void unpack(const PackedRows& p, float (&x)[8]) const { restore8(w, p.e4m3, scale, x); }
 };
 
 template <>
 struct CodeChunk<false> {
-    float x[8];
-    __device__ __forceinline__ void load(const PackedRows& p, const Columns<false>& c, int64_t row)
+    uint8_t code[8];
+    float scale;  // of value lane % 8
+    __device__ __forceinline__ void load(const PackedRows& p, const Columns<false>& c, int64_t row, int lane)
     {
         const uint8_t* codes = p.codes + row * p.stride + c.at;
-        const float* scales = p.scales + row * p.scale_stride;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x[k] = 0.0f;
-            if (k < c.count) {
-                float v, unused;
-                numbers4(codes[32 * k], p.e4m3, v, unused, unused, unused);
-                x[k] = __fmul_rn(v, scales[(c.at + 32 * k) >> p.log_group]);
-            }
-        }
-    }
-    __device__ __forceinline__ void unpack(const PackedRows&, float (&y)[8]) const
-    {
+        const int64_t at = c.at - lane + 32 * (lane & 7);
+        scale = at < p.cols ? p.scales[row * p.scale_stride + (at >> p.log_group)] : 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            y[k] = x[k];
+            code[k] = k < c.count ? codes[32 * k] : 0;
+    }
+    __device__ __forceinline__ void unpack(const PackedRows& p, float (&y)[8]) const
+    {
+        const bool e4m3 = p.e4m3;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            y[k] = restore1(code[k], e4m3, __shfl_sync(kAll, scale, k));
     }
 };
 

@@ -50,15 +50,13 @@ __device__ __forceinline__ void pack_row(const PackedRows& p, const Columns<VEC>
     if (p.log_group != kRowGroup) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            pack_chunk<VEC>(p, cols[c], row, x[c], lane);
+            pack_chunk<VEC>(p, cols[c], row, x[c], largest_of(x[c]), lane);
         return;
     }
     uint32_t largest = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            largest = max(largest, magnitude(x[c][k]));
+        largest = max(largest, largest_of(x[c]));
     const GroupScale s(row_max(largest, shared, warps, warp, lane), p.e4m3);
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -67,7 +65,7 @@ __device__ __forceinline__ void pack_row(const PackedRows& p, const Columns<VEC>
         p.scales[row * p.scale_stride] = s.scale;
 }
 
-// A row is that of `warps` warps, C chunks each: warp w has chunks w, w + warps, ...
+// A row is that of `warps` warps, C neighbouring chunks each.
 template <typename XT, typename RT, int C, bool VEC>
 __global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__ NormArgs a)
 {
@@ -82,7 +80,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__
     Columns<VEC> cols[C];
 #pragma unroll
     for (int c = 0; c < C; ++c)
-        cols[c] = Columns<VEC>((warp + c * warps) * kChunk, lane, a.dim);
+        cols[c] = Columns<VEC>((warp * C + c) * kChunk, lane, a.dim);
 
     float h[C][8];
     {
@@ -101,8 +99,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__
                 x[c].unpack(h[c]);
                 r[c].unpack(y);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    h[c][k] = __fadd_rn(h[c][k], y[k]);
+                for (int k = 0; k < 4; ++k)
+                    set_pair(h[c], k, add2(pair_of(h[c], k), pair_of(y, k)));
             }
         } else {
 #pragma unroll
@@ -115,14 +113,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__
         for (int c = 0; c < C; ++c)
             store_typed<VEC>(cols[c], a.summed.data, row * a.summed.stride, a.summed.type, h[c]);
 
-    float sum = 0.0f;
+    float2 squares = both(0.0f);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            sum = fmaf(h[c][k], h[c][k], sum);
+        for (int k = 0; k < 4; ++k)
+            squares = fma2(pair_of(h[c], k), pair_of(h[c], k), squares);
+    float sum = __fadd_rn(squares.x, squares.y);
     sum = row_sum(sum, sums, warps, warp, lane);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.dim)), a.eps)));
+    const float rstd = rsqrtf(fmaf(sum, a.per_column, a.eps));
     if (a.rstd && warp == 0 && lane == 0)
         a.rstd[row] = rstd;
     if (a.saved.codes)
@@ -131,14 +130,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            h[c][k] = __fmul_rn(h[c][k], rstd);
+        for (int k = 0; k < 4; ++k)
+            set_pair(h[c], k, mul2(pair_of(h[c], k), both(rstd)));
         if (a.weight.data) {
             float w[8];
             load_typed<VEC>(cols[c], a.weight.data, 0, a.weight.type, w);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                h[c][k] = __fmul_rn(h[c][k], w[k]);
+            for (int k = 0; k < 4; ++k)
+                set_pair(h[c], k, mul2(pair_of(h[c], k), pair_of(w, k)));
         }
     }
     if (a.packed.codes) {
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) k_pack_rows(const TypedRows x,
     float h[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        cols[c] = Columns<VEC>((warp + c * warps) * kChunk, lane, dim);
+        cols[c] = Columns<VEC>((warp * C + c) * kChunk, lane, dim);
         v[c].load(cols[c], x.data, row * x.stride, x.type);
     }
 #pragma unroll
@@ -175,15 +174,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32) k_pack_rows(const TypedRows x,
     pack_row<C, VEC>(out, cols, row, h, maxima, warps, warp, lane);
 }
 
-// How a row of `dim` columns is spread: C chunks for each of `warps` warps.
+// How a row of `dim` columns is spread: C chunks for each of `warps` warps.  Two,
+// but one while there are few chunks in all, whose rows are then done sooner (8
+// rows of 768: 1.5 us, with two 2.0, with three 2.9; 8192 rows onto an fp32
+// residual 12.8, 13.6, 14.0), though not of wide rows, whose barriers then cost more
+// (2048 rows of 2048: 6.6 and 6.2; 65536: 170 and 139).
 struct Spread {
     int c, warps;
-    explicit Spread(int dim)
+    Spread(int64_t rows, int dim)
     {
         const int chunks = (dim + kChunk - 1) / kChunk;
-        c = chunks <= 4 ? chunks : 2;
-        if (chunks > 2 * kMaxWarps)
-            c = 4;
+        const int64_t all = rows * chunks;
+        c = chunks <= kMaxWarps && (all <= 4096 || (chunks <= 4 && all <= 32768)) ? 1 : chunks <= 2 * kMaxWarps ? 2 : 4;
+        c = c < chunks ? c : chunks;
         warps = (chunks + c - 1) / c;
     }
 };
@@ -195,7 +198,6 @@ cudaError_t with_chunks(int c, F&& f)
     switch (c) {
     case 1: return f(std::integral_constant<int, 1>());
     case 2: return f(std::integral_constant<int, 2>());
-    case 3: return f(std::integral_constant<int, 3>());
     default: return f(std::integral_constant<int, 4>());
     }
 }
@@ -217,8 +219,9 @@ cudaError_t launch_norm(NormArgs a, bool vec, cudaStream_t s)
 {
     if (a.n == 0)
         return cudaSuccess;
-    const Spread spread(a.dim);
+    const Spread spread(a.n, a.dim);
     a.warps = spread.warps;
+    a.per_column = 1.0f / static_cast<float>(a.dim);
     if (!vec)
         return launch_t<float, float, false>(a, spread.c, s);
     const bool xb = a.x.type == LIONCUB_ROWS_BF16, rb = a.residual.type == LIONCUB_ROWS_BF16;
@@ -229,7 +232,7 @@ cudaError_t launch_norm(NormArgs a, bool vec, cudaStream_t s)
 
 cudaError_t launch_pack_rows(const TypedRows& x, const PackedRows& out, int64_t rows, int dim, bool vec, cudaStream_t s)
 {
-    const Spread spread(dim);
+    const Spread spread(rows, dim);
     return with_chunks(spread.c, [&](auto n) {
         constexpr int C = decltype(n)::value;
         const unsigned blocks = row_blocks(rows, spread.warps);

@@ -3,66 +3,161 @@
 //   dx = residual_grad + rstd * (g - n * mean(g * n)),  again = n * weight,
 //   weight_grad_j = weight_base_j + sum over rows of dout * n.
 //
-// Memory-bound.  A team of warps takes a row, whose chunks stay in registers
-// across the one sum over the row.  Teams walk over rows (persistent blocks, one
+// Memory-bound.  A team of warps takes a row at a time, with one sum over the row
+// between reading and writing it.  Teams walk over rows (persistent blocks, one
 // for each multiprocessor), so that a column's share of the weight's gradient
-// stays in registers too; a block adds its teams' in order and leaves one row of
-// sums, and a second launch adds those of all blocks in order.
+// stays in a register; a thread of the team has the next rows brought into a
+// ring in shared memory by bulk copies meanwhile.  A block adds its teams'
+// columns in order and leaves one row of sums, and a second launch adds those of
+// all blocks in order.
 #include "block_device.cuh"
 
 namespace lc {
 namespace {
 
-constexpr int kMaxWarps = 16;    // of a row
-constexpr int kBlockWarps = 16;  // of a block
+constexpr int kBlockWarps = 16;
+constexpr int kMaxSlots = 8;              // rows of a team in flight
+constexpr int kRingBytes = 208 * 1024;    // at most
+constexpr uint32_t kWaitLimit = 1u << 20;  // polls
 
-// Where h comes from.
+// Where h comes from; scalar reads go by the type that the launch gives.
 enum Source { kFromBf16, kFromF32, kFromCodes };
 
-template <int SOURCE, bool VEC>
-struct SavedChunk {
-    std::conditional_t<SOURCE == kFromCodes, CodeChunk<VEC>, Chunk<std::conditional_t<SOURCE == kFromBf16, __nv_bfloat16, float>, VEC>> v;
-    __device__ __forceinline__ void load(const NormGradArgs& a, const Columns<VEC>& c, int64_t row)
-    {
-        if constexpr (SOURCE == kFromCodes)
-            v.load(a.packed, c, row);
-        else
-            v.load(c, a.saved.data, row * a.saved.stride, a.saved.type);
-    }
-    __device__ __forceinline__ void unpack(const NormGradArgs& a, float (&x)[8]) const
-    {
-        if constexpr (SOURCE == kFromCodes)
-            v.unpack(a.packed, x);
-        else
-            v.unpack(x);
-    }
-};
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// What a team reads of a row.
-template <typename DT, typename GT, int SOURCE, int C, bool VEC>
-struct RowInputs {
-    Chunk<DT, VEC> dout[C];
-    SavedChunk<SOURCE, VEC> saved[C];
-    Chunk<GT, VEC> residual[C];
-    float rstd;
-    __device__ __forceinline__ void load(const NormGradArgs& a, const Columns<VEC> (&cols)[C], int64_t row)
-    {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            dout[c].load(cols[c], a.dout.data, row * a.dout.stride, a.dout.type);
-            saved[c].load(a, cols[c], row);
-        }
-        rstd = a.rstd[row];
-        if (a.residual_grad.data)
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                residual[c].load(cols[c], a.residual_grad.data, row * a.residual_grad.stride, a.residual_grad.type);
-    }
-};
+// Waits for a phase of a barrier, for a bounded time; false when it gave up.
+__device__ __forceinline__ bool wait_phase(uint32_t barrier, uint32_t parity)
+{
+    uint32_t ok = 0;
+    for (uint32_t i = 0; i < kWaitLimit && !ok; ++i)
+        asm volatile("{\n .reg .pred P;\n mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.u32 %0, 1, 0, P;\n}"
+                     : "=r"(ok) : "r"(barrier), "r"(parity) : "memory");
+    return ok != 0;
+}
+// The same with at most `polls` tests that return at once: the stand-in for a wait
+// that runs out, and all that is left after one did.
+__device__ __forceinline__ bool test_phase(uint32_t barrier, uint32_t parity, uint32_t polls)
+{
+    uint32_t ok = 0;
+    for (uint32_t i = 0; i < polls && !ok; ++i)
+        asm volatile("{\n .reg .pred P;\n mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.u32 %0, 1, 0, P;\n}"
+                     : "=r"(ok) : "r"(barrier), "r"(parity) : "memory");
+    return ok != 0;
+}
 
+// Meets the warps of a team, whose earlier reads and writes of shared memory are then done.
 __device__ __forceinline__ void team_barrier(int team, int warps)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
+    if (warps == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
+}
+
+// A matrix whose rows are brought into shared memory: those of a slot start `at`
+// bytes behind the slot's start, on a 16-byte boundary of memory.
+struct Stream {
+    const char* base;
+    int64_t step;  // bytes between rows
+    int32_t bytes;  // of a row; 0: no such matrix
+    int32_t at;
+};
+
+// The slot of a row that starts `shift` bytes behind a boundary has it `shift`
+// bytes behind its own start.
+__device__ __forceinline__ int shift_of(const Stream& m, int64_t row) { return static_cast<int>(reinterpret_cast<uintptr_t>(m.base + row * m.step) & 15); }
+
+// Bytes that the copies of a row bring: whole 16-byte pieces, but none that lies
+// partly before the matrix's first or behind its last element.
+struct Window {
+    const char *row, *from, *to;
+    __device__ __forceinline__ Window(const Stream& m, int64_t i, int64_t n)
+    {
+        constexpr uintptr_t kPiece = 15;
+        row = m.base + i * m.step;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(row), first = reinterpret_cast<uintptr_t>(m.base);
+        const uintptr_t last = first + (n - 1) * m.step + m.bytes;
+        const uintptr_t low = max(a & ~kPiece, (first + kPiece) & ~kPiece), high = min((a + m.bytes + kPiece) & ~kPiece, last & ~kPiece);
+        from = reinterpret_cast<const char*>(low);
+        to = reinterpret_cast<const char*>(max(low, high));
+    }
+    __device__ __forceinline__ uint32_t bytes() const { return static_cast<uint32_t>(to - from); }
+};
+
+// One thread: starts the copies of row i of every stream into a slot.
+template <int N, bool VEC>
+__device__ __forceinline__ void start_row(const Stream (&streams)[N], int64_t i, int64_t n, char* slot, uint32_t barrier)
+{
+    uint32_t bytes = 0;
+    // what was read and written in the slot by ordinary accesses comes before the copies
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const Stream& m = streams[k];
+        if constexpr (VEC) {
+            bytes += m.bytes;
+        } else if (m.bytes) {
+            const Window w(m, i, n);
+            bytes += w.bytes();
+            // what lies outside, in the first and the last rows
+            char* to = slot + m.at + shift_of(m, i);
+            const char* end = w.row + m.bytes;
+            for (const char* p = w.row; p < w.from && p < end; ++p)
+                to[p - w.row] = *p;
+            for (const char* p = w.to > w.row ? w.to : w.row; p < end; ++p)
+                to[p - w.row] = *p;
+        }
+    }
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(barrier), "r"(bytes) : "memory");
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const Stream& m = streams[k];
+        if (!m.bytes)
+            continue;
+        const char* from = m.base + i * m.step;
+        uint32_t size = m.bytes;
+        char* to = slot + m.at;
+        if constexpr (!VEC) {
+            const Window w(m, i, n);
+            to += shift_of(m, i) + (w.from - w.row);
+            from = w.from;
+            size = w.bytes();
+            if (!size)
+                continue;
+        }
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(shared_address(to)),
+                     "l"(from), "r"(size), "r"(barrier)
+                     : "memory");
+    }
+}
+
+// A lane's elements of a chunk, from a row in shared memory.
+template <typename T, bool VEC>
+__device__ __forceinline__ void read_chunk(Chunk<T, VEC>& v, const Columns<VEC>& c, const char* row, int type)
+{
+    if constexpr (VEC) {
+        if constexpr (sizeof(T) == 2) {
+            v.g.raw = c.count ? *reinterpret_cast<const uint4*>(row + c.at * 2) : make_uint4(0, 0, 0, 0);
+        } else {
+            const float4* p = reinterpret_cast<const float4*>(row + c.at * 4);
+            v.g.a = c.count ? p[0] : make_float4(0, 0, 0, 0);
+            v.g.b = c.count ? p[1] : make_float4(0, 0, 0, 0);
+        }
+    } else {
+        v.load(c, row, 0, type);
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void read_codes(CodeChunk<VEC>& v, const Columns<VEC>& c, const char* row)
+{
+    if constexpr (VEC) {
+        v.w = c.count ? *reinterpret_cast<const uint2*>(row + c.at) : make_uint2(0, 0);
+    } else {
+        const uint8_t* codes = reinterpret_cast<const uint8_t*>(row) + c.at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v.code[k] = k < c.count ? codes[32 * k] : 0;
+    }
 }
 
 template <bool VEC>
@@ -78,131 +173,211 @@ __device__ __forceinline__ void load_weight(const NormGradArgs& a, const Columns
 }
 
 template <typename DT, typename GT, int SOURCE, int C, bool VEC>
-__global__ void __launch_bounds__(kBlockWarps * 32) k_norm_grad(const __grid_constant__ NormGradArgs a)
+__global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_constant__ NormGradArgs a)
 {
-    // Wide rows need their registers for one row: the next one is then not loaded
-    // ahead, and the widest read the weight again from cache.
-    constexpr bool kAhead = C == 1;
-    constexpr int kKept = C < 4 ? C : 1;
-    extern __shared__ float columns[];  // the block's sums of its columns
+    constexpr bool kKeepWeight = C <= 2;  // else it is read again from cache, for the registers
+    constexpr bool kCodes = SOURCE == kFromCodes;
+    extern __shared__ __align__(16) char shared[];  // the ring; in the end the block's sums of its columns
     __shared__ float sums[2][kBlockWarps];
+    __shared__ int gave_up[kBlockWarps];  // a team's wait ran out
+    __shared__ __align__(8) uint64_t barriers[kBlockWarps * kMaxSlots];
     const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5;
     const int warps = a.warps, team = in_block / warps, warp = in_block - team * warps;
     Columns<VEC> cols[C];
 #pragma unroll
     for (int c = 0; c < C; ++c)
-        cols[c] = Columns<VEC>((warp + c * warps) * kChunk, lane, a.dim);
+        cols[c] = Columns<VEC>((warp * C + c) * kChunk, lane, a.dim);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * a.teams;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + team;
+    const int size_d = VEC ? sizeof(DT) : a.dout.type == LIONCUB_ROWS_BF16 ? 2 : 4;
+    const int size_h = kCodes ? 1 : VEC ? (SOURCE == kFromBf16 ? 2 : 4) : a.saved.type == LIONCUB_ROWS_BF16 ? 2 : 4;
+    const int size_g = VEC ? sizeof(GT) : a.residual_grad.type == LIONCUB_ROWS_BF16 ? 2 : 4;
+    const Stream streams[3] = {
+        {static_cast<const char*>(a.dout.data), a.dout.stride * size_d, a.dim * size_d, 0},
+        {kCodes ? reinterpret_cast<const char*>(a.packed.codes) : static_cast<const char*>(a.saved.data),
+         kCodes ? a.packed.stride : a.saved.stride * size_h, a.dim * size_h, a.at_saved},
+        {static_cast<const char*>(a.residual_grad.data), a.residual_grad.stride * size_g, a.residual_grad.data ? a.dim * size_g : 0,
+         a.at_residual}};
+    char* ring = shared + static_cast<int64_t>(team) * a.slots * a.slot_bytes;
+    const uint32_t full = shared_address(barriers + team * kMaxSlots);
+    const bool leads = warp == 0 && lane == 0;
+    if (leads) {
+        gave_up[team] = 0;
+        for (int k = 0; k < a.slots; ++k)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(full + 8 * k) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    team_barrier(team, warps);
+    let_next_launch_start();
     wait_for_launch_before();
+    uint32_t started = 0, last_parity = 0;  // of the slots, a bit each
+    if (leads)
+        for (int k = 0; k < a.slots && row + k * step < a.n; ++k) {
+            start_row<3, VEC>(streams, row + k * step, a.n, ring + k * a.slot_bytes, full + 8 * k);
+            started |= 1u << k;
+        }
 
-    float weight[kKept][8], grad[C][8];
+    // what is small is loaded a row ahead
+    float rstd = 0.0f, scale[C] = {};
+    const auto load_small = [&](int64_t i) {
+        rstd = a.rstd[i];
+        if constexpr (kCodes) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c) {
+                const int64_t at = VEC ? cols[c].at : cols[c].at - lane + 32 * (lane & 7);
+                scale[c] = at < a.dim ? a.packed.scales[i * a.packed.scale_stride + (at >> a.packed.log_group)] : 0.0f;
+            }
+        }
+    };
+    if (row < a.n)
+        load_small(row);
+    float weight[kKeepWeight ? C : 1][8], grad[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             grad[c][k] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kKept; ++c)
-        load_weight<VEC>(a, cols[c], weight[c]);
-    const float size = static_cast<float>(a.dim);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * a.teams;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + team;
-    int turn = 0;
-    RowInputs<DT, GT, SOURCE, C, VEC> in;
-    if (kAhead && row < a.n)
-        in.load(a, cols, row);
+        if constexpr (kKeepWeight)
+            load_weight<VEC>(a, cols[c], weight[c]);
+    }
+    uint32_t parity = 0, polls = a.first_wait_polls;  // polls: 0 for the ordinary wait
+    bool failed = false;
+    int turn = 0, slot = 0;
     for (; row < a.n; row += step) {
-        if (!kAhead)
-            in.load(a, cols, row);
+        if (!(polls ? test_phase(full + 8 * slot, parity, polls) : wait_phase(full + 8 * slot, parity))) {
+            gave_up[team] = 1;
+            flag(a.status, kStatusWaitTimeout);
+        }
         // dout, then g = dout * weight; n = h * rstd
-        float g[C][8], n[C][8], sum = 0.0f;
-        const float rstd = in.rstd;
+        float g[C][8], n[C][8];
+        float2 sums2 = both(0.0f);
+        Chunk<GT, VEC> residual[C];
+        const float r = rstd;
+        const char* in = ring + slot * a.slot_bytes;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            in.dout[c].unpack(g[c]);
-            in.saved[c].unpack(a, n[c]);
             float w[8];
-            if (kKept < C)
+            if constexpr (!kKeepWeight)
                 load_weight<VEC>(a, cols[c], w);
+            Chunk<DT, VEC> d;
+            read_chunk(d, cols[c], in + (VEC ? 0 : shift_of(streams[0], row)), a.dout.type);
+            d.unpack(g[c]);
+            const char* h = in + a.at_saved + (VEC ? 0 : shift_of(streams[1], row));
+            if constexpr (kCodes) {
+                CodeChunk<VEC> v;
+                read_codes(v, cols[c], h);
+                v.scale = scale[c];
+                v.unpack(a.packed, n[c]);
+            } else {
+                Chunk<std::conditional_t<SOURCE == kFromBf16, __nv_bfloat16, float>, VEC> v;
+                read_chunk(v, cols[c], h, a.saved.type);
+                v.unpack(n[c]);
+            }
+            if (a.residual_grad.data)
+                read_chunk(residual[c], cols[c], in + a.at_residual + (VEC ? 0 : shift_of(streams[2], row)), a.residual_grad.type);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                n[c][k] = __fmul_rn(n[c][k], rstd);
-                grad[c][k] = fmaf(g[c][k], n[c][k], grad[c][k]);
-                g[c][k] = __fmul_rn(g[c][k], kKept < C ? w[k] : weight[c % kKept][k]);
-                sum = fmaf(g[c][k], n[c][k], sum);
+            for (int k = 0; k < 4; ++k) {
+                const float2 nk = mul2(pair_of(n[c], k), both(r)), dk = pair_of(g[c], k);
+                const float2 gk = mul2(dk, pair_of(kKeepWeight ? weight[kKeepWeight ? c : 0] : w, k));
+                set_pair(grad[c], k, fma2(dk, nk, pair_of(grad[c], k)));
+                sums2 = fma2(gk, nk, sums2);
+                set_pair(n[c], k, nk);
+                set_pair(g[c], k, gk);
             }
         }
-        Chunk<GT, VEC> residual[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            residual[c] = in.residual[c];
-        if (kAhead && row + step < a.n)
-            in.load(a, cols, row + step);
-        sum = warp_sum(sum);
-        if (warps > 1) {  // sums of two rows take turns, so one barrier a row is enough
-            if (lane == 0)
-                sums[turn][in_block] = sum;
-            team_barrier(team, warps);
+        if (row + step < a.n)
+            load_small(row + step);
+        float sum = warp_sum(__fadd_rn(sums2.x, sums2.y));
+        if (warps > 1 && lane == 0)  // sums of two rows take turns, so one barrier a row is enough
+            sums[turn][in_block] = sum;
+        team_barrier(team, warps);
+        // What follows a wait that ran out is not what it should be, but ends soon: the team
+        // starts no row and has no long wait any more.
+        failed = gave_up[team];
+        polls = failed ? 1 : 0;
+        if (leads && !failed && row + a.slots * step < a.n) {  // the slot has been read
+            start_row<3, VEC>(streams, row + a.slots * step, a.n, ring + slot * a.slot_bytes, full + 8 * slot);
+            last_parity ^= 1u << slot;
+        }
+        if (++slot == a.slots) {
+            slot = 0;
+            parity ^= 1;
+        }
+        if (warps > 1) {
             sum = 0.0f;
             for (int k = 0; k < warps; ++k)
                 sum = __fadd_rn(sum, sums[turn][team * warps + k]);
             turn ^= 1;
         }
-        const float mean = __fdiv_rn(sum, size);
+        const float mean = __fmul_rn(sum, a.per_column);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (a.again.data) {
                 float y[8], w[8];
-                if (kKept < C)
+                if constexpr (!kKeepWeight)
                     load_weight<VEC>(a, cols[c], w);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    y[k] = __fmul_rn(n[c][k], kKept < C ? w[k] : weight[c % kKept][k]);
+                for (int k = 0; k < 4; ++k)
+                    set_pair(y, k, mul2(pair_of(n[c], k), pair_of(kKeepWeight ? weight[kKeepWeight ? c : 0] : w, k)));
                 store_typed<VEC>(cols[c], a.again.data, row * a.again.stride, a.again.type, y);
             }
-            float rest[8];
+            float rest[8] = {};
             if (a.residual_grad.data)
                 residual[c].unpack(rest);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float d = __fmul_rn(rstd, fmaf(-n[c][k], mean, g[c][k]));
-                g[c][k] = a.residual_grad.data ? __fadd_rn(d, rest[k]) : d;
-            }
+            for (int k = 0; k < 4; ++k)
+                set_pair(g[c], k, fma2(both(r), fma2(pair_of(n[c], k), both(-mean), pair_of(g[c], k)), pair_of(rest, k)));
             store_typed<VEC>(cols[c], a.dx.data, row * a.dx.stride, a.dx.type, g[c]);
         }
     }
+    if (failed)  // no copy may still be under way when the block ends
+        for (int k = 0; k < a.slots; ++k)
+            if (started >> k & 1)
+                wait_phase(full + 8 * k, last_parity >> k & 1);
     if (!a.partial)
         return;
-    for (int t = 0; t < a.teams; ++t) {  // a column is one lane's in every team
-        if (team == t) {
+    float* columns = reinterpret_cast<float*>(shared);  // a row for each team
+    __syncthreads();
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+        float* mine = columns + team * a.dim + cols[c].at;
+        if (VEC) {
+            if (cols[c].count) {
+                Group8<float> v;
+                v.pack(grad[c]);
+                v.store(mine, 0);
+            }
+        } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < cols[c].count) {
-                        const int j = static_cast<int>(cols[c].at) + (VEC ? k : 32 * k);
-                        columns[j] = t ? __fadd_rn(columns[j], grad[c][k]) : grad[c][k];
-                    }
+            for (int k = 0; k < 8; ++k)
+                if (k < cols[c].count)
+                    mine[32 * k] = grad[c][k];
         }
-        __syncthreads();
     }
+    __syncthreads();
     float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.dim;
     if (index_ok(a.status, static_cast<int64_t>(blockIdx.x) < a.partial_rows))
-        for (int j = threadIdx.x; j < a.dim; j += blockDim.x)
-            to[j] = columns[j];
+        for (int j = threadIdx.x; j < a.dim; j += blockDim.x) {
+            float sum = columns[j];
+            for (int t = 1; t < a.teams; ++t)
+                sum = __fadd_rn(sum, columns[t * a.dim + j]);
+            to[j] = sum;
+        }
 }
 
-// The blocks' rows, added in order: a warp adds every eighth row of 32 columns,
-// and one of them the eight sums.
-constexpr int kJoinWarps = 8;
+// The blocks' rows, added in order: a warp adds every 32nd row of 32 columns,
+// and one of them the 32 sums.
+constexpr int kJoinWarps = 32;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) k_weight_grad(const __grid_constant__ WeightGradArgs a)
 {
     __shared__ float sums[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
+    let_next_launch_start();
     wait_for_launch_before();
     float sum = 0.0f;
     if (j < a.dim)
-#pragma unroll 4
+#pragma unroll 5
         for (int64_t i = warp; i < a.rows; i += kJoinWarps)
             sum = __fadd_rn(sum, a.partial[i * a.dim + j]);
     sums[warp][lane] = sum;
@@ -226,7 +401,7 @@ struct Spread {
     explicit Spread(int dim)
     {
         const int chunks = (dim + kChunk - 1) / kChunk;
-        c = chunks <= kMaxWarps ? 1 : chunks <= 2 * kMaxWarps ? 2 : 4;
+        c = chunks == 1 ? 1 : chunks <= 2 * kBlockWarps ? 2 : 4;
         warps = (chunks + c - 1) / c;
         teams = kBlockWarps / warps;
     }
@@ -236,13 +411,12 @@ template <typename DT, typename GT, int SOURCE, int C, bool VEC>
 cudaError_t launch_c(const NormGradArgs& a, int blocks, cudaStream_t s)
 {
     const auto kernel = k_norm_grad<DT, GT, SOURCE, C, VEC>;
-    const size_t shared = a.partial ? a.dim * sizeof(float) : 0;
-    if (shared > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LIONCUB_NORM_MAX_DIM * sizeof(float));
-        if (e != cudaSuccess)
-            return e;
-    }
-    return launch_programmatic(kernel, static_cast<unsigned>(blocks), a.warps * a.teams * 32, shared, s, a);
+    const int ring = a.slots * a.slot_bytes * a.teams, columns = a.partial ? a.teams * a.dim * static_cast<int>(sizeof(float)) : 0;
+    // the kernel's limit, the same for every call: calls of other threads launch by it too
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_programmatic(kernel, static_cast<unsigned>(blocks), a.warps * a.teams * 32, ring > columns ? ring : columns, s, a);
 }
 
 template <typename DT, typename GT, int SOURCE, bool VEC>
@@ -281,6 +455,16 @@ cudaError_t launch_norm_grad(NormGradArgs a, int blocks, bool vec, cudaStream_t 
     const Spread spread(a.dim);
     a.warps = spread.warps;
     a.teams = spread.teams;
+    // a slot: a row of each matrix, from a 16-byte boundary to one
+    const auto room = [&](int size) { return (a.dim * size + 15 + 15) / 16 * 16; };
+    const auto size_of = [](const TypedRows& m) { return m.type == LIONCUB_ROWS_BF16 ? 2 : 4; };
+    a.at_saved = room(size_of(a.dout));
+    a.at_residual = a.at_saved + room(a.packed.codes ? 1 : size_of(a.saved));
+    a.slot_bytes = a.at_residual + (a.residual_grad.data ? room(size_of(a.residual_grad)) : 0);
+    const int slots = kRingBytes / (a.slot_bytes * a.teams);
+    a.slots = slots > kMaxSlots ? kMaxSlots : slots;
+    static_assert(3 * (LIONCUB_NORM_MAX_DIM * 4 + 30) <= kRingBytes, "a row of every width has a slot");
+    a.per_column = 1.0f / static_cast<float>(a.dim);
     if (!vec)
         return launch_t<float, float, false>(a, spread.c, blocks, s);
     const bool db = a.dout.type == LIONCUB_ROWS_BF16, gb = a.residual_grad.type == LIONCUB_ROWS_BF16;

@@ -2,11 +2,13 @@
 // position * frequency,
 //   (a, b) -> m * (a cos - b sin, a sin + b cos).
 //
-// Memory-bound.  The angle is the same for all heads of a place, so a thread
-// takes the same columns of several heads and computes sines and cosines once.
+// Memory-bound.  The angle is the same for all heads of a place, so a block takes
+// a few places, works out their cosines and sines once into shared memory, and
+// then walks over the places' heads in the order of memory.
 // Angles are turns in 64-bit fixed point: position * turns-a-position wraps
 // around by itself, which is the exact reduction that far positions need (in
 // fp32 the angle of position 100000 would be off by 0.004).
+#include <algorithm>
 #include <climits>
 
 #include "block_device.cuh"
@@ -15,6 +17,8 @@ namespace lc {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kMaxPlaces = 8;  // of a block
+constexpr int kItems = 8;      // of a thread, about, where there are many places
 
 // cos and sin of a position's angle.  The nearest quarter turn is taken off in
 // whole numbers, so what is left is at most an eighth of a turn.
@@ -36,164 +40,193 @@ __device__ __forceinline__ void angle_of(uint64_t position, uint64_t turns, cons
     s = __fmul_rn(s, a.sin_factor);
 }
 
-__device__ __forceinline__ float first_turned(float x, float y, float c, float s) { return fmaf(x, c, -__fmul_rn(y, s)); }
-__device__ __forceinline__ float second_turned(float x, float y, float c, float s) { return fmaf(y, c, __fmul_rn(x, s)); }
+// What a thread moves at once: twice 8 columns, half of the rotated ones apart, or a
+// pair of columns; items behind the turning ones are copied, 8 columns or one.
+template <typename T, bool INTERLEAVED, bool VEC>
+struct Item {
+    Group8<T> g[2];
+    T x[2];
+    int first, second;  // columns; second < 0: to be copied
 
-// A thread's place, the item of each head that it has, and its share of heads.
-struct Share {
-    int64_t place, b;
-    int item, group, s;
-    bool on;
-    __device__ __forceinline__ Share(const RotaryArgs& a, int items)
+    __device__ __forceinline__ void place(const RotaryArgs& a, int item, int turning)
     {
-        const int64_t t = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
-        const int64_t rest = quotient(t, items);
-        item = static_cast<int>(t - rest * items);
-        place = quotient(rest, a.groups);
-        group = static_cast<int>(rest - place * a.groups);
-        on = place < a.places;
-        b = quotient(place, a.seq);
-        s = static_cast<int>(place - b * a.seq);
-    }
-    __device__ __forceinline__ uint64_t position(const RotaryArgs& a) const
-    {
-        return static_cast<uint64_t>(a.positions ? index_at(a.positions, place, a.wide) : a.first + s);
-    }
-};
-
-struct Head {
-    int64_t in, out;
-    const HeadsArgs* side;
-    __device__ __forceinline__ Head(const RotaryArgs& a, const Share& t, int h)
-    {
-        const int second = h >= a.heads[0];
-        side = &a.side[second];
-        const int at = second ? h - a.heads[0] : h;
-        in = t.b * side->in_batch + t.s * side->in_place + at * side->in_head;
-        out = t.b * side->out_batch + t.s * side->out_place + at * side->out_head;
-    }
-};
-
-// 8 columns a move.  Items: halves: pairs / 8 of two groups of 8 columns that
-// turn together; interleaved: pairs / 4 of one group; then groups that are copied.
-template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kBlock) k_rotary(const __grid_constant__ RotaryArgs a, const int turning, const int items)
-{
-    const Share t(a, items);
-    wait_for_launch_before();
-    if (!t.on)
-        return;
-    const int heads = a.heads[0] + a.heads[1];
-    if (t.item >= turning) {
-        const int col = 2 * a.pairs + (t.item - turning) * 8;
-        for (int h = t.group; h < heads; h += a.groups) {
-            const Head at(a, t, h);
-            Group8<T> x;
-            x.load(at.side->in, at.in + col);
-            x.store(at.side->out, at.out + col);
-        }
-        return;
-    }
-    constexpr int N = INTERLEAVED ? 4 : 8;  // pairs
-    const uint64_t position = t.position(a);
-    float c[N], s[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        angle_of(position, a.turns[t.item * N + k], a, c[k], s[k]);
-    for (int h = t.group; h < heads; h += a.groups) {
-        const Head at(a, t, h);
-        if constexpr (INTERLEAVED) {
-            const int col = t.item * 8;
-            Group8<T> g;
-            g.load(at.side->in, at.in + col);
-            float x[8], y[8];
-            g.unpack(x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[2 * k] = first_turned(x[2 * k], x[2 * k + 1], c[k], s[k]);
-                y[2 * k + 1] = second_turned(x[2 * k], x[2 * k + 1], c[k], s[k]);
-            }
-            g.pack(y);
-            g.store(at.side->out, at.out + col);
+        const int pairs = a.pairs;
+        if (item >= turning) {
+            first = 2 * pairs + (item - turning) * (VEC ? 8 : 1);
+            second = -1;
+        } else if (VEC) {
+            first = item * 8;
+            second = first + pairs;
         } else {
-            const int col = t.item * 8;
-            Group8<T> g, o;
-            g.load(at.side->in, at.in + col);
-            o.load(at.side->in, at.in + col + a.pairs);
-            float x[8], y[8], u[8], v[8];
-            g.unpack(x);
-            o.unpack(y);
+            first = INTERLEAVED ? 2 * item : item;
+            second = INTERLEAVED ? first + 1 : first + pairs;
+        }
+    }
+    __device__ __forceinline__ void load(const T* in)
+    {
+        if constexpr (VEC) {
+            g[0].load(in, first);
+            if (second >= 0)
+                g[1].load(in, second);
+        } else {
+            x[0] = in[first];
+            if (second >= 0)
+                x[1] = in[second];
+        }
+    }
+    __device__ __forceinline__ void turn(const float* cosines, const float* sines, int item, int pairs)
+    {
+        if (second < 0)
+            return;
+        if constexpr (!VEC) {
+            const float u = static_cast<float>(x[0]), v = static_cast<float>(x[1]), c = cosines[item], s = sines[item];
+            x[0] = static_cast<T>(fmaf(u, c, -__fmul_rn(v, s)));
+            x[1] = static_cast<T>(fmaf(v, c, __fmul_rn(u, s)));
+            return;
+        }
+        float u[8], v[8];
+        g[0].unpack(u);
+        g[1].unpack(v);
+        // four pairs a round: of either move (interleaved), or half of both
+        const int at = INTERLEAVED ? item * 4 : item * 8, next = INTERLEAVED ? pairs / 2 : 4;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                u[k] = first_turned(x[k], y[k], c[k], s[k]);
-                v[k] = second_turned(x[k], y[k], c[k], s[k]);
+        for (int h = 0; h < 2; ++h) {
+            const float4 c = *reinterpret_cast<const float4*>(cosines + at + h * next), s = *reinterpret_cast<const float4*>(sines + at + h * next);
+            if constexpr (INTERLEAVED) {  // (x c - y s, y c + x s)
+                float(&y)[8] = h ? v : u;
+                const float ck[4] = {c.x, c.y, c.z, c.w}, sk[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 w = pair_of(y, k);
+                    set_pair(y, k, fma2(make_float2(w.y, w.x), make_float2(-sk[k], sk[k]), mul2(w, both(ck[k]))));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 ck = k ? make_float2(c.z, c.w) : make_float2(c.x, c.y), sk = k ? make_float2(s.z, s.w) : make_float2(s.x, s.y);
+                    const float2 p = pair_of(u, 2 * h + k), q = pair_of(v, 2 * h + k);
+                    set_pair(u, 2 * h + k, fma2(q, make_float2(-sk.x, -sk.y), mul2(p, ck)));
+                    set_pair(v, 2 * h + k, fma2(p, sk, mul2(q, ck)));
+                }
             }
-            g.pack(u);
-            o.pack(v);
-            g.store(at.side->out, at.out + col);
-            o.store(at.side->out, at.out + col + a.pairs);
+        }
+        g[0].pack(u);
+        g[1].pack(v);
+    }
+    __device__ __forceinline__ void store(T* out) const
+    {
+        if constexpr (VEC) {
+            g[0].store(out, first);
+            if (second >= 0)
+                g[1].store(out, second);
+        } else {
+            out[first] = x[0];
+            if (second >= 0)
+                out[second] = x[1];
+        }
+    }
+};
+
+// n / d by a product, for n * d < 2^32; a block whose numbers are larger divides.
+struct Divisor {
+    uint32_t d, magic;  // magic 0: divide
+    __device__ __forceinline__ uint32_t of(uint32_t n) const { return magic ? __umulhi(n, magic) : n / d; }
+};
+Divisor divisor(uint32_t d, uint64_t largest) { return {d, d > 1 && largest * d < (1ull << 32) ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0}; }
+
+template <typename T, bool INTERLEAVED, bool VEC>
+__global__ void __launch_bounds__(kBlock) k_rotary(const __grid_constant__ RotaryArgs a, const int turning, const Divisor items,
+                                                   const Divisor heads0, const Divisor heads1, const int block_places)
+{
+    constexpr int kUnits = VEC ? 2 : 4;  // items of a thread, whose loads are in flight together
+    extern __shared__ __align__(16) float cosines[];  // of each place and pair; then the sines
+    __shared__ int64_t starts[kMaxPlaces][4];         // of a place: elements to its in and out of either side
+    float* sines = cosines + block_places * a.pairs;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * block_places;
+    const int places = static_cast<int>(min(a.places - first, static_cast<int64_t>(block_places)));
+    if (threadIdx.x < places) {
+        const int64_t place = first + threadIdx.x, b = quotient(place, a.seq), s = place - b * a.seq;
+        for (int k = 0; k < 2; ++k) {
+            starts[threadIdx.x][2 * k] = b * a.side[k].in_batch + s * a.side[k].in_place;
+            starts[threadIdx.x][2 * k + 1] = b * a.side[k].out_batch + s * a.side[k].out_place;
+        }
+    }
+    if (a.positions)
+        wait_for_launch_before();
+    for (int i = threadIdx.x; i < places * a.pairs; i += kBlock) {
+        const int p = i / a.pairs;
+        const int64_t place = first + p;
+        const int64_t position = a.positions ? index_at(a.positions, place, a.wide) : a.first + place % a.seq;
+        angle_of(static_cast<uint64_t>(position), a.turns[i - p * a.pairs], a, cosines[i], sines[i]);
+    }
+    if (!a.positions)  // the angles need nothing of the launches before
+        wait_for_launch_before();
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const Divisor heads = k ? heads1 : heads0;
+        const uint32_t units = places * heads.d * items.d;
+        const T* in = static_cast<const T*>(a.side[k].in);
+        T* out = static_cast<T*>(a.side[k].out);
+        const int64_t in_head = a.side[k].in_head, out_head = a.side[k].out_head;
+        for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kUnits * kBlock) {
+            Item<T, INTERLEAVED, VEC> x[kUnits];
+            uint32_t item[kUnits], p[kUnits], h[kUnits];
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const uint32_t unit = u0 + u * kBlock;
+                if (unit < units) {
+                    const uint32_t head = items.of(unit);  // of all places
+                    item[u] = unit - head * items.d;
+                    p[u] = heads.of(head);
+                    h[u] = head - p[u] * heads.d;
+                    x[u].place(a, item[u], turning);
+                    x[u].load(in + (starts[p[u]][2 * k] + h[u] * in_head));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+                if (u0 + u * kBlock < units) {
+                    x[u].turn(cosines + p[u] * a.pairs, sines + p[u] * a.pairs, item[u], a.pairs);
+                    x[u].store(out + (starts[p[u]][2 * k + 1] + h[u] * out_head));
+                }
         }
     }
 }
 
-// Any alignment: an item is a pair, or a column that is copied.
-template <typename T>
-__global__ void __launch_bounds__(kBlock) k_rotary_scalar(const __grid_constant__ RotaryArgs a, const int interleaved, const int items)
+template <typename T, bool INTERLEAVED, bool VEC>
+cudaError_t launch_t(const RotaryArgs& a, cudaStream_t s)
 {
-    const Share t(a, items);
-    wait_for_launch_before();
-    if (!t.on)
-        return;
-    const int heads = a.heads[0] + a.heads[1];
-    if (t.item >= a.pairs) {
-        const int col = a.pairs + t.item;
-        for (int h = t.group; h < heads; h += a.groups) {
-            const Head at(a, t, h);
-            static_cast<T*>(at.side->out)[at.out + col] = static_cast<const T*>(at.side->in)[at.in + col];
-        }
-        return;
-    }
-    float c, s;
-    angle_of(t.position(a), a.turns[t.item], a, c, s);
-    const int one = interleaved ? 2 * t.item : t.item, two = interleaved ? one + 1 : one + a.pairs;
-    for (int h = t.group; h < heads; h += a.groups) {
-        const Head at(a, t, h);
-        const T* in = static_cast<const T*>(at.side->in) + at.in;
-        T* out = static_cast<T*>(at.side->out) + at.out;
-        const float x = static_cast<float>(in[one]), y = static_cast<float>(in[two]);
-        out[one] = static_cast<T>(first_turned(x, y, c, s));
-        out[two] = static_cast<T>(second_turned(x, y, c, s));
-    }
+    const int rest = a.copy ? a.head_dim - 2 * a.pairs : 0;
+    const int turning = VEC ? a.pairs / 8 : a.pairs, items = turning + (VEC ? rest / 8 : rest);
+    // Places of a block: about kItems items for each of its threads, fewer while that leaves
+    // less than four blocks a multiprocessor.
+    const int64_t of_place = int64_t(a.heads[0] + a.heads[1]) * items;
+    int64_t places = std::min<int64_t>(kMaxPlaces, (kItems * kBlock + of_place - 1) / of_place);
+    places = std::max<int64_t>(1, std::min<int64_t>(places, a.places / (152 * 4)));
+    const int64_t blocks = (a.places + places - 1) / places;
+    const int64_t most = places * std::max(a.heads[0], a.heads[1]) * items;
+    if (blocks > INT_MAX || most > INT_MAX)
+        return cudaErrorInvalidConfiguration;
+    return launch_programmatic(k_rotary<T, INTERLEAVED, VEC>, static_cast<unsigned>(blocks), kBlock, places * a.pairs * 2 * sizeof(float), s, a,
+                               turning, divisor(items, most), divisor(a.heads[0], most), divisor(a.heads[1], most), static_cast<int>(places));
+}
+
+template <typename T>
+cudaError_t launch_l(const RotaryArgs& a, bool interleaved, bool vec, cudaStream_t s)
+{
+    if (vec)
+        return interleaved ? launch_t<T, true, true>(a, s) : launch_t<T, false, true>(a, s);
+    return interleaved ? launch_t<T, true, false>(a, s) : launch_t<T, false, false>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_rotary(RotaryArgs a, int type, bool interleaved, bool vec, cudaStream_t s)
+cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, bool vec, cudaStream_t s)
 {
-    const int heads = a.heads[0] + a.heads[1];
-    if (a.places == 0 || heads == 0)
+    if (a.places == 0 || a.heads[0] + a.heads[1] == 0)
         return cudaSuccess;
-    const int rest = a.copy ? a.head_dim - 2 * a.pairs : 0;
-    const int turning = vec ? (interleaved ? a.pairs / 4 : a.pairs / 8) : a.pairs;
-    const int items = turning + (vec ? rest / 8 : rest);
-    // About four heads a thread, fewer while threads are too few for all multiprocessors.
-    const int64_t lanes = a.places * items;
-    int64_t groups = (heads + 3) / 4;
-    const int64_t wanted = (int64_t(152) * 1024 + lanes - 1) / lanes;
-    groups = groups < wanted ? wanted : groups;
-    a.groups = static_cast<int32_t>(groups < heads ? groups : heads);
-    const int64_t blocks = (lanes * a.groups + kBlock - 1) / kBlock;
-    if (blocks > INT_MAX)
-        return cudaErrorInvalidConfiguration;
-    const unsigned n = static_cast<unsigned>(blocks);
-    if (!vec)
-        return type == LIONCUB_ROWS_BF16 ? launch_programmatic(k_rotary_scalar<__nv_bfloat16>, n, kBlock, 0, s, a, int(interleaved), items)
-                                         : launch_programmatic(k_rotary_scalar<float>, n, kBlock, 0, s, a, int(interleaved), items);
-    if (type == LIONCUB_ROWS_BF16)
-        return interleaved ? launch_programmatic(k_rotary<__nv_bfloat16, true>, n, kBlock, 0, s, a, turning, items)
-                           : launch_programmatic(k_rotary<__nv_bfloat16, false>, n, kBlock, 0, s, a, turning, items);
-    return interleaved ? launch_programmatic(k_rotary<float, true>, n, kBlock, 0, s, a, turning, items)
-                       : launch_programmatic(k_rotary<float, false>, n, kBlock, 0, s, a, turning, items);
+    return type == LIONCUB_ROWS_BF16 ? launch_l<__nv_bfloat16>(a, interleaved, vec, s) : launch_l<float>(a, interleaved, vec, s);
 }
 
 }  // namespace lc
