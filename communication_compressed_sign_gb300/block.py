@@ -18,7 +18,7 @@ import struct
 from typing import NamedTuple
 
 from . import embed
-from .embed import _empty, _matrix, _rows
+from .embed import _empty, _matrix, _rows, _step
 from .lioncub import ERR_STATE, OK, LionCubError
 
 CODES_INT8, CODES_E4M3 = 0, 1
@@ -241,21 +241,9 @@ def _codes(p, name, nrows, cols, device):
         raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(codes.shape)})")
     if not scales.dim() or scales.size(-1) != groups or scales.numel() != nrows * groups:
         raise ValueError(f"{name} must have {nrows} rows of {groups} scales (got {tuple(scales.shape)})")
-    return _pack_packed(codes.data_ptr(), scales.data_ptr(), _step(codes, f"{name}: codes", nrows, cols),
-                        _step(scales, f"{name}: scales", nrows, groups), group, kind)
-
-
-def _step(t, name, nrows, cols):
-    """The distance between a tensor's rows."""
-    if t.is_contiguous() or nrows == 0:
-        return cols
-    try:
-        t = t.view(-1, cols)
-    except RuntimeError:
-        raise ValueError(f"{name}: its rows do not lie a fixed distance apart") from None
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the columns of a row must be contiguous")
-    return t.stride(0) if nrows > 1 else cols
+    step = cols if codes.is_contiguous() else _step(codes, name, nrows, cols)
+    scale_step = groups if scales.is_contiguous() else _step(scales, name, nrows, groups)
+    return _pack_packed(codes.data_ptr(), scales.data_ptr(), step, scale_step, group, kind)
 
 
 def _either(t, name, nrows, cols, device):

@@ -6,6 +6,7 @@
 // Memory-bound: each element is read and written once; groups of columns that
 // share a scale lie inside a warp's chunk of 256 columns, so their maxima need
 // shuffles only.  Dense matrices whose rows are whole groups are one long row.
+#include <algorithm>
 #include <climits>
 
 #include "block_device.cuh"
@@ -15,7 +16,11 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
-constexpr int kUnits = 2;  // chunks of a warp, whose loads are in flight together
+// Chunks of a warp, whose loads are in flight together.  An activation by scalar
+// moves has too few registers for two (4907 x 771 bf16 with two inputs saved in 8
+// bits, both ways: 28.4 us, 27.0 with one); packing by them has not (9.9 with one, 9.4).
+template <int KIND, bool VEC>
+constexpr int kUnitsOf = VEC || KIND == kIdentity ? 2 : 1;
 
 __device__ __forceinline__ float exp2_approx(float x)  // off by at most 2 units in the last place
 {
@@ -57,50 +62,73 @@ __device__ __forceinline__ void value_and_slope(float2 x, float2& f, float2& slo
     }
 }
 
-// The chunks of a warp: kUnits neighbours in a row, of which it has `spans` times as many.
-template <bool VEC>
-struct Units {
-    int64_t row, first, width;
-    Columns<VEC> cols[kUnits];
-    __device__ __forceinline__ Units(int64_t rows, int64_t w, int64_t spans) : width(w)
-    {
-        const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-        row = rows == 1 ? 0 : quotient(unit, static_cast<int>(spans));
-        first = (unit - row * spans) * (kUnits * kChunk);
-        if (row >= rows)  // behind the last
-            first = width;
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-            cols[u] = Columns<VEC>(first + u * kChunk, threadIdx.x & 31, width);
-    }
-    __device__ __forceinline__ bool none() const { return first >= width; }
-    __device__ __forceinline__ bool on(int u) const { return first + u * kChunk < width; }
+// How the work is cut.  A warp has kUnits neighbouring chunks of a row, which has
+// `spans` times as many; or, where that would leave lanes idle, each lane has groups
+// of 8 columns by itself, of which a row has `lanes` (0: not), so that a warp
+// may have several rows.
+struct Cut {
+    int64_t spans;
+    int32_t lanes;
 };
 
-template <typename T, int KIND, bool VEC>
-__global__ void __launch_bounds__(kBlock) k_activation(const __grid_constant__ ActivationArgs a, const int64_t spans)
+template <int kUnits, bool VEC, bool LANES>
+struct Units {
+    int64_t row[kUnits];
+    Columns<VEC> cols[kUnits];
+    bool on[kUnits];  // the warp has something to do
+    __device__ __forceinline__ Units(int64_t rows, int64_t width, const Cut& cut)
+    {
+        const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+        const int lane = threadIdx.x & 31;
+        if constexpr (LANES) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int64_t first = (unit * kUnits + u) * 32;
+                row[u] = quotient(first + lane, cut.lanes);
+                const bool there = row[u] < rows;
+                cols[u].at = there ? (first + lane - row[u] * cut.lanes) * 8 : 0;
+                cols[u].count = there ? 8 : 0;
+                row[u] = there ? row[u] : 0;
+                on[u] = first < rows * cut.lanes;
+            }
+        } else {
+            const int64_t r = rows == 1 ? 0 : quotient(unit, static_cast<int>(cut.spans));
+            const int64_t first = r < rows ? (unit - r * cut.spans) * (kUnits * kChunk) : width;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                row[u] = r;
+                cols[u] = Columns<VEC>(first + u * kChunk, lane, width);
+                on[u] = first + u * kChunk < width;
+            }
+        }
+    }
+};
+
+template <typename T, int KIND, bool VEC, bool LANES>
+__global__ void __launch_bounds__(kBlock) k_activation(const __grid_constant__ ActivationArgs a, const Cut cut)
 {
-    const Units<VEC> u(a.rows, a.cols, spans);
+    constexpr int kUnits = kUnitsOf<KIND, VEC>;
+    const Units<kUnits, VEC, LANES> u(a.rows, a.cols, cut);
     const int lane = threadIdx.x & 31;
     wait_for_launch_before();
-    if (u.none())
+    if (!u.on[0])
         return;
     Chunk<T, VEC> vx[kUnits], vup[kUnits];
     const bool gated = KIND != kIdentity && a.up.data;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        vx[i].load(u.cols[i], a.x.data, u.row * a.x.stride, a.x.type);
+        vx[i].load(u.cols[i], a.x.data, u.row[i] * a.x.stride, a.x.type);
         if (gated)
-            vup[i].load(u.cols[i], a.up.data, u.row * a.up.stride, a.up.type);
+            vup[i].load(u.cols[i], a.up.data, u.row[i] * a.up.stride, a.up.type);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        if (!u.on(i))
+        if (!u.on[i])
             continue;
         float x[8];
         vx[i].unpack(x);
         if (a.saved.codes)
-            pack_chunk<VEC>(a.saved, u.cols[i], u.row, x, vx[i].largest(), lane);
+            pack_chunk<VEC>(a.saved, u.cols[i], u.row[i], x, vx[i].largest(), lane);
         if constexpr (KIND != kIdentity) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -112,23 +140,24 @@ __global__ void __launch_bounds__(kBlock) k_activation(const __grid_constant__ A
                 float y[8];
                 vup[i].unpack(y);
                 if (a.saved_up.codes)
-                    pack_chunk<VEC>(a.saved_up, u.cols[i], u.row, y, vup[i].largest(), lane);
+                    pack_chunk<VEC>(a.saved_up, u.cols[i], u.row[i], y, vup[i].largest(), lane);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     set_pair(x, k, mul2(pair_of(x, k), pair_of(y, k)));
             }
-            store_typed<VEC>(u.cols[i], a.out.data, u.row * a.out.stride, a.out.type, x);
+            store_typed<VEC>(u.cols[i], a.out.data, u.row[i] * a.out.stride, a.out.type, x);
         }
     }
 }
 
-template <typename T, int KIND, bool PACKED, bool VEC>
-__global__ void __launch_bounds__(kBlock) k_activation_grad(const __grid_constant__ ActivationArgs a, const int64_t spans)
+template <typename T, int KIND, bool PACKED, bool VEC, bool LANES>
+__global__ void __launch_bounds__(kBlock) k_activation_grad(const __grid_constant__ ActivationArgs a, const Cut cut)
 {
-    const Units<VEC> u(a.rows, a.cols, spans);
+    constexpr int kUnits = kUnitsOf<KIND, VEC>;
+    const Units<kUnits, VEC, LANES> u(a.rows, a.cols, cut);
     const int lane = threadIdx.x & 31;
     wait_for_launch_before();
-    if (u.none())
+    if (!u.on[0])
         return;
     const bool gated = PACKED ? a.saved_up.codes != nullptr : a.up.data != nullptr;
     using Saved = std::conditional_t<PACKED, CodeChunk<VEC>, Chunk<T, VEC>>;
@@ -136,20 +165,20 @@ __global__ void __launch_bounds__(kBlock) k_activation_grad(const __grid_constan
     Saved vx[kUnits], vup[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        vd[i].load(u.cols[i], a.dout.data, u.row * a.dout.stride, a.dout.type);
+        vd[i].load(u.cols[i], a.dout.data, u.row[i] * a.dout.stride, a.dout.type);
         if constexpr (PACKED) {
-            vx[i].load(a.saved, u.cols[i], u.row, lane);
+            vx[i].load(a.saved, u.cols[i], u.row[i], lane);
             if (gated)
-                vup[i].load(a.saved_up, u.cols[i], u.row, lane);
+                vup[i].load(a.saved_up, u.cols[i], u.row[i], lane);
         } else {
-            vx[i].load(u.cols[i], a.x.data, u.row * a.x.stride, a.x.type);
+            vx[i].load(u.cols[i], a.x.data, u.row[i] * a.x.stride, a.x.type);
             if (gated)
-                vup[i].load(u.cols[i], a.up.data, u.row * a.up.stride, a.up.type);
+                vup[i].load(u.cols[i], a.up.data, u.row[i] * a.up.stride, a.up.type);
         }
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        if (!u.on(i))
+        if (!u.on[i])
             continue;
         float x[8], up[8], d[8];
         vd[i].unpack(d);
@@ -176,68 +205,100 @@ __global__ void __launch_bounds__(kBlock) k_activation_grad(const __grid_constan
             set_pair(y, k, f);
             set_pair(x, k, mul2(g, slope));
         }
-        store_typed<VEC>(u.cols[i], a.dx.data, u.row * a.dx.stride, a.dx.type, x);
+        store_typed<VEC>(u.cols[i], a.dx.data, u.row[i] * a.dx.stride, a.dx.type, x);
         if (gated && a.dup.data)
-            store_typed<VEC>(u.cols[i], a.dup.data, u.row * a.dup.stride, a.dup.type, dup);
+            store_typed<VEC>(u.cols[i], a.dup.data, u.row[i] * a.dup.stride, a.dup.type, dup);
         if (a.again.data)
-            store_typed<VEC>(u.cols[i], a.again.data, u.row * a.again.stride, a.again.type, y);
+            store_typed<VEC>(u.cols[i], a.again.data, u.row[i] * a.again.stride, a.again.type, y);
     }
 }
 
-template <bool VEC>
+template <bool VEC, bool LANES>
 __global__ void __launch_bounds__(kBlock) k_unpack(const PackedRows x, const TypedRows out, const int64_t rows, const int64_t cols,
-                                                   const int64_t spans)
+                                                   const Cut cut)
 {
-    const Units<VEC> u(rows, cols, spans);
+    constexpr int kUnits = kUnitsOf<kIdentity, VEC>;
+    const Units<kUnits, VEC, LANES> u(rows, cols, cut);
     wait_for_launch_before();
-    if (u.none())
+    if (!u.on[0])
         return;
     CodeChunk<VEC> v[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-        v[i].load(x, u.cols[i], u.row, threadIdx.x & 31);
+        v[i].load(x, u.cols[i], u.row[i], threadIdx.x & 31);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         float y[8];
         v[i].unpack(x, y);
-        store_typed<VEC>(u.cols[i], out.data, u.row * out.stride, out.type, y);
+        store_typed<VEC>(u.cols[i], out.data, u.row[i] * out.stride, out.type, y);
     }
 }
 
+// group: the most columns that share a scale.
 struct Grid {
-    int64_t spans, blocks;
-    Grid(int64_t rows, int64_t cols)
+    Cut cut;
+    int64_t blocks;
+    Grid(int64_t rows, int64_t cols, int units, bool vec, int group)
     {
-        spans = (cols + kUnits * kChunk - 1) / (kUnits * kChunk);
-        blocks = (rows * spans + kWarps - 1) / kWarps;
+        const int64_t width = int64_t(units) * kChunk;
+        cut.spans = (cols + width - 1) / width;
+        int64_t all = rows * cut.spans;  // warps
+        cut.lanes = 0;
+        // By lanes where more than a quarter of the chunks' lanes had no columns, if groups are then
+        // whole (and so lie within a warp).  Forward and backward, two inputs saved in 8 bits out
+        // of wider rows: 13131 rows of 128 41.7 us by chunks, 7.2 by lanes; 16384 of 768 41.9 and 42.7.
+        if (vec && rows > 1 && cols % std::max(group, 8) == 0 && cut.spans * width * 3 > cols * 4 && cols / 8 <= INT_MAX) {
+            cut.lanes = static_cast<int32_t>(cols / 8);
+            all = (rows * cut.lanes + 32 * units - 1) / (32 * units);
+        }
+        blocks = (all + kWarps - 1) / kWarps;
     }
-    bool fits(int64_t rows) const { return blocks <= INT_MAX && (rows == 1 || spans <= INT_MAX); }
+    bool fits() const { return blocks <= INT_MAX && cut.spans <= INT_MAX; }
 };
 
-template <typename T, bool VEC>
-cudaError_t forward_t(const ActivationArgs& a, int kind, cudaStream_t s)
+int group_of(const PackedRows& p) { return !p.codes ? 1 : p.log_group == kRowGroup ? 8 : 1 << p.log_group; }
+
+template <typename T, bool VEC, int KIND>
+cudaError_t forward_t(const ActivationArgs& a, cudaStream_t s)
 {
-    const Grid g(a.rows, a.cols);
-    if (!g.fits(a.rows))
+    const Grid g(a.rows, a.cols, kUnitsOf<KIND, VEC>, VEC, std::max(group_of(a.saved), group_of(a.saved_up)));
+    if (!g.fits())
         return cudaErrorInvalidConfiguration;
-    const unsigned blocks = static_cast<unsigned>(g.blocks);
+    const auto go = [&](auto kernel) { return launch_programmatic(kernel, static_cast<unsigned>(g.blocks), kBlock, 0, s, a, g.cut); };
+    if constexpr (VEC)
+        if (g.cut.lanes)
+            return go(k_activation<T, KIND, VEC, true>);
+    return go(k_activation<T, KIND, VEC, false>);
+}
+
+template <typename T, bool VEC>
+cudaError_t forward_k(const ActivationArgs& a, int kind, cudaStream_t s)
+{
     switch (kind) {
-    case LIONCUB_ACTIVATION_SILU: return launch_programmatic(k_activation<T, LIONCUB_ACTIVATION_SILU, VEC>, blocks, kBlock, 0, s, a, g.spans);
-    case LIONCUB_ACTIVATION_GELU: return launch_programmatic(k_activation<T, LIONCUB_ACTIVATION_GELU, VEC>, blocks, kBlock, 0, s, a, g.spans);
-    default: return launch_programmatic(k_activation<T, kIdentity, VEC>, blocks, kBlock, 0, s, a, g.spans);
+    case LIONCUB_ACTIVATION_SILU: return forward_t<T, VEC, LIONCUB_ACTIVATION_SILU>(a, s);
+    case LIONCUB_ACTIVATION_GELU: return forward_t<T, VEC, LIONCUB_ACTIVATION_GELU>(a, s);
+    default: return forward_t<T, VEC, kIdentity>(a, s);
     }
+}
+
+template <typename T, bool VEC, bool PACKED, int KIND>
+cudaError_t backward_k(const ActivationArgs& a, cudaStream_t s)
+{
+    const Grid g(a.rows, a.cols, kUnitsOf<KIND, VEC>, VEC, 8);
+    if (!g.fits())
+        return cudaErrorInvalidConfiguration;
+    const auto go = [&](auto kernel) { return launch_programmatic(kernel, static_cast<unsigned>(g.blocks), kBlock, 0, s, a, g.cut); };
+    if constexpr (VEC)
+        if (g.cut.lanes)
+            return go(k_activation_grad<T, KIND, PACKED, VEC, true>);
+    return go(k_activation_grad<T, KIND, PACKED, VEC, false>);
 }
 
 template <typename T, bool VEC, bool PACKED>
 cudaError_t backward_t(const ActivationArgs& a, int kind, cudaStream_t s)
 {
-    const Grid g(a.rows, a.cols);
-    if (!g.fits(a.rows))
-        return cudaErrorInvalidConfiguration;
-    const unsigned blocks = static_cast<unsigned>(g.blocks);
-    return kind == LIONCUB_ACTIVATION_SILU
-               ? launch_programmatic(k_activation_grad<T, LIONCUB_ACTIVATION_SILU, PACKED, VEC>, blocks, kBlock, 0, s, a, g.spans)
-               : launch_programmatic(k_activation_grad<T, LIONCUB_ACTIVATION_GELU, PACKED, VEC>, blocks, kBlock, 0, s, a, g.spans);
+    return kind == LIONCUB_ACTIVATION_SILU ? backward_k<T, VEC, PACKED, LIONCUB_ACTIVATION_SILU>(a, s)
+                                           : backward_k<T, VEC, PACKED, LIONCUB_ACTIVATION_GELU>(a, s);
 }
 
 template <bool PACKED>
@@ -255,8 +316,8 @@ cudaError_t launch_activation(const ActivationArgs& a, int kind, bool vec, cudaS
     if (a.rows == 0 || a.cols == 0)
         return cudaSuccess;
     if (!vec)
-        return forward_t<float, false>(a, kind, s);
-    return a.x.type == LIONCUB_ROWS_BF16 ? forward_t<__nv_bfloat16, true>(a, kind, s) : forward_t<float, true>(a, kind, s);
+        return forward_k<float, false>(a, kind, s);
+    return a.x.type == LIONCUB_ROWS_BF16 ? forward_k<__nv_bfloat16, true>(a, kind, s) : forward_k<float, true>(a, kind, s);
 }
 
 cudaError_t launch_activation_grad(const ActivationArgs& a, int kind, bool vec, cudaStream_t s)
@@ -270,12 +331,11 @@ cudaError_t launch_unpack(const PackedRows& x, const TypedRows& out, int64_t row
 {
     if (rows == 0 || cols == 0)
         return cudaSuccess;
-    const Grid g(rows, cols);
-    if (!g.fits(rows))
+    const Grid g(rows, cols, vec ? kUnitsOf<kIdentity, true> : kUnitsOf<kIdentity, false>, vec, 8);
+    if (!g.fits())
         return cudaErrorInvalidConfiguration;
-    const unsigned blocks = static_cast<unsigned>(g.blocks);
-    return vec ? launch_programmatic(k_unpack<true>, blocks, kBlock, 0, s, x, out, rows, cols, g.spans)
-               : launch_programmatic(k_unpack<false>, blocks, kBlock, 0, s, x, out, rows, cols, g.spans);
+    const auto go = [&](auto kernel) { return launch_programmatic(kernel, static_cast<unsigned>(g.blocks), kBlock, 0, s, x, out, rows, cols, g.cut); };
+    return !vec ? go(k_unpack<false, false>) : g.cut.lanes ? go(k_unpack<true, true>) : go(k_unpack<true, false>);
 }
 
 }  // namespace lc

@@ -324,7 +324,8 @@ bool overlap(const Box& a, const Box& b)
     return meet(a, b, order, 0, static_cast<int64_t>(b.at) - static_cast<int64_t>(a.at));
 }
 
-int check_heads(const char* name, const lioncub_heads* m, const lioncub_sequences& p, int64_t head_dim, bool is_result, bool* vec)
+// reach: the bits of all addresses and strides in bytes, of which the lowest tells the alignment.
+int check_heads(const char* name, const lioncub_heads* m, const lioncub_sequences& p, int64_t head_dim, bool is_result, uintptr_t* reach)
 {
     if (m->heads < 0 || m->heads > 1 << 20)
         return fail(LIONCUB_ERR_ARG, "%s: %d heads", name, m->heads);
@@ -336,14 +337,13 @@ int check_heads(const char* name, const lioncub_heads* m, const lioncub_sequence
     if (reinterpret_cast<uintptr_t>(m->data) % element_size(m->type))
         return fail(LIONCUB_ERR_ALIGN, "%s is not aligned to its elements", name);
     const int64_t stride[3] = {m->batch_stride, m->place_stride, m->head_stride}, count[3] = {p.batch, p.seq_len, m->heads};
-    const int64_t per16 = 16 / static_cast<int64_t>(element_size(m->type));
-    *vec = *vec && reinterpret_cast<uintptr_t>(m->data) % 16 == 0;
+    *reach |= reinterpret_cast<uintptr_t>(m->data);
     for (int k = 0; k < 3; ++k) {
         if (count[k] <= 1)
             continue;
         if (stride[k] < 0 || stride[k] > kMaxStride || stride[k] > (int64_t(1) << 46) / count[k])
             return fail(LIONCUB_ERR_ARG, "%s: stride %lld", name, (long long)stride[k]);
-        *vec = *vec && stride[k] % per16 == 0;
+        *reach |= stride[k] * element_size(m->type);
     }
     if (is_result && !none) {
         const Box b = box_of(*m, p, head_dim);
@@ -808,12 +808,12 @@ int lioncub_rotary_apply(lioncub_rotary_t h, const lioncub_sequences* places, co
     const lioncub_heads* in[2] = {q, k};
     const lioncub_heads* to[2] = {q_out, k_out};
     static const char* const names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
-    bool vec = h->head_dim % 8 == 0 && h->rotary_dim % 16 == 0;
+    uintptr_t reach = 0;
     bool copy = false;
     for (int i = 0; i < 2 && in[i]; ++i) {
-        int rc = check_heads(names[i][0], in[i], p, h->head_dim, false, &vec);
+        int rc = check_heads(names[i][0], in[i], p, h->head_dim, false, &reach);
         if (rc == LIONCUB_OK)
-            rc = check_heads(names[i][1], to[i], p, h->head_dim, true, &vec);
+            rc = check_heads(names[i][1], to[i], p, h->head_dim, true, &reach);
         if (rc == LIONCUB_OK)
             rc = check_positions(names[i][1], *to[i], p, h->head_dim);
         if (rc != LIONCUB_OK)
@@ -855,7 +855,12 @@ int lioncub_rotary_apply(lioncub_rotary_t h, const lioncub_sequences* places, co
     a.copy = copy;
     a.cos_factor = h->magnitude;
     a.sin_factor = inverse ? -h->magnitude : h->magnitude;
-    return finish_launch(launch(h, "rotary", [&] { return lc::launch_rotary(a, q->type, h->interleaved, vec, stream); }), "rotary launch");
+    // elements moved at once: halves of the rotated columns, and those behind, are whole moves
+    const int64_t size = static_cast<int64_t>(element_size(q->type));
+    int move = reach % 16 == 0 && h->head_dim % 8 == 0 && a.pairs % 8 == 0 ? 8 : 4;
+    while (move < 8 && move > 1 && (reach % (move * size) || (h->head_dim | a.pairs) % move))
+        move /= 2;
+    return finish_launch(launch(h, "rotary", [&] { return lc::launch_rotary(a, q->type, h->interleaved, move, stream); }), "rotary launch");
 }
 
 void lioncub_rotary_destroy(lioncub_rotary_t h)

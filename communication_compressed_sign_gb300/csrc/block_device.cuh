@@ -276,15 +276,20 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const GroupScale& s
     return w;
 }
 
-// One code.
-__device__ __forceinline__ uint8_t code1(float x, float inv, bool bad, bool e4m3)
+// Two codes, in the lowest bytes of either number.
+__device__ __forceinline__ void codes2(float2 x, float inv, bool e4m3, uint32_t& a, uint32_t& b)
 {
-    uint32_t w;
-    if (e4m3)
-        w = __nv_cvt_float_to_fp8(__fmul_rn(x, inv), __NV_SATFINITE, __NV_E4M3);
-    else
-        w = __float_as_uint(fmaf(x, inv, 12582912.0f));
-    return static_cast<uint8_t>(bad ? 0 : w);
+    if (e4m3) {
+        x = mul2(x, both(inv));
+        uint16_t w;
+        asm volatile("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(w) : "f"(x.x), "f"(x.y));
+        a = w;
+        b = w >> 8;
+    } else {
+        x = fma2(x, both(inv), both(12582912.0f));
+        a = __float_as_uint(x.x);
+        b = __float_as_uint(x.y);
+    }
 }
 
 // What eight codes stand for.
@@ -340,27 +345,62 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
                 scales[c.at >> p.log_group] = s.scale;
         }
     } else {
-        // A group is 32 lanes wide and 1 to 8 values deep.  Lane k works out the scale of
-        // the group of value k, and the warp takes it from there.
-        const int deep = 1 << (p.log_group - 5), mine = lane & 7;
-        uint32_t m = 0;
+        // a group is 32 lanes wide and 1 to 8 values deep
+        const auto pack = [&](auto d) {
+            constexpr int kDeep = decltype(d)::value, kGroups = 8 / kDeep;
+            uint32_t m = 0;  // lane g: the largest of group g
+            const int mine = lane & (kGroups - 1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t all = __reduce_max_sync(kAll, __float_as_uint(x[k]) & 0x7fffffffu);
-            m = mine == k ? all : m;
-        }
-        for (int by = 1; by < deep; by <<= 1)
-            m = max(m, __shfl_xor_sync(kAll, m, by));
-        const GroupScale s(m, e4m3);
-        const uint32_t bad = __ballot_sync(kAll, s.bad);
-        const int64_t at = c.at - lane + 32 * mine;  // the first column of value `mine`
-        if (lane < 8 && (mine & (deep - 1)) == 0 && at < p.cols)
-            scales[at >> p.log_group] = s.scale;
+            for (int g = 0; g < kGroups; ++g) {
+                float v = x[g * kDeep];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float inv = __shfl_sync(kAll, s.inv, k);
-            if (k < c.count)
-                codes[32 * k] = code1(x[k], inv, bad >> k & 1, e4m3);
+                for (int k = 1; k < kDeep; k += 2)  // three at a time
+                    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(v) : "f"(x[g * kDeep + k]), "f"(x[g * kDeep + (k + 1 < kDeep ? k + 1 : k)]));
+                const uint32_t all = __reduce_max_sync(kAll, __float_as_uint(v) & 0x7fffffffu);
+                m = mine == g ? all : m;
+            }
+            const GroupScale s(m, e4m3);
+            const int64_t at = c.at - lane + 32 * kDeep * mine;  // the group's first column
+            if (lane < kGroups && at < p.cols)
+                scales[at >> p.log_group] = s.scale;
+            if (c.whole && !__any_sync(kAll, s.bad)) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const float inv = __shfl_sync(kAll, s.inv, g);
+                    if constexpr (kDeep == 1) {
+                        uint32_t code, unused;
+                        codes2(make_float2(x[g], 0.0f), inv, e4m3, code, unused);
+                        codes[32 * g] = static_cast<uint8_t>(code);
+                    } else {
+#pragma unroll
+                        for (int k = g * kDeep; k < (g + 1) * kDeep; k += 2) {
+                            uint32_t a, b;
+                            codes2(make_float2(x[k], x[k + 1]), inv, e4m3, a, b);
+                            codes[32 * k] = static_cast<uint8_t>(a);
+                            codes[32 * k + 32] = static_cast<uint8_t>(b);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const float inv = __shfl_sync(kAll, s.inv, g);
+                    const bool none = __shfl_sync(kAll, s.bad, g);
+#pragma unroll
+                    for (int k = g * kDeep; k < (g + 1) * kDeep; ++k)
+                        if (k < c.count) {
+                            uint32_t code, unused;
+                            codes2(make_float2(x[k], 0.0f), inv, e4m3, code, unused);
+                            codes[32 * k] = none ? 0 : static_cast<uint8_t>(code);
+                        }
+                }
+            }
+        };
+        switch (p.log_group) {
+        case 5: pack(std::integral_constant<int, 1>()); break;
+        case 6: pack(std::integral_constant<int, 2>()); break;
+        case 7: pack(std::integral_constant<int, 4>()); break;
+        default: pack(std::integral_constant<int, 8>()); break;
         }
     }
 }
@@ -376,10 +416,21 @@ __device__ __forceinline__ void pack_chunk_of_row(const PackedRows& p, const Col
         if (c.count)
             *reinterpret_cast<uint2*>(codes) = codes8(x, s, e4m3);
     } else {
+        const bool plain = c.whole && !s.bad;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < c.count)
-                codes[32 * k] = code1(x[k], s.inv, s.bad, e4m3);
+        for (int k = 0; k < 8; k += 2) {
+            uint32_t a, b;
+            codes2(make_float2(x[k], x[k + 1]), s.inv, e4m3, a, b);
+            if (plain) {
+                codes[32 * k] = static_cast<uint8_t>(a);
+                codes[32 * k + 32] = static_cast<uint8_t>(b);
+            } else {
+                if (k < c.count)
+                    codes[32 * k] = s.bad ? 0 : static_cast<uint8_t>(a);
+                if (k + 1 < c.count)
+                    codes[32 * k + 32] = s.bad ? 0 : static_cast<uint8_t>(b);
+            }
+        }
     }
 }
 
@@ -412,16 +463,27 @@ struct CodeChunk<false> {
         const uint8_t* codes = p.codes + row * p.stride + c.at;
         const int64_t at = c.at - lane + 32 * (lane & 7);
         scale = at < p.cols ? p.scales[row * p.scale_stride + (at >> p.log_group)] : 0.0f;
+        if (c.whole) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            code[k] = k < c.count ? codes[32 * k] : 0;
+            for (int k = 0; k < 8; ++k)
+                code[k] = codes[32 * k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                code[k] = k < c.count ? codes[32 * k] : 0;
+        }
     }
     __device__ __forceinline__ void unpack(const PackedRows& p, float (&y)[8]) const
     {
-        const bool e4m3 = p.e4m3;
+        if (p.e4m3) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            y[k] = restore1(code[k], e4m3, __shfl_sync(kAll, scale, k));
+            for (int k = 0; k < 8; ++k)
+                y[k] = restore1(code[k], true, __shfl_sync(kAll, scale, k));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                y[k] = restore1(code[k], false, __shfl_sync(kAll, scale, k));
+        }
     }
 };
 

@@ -40,50 +40,29 @@ __device__ __forceinline__ void angle_of(uint64_t position, uint64_t turns, cons
     s = __fmul_rn(s, a.sin_factor);
 }
 
-// What a thread moves at once: twice 8 columns, half of the rotated ones apart, or a
-// pair of columns; items behind the turning ones are copied, 8 columns or one.
-template <typename T, bool INTERLEAVED, bool VEC>
-struct Item {
+// What a thread moves at once.  16-byte moves: twice 8 columns, half of the rotated
+// ones apart, or 8 columns that are copied.
+template <typename T, bool INTERLEAVED>
+struct WideItem {
+    static constexpr int kPairs = 8, kCopied = 8;
     Group8<T> g[2];
-    T x[2];
     int first, second;  // columns; second < 0: to be copied
 
     __device__ __forceinline__ void place(const RotaryArgs& a, int item, int turning)
     {
-        const int pairs = a.pairs;
-        if (item >= turning) {
-            first = 2 * pairs + (item - turning) * (VEC ? 8 : 1);
-            second = -1;
-        } else if (VEC) {
-            first = item * 8;
-            second = first + pairs;
-        } else {
-            first = INTERLEAVED ? 2 * item : item;
-            second = INTERLEAVED ? first + 1 : first + pairs;
-        }
+        first = item < turning ? item * 8 : 2 * a.pairs + (item - turning) * 8;
+        second = item < turning ? first + a.pairs : -1;
     }
-    __device__ __forceinline__ void load(const T* in)
+    __device__ __forceinline__ void load(const RotaryArgs&, const T* in)
     {
-        if constexpr (VEC) {
-            g[0].load(in, first);
-            if (second >= 0)
-                g[1].load(in, second);
-        } else {
-            x[0] = in[first];
-            if (second >= 0)
-                x[1] = in[second];
-        }
+        g[0].load(in, first);
+        if (second >= 0)
+            g[1].load(in, second);
     }
     __device__ __forceinline__ void turn(const float* cosines, const float* sines, int item, int pairs)
     {
         if (second < 0)
             return;
-        if constexpr (!VEC) {
-            const float u = static_cast<float>(x[0]), v = static_cast<float>(x[1]), c = cosines[item], s = sines[item];
-            x[0] = static_cast<T>(fmaf(u, c, -__fmul_rn(v, s)));
-            x[1] = static_cast<T>(fmaf(v, c, __fmul_rn(u, s)));
-            return;
-        }
         float u[8], v[8];
         g[0].unpack(u);
         g[1].unpack(v);
@@ -113,19 +92,68 @@ struct Item {
         g[0].pack(u);
         g[1].pack(v);
     }
-    __device__ __forceinline__ void store(T* out) const
+    __device__ __forceinline__ void store(const RotaryArgs&, T* out) const
     {
-        if constexpr (VEC) {
-            g[0].store(out, first);
-            if (second >= 0)
-                g[1].store(out, second);
-        } else {
-            out[first] = x[0];
-            if (second >= 0)
-                out[second] = x[1];
-        }
+        g[0].store(out, first);
+        if (second >= 0)
+            g[1].store(out, second);
     }
 };
+
+// Other alignments: four pairs, or eight columns that are copied, MOVE elements at a time.
+template <typename T, bool INTERLEAVED, int MOVE>
+struct NarrowItem {
+    static constexpr int kPairs = 4, kCopied = 8;
+    struct alignas(MOVE * sizeof(T)) Move {
+        T x[MOVE];
+    };
+    Move m[8 / MOVE];  // elements in the order of columns: pairs lie 4 apart, or side by side
+    int first, count;  // a column, or a pair, and how many are left from it
+    bool copied;
+
+    __device__ __forceinline__ void place(const RotaryArgs& a, int item, int turning)
+    {
+        copied = item >= turning;
+        first = copied ? 2 * a.pairs + (item - turning) * 8 : item * 4;
+        count = copied ? a.head_dim - first : a.pairs - first;
+    }
+    __device__ __forceinline__ int column(const RotaryArgs& a, int k) const
+    {
+        return copied ? first + k : INTERLEAVED ? 2 * first + k : first + (k & 3) + (k >> 2) * a.pairs;
+    }
+    __device__ __forceinline__ bool has(int k) const { return (copied ? k : INTERLEAVED ? k >> 1 : k & 3) < count; }
+    __device__ __forceinline__ T& element(int k) { return m[k / MOVE].x[k % MOVE]; }
+    __device__ __forceinline__ void load(const RotaryArgs& a, const T* in)
+    {
+#pragma unroll
+        for (int k = 0; k < 8; k += MOVE)
+            if (has(k))
+                m[k / MOVE] = *reinterpret_cast<const Move*>(in + column(a, k));
+    }
+    __device__ __forceinline__ void turn(const float* cosines, const float* sines, int item, int)
+    {
+        if (copied)
+            return;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < count) {
+                T &one = element(INTERLEAVED ? 2 * k : k), &two = element(INTERLEAVED ? 2 * k + 1 : k + 4);
+                const float u = static_cast<float>(one), v = static_cast<float>(two), c = cosines[item * 4 + k], s = sines[item * 4 + k];
+                one = static_cast<T>(fmaf(u, c, -__fmul_rn(v, s)));
+                two = static_cast<T>(fmaf(v, c, __fmul_rn(u, s)));
+            }
+    }
+    __device__ __forceinline__ void store(const RotaryArgs& a, T* out) const
+    {
+#pragma unroll
+        for (int k = 0; k < 8; k += MOVE)
+            if (has(k))
+                *reinterpret_cast<Move*>(out + column(a, k)) = m[k / MOVE];
+    }
+};
+
+template <typename T, bool INTERLEAVED, int MOVE>
+using ItemOf = std::conditional_t<MOVE == 8, WideItem<T, INTERLEAVED>, NarrowItem<T, INTERLEAVED, MOVE>>;
 
 // n / d by a product, for n * d < 2^32; a block whose numbers are larger divides.
 struct Divisor {
@@ -134,11 +162,12 @@ struct Divisor {
 };
 Divisor divisor(uint32_t d, uint64_t largest) { return {d, d > 1 && largest * d < (1ull << 32) ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0}; }
 
-template <typename T, bool INTERLEAVED, bool VEC>
+template <typename T, bool INTERLEAVED, int MOVE>
 __global__ void __launch_bounds__(kBlock) k_rotary(const __grid_constant__ RotaryArgs a, const int turning, const Divisor items,
                                                    const Divisor heads0, const Divisor heads1, const int block_places)
 {
-    constexpr int kUnits = VEC ? 2 : 4;  // items of a thread, whose loads are in flight together
+    constexpr int kUnits = 2;  // items of a thread, whose loads are in flight together
+    using Item = ItemOf<T, INTERLEAVED, MOVE>;
     extern __shared__ __align__(16) float cosines[];  // of each place and pair; then the sines
     __shared__ int64_t starts[kMaxPlaces][4];         // of a place: elements to its in and out of either side
     float* sines = cosines + block_places * a.pairs;
@@ -170,7 +199,7 @@ __global__ void __launch_bounds__(kBlock) k_rotary(const __grid_constant__ Rotar
         T* out = static_cast<T*>(a.side[k].out);
         const int64_t in_head = a.side[k].in_head, out_head = a.side[k].out_head;
         for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kUnits * kBlock) {
-            Item<T, INTERLEAVED, VEC> x[kUnits];
+            Item x[kUnits];
             uint32_t item[kUnits], p[kUnits], h[kUnits];
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
@@ -181,24 +210,25 @@ __global__ void __launch_bounds__(kBlock) k_rotary(const __grid_constant__ Rotar
                     p[u] = heads.of(head);
                     h[u] = head - p[u] * heads.d;
                     x[u].place(a, item[u], turning);
-                    x[u].load(in + (starts[p[u]][2 * k] + h[u] * in_head));
+                    x[u].load(a, in + (starts[p[u]][2 * k] + h[u] * in_head));
                 }
             }
 #pragma unroll
             for (int u = 0; u < kUnits; ++u)
                 if (u0 + u * kBlock < units) {
                     x[u].turn(cosines + p[u] * a.pairs, sines + p[u] * a.pairs, item[u], a.pairs);
-                    x[u].store(out + (starts[p[u]][2 * k + 1] + h[u] * out_head));
+                    x[u].store(a, out + (starts[p[u]][2 * k + 1] + h[u] * out_head));
                 }
         }
     }
 }
 
-template <typename T, bool INTERLEAVED, bool VEC>
+template <typename T, bool INTERLEAVED, int MOVE>
 cudaError_t launch_t(const RotaryArgs& a, cudaStream_t s)
 {
     const int rest = a.copy ? a.head_dim - 2 * a.pairs : 0;
-    const int turning = VEC ? a.pairs / 8 : a.pairs, items = turning + (VEC ? rest / 8 : rest);
+    using Item = ItemOf<T, INTERLEAVED, MOVE>;
+    const int turning = (a.pairs + Item::kPairs - 1) / Item::kPairs, items = turning + (rest + Item::kCopied - 1) / Item::kCopied;
     // Places of a block: about kItems items for each of its threads, fewer while that leaves
     // less than four blocks a multiprocessor.
     const int64_t of_place = int64_t(a.heads[0] + a.heads[1]) * items;
@@ -208,25 +238,30 @@ cudaError_t launch_t(const RotaryArgs& a, cudaStream_t s)
     const int64_t most = places * std::max(a.heads[0], a.heads[1]) * items;
     if (blocks > INT_MAX || most > INT_MAX)
         return cudaErrorInvalidConfiguration;
-    return launch_programmatic(k_rotary<T, INTERLEAVED, VEC>, static_cast<unsigned>(blocks), kBlock, places * a.pairs * 2 * sizeof(float), s, a,
+    return launch_programmatic(k_rotary<T, INTERLEAVED, MOVE>, static_cast<unsigned>(blocks), kBlock, places * a.pairs * 2 * sizeof(float), s, a,
                                turning, divisor(items, most), divisor(a.heads[0], most), divisor(a.heads[1], most), static_cast<int>(places));
 }
 
-template <typename T>
-cudaError_t launch_l(const RotaryArgs& a, bool interleaved, bool vec, cudaStream_t s)
+template <typename T, bool INTERLEAVED>
+cudaError_t launch_l(const RotaryArgs& a, int move, cudaStream_t s)
 {
-    if (vec)
-        return interleaved ? launch_t<T, true, true>(a, s) : launch_t<T, false, true>(a, s);
-    return interleaved ? launch_t<T, true, false>(a, s) : launch_t<T, false, false>(a, s);
+    switch (move) {
+    case 8: return launch_t<T, INTERLEAVED, 8>(a, s);
+    case 4: return launch_t<T, INTERLEAVED, 4>(a, s);
+    case 2: return launch_t<T, INTERLEAVED, 2>(a, s);
+    default: return launch_t<T, INTERLEAVED, 1>(a, s);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, bool vec, cudaStream_t s)
+cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, int move, cudaStream_t s)
 {
     if (a.places == 0 || a.heads[0] + a.heads[1] == 0)
         return cudaSuccess;
-    return type == LIONCUB_ROWS_BF16 ? launch_l<__nv_bfloat16>(a, interleaved, vec, s) : launch_l<float>(a, interleaved, vec, s);
+    if (type == LIONCUB_ROWS_BF16)
+        return interleaved ? launch_l<__nv_bfloat16, true>(a, move, s) : launch_l<__nv_bfloat16, false>(a, move, s);
+    return interleaved ? launch_l<float, true>(a, move, s) : launch_l<float, false>(a, move, s);
 }
 
 }  // namespace lc

@@ -173,13 +173,26 @@ def _rows(t, name, nrows, cols, device):
         raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(t.shape)})")
     if t.is_contiguous():
         return _pack_rows(t.data_ptr(), cols, kind, 0)
-    try:
-        t = t.view(-1, cols)  # rows a fixed distance apart
-    except RuntimeError:
-        raise ValueError(f"{name}: its rows do not lie a fixed distance apart") from None
-    if cols > 1 and t.stride(1) != 1:
+    return _pack_rows(t.data_ptr(), _step(t, name, nrows, cols), kind, 0)
+
+
+def _step(t, name, nrows, cols):
+    """The distance between the rows of a tensor that is not contiguous."""
+    strides = t.stride()
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the columns of a row must be contiguous")
-    return _pack_rows(t.data_ptr(), t.stride(0) if nrows > 1 else cols, kind, 0)
+    if len(strides) == 2:
+        return strides[0] if nrows > 1 else cols
+    step = reach = None  # of the dimensions so far, from the inner ones outwards
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(strides[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = reach = stride
+        elif stride != reach:
+            raise ValueError(f"{name}: its rows do not lie a fixed distance apart")
+        reach *= size
+    return cols if step is None else step
 
 
 def _drop_spec(drop):
