@@ -268,6 +268,39 @@ def test_norm_gradient(ops, n, D, dk, hk, gk):
     assert layer.status() == 0
 
 
+@pytest.mark.parametrize("n,D", [(30000, 768), (30000, 771), (12000, 2048), (40000, 192), (2000, 8200), (700, 16384), (600, 16383), (5000, 520)])
+@pytest.mark.parametrize("hk", ["f32", "int8"])
+def test_norm_gradient_of_many_rows(ops, n, D, hk):
+    """Rows enough that every place of the rings is used several times."""
+    g = torch.Generator(device="cuda").manual_seed(n + D)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
+    dout, res = rand(n, D).bfloat16(), rand(n, D)
+    h, w = rand(n, D), 1 + 0.1 * rand(D)
+    rstd = (h.double().square().mean(1) + EPS).rsqrt().float()
+    saved = h if hk == "f32" else ops.pack8(h, group=64)
+    h = h if hk == "f32" else ops.unpack8(saved, out_dtype=torch.float32)
+    layer = ops.RmsNorm(D)
+    dw, again = torch.empty(D, device="cuda"), torch.empty(n, D, dtype=torch.bfloat16, device="cuda")
+    dx = layer.backward(dout, saved, rstd, w, residual_grad=res, weight_grad=dw, again=again, out_dtype=torch.float32)
+    worst = 0.0
+    dw0, wm = torch.zeros(D, dtype=torch.float64, device="cuda"), torch.zeros(D, dtype=torch.float64, device="cuda")
+    for part in torch.arange(n, device="cuda").split(4096):
+        d, hh, r = dout[part].double(), h[part].double(), rstd[part].double()[:, None]
+        nn, gg = hh * r, d * w.double()
+        exact = r * (gg - nn * (gg * nn).mean(1, keepdim=True)) + res[part].double()
+        mag = r * (gg.abs() + nn.abs() * (gg * nn).abs().mean(1, keepdim=True)) + res[part].double().abs()
+        worst = max(worst, ((dx[part].double() - exact).abs() / mag).max().item())
+        y = nn * w.double()
+        assert ((again[part].double() - y).abs() <= y.abs() * (2.0 ** -8 + 2.0 ** -20)).all()
+        dw0 += (d * nn).sum(0)
+        wm += (d * nn).abs().sum(0)
+    assert worst < 64 * 2.0 ** -24
+    # a column's chain: one row of each ring's turn, then the teams and blocks
+    assert ((dw.double() - dw0).abs() <= wm * (n / 152 + 200) * 2.0 ** -24).all()
+    assert torch.equal(dx, layer.backward(dout, saved, rstd, w, residual_grad=res, weight_grad=dw, out_dtype=torch.float32))
+    assert layer.status() == 0
+
+
 def test_norm_gradient_of_no_rows_and_in_place(ops):
     D = 264
     layer = ops.RmsNorm(D)
@@ -375,6 +408,33 @@ def test_activation_in_place_and_side_by_side(ops):
     assert ops.activation(torch.empty(0, 5, device="cuda")).shape == (0, 5)
 
 
+@pytest.mark.parametrize("rows,cols", [(300, 128), (70, 40), (13, 640), (1, 64), (129, 8), (5, 1032)])
+@pytest.mark.parametrize("code,group", [("int8", 32), ("e4m3", 128), ("int8", 256)])
+def test_rows_narrower_than_a_warps_chunks(ops, rows, cols, code, group):
+    """Rows out of wider ones, whole groups of columns or not, of several a warp: each as by itself in one piece."""
+    wide = _rand((rows, 3 * cols + 8), "bf16", rows + cols).cuda()
+    x, up, dout = wide[:, :cols], wide[:, cols:2 * cols], wide[:, 2 * cols:3 * cols]
+    apart = [ops.Packed.empty((rows, cols + 256), group=group, dtype=CODES[code]) for _ in range(2)]
+    groups = -(-cols // group)
+    saved, saved_up = (ops.Packed(p.codes[:, :cols], p.scales[:, :groups], group) for p in apart)
+    y = ops.activation(x, up, kind="silu", saved=saved, saved_up=saved_up)
+    f, fm, _, _ = ref.value_and_slope(_np(x), "silu")
+    _check(y, f * _np(up), fm * np.abs(_np(up)), 16, torch.bfloat16)
+    for p, m in ((saved, x), (saved_up, up)):
+        codes, scales = ref.pack(m.float().cpu().numpy(), code, group)
+        assert np.array_equal(_bits(p.codes).reshape(rows, cols), codes) and np.array_equal(p.scales.cpu().numpy(), scales)
+        assert torch.equal(ops.unpack8(p, out_dtype=torch.float32).cpu(), torch.from_numpy(ref.unpack(codes, scales, code, group)))
+        q = ops.pack8(m, group=group, dtype=CODES[code])
+        assert np.array_equal(_bits(q.codes).reshape(rows, cols), codes) and np.array_equal(q.scales.cpu().numpy(), scales)
+    again = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    dx, dup = ops.activation_backward(dout, saved, saved_up, kind="silu", again=again)
+    x64, u64, d64 = _restored(saved, code).astype(np.float64), _restored(saved_up, code).astype(np.float64), _np(dout)
+    f, fm, slope, sm = ref.value_and_slope(x64, "silu")
+    _check(dx, d64 * u64 * slope, np.abs(d64 * u64) * sm, 32, torch.bfloat16)
+    _check(dup, d64 * f, np.abs(d64) * fm, 16, torch.bfloat16)
+    _check(again, f * u64, fm * np.abs(u64), 16, torch.bfloat16)
+
+
 # ---- rotary positions ----------------------------------------------------------------------
 
 def _frequencies(dim, base=10000.0):
@@ -383,7 +443,7 @@ def _frequencies(dim, base=10000.0):
 
 @pytest.mark.parametrize("B,S,H,K,D,R", [(1, 1, 1, 1, 2, 2), (2, 3, 2, 1, 64, 64), (1, 17, 12, 12, 64, 32), (3, 5, 7, 3, 80, 40),
                                          (2, 4, 32, 8, 128, 128), (1, 2, 3, 0, 256, 64), (2, 3, 5, 2, 66, 22), (1, 3, 2, 2, 96, 48),
-                                         (4, 1, 1, 0, 24, 8)])
+                                         (4, 1, 1, 0, 24, 8), (3, 7, 4, 8, 80, 20), (1, 40, 3, 2, 1024, 1024)])
 @pytest.mark.parametrize("kind", list(T))
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotary(ops, B, S, H, K, D, R, kind, interleaved):
@@ -580,6 +640,90 @@ def test_streams_and_graphs(ops):
     assert layer.status() == 0
 
 
+def test_launches_in_a_row_see_each_others_results(ops):
+    """Kernels may start before the one before them has ended: a chain without any wait between equals one with them."""
+    D, n = 512, 2000
+    layer, rot = ops.RmsNorm(D), ops.Rotary(64, interleaved=True)
+    w, dw = 1 + _rand((D,), "f32", 2, 0.1).cuda(), torch.zeros(D, device="cuda")
+    x0 = _rand((n, D), "bf16", 3).cuda()
+    p, pa, rstd, dup = ops.Packed.empty((n, D)), ops.Packed.empty((n, D)), torch.empty(n, device="cuda"), torch.empty_like(x0)
+
+    def go(x, wait):
+        w_ = w.clone()
+        for _ in range(12):
+            for step in (lambda: layer.forward(x, w_, residual=x0, saved=p, rstd=rstd, out=x),
+                         lambda: rot.forward(x.view(1, n, 8, 64), q_out=x.view(1, n, 8, 64), first_position=5),
+                         lambda: ops.activation(x, x0, kind="gelu", out=x, saved=pa),
+                         lambda: ops.unpack8(pa, out=dup),
+                         lambda: layer.backward(x, p, rstd, w_, residual_grad=dup, out=x, weight_grad=w_, weight_base=w_),
+                         lambda: x.mul_(0.25), lambda: w_.clamp_(0.5, 2.0),
+                         lambda: ops.pack8(x, out=pa),
+                         lambda: ops.activation_backward(x, pa, kind="silu", dx=x)):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        return x, w_
+
+    want = go(x0.clone(), True)
+    for _ in range(5):
+        got = go(x0.clone(), False)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert layer.status() == 0 and bool(want[0].isfinite().all()) and dw.sum() == 0
+
+
+def test_calls_of_several_host_threads(ops):
+    import threading
+    D, n = 264, 500
+    layer, rot = ops.RmsNorm(D), ops.Rotary(66, rotary_dim=32)
+    x = _rand((n, D), "bf16", 3).cuda()
+    want = (layer.forward(x), rot.forward(x.view(1, n, 4, 66)), ops.activation(x), ops.unpack8(ops.pack8(x)))
+    failed = []
+
+    def work(i):
+        try:
+            own, stream = ops.RmsNorm(D), torch.cuda.Stream()
+            rstd, dw = torch.ones(n, device="cuda"), torch.empty(D, device="cuda")
+            stream.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(stream):
+                for k in range(50):
+                    got = (layer.forward(x), rot.forward(x.view(1, n, 4, 66)), ops.activation(x), ops.unpack8(ops.pack8(x)))
+                    own.backward(x, x, rstd, weight_grad=dw)
+                    bad = ops.Packed.empty((n, D), group=7)
+                    try:
+                        ops.pack8(x, out=bad)
+                        failed.append("no refusal")
+                    except ops.LionCubError as e:
+                        if "group" not in str(e):
+                            failed.append(str(e))
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        failed.append((i, k))
+            assert own.status() == 0
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed, failed[:3]
+
+
+def test_waits_that_run_out_and_guards(ops, monkeypatch):
+    """The first wait for a row's copies gives up after one test: the call ends, and the status word tells."""
+    n, D = 4000, 768
+    dout, h, rstd = _rand((n, D), "bf16", 1).cuda(), _rand((n, D), "f32", 2).cuda(), torch.ones(n, device="cuda")
+    good = ops.RmsNorm(D)
+    dw, want = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    dx = good.backward(dout, h, rstd, weight_grad=want)
+    monkeypatch.setenv("LIONCUB_WAIT_POLLS", "1")
+    bad = ops.RmsNorm(D)
+    monkeypatch.delenv("LIONCUB_WAIT_POLLS")
+    bad.backward(dout, h, rstd, weight_grad=dw)
+    assert bad.status() == 1  # LIONCUB_STATUS_WAIT_TIMEOUT
+    bad.close()
+    assert torch.equal(good.backward(dout, h, rstd, weight_grad=dw), dx) and torch.equal(dw, want) and good.status() == 0
+
+
 def test_offsets_beyond_32_bits(ops):
     """More than 2^32 elements: the first, a middle and the last rows are those of a small call."""
     D, n = 16384, (1 << 18) + 1037
@@ -767,6 +911,6 @@ def test_bounds_checked_build(ops):
     if os.environ.get("LIONCUB_LIBRARY") == lib:
         return
     r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_gpu_block.py", "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider",
-                        "-k", "norm_gradient and not bounds or streams or block_forward"],
+                        "-k", "norm_gradient or streams or block_forward"],
                        cwd=root, env={**os.environ, "LIONCUB_LIBRARY": lib}, capture_output=True, text=True, timeout=1200)
     assert r.returncode == 0 and " passed" in r.stdout, (r.stdout + r.stderr)[-3000:]
