@@ -263,6 +263,8 @@ def _vector(t, name, n, device):
     """The address of n contiguous fp32 numbers."""
     if t.dtype != _torch.float32 or t.get_device() != device or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements on cuda:{device}")
+    if t.requires_grad and _torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, but results are not part of torch's graph")
     return t.data_ptr()
 
 

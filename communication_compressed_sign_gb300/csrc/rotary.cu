@@ -170,23 +170,24 @@ __global__ void __launch_bounds__(kBlock) k_rotary(const __grid_constant__ Rotar
     using Item = ItemOf<T, INTERLEAVED, MOVE>;
     extern __shared__ __align__(16) float cosines[];  // of each place and pair; then the sines
     __shared__ int64_t starts[kMaxPlaces][4];         // of a place: elements to its in and out of either side
+    __shared__ int64_t positions[kMaxPlaces];
     float* sines = cosines + block_places * a.pairs;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * block_places;
     const int places = static_cast<int>(min(a.places - first, static_cast<int64_t>(block_places)));
+    if (a.positions)
+        wait_for_launch_before();
     if (threadIdx.x < places) {
         const int64_t place = first + threadIdx.x, b = quotient(place, a.seq), s = place - b * a.seq;
+        positions[threadIdx.x] = a.positions ? index_at(a.positions, place, a.wide) : a.first + s;
         for (int k = 0; k < 2; ++k) {
             starts[threadIdx.x][2 * k] = b * a.side[k].in_batch + s * a.side[k].in_place;
             starts[threadIdx.x][2 * k + 1] = b * a.side[k].out_batch + s * a.side[k].out_place;
         }
     }
-    if (a.positions)
-        wait_for_launch_before();
+    __syncthreads();
     for (int i = threadIdx.x; i < places * a.pairs; i += kBlock) {
         const int p = i / a.pairs;
-        const int64_t place = first + p;
-        const int64_t position = a.positions ? index_at(a.positions, place, a.wide) : a.first + place % a.seq;
-        angle_of(static_cast<uint64_t>(position), a.turns[i - p * a.pairs], a, cosines[i], sines[i]);
+        angle_of(static_cast<uint64_t>(positions[p]), a.turns[i - p * a.pairs], a, cosines[i], sines[i]);
     }
     if (!a.positions)  // the angles need nothing of the launches before
         wait_for_launch_before();

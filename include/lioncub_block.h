@@ -42,7 +42,11 @@
  * Return codes are those of lioncub.h.
  *
  * Matrices are lioncub_rows, as in lioncub_embed.h; rows that start on 16-byte
- * boundaries and whose width is a multiple of 8 are moved 16 bytes at a time.
+ * boundaries and whose width is a multiple of 8 are moved 16 bytes at a time, if
+ * all matrices of a call allow it and rows of codes start on 8-byte boundaries
+ * (read by a norm's gradient: 16, and a width that is a multiple of 16).  Heads
+ * want 16-byte boundaries and halves of the rotated columns of 8.  Anything else
+ * works element by element, at two to four times the cost.
  * A result may be the same matrix as an input of its type (the same address and
  * stride), each element then being read before it is written; results may not
  * share bytes with inputs in any other way, nor with one another.
@@ -118,7 +122,8 @@ typedef struct {
  * dim bytes for each multiprocessor) on the current device, which must be
  * current in every later call on the handle, and synchronizes the legacy default
  * stream once.  LIONCUB_FAIL_ALLOC and LIONCUB_FAIL_LAUNCH (lioncub.h) apply to
- * the handle's own allocations and kernel launches.  eps must be positive (a row
+ * the handle's own allocations and kernel launches, LIONCUB_WAIT_POLLS to the first wait of
+ * each of a gradient's teams of warps for the copies that bring it rows.  eps must be positive (a row
  * of zeros then gives zeros).  Errors: ERR_ARG, ERR_OOM, ERR_CUDA (*out is NULL then).
  */
 LIONCUB_API int lioncub_rms_norm_create(lioncub_rms_norm_t* out, int64_t dim, float eps);
