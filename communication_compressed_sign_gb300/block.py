@@ -14,11 +14,10 @@ from __future__ import annotations
 
 import ctypes
 import math
-import struct
 from typing import NamedTuple
 
 from . import embed
-from .embed import _empty, _matrix, _rows, _step
+from .embed import _empty
 from .lioncub import ERR_STATE, OK, LionCubError
 
 CODES_INT8, CODES_E4M3 = 0, 1
@@ -59,11 +58,6 @@ class ScalingSpec(ctypes.Structure):
                 ("kind", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-# The first three as bytes, as in embed.
-_pack_packed = struct.Struct("@PPqqii").pack
-_pack_heads = struct.Struct("@Pqqqii").pack
-_pack_sequences = struct.Struct("@Pqqqii").pack
-
 _lib = None
 
 
@@ -100,7 +94,7 @@ def _check(rc: int) -> None:
         raise LionCubError(rc, L.lioncub_block_last_error().decode() or L.lioncub_strerror(rc).decode())
 
 
-# Matrices are structs as bytes or ctypes.byref(), vectors addresses, None for NULL.
+# Matrices are ctypes.byref() of a struct, vectors addresses, None for NULL.
 
 def lioncub_rms_norm_create(dim: int, eps: float) -> int:
     h = ctypes.c_void_p()
@@ -181,17 +175,29 @@ def lioncub_rotary_destroy(h: int) -> None:
 
 
 # ---- torch tensors -------------------------------------------------------------
+#
+# The module _tensors reads what a call needs from the tensors and calls the library.
 
 _torch = None
-_formats = None
+_tensors = None
+_device = None
 
 
 def _use_torch():
-    global _torch, _formats
+    global _torch, _tensors, _device
     embed._use_torch()
     import torch
-    _formats = {torch.int8: CODES_INT8, torch.float8_e4m3fn: CODES_E4M3}
-    _torch = torch
+    try:
+        from . import _tensors as module
+    except ImportError as e:
+        raise RuntimeError("the _tensors module is missing or does not fit this torch: run "
+                           "python -m communication_compressed_sign_gb300.build") from e
+    L = load()
+    module.bind(*(ctypes.cast(getattr(L, f"lioncub_{name}"), ctypes.c_void_p).value for name in (
+        "rms_norm_forward", "rms_norm_backward", "pack8", "unpack8", "activation_forward", "activation_backward", "rotary_apply")))
+    # the current device's number, without what torch.cuda.current_device() does before
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _tensors, _torch = module, torch
 
 
 def _raw(dev, stream):
@@ -228,46 +234,6 @@ class Packed:
         return f"Packed({tuple(self.codes.shape)}, {self.codes.dtype}, group={self.group})"
 
 
-def _codes(p, name, nrows, cols, device):
-    """A Packed of nrows rows as a packed lioncub_packed."""
-    codes, scales, group = p.codes, p.scales, p.group
-    kind = _formats.get(codes.dtype)
-    if kind is None or codes.get_device() != device:
-        raise ValueError(f"{name}: codes must be an int8 or float8_e4m3fn tensor on cuda:{device}")
-    if scales.dtype != _torch.float32 or scales.get_device() != device:
-        raise ValueError(f"{name}: scales must be a float32 tensor on cuda:{device}")
-    groups = -(-cols // group) if group > 0 else 1
-    if not codes.dim() or codes.size(-1) != cols or codes.numel() != nrows * cols:
-        raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(codes.shape)})")
-    if not scales.dim() or scales.size(-1) != groups or scales.numel() != nrows * groups:
-        raise ValueError(f"{name} must have {nrows} rows of {groups} scales (got {tuple(scales.shape)})")
-    step = cols if codes.is_contiguous() else _step(codes, name, nrows, cols)
-    scale_step = groups if scales.is_contiguous() else _step(scales, name, nrows, groups)
-    return _pack_packed(codes.data_ptr(), scales.data_ptr(), step, scale_step, group, kind)
-
-
-def _either(t, name, nrows, cols, device):
-    """(matrix, None) or (None, codes) of a tensor or a Packed; two Nones of None."""
-    if t is None:
-        return None, None
-    if isinstance(t, Packed):
-        return None, _codes(t, name, nrows, cols, device)
-    return _rows(t, name, nrows, cols, device), None
-
-
-def _optional(t, name, nrows, cols, device):
-    return None if t is None else _rows(t, name, nrows, cols, device)
-
-
-def _vector(t, name, n, device):
-    """The address of n contiguous fp32 numbers."""
-    if t.dtype != _torch.float32 or t.get_device() != device or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements on cuda:{device}")
-    if t.requires_grad and _torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient, but results are not part of torch's graph")
-    return t.data_ptr()
-
-
 class RmsNorm:
     """The root-mean-square norm of rows of `dim` columns,
     h * rstd * weight with h = x + residual and rstd = 1 / sqrt(mean(h^2) + eps),
@@ -283,17 +249,10 @@ class RmsNorm:
         if _torch is None:
             _use_torch()
         self.dim, self.eps = int(dim), float(eps)
-        self.h = None
+        self.h = 0
         self.h = lioncub_rms_norm_create(self.dim, self.eps)
         self.device = _torch.device("cuda", embed._device())
         self._index = self.device.index
-
-    def _count(self, x, name):
-        if not self.h:
-            raise LionCubError(ERR_STATE, "the norm is closed")
-        if not x.dim() or x.size(-1) != self.dim:
-            raise ValueError(f"{name} must have rows of {self.dim} columns (got {tuple(x.shape)})")
-        return x.numel() // self.dim
 
     def forward(self, x, weight=None, *, residual=None, summed=None, saved=None, rstd=None, out=None, out_dtype=None, stream=None):
         """The normed rows of x (..., dim) + residual: `out`, a tensor or a
@@ -302,14 +261,14 @@ class RmsNorm:
         the residual itself is allowed), saved (a Packed) the same in 8 bits,
         and rstd (float32, one a row); the backward pass needs rstd and one of
         the two."""
-        n, D, dev = self._count(x, "x"), self.dim, self._index
+        if not self.h:
+            raise LionCubError(ERR_STATE, "the norm is closed")
         if out is None:
             out = _empty(x.shape, out_dtype or x.dtype, self.device, stream)
-        y, packed_y = _either(out, "out", n, D, dev)
-        lioncub_rms_norm_forward(
-            self.h, n, _rows(x, "x", n, D, dev), _optional(residual, "residual", n, D, dev), _optional(weight, "weight", 1, D, dev),
-            _optional(summed, "summed", n, D, dev), None if saved is None else _codes(saved, "saved", n, D, dev),
-            None if rstd is None else _vector(rstd, "rstd", n, dev), y, packed_y, _raw(dev, stream))
+        rc = _tensors.rms_norm_forward(self.h, self.dim, self._index, x, residual, weight, summed, saved, rstd, out,
+                                       _raw(self._index, stream))
+        if rc:
+            _check(rc)
         return out
 
     def backward(self, dout, saved, rstd, weight=None, *, residual_grad=None, out=None, out_dtype=None, weight_grad=None,
@@ -319,15 +278,14 @@ class RmsNorm:
         residual_grad is added: what reaches the sum by another way.  weight_grad
         (dim,) is written where it is given, weight_base added to it (weight_grad
         itself adds in place); again receives the normed rows once more."""
-        n, D, dev = self._count(dout, "dout"), self.dim, self._index
+        if not self.h:
+            raise LionCubError(ERR_STATE, "the norm is closed")
         if out is None:
             out = _empty(dout.shape, out_dtype or dout.dtype, self.device, stream)
-        h, packed_h = _either(saved, "saved", n, D, dev)
-        lioncub_rms_norm_backward(
-            self.h, n, _rows(dout, "dout", n, D, dev), h, packed_h, _vector(rstd, "rstd", n, dev),
-            _optional(weight, "weight", 1, D, dev), _optional(residual_grad, "residual_grad", n, D, dev),
-            _rows(out, "out", n, D, dev), _optional(weight_base, "weight_base", 1, D, dev),
-            _optional(weight_grad, "weight_grad", 1, D, dev), _optional(again, "again", n, D, dev), _raw(dev, stream))
+        rc = _tensors.rms_norm_backward(self.h, self.dim, self._index, dout, saved, rstd, weight, residual_grad, out, weight_base,
+                                        weight_grad, again, _raw(self._index, stream))
+        if rc:
+            _check(rc)
         return out
 
     def status(self) -> int:
@@ -342,7 +300,7 @@ class RmsNorm:
     def close(self):
         if self.h:
             lioncub_rms_norm_destroy(self.h)
-            self.h = None
+            self.h = 0
 
     def __del__(self):
         try:
@@ -355,10 +313,12 @@ def pack8(x, *, group=128, dtype=None, out=None, stream=None) -> Packed:
     """x in 8 bits: `out`, or a new Packed of `group` and dtype (int8 by default)."""
     if _torch is None:
         _use_torch()
-    rows, cols, dev = _matrix(x, "x")
+    dev = _device()
     if out is None:
         out = Packed.empty(x.shape, group, dtype, x.device, stream)
-    lioncub_pack8(rows, cols, _rows(x, "x", rows, cols, dev), _codes(out, "out", rows, cols, dev), _raw(dev, stream))
+    rc = _tensors.pack8(dev, x, out, _raw(dev, stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -366,10 +326,12 @@ def unpack8(x: Packed, *, out=None, out_dtype=None, stream=None):
     """What a Packed stands for: `out`, or a new tensor of out_dtype (bfloat16 by default)."""
     if _torch is None:
         _use_torch()
-    rows, cols, dev = _matrix(x.codes, "x")
+    dev, codes = _device(), x.codes
     if out is None:
-        out = _empty(x.codes.shape, out_dtype or _torch.bfloat16, x.codes.device, stream)
-    lioncub_unpack8(rows, cols, _codes(x, "x", rows, cols, dev), _rows(out, "out", rows, cols, dev), _raw(dev, stream))
+        out = _empty(codes.shape, out_dtype or _torch.bfloat16, codes.device, stream)
+    rc = _tensors.unpack8(dev, codes, x, out, _raw(dev, stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -389,13 +351,12 @@ def activation(x, up=None, *, kind="gelu", out=None, saved=None, saved_up=None, 
     saved_up (Packed, groups of columns) receive x and up in 8 bits."""
     if _torch is None:
         _use_torch()
-    rows, cols, dev = _matrix(x, "x")
+    dev = _device()
     if out is None:
         out = _empty(x.shape, x.dtype, x.device, stream)
-    lioncub_activation_forward(
-        rows, cols, _kind(kind), _rows(x, "x", rows, cols, dev), _optional(up, "up", rows, cols, dev),
-        _rows(out, "out", rows, cols, dev), None if saved is None else _codes(saved, "saved", rows, cols, dev),
-        None if saved_up is None else _codes(saved_up, "saved_up", rows, cols, dev), _raw(dev, stream))
+    rc = _tensors.activation_forward(dev, _kind(kind), x, up, out, saved, saved_up, _raw(dev, stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -406,16 +367,14 @@ def activation_backward(dout, x, up=None, *, kind="gelu", dx=None, dup=None, aga
     receives the forward call's result once more."""
     if _torch is None:
         _use_torch()
-    rows, cols, dev = _matrix(dout, "dout")
+    dev = _device()
     if dx is None:
         dx = _empty(dout.shape, dout.dtype, dout.device, stream)
     if up is not None and dup is None:
         dup = _empty(dout.shape, dout.dtype, dout.device, stream)
-    xr, xc = _either(x, "x", rows, cols, dev)
-    ur, uc = _either(up, "up", rows, cols, dev)
-    lioncub_activation_backward(
-        rows, cols, _kind(kind), _rows(dout, "dout", rows, cols, dev), xr, ur, xc, uc, _rows(dx, "dx", rows, cols, dev),
-        _optional(dup, "dup", rows, cols, dev), _optional(again, "again", rows, cols, dev), _raw(dev, stream))
+    rc = _tensors.activation_backward(dev, _kind(kind), dout, x, up, dx, dup, again, _raw(dev, stream))
+    if rc:
+        _check(rc)
     return dx if up is None else (dx, dup)
 
 
@@ -477,50 +436,24 @@ class Rotary:
                 if magnitude is None:
                     magnitude = 0.1 * math.log(scaling.factor) + 1.0 if scaling.kind == "parts" else 1.0
         self.frequencies, self.magnitude = tuple(float(f) for f in frequencies), float(magnitude)
-        self.h = None
+        self.h = 0
         self.h = lioncub_rotary_create(self.head_dim, self.rotary_dim, self.frequencies, self.magnitude, self.interleaved)
         self.device = _torch.device("cuda", embed._device())
         self._index = self.device.index
 
-    def _heads(self, t, name, batch, places):
-        kind = embed._row_types.get(t.dtype)
-        if kind is None or t.get_device() != self._index:
-            raise ValueError(f"{name} must be a bfloat16 or float32 tensor on {self.device}")
-        if t.requires_grad and _torch.is_grad_enabled():
-            raise ValueError(f"{name} requires a gradient, but results are not part of torch's graph: "
-                             "call under torch.no_grad() or pass a detached tensor")
-        shape, stride = t.shape, t.stride()
-        if len(shape) == 3:
-            shape, stride = (1, *shape), (0, *stride)
-        if len(shape) != 4 or shape[0] != batch or shape[1] != places or shape[3] != self.head_dim:
-            raise ValueError(f"{name} must be ({batch}, {places}, heads, {self.head_dim}) (got {tuple(t.shape)})")
-        if stride[3] != 1 and t.numel():
-            raise ValueError(f"{name}: the columns of a head must be contiguous")
-        return _pack_heads(t.data_ptr(), stride[0], stride[1], stride[2], shape[2], kind)
-
     def _apply(self, q, k, positions, first_position, q_out, k_out, stream, inverse):
         if not self.h:
             raise LionCubError(ERR_STATE, "the rotary positions are closed")
-        if q.dim() not in (3, 4):
-            raise ValueError(f"q must be (batch, places, heads, {self.head_dim}) (got {tuple(q.shape)})")
-        batch, places = (1, q.size(0)) if q.dim() == 3 else (q.size(0), q.size(1))
-        at = kind = 0
-        if positions is not None:
-            kind = embed._index_types.get(positions.dtype)
-            if (kind is None or positions.get_device() != self._index or not positions.is_contiguous()
-                    or positions.numel() != batch * places):
-                raise ValueError(f"positions must be a contiguous int64 or int32 tensor of {batch} x {places} on {self.device}")
-            at = positions.data_ptr()
         if k is None and k_out is not None:
             raise ValueError("k_out without k")
         if q_out is None:
             q_out = _empty(q.shape, q.dtype, self.device, stream)
         if k is not None and k_out is None:
             k_out = _empty(k.shape, k.dtype, self.device, stream)
-        lioncub_rotary_apply(
-            self.h, _pack_sequences(at, batch, places, first_position, kind, 0), self._heads(q, "q", batch, places),
-            self._heads(q_out, "q_out", batch, places), None if k is None else self._heads(k, "k", batch, places),
-            None if k is None else self._heads(k_out, "k_out", batch, places), inverse, _raw(self._index, stream))
+        rc = _tensors.rotary_apply(self.h, self.head_dim, self._index, q, q_out, k, k_out, positions, first_position, inverse,
+                                   _raw(self._index, stream))
+        if rc:
+            _check(rc)
         return q_out if k is None else (q_out, k_out)
 
     def forward(self, q, k=None, *, positions=None, first_position=0, q_out=None, k_out=None, stream=None):
@@ -537,7 +470,7 @@ class Rotary:
     def close(self):
         if self.h:
             lioncub_rotary_destroy(self.h)
-            self.h = None
+            self.h = 0
 
     def __del__(self):
         try:

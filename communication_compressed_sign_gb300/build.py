@@ -2,18 +2,22 @@
 
 Each .cu file under csrc/ is compiled in parallel with nvcc and the objects
 are linked into one shared library with the C ABIs of include/lioncub.h,
-include/lioncub_embed.h and include/lioncub_block.h.  No PyTorch headers or types are involved: the
-library is plain CUDA C++ with the CUDA runtime linked statically.
+include/lioncub_embed.h and include/lioncub_block.h.  No PyTorch headers or types are
+involved: the library is plain CUDA C++ with the CUDA runtime linked statically.
+Beside it a small Python module, _tensors, is compiled against the installed
+torch: it reads the block operators' arguments from tensors and calls the library.
 
     python -m communication_compressed_sign_gb300.build [--verbose]
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +29,9 @@ OBJ_DIR = os.path.join(PKG, "_build")
 # a status bit instead of touching memory); used by the tests as a stand-in
 # for a memory checker.
 CHECKED_LIB = os.path.join(PKG, "liblioncub_checked.so")
+
+TENSORS = os.path.join(PKG, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))
+TENSORS_SOURCE = os.path.join(CSRC, "tensors.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC",
@@ -90,5 +97,36 @@ def build(force: bool = False, verbose: bool = False, bounds_check: bool = False
     return lib
 
 
+def _torch_dir() -> str | None:
+    """Where torch is installed (found without importing it), or None."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def build_tensors(force: bool = False) -> str:
+    """Compile the _tensors module; it needs torch's and Python's headers and a C++ compiler."""
+    torch = _torch_dir()
+    if torch is None:
+        raise RuntimeError("torch is not installed: the _tensors module cannot be built")
+    version = os.path.join(torch, "version.py")
+    inputs = [TENSORS_SOURCE, version, os.path.abspath(__file__),
+              *(os.path.join(INCLUDE, f) for f in ("lioncub.h", "lioncub_embed.h", "lioncub_block.h"))]
+    if not force and os.path.exists(TENSORS) and all(os.path.getmtime(f) <= os.path.getmtime(TENSORS) for f in inputs):
+        return TENSORS
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler: the _tensors module cannot be built")
+    tmp, libs = TENSORS + f".tmp{os.getpid()}", os.path.join(torch, "lib")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-I{INCLUDE}", f"-I{os.path.join(torch, 'include')}",
+           f"-I{os.path.join(torch, 'include', 'torch', 'csrc', 'api', 'include')}", f"-I{sysconfig.get_paths()['include']}",
+           TENSORS_SOURCE, "-o", tmp, f"-L{libs}", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {TENSORS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+    return TENSORS
+
+
 if __name__ == "__main__":
     print(build(force=True, verbose="--verbose" in sys.argv, bounds_check="--bounds-check" in sys.argv))
+    print(build_tensors(force=True))
