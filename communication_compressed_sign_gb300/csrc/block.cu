@@ -210,7 +210,7 @@ lc::PackedRows packed(const lioncub_packed* m, int64_t cols)
     for (int k = 5; k <= 8; ++k)
         if (m->group == 1 << k)
             log_group = k;
-    return lc::PackedRows{static_cast<uint8_t*>(m->codes), m->scales, m->stride, m->scale_stride, cols, log_group, m->format == LIONCUB_CODES_E4M3};
+    return lc::PackedRows{static_cast<uint8_t*>(m->codes), m->scales, m->stride, m->scale_stride, cols, log_group, m->format == LIONCUB_CODES_E4M3, 1.0f};
 }
 
 // Matrices whose rows follow one another are one long row to the kernels that

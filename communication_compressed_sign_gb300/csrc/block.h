@@ -25,6 +25,7 @@ struct PackedRows {
     int64_t cols;
     int32_t log_group;
     int32_t e4m3;  // else whole numbers
+    float one;     // 1 (see codes8)
 };
 
 struct NormArgs {

@@ -251,42 +251,43 @@ __device__ __forceinline__ uint32_t e4m3_pairs(float2 a, float2 b)
                  "mov.b32 %0, {lo, hi};\n\t}" : "=r"(w) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return w;
 }
-// 1.5 * 2^23 more is rounded to a whole number, whose two's complement is then the lowest bits
-__device__ __forceinline__ uint32_t int8_pairs(float2 a, float2 b, float2 inv)
+// 1.5 * 2^23 more is rounded to a whole number, whose two's complement is then the
+// lowest bits.  `one` is 1, which only the host knows: the products stay rounded.
+__device__ __forceinline__ uint32_t int8_pairs(float2 a, float2 b, float one)
 {
     const float2 magic = both(12582912.0f);
-    a = fma2(a, inv, magic);
-    b = fma2(b, inv, magic);
+    a = fma2(a, both(one), magic);
+    b = fma2(b, both(one), magic);
     return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                        __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], const GroupScale& s, bool e4m3)
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const GroupScale& s, const PackedRows& p)
 {
     uint2 w;
-    const float2 inv = both(s.inv);
-    if (e4m3) {
-        w.x = e4m3_pairs(mul2(pair_of(x, 0), inv), mul2(pair_of(x, 1), inv));
-        w.y = e4m3_pairs(mul2(pair_of(x, 2), inv), mul2(pair_of(x, 3), inv));
-    } else {
-        w.x = int8_pairs(pair_of(x, 0), pair_of(x, 1), inv);
-        w.y = int8_pairs(pair_of(x, 2), pair_of(x, 3), inv);
-    }
+    float2 y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        y[k] = mul2(pair_of(x, k), both(s.inv));
+    if (p.e4m3)
+        w = make_uint2(e4m3_pairs(y[0], y[1]), e4m3_pairs(y[2], y[3]));
+    else
+        w = make_uint2(int8_pairs(y[0], y[1], p.one), int8_pairs(y[2], y[3], p.one));
     if (s.bad)
         w = make_uint2(0, 0);
     return w;
 }
 
 // Two codes, in the lowest bytes of either number.
-__device__ __forceinline__ void codes2(float2 x, float inv, bool e4m3, uint32_t& a, uint32_t& b)
+__device__ __forceinline__ void codes2(float2 x, float inv, const PackedRows& p, uint32_t& a, uint32_t& b)
 {
-    if (e4m3) {
-        x = mul2(x, both(inv));
+    x = mul2(x, both(inv));
+    if (p.e4m3) {
         uint16_t w;
         asm volatile("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(w) : "f"(x.x), "f"(x.y));
         a = w;
         b = w >> 8;
     } else {
-        x = fma2(x, both(inv), both(12582912.0f));
+        x = fma2(x, both(p.one), both(12582912.0f));
         a = __float_as_uint(x.x);
         b = __float_as_uint(x.y);
     }
@@ -338,7 +339,7 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
     if constexpr (VEC) {
         const int log_lanes = p.log_group - 3;  // of a group
         const GroupScale s(lanes_max(largest, log_lanes), e4m3);
-        const uint2 w = codes8(x, s, e4m3);
+        const uint2 w = codes8(x, s, p);
         if (c.count) {
             *reinterpret_cast<uint2*>(codes) = w;
             if ((lane & ((1 << log_lanes) - 1)) == 0)
@@ -369,13 +370,13 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
                     const float inv = __shfl_sync(kAll, s.inv, g);
                     if constexpr (kDeep == 1) {
                         uint32_t code, unused;
-                        codes2(make_float2(x[g], 0.0f), inv, e4m3, code, unused);
+                        codes2(make_float2(x[g], 0.0f), inv, p, code, unused);
                         codes[32 * g] = static_cast<uint8_t>(code);
                     } else {
 #pragma unroll
                         for (int k = g * kDeep; k < (g + 1) * kDeep; k += 2) {
                             uint32_t a, b;
-                            codes2(make_float2(x[k], x[k + 1]), inv, e4m3, a, b);
+                            codes2(make_float2(x[k], x[k + 1]), inv, p, a, b);
                             codes[32 * k] = static_cast<uint8_t>(a);
                             codes[32 * k + 32] = static_cast<uint8_t>(b);
                         }
@@ -390,7 +391,7 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
                     for (int k = g * kDeep; k < (g + 1) * kDeep; ++k)
                         if (k < c.count) {
                             uint32_t code, unused;
-                            codes2(make_float2(x[k], 0.0f), inv, e4m3, code, unused);
+                            codes2(make_float2(x[k], 0.0f), inv, p, code, unused);
                             codes[32 * k] = none ? 0 : static_cast<uint8_t>(code);
                         }
                 }
@@ -411,16 +412,15 @@ __device__ __forceinline__ void pack_chunk_of_row(const PackedRows& p, const Col
                                                   const GroupScale& s)
 {
     uint8_t* codes = p.codes + row * p.stride + c.at;
-    const bool e4m3 = p.e4m3;
     if constexpr (VEC) {
         if (c.count)
-            *reinterpret_cast<uint2*>(codes) = codes8(x, s, e4m3);
+            *reinterpret_cast<uint2*>(codes) = codes8(x, s, p);
     } else {
         const bool plain = c.whole && !s.bad;
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
             uint32_t a, b;
-            codes2(make_float2(x[k], x[k + 1]), s.inv, e4m3, a, b);
+            codes2(make_float2(x[k], x[k + 1]), s.inv, p, a, b);
             if (plain) {
                 codes[32 * k] = static_cast<uint8_t>(a);
                 codes[32 * k + 32] = static_cast<uint8_t>(b);

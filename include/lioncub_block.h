@@ -25,7 +25,7 @@
  * may be shorter) that share an fp32 scale.  With a the largest magnitude of a
  * group and top = 127 (whole numbers) or 448 (e4m3):
  *   inv = RN(top / a),  scale = RN(a * RN(1 / top)),
- *   code = x * inv rounded once to a whole number, or RN(x * inv) rounded to e4m3 (to nearest, ties to even),
+ *   code = RN(x * inv) rounded to a whole number or to e4m3 (to nearest, ties to even),
  * and a code stands for RN(code * scale).  A group whose a is below 2^-100 is
  * held as zeros (scale 0); one that holds an infinity or a NaN has codes of 0
  * and a NaN as its scale, so that all of it stands for NaN.

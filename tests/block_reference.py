@@ -52,8 +52,8 @@ def pack(x, fmt, group):
         with np.errstate(divide="ignore", over="ignore"):
             inv = np.where(none, np.float32(0), top / np.where(none, np.float32(1), a)).astype(np.float32)
         scale = np.where(none, np.float32(0), a * (np.float32(1) / top)).astype(np.float32)
-        y = np.where(bad[:, None], np.float32(0), part).astype(np.float64) * inv[:, None].astype(np.float64)  # exact: 48 bits
-        c = np.rint(y).astype(np.int8).view(np.uint8) if fmt == "int8" else to_e4m3(y.astype(np.float32).astype(np.float64))
+        y = (np.where(bad[:, None], np.float32(0), part) * inv[:, None]).astype(np.float32)
+        c = np.rint(y).astype(np.int8).view(np.uint8) if fmt == "int8" else to_e4m3(y.astype(np.float64))
         codes[:, g * width:(g + 1) * width] = np.where(bad[:, None], 0, c)
         scales[:, g] = np.where(bad, np.float32(np.nan), scale)
     return codes, scales
