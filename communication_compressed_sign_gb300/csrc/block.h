@@ -58,7 +58,7 @@ struct NormGradArgs {
 
 struct WeightGradArgs {
     const float* partial;
-    int64_t rows;  // of partial
+    int32_t rows;  // of partial
     TypedRows base, grad;
     int32_t dim;
     int* status;

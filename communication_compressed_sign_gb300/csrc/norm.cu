@@ -66,16 +66,16 @@ __device__ __forceinline__ void pack_row(const PackedRows& p, const Columns<VEC>
 }
 
 // A row is that of `warps` warps, C neighbouring chunks each.
-template <typename XT, typename RT, int C, bool VEC>
+template <typename XT, typename RT, int C, bool VEC, bool WARP_ROWS>
 __global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__ NormArgs a)
 {
     __shared__ float sums[kMaxWarps];
     __shared__ uint32_t maxima[2][kMaxWarps];
     const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5;
-    const int warps = a.warps, warp = warps == 1 ? 0 : in_block;
-    const int64_t row = warps == 1 ? static_cast<int64_t>(blockIdx.x) * kRowsOfWarps + in_block : blockIdx.x;
+    const int warps = WARP_ROWS ? 1 : a.warps, warp = WARP_ROWS ? 0 : in_block;
+    const int64_t row = WARP_ROWS ? static_cast<int64_t>(blockIdx.x) * kRowsOfWarps + in_block : blockIdx.x;
     wait_for_launch_before();
-    if (row >= a.n)  // only where a row is one warp's, which meets no barrier
+    if (WARP_ROWS && row >= a.n)
         return;
     Columns<VEC> cols[C];
 #pragma unroll
@@ -209,7 +209,11 @@ template <typename XT, typename RT, bool VEC>
 cudaError_t launch_t(const NormArgs& a, int c, cudaStream_t s)
 {
     return with_chunks(c, [&](auto n) {
-        return launch_programmatic(k_norm<XT, RT, decltype(n)::value, VEC>, row_blocks(a.n, a.warps), row_threads(a.warps), 0, s, a);
+        constexpr int C = decltype(n)::value;
+        if constexpr (C <= 2)
+            if (a.warps == 1)
+                return launch_programmatic(k_norm<XT, RT, C, VEC, true>, row_blocks(a.n, 1), row_threads(1), 0, s, a);
+        return launch_programmatic(k_norm<XT, RT, C, VEC, false>, row_blocks(a.n, a.warps), row_threads(a.warps), 0, s, a);
     });
 }
 

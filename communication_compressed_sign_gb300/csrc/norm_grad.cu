@@ -365,27 +365,35 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
         }
 }
 
-// The blocks' rows, added in order: a warp adds every 32nd row of 32 columns,
-// and one of them the 32 sums.
-constexpr int kJoinWarps = 32;
+// The blocks' rows, added in a fixed order: a warp adds every 32nd row of 32
+// columns, all of its loads in flight at once, and then takes one of the columns.
+constexpr int kJoinWarps = 32, kJoinLoads = 5;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) k_weight_grad(const __grid_constant__ WeightGradArgs a)
 {
-    __shared__ float sums[kJoinWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
+    __shared__ float sums[kJoinWarps][33];  // a column of it touches every bank once
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x * 32;
     let_next_launch_start();
     wait_for_launch_before();
     float sum = 0.0f;
-    if (j < a.dim)
-#pragma unroll 5
-        for (int64_t i = warp; i < a.rows; i += kJoinWarps)
-            sum = __fadd_rn(sum, a.partial[i * a.dim + j]);
+    if (first + lane < a.dim)
+        for (int row = warp; row < a.rows; row += kJoinLoads * kJoinWarps) {
+            float v[kJoinLoads];
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u) {
+                const int i = row + u * kJoinWarps;
+                v[u] = i < a.rows ? a.partial[static_cast<int64_t>(i) * a.dim + first + lane] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u)
+                sum = __fadd_rn(sum, v[u]);
+        }
     sums[warp][lane] = sum;
     __syncthreads();
-    if (warp || j >= a.dim)
+    const int j = first + warp;
+    sum = warp_sum(sums[lane][warp]);
+    if (lane || j >= a.dim)
         return;
-    for (int k = 1; k < kJoinWarps; ++k)
-        sum = __fadd_rn(sum, sums[k][lane]);
     if (a.base.data)
         sum = __fadd_rn(sum, a.base.type == LIONCUB_ROWS_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.base.data)[j])
                                                                : static_cast<const float*>(a.base.data)[j]);
