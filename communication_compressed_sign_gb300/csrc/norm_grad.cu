@@ -16,8 +16,12 @@ namespace lc {
 namespace {
 
 constexpr int kBlockWarps = 16;
-constexpr int kMaxSlots = 8;              // rows of a team in flight
-constexpr int kRingBytes = 208 * 1024;    // at most
+// Rows of a team in flight: as many as fit kRingWanted, two where that is one and
+// kRingBytes has room.  More only let reads run further ahead of the writes: 8192
+// fp32 rows of 768 took 14.9 us with two, 15.8 with three, 17.1 with five; 16384
+// rows of 2048 from 8 bits 51.0, 51.8 and 53.2.
+constexpr int kMaxSlots = 8;
+constexpr int kRingWanted = 72 * 1024, kRingBytes = 208 * 1024;
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls
 
 // Where h comes from; scalar reads go by the type that the launch gives.
@@ -469,8 +473,9 @@ cudaError_t launch_norm_grad(NormGradArgs a, int blocks, bool vec, cudaStream_t 
     a.at_saved = room(size_of(a.dout));
     a.at_residual = a.at_saved + room(a.packed.codes ? 1 : size_of(a.saved));
     a.slot_bytes = a.at_residual + (a.residual_grad.data ? room(size_of(a.residual_grad)) : 0);
-    const int slots = kRingBytes / (a.slot_bytes * a.teams);
-    a.slots = slots > kMaxSlots ? kMaxSlots : slots;
+    const int all = a.slot_bytes * a.teams, most = kRingBytes / all;
+    a.slots = kRingWanted / all < 2 ? 2 : kRingWanted / all;
+    a.slots = a.slots > most ? most : a.slots > kMaxSlots ? kMaxSlots : a.slots;
     static_assert(3 * (LIONCUB_NORM_MAX_DIM * 4 + 30) <= kRingBytes, "a row of every width has a slot");
     a.per_column = 1.0f / static_cast<float>(a.dim);
     if (!vec)
