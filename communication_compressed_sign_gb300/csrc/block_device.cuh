@@ -38,7 +38,9 @@ struct Columns {
 // --- fp32 pairs ---------------------------------------------------------------------------
 //
 // These kernels move so few bytes an element that instructions bound them before
-// memory does, so arithmetic is done two elements an instruction.  The assembler
+// memory does, so arithmetic is done two elements an instruction (with that, maxima
+// on bf16 pairs and approximate exponentials the gated activation of 16384 x 8192,
+// both ways, went from 503 to 369 us).  The assembler
 // fuses a paired product with a paired sum that takes it, whatever their rounding
 // modifiers say: what must be rounded between is written as an fma, or its product
 // goes elsewhere.
@@ -456,7 +458,7 @@ struct CodeChunk<true> {
 
 template <>
 struct CodeChunk<false> {
-    uint8_t code[8];
+    uint32_t code[8];
     float scale;  // of value lane % 8
     __device__ __forceinline__ void load(const PackedRows& p, const Columns<false>& c, int64_t row, int lane)
     {

@@ -3,7 +3,13 @@
 //   h = x + residual,  out = h * rstd * weight,  rstd = 1 / sqrt(mean(h^2) + eps).
 //
 // Memory-bound.  A row stays in the registers of one or more warps from its only
-// reading to its writing; one sum over the row stands between.
+// reading to its writing; one sum over the row stands between (a cluster or a
+// second reading is not needed: 16384 columns are 16 warps of 32 elements a lane).
+// Measured: 65536 x 2048 bf16 with a residual into e4m3 134.8 us (7.0 TB/s, above a
+// measured copy's rate), 8192 x 768 onto an fp32 residual 12.8 us (5.9 TB/s), 4907
+// x 771 fp32 11.1 us (5.5 TB/s, scalar moves), 8 rows 1.5 us.  Rows of 3905 bf16
+// with one scale each, by scalar moves, take 205 us for 41152 (2.4 TB/s): about 30
+// instructions an element, half of them a warp's overhead, and two barriers a row.
 #include <climits>
 
 #include "block_device.cuh"

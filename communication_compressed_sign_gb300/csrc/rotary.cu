@@ -4,7 +4,14 @@
 //
 // Memory-bound.  The angle is the same for all heads of a place, so a block takes
 // a few places, works out their cosines and sines once into shared memory, and
-// then walks over the places' heads in the order of memory.
+// then walks over the places' heads in the order of memory.  (A thread with the
+// same columns of several heads keeps its angles in registers, but then all blocks
+// read the same few heads of every place at a time: 192 to 275 us by how many
+// heads, where this takes 196 whatever the layout.)
+// Measured: 65536 places, 40 heads of 128 bf16 196 us (6.8 TB/s); 8192 places, 24
+// heads of 64 out of a fused product 11.6 us (4.3 TB/s; one wave); 8 places 2.3 us.
+// Heads of 80 with 40 interleaved columns, 4 elements at a time, 9.6 us for 8192 x
+// 10 (2.7 TB/s); with 20, 2 at a time, 71 us for 45708 x 12 (2.5 TB/s).
 // Angles are turns in 64-bit fixed point: position * turns-a-position wraps
 // around by itself, which is the exact reduction that far positions need (in
 // fp32 the angle of position 100000 would be off by 0.004).

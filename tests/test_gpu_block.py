@@ -121,6 +121,25 @@ def test_codes_are_equal_to_the_bit(ops, rows, cols, code, group):
         _untouched(whole, rows, cols, pad, shift)
 
 
+@pytest.mark.parametrize("cols", [256, 259])
+def test_products_are_rounded_before_codes_are(ops, cols):
+    """Numbers whose exact product with inv and its fp32 rounding lie on two sides of a border between whole numbers."""
+    rng = np.random.default_rng(1)
+    a = (1 + rng.random(200000)).astype(np.float32)
+    x = (a * (rng.integers(0, 126, a.size) + 0.5) / 127).astype(np.float32)
+    inv = (np.float32(127) / a).astype(np.float32)
+    rounded, exact = np.rint(x * inv), np.rint(x.astype(np.float64) * inv.astype(np.float64))
+    pick = np.flatnonzero(rounded != exact)[:500]
+    assert pick.size >= 100
+    rows = np.zeros((pick.size, cols), np.float32)
+    rows[:, 5] = a[pick]
+    rows[:, 6:40] = x[pick][:, None]
+    codes, scales = ref.pack(rows, "int8", 128)
+    p = ops.pack8(torch.from_numpy(rows).cuda())
+    assert np.array_equal(_bits(p.codes).reshape(rows.shape), codes) and np.array_equal(p.scales.cpu().numpy(), scales)
+    assert (codes[:, 6].view(np.int8) == rounded[pick]).all()
+
+
 @pytest.mark.parametrize("code", list(CODES))
 @pytest.mark.parametrize("group", [64, 0])
 @pytest.mark.parametrize("cols", [256, 77])
