@@ -81,6 +81,22 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// The sum of what up to 16 warps left in shared memory, in every lane.
+__device__ __forceinline__ float sum_of_warps(const float* part, int warps, int lane)
+{
+    if (warps <= 4) {  // fewer instructions and less latency than by shuffles
+        float v = 0.0f;
+        for (int k = 0; k < warps; ++k)
+            v = __fadd_rn(v, part[k]);
+        return v;
+    }
+    float v = (lane & 15) < warps ? part[lane & 15] : 0.0f;
+#pragma unroll
+    for (int by = 8; by; by >>= 1)
+        v = __fadd_rn(v, __shfl_xor_sync(kAll, v, by));
+    return v;
+}
+
 // The largest magnitude of 8 elements, as the bits of a float: infinities come after all
 // finite ones and NaN after those, so a maximum of these numbers keeps them.
 __device__ __forceinline__ uint32_t largest_of(const float (&x)[8])

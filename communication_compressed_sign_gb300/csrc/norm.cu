@@ -28,9 +28,7 @@ __device__ __forceinline__ float row_sum(float v, float* shared, int warps, int 
         if (lane == 0)
             shared[warp] = v;
         __syncthreads();
-        v = 0.0f;
-        for (int k = 0; k < warps; ++k)
-            v = __fadd_rn(v, shared[k]);
+        v = sum_of_warps(shared, warps, lane);
     }
     return v;
 }
@@ -42,8 +40,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* shared, int wa
         if (lane == 0)
             shared[warp] = v;
         __syncthreads();
-        for (int k = 0; k < warps; ++k)
-            v = max(v, shared[k]);
+        v = __reduce_max_sync(kAll, lane < warps ? shared[lane] : 0);
     }
     return v;
 }
