@@ -6,9 +6,9 @@
 // reading to its writing; one sum over the row stands between (a cluster or a
 // second reading is not needed: 16384 columns are 16 warps of 32 elements a lane).
 // Measured: 65536 x 2048 bf16 with a residual into e4m3 134.8 us (7.0 TB/s, above a
-// measured copy's rate), 8192 x 768 onto an fp32 residual 12.8 us (5.9 TB/s), 4907
+// measured copy's rate), 8192 x 768 onto an fp32 residual 12.7 us (5.9 TB/s), 4907
 // x 771 fp32 11.1 us (5.5 TB/s, scalar moves), 8 rows 1.5 us.  Rows of 3905 bf16
-// with one scale each, by scalar moves, take 205 us for 41152 (2.4 TB/s): about 30
+// with one scale each, by scalar moves, take 161 us for 41152 (3.0 TB/s): about 30
 // instructions an element, half of them a warp's overhead, and two barriers a row.
 #include <climits>
 
@@ -68,9 +68,11 @@ __device__ __forceinline__ void pack_row(const PackedRows& p, const Columns<VEC>
         p.scales[row * p.scale_stride] = s.scale;
 }
 
-// A row is that of `warps` warps, C neighbouring chunks each.
+// A row is that of `warps` warps, C neighbouring chunks each.  Registers are capped
+// for three blocks of 16 warps an SM: 41152 rows of 3905 bf16, whose scalar moves are
+// 64 bytes a warp, took 202 us with the 64 of before, 161 so.
 template <typename XT, typename RT, int C, bool VEC, bool WARP_ROWS>
-__global__ void __launch_bounds__(kMaxWarps * 32) k_norm(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(kMaxWarps * 32, C <= 2 ? 3 : 2) k_norm(const __grid_constant__ NormArgs a)
 {
     __shared__ float sums[kMaxWarps];
     __shared__ uint32_t maxima[2][kMaxWarps];
