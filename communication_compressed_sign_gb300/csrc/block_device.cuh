@@ -44,25 +44,9 @@ struct Columns {
 // fuses a paired product with a paired sum that takes it, whatever their rounding
 // modifiers say: what must be rounded between is written as an fma, or its product
 // goes elsewhere.
-#define LC_PAIR_OP2(name, op)                                                                                            \
-    __device__ __forceinline__ float2 name(float2 x, float2 y)                                                           \
-    {                                                                                                                    \
-        float2 d;                                                                                                        \
-        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t" op " a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}" \
-            : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));                                            \
-        return d;                                                                                                        \
-    }
-LC_PAIR_OP2(add2, "add.rn.f32x2")
-LC_PAIR_OP2(mul2, "mul.rn.f32x2")
-#undef LC_PAIR_OP2
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
-    return d;
-}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) { return __fadd2_rn(x, y); }
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) { return __fmul2_rn(x, y); }
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) { return __ffma2_rn(x, y, z); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 pair_of(const float (&x)[8], int k) { return make_float2(x[2 * k], x[2 * k + 1]); }
 __device__ __forceinline__ void set_pair(float (&x)[8], int k, float2 v)

@@ -320,7 +320,9 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
             parity ^= 1;
         }
         if (warps > 1) {
-            sum = sum_of_warps(&sums[turn][team * warps], warps, lane);
+            sum = 0.0f;
+            for (int k = 0; k < warps; ++k)
+                sum = __fadd_rn(sum, sums[turn][team * warps + k]);
             turn ^= 1;
         }
         const float mean = __fmul_rn(sum, a.per_column);
