@@ -91,11 +91,11 @@ struct RotaryArgs {
     float cos_factor, sin_factor;
 };
 
-// Blocks that leave a row of partial sums each: one for each multiprocessor.
 // vec: the matrices allow 16-byte moves.
 cudaError_t launch_norm(NormArgs a, bool vec, cudaStream_t s);
-cudaError_t launch_norm_grad(NormGradArgs a, int blocks, bool vec, cudaStream_t s);
+// Its blocks, one for each multiprocessor at most, leave a row of partial sums each.
 int norm_grad_blocks(int64_t n, int dim, int multiprocessors);
+cudaError_t launch_norm_grad(NormGradArgs a, int blocks, bool vec, cudaStream_t s);
 cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t s);
 // Codes with one scale a row (forward norms without the norm).
 cudaError_t launch_pack_rows(const TypedRows& x, const PackedRows& out, int64_t rows, int dim, bool vec, cudaStream_t s);

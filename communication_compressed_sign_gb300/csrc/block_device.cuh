@@ -40,10 +40,9 @@ struct Columns {
 // These kernels move so few bytes an element that instructions bound them before
 // memory does, so arithmetic is done two elements an instruction (with that, maxima
 // on bf16 pairs and approximate exponentials the gated activation of 16384 x 8192,
-// both ways, went from 503 to 369 us).  The assembler
-// fuses a paired product with a paired sum that takes it, whatever their rounding
-// modifiers say: what must be rounded between is written as an fma, or its product
-// goes elsewhere.
+// both ways, went from 503 to 369 us).  The assembler fuses a paired product with
+// a paired sum that takes it, whatever their rounding says: where the product must
+// be rounded first, the sum is an fma whose other factor only the host knows.
 __device__ __forceinline__ float2 add2(float2 x, float2 y) { return __fadd2_rn(x, y); }
 __device__ __forceinline__ float2 mul2(float2 x, float2 y) { return __fmul2_rn(x, y); }
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) { return __ffma2_rn(x, y, z); }

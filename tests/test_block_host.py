@@ -124,6 +124,46 @@ def test_activation_refusals(bl):
     assert backward(r(1), r(2, 0), None, None, None, r(3)) == arg and backward(r(1), r(2), None, None, None, r(3, 0)) == arg
 
 
+def test_arguments_from_tensors_are_refused(bl):
+    """The module that reads arguments from tensors, on tensors that are not the GPU's: nothing reaches the library."""
+    torch = pytest.importorskip("torch")
+    from communication_compressed_sign_gb300 import Packed, build
+    build.build_tensors()
+    bl._use_torch()
+    t, x = bl._tensors, torch.zeros(4, 64)
+    packed = Packed(torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 1), 128)
+    calls = {
+        "pack8": (0, x, packed, 0), "unpack8": (0, packed.codes, packed, x, 0), "activation_forward": (0, 0, x, None, x, None, None, 0),
+        "activation_backward": (0, 0, x, x, None, x, None, None, 0),
+        "rms_norm_forward": (0, 64, 0, x, None, None, None, None, None, x, 0),
+        "rms_norm_backward": (0, 64, 0, x, packed, torch.zeros(4), None, None, x, None, None, None, 0),
+        "rotary_apply": (0, 64, 0, x.view(1, 4, 1, 64), x.view(1, 4, 1, 64), None, None, None, 0, 0, 0),
+    }
+    for name, args in calls.items():
+        f = getattr(t, name)
+        with pytest.raises(ValueError, match="cuda:0|CUDA device"):
+            f(*args)
+        with pytest.raises(TypeError, match="arguments"):
+            f(*args[:-1])
+        with pytest.raises(TypeError, match="arguments"):
+            f(*args, 0)
+        first = next(i for i, a in enumerate(args) if torch.is_tensor(a))
+        for bad in (None, 5, "x", [x]):  # what is not a tensor
+            with pytest.raises(ValueError, match="must be a tensor"):
+                f(*args[:first], bad, *args[first + 1:])
+        with pytest.raises((ValueError, RuntimeError)):
+            f(*args[:first], torch.zeros(4, 64).to_sparse(), *args[first + 1:])
+    for dim in (63, 0):
+        with pytest.raises(ValueError, match="columns"):
+            t.rms_norm_forward(0, dim, *calls["rms_norm_forward"][2:])
+    with pytest.raises(TypeError):
+        t.pack8("0", x, packed, 0)  # no device number
+    with pytest.raises(OverflowError):
+        t.pack8(1 << 70, x, packed, 0)
+    with pytest.raises(ValueError, match="kind"):
+        bl._kind("relu")
+
+
 def test_frequencies(bl):
     f = bl.lioncub_rotary_frequencies(64, 10000.0)
     assert np.allclose(f, 10000.0 ** (-np.arange(32) / 32), rtol=1e-14)
