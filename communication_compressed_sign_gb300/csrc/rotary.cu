@@ -10,9 +10,9 @@
 // heads, where this takes 196 whatever the layout.  The first items loaded before
 // the angles are worked out: 202, and nothing gained by small calls.)
 // Measured: 65536 places, 40 heads of 128 bf16 196 us (6.8 TB/s); 8192 places, 24
-// heads of 64 out of a fused product 11.6 us (4.3 TB/s; one wave); 8 places 2.3 us.
-// Heads of 80 with 40 interleaved columns, 4 elements at a time, 8.5 us for 8192 x
-// 10 (3.0 TB/s); with 20, 2 at a time, 68 us for 45708 x 12 (2.6 TB/s).
+// heads of 64 out of a fused product 11.3 us (4.5 TB/s; two waves); 8 places 2.4 us.
+// Heads of 80 with 40 interleaved columns, 4 elements at a time, 8.4 us for 8192 x
+// 10 (3.0 TB/s); with 20, 2 at a time, 66 us for 45708 x 12 (2.6 TB/s).
 // Angles are turns in 64-bit fixed point: position * turns-a-position wraps
 // around by itself, which is the exact reduction that far positions need (in
 // fp32 the angle of position 100000 would be off by 0.004).
@@ -24,11 +24,12 @@
 namespace lc {
 namespace {
 
-constexpr int kBlock = 256;
-// Of a block.  8192 places of 24 x 64 and 65536 of 40 x 128, by 2, 4, 6, 8 and 14: 19.8,
-// 14.2, 13.0, 11.6 and 14.5 us (fewer repeat the start, more leave SMs idle); 215, 196,
-// 195, 196 and 195.
-constexpr int kMaxPlaces = 8;
+// Threads and places of a block.  8192 places of 24 x 64 and 65536 of 40 x 128: blocks of
+// 256 with 2, 4, 6, 8 and 14 places 19.8, 14.2, 13.0, 11.6 and 14.5 us (fewer repeat the
+// start, more leave SMs idle) and 215, 196, 195, 196 and 195; of 128 with 4 11.3 and 196,
+// with 8 14.5 and 196.
+constexpr int kBlock = 128;
+constexpr int kMaxPlaces = 4;
 constexpr int kItems = 8;      // of a thread, about, where there are many places
 
 // cos and sin of a position's angle.  The nearest quarter turn is taken off in
@@ -174,7 +175,7 @@ struct Divisor {
 Divisor divisor(uint32_t d, uint64_t largest) { return {d, d > 1 && largest * d < (1ull << 32) ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0}; }
 
 template <typename T, bool INTERLEAVED, int MOVE>
-__global__ void __launch_bounds__(kBlock, 4) k_rotary(const __grid_constant__ RotaryArgs a, const int turning, const Divisor items,
+__global__ void __launch_bounds__(kBlock, 8) k_rotary(const __grid_constant__ RotaryArgs a, const int turning, const Divisor items,
                                                    const Divisor heads0, const Divisor heads1, const int block_places)
 {
     constexpr int kUnits = 2;  // items of a thread, whose loads are in flight together
