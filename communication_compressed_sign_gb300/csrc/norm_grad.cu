@@ -6,22 +6,23 @@
 // Memory-bound.  A team of warps takes a row at a time, with one sum over the row
 // between reading and writing it.  Teams walk over rows (persistent blocks, one
 // for each multiprocessor), so that a column's share of the weight's gradient
-// stays in a register; a thread of the team has the next rows brought into a
-// ring in shared memory by bulk copies meanwhile.  A block adds its teams'
+// stays in a register; three threads of the team have the next rows brought into
+// a ring in shared memory by bulk copies meanwhile, one matrix each.  A block adds its teams'
 // columns in order and leaves one row of sums, and a second launch adds those of
 // all blocks in order.
 //
-// Measured: 65536 x 2048 bf16 from int8, with the normed rows again, 182.4 us (6.6
+// Measured: 65536 x 2048 bf16 from int8, with the normed rows again, 181.8 us (6.7
 // TB/s, 98 % of a measured copy); 8192 x 768 onto fp32 18.5 us (4.8 TB/s; some 6
 // of them are the two launches' beginnings and ends, 2.6 the second launch); 4907
-// x 771 bf16 16.7 us (1.8 TB/s, scalar reads of the ring).  The first with its rows
+// x 771 bf16 13.8 us (2.2 TB/s, scalar reads of the ring; 16.7 with one thread
+// starting the copies of all matrices).  The first with its rows
 // loaded ahead into registers, 16 warps an SM: 241 us (too few loads in flight);
 // with each thread's elements copied ahead by itself (cp.async): 246 us (as many
 // instructions for the load-store unit as bytes allow).
 //
 // A row of any alignment comes by bulk copies: of the 16-byte pieces that it
 // touches, as far as they lie within the matrix; the ends of the first and the last
-// row that do not are copied by the thread that starts the copies.
+// row that do not are copied by the thread that starts the copy.
 #include "block_device.cuh"
 
 namespace lc {
@@ -81,7 +82,10 @@ struct Stream {
 
 // The slot of a row that starts `shift` bytes behind a boundary has it `shift`
 // bytes behind its own start.
-__device__ __forceinline__ int shift_of(const Stream& m, int64_t row) { return static_cast<int>(reinterpret_cast<uintptr_t>(m.base + row * m.step) & 15); }
+__device__ __forceinline__ uint32_t shift_of(const Stream& m, int64_t row)
+{
+    return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(m.base)) + static_cast<uint32_t>(row) * static_cast<uint32_t>(m.step)) & 15;
+}
 
 // Bytes that the copies of a row bring: whole 16-byte pieces, but none that lies
 // partly before the matrix's first or behind its last element.
@@ -100,51 +104,33 @@ struct Window {
     __device__ __forceinline__ uint32_t bytes() const { return static_cast<uint32_t>(to - from); }
 };
 
-// One thread: starts the copies of row i of every stream into a slot.
-template <int N, bool VEC>
-__device__ __forceinline__ void start_row(const Stream (&streams)[N], int64_t i, int64_t n, char* slot, uint32_t barrier)
+// One thread for each stream: starts the copy of its row i into a slot.
+template <bool VEC>
+__device__ __forceinline__ void start_row(const Stream& m, int64_t i, int64_t n, char* slot, uint32_t barrier)
 {
-    uint32_t bytes = 0;
-    // what was read and written in the slot by ordinary accesses comes before the copies
+    const char* from = m.base + i * m.step;
+    uint32_t bytes = m.bytes;
+    char* to = slot + m.at;
+    // what was read and written in the slot by ordinary accesses comes before the copy
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const Stream& m = streams[k];
-        if constexpr (VEC) {
-            bytes += m.bytes;
-        } else if (m.bytes) {
-            const Window w(m, i, n);
-            bytes += w.bytes();
-            // what lies outside, in the first and the last rows
-            char* to = slot + m.at + shift_of(m, i);
-            const char* end = w.row + m.bytes;
-            for (const char* p = w.row; p < w.from && p < end; ++p)
-                to[p - w.row] = *p;
-            for (const char* p = w.to > w.row ? w.to : w.row; p < end; ++p)
-                to[p - w.row] = *p;
-        }
+    if constexpr (!VEC) {
+        const Window w(m, i, n);
+        to += shift_of(m, i);
+        // what lies outside, in the first and the last rows
+        const char* end = w.row + m.bytes;
+        for (const char* p = w.row; p < w.from && p < end; ++p)
+            to[p - w.row] = *p;
+        for (const char* p = w.to > w.row ? w.to : w.row; p < end; ++p)
+            to[p - w.row] = *p;
+        to += w.from - w.row;
+        from = w.from;
+        bytes = w.bytes();
     }
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(barrier), "r"(bytes) : "memory");
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const Stream& m = streams[k];
-        if (!m.bytes)
-            continue;
-        const char* from = m.base + i * m.step;
-        uint32_t size = m.bytes;
-        char* to = slot + m.at;
-        if constexpr (!VEC) {
-            const Window w(m, i, n);
-            to += shift_of(m, i) + (w.from - w.row);
-            from = w.from;
-            size = w.bytes();
-            if (!size)
-                continue;
-        }
+    if (bytes)
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(shared_address(to)),
-                     "l"(from), "r"(size), "r"(barrier)
+                     "l"(from), "r"(bytes), "r"(barrier)
                      : "memory");
-    }
 }
 
 // A lane's elements of a chunk, from a row in shared memory.
@@ -216,20 +202,22 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
          a.at_residual}};
     char* ring = shared + static_cast<int64_t>(team) * a.slots * a.slot_bytes;
     const uint32_t full = shared_address(barriers + team * kMaxSlots);
-    const bool leads = warp == 0 && lane == 0;
-    if (leads) {
+    // the first lanes of a team start the copies, one stream each
+    const Stream mine = lane == 0 ? streams[0] : lane == 1 ? streams[1] : streams[2];
+    const bool starts = warp == 0 && lane < 3 && mine.bytes;
+    if (warp == 0 && lane == 0) {
         gave_up[team] = 0;
         for (int k = 0; k < a.slots; ++k)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(full + 8 * k) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(full + 8 * k), "r"(a.residual_grad.data ? 3 : 2) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     team_barrier(team, warps);
     let_next_launch_start();
     wait_for_launch_before();
     uint32_t started = 0, last_parity = 0;  // of the slots, a bit each
-    if (leads)
+    if (starts)
         for (int k = 0; k < a.slots && row + k * step < a.n; ++k) {
-            start_row<3, VEC>(streams, row + k * step, a.n, ring + k * a.slot_bytes, full + 8 * k);
+            start_row<VEC>(mine, row + k * step, a.n, ring + k * a.slot_bytes, full + 8 * k);
             started |= 1u << k;
         }
 
@@ -311,8 +299,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
         // starts no row and has no long wait any more.
         failed = gave_up[team];
         polls = failed ? 1 : 0;
-        if (leads && !failed && row + a.slots * step < a.n) {  // the slot has been read
-            start_row<3, VEC>(streams, row + a.slots * step, a.n, ring + slot * a.slot_bytes, full + 8 * slot);
+        if (starts && !failed && row + a.slots * step < a.n) {  // the slot has been read
+            start_row<VEC>(mine, row + a.slots * step, a.n, ring + slot * a.slot_bytes, full + 8 * slot);
             last_parity ^= 1u << slot;
         }
         if (++slot == a.slots) {
