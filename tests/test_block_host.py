@@ -164,6 +164,30 @@ def test_arguments_from_tensors_are_refused(bl):
         bl._kind("relu")
 
 
+def test_steps_between_rows(bl):
+    """The distance between a view's rows, against what torch's own view of it as a matrix has."""
+    torch = pytest.importorskip("torch")
+    a, b = torch.zeros(4, 5, 30), torch.zeros(3, 4, 2, 6)
+    views = (a[..., :7], a[:, 1:3, :7], a[:, :1, :7], a[:1, :, :7], a[:, ::2, :7], a.transpose(0, 1)[..., :7], a[..., ::2], a[:, :, None, :7],
+             a[:1, :1, :7], a[0, :, :9], a[0].t(), a[..., :1], a[:, :, 3:4], a[:, :1].expand(4, 5, 30), b[..., :4], b[:, :, :1, :4],
+             b.permute(1, 0, 2, 3)[..., :4], b[:, :, 0], b[:, 1, :, :4], a[0, 0, ::3], a[0, 1:2, :9])
+    for t in views:
+        cols = t.size(-1)
+        n = t.numel() // cols
+        if t.is_contiguous():
+            continue
+        try:
+            m = t.view(-1, cols)
+            want = "columns" if cols > 1 and m.stride(1) != 1 else m.stride(0) if n > 1 else cols
+        except RuntimeError:
+            want = "fixed distance"
+        if isinstance(want, str):
+            with pytest.raises(ValueError, match="columns|fixed distance"):
+                bl.embed._step(t, "x", n, cols)
+        else:
+            assert bl.embed._step(t, "x", n, cols) == want, (t.shape, t.stride())
+
+
 def test_frequencies(bl):
     f = bl.lioncub_rotary_frequencies(64, 10000.0)
     assert np.allclose(f, 10000.0 ** (-np.arange(32) / 32), rtol=1e-14)
