@@ -6,9 +6,9 @@ its gradient, :class:`Packed` a matrix in 8 bits with scales (:func:`pack8`,
 :func:`unpack8`), :func:`activation` and :func:`activation_backward` a SiLU or
 GELU, gated or not, and :class:`Rotary` rotary positions.  A norm and an
 activation can leave what their backward pass needs in 8 bits.  As in
-:mod:`.embed`, the functions named ``lioncub_*`` keep the C names, results are
-not part of torch's autograd graph and gradients come from the backward
-functions, called by hand.
+:mod:`.embed`, results are not part of torch's autograd graph and gradients come
+from the backward functions, called by hand; :func:`load` gives the library with
+the C functions declared.
 """
 from __future__ import annotations
 
@@ -94,26 +94,10 @@ def _check(rc: int) -> None:
         raise LionCubError(rc, L.lioncub_block_last_error().decode() or L.lioncub_strerror(rc).decode())
 
 
-# Matrices are ctypes.byref() of a struct, vectors addresses, None for NULL.
-
 def lioncub_rms_norm_create(dim: int, eps: float) -> int:
     h = ctypes.c_void_p()
     _check(load().lioncub_rms_norm_create(ctypes.byref(h), dim, eps))
     return h.value
-
-
-def lioncub_rms_norm_forward(h, n, x, residual, weight, summed, saved, rstd, out, packed_out, stream=0) -> None:
-    rc = (_lib or load()).lioncub_rms_norm_forward(h, n, x, residual, weight, summed, saved, rstd, out, packed_out, stream or None)
-    if rc:
-        _check(rc)
-
-
-def lioncub_rms_norm_backward(h, n, dout, saved, packed_saved, rstd, weight, residual_grad, dx, weight_base, weight_grad, again,
-                              stream=0) -> None:
-    rc = (_lib or load()).lioncub_rms_norm_backward(h, n, dout, saved, packed_saved, rstd, weight, residual_grad, dx, weight_base,
-                                                    weight_grad, again, stream or None)
-    if rc:
-        _check(rc)
 
 
 def lioncub_rms_norm_status(h: int, dst_ptr: int, stream: int = 0) -> None:
@@ -125,33 +109,8 @@ def lioncub_rms_norm_destroy(h: int) -> None:
         load().lioncub_rms_norm_destroy(h)
 
 
-def lioncub_pack8(rows: int, cols: int, x, out, stream: int = 0) -> None:
-    rc = (_lib or load()).lioncub_pack8(rows, cols, x, out, stream or None)
-    if rc:
-        _check(rc)
-
-
-def lioncub_unpack8(rows: int, cols: int, x, out, stream: int = 0) -> None:
-    rc = (_lib or load()).lioncub_unpack8(rows, cols, x, out, stream or None)
-    if rc:
-        _check(rc)
-
-
-def lioncub_activation_forward(rows, cols, kind, x, up, out, saved, saved_up, stream=0) -> None:
-    rc = (_lib or load()).lioncub_activation_forward(rows, cols, kind, x, up, out, saved, saved_up, stream or None)
-    if rc:
-        _check(rc)
-
-
-def lioncub_activation_backward(rows, cols, kind, dout, x, up, packed_x, packed_up, dx, dup, again, stream=0) -> None:
-    rc = (_lib or load()).lioncub_activation_backward(rows, cols, kind, dout, x, up, packed_x, packed_up, dx, dup, again,
-                                                      stream or None)
-    if rc:
-        _check(rc)
-
-
 def lioncub_rotary_frequencies(rotary_dim: int, base: float, scaling=None) -> list[float]:
-    out = (ctypes.c_double * max(1, rotary_dim // 2))()
+    out = (ctypes.c_double * max(1, min(rotary_dim, ROTARY_MAX_DIM) // 2))()
     _check(load().lioncub_rotary_frequencies(rotary_dim, base, None if scaling is None else ctypes.byref(scaling), out))
     return list(out)
 
@@ -161,12 +120,6 @@ def lioncub_rotary_create(head_dim: int, rotary_dim: int, frequencies, magnitude
     table = (ctypes.c_double * len(frequencies))(*frequencies)
     _check(load().lioncub_rotary_create(ctypes.byref(h), head_dim, rotary_dim, table, magnitude, int(interleaved)))
     return h.value
-
-
-def lioncub_rotary_apply(h, places, q, q_out, k, k_out, inverse, stream=0) -> None:
-    rc = (_lib or load()).lioncub_rotary_apply(h, places, q, q_out, k, k_out, inverse, stream or None)
-    if rc:
-        _check(rc)
 
 
 def lioncub_rotary_destroy(h: int) -> None:

@@ -495,7 +495,6 @@ int lioncub_rms_norm_forward(lioncub_rms_norm_t h, int64_t n, const lioncub_rows
     a.n = n;
     a.dim = static_cast<int32_t>(h->dim);
     a.eps = h->eps;
-    a.status = h->status;
     const bool vec = o.vec && h->dim % 8 == 0;
     return finish_launch(launch(h, "rms_norm", [&] { return lc::launch_norm(a, vec, stream); }), "norm launch");
 }
@@ -565,7 +564,6 @@ int lioncub_rms_norm_backward(lioncub_rms_norm_t h, int64_t n, const lioncub_row
     w.base = typed(weight_base);
     w.grad = typed(weight_grad);
     w.dim = a.dim;
-    w.status = h->status;
     return finish_launch(launch(h, "rms_norm_weight_grad", [&] { return lc::launch_weight_grad(w, stream); }), "weight gradient launch");
 }
 

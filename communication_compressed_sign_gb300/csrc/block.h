@@ -37,7 +37,6 @@ struct NormArgs {
     int32_t warps;  // of a row; set by launch_norm, per_column too
     float eps;
     float per_column;  // 1 / dim
-    int* status;
 };
 
 struct NormGradArgs {
@@ -61,7 +60,6 @@ struct WeightGradArgs {
     int32_t rows;  // of partial
     TypedRows base, grad;
     int32_t dim;
-    int* status;
 };
 
 struct ActivationArgs {
