@@ -6,10 +6,10 @@
 // Memory-bound: each element is read and written once; groups of columns that
 // share a scale lie inside a warp's chunk of 256 columns, so their maxima need
 // shuffles only.  Dense matrices whose rows are whole groups are one long row.
-// Measured: SiLU, gated, 16384 x 8192 bf16, saved in int8, forward and backward 370
-// us (6.6 TB/s, 97 % of a measured copy; the forward pass issues 80 % of its
-// cycles), GELU without a gate 209 us (6.4 TB/s); 16384 x 4096 bf16 packed and
-// unpacked 67.5 us (6.0 TB/s; packing issues 78 %); 4925 x 771 fp32 out of rows of
+// Measured: SiLU, gated, 16384 x 8192 bf16, saved in int8, forward and backward 366
+// us (6.6 TB/s, 98 % of a measured copy; the forward pass issues 78 % of its
+// cycles), GELU without a gate 204 us (6.6 TB/s); 16384 x 4096 bf16 packed and
+// unpacked 63.5 us (6.4 TB/s; packing issues 75 %); 4925 x 771 fp32 out of rows of
 // 776 9.1 us (3.4 TB/s, scalar moves).
 #include <algorithm>
 #include <climits>
@@ -115,10 +115,38 @@ struct Units {
     }
 };
 
-template <typename T, int KIND, bool VEC, bool LANES>
+// The scales of up to four groups that a lane belongs to, one of each of its chunks
+// and matrices: a group has four lanes at least, so each works out one (a quotient is
+// most of the work) and the others take it from there.  Each lane by itself: the
+// gated 16384 x 8192 above 371.7 us (366.2 so), 16384 x 4096 packed only, by two chunks
+// a warp, 67.3 (66.6).
+template <int N>
+struct SharedScales {
+    float inv[N];  // negative: the group stands for NaN
+    float scale;   // of number lane % N
+    __device__ __forceinline__ SharedScales(const uint32_t (&largest)[N], const PackedRows* const (&to)[N], int lane)
+    {
+        static_assert(N == 1 || N == 2 || N == 4, "a power of two, and no more than a group's lanes");
+        const int pick = lane & (N - 1);
+        uint32_t m = largest[0];
+        int e4m3 = to[0]->e4m3;
+#pragma unroll
+        for (int k = 1; k < N; ++k) {
+            m = pick == k ? largest[k] : m;
+            e4m3 = pick == k ? to[k]->e4m3 : e4m3;
+        }
+        const GroupScale s(m, e4m3);
+        scale = s.scale;
+        const float mine = s.bad ? -1.0f : s.inv;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            inv[k] = __shfl_sync(kAll, mine, (lane & ~(N - 1)) | k);
+    }
+};
+
+template <typename T, int KIND, bool VEC, bool LANES, int kUnits = kUnitsOf<KIND, VEC>>
 __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation(const __grid_constant__ ActivationArgs a, const Cut cut)
 {
-    constexpr int kUnits = kUnitsOf<KIND, VEC>;
     const Units<kUnits, VEC, LANES> u(a.rows, a.cols, cut);
     const int lane = threadIdx.x & 31;
     wait_for_launch_before();
@@ -132,14 +160,52 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation(const __gri
         if (gated)
             vup[i].load(u.cols[i], a.up.data, u.row[i] * a.up.stride, a.up.type);
     }
+    // codes of a chunk, number k of the shared scales (VEC)
+    constexpr int N = KIND == kIdentity ? kUnits : 2 * kUnits;
+    float inv[N] = {}, scale = 0.0f;
+    const auto pack = [&](const PackedRows& p, int i, const float(&x)[8], int k) {
+        if constexpr (VEC) {
+            const Columns<VEC>& c = u.cols[i];
+            const uint2 w = codes8(x, inv[k], inv[k] < 0.0f, p);
+            if (c.count)
+                *reinterpret_cast<uint2*>(p.codes + u.row[i] * p.stride + c.at) = w;
+            // lane k of a group has its scale, and columns or not
+            const int64_t group = c.at >> p.log_group;
+            if ((lane & ((1 << (p.log_group - 3)) - 1)) == k && (LANES ? c.count != 0 : group << p.log_group < a.cols))
+                p.scales[u.row[i] * p.scale_stride + group] = scale;
+        }
+    };
+    if constexpr (VEC)
+        if (a.saved.codes || (gated && a.saved_up.codes)) {
+            uint32_t largest[N];
+            const PackedRows* to[N];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                largest[i] = a.saved.codes ? lanes_max(vx[i].largest(), a.saved.log_group - 3) : 0;
+                to[i] = &a.saved;
+                if constexpr (KIND != kIdentity) {
+                    largest[kUnits + i] = gated && a.saved_up.codes ? lanes_max(vup[i].largest(), a.saved_up.log_group - 3) : 0;
+                    to[kUnits + i] = &a.saved_up;
+                }
+            }
+            const SharedScales<N> s(largest, to, lane);
+            scale = s.scale;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                inv[k] = s.inv[k];
+        }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         if (!u.on[i])
             continue;
         float x[8];
         vx[i].unpack(x);
-        if (a.saved.codes)
-            pack_chunk<VEC>(a.saved, u.cols[i], u.row[i], x, vx[i].largest(), lane);
+        if (a.saved.codes) {
+            if constexpr (VEC)
+                pack(a.saved, i, x, i);
+            else
+                pack_chunk<VEC>(a.saved, u.cols[i], u.row[i], x, 0, lane);
+        }
         if constexpr (KIND != kIdentity) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -150,8 +216,12 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation(const __gri
             if (gated) {
                 float y[8];
                 vup[i].unpack(y);
-                if (a.saved_up.codes)
-                    pack_chunk<VEC>(a.saved_up, u.cols[i], u.row[i], y, vup[i].largest(), lane);
+                if (a.saved_up.codes) {
+                    if constexpr (VEC)
+                        pack(a.saved_up, i, y, kUnits + i);
+                    else
+                        pack_chunk<VEC>(a.saved_up, u.cols[i], u.row[i], y, 0, lane);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     set_pair(x, k, mul2(pair_of(x, k), pair_of(y, k)));
@@ -224,11 +294,10 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation_grad(const 
     }
 }
 
-template <bool VEC, bool LANES>
+template <bool VEC, bool LANES, int kUnits = kUnitsOf<kIdentity, VEC>>
 __global__ void __launch_bounds__(kBlock) k_unpack(const PackedRows x, const TypedRows out, const int64_t rows, const int64_t cols,
                                                    const Cut cut)
 {
-    constexpr int kUnits = kUnitsOf<kIdentity, VEC>;
     const Units<kUnits, VEC, LANES> u(rows, cols, cut);
     wait_for_launch_before();
     if (!u.on[0])
@@ -265,6 +334,15 @@ struct Grid {
         blocks = (all + kWarps - 1) / kWarps;
     }
     bool fits() const { return blocks <= INT_MAX && cut.spans <= INT_MAX; }
+    // bf16 packed or unpacked only, by four chunks a warp, which then share one quotient, and not two
+    // (that is g): where it leaves hardly more chunks without columns and there is a block for each
+    // place of 152 SMs.  Packed by two and by four: 8192 x 4096 20.1, 19.0 us, 8192 rows of 768 out of
+    // 776 5.0, 4.5, 4096 x 2048 5.27, 5.03; but 3060 x 2048 4.19, 4.27, 788 x 768 1.5, 1.9, 16384 rows
+    // of 1536 16.2, 17.5; 8192 x 4096 fp32 25.5, 26.1.  Unpacked as well 16384 x 4096 takes 1 us less.
+    bool better_than(const Grid& g) const
+    {
+        return !cut.lanes && !g.cut.lanes && cut.spans * 30 <= g.cut.spans * 16 && blocks >= 6 * 152;
+    }
 };
 
 int group_of(const PackedRows& p) { return !p.codes ? 1 : p.log_group == kRowGroup ? 8 : 1 << p.log_group; }
@@ -279,6 +357,11 @@ cudaError_t forward_t(const ActivationArgs& a, cudaStream_t s)
     if constexpr (VEC)
         if (g.cut.lanes)
             return go(k_activation<T, KIND, VEC, true>);
+    if constexpr (VEC && KIND == kIdentity && std::is_same_v<T, __nv_bfloat16>) {
+        const Grid wide(a.rows, a.cols, 4, VEC, group_of(a.saved));
+        if (wide.better_than(g))
+            return launch_programmatic(k_activation<T, KIND, VEC, false, 4>, static_cast<unsigned>(wide.blocks), kBlock, 0, s, a, wide.cut);
+    }
     return go(k_activation<T, KIND, VEC, false>);
 }
 
@@ -345,6 +428,9 @@ cudaError_t launch_unpack(const PackedRows& x, const TypedRows& out, int64_t row
     const Grid g(rows, cols, vec ? kUnitsOf<kIdentity, true> : kUnitsOf<kIdentity, false>, vec, 8);
     if (!g.fits())
         return cudaErrorInvalidConfiguration;
+    const Grid wide(rows, cols, 4, vec, 8);
+    if (vec && out.type == LIONCUB_ROWS_BF16 && wide.better_than(g))
+        return launch_programmatic(k_unpack<true, false, 4>, static_cast<unsigned>(wide.blocks), kBlock, 0, s, x, out, rows, cols, wide.cut);
     const auto go = [&](auto kernel) { return launch_programmatic(kernel, static_cast<unsigned>(g.blocks), kBlock, 0, s, x, out, rows, cols, g.cut); };
     return !vec ? go(k_unpack<false, false>) : g.cut.lanes ? go(k_unpack<true, true>) : go(k_unpack<true, false>);
 }

@@ -262,18 +262,18 @@ __device__ __forceinline__ uint32_t int8_pairs(float2 a, float2 b, float one)
     return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                        __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], const GroupScale& s, const PackedRows& p)
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv, bool bad, const PackedRows& p)
 {
     uint2 w;
     float2 y[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        y[k] = mul2(pair_of(x, k), both(s.inv));
+        y[k] = mul2(pair_of(x, k), both(inv));
     if (p.e4m3)
         w = make_uint2(e4m3_pairs(y[0], y[1]), e4m3_pairs(y[2], y[3]));
     else
         w = make_uint2(int8_pairs(y[0], y[1], p.one), int8_pairs(y[2], y[3], p.one));
-    if (s.bad)
+    if (bad)
         w = make_uint2(0, 0);
     return w;
 }
@@ -340,7 +340,7 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
     if constexpr (VEC) {
         const int log_lanes = p.log_group - 3;  // of a group
         const GroupScale s(lanes_max(largest, log_lanes), e4m3);
-        const uint2 w = codes8(x, s, p);
+        const uint2 w = codes8(x, s.inv, s.bad, p);
         if (c.count) {
             *reinterpret_cast<uint2*>(codes) = w;
             if ((lane & ((1 << log_lanes) - 1)) == 0)
@@ -415,7 +415,7 @@ __device__ __forceinline__ void pack_chunk_of_row(const PackedRows& p, const Col
     uint8_t* codes = p.codes + row * p.stride + c.at;
     if constexpr (VEC) {
         if (c.count)
-            *reinterpret_cast<uint2*>(codes) = codes8(x, s, p);
+            *reinterpret_cast<uint2*>(codes) = codes8(x, s.inv, s.bad, p);
     } else {
         const bool plain = c.whole && !s.bad;
 #pragma unroll

@@ -121,6 +121,28 @@ def test_codes_are_equal_to_the_bit(ops, rows, cols, code, group):
         _untouched(whole, rows, cols, pad, shift)
 
 
+@pytest.mark.parametrize("rows,cols,pad", [(7999, 1000, 16), (8200, 1024, 0), (7777, 968, 8), (3900, 2016, 24), (1, 8000008, 0)])
+@pytest.mark.parametrize("code,group", [("int8", 32), ("e4m3", 64), ("int8", 256)])
+def test_codes_of_many_rows(ops, rows, cols, pad, code, group):
+    """Sizes at which a warp takes four chunks at once."""
+    x = _rand((rows, cols), "bf16", rows + cols)
+    x[0, 3], x[rows - 1, cols - 1] = float("nan"), float("-inf")
+    codes, scales = ref.pack(x.float().numpy(), code, group)
+    out, whole, around = _packed(ops, rows, cols, code, group, pad)
+    ops.pack8(_strided(x, pad, 0)[0], out=out)
+    got = _bits(out.codes).reshape(rows, cols)
+    assert ((got == codes) | ((got | codes) & 127 == 0)).all()  # a zero may have either sign
+    assert np.array_equal(out.scales.cpu().numpy(), scales, equal_nan=True)
+    _untouched(whole, rows, cols, pad, 0)
+    _untouched(around, rows, scales.shape[1], 3 if pad else 0, 0)
+    back, whole = _strided(torch.zeros(rows, cols, dtype=torch.bfloat16), pad, 0)
+    ops.unpack8(out, out=back)
+    want = torch.from_numpy(ref.unpack(codes, scales, code, group)).to(torch.bfloat16)
+    assert torch.equal(back.cpu().nan_to_num(nan=123.0), want.nan_to_num(nan=123.0))
+    assert torch.equal(back.cpu().isnan(), want.isnan())
+    _untouched(whole, rows, cols, pad, 0)
+
+
 @pytest.mark.parametrize("cols", [256, 259])
 def test_products_are_rounded_before_codes_are(ops, cols):
     """Numbers whose exact product with inv and its fp32 rounding lie on two sides of a border between whole numbers."""
@@ -397,6 +419,29 @@ def test_activation(ops, rows, cols, kind, gated, xk):
             _check(dup, d64 * f, np.abs(d64) * fm, 16, dtype)
         for _, whole in bufs[:2] + bufs[3:] + (bufs[2:3] if gated else []):
             _untouched(whole, rows, cols, pad, shift)
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 1000), (40, 256), (1, 8), (9, 264), (2, 96), (4, 77)])
+@pytest.mark.parametrize("kinds", [("int8", 32, "e4m3", 256), ("e4m3", 128, "int8", 64), ("int8", 256, "int8", 32)])
+@pytest.mark.parametrize("xk", list(T))
+def test_two_saved_matrices_of_different_codes(ops, rows, cols, kinds, xk):
+    """Codes, groups and what is not finite of one are no matter of the other's."""
+    code, group, code_up, group_up = kinds
+    x, up = (_rand((rows, cols), xk, rows + k, 3.0) for k in range(2))
+    x[0, 0], x[-1, cols // 2] = float("nan"), float("inf")
+    up[0, cols - 1], up[rows // 2, cols // 3] = float("-inf"), 1e-35
+    saved, *rest = _packed(ops, rows, cols, code, group, 16)
+    saved_up, *rest_up = _packed(ops, rows, cols, code_up, group_up, 16)
+    ops.activation(x.cuda(), up.cuda(), kind="silu", saved=saved, saved_up=saved_up)
+    for p, v, c, g, (whole, around) in ((saved, x, code, group, rest), (saved_up, up, code_up, group_up, rest_up)):
+        codes, scales = ref.pack(v.float().numpy(), c, g)
+        got = _bits(p.codes).reshape(rows, cols)
+        assert ((got == codes) | ((got | codes) & 127 == 0)).all()  # a zero may have either sign
+        assert np.array_equal(p.scales.cpu().numpy(), scales, equal_nan=True)
+        _untouched(whole, rows, cols, 16, 0)
+        _untouched(around, rows, scales.shape[1], 3, 0)
+        only = ops.pack8(v.cuda(), group=g, dtype=CODES[c])
+        assert np.array_equal(_bits(only.codes), _bits(p.codes))
 
 
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
