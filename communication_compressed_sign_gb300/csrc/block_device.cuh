@@ -114,15 +114,33 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int log_lanes)
 template <typename T, bool VEC>
 struct Chunk;
 
+// Eight fp32 numbers by one move of 32 bytes where their place allows (rows of which
+// do all lanes or none), so that a store fills whole sectors of memory: 8192 x 4096
+// fp32 packed and unpacked 59.8 us by moves of 16 bytes, 51.5 by stores of 32; GELU of
+// 788 x 768 fp32, both ways, 3.59, 3.76, and 3.57 by loads of 32 too.
+__device__ __forceinline__ void load8(const float* p, Group8<float>& g)
+{
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(g.a.x), "=f"(g.a.y), "=f"(g.a.z), "=f"(g.a.w), "=f"(g.b.x), "=f"(g.b.y), "=f"(g.b.z), "=f"(g.b.w)
+                     : "l"(p) : "memory");
+    } else {
+        g.a = reinterpret_cast<const float4*>(p)[0];
+        g.b = reinterpret_cast<const float4*>(p)[1];
+    }
+}
+
 template <typename T>
 struct Chunk<T, true> {
     Group8<T> g;
     __device__ __forceinline__ void load(const Columns<true>& c, const void* base, int64_t e, int)
     {
-        if (c.count)
-            g.load(base, e + c.at);
-        else
+        if (!c.count)
             g = Group8<T>{};
+        else if constexpr (sizeof(T) == 4)
+            load8(static_cast<const float*>(base) + e + c.at, g);
+        else
+            g.load(base, e + c.at);
     }
     __device__ __forceinline__ void unpack(float (&x)[8]) const { g.unpack(x); }
     // the bits of the largest magnitude (see largest_of)
@@ -190,6 +208,18 @@ __device__ __forceinline__ void load_typed(const Columns<VEC>& c, const void* ba
     }
 }
 
+__device__ __forceinline__ void store8(float* p, const float (&x)[8])
+{
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     :: "l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
 template <bool VEC>
 __device__ __forceinline__ void store_typed(const Columns<VEC>& c, void* base, int64_t e, int type, const float (&x)[8])
 {
@@ -201,9 +231,7 @@ __device__ __forceinline__ void store_typed(const Columns<VEC>& c, void* base, i
             g.pack(x);
             g.store(base, e + c.at);
         } else {
-            Group8<float> g;
-            g.pack(x);
-            g.store(base, e + c.at);
+            store8(static_cast<float*>(base) + e + c.at, x);
         }
     } else {
         const auto store = [&](auto* p) {

@@ -12,7 +12,7 @@
 // all blocks in order.
 //
 // Measured: 65536 x 2048 bf16 from int8, with the normed rows again, 181.8 us (6.7
-// TB/s, 98 % of a measured copy); 8192 x 768 onto fp32 18.5 us (4.8 TB/s; some 6
+// TB/s, 98 % of a measured copy); 8192 x 768 onto fp32 18.0 us (4.9 TB/s; some 6
 // of them are the two launches' beginnings and ends, 2.6 the second launch); 4907
 // x 771 bf16 13.8 us (2.2 TB/s, scalar reads of the ring; 16.7 with one thread
 // starting the copies of all matrices).  The first with its rows

@@ -444,6 +444,41 @@ def test_two_saved_matrices_of_different_codes(ops, rows, cols, kinds, xk):
         assert np.array_equal(_bits(only.codes), _bits(p.codes))
 
 
+@pytest.mark.parametrize("pad,shift", [(4, 0), (0, 4), (4, 4), (12, 8)])
+def test_fp32_rows_between_two_alignments(ops, pad, shift):
+    """Rows that begin at multiples of 16 bytes, only some of them of 32: results are those of rows in one piece."""
+    rows, cols = 37, 192
+    plain = [_rand((rows, cols), "f32", k, 3.0).cuda() for k in range(3)]
+    weight = _rand((cols,), "f32", 9).cuda()
+
+    def run(pad, shift):
+        x, up, dout = (_strided(v.cpu(), pad, shift)[0] for v in plain)
+        w = _strided(weight.cpu()[None], pad, shift)[0][0]
+        made = []
+
+        def new():
+            made.append(_strided(torch.zeros(rows, cols), pad, shift))
+            return made[-1][0]
+
+        p, q = (_packed(ops, rows, cols, "int8", 32, 16)[0] for _ in range(2))
+        ops.pack8(x, out=p)
+        ops.unpack8(p, out=new())
+        ops.activation(x, up, kind="silu", out=new(), saved=q)
+        ops.activation_backward(dout, x, up, kind="gelu", dx=new(), dup=new(), again=new())
+        layer = ops.RmsNorm(cols)
+        rstd = torch.empty(rows, device="cuda")
+        summed = new()
+        layer.forward(x, w, residual=up, summed=summed, rstd=rstd, out=new())
+        grad = torch.empty(cols + 4, device="cuda")[shift and 4:][:cols]
+        layer.backward(dout, summed, rstd, w, residual_grad=up, out=new(), weight_grad=grad, again=new())
+        for _, whole in made:
+            _untouched(whole, rows, cols, pad, shift)
+        return [v.cpu().clone() for v, _ in made] + [rstd.cpu(), grad.cpu(), p.scales.cpu(), p.codes.cpu(), q.scales.cpu(), q.codes.cpu()]
+
+    for k, (a, b) in enumerate(zip(run(0, 0), run(pad, shift))):
+        assert torch.equal(a, b), k
+
+
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 def test_activation_far_out(ops, kind):
     x = torch.tensor([0.0, -0.0, 1e-30, 20.0, -20.0, 80.0, -80.0, 90.0, -90.0, 1e10, -1e10, 1e19, -1e19, 3e38, -3e38], device="cuda")
