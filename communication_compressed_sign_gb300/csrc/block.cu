@@ -853,10 +853,12 @@ int lioncub_rotary_apply(lioncub_rotary_t h, const lioncub_sequences* places, co
     a.copy = copy;
     a.cos_factor = h->magnitude;
     a.sin_factor = inverse ? -h->magnitude : h->magnitude;
-    // elements moved at once: halves of the rotated columns, and those behind, are whole moves
+    // elements moved at once: halves of the rotated columns (or all of them, where pairs lie side
+    // by side), and those behind, are whole moves
+    const int64_t widths = h->head_dim | (h->interleaved ? 2 * a.pairs : a.pairs);
     const int64_t size = static_cast<int64_t>(element_size(q->type));
     int move = reach % 16 == 0 && h->head_dim % 8 == 0 && a.pairs % 8 == 0 ? 8 : 4;
-    while (move < 8 && move > 1 && (reach % (move * size) || (h->head_dim | a.pairs) % move))
+    while (move < 8 && move > 1 && (reach % (move * size) || widths % move))
         move /= 2;
     return finish_launch(launch(h, "rotary", [&] { return lc::launch_rotary(a, q->type, h->interleaved, move, stream); }), "rotary launch");
 }

@@ -12,7 +12,8 @@
 // Measured: 65536 places, 40 heads of 128 bf16 196 us (6.8 TB/s); 8192 places, 24
 // heads of 64 out of a fused product 11.3 us (4.5 TB/s; two waves); 8 places 2.4 us.
 // Heads of 80 with 40 interleaved columns, 4 elements at a time, 8.4 us for 8192 x
-// 10 (3.0 TB/s); with 20, 2 at a time, 66 us for 45708 x 12 (2.6 TB/s).
+// 10 (3.0 TB/s); with 20, 45708 x 12 heads: halves, 2 at a time, 67 us (2.6 TB/s), and
+// interleaved, 4 at a time, 58 (3.0 TB/s).
 // Angles are turns in 64-bit fixed point: position * turns-a-position wraps
 // around by itself, which is the exact reduction that far positions need (in
 // fp32 the angle of position 100000 would be off by 0.004).
