@@ -860,7 +860,8 @@ int lioncub_rotary_apply(lioncub_rotary_t h, const lioncub_sequences* places, co
     int move = reach % 16 == 0 && h->head_dim % 8 == 0 && a.pairs % 8 == 0 ? 8 : 4;
     while (move < 8 && move > 1 && (reach % (move * size) || widths % move))
         move /= 2;
-    return finish_launch(launch(h, "rotary", [&] { return lc::launch_rotary(a, q->type, h->interleaved, move, stream); }), "rotary launch");
+    const bool copy_by_four = reach % (4 * size) == 0 && h->head_dim % 4 == 0 && a.pairs % 2 == 0;
+    return finish_launch(launch(h, "rotary", [&] { return lc::launch_rotary(a, q->type, h->interleaved, move, copy_by_four, stream); }), "rotary launch");
 }
 
 void lioncub_rotary_destroy(lioncub_rotary_t h)

@@ -103,6 +103,7 @@ cudaError_t launch_activation(const ActivationArgs& a, int kind, bool vec, cudaS
 cudaError_t launch_activation_grad(const ActivationArgs& a, int kind, bool vec, cudaStream_t s);
 cudaError_t launch_unpack(const PackedRows& x, const TypedRows& out, int64_t rows, int64_t cols, bool vec, cudaStream_t s);
 // move: elements at a time, 8 (then 16-byte aligned, and whole halves of 8 pairs), 4, 2 or 1.
-cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, int move, cudaStream_t s);
+// copy_by_four: columns that are copied may be moved four at a time.
+cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, int move, bool copy_by_four, cudaStream_t s);
 
 }  // namespace lc

@@ -7,13 +7,15 @@
 // then walks over the places' heads in the order of memory.  (A thread with the
 // same columns of several heads keeps its angles in registers, but then all blocks
 // read the same few heads of every place at a time: 192 to 275 us by how many
-// heads, where this takes 196 whatever the layout.  The first items loaded before
-// the angles are worked out: 202, and nothing gained by small calls.)
-// Measured: 65536 places, 40 heads of 128 bf16 196 us (6.8 TB/s); 8192 places, 24
-// heads of 64 out of a fused product 11.3 us (4.5 TB/s; two waves); 8 places 2.4 us.
-// Heads of 80 with 40 interleaved columns, 4 elements at a time, 8.4 us for 8192 x
-// 10 (3.0 TB/s); with 20, 45708 x 12 heads: halves, 2 at a time, 67 us (2.6 TB/s), and
-// interleaved, 4 at a time, 58 (3.0 TB/s).
+// heads, where this took 196 whatever the layout.  The first items loaded before
+// the angles are worked out: 202, and nothing gained by small calls.)  Queries and
+// keys are one list of heads, so that a block waits for memory as seldom as it can: one
+// after the other 8 places took 2.4 us, 45708 x 12 heads of 80 60 us.
+// Measured: 65536 places, 40 heads of 128 bf16 193 us (6.95 TB/s); 8192 places, 24
+// heads of 64 out of a fused product 10.9 us (4.6 TB/s; two waves); 8 places 1.8 us.
+// Heads of 80 with 40 interleaved columns, 4 elements at a time, 7.0 us for 8192 x
+// 10 (3.7 TB/s); with 20, 45708 x 12 heads: halves, 2 at a time, 38 us (4.6 TB/s), and
+// interleaved, 4 at a time, 35.6.
 // Angles are turns in 64-bit fixed point: position * turns-a-position wraps
 // around by itself, which is the exact reduction that far positions need (in
 // fp32 the angle of position 100000 would be off by 0.004).
@@ -25,13 +27,13 @@
 namespace lc {
 namespace {
 
-// Threads and places of a block.  8192 places of 24 x 64 and 65536 of 40 x 128: blocks of
-// 256 with 2, 4, 6, 8 and 14 places 19.8, 14.2, 13.0, 11.6 and 14.5 us (fewer repeat the
-// start, more leave SMs idle) and 215, 196, 195, 196 and 195; of 128 with 4 11.3 and 196,
-// with 8 14.5 and 196.
+// Threads of a block, and its places: as many as make up kBytes of heads, kMaxPlaces at most.
+// By 9, 12 and 16 KB: 8192 places of 24 x 64 bf16 12.0, 10.9, 12.4 us, fp32 17.0, 17.0, 18.1;
+// 65536 of 40 x 128 bf16 202, 193, 193.  Blocks of 192 threads 11.0, 17.3, 195; of 256 11.7,
+// 16.9, 195 (4 places each).
 constexpr int kBlock = 128;
-constexpr int kMaxPlaces = 4;
-constexpr int kItems = 8;      // of a thread, about, where there are many places
+constexpr int kMaxPlaces = 8;
+constexpr int kBytes = 12288;
 
 // cos and sin of a position's angle.  The nearest quarter turn is taken off in
 // whole numbers, so what is left is at most an eighth of a turn.
@@ -165,6 +167,37 @@ struct NarrowItem {
     }
 };
 
+// Eight columns that are copied, four at a time.
+template <typename T>
+struct CopiedItem {
+    struct alignas(4 * sizeof(T)) Move {
+        T x[4];
+    };
+    Move m[2];
+    int first, count;
+
+    __device__ __forceinline__ void place(const RotaryArgs& a, int item, int)
+    {
+        first = 2 * a.pairs + item * 8;
+        count = a.head_dim - first;
+    }
+    __device__ __forceinline__ void load(const RotaryArgs&, const T* in)
+    {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (4 * k < count)
+                m[k] = *reinterpret_cast<const Move*>(in + first + 4 * k);
+    }
+    __device__ __forceinline__ void turn(const float*, const float*, int, int) {}
+    __device__ __forceinline__ void store(const RotaryArgs&, T* out) const
+    {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (4 * k < count)
+                *reinterpret_cast<Move*>(out + first + 4 * k) = m[k];
+    }
+};
+
 template <typename T, bool INTERLEAVED, int MOVE>
 using ItemOf = std::conditional_t<MOVE == 8, WideItem<T, INTERLEAVED>, NarrowItem<T, INTERLEAVED, MOVE>>;
 
@@ -175,14 +208,56 @@ struct Divisor {
 };
 Divisor divisor(uint32_t d, uint64_t largest) { return {d, d > 1 && largest * d < (1ull << 32) ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0}; }
 
-template <typename T, bool INTERLEAVED, int MOVE>
-__global__ void __launch_bounds__(kBlock, 8) k_rotary(const __grid_constant__ RotaryArgs a, const int turning, const Divisor items,
-                                                   const Divisor heads0, const Divisor heads1, const int block_places)
+// Where the heads of a place are, of either side.
+template <typename T>
+struct Place {
+    const T* in[2];
+    T* out[2];
+};
+
+// The items of the heads of some places, of both sides, over the block's threads.
+template <typename Item, typename T>
+__device__ __forceinline__ void walk(const RotaryArgs& a, int places, const Place<T>* at, const float* cosines, const float* sines,
+                                     const Divisor& items, const Divisor& heads, int turning)
 {
     constexpr int kUnits = 2;  // items of a thread, whose loads are in flight together
+    const uint32_t units = places * heads.d * items.d;
+    for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kUnits * kBlock) {
+        Item x[kUnits];
+        uint32_t item[kUnits], p[kUnits];
+        T* out[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const uint32_t unit = u0 + u * kBlock;
+            if (unit < units) {
+                const uint32_t head = items.of(unit);  // of all places
+                item[u] = unit - head * items.d;
+                p[u] = heads.of(head);
+                uint32_t h = head - p[u] * heads.d;
+                const bool side = h >= a.heads[0];
+                h -= side ? a.heads[0] : 0;
+                out[u] = at[p[u]].out[side] + h * (side ? a.side[1].out_head : a.side[0].out_head);
+                x[u].place(a, item[u], turning);
+                x[u].load(a, at[p[u]].in[side] + h * (side ? a.side[1].in_head : a.side[0].in_head));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+            if (u0 + u * kBlock < units) {
+                x[u].turn(cosines + p[u] * a.pairs, sines + p[u] * a.pairs, item[u], a.pairs);
+                x[u].store(a, out[u]);
+            }
+    }
+}
+
+// APART: columns that are copied are walked over by themselves (copied: their items).
+template <typename T, bool INTERLEAVED, int MOVE, bool APART>
+__global__ void __launch_bounds__(kBlock, 8) k_rotary(const __grid_constant__ RotaryArgs a, const int turning, const Divisor items,
+                                                   const Divisor copied, const Divisor heads, const int block_places)
+{
     using Item = ItemOf<T, INTERLEAVED, MOVE>;
     extern __shared__ __align__(16) float cosines[];  // of each place and pair; then the sines
-    __shared__ int64_t starts[kMaxPlaces][4];         // of a place: elements to its in and out of either side
+    __shared__ Place<T> at[kMaxPlaces];
     __shared__ int64_t positions[kMaxPlaces];
     float* sines = cosines + block_places * a.pairs;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * block_places;
@@ -193,8 +268,8 @@ __global__ void __launch_bounds__(kBlock, 8) k_rotary(const __grid_constant__ Ro
         const int64_t place = first + threadIdx.x, b = quotient(place, a.seq), s = place - b * a.seq;
         positions[threadIdx.x] = a.positions ? index_at(a.positions, place, a.wide) : a.first + s;
         for (int k = 0; k < 2; ++k) {
-            starts[threadIdx.x][2 * k] = b * a.side[k].in_batch + s * a.side[k].in_place;
-            starts[threadIdx.x][2 * k + 1] = b * a.side[k].out_batch + s * a.side[k].out_place;
+            at[threadIdx.x].in[k] = static_cast<const T*>(a.side[k].in) + (b * a.side[k].in_batch + s * a.side[k].in_place);
+            at[threadIdx.x].out[k] = static_cast<T*>(a.side[k].out) + (b * a.side[k].out_batch + s * a.side[k].out_place);
         }
     }
     __syncthreads();
@@ -205,60 +280,45 @@ __global__ void __launch_bounds__(kBlock, 8) k_rotary(const __grid_constant__ Ro
     if (!a.positions)  // the angles need nothing of the launches before
         wait_for_launch_before();
     __syncthreads();
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        const Divisor heads = k ? heads1 : heads0;
-        const uint32_t units = places * heads.d * items.d;
-        const T* in = static_cast<const T*>(a.side[k].in);
-        T* out = static_cast<T*>(a.side[k].out);
-        const int64_t in_head = a.side[k].in_head, out_head = a.side[k].out_head;
-        for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kUnits * kBlock) {
-            Item x[kUnits];
-            uint32_t item[kUnits], p[kUnits], h[kUnits];
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-                const uint32_t unit = u0 + u * kBlock;
-                if (unit < units) {
-                    const uint32_t head = items.of(unit);  // of all places
-                    item[u] = unit - head * items.d;
-                    p[u] = heads.of(head);
-                    h[u] = head - p[u] * heads.d;
-                    x[u].place(a, item[u], turning);
-                    x[u].load(a, in + (starts[p[u]][2 * k] + h[u] * in_head));
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u)
-                if (u0 + u * kBlock < units) {
-                    x[u].turn(cosines + p[u] * a.pairs, sines + p[u] * a.pairs, item[u], a.pairs);
-                    x[u].store(a, out + (starts[p[u]][2 * k + 1] + h[u] * out_head));
-                }
-        }
-    }
+    walk<Item, T>(a, places, at, cosines, sines, items, heads, turning);
+    if constexpr (APART)
+        walk<CopiedItem<T>, T>(a, places, at, cosines, sines, copied, heads, 0);
 }
 
-template <typename T, bool INTERLEAVED, int MOVE>
+template <typename T, bool INTERLEAVED, int MOVE, bool APART = false>
 cudaError_t launch_t(const RotaryArgs& a, cudaStream_t s)
 {
     const int rest = a.copy ? a.head_dim - 2 * a.pairs : 0;
     using Item = ItemOf<T, INTERLEAVED, MOVE>;
-    const int turning = (a.pairs + Item::kPairs - 1) / Item::kPairs, items = turning + (rest + Item::kCopied - 1) / Item::kCopied;
-    // Places of a block: about kItems items for each of its threads, fewer while that leaves
-    // less than four blocks a multiprocessor.
-    const int64_t of_place = int64_t(a.heads[0] + a.heads[1]) * items;
-    int64_t places = std::min<int64_t>(kMaxPlaces, (kItems * kBlock + of_place - 1) / of_place);
+    const int turning = (a.pairs + Item::kPairs - 1) / Item::kPairs, copied = (rest + Item::kCopied - 1) / Item::kCopied;
+    const int items = turning + copied;
+    // Places of a block: kBytes of heads, but fewer while that leaves less than four blocks a
+    // multiprocessor.
+    const int64_t heads = int64_t(a.heads[0]) + a.heads[1], of_place = heads * a.head_dim * sizeof(T);
+    int64_t places = std::min<int64_t>(kMaxPlaces, (kBytes + of_place - 1) / of_place);
     places = std::max<int64_t>(1, std::min<int64_t>(places, a.places / (152 * 4)));
     const int64_t blocks = (a.places + places - 1) / places;
-    const int64_t most = places * std::max(a.heads[0], a.heads[1]) * items;
+    const int64_t most = places * heads * items;
     if (blocks > INT_MAX || most > INT_MAX)
         return cudaErrorInvalidConfiguration;
-    return launch_programmatic(k_rotary<T, INTERLEAVED, MOVE>, static_cast<unsigned>(blocks), kBlock, places * a.pairs * 2 * sizeof(float), s, a,
-                               turning, divisor(items, most), divisor(a.heads[0], most), divisor(a.heads[1], most), static_cast<int>(places));
+    return launch_programmatic(k_rotary<T, INTERLEAVED, MOVE, APART>, static_cast<unsigned>(blocks), kBlock,
+                               places * a.pairs * 2 * sizeof(float), s, a, turning, divisor(APART ? turning : items, most),
+                               divisor(copied, most), divisor(static_cast<uint32_t>(heads), most), static_cast<int>(places));
 }
 
 template <typename T, bool INTERLEAVED>
-cudaError_t launch_l(const RotaryArgs& a, int move, cudaStream_t s)
+cudaError_t launch_l(const RotaryArgs& a, int move, bool copy_by_four, cudaStream_t s)
 {
+    // Columns that are copied go by themselves, four at a time, unless all are moved by eight:
+    // warps whose lanes do either do both.  45708 x 12 heads of 80, 20 columns in halves 66.6 us
+    // among one another, 60.5 apart; interleaved 52.5, 36.5.
+    if (copy_by_four && a.copy && a.head_dim > 2 * a.pairs) {
+        if (move == 4)
+            return launch_t<T, INTERLEAVED, 4, true>(a, s);
+        if constexpr (!INTERLEAVED)
+            if (move == 2)
+                return launch_t<T, INTERLEAVED, 2, true>(a, s);
+    }
     switch (move) {
     case 8: return launch_t<T, INTERLEAVED, 8>(a, s);
     case 4: return launch_t<T, INTERLEAVED, 4>(a, s);
@@ -269,13 +329,13 @@ cudaError_t launch_l(const RotaryArgs& a, int move, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, int move, cudaStream_t s)
+cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, int move, bool copy_by_four, cudaStream_t s)
 {
     if (a.places == 0 || a.heads[0] + a.heads[1] == 0)
         return cudaSuccess;
     if (type == LIONCUB_ROWS_BF16)
-        return interleaved ? launch_l<__nv_bfloat16, true>(a, move, s) : launch_l<__nv_bfloat16, false>(a, move, s);
-    return interleaved ? launch_l<float, true>(a, move, s) : launch_l<float, false>(a, move, s);
+        return interleaved ? launch_l<__nv_bfloat16, true>(a, move, copy_by_four, s) : launch_l<__nv_bfloat16, false>(a, move, copy_by_four, s);
+    return interleaved ? launch_l<float, true>(a, move, copy_by_four, s) : launch_l<float, false>(a, move, copy_by_four, s);
 }
 
 }  // namespace lc

@@ -584,6 +584,31 @@ def test_rotary(ops, B, S, H, K, D, R, kind, interleaved):
         assert rest is None or torch.equal(buf[:, :, H + K:], rest)
 
 
+@pytest.mark.parametrize("B,S,H,K,D,R", [(3, 1777, 2, 1, 80, 20), (2, 3001, 1, 2, 80, 40), (1, 1217, 3, 0, 64, 64), (7, 701, 2, 2, 20, 10),
+                                         (1, 5003, 1, 1, 66, 22), (5, 433, 4, 3, 128, 96), (4, 999, 2, 1, 24, 8)])
+@pytest.mark.parametrize("kind", list(T))
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_of_many_places(ops, B, S, H, K, D, R, kind, interleaved):
+    """Several places a block, of two sequences too, and a last block with fewer."""
+    rot = ops.Rotary(D, rotary_dim=R, interleaved=interleaved)
+    buf = _rand((B, S, H + K + 1, D), kind, B * S + H).cuda()
+    at = np.random.default_rng(S).integers(0, 1 << 20, B * S)
+    p = torch.from_numpy(at).view(B, S).cuda()
+    q, k = buf[:, :, :H], buf[:, :, H:H + K]
+    outs = [torch.full((B, S, h, D + 8), 777.0, dtype=T[kind], device="cuda") for h in (H, K)]
+    to = [o[..., :D] for o in outs]
+    rot.forward(q, k if K else None, positions=p, q_out=to[0], k_out=to[1] if K else None)
+    for x, y, o in zip((q, k), to, outs):
+        if x.shape[2]:
+            exact, mag = ref.rotate(_np(x).reshape(B * S, -1, D), at, _frequencies(R), 1.0, interleaved, False)
+            _check(y, exact, mag, 10, T[kind])
+            assert torch.equal(y[..., R:], x[..., R:])
+            assert (o[..., D:] == 777.0).all()
+    rest = buf[:, :, H + K:].clone()
+    rot.forward(q, k if K else None, positions=p, q_out=q, k_out=k if K else None)
+    assert torch.equal(q, to[0]) and torch.equal(k, to[1]) and torch.equal(buf[:, :, H + K:], rest)
+
+
 def test_rotary_scalings_far_positions_and_adjoint(ops):
     D = 128
     turns = _frequencies(D)
