@@ -609,6 +609,21 @@ def test_rotary_of_many_places(ops, B, S, H, K, D, R, kind, interleaved):
     assert torch.equal(q, to[0]) and torch.equal(k, to[1]) and torch.equal(buf[:, :, H + K:], rest)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_of_fp32_heads_between_two_alignments(ops, interleaved):
+    """Heads that begin at multiples of 16 bytes but not of 32: results are those of others."""
+    rot = ops.Rotary(96, rotary_dim=64, interleaved=interleaved)
+    q = _rand((3, 50, 4, 96), "f32", 5).cuda()
+    want = rot.forward(q, first_position=9)
+    for shift, pad in ((4, 0), (0, 4), (4, 4), (12, 12)):
+        x, y = (torch.full((q.numel() // 96 * (96 + pad) + shift,), 777.0, device="cuda") for _ in range(2))
+        xv, yv = (t[shift:].view(3, 50, 4, 96 + pad)[..., :96] for t in (x, y))
+        xv.copy_(q)
+        rot.forward(xv, first_position=9, q_out=yv)
+        assert torch.equal(yv, want) and torch.equal(xv, q)
+        assert (y[:shift] == 777.0).all() and (y[shift:].view(3, 50, 4, 96 + pad)[..., 96:] == 777.0).all()
+
+
 def test_rotary_scalings_far_positions_and_adjoint(ops):
     D = 128
     turns = _frequencies(D)
