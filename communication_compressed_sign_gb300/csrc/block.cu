@@ -103,15 +103,17 @@ int check_size(int64_t rows, int64_t cols)
 }
 
 // The operands of a call: each is checked as it is added, and in the end the
-// results must share no bytes with one another, nor with an input unless they are it.
+// results must share no bytes with one another, nor with an input unless they are it
+// and it has been read by then.  `step` counts the parts of a call that follow one
+// another over all its rows: an input's is that of its last reading, a result's that of its writing.
 class Operands {
 public:
     int code = LIONCUB_OK;  // of the first refusal
     bool vec = true;        // all allow 16-byte moves (but for the width)
     bool dense = true;      // rows follow one another, groups do not cross them
 
-    void input(const char* name, const lioncub_rows* m, int64_t rows, int64_t cols) { add(name, m, rows, cols, false); }
-    void result(const char* name, const lioncub_rows* m, int64_t rows, int64_t cols) { add(name, m, rows, cols, true); }
+    void input(const char* name, const lioncub_rows* m, int64_t rows, int64_t cols, int step = 0) { add(name, m, rows, cols, false, step); }
+    void result(const char* name, const lioncub_rows* m, int64_t rows, int64_t cols, int step = 0) { add(name, m, rows, cols, true, step); }
     void input(const char* name, const lioncub_packed* m, int64_t rows, int64_t cols) { add(name, m, rows, cols, false); }
     void result(const char* name, const lioncub_packed* m, int64_t rows, int64_t cols) { add(name, m, rows, cols, true); }
     void vector(const char* name, const float* v, int64_t n, bool is_result)
@@ -131,7 +133,7 @@ public:
                 if (i == j || !a.result || (b.result && j < i) || !lc::overlap(a.span, b.span))
                     continue;
                 const bool same = a.span.at == b.span.at && a.span.step == b.span.step && a.span.width == b.span.width &&
-                                  a.span.rows == b.span.rows;
+                                  a.span.rows == b.span.rows && b.step <= a.step;
                 if (b.result || !same)
                     code = fail(LIONCUB_ERR_ARG, b.result ? "%s overlaps %s" : "%s overlaps %s without being it", a.name, b.name);
             }
@@ -143,13 +145,14 @@ private:
         const char* name;
         Span span;
         bool result;
+        int step;
     };
     Item items_[16];
     int count_ = 0;
 
-    void keep(const char* name, const Span& span, bool is_result) { items_[count_++] = {name, span, is_result}; }
+    void keep(const char* name, const Span& span, bool is_result, int step = 0) { items_[count_++] = {name, span, is_result, step}; }
 
-    void add(const char* name, const lioncub_rows* m, int64_t rows, int64_t cols, bool is_result)
+    void add(const char* name, const lioncub_rows* m, int64_t rows, int64_t cols, bool is_result, int step)
     {
         if (code != LIONCUB_OK || !m)
             return;
@@ -166,7 +169,7 @@ private:
         const bool starts = reinterpret_cast<uintptr_t>(m->data) % 16 == 0;
         vec = vec && (rows == 1 || m->stride == cols ? starts : aligned_rows(m));
         dense = dense && (rows == 1 || m->stride == cols);
-        keep(name, lc::span_of(*m, rows, cols), is_result);
+        keep(name, lc::span_of(*m, rows, cols), is_result, step);
     }
 
     void add(const char* name, const lioncub_packed* m, int64_t rows, int64_t cols, bool is_result)
@@ -530,8 +533,8 @@ int lioncub_rms_norm_backward(lioncub_rms_norm_t h, int64_t n, const lioncub_row
     // Rows are copied by 16 bytes, codes among them.  The weight's gradient is moved element by element.
     const bool vec = o.vec && h->dim % (packed_saved ? 16 : 8) == 0 &&
                      (!packed_saved || (reinterpret_cast<uintptr_t>(packed_saved->codes) | (n > 1 ? packed_saved->stride : 0)) % 16 == 0);
-    o.input("weight_base", weight_base, 1, h->dim);
-    o.result("weight_grad", weight_grad, 1, h->dim);
+    o.input("weight_base", weight_base, 1, h->dim, 1);  // by the second launch
+    o.result("weight_grad", weight_grad, 1, h->dim, 1);
     int rc = o.finish();
     if (rc == LIONCUB_OK)
         rc = check_device(h);

@@ -48,7 +48,8 @@
  * want 16-byte boundaries and halves of the rotated columns of 8.  Anything else
  * works element by element, at two to four times the cost.
  * A result may be the same matrix as an input of its type (the same address and
- * stride), each element then being read before it is written; results may not
+ * stride), each element then being read before it is written, but for
+ * weight_base, which is read last and may be weight_grad only; results may not
  * share bytes with inputs in any other way, nor with one another.
  */
 #ifndef LIONCUB_BLOCK_H
