@@ -475,11 +475,11 @@ int lioncub_rms_norm_forward(lioncub_rms_norm_t h, int64_t n, const lioncub_rows
     o.code = check_size(n, h->dim);
     o.input("x", x, n, h->dim);
     o.input("residual", residual, n, h->dim);
-    o.input("weight", weight, 1, h->dim);
+    o.input("weight", weight, 1, h->dim, 1);  // read between the sum's writing and the result's
     o.result("summed", summed, n, h->dim);
     o.result("saved", saved, n, h->dim);
     o.vector("rstd", rstd, n, true);
-    o.result("out", out, n, h->dim);
+    o.result("out", out, n, h->dim, 1);
     o.result("packed_out", packed_out, n, h->dim);
     int rc = o.finish();
     if (rc == LIONCUB_OK)

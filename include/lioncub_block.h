@@ -48,9 +48,10 @@
  * want 16-byte boundaries and halves of the rotated columns of 8.  Anything else
  * works element by element, at two to four times the cost.
  * A result may be the same matrix as an input of its type (the same address and
- * stride), each element then being read before it is written, but for
- * weight_base, which is read last and may be weight_grad only; results may not
- * share bytes with inputs in any other way, nor with one another.
+ * stride), each element then being read before it is written, but for what is
+ * read later: weight_base may be weight_grad only, and a forward call's weight
+ * not summed; results may not share bytes with inputs in any other way, nor with
+ * one another.
  */
 #ifndef LIONCUB_BLOCK_H
 #define LIONCUB_BLOCK_H

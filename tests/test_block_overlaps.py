@@ -139,3 +139,15 @@ def test_what_is_added_to_the_weights_gradient_is_no_result_of_the_rows(entries,
     assert not back(n, 64, A, B, C, D, weight=E, base=E, grad=F, again=E)
     assert not back(n, 1, A, B, C, D, base=D, grad=E)
     assert back(n, 64, A, B, C, D, weight=E, base=E, grad=F)  # two inputs
+
+
+@pytest.mark.parametrize("n", [1, 5])
+def test_the_norms_weight_is_no_sum(entries, n):
+    """The weight of one row's norm is read after the sum is written, but before the result is."""
+    go = entries.forward
+    assert not go(n, 64, A, B, weight=C, summed=C)
+    assert not go(n, 64, A, B, residual=D, weight=C, summed=C)
+    assert go(1, 64, A, C, weight=C) and not go(5, 64, A, C, weight=C)
+    for x, out, residual, summed in ((A, A, None, None), (A, A, B, B), (A, B, B, A), (A, C, B, B), (A, C, B, A), (A, B, None, A)):
+        assert go(n, 64, x, out, residual=residual, summed=summed, weight=F)
+    assert not go(n, 64, A, B, summed=B)
