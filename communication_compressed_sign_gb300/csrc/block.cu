@@ -103,8 +103,8 @@ int check_size(int64_t rows, int64_t cols)
 }
 
 // The operands of a call: each is checked as it is added, and in the end the
-// results must share no bytes with one another, nor with an input unless they are it
-// and it has been read by then.  `step` counts the parts of a call that follow one
+// results must share no bytes with one another, nor with an input unless both are one
+// matrix of elements (neither codes, scales nor a vector) and it has been read by then.  `step` counts the parts of a call that follow one
 // another over all its rows: an input's is that of its last reading, a result's that of its writing.
 class Operands {
 public:
@@ -132,8 +132,8 @@ public:
                 const Item &a = items_[i], &b = items_[j];
                 if (i == j || !a.result || (b.result && j < i) || !lc::overlap(a.span, b.span))
                     continue;
-                const bool same = a.span.at == b.span.at && a.span.step == b.span.step && a.span.width == b.span.width &&
-                                  a.span.rows == b.span.rows && b.step <= a.step;
+                const bool same = a.matrix && b.matrix && a.span.at == b.span.at && a.span.step == b.span.step &&
+                                  a.span.width == b.span.width && a.span.rows == b.span.rows && b.step <= a.step;
                 if (b.result || !same)
                     code = fail(LIONCUB_ERR_ARG, b.result ? "%s overlaps %s" : "%s overlaps %s without being it", a.name, b.name);
             }
@@ -144,13 +144,16 @@ private:
     struct Item {
         const char* name;
         Span span;
-        bool result;
+        bool result, matrix;
         int step;
     };
     Item items_[16];
     int count_ = 0;
 
-    void keep(const char* name, const Span& span, bool is_result, int step = 0) { items_[count_++] = {name, span, is_result, step}; }
+    void keep(const char* name, const Span& span, bool is_result, bool is_matrix = false, int step = 0)
+    {
+        items_[count_++] = {name, span, is_result, is_matrix, step};
+    }
 
     void add(const char* name, const lioncub_rows* m, int64_t rows, int64_t cols, bool is_result, int step)
     {
@@ -169,7 +172,7 @@ private:
         const bool starts = reinterpret_cast<uintptr_t>(m->data) % 16 == 0;
         vec = vec && (rows == 1 || m->stride == cols ? starts : aligned_rows(m));
         dense = dense && (rows == 1 || m->stride == cols);
-        keep(name, lc::span_of(*m, rows, cols), is_result, step);
+        keep(name, lc::span_of(*m, rows, cols), is_result, true, step);
     }
 
     void add(const char* name, const lioncub_packed* m, int64_t rows, int64_t cols, bool is_result)

@@ -47,11 +47,11 @@
  * (read by a norm's gradient: 16, and a width that is a multiple of 16).  Heads
  * want 16-byte boundaries and halves of the rotated columns of 8.  Anything else
  * works element by element, at two to four times the cost.
- * A result may be the same matrix as an input of its type (the same address and
- * stride), each element then being read before it is written, but for what is
- * read later: weight_base may be weight_grad only, and a forward call's weight
- * not summed; results may not share bytes with inputs in any other way, nor with
- * one another.
+ * A result may be the same lioncub_rows matrix as an input of its type (the same
+ * address and stride), each element then being read before it is written, but for
+ * what is read later: weight_base may be weight_grad only, and a forward call's
+ * weight not summed.  Results may not share bytes with inputs in any other way,
+ * nor with one another.
  */
 #ifndef LIONCUB_BLOCK_H
 #define LIONCUB_BLOCK_H

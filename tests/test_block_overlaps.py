@@ -151,3 +151,27 @@ def test_the_norms_weight_is_no_sum(entries, n):
     for x, out, residual, summed in ((A, A, None, None), (A, A, B, B), (A, B, B, A), (A, C, B, B), (A, C, B, A), (A, B, None, A)):
         assert go(n, 64, x, out, residual=residual, summed=summed, weight=F)
     assert not go(n, 64, A, B, summed=B)
+
+
+@pytest.mark.parametrize("n", [1, 5, 64])
+def test_a_vector_is_no_matrix(entries, n):
+    """rstd has a number for each row, a weight one for each column: with as many of both they are still not one matrix."""
+    for dim in (n, n + 1):
+        assert not entries.forward(n, dim, A, B, weight=C, rstd=C)
+        assert not entries.backward(n, dim, A, B, C, D, grad=C)
+    assert not entries.forward(1, 1, A, B, rstd=A)
+    assert not entries.backward(1, 1, A, B, C, C)
+    assert entries.forward(n, n, A, B, weight=C, rstd=D)
+
+
+def test_scales_and_codes_are_no_matrix(entries):
+    """Scales may lie like a column of fp32, and codes like bytes, but neither is the matrix that is packed."""
+    for rows in (1, 7):
+        assert not entries.pack(rows, 1, A, entries.packed(B, A, 1))
+        assert not entries.pack(rows, 1, A, entries.packed(B, A, 1, group=0))
+        assert not entries.pack(rows, 1, A, entries.packed(A, B, 1))
+        assert entries.pack(rows, 1, A, entries.packed(B, C, 1))
+        assert not entries.forward(rows, 1, A, B, weight=C, saved=entries.packed(D, A, 1))
+        assert not entries.forward(rows, 1, A, B, residual=E, saved=entries.packed(D, E, 1))
+    assert not entries.forward(1, 1, A, B, weight=C, saved=entries.packed(D, C, 1))
+    assert not entries.forward(1, 1, A, None, weight=C, packed_out=entries.packed(D, C, 1))
