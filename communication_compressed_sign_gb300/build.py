@@ -103,11 +103,16 @@ def _torch_dir() -> str | None:
     return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
-def build_tensors(force: bool = False) -> str:
-    """Compile the _tensors module; it needs torch's and Python's headers and a C++ compiler."""
-    torch = _torch_dir()
-    if torch is None:
-        raise RuntimeError("torch is not installed: the _tensors module cannot be built")
+def build_tensors(force: bool = False) -> str | None:
+    """Compile the _tensors module; it needs torch's and Python's headers and a C++ compiler.
+
+    Without those headers nothing else needs it (its users say that it is missing): None then.
+    """
+    torch, python = _torch_dir(), sysconfig.get_paths()["include"]
+    if torch is None or not os.path.exists(os.path.join(python, "Python.h")):
+        print(f"{'torch is not installed' if torch is None else 'there is no Python.h'}: the _tensors module is not built",
+              file=sys.stderr)
+        return None
     version = os.path.join(torch, "version.py")
     inputs = [TENSORS_SOURCE, version, os.path.abspath(__file__),
               *(os.path.join(INCLUDE, f) for f in ("lioncub.h", "lioncub_embed.h", "lioncub_block.h"))]
@@ -118,7 +123,7 @@ def build_tensors(force: bool = False) -> str:
         raise RuntimeError("no C++ compiler: the _tensors module cannot be built")
     tmp, libs = TENSORS + f".tmp{os.getpid()}", os.path.join(torch, "lib")
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-I{INCLUDE}", f"-I{os.path.join(torch, 'include')}",
-           f"-I{os.path.join(torch, 'include', 'torch', 'csrc', 'api', 'include')}", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{os.path.join(torch, 'include', 'torch', 'csrc', 'api', 'include')}", f"-I{python}",
            TENSORS_SOURCE, "-o", tmp, f"-L{libs}", "-lc10", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -129,4 +134,5 @@ def build_tensors(force: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(force=True, verbose="--verbose" in sys.argv, bounds_check="--bounds-check" in sys.argv))
-    print(build_tensors(force=True))
+    if tensors := build_tensors(force=True):
+        print(tensors)
