@@ -7,8 +7,9 @@ its gradient, :class:`Packed` a matrix in 8 bits with scales (:func:`pack8`,
 GELU, gated or not, and :class:`Rotary` rotary positions.  A norm and an
 activation can leave what their backward pass needs in 8 bits.  As in
 :mod:`.embed`, results are not part of torch's autograd graph and gradients come
-from the backward functions, called by hand; :func:`load` gives the library with
-the C functions declared.
+from the backward functions, called by hand: tensors that require a gradient while
+torch records one, or have a forward-mode tangent, are refused.  :func:`load`
+gives the library with the C functions declared.
 """
 from __future__ import annotations
 

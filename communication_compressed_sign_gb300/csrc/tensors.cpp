@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/grad_mode.h>
+#include <c10/core/AutogradState.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -74,6 +75,8 @@ void check_gradient(const at::Tensor& t, const char* name)
 {
     if (t.requires_grad() && at::GradMode::is_enabled())
         refuse(name, " requires a gradient, but results are not part of torch's graph: call under torch.no_grad() or pass a detached tensor");
+    if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+        refuse(name, " has a tangent (a forward-mode derivative), but results have none: pass its primal value");
 }
 
 int row_type(const at::Tensor& t, const char* name, int64_t device)
