@@ -10,7 +10,7 @@ library's message; the wrappers check tensors, pass their pointers through and
 allocate results with torch.  Results are not part of torch's autograd graph:
 gradients come from the backward functions, called by hand (or from a
 torch.autograd.Function of the caller's), and tensors that require a gradient
-are refused while torch records one.
+are refused while torch records one, tensors that have a forward-mode tangent too.
 """
 from __future__ import annotations
 
@@ -144,20 +144,21 @@ def lioncub_dropout_backward(rows: int, cols: int, dout, dx, drop, stream: int =
 # ---- torch tensors -------------------------------------------------------------
 
 # What the wrappers use of torch, looked up at their first call.
-_torch = None
+_torch = _forward_ad = None
 _row_types = _index_types = _raw_stream = _device = None
 
 
 def _use_torch():
-    global _torch, _row_types, _index_types, _raw_stream, _device
+    global _torch, _forward_ad, _row_types, _index_types, _raw_stream, _device
     import torch
+    from torch.autograd import forward_ad
     _row_types = {torch.bfloat16: ROWS_BF16, torch.float32: ROWS_F32}
     _index_types = {torch.int64: INDEX_I64, torch.int32: INDEX_I32}
     # the current stream's handle, without the Stream object that torch.cuda.current_stream() makes
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     _device = torch.cuda.current_device
-    _torch = torch
+    _torch, _forward_ad = torch, forward_ad
 
 
 def _rows(t, name, nrows, cols, device):
@@ -169,6 +170,8 @@ def _rows(t, name, nrows, cols, device):
     if t.requires_grad and _torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, but results are not part of torch's graph: "
                          "call under torch.no_grad() or pass a detached tensor")
+    if _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(t).tangent is not None and _torch._C._is_fwd_grad_enabled():
+        raise ValueError(f"{name} has a tangent (a forward-mode derivative), but results have none: pass its primal value")
     if not t.dim() or t.size(-1) != cols or t.numel() != nrows * cols:
         raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(t.shape)})")
     if t.is_contiguous():
