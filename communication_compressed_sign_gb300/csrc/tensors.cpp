@@ -112,14 +112,18 @@ int64_t step_of(const at::Tensor& t, const char* name, int64_t n, int64_t cols)
     return n > 1 ? step : cols;
 }
 
-void* address(const at::Tensor& t) { return const_cast<void*>(t.const_data_ptr()); }
+// What a call does with a tensor.  One that is written gets memory of its own first
+// if it shares that of another until then (a lazy clone).
+enum Use { kRead, kWrite };
+
+void* address(const at::Tensor& t, Use use) { return use == kWrite ? t.mutable_data_ptr() : const_cast<void*>(t.const_data_ptr()); }
 
 // A matrix argument; None is a null pointer.
 struct Matrix {
     lioncub_rows rows;
     const lioncub_rows* p = nullptr;
     Matrix() = default;
-    Matrix(PyObject* o, const char* name, int64_t n, int64_t cols, int64_t device)
+    Matrix(PyObject* o, const char* name, int64_t n, int64_t cols, int64_t device, Use use = kRead)
     {
         if (o == Py_None)
             return;
@@ -127,7 +131,7 @@ struct Matrix {
         const int type = row_type(t, name, device);
         if (!t.dim() || t.size(-1) != cols || t.numel() != n * cols)
             refuse(name, " must have ", n, " rows of ", cols, " columns (got ", shape_of(t), ")");
-        rows = {address(t), step_of(t, name, n, cols), type, 0};
+        rows = {address(t, use), step_of(t, name, n, cols), type, 0};
         p = &rows;
     }
 };
@@ -137,7 +141,7 @@ struct PackedMatrix {
     lioncub_packed packed;
     const lioncub_packed* p = nullptr;
     PackedMatrix() = default;
-    PackedMatrix(PyObject* o, const char* name, int64_t n, int64_t cols, int64_t device)
+    PackedMatrix(PyObject* o, const char* name, int64_t n, int64_t cols, int64_t device, Use use = kRead)
     {
         if (o == Py_None)
             return;
@@ -159,7 +163,7 @@ struct PackedMatrix {
             refuse(name, " must have ", n, " rows of ", cols, " columns (got ", shape_of(c), ")");
         if (!s.dim() || s.size(-1) != groups || s.numel() != n * groups)
             refuse(name, " must have ", n, " rows of ", groups, " scales (got ", shape_of(s), ")");
-        packed = {address(c), static_cast<float*>(address(s)), step_of(c, name, n, cols), step_of(s, name, n, groups),
+        packed = {address(c, use), static_cast<float*>(address(s, use)), step_of(c, name, n, cols), step_of(s, name, n, groups),
                   static_cast<int32_t>(g < -1 || g > 1 << 30 ? -1 : g), type == at::kChar ? LIONCUB_CODES_INT8 : LIONCUB_CODES_E4M3};
         p = &packed;
     }
@@ -182,14 +186,14 @@ private:
 struct Either {
     Matrix m;
     PackedMatrix c;
-    Either(PyObject* o, const char* name, int64_t n, int64_t cols, int64_t device)
+    Either(PyObject* o, const char* name, int64_t n, int64_t cols, int64_t device, Use use = kRead)
     {
         if (o == Py_None)
             return;
         if (THPVariable_Check(o))
-            fill(m, Matrix(o, name, n, cols, device));
+            fill(m, Matrix(o, name, n, cols, device, use));
         else
-            fill(c, PackedMatrix(o, name, n, cols, device));
+            fill(c, PackedMatrix(o, name, n, cols, device, use));
     }
 
 private:
@@ -205,7 +209,7 @@ private:
     }
 };
 
-float* vector(PyObject* o, const char* name, int64_t n, int64_t device)
+float* vector(PyObject* o, const char* name, int64_t n, int64_t device, Use use)
 {
     if (o == Py_None)
         return nullptr;
@@ -213,7 +217,7 @@ float* vector(PyObject* o, const char* name, int64_t n, int64_t device)
     if (t.scalar_type() != at::kFloat || !on_device(t, device) || t.numel() != n || !t.is_contiguous())
         refuse(name, " must be a contiguous float32 tensor of ", n, " elements on cuda:", device);
     check_gradient(t, name);
-    return static_cast<float*>(address(t));
+    return static_cast<float*>(address(t, use));
 }
 
 int64_t integer(PyObject* o)
@@ -291,10 +295,10 @@ PyObject* rms_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t count)
         const auto h = pointer<lioncub_rms_norm_t>(a[0]);
         const int64_t D = integer(a[1]), dev = integer(a[2]), n = rows_of(a[3], "x", D);
         const Matrix x(a[3], "x", n, D, dev), residual(a[4], "residual", n, D, dev), weight(a[5], "weight", 1, D, dev),
-            summed(a[6], "summed", n, D, dev);
-        const PackedMatrix saved(a[7], "saved", n, D, dev);
-        float* const rstd = vector(a[8], "rstd", n, dev);
-        const Either out(a[9], "out", n, D, dev);
+            summed(a[6], "summed", n, D, dev, kWrite);
+        const PackedMatrix saved(a[7], "saved", n, D, dev, kWrite);
+        float* const rstd = vector(a[8], "rstd", n, dev, kWrite);
+        const Either out(a[9], "out", n, D, dev, kWrite);
         const auto stream = pointer<lioncub_stream_t>(a[10]);
         return code_of([&] {
             return lib.rms_norm_forward(h, n, x.p, residual.p, weight.p, summed.p, saved.p, rstd, out.m.p, out.c.p, stream);
@@ -310,9 +314,10 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count)
         const int64_t D = integer(a[1]), dev = integer(a[2]), n = rows_of(a[3], "dout", D);
         const Matrix dout(a[3], "dout", n, D, dev);
         const Either saved(a[4], "saved", n, D, dev);
-        const float* const rstd = vector(a[5], "rstd", n, dev);
-        const Matrix weight(a[6], "weight", 1, D, dev), residual_grad(a[7], "residual_grad", n, D, dev), dx(a[8], "out", n, D, dev),
-            base(a[9], "weight_base", 1, D, dev), grad(a[10], "weight_grad", 1, D, dev), again(a[11], "again", n, D, dev);
+        const float* const rstd = vector(a[5], "rstd", n, dev, kRead);
+        const Matrix weight(a[6], "weight", 1, D, dev), residual_grad(a[7], "residual_grad", n, D, dev),
+            dx(a[8], "out", n, D, dev, kWrite), base(a[9], "weight_base", 1, D, dev), grad(a[10], "weight_grad", 1, D, dev, kWrite),
+            again(a[11], "again", n, D, dev, kWrite);
         const auto stream = pointer<lioncub_stream_t>(a[12]);
         return code_of([&] {
             return lib.rms_norm_backward(h, n, dout.p, saved.m.p, saved.c.p, rstd, weight.p, residual_grad.p, dx.p, base.p, grad.p, again.p,
@@ -328,7 +333,7 @@ PyObject* pack8(PyObject*, PyObject* const* a, Py_ssize_t count)
         const int64_t dev = integer(a[0]);
         const Size size(tensor(a[1], "x"), "x", dev);
         const Matrix x(a[1], "x", size.n, size.cols, dev);
-        const PackedMatrix out(a[2], "out", size.n, size.cols, dev);
+        const PackedMatrix out(a[2], "out", size.n, size.cols, dev, kWrite);
         const auto stream = pointer<lioncub_stream_t>(a[3]);
         return code_of([&] { return lib.pack8(size.n, size.cols, x.p, out.p, stream); });
     });
@@ -341,7 +346,7 @@ PyObject* unpack8(PyObject*, PyObject* const* a, Py_ssize_t count)
         const int64_t dev = integer(a[0]);
         const Size size(tensor(a[1], "x"), "x", dev);
         const PackedMatrix x(a[2], "x", size.n, size.cols, dev);
-        const Matrix out(a[3], "out", size.n, size.cols, dev);
+        const Matrix out(a[3], "out", size.n, size.cols, dev, kWrite);
         const auto stream = pointer<lioncub_stream_t>(a[4]);
         return code_of([&] { return lib.unpack8(size.n, size.cols, x.p, out.p, stream); });
     });
@@ -353,11 +358,12 @@ PyObject* activation_forward(PyObject*, PyObject* const* a, Py_ssize_t count)
     return guarded("activation_forward", count, 8, [&] {
         const int64_t dev = integer(a[0]), kind = integer(a[1]);
         const Size size(tensor(a[2], "x"), "x", dev);
-        const Matrix x(a[2], "x", size.n, size.cols, dev), up(a[3], "up", size.n, size.cols, dev), out(a[4], "out", size.n, size.cols, dev);
-        const PackedMatrix saved(a[5], "saved", size.n, size.cols, dev), saved_up(a[6], "saved_up", size.n, size.cols, dev);
+        const int64_t n = size.n, cols = size.cols;
+        const Matrix x(a[2], "x", n, cols, dev), up(a[3], "up", n, cols, dev), out(a[4], "out", n, cols, dev, kWrite);
+        const PackedMatrix saved(a[5], "saved", n, cols, dev, kWrite), saved_up(a[6], "saved_up", n, cols, dev, kWrite);
         const auto stream = pointer<lioncub_stream_t>(a[7]);
         return code_of([&] {
-            return lib.activation_forward(size.n, size.cols, static_cast<int>(kind), x.p, up.p, out.p, saved.p, saved_up.p, stream);
+            return lib.activation_forward(n, cols, static_cast<int>(kind), x.p, up.p, out.p, saved.p, saved_up.p, stream);
         });
     });
 }
@@ -371,7 +377,7 @@ PyObject* activation_backward(PyObject*, PyObject* const* a, Py_ssize_t count)
         const int64_t n = size.n, cols = size.cols;
         const Matrix dout(a[2], "dout", n, cols, dev);
         const Either x(a[3], "x", n, cols, dev), up(a[4], "up", n, cols, dev);
-        const Matrix dx(a[5], "dx", n, cols, dev), dup(a[6], "dup", n, cols, dev), again(a[7], "again", n, cols, dev);
+        const Matrix dx(a[5], "dx", n, cols, dev, kWrite), dup(a[6], "dup", n, cols, dev, kWrite), again(a[7], "again", n, cols, dev, kWrite);
         const auto stream = pointer<lioncub_stream_t>(a[8]);
         return code_of([&] {
             return lib.activation_backward(n, cols, static_cast<int>(kind), dout.p, x.m.p, up.m.p, x.c.p, up.c.p, dx.p, dup.p, again.p, stream);
@@ -382,7 +388,7 @@ PyObject* activation_backward(PyObject*, PyObject* const* a, Py_ssize_t count)
 struct HeadsArgument {
     lioncub_heads heads;
     const lioncub_heads* p = nullptr;
-    HeadsArgument(PyObject* o, const char* name, int64_t batch, int64_t places, int64_t head_dim, int64_t device)
+    HeadsArgument(PyObject* o, const char* name, int64_t batch, int64_t places, int64_t head_dim, int64_t device, Use use = kRead)
     {
         if (o == Py_None)
             return;
@@ -395,7 +401,7 @@ struct HeadsArgument {
             refuse(name, ": the columns of a head must be contiguous");
         if (t.size(lead + 1) > INT32_MAX)
             refuse(name, " has too many heads");
-        heads = {address(t), lead ? t.stride(0) : 0, t.stride(lead), t.stride(lead + 1), static_cast<int32_t>(t.size(lead + 1)), type};
+        heads = {address(t, use), lead ? t.stride(0) : 0, t.stride(lead), t.stride(lead + 1), static_cast<int32_t>(t.size(lead + 1)), type};
         p = &heads;
     }
 };
@@ -410,8 +416,8 @@ PyObject* rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t count)
         if (first.dim() != 3 && first.dim() != 4)
             refuse("q must be (batch, places, heads, ", D, ") (got ", shape_of(first), ")");
         const int64_t batch = first.dim() == 4 ? first.size(0) : 1, places = first.size(first.dim() - 3);
-        const HeadsArgument q(a[3], "q", batch, places, D, dev), q_out(a[4], "q_out", batch, places, D, dev), k(a[5], "k", batch, places, D, dev),
-            k_out(a[6], "k_out", batch, places, D, dev);
+        const HeadsArgument q(a[3], "q", batch, places, D, dev), q_out(a[4], "q_out", batch, places, D, dev, kWrite),
+            k(a[5], "k", batch, places, D, dev), k_out(a[6], "k_out", batch, places, D, dev, kWrite);
         lioncub_sequences s = {nullptr, batch, places, integer(a[8]), LIONCUB_INDEX_I64, 0};
         if (a[7] != Py_None) {
             const at::Tensor& t = tensor(a[7], "positions");

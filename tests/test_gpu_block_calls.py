@@ -1,6 +1,6 @@
 """Calls of the block operators by tensors of many kinds: views whose rows lie
-apart and tensors that carry a tangent, and the norm's gradient without the
-weight's."""
+apart, tensors that carry a tangent and lazily cloned ones, and the norm's
+gradient without the weight's."""
 import numpy as np
 import pytest
 
@@ -116,6 +116,19 @@ def test_tensors_with_a_tangent_are_refused(ops, number):  # noqa: F811
                     call(**dual)
             call(**{**dual, name: forward_ad.unpack_dual(dual[name]).primal})
     call(**results, **inputs)
+
+
+@pytest.mark.parametrize("number", range(7))
+def test_lazily_cloned_results(ops, number):  # noqa: F811
+    """A result that shares its memory with another tensor until one of them is written: the other keeps its values."""
+    _, call, results, inputs = _calls(ops)[number]
+    call(**results, **inputs)
+    want = {k: t.clone() for k, t in results.items()}
+    for name, t in results.items():
+        other = torch.full(t.shape, 7.0, device="cuda").to(t.dtype)
+        mine = torch._lazy_clone(other)
+        call(**{**results, name: mine}, **inputs)
+        assert (other == 7).all() and torch.equal(mine, want[name]), name
 
 
 @pytest.mark.parametrize("n,D", DIMS + [(700, 771), (1000, 768)])
