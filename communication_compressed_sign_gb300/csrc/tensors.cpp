@@ -66,6 +66,8 @@ const at::Tensor& tensor(PyObject* o, const char* name)
     const at::Tensor& t = THPVariable_Unpack(o);
     if (t.layout() != at::kStrided)
         refuse(name, " must be a dense tensor");
+    if (t.is_neg())
+        refuse(name, " is a negated view, whose memory holds other numbers: pass resolve_neg() of it");
     return t;
 }
 

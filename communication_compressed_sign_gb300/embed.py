@@ -174,6 +174,8 @@ def _rows(t, name, nrows, cols, device):
         raise ValueError(f"{name} has a tangent (a forward-mode derivative), but results have none: pass its primal value")
     if not t.dim() or t.size(-1) != cols or t.numel() != nrows * cols:
         raise ValueError(f"{name} must have {nrows} rows of {cols} columns (got {tuple(t.shape)})")
+    if t.is_neg():
+        raise ValueError(f"{name} is a negated view, whose memory holds other numbers: pass resolve_neg() of it")
     if t.is_contiguous():
         return _pack_rows(t.data_ptr(), cols, kind, 0)
     return _pack_rows(t.data_ptr(), _step(t, name, nrows, cols), kind, 0)

@@ -27,3 +27,12 @@ def test_tensors_with_a_tangent_are_refused(em):
             em._rows(dual, "x", 4, 8, -1)
         assert em._rows(forward_ad.unpack_dual(dual).primal, "x", 4, 8, -1) == want
     assert em._rows(t, "x", 4, 8, -1) == want
+
+
+def test_negated_views_are_refused(em):
+    """Their memory holds other numbers than they do."""
+    t = torch.randn(4, 1, dtype=torch.complex64).conj().imag
+    assert t.is_neg()
+    with pytest.raises(ValueError, match="x is a negated view"):
+        em._rows(t, "x", 4, 1, -1)
+    assert em._rows(t.resolve_neg(), "x", 4, 1, -1)

@@ -1,6 +1,6 @@
 """Calls of the block operators by tensors of many kinds: views whose rows lie
-apart, tensors that carry a tangent and lazily cloned ones, and the norm's
-gradient without the weight's."""
+apart, tensors that carry a tangent, lazily cloned and negated ones, and the
+norm's gradient without the weight's."""
 import numpy as np
 import pytest
 
@@ -129,6 +129,16 @@ def test_lazily_cloned_results(ops, number):  # noqa: F811
         mine = torch._lazy_clone(other)
         call(**{**results, name: mine}, **inputs)
         assert (other == 7).all() and torch.equal(mine, want[name]), name
+
+
+@pytest.mark.parametrize("number", range(7))
+def test_negated_views_are_refused(ops, number):  # noqa: F811
+    """Their memory holds other numbers than they do."""
+    _, call, results, inputs = _calls(ops)[number]
+    for name, t in {**results, **inputs}.items():
+        if t.is_floating_point():
+            with pytest.raises(ValueError, match="negated"):
+                call(**{**results, **inputs, name: torch._neg_view(t)})
 
 
 @pytest.mark.parametrize("n,D", DIMS + [(700, 771), (1000, 768)])
