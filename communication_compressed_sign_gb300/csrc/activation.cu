@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation(const __gri
     const bool gated = KIND != kIdentity && a.up.data;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        vx[i].load(u.cols[i], a.x.data, u.row[i] * a.x.stride, a.x.type);
+        load_row(vx[i], u.cols[i], a.x, u.row[i]);
         if (gated)
-            vup[i].load(u.cols[i], a.up.data, u.row[i] * a.up.stride, a.up.type);
+            load_row(vup[i], u.cols[i], a.up, u.row[i]);
     }
     // codes of a chunk, number k of the shared scales (VEC)
     constexpr int N = KIND == kIdentity ? kUnits : 2 * kUnits;
@@ -167,11 +167,12 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation(const __gri
         if constexpr (VEC) {
             const Columns<VEC>& c = u.cols[i];
             const uint2 w = codes8(x, inv[k], inv[k] < 0.0f, p);
-            if (c.count)
+            if (c.count && inside(p, c, u.row[i]))
                 *reinterpret_cast<uint2*>(p.codes + u.row[i] * p.stride + c.at) = w;
             // lane k of a group has its scale, and columns or not
             const int64_t group = c.at >> p.log_group;
-            if ((lane & ((1 << (p.log_group - 3)) - 1)) == k && (LANES ? c.count != 0 : group << p.log_group < a.cols))
+            if ((lane & ((1 << (p.log_group - 3)) - 1)) == k && (LANES ? c.count != 0 : group << p.log_group < a.cols) &&
+                scale_inside(p, u.row[i], group))
                 p.scales[u.row[i] * p.scale_stride + group] = scale;
         }
     };
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation(const __gri
                 for (int k = 0; k < 4; ++k)
                     set_pair(x, k, mul2(pair_of(x, k), pair_of(y, k)));
             }
-            store_typed<VEC>(u.cols[i], a.out.data, u.row[i] * a.out.stride, a.out.type, x);
+            store_typed<VEC>(u.cols[i], a.out, u.row[i], x);
         }
     }
 }
@@ -246,15 +247,15 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation_grad(const 
     Saved vx[kUnits], vup[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        vd[i].load(u.cols[i], a.dout.data, u.row[i] * a.dout.stride, a.dout.type);
+        load_row(vd[i], u.cols[i], a.dout, u.row[i]);
         if constexpr (PACKED) {
             vx[i].load(a.saved, u.cols[i], u.row[i], lane);
             if (gated)
                 vup[i].load(a.saved_up, u.cols[i], u.row[i], lane);
         } else {
-            vx[i].load(u.cols[i], a.x.data, u.row[i] * a.x.stride, a.x.type);
+            load_row(vx[i], u.cols[i], a.x, u.row[i]);
             if (gated)
-                vup[i].load(u.cols[i], a.up.data, u.row[i] * a.up.stride, a.up.type);
+                load_row(vup[i], u.cols[i], a.up, u.row[i]);
         }
     }
 #pragma unroll
@@ -286,11 +287,11 @@ __global__ void __launch_bounds__(kBlock, kBlocks<VEC>) k_activation_grad(const 
             set_pair(y, k, f);
             set_pair(x, k, mul2(g, slope));
         }
-        store_typed<VEC>(u.cols[i], a.dx.data, u.row[i] * a.dx.stride, a.dx.type, x);
+        store_typed<VEC>(u.cols[i], a.dx, u.row[i], x);
         if (gated && a.dup.data)
-            store_typed<VEC>(u.cols[i], a.dup.data, u.row[i] * a.dup.stride, a.dup.type, dup);
+            store_typed<VEC>(u.cols[i], a.dup, u.row[i], dup);
         if (a.again.data)
-            store_typed<VEC>(u.cols[i], a.again.data, u.row[i] * a.again.stride, a.again.type, y);
+            store_typed<VEC>(u.cols[i], a.again, u.row[i], y);
     }
 }
 
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kBlock) k_unpack(const PackedRows x, const Typ
     for (int i = 0; i < kUnits; ++i) {
         float y[8];
         v[i].unpack(x, y);
-        store_typed<VEC>(u.cols[i], out.data, u.row[i] * out.stride, out.type, y);
+        store_typed<VEC>(u.cols[i], out, u.row[i], y);
     }
 }
 
@@ -404,6 +405,10 @@ cudaError_t backward_p(const ActivationArgs& a, int kind, bool vec, cudaStream_t
 }
 
 }  // namespace
+
+#ifdef LIONCUB_BOUNDS_CHECK
+cudaError_t take_activation_word(int* word) { return take_word(word); }
+#endif
 
 cudaError_t launch_activation(const ActivationArgs& a, int kind, bool vec, cudaStream_t s)
 {

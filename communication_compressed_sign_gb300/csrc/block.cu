@@ -203,12 +203,31 @@ private:
     }
 };
 
-lc::TypedRows typed(const lioncub_rows* m)
+// As many rows of matrices as a checked build's kernels may touch: fewer than there are by
+// LIONCUB_CHECKED_ROWS, to see that the checks find what lies beyond.
+[[maybe_unused]] int64_t checked_rows(int64_t rows)
 {
-    return m ? lc::TypedRows{m->data, m->stride, m->type} : lc::TypedRows{nullptr, 0, LIONCUB_ROWS_BF16};
+    const int64_t most = lc::env_index("LIONCUB_CHECKED_ROWS");
+    return most ? std::min(most, rows) : rows;
 }
 
-lc::PackedRows packed(const lioncub_packed* m, int64_t cols)
+lc::TypedRows typed(const lioncub_rows* m, [[maybe_unused]] int64_t rows, [[maybe_unused]] int64_t cols)
+{
+    lc::TypedRows t = {};
+    t.type = LIONCUB_ROWS_BF16;
+    if (!m)
+        return t;
+    t.data = m->data;
+    t.stride = m->stride;
+    t.type = m->type;
+#ifdef LIONCUB_BOUNDS_CHECK
+    t.rows = checked_rows(rows);
+    t.cols = cols;
+#endif
+    return t;
+}
+
+lc::PackedRows packed(const lioncub_packed* m, [[maybe_unused]] int64_t rows, int64_t cols)
 {
     if (!m)
         return lc::PackedRows{};
@@ -216,7 +235,11 @@ lc::PackedRows packed(const lioncub_packed* m, int64_t cols)
     for (int k = 5; k <= 8; ++k)
         if (m->group == 1 << k)
             log_group = k;
-    return lc::PackedRows{static_cast<uint8_t*>(m->codes), m->scales, m->stride, m->scale_stride, cols, log_group, m->format == LIONCUB_CODES_E4M3, 1.0f};
+    lc::PackedRows p = {static_cast<uint8_t*>(m->codes), m->scales, m->stride, m->scale_stride, cols, log_group, m->format == LIONCUB_CODES_E4M3, 1.0f};
+#ifdef LIONCUB_BOUNDS_CHECK
+    p.rows = checked_rows(rows);
+#endif
+    return p;
 }
 
 // Matrices whose rows follow one another are one long row to the kernels that
@@ -380,9 +403,17 @@ int check_positions(const char* name, const lioncub_heads& m, const lioncub_sequ
     return LIONCUB_OK;
 }
 
-lc::HeadsArgs heads_of(const lioncub_heads& in, const lioncub_heads& out)
+lc::HeadsArgs heads_of(const lioncub_heads& in, const lioncub_heads& out, [[maybe_unused]] const lioncub_sequences& p,
+                       [[maybe_unused]] int64_t head_dim)
 {
-    return {in.data, out.data, in.batch_stride, in.place_stride, in.head_stride, out.batch_stride, out.place_stride, out.head_stride};
+    lc::HeadsArgs a = {in.data, out.data, in.batch_stride, in.place_stride, in.head_stride, out.batch_stride, out.place_stride, out.head_stride};
+#ifdef LIONCUB_BOUNDS_CHECK
+    lioncub_sequences some = p;
+    some.seq_len = checked_rows(p.seq_len);
+    a.in_end = static_cast<const char*>(in.data) + extent(box_of(in, some, head_dim), kAnyOrder, 0);
+    a.out_end = static_cast<const char*>(out.data) + extent(box_of(out, some, head_dim), kAnyOrder, 0);
+#endif
+    return a;
 }
 
 }  // namespace
@@ -390,6 +421,22 @@ lc::HeadsArgs heads_of(const lioncub_heads& in, const lioncub_heads& out)
 extern "C" {
 
 const char* lioncub_block_last_error(void) { return t_error; }
+
+#ifdef LIONCUB_BOUNDS_CHECK
+// Only in checked builds: what the kernels recorded since the last call; synchronizes.
+LIONCUB_API int lioncub_block_checked_word(int32_t* word)
+{
+    *word = 0;
+    for (const auto take : {lc::take_norm_word, lc::take_norm_grad_word, lc::take_activation_word, lc::take_rotary_word}) {
+        int one = 0;
+        const cudaError_t e = take(&one);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "checked word");
+        *word |= one;
+    }
+    return LIONCUB_OK;
+}
+#endif
 
 // ---- the norm ---------------------------------------------------------------------------
 
@@ -490,13 +537,13 @@ int lioncub_rms_norm_forward(lioncub_rms_norm_t h, int64_t n, const lioncub_rows
     if (rc != LIONCUB_OK)
         return rc;
     lc::NormArgs a{};
-    a.x = typed(x);
-    a.residual = typed(residual);
-    a.weight = typed(weight);
-    a.summed = typed(summed);
-    a.out = typed(out);
-    a.saved = packed(saved, h->dim);
-    a.packed = packed(packed_out, h->dim);
+    a.x = typed(x, n, h->dim);
+    a.residual = typed(residual, n, h->dim);
+    a.weight = typed(weight, 1, h->dim);
+    a.summed = typed(summed, n, h->dim);
+    a.out = typed(out, n, h->dim);
+    a.saved = packed(saved, n, h->dim);
+    a.packed = packed(packed_out, n, h->dim);
     a.rstd = rstd;
     a.n = n;
     a.dim = static_cast<int32_t>(h->dim);
@@ -544,13 +591,13 @@ int lioncub_rms_norm_backward(lioncub_rms_norm_t h, int64_t n, const lioncub_row
     if (rc != LIONCUB_OK)
         return rc;
     lc::NormGradArgs a{};
-    a.dout = typed(dout);
-    a.saved = typed(saved);
-    a.residual_grad = typed(residual_grad);
-    a.dx = typed(dx);
-    a.weight = typed(weight);
-    a.again = typed(again);
-    a.packed = packed(packed_saved, h->dim);
+    a.dout = typed(dout, n, h->dim);
+    a.saved = typed(saved, n, h->dim);
+    a.residual_grad = typed(residual_grad, n, h->dim);
+    a.dx = typed(dx, n, h->dim);
+    a.weight = typed(weight, 1, h->dim);
+    a.again = typed(again, n, h->dim);
+    a.packed = packed(packed_saved, n, h->dim);
     a.rstd = rstd;
     a.partial = weight_grad ? h->partial : nullptr;
     a.partial_rows = h->multiprocessors;
@@ -567,8 +614,8 @@ int lioncub_rms_norm_backward(lioncub_rms_norm_t h, int64_t n, const lioncub_row
     lc::WeightGradArgs w{};
     w.partial = h->partial;
     w.rows = blocks;
-    w.base = typed(weight_base);
-    w.grad = typed(weight_grad);
+    w.base = typed(weight_base, 1, h->dim);
+    w.grad = typed(weight_grad, 1, h->dim);
     w.dim = a.dim;
     return finish_launch(launch(h, "rms_norm_weight_grad", [&] { return lc::launch_weight_grad(w, stream); }), "weight gradient launch");
 }
@@ -592,12 +639,12 @@ int lioncub_pack8(int64_t rows, int64_t cols, const lioncub_rows* x, const lionc
     if (rows == 0 || cols == 0)
         return LIONCUB_OK;
     if (out->group == 0)
-        return finish_launch(lc::launch_pack_rows(typed(x), packed(out, cols), rows, static_cast<int>(cols), o.vec && cols % 8 == 0, stream),
+        return finish_launch(lc::launch_pack_rows(typed(x, rows, cols), packed(out, rows, cols), rows, static_cast<int>(cols), o.vec && cols % 8 == 0, stream),
                              "pack launch");
     lc::ActivationArgs a{};
     const bool vec = as_one_row(o, rows, cols);
-    a.x = typed(x);
-    a.saved = packed(out, cols);
+    a.x = typed(x, rows, cols);
+    a.saved = packed(out, rows, cols);
     a.rows = rows;
     a.cols = cols;
     return finish_launch(lc::launch_activation(a, lc::kIdentity, vec, stream), "pack launch");
@@ -616,7 +663,7 @@ int lioncub_unpack8(int64_t rows, int64_t cols, const lioncub_packed* x, const l
     if (rc != LIONCUB_OK)
         return rc;
     const bool vec = as_one_row(o, rows, cols);
-    return finish_launch(lc::launch_unpack(packed(x, cols), typed(out), rows, cols, vec, stream), "unpack launch");
+    return finish_launch(lc::launch_unpack(packed(x, rows, cols), typed(out, rows, cols), rows, cols, vec, stream), "unpack launch");
 }
 
 // ---- the activation --------------------------------------------------------------------------
@@ -650,11 +697,11 @@ int lioncub_activation_forward(int64_t rows, int64_t cols, int kind, const lionc
         return rc;
     lc::ActivationArgs a{};
     const bool vec = as_one_row(o, rows, cols);
-    a.x = typed(x);
-    a.up = typed(up);
-    a.out = typed(out);
-    a.saved = packed(saved, cols);
-    a.saved_up = packed(saved_up, cols);
+    a.x = typed(x, rows, cols);
+    a.up = typed(up, rows, cols);
+    a.out = typed(out, rows, cols);
+    a.saved = packed(saved, rows, cols);
+    a.saved_up = packed(saved_up, rows, cols);
     a.rows = rows;
     a.cols = cols;
     return finish_launch(lc::launch_activation(a, kind, vec, stream), "activation launch");
@@ -692,14 +739,14 @@ int lioncub_activation_backward(int64_t rows, int64_t cols, int kind, const lion
         return rc;
     lc::ActivationArgs a{};
     const bool vec = as_one_row(o, rows, cols);
-    a.dout = typed(dout);
-    a.x = typed(x);
-    a.up = typed(up);
-    a.saved = packed(packed_x, cols);
-    a.saved_up = packed(packed_up, cols);
-    a.dx = typed(dx);
-    a.dup = typed(dup);
-    a.again = typed(again);
+    a.dout = typed(dout, rows, cols);
+    a.x = typed(x, rows, cols);
+    a.up = typed(up, rows, cols);
+    a.saved = packed(packed_x, rows, cols);
+    a.saved_up = packed(packed_up, rows, cols);
+    a.dx = typed(dx, rows, cols);
+    a.dup = typed(dup, rows, cols);
+    a.again = typed(again, rows, cols);
     a.rows = rows;
     a.cols = cols;
     return finish_launch(lc::launch_activation_grad(a, kind, vec, stream), "activation gradient launch");
@@ -842,10 +889,10 @@ int lioncub_rotary_apply(lioncub_rotary_t h, const lioncub_sequences* places, co
     if (rc != LIONCUB_OK)
         return rc;
     lc::RotaryArgs a{};
-    a.side[0] = heads_of(*q, *q_out);
+    a.side[0] = heads_of(*q, *q_out, p, h->head_dim);
     a.heads[0] = q->heads;
     if (k) {
-        a.side[1] = heads_of(*k, *k_out);
+        a.side[1] = heads_of(*k, *k_out, p, h->head_dim);
         a.heads[1] = k->heads;
     }
     a.turns = h->turns;

@@ -13,6 +13,9 @@ struct TypedRows {
     void* data;
     int64_t stride;
     int32_t type;
+#ifdef LIONCUB_BOUNDS_CHECK
+    int64_t rows, cols;
+#endif
 };
 
 // A matrix in 8 bits; codes may be null.  Groups are 1 << log_group columns, or
@@ -26,6 +29,9 @@ struct PackedRows {
     int32_t log_group;
     int32_t e4m3;  // else whole numbers
     float one;     // 1 (see codes8)
+#ifdef LIONCUB_BOUNDS_CHECK
+    int64_t rows;
+#endif
 };
 
 struct NormArgs {
@@ -73,6 +79,9 @@ struct HeadsArgs {
     const void* in;
     void* out;
     int64_t in_batch, in_place, in_head, out_batch, out_place, out_head;
+#ifdef LIONCUB_BOUNDS_CHECK
+    const char *in_end, *out_end;
+#endif
 };
 
 struct RotaryArgs {
@@ -105,5 +114,14 @@ cudaError_t launch_unpack(const PackedRows& x, const TypedRows& out, int64_t row
 // move: elements at a time, 8 (then 16-byte aligned, and whole halves of 8 pairs), 4, 2 or 1.
 // copy_by_four: columns that are copied may be moved four at a time.
 cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, int move, bool copy_by_four, cudaStream_t s);
+
+#ifdef LIONCUB_BOUNDS_CHECK
+// Checked builds: each file of kernels has a word that they set bits of (kStatusOutOfBounds)
+// for an access that lies outside, which is left out.  Reads and clears it; synchronizes.
+cudaError_t take_norm_word(int* word);
+cudaError_t take_norm_grad_word(int* word);
+cudaError_t take_activation_word(int* word);
+cudaError_t take_rotary_word(int* word);
+#endif
 
 }  // namespace lc

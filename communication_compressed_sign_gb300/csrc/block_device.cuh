@@ -33,7 +33,76 @@ struct Columns {
         else
             count = left <= 0 ? 0 : left > 224 ? 8 : static_cast<int>((left + 31) >> 5);
     }
+    __device__ __forceinline__ int64_t last() const { return VEC ? at + 7 : at + 32 * (count - 1); }
+    __device__ __forceinline__ Columns none() const
+    {
+        Columns c = *this;
+        c.count = 0;
+        c.whole = false;
+        return c;
+    }
 };
+
+// --- checked builds ----------------------------------------------------------------------
+//
+// With -DLIONCUB_BOUNDS_CHECK the rows, columns, groups and moves of every access, of
+// memory and of rings in shared memory, are compared with the matrices' sizes; one
+// that lies outside is recorded and left out.  Elsewhere all of this is true and gone.
+#ifdef LIONCUB_BOUNDS_CHECK
+namespace {
+__device__ int t_word;
+
+cudaError_t take_word(int* word)
+{
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess)
+        e = cudaMemcpyFromSymbol(word, t_word, sizeof *word);
+    const int none = 0;
+    return e == cudaSuccess ? cudaMemcpyToSymbol(t_word, &none, sizeof none) : e;
+}
+}  // namespace
+#endif
+
+__device__ __forceinline__ bool access_ok(bool ok)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    return index_ok(&t_word, ok);
+#else
+    return true;
+#endif
+}
+
+// A lane's columns of a row.
+template <bool VEC>
+__device__ __forceinline__ bool inside(const TypedRows& m, const Columns<VEC>& c, int64_t row)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    const int64_t size = m.type == LIONCUB_ROWS_BF16 ? 2 : 4;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(m.data) + (row * m.stride + c.at) * size;
+    return !c.count || access_ok(row >= 0 && row < m.rows && c.at >= 0 && c.last() < m.cols && at % (VEC ? 16 : size) == 0);
+#else
+    return true;
+#endif
+}
+// The same of codes.
+template <bool VEC>
+__device__ __forceinline__ bool inside(const PackedRows& p, const Columns<VEC>& c, int64_t row)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.codes) + row * p.stride + c.at;
+    return !c.count || access_ok(row >= 0 && row < p.rows && c.at >= 0 && c.last() < p.cols && at % (VEC ? 8 : 1) == 0);
+#else
+    return true;
+#endif
+}
+__device__ __forceinline__ bool scale_inside(const PackedRows& p, int64_t row, int64_t group)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    return access_ok(row >= 0 && row < p.rows && group >= 0 && group <= (p.cols - 1) >> p.log_group);
+#else
+    return true;
+#endif
+}
 
 // --- fp32 pairs ---------------------------------------------------------------------------
 //
@@ -193,17 +262,24 @@ struct Chunk<T, false> {
     __device__ __forceinline__ uint32_t largest() const { return 0; }  // not used
 };
 
+// A lane's columns of a row of a matrix.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_row(Chunk<T, VEC>& v, const Columns<VEC>& c, const TypedRows& m, int64_t row)
+{
+    v.load(inside(m, c, row) ? c : c.none(), m.data, row * m.stride, m.type);
+}
+
 // Loads and stores of a type that the launch gives.
 template <bool VEC>
-__device__ __forceinline__ void load_typed(const Columns<VEC>& c, const void* base, int64_t e, int type, float (&x)[8])
+__device__ __forceinline__ void load_typed(const Columns<VEC>& c, const TypedRows& m, int64_t row, float (&x)[8])
 {
-    if (VEC && type == LIONCUB_ROWS_F32) {
+    if (VEC && m.type == LIONCUB_ROWS_F32) {
         Chunk<float, VEC> v;
-        v.load(c, base, e, type);
+        load_row(v, c, m, row);
         v.unpack(x);
     } else {
         Chunk<__nv_bfloat16, VEC> v;
-        v.load(c, base, e, type);
+        load_row(v, c, m, row);
         v.unpack(x);
     }
 }
@@ -221,17 +297,20 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8])
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store_typed(const Columns<VEC>& c, void* base, int64_t e, int type, const float (&x)[8])
+__device__ __forceinline__ void store_typed(const Columns<VEC>& c, const TypedRows& m, int64_t row, const float (&x)[8])
 {
+    if (!inside(m, c, row))
+        return;
+    const int64_t e = row * m.stride;
     if constexpr (VEC) {
         if (!c.count)
             return;
-        if (type == LIONCUB_ROWS_BF16) {
+        if (m.type == LIONCUB_ROWS_BF16) {
             Group8<__nv_bfloat16> g;
             g.pack(x);
-            g.store(base, e + c.at);
+            g.store(m.data, e + c.at);
         } else {
-            store8(static_cast<float*>(base) + e + c.at, x);
+            store8(static_cast<float*>(m.data) + e + c.at, x);
         }
     } else {
         const auto store = [&](auto* p) {
@@ -247,10 +326,10 @@ __device__ __forceinline__ void store_typed(const Columns<VEC>& c, void* base, i
                         p[32 * k] = static_cast<E>(x[k]);
             }
         };
-        if (type == LIONCUB_ROWS_BF16)
-            store(static_cast<__nv_bfloat16*>(base) + e + c.at);
+        if (m.type == LIONCUB_ROWS_BF16)
+            store(static_cast<__nv_bfloat16*>(m.data) + e + c.at);
         else
-            store(static_cast<float*>(base) + e + c.at);
+            store(static_cast<float*>(m.data) + e + c.at);
     }
 }
 
@@ -369,9 +448,9 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
         const int log_lanes = p.log_group - 3;  // of a group
         const GroupScale s(lanes_max(largest, log_lanes), e4m3);
         const uint2 w = codes8(x, s.inv, s.bad, p);
-        if (c.count) {
+        if (c.count && inside(p, c, row)) {
             *reinterpret_cast<uint2*>(codes) = w;
-            if ((lane & ((1 << log_lanes) - 1)) == 0)
+            if ((lane & ((1 << log_lanes) - 1)) == 0 && scale_inside(p, row, c.at >> p.log_group))
                 scales[c.at >> p.log_group] = s.scale;
         }
     } else {
@@ -391,9 +470,10 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
             }
             const GroupScale s(m, e4m3);
             const int64_t at = c.at - lane + 32 * kDeep * mine;  // the group's first column
-            if (lane < kGroups && at < p.cols)
+            if (lane < kGroups && at < p.cols && scale_inside(p, row, at >> p.log_group))
                 scales[at >> p.log_group] = s.scale;
-            if (c.whole && !__any_sync(kAll, s.bad)) {
+            const bool ok = inside(p, c, row);
+            if (c.whole && (!kBoundsCheck || __all_sync(kAll, ok)) && !__any_sync(kAll, s.bad)) {
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     const float inv = __shfl_sync(kAll, s.inv, g);
@@ -418,7 +498,7 @@ __device__ __forceinline__ void pack_chunk(const PackedRows& p, const Columns<VE
                     const bool none = __shfl_sync(kAll, s.bad, g);
 #pragma unroll
                     for (int k = g * kDeep; k < (g + 1) * kDeep; ++k)
-                        if (k < c.count) {
+                        if (k < c.count && ok) {
                             uint32_t code, unused;
                             codes2(make_float2(x[k], 0.0f), inv, p, code, unused);
                             codes[32 * k] = none ? 0 : static_cast<uint8_t>(code);
@@ -441,6 +521,8 @@ __device__ __forceinline__ void pack_chunk_of_row(const PackedRows& p, const Col
                                                   const GroupScale& s)
 {
     uint8_t* codes = p.codes + row * p.stride + c.at;
+    if (!inside(p, c, row))
+        return;
     if constexpr (VEC) {
         if (c.count)
             *reinterpret_cast<uint2*>(codes) = codes8(x, s.inv, s.bad, p);
@@ -475,7 +557,7 @@ struct CodeChunk<true> {
     {
         w = make_uint2(0, 0);
         scale = 0.0f;
-        if (c.count) {
+        if (c.count && inside(p, c, row) && scale_inside(p, row, c.at >> p.log_group)) {
             w = *reinterpret_cast<const uint2*>(p.codes + row * p.stride + c.at);
             scale = p.scales[row * p.scale_stride + (c.at >> p.log_group)];
         }
@@ -491,15 +573,16 @@ struct CodeChunk<false> {
     {
         const uint8_t* codes = p.codes + row * p.stride + c.at;
         const int64_t at = c.at - lane + 32 * (lane & 7);
-        scale = at < p.cols ? p.scales[row * p.scale_stride + (at >> p.log_group)] : 0.0f;
-        if (c.whole) {
+        scale = at < p.cols && scale_inside(p, row, at >> p.log_group) ? p.scales[row * p.scale_stride + (at >> p.log_group)] : 0.0f;
+        const bool ok = inside(p, c, row);
+        if (c.whole && ok) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 code[k] = codes[32 * k];
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                code[k] = k < c.count ? codes[32 * k] : 0;
+                code[k] = k < c.count && ok ? codes[32 * k] : 0;
         }
     }
     __device__ __forceinline__ void unpack(const PackedRows& p, float (&y)[8]) const

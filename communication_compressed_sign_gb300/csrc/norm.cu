@@ -64,7 +64,7 @@ __device__ __forceinline__ void pack_row(const PackedRows& p, const Columns<VEC>
 #pragma unroll
     for (int c = 0; c < C; ++c)
         pack_chunk_of_row<VEC>(p, cols[c], row, x[c], s);
-    if (warp == 0 && lane == 0)
+    if (warp == 0 && lane == 0 && scale_inside(p, row, 0))
         p.scales[row * p.scale_stride] = s.scale;
 }
 
@@ -92,12 +92,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, C <= 2 ? 3 : 2) k_norm(const _
         Chunk<XT, VEC> x[C];
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            x[c].load(cols[c], a.x.data, row * a.x.stride, a.x.type);
+            load_row(x[c], cols[c], a.x, row);
         if (a.residual.data) {
             Chunk<RT, VEC> r[C];
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                r[c].load(cols[c], a.residual.data, row * a.residual.stride, a.residual.type);
+                load_row(r[c], cols[c], a.residual, row);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 float y[8];
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, C <= 2 ? 3 : 2) k_norm(const _
     if (a.summed.data)
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            store_typed<VEC>(cols[c], a.summed.data, row * a.summed.stride, a.summed.type, h[c]);
+            store_typed<VEC>(cols[c], a.summed, row, h[c]);
 
     float2 squares = both(0.0f);
 #pragma unroll
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, C <= 2 ? 3 : 2) k_norm(const _
     float sum = __fadd_rn(squares.x, squares.y);
     sum = row_sum(sum, sums, warps, warp, lane);
     const float rstd = rsqrtf(fmaf(sum, a.per_column, a.eps));
-    if (a.rstd && warp == 0 && lane == 0)
+    if (a.rstd && warp == 0 && lane == 0 && access_ok(row < a.n))
         a.rstd[row] = rstd;
     if (a.saved.codes)
         pack_row<C, VEC>(a.saved, cols, row, h, maxima[0], warps, warp, lane);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, C <= 2 ? 3 : 2) k_norm(const _
             set_pair(h[c], k, mul2(pair_of(h[c], k), both(rstd)));
         if (a.weight.data) {
             float w[8];
-            load_typed<VEC>(cols[c], a.weight.data, 0, a.weight.type, w);
+            load_typed<VEC>(cols[c], a.weight, 0, w);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 set_pair(h[c], k, mul2(pair_of(h[c], k), pair_of(w, k)));
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, C <= 2 ? 3 : 2) k_norm(const _
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            store_typed<VEC>(cols[c], a.out.data, row * a.out.stride, a.out.type, h[c]);
+            store_typed<VEC>(cols[c], a.out, row, h[c]);
     }
 }
 
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) k_pack_rows(const TypedRows x,
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         cols[c] = Columns<VEC>((warp * C + c) * kChunk, lane, dim);
-        v[c].load(cols[c], x.data, row * x.stride, x.type);
+        load_row(v[c], cols[c], x, row);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -223,6 +223,10 @@ cudaError_t launch_t(const NormArgs& a, int c, cudaStream_t s)
 }
 
 }  // namespace
+
+#ifdef LIONCUB_BOUNDS_CHECK
+cudaError_t take_norm_word(int* word) { return take_word(word); }
+#endif
 
 cudaError_t launch_norm(NormArgs a, bool vec, cudaStream_t s)
 {

@@ -80,6 +80,53 @@ struct Stream {
     int32_t at;
 };
 
+#ifdef LIONCUB_BOUNDS_CHECK
+// Where the room of a matrix ends in a slot.
+__device__ __forceinline__ int32_t room_end(const NormGradArgs& a, const Stream& m)
+{
+    return m.at == 0 ? a.at_saved : m.at == a.at_saved ? a.at_residual : a.slot_bytes;
+}
+__device__ __forceinline__ uint32_t ring_bytes()
+{
+    uint32_t n;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+    return n;
+}
+#endif
+
+// Checked builds: whether the bytes [begin, end) of a slot are in the room of a matrix there.
+__device__ __forceinline__ bool room_ok(const NormGradArgs& a, const Stream& m, const char* slot, int64_t begin, int64_t end)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    extern __shared__ __align__(16) char shared[];
+    const int64_t at = slot - shared;
+    return access_ok(begin >= m.at && begin <= end && end <= room_end(a, m) && at >= 0 && at % a.slot_bytes == 0 && at + end <= ring_bytes());
+#else
+    return true;
+#endif
+}
+
+// Checked builds: whether a row is one of a matrix, and whether a copy starts and ends at
+// 16-byte boundaries, between the first and the last of its elements.
+__device__ __forceinline__ bool row_ok(const NormGradArgs& a, const Stream& m, int64_t row)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    const int64_t rows = m.at == 0 ? a.dout.rows : m.at != a.at_saved ? a.residual_grad.rows : a.packed.codes ? a.packed.rows : a.saved.rows;
+    return access_ok(row >= 0 && row < rows && row < a.n);
+#else
+    return true;
+#endif
+}
+__device__ __forceinline__ bool copy_ok(const NormGradArgs& a, const Stream& m, const char* from, const char* to, uint32_t bytes)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    return access_ok(((reinterpret_cast<uintptr_t>(from) | shared_address(to) | bytes) & 15) == 0 && from >= m.base &&
+                     from + bytes <= m.base + (a.n - 1) * m.step + m.bytes);
+#else
+    return true;
+#endif
+}
+
 // The slot of a row that starts `shift` bytes behind a boundary has it `shift`
 // bytes behind its own start.
 __device__ __forceinline__ uint32_t shift_of(const Stream& m, int64_t row)
@@ -106,7 +153,7 @@ struct Window {
 
 // One thread for each stream: starts the copy of its row i into a slot.
 template <bool VEC>
-__device__ __forceinline__ void start_row(const Stream& m, int64_t i, int64_t n, char* slot, uint32_t barrier)
+__device__ __forceinline__ void start_row(const NormGradArgs& a, const Stream& m, int64_t i, char* slot, uint32_t barrier)
 {
     const char* from = m.base + i * m.step;
     uint32_t bytes = m.bytes;
@@ -114,18 +161,22 @@ __device__ __forceinline__ void start_row(const Stream& m, int64_t i, int64_t n,
     // what was read and written in the slot by ordinary accesses comes before the copy
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if constexpr (!VEC) {
-        const Window w(m, i, n);
+        const Window w(m, i, a.n);
         to += shift_of(m, i);
         // what lies outside, in the first and the last rows
         const char* end = w.row + m.bytes;
-        for (const char* p = w.row; p < w.from && p < end; ++p)
-            to[p - w.row] = *p;
-        for (const char* p = w.to > w.row ? w.to : w.row; p < end; ++p)
-            to[p - w.row] = *p;
+        if (row_ok(a, m, i) && room_ok(a, m, slot, to - slot, to - slot + m.bytes)) {
+            for (const char* p = w.row; p < w.from && p < end; ++p)
+                to[p - w.row] = *p;
+            for (const char* p = w.to > w.row ? w.to : w.row; p < end; ++p)
+                to[p - w.row] = *p;
+        }
         to += w.from - w.row;
         from = w.from;
         bytes = w.bytes();
     }
+    if (bytes && !(row_ok(a, m, i) && room_ok(a, m, slot, to - slot, to - slot + bytes) && copy_ok(a, m, from, to, bytes)))
+        bytes = 0;
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(barrier), "r"(bytes) : "memory");
     if (bytes)
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(shared_address(to)),
@@ -162,11 +213,21 @@ __device__ __forceinline__ void read_codes(CodeChunk<VEC>& v, const Columns<VEC>
     }
 }
 
+// Checked builds: whether a column of a team has a place among the block's sums.
+__device__ __forceinline__ bool sums_ok(const NormGradArgs& a, int team, int64_t column)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    return access_ok(team < a.teams && column < a.dim && (int64_t(team) * a.dim + column + 1) * int64_t(sizeof(float)) <= ring_bytes());
+#else
+    return true;
+#endif
+}
+
 template <bool VEC>
 __device__ __forceinline__ void load_weight(const NormGradArgs& a, const Columns<VEC>& c, float (&w)[8])
 {
     if (a.weight.data) {
-        load_typed<VEC>(c, a.weight.data, 0, a.weight.type, w);
+        load_typed<VEC>(c, a.weight, 0, w);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -217,19 +278,19 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
     uint32_t started = 0, last_parity = 0;  // of the slots, a bit each
     if (starts)
         for (int k = 0; k < a.slots && row + k * step < a.n; ++k) {
-            start_row<VEC>(mine, row + k * step, a.n, ring + k * a.slot_bytes, full + 8 * k);
+            start_row<VEC>(a, mine, row + k * step, ring + k * a.slot_bytes, full + 8 * k);
             started |= 1u << k;
         }
 
     // what is small is loaded a row ahead
     float rstd = 0.0f, scale[C] = {};
     const auto load_small = [&](int64_t i) {
-        rstd = a.rstd[i];
+        rstd = access_ok(i >= 0 && i < a.n) ? a.rstd[i] : 0.0f;
         if constexpr (kCodes) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int64_t at = VEC ? cols[c].at : cols[c].at - lane + 32 * (lane & 7);
-                scale[c] = at < a.dim ? a.packed.scales[i * a.packed.scale_stride + (at >> a.packed.log_group)] : 0.0f;
+                scale[c] = at < a.dim && scale_inside(a.packed, i, at >> a.packed.log_group) ? a.packed.scales[i * a.packed.scale_stride + (at >> a.packed.log_group)] : 0.0f;
             }
         }
     };
@@ -258,27 +319,34 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
         Chunk<GT, VEC> residual[C];
         const float r = rstd;
         const char* in = ring + slot * a.slot_bytes;
+        // checked builds: none of a lane's columns where they are not in the matrix's room of the slot
+        const auto in_slot = [&](const Stream& m, const Columns<VEC>& c, int size) {
+            const int64_t at = m.at + (VEC ? 0 : shift_of(m, row));
+            return !c.count || (access_ok(c.last() < a.dim) && room_ok(a, m, in, at + c.at * size, at + (c.last() + 1) * size)) ? c : c.none();
+        };
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float w[8];
             if constexpr (!kKeepWeight)
                 load_weight<VEC>(a, cols[c], w);
             Chunk<DT, VEC> d;
-            read_chunk(d, cols[c], in + (VEC ? 0 : shift_of(streams[0], row)), a.dout.type);
+            read_chunk(d, in_slot(streams[0], cols[c], size_d), in + (VEC ? 0 : shift_of(streams[0], row)), a.dout.type);
             d.unpack(g[c]);
             const char* h = in + a.at_saved + (VEC ? 0 : shift_of(streams[1], row));
+            const Columns<VEC> from = in_slot(streams[1], cols[c], size_h);
             if constexpr (kCodes) {
                 CodeChunk<VEC> v;
-                read_codes(v, cols[c], h);
+                read_codes(v, from, h);
                 v.scale = scale[c];
                 v.unpack(a.packed, n[c]);
             } else {
                 Chunk<std::conditional_t<SOURCE == kFromBf16, __nv_bfloat16, float>, VEC> v;
-                read_chunk(v, cols[c], h, a.saved.type);
+                read_chunk(v, from, h, a.saved.type);
                 v.unpack(n[c]);
             }
             if (a.residual_grad.data)
-                read_chunk(residual[c], cols[c], in + a.at_residual + (VEC ? 0 : shift_of(streams[2], row)), a.residual_grad.type);
+                read_chunk(residual[c], in_slot(streams[2], cols[c], size_g), in + a.at_residual + (VEC ? 0 : shift_of(streams[2], row)),
+                           a.residual_grad.type);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float2 nk = mul2(pair_of(n[c], k), both(r)), dk = pair_of(g[c], k);
@@ -300,7 +368,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
         failed = gave_up[team];
         polls = failed ? 1 : 0;
         if (starts && !failed && row + a.slots * step < a.n) {  // the slot has been read
-            start_row<VEC>(mine, row + a.slots * step, a.n, ring + slot * a.slot_bytes, full + 8 * slot);
+            start_row<VEC>(a, mine, row + a.slots * step, ring + slot * a.slot_bytes, full + 8 * slot);
             last_parity ^= 1u << slot;
         }
         if (++slot == a.slots) {
@@ -323,7 +391,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     set_pair(y, k, mul2(pair_of(n[c], k), pair_of(kKeepWeight ? weight[kKeepWeight ? c : 0] : w, k)));
-                store_typed<VEC>(cols[c], a.again.data, row * a.again.stride, a.again.type, y);
+                store_typed<VEC>(cols[c], a.again, row, y);
             }
             float rest[8] = {};
             if (a.residual_grad.data)
@@ -331,7 +399,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 set_pair(g[c], k, fma2(both(r), fma2(pair_of(n[c], k), both(-mean), pair_of(g[c], k)), pair_of(rest, k)));
-            store_typed<VEC>(cols[c], a.dx.data, row * a.dx.stride, a.dx.type, g[c]);
+            store_typed<VEC>(cols[c], a.dx, row, g[c]);
         }
     }
     if (failed)  // no copy may still be under way when the block ends
@@ -345,6 +413,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         float* mine = columns + team * a.dim + cols[c].at;
+        if (cols[c].count && !sums_ok(a, team, cols[c].last()))
+            continue;
         if (VEC) {
             if (cols[c].count) {
                 Group8<float> v;
@@ -373,6 +443,16 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 1) k_norm_grad(const __grid_
 // columns, all of its loads in flight at once, and then takes one of the columns.
 constexpr int kJoinWarps = 32, kJoinLoads = 5;
 
+// Checked builds: whether a column is one of a row's.
+__device__ __forceinline__ bool one_row_ok(const TypedRows& m, int column)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    return access_ok(m.rows == 1 && column >= 0 && column < m.cols);
+#else
+    return true;
+#endif
+}
+
 __global__ void __launch_bounds__(kJoinWarps * 32) k_weight_grad(const __grid_constant__ WeightGradArgs a)
 {
     __shared__ float sums[kJoinWarps][33];  // a column of it touches every bank once
@@ -386,7 +466,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_weight_grad(const __grid_co
 #pragma unroll
             for (int u = 0; u < kJoinLoads; ++u) {
                 const int i = row + u * kJoinWarps;
-                v[u] = i < a.rows ? a.partial[static_cast<int64_t>(i) * a.dim + first + lane] : 0.0f;
+                v[u] = i < a.rows && access_ok(first + lane < a.dim) ? a.partial[static_cast<int64_t>(i) * a.dim + first + lane] : 0.0f;
             }
 #pragma unroll
             for (int u = 0; u < kJoinLoads; ++u)
@@ -396,7 +476,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_weight_grad(const __grid_co
     __syncthreads();
     const int j = first + warp;
     sum = warp_sum(sums[lane][warp]);
-    if (lane || j >= a.dim)
+    if (lane || j >= a.dim || !one_row_ok(a.grad, j) || (a.base.data && !one_row_ok(a.base, j)))
         return;
     if (a.base.data)
         sum = __fadd_rn(sum, a.base.type == LIONCUB_ROWS_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.base.data)[j])
@@ -452,6 +532,10 @@ cudaError_t launch_t(const NormGradArgs& a, int c, int blocks, cudaStream_t s)
 }
 
 }  // namespace
+
+#ifdef LIONCUB_BOUNDS_CHECK
+cudaError_t take_norm_grad_word(int* word) { return take_word(word); }
+#endif
 
 int norm_grad_blocks(int64_t n, int dim, int multiprocessors)
 {

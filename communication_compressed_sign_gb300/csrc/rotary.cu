@@ -68,6 +68,15 @@ struct WideItem {
         first = item < turning ? item * 8 : 2 * a.pairs + (item - turning) * 8;
         second = item < turning ? first + a.pairs : -1;
     }
+    // checked builds: whether move k (of two) is within a head (unless there is none), and where it begins
+    static constexpr int kMoves = 2, kMove = 8;
+    __device__ __forceinline__ int move_at(const RotaryArgs&, int k) const { return k ? second : first; }
+    __device__ __forceinline__ bool has_move(int k) const { return !k || second >= 0; }
+    // ... and the last of its pairs' angles, or -1
+    __device__ __forceinline__ int last_pair(const RotaryArgs& a, int item) const
+    {
+        return second < 0 ? -1 : INTERLEAVED ? item * 4 + a.pairs / 2 + 3 : item * 8 + 7;
+    }
     __device__ __forceinline__ void load(const RotaryArgs&, const T* in)
     {
         load(g[0], in + first);
@@ -155,6 +164,10 @@ struct NarrowItem {
         return copied ? first + k : INTERLEAVED ? 2 * first + k : first + (k & 3) + (k >> 2) * a.pairs;
     }
     __device__ __forceinline__ bool has(int k) const { return (copied ? k : INTERLEAVED ? k >> 1 : k & 3) < count; }
+    static constexpr int kMoves = 8 / MOVE, kMove = MOVE;
+    __device__ __forceinline__ int move_at(const RotaryArgs& a, int k) const { return column(a, k * MOVE); }
+    __device__ __forceinline__ bool has_move(int k) const { return has(k * MOVE); }
+    __device__ __forceinline__ int last_pair(const RotaryArgs&, int item) const { return copied ? -1 : item * 4 + min(count, 4) - 1; }
     __device__ __forceinline__ T& element(int k) { return m[k / MOVE].x[k % MOVE]; }
     __device__ __forceinline__ void load(const RotaryArgs& a, const T* in)
     {
@@ -199,6 +212,10 @@ struct CopiedItem {
         first = 2 * a.pairs + item * 8;
         count = a.head_dim - first;
     }
+    static constexpr int kMoves = 2, kMove = 4;
+    __device__ __forceinline__ int move_at(const RotaryArgs&, int k) const { return first + 4 * k; }
+    __device__ __forceinline__ bool has_move(int k) const { return 4 * k < count; }
+    __device__ __forceinline__ int last_pair(const RotaryArgs&, int) const { return -1; }
     __device__ __forceinline__ void load(const RotaryArgs&, const T* in)
     {
 #pragma unroll
@@ -233,6 +250,30 @@ struct Place {
     T* out[2];
 };
 
+// Checked builds: whether an item's moves of a head lie in it and in its matrices, on boundaries
+// of their size, and its pairs have angles.
+template <typename Item, typename T>
+__device__ __forceinline__ bool item_ok(const RotaryArgs& a, const Item& x, int item, int place, int places, int side, int head, const T* in,
+                                        const T* out)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    const HeadsArgs& s = a.side[side];
+    bool ok = place < places && places <= kMaxPlaces && head >= 0 && head < a.heads[side] && x.last_pair(a, item) < a.pairs;
+    for (int k = 0; k < Item::kMoves; ++k)
+        if (x.has_move(k)) {
+            const int at = x.move_at(a, k);
+            constexpr uintptr_t kAlign = Item::kMove == 8 ? 16 : Item::kMove * sizeof(T);
+            ok = ok && at >= 0 && at + Item::kMove <= a.head_dim && in >= s.in && out >= s.out &&
+                 reinterpret_cast<const char*>(in + at + Item::kMove) <= s.in_end &&
+                 reinterpret_cast<const char*>(out + at + Item::kMove) <= s.out_end && reinterpret_cast<uintptr_t>(in + at) % kAlign == 0 &&
+                 reinterpret_cast<uintptr_t>(out + at) % kAlign == 0;
+        }
+    return access_ok(ok);
+#else
+    return true;
+#endif
+}
+
 // The items of the heads of some places, of both sides, over the block's threads.
 template <typename Item, typename T>
 __device__ __forceinline__ void walk(const RotaryArgs& a, int places, const Place<T>* at, const float* cosines, const float* sines,
@@ -244,6 +285,7 @@ __device__ __forceinline__ void walk(const RotaryArgs& a, int places, const Plac
         Item x[kUnits];
         uint32_t item[kUnits], p[kUnits];
         T* out[kUnits];
+        bool ok[kUnits];
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const uint32_t unit = u0 + u * kBlock;
@@ -256,16 +298,31 @@ __device__ __forceinline__ void walk(const RotaryArgs& a, int places, const Plac
                 h -= side ? a.heads[0] : 0;
                 out[u] = at[p[u]].out[side] + h * (side ? a.side[1].out_head : a.side[0].out_head);
                 x[u].place(a, item[u], turning);
-                x[u].load(a, at[p[u]].in[side] + h * (side ? a.side[1].in_head : a.side[0].in_head));
+                const T* in = at[p[u]].in[side] + h * (side ? a.side[1].in_head : a.side[0].in_head);
+                ok[u] = item_ok(a, x[u], item[u], p[u], places, side, h, in, out[u]);
+                if (ok[u])
+                    x[u].load(a, in);
             }
         }
 #pragma unroll
         for (int u = 0; u < kUnits; ++u)
-            if (u0 + u * kBlock < units) {
+            if (u0 + u * kBlock < units && (!kBoundsCheck || ok[u])) {
                 x[u].turn(cosines + p[u] * a.pairs, sines + p[u] * a.pairs, item[u], a.pairs);
                 x[u].store(a, out[u]);
             }
     }
+}
+
+// Checked builds: whether a place's pair has its cosine and sine in shared memory.
+__device__ __forceinline__ bool angles_ok(int all, int i)
+{
+#ifdef LIONCUB_BOUNDS_CHECK
+    uint32_t bytes;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(bytes));
+    return access_ok(i < all && 2 * all * sizeof(float) <= bytes);
+#else
+    return true;
+#endif
 }
 
 // APART: columns that are copied are walked over by themselves (copied: their items).
@@ -282,7 +339,7 @@ __global__ void __launch_bounds__(kBlock, 8) k_rotary(const __grid_constant__ Ro
     const int places = static_cast<int>(min(a.places - first, static_cast<int64_t>(block_places)));
     if (a.positions)
         wait_for_launch_before();
-    if (threadIdx.x < places) {
+    if (threadIdx.x < places && access_ok(places <= kMaxPlaces && first + places <= a.places)) {
         const int64_t place = first + threadIdx.x, b = quotient(place, a.seq), s = place - b * a.seq;
         positions[threadIdx.x] = a.positions ? index_at(a.positions, place, a.wide) : a.first + s;
         for (int k = 0; k < 2; ++k) {
@@ -293,6 +350,8 @@ __global__ void __launch_bounds__(kBlock, 8) k_rotary(const __grid_constant__ Ro
     __syncthreads();
     for (int i = threadIdx.x; i < places * a.pairs; i += kBlock) {
         const int p = i / a.pairs;
+        if (!angles_ok(block_places * a.pairs, i))
+            continue;
         angle_of(static_cast<uint64_t>(positions[p]), a.turns[i - p * a.pairs], a, cosines[i], sines[i]);
     }
     if (!a.positions)  // the angles need nothing of the launches before
@@ -346,6 +405,10 @@ cudaError_t launch_l(const RotaryArgs& a, int move, bool copy_by_four, cudaStrea
 }
 
 }  // namespace
+
+#ifdef LIONCUB_BOUNDS_CHECK
+cudaError_t take_rotary_word(int* word) { return take_word(word); }
+#endif
 
 cudaError_t launch_rotary(const RotaryArgs& a, int type, bool interleaved, int move, bool copy_by_four, cudaStream_t s)
 {
