@@ -27,9 +27,12 @@ constexpr int kWarps = kBlock / 32;
 template <int KIND, bool VEC>
 constexpr int kUnitsOf = VEC || KIND == kIdentity ? 2 : 1;
 
-// Blocks that an SM should have room for, which caps the registers.  Both ways, by 4, 5
+// Blocks that an SM should have room for, which caps the registers.  bf16 both ways, by 4, 5
 // and 6 blocks: SiLU, gated, 16384 x 8192 387, 370, 382 us; GELU 218, 205, 199; by
 // scalar moves 4907 x 771 x 2 (1, 5, 6) 28.6, 26.1, 24.2, 8192 x 3905 x 2 163, 155, 145.
+// The caps hold for fp32 too, whose gradient from matrices spills 240 to 312 bytes a
+// thread by them (it was not measured by others): SiLU, gated, 8192 x 8192 226 us,
+// 6.0 TB/s; GELU 116 us, 6.9 TB/s.
 template <bool VEC>
 constexpr int kBlocks = VEC ? 5 : 6;
 

@@ -6,7 +6,7 @@
 // Memory-bound.  A team of warps takes a row at a time, with one sum over the row
 // between reading and writing it.  Teams walk over rows (persistent blocks, one
 // for each multiprocessor), so that a column's share of the weight's gradient
-// stays in a register; three threads of the team have the next rows brought into
+// stays in a register (up to 8192 columns); three threads of the team have the next rows brought into
 // a ring in shared memory by bulk copies meanwhile, one matrix each.  A block adds its teams'
 // columns in order and leaves one row of sums, and a second launch adds those of
 // all blocks in order.
@@ -15,10 +15,13 @@
 // TB/s, 98 % of a measured copy); 8192 x 768 onto fp32 18.0 us (4.9 TB/s; some 6
 // of them are the two launches' beginnings and ends, 2.6 the second launch); 4907
 // x 771 bf16 13.8 us (2.2 TB/s, scalar reads of the ring; 16.7 with one thread
-// starting the copies of all matrices).  The first with its rows
-// loaded ahead into registers, 16 warps an SM: 241 us (too few loads in flight);
-// with each thread's elements copied ahead by itself (cp.async): 246 us (as many
-// instructions for the load-store unit as bytes allow).
+// starting the copies of all matrices).  Above 8192 columns a lane has 32 elements
+// of a row, and of what it keeps for them (the weight's sums, dout, h, the residual)
+// 236 to 636 bytes a thread are spilled: 4096 x 16384 bf16 153 us (3.5 TB/s), from
+// int8 150 (3.1 TB/s).  65536 x 2048 with its rows loaded ahead into registers, 16
+// warps an SM: 241 us (too few loads in flight); with each thread's elements copied
+// ahead by itself (cp.async): 246 us (as many instructions for the load-store unit as
+// bytes allow).
 //
 // A row of any alignment comes by bulk copies: of the 16-byte pieces that it
 // touches, as far as they lie within the matrix; the ends of the first and the last

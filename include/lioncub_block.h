@@ -20,6 +20,9 @@
  * Every operation is in fp32 (sums of a row and of a column too), and each
  * result is rounded once to its own type; the norm is that of h before it is
  * rounded to the type of `summed`.  Mean squares must lie within fp32's range.
+ * The activation's exponential and quotient are the GPU's approximate ones: f is
+ * off by at most 16 (1 + (1 - s) |z|) units of 2^-24 of itself, each term of f' by
+ * at most 32, and an s below 2^-126 counts as 0.
  *
  * 8 bits (lioncub_packed): the columns of a row are cut into groups (the last
  * may be shorter) that share an fp32 scale.  With a the largest magnitude of a
