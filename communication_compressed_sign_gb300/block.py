@@ -8,8 +8,9 @@ GELU, gated or not, and :class:`Rotary` rotary positions.  A norm and an
 activation can leave what their backward pass needs in 8 bits.  As in
 :mod:`.embed`, results are not part of torch's autograd graph and gradients come
 from the backward functions, called by hand: tensors that require a gradient while
-torch records one, or have a forward-mode tangent, are refused.  :func:`load`
-gives the library with the C functions declared.
+torch records one, or have a forward-mode tangent, are refused.  A result that is a
+lazy clone gets memory of its own first, by a copy on torch's current stream.
+:func:`load` gives the library with the C functions declared.
 """
 from __future__ import annotations
 

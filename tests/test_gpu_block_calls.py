@@ -170,3 +170,29 @@ def test_norm_gradient_without_the_weights(ops, n, D, dk, hk, gk):  # noqa: F811
             both.append(dx)
         assert torch.equal(*both)
     assert layer.status() == 0
+
+
+@pytest.mark.parametrize("D", [1, 64, 771, 2048, 9001, 16384])
+def test_one_row_in_the_weights_place(ops, D):  # noqa: F811
+    """Results of one row that are the weight (read by then), and the weight's gradient over the weight of any rows."""
+    for n in (1, 5):
+        x, dout, r, w = (_rand((n, D) if k < 3 else (1, D), "f32", k + D).cuda() for k in range(4))
+        layer, rstd = ops.RmsNorm(D), torch.empty(n, device="cuda")
+        kept = ops.Packed.empty((n, D))
+        y = layer.forward(x, w, residual=r, rstd=rstd, saved=kept)
+        saved, dw, again = x + r, torch.empty(D, device="cuda"), torch.empty_like(x)
+        dx = layer.backward(dout, saved, rstd, w, residual_grad=r, weight_grad=dw, again=again)
+        if n == 1:
+            v = w.clone()
+            assert torch.equal(layer.forward(x, v, residual=r, out=v), y) and torch.equal(v, y)
+            for out, more in ((True, False), (False, True)):
+                v, grad, other = w.clone(), torch.empty_like(dw), torch.empty_like(x)
+                layer.backward(dout, saved, rstd, v, residual_grad=r, weight_grad=grad, out=v if out else other, again=v if more else other)
+                a, b = (v, other) if out else (other, v)
+                assert torch.equal(a, dx) and torch.equal(b, again) and torch.equal(grad, dw)
+        v = w.clone()
+        assert torch.equal(layer.backward(dout, saved, rstd, v, residual_grad=r, weight_grad=v), dx) and torch.equal(v[0], dw)
+        v = w.clone()
+        layer.backward(dout, saved, rstd, v, weight_grad=v, weight_base=v)
+        assert torch.equal(v[0], dw + w[0])
+        assert layer.status() == 0
